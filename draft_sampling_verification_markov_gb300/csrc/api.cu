@@ -7,6 +7,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "mx.cuh"
 #include "spec_markov.h"
 
 namespace spec {
@@ -867,6 +868,137 @@ int spec_tv_confidence_masked(const void* U, const void* target, int l_dtype, co
   return tv_confidence_impl(U, target, l_dtype, W1, W2, w_dtype, rank, anchors, draft_tokens,
                             draft_stats, target_stats, temperature, R, gamma, V, conf, survival,
                             ws, ws_bytes, stream, allowed);
+}
+
+// ------------------------------------------------------------------------------ vocabulary head
+
+static bool mx_fmt_ok(int fmt) { return fmt == SPEC_MX_E2M1 || fmt == SPEC_MX_E4M3; }
+
+// rows * K within the range the other calls allow, and K small enough for int element indexes.
+static bool mx_sizes_ok(int rows, int K) {
+  return rows >= 0 && rows <= (1 << 30) && K >= 1 && K <= (1 << 24) &&
+         (long long)rows * K <= (1LL << 46);
+}
+
+static bool mx_aligned(const void* codes, const void* scales) {
+  return (reinterpret_cast<uintptr_t>(codes) & 31) == 0 && aligned16(scales);
+}
+
+static bool elem_aligned(const void* p, int dtype) {
+  return (reinterpret_cast<uintptr_t>(p) & (esize(dtype) - 1)) == 0;
+}
+
+static bool status_ws_ok(void* ws) {
+  return ws && (reinterpret_cast<uintptr_t>(ws) % kAlign) == 0;
+}
+
+size_t spec_mx_code_bytes(int fmt, int rows, int K) {
+  if (!mx_fmt_ok(fmt) || !mx_sizes_ok(rows, K)) return 0;
+  return (size_t)rows * mx::code_row(fmt, mx::padded(K));
+}
+
+size_t spec_mx_scale_bytes(int rows, int K) {
+  if (!mx_sizes_ok(rows, K)) return 0;
+  return (size_t)((rows + mx::kTileRows - 1) / mx::kTileRows) * mx::groups(K) * mx::kTileBytes;
+}
+
+int spec_mx_quantize(const void* x, int x_dtype, long long ldx, int rows, int K, int fmt,
+                     uint8_t* codes, uint8_t* scales, void* ws, size_t ws_bytes, void* stream) {
+  if (!mx_sizes_ok(rows, K) || ldx < K || !mx_fmt_ok(fmt)) return SPEC_ERR_INVALID_ARG;
+  if (!dtype_ok(x_dtype)) return SPEC_ERR_UNSUPPORTED_DTYPE;
+  if (!status_ws_ok(ws)) return SPEC_ERR_INVALID_ARG;
+  if (ws_bytes < kHeader) return SPEC_ERR_WORKSPACE_TOO_SMALL;
+  if (rows == 0) return SPEC_OK;
+  if (!x || !codes || !scales || !mx_aligned(codes, scales) || !elem_aligned(x, x_dtype))
+    return SPEC_ERR_INVALID_ARG;
+  launch_mx_quantize(x, x_dtype, ldx, rows, K, fmt, codes, scales, static_cast<uint32_t*>(ws),
+                     static_cast<cudaStream_t>(stream));
+  return finish();
+}
+
+int spec_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int fmt, int rows, int K,
+                       void* out, int out_dtype, long long ld_out, void* ws, size_t ws_bytes,
+                       void* stream) {
+  if (!mx_sizes_ok(rows, K) || ld_out < K || !mx_fmt_ok(fmt)) return SPEC_ERR_INVALID_ARG;
+  if (!dtype_ok(out_dtype)) return SPEC_ERR_UNSUPPORTED_DTYPE;
+  if (!status_ws_ok(ws)) return SPEC_ERR_INVALID_ARG;
+  if (ws_bytes < kHeader) return SPEC_ERR_WORKSPACE_TOO_SMALL;
+  if (rows == 0) return SPEC_OK;
+  if (!codes || !scales || !out || !mx_aligned(codes, scales) || !elem_aligned(out, out_dtype))
+    return SPEC_ERR_INVALID_ARG;
+  launch_mx_dequantize(codes, scales, fmt, rows, K, out, out_dtype, ld_out,
+                       static_cast<cudaStream_t>(stream));
+  return finish();
+}
+
+int spec_rmsnorm_mx(const void* x, long long ldx, const void* residual, long long ldr, int dtype,
+                    const void* weight, int w_dtype, float eps, int rows, int K,
+                    void* residual_out, long long ldo, int fmt, uint8_t* codes, uint8_t* scales,
+                    void* ws, size_t ws_bytes, void* stream) {
+  if (!mx_sizes_ok(rows, K) || ldx < K || !mx_fmt_ok(fmt)) return SPEC_ERR_INVALID_ARG;
+  if (!dtype_ok(dtype) || !dtype_ok(w_dtype)) return SPEC_ERR_UNSUPPORTED_DTYPE;
+  if (!(eps >= 0.0f) || !isfinite(eps)) return SPEC_ERR_INVALID_ARG;
+  if (!status_ws_ok(ws)) return SPEC_ERR_INVALID_ARG;
+  if (ws_bytes < kHeader) return SPEC_ERR_WORKSPACE_TOO_SMALL;
+  if (residual && (ldr < K || ldo < K)) return SPEC_ERR_INVALID_ARG;
+  if (rows == 0) return SPEC_OK;
+  if (!x || !weight || !codes || !scales || !mx_aligned(codes, scales) ||
+      !elem_aligned(x, dtype) || !elem_aligned(weight, w_dtype))
+    return SPEC_ERR_INVALID_ARG;
+  if (residual && (!residual_out || !elem_aligned(residual, dtype) ||
+                   !elem_aligned(residual_out, dtype)))
+    return SPEC_ERR_INVALID_ARG;
+  // written in place only where it has the stride of what it replaces
+  if (residual && ((residual_out == x && ldo != ldx) || (residual_out == residual && ldo != ldr)))
+    return SPEC_ERR_INVALID_ARG;
+  launch_rmsnorm_mx(x, ldx, residual, ldr, dtype, weight, w_dtype, eps, rows, K, residual_out, ldo,
+                    fmt, codes, scales, static_cast<uint32_t*>(ws),
+                    static_cast<cudaStream_t>(stream));
+  return finish();
+}
+
+int spec_mx_logits(const uint8_t* a_codes, const uint8_t* a_scales, int a_fmt,
+                   const uint8_t* w_codes, const uint8_t* w_scales, int w_fmt, int M, int V,
+                   int K, void* out, int out_dtype, long long ld_out, void* ws, size_t ws_bytes,
+                   void* stream) {
+  if (!mx_sizes_ok(M, K) || !mx_sizes_ok(V, K) || V < 1 || ld_out < V || !mx_fmt_ok(a_fmt) ||
+      !mx_fmt_ok(w_fmt) || (long long)M * V > (1LL << 46))
+    return SPEC_ERR_INVALID_ARG;
+  if (!dtype_ok(out_dtype)) return SPEC_ERR_UNSUPPORTED_DTYPE;
+  if (!status_ws_ok(ws)) return SPEC_ERR_INVALID_ARG;
+  if (ws_bytes < kHeader) return SPEC_ERR_WORKSPACE_TOO_SMALL;
+  if (M == 0) return SPEC_OK;
+  if (!a_codes || !a_scales || !w_codes || !w_scales || !out || !mx_aligned(a_codes, a_scales) ||
+      !mx_aligned(w_codes, w_scales) || !elem_aligned(out, out_dtype))
+    return SPEC_ERR_INVALID_ARG;
+  if (launch_mx_logits(a_codes, a_scales, a_fmt, w_codes, w_scales, w_fmt, M, V, K, out, out_dtype,
+                       ld_out, static_cast<uint32_t*>(ws),
+                       static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return SPEC_ERR_CUDA;
+  return finish();
+}
+
+int spec_token_logprobs(const void* logits, int dtype, long long ld, const int32_t* tokens,
+                        float temperature, int rows, int V, int top, float* logp, int32_t* rank,
+                        float* entropy, int32_t* top_ids, float* top_logp, void* ws,
+                        size_t ws_bytes, void* stream) {
+  if (rows < 0 || rows > (1 << 30) || V < 1 || (long long)rows * V > (1LL << 46) || ld < V)
+    return SPEC_ERR_INVALID_ARG;
+  if (!dtype_ok(dtype)) return SPEC_ERR_UNSUPPORTED_DTYPE;
+  if (!(temperature >= 0.0f) || !isfinite(temperature) || top < 0) return SPEC_ERR_INVALID_ARG;
+  if (temperature > 0.0f && !isfinite(1.0f / temperature)) return SPEC_ERR_INVALID_ARG;
+  if (top > SPEC_LOGPROBS_MAX_TOP) return SPEC_ERR_TOO_LARGE;
+  if (!status_ws_ok(ws)) return SPEC_ERR_INVALID_ARG;
+  if (ws_bytes < kHeader) return SPEC_ERR_WORKSPACE_TOO_SMALL;
+  if (rows == 0) return SPEC_OK;
+  if (!logits || !elem_aligned(logits, dtype)) return SPEC_ERR_INVALID_ARG;
+  if (!tokens && (logp || rank)) return SPEC_ERR_INVALID_ARG;
+  LogprobArgs a{logits, ld, tokens, temperature > 0.0f ? 1.0f / temperature : 1.0f, rows, V,
+                top_ids || top_logp ? top : 0, logp, rank, entropy, top_ids, top_logp,
+                static_cast<uint32_t*>(ws)};
+  if (launch_token_logprobs(a, dtype, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return SPEC_ERR_CUDA;
+  return finish();
 }
 
 }  // extern "C"

@@ -122,6 +122,35 @@ cudaError_t launch_mtp_greedy(int dtype, const void* D, const void* T, int R, in
 // Smallest partial segment any Markov producer writes (sizes the workspace).
 constexpr int kMarkovMinSeg = 32;
 
+// Block-scaled matrices and the vocabulary head (mx.cu, mx_logits.cu); strides in elements.
+void launch_mx_quantize(const void* x, int dt, long long ldx, int rows, int K, int fmt,
+                        uint8_t* codes, uint8_t* scales, uint32_t* status, cudaStream_t s);
+void launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int fmt, int rows, int K,
+                          void* out, int dt, long long ldo, cudaStream_t s);
+void launch_rmsnorm_mx(const void* x, long long ldx, const void* res, long long ldr, int dt,
+                       const void* weight, int wdt, float eps, int rows, int K, void* res_out,
+                       long long ldo, int fmt, uint8_t* codes, uint8_t* scales, uint32_t* status,
+                       cudaStream_t s);
+cudaError_t launch_mx_logits(const uint8_t* ac, const uint8_t* as, int af, const uint8_t* wc,
+                             const uint8_t* wsc, int wf, int M, int V, int K, void* out, int odt,
+                             long long ldo, uint32_t* status, cudaStream_t s);
+
+// Token log-probabilities (logprobs.cu).
+struct LogprobArgs {
+  const void* x;          // [rows, V], row stride ld
+  long long ld;
+  const int32_t* tokens;  // [rows] or null
+  float scale;            // 1/T
+  int rows, V, top;
+  float* logp;            // outputs, each may be null
+  int32_t* rank;
+  float* entropy;
+  int32_t* top_ids;
+  float* top_logp;
+  uint32_t* status;
+};
+cudaError_t launch_token_logprobs(const LogprobArgs& a, int dt, cudaStream_t s);
+
 int num_sms();
 
 // Tracing hooks around every launch (api.cu): count the launch and record the attached begin /

@@ -1,0 +1,89 @@
+// mx.cuh -- block-scaled (microscaled) floating point: formats, scale rule and layout, shared by
+// the kernels that write such matrices (mx.cu) and the product that reads them (mx_logits.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace spec {
+namespace mx {
+
+constexpr int kBlock = SPEC_MX_BLOCK;  // elements that share a scale
+constexpr int kGroup = SPEC_MX_GROUP;  // elements whose four scales share a 32-bit word
+constexpr int kTileRows = 128;         // rows of a scale tile
+constexpr int kTileBytes = 512;        // bytes of a scale tile: 128 rows x 4 scales
+constexpr int kNanScale = 255;
+
+__host__ __device__ inline int padded(int K) { return (K + kGroup - 1) / kGroup * kGroup; }
+__host__ __device__ inline int groups(int K) { return (K + kGroup - 1) / kGroup; }
+
+// Bytes of a padded row's codes.
+__host__ __device__ inline size_t code_row(int fmt, int Kp) {
+  return fmt == SPEC_MX_E2M1 ? (size_t)Kp / 2 : (size_t)Kp;
+}
+
+// Byte offset of the scale word (four scales, 128 elements) of row r and group g. The tile is
+// what tcgen05.cp spreads over tensor memory: lane r % 32, column r % 128 / 32.
+__host__ __device__ inline size_t scale_word(int r, int g, int G) {
+  return ((size_t)(r >> 7) * G + g) * kTileBytes + (size_t)((r & 31) * 16 + ((r >> 5) & 3) * 4);
+}
+
+// Stored scale byte of a block whose largest magnitude has the fp32 bits `amax`: the smallest
+// power of two 2^(byte - 127) with amax <= top * 2^(byte - 127). top = 1.5 * 2^2 (E2M1) or
+// 1.75 * 2^8 (E4M3), so the exponent is amax's less 2 (less 8), plus one if amax's significand
+// passes top's. 255 for a block that is not finite (integer order: NaN above infinity).
+template <int FMT>
+__device__ __forceinline__ int scale_byte(uint32_t amax) {
+  if (amax >= 0x7f800000u) return kNanScale;
+  const int ex = (int)(amax >> 23), man = (int)(amax & 0x7fffffu);
+  const int b = FMT == SPEC_MX_E2M1 ? ex - 2 + (man > 0x400000) : ex - 8 + (man > 0x600000);
+  return b < 0 ? 0 : b;
+}
+
+// 2^(127 - byte), the factor that brings a block into the format's range (a normal fp32 number
+// for every byte a finite block has: 0 .. 253).
+__device__ __forceinline__ float unscale(int byte) {
+  return __uint_as_float((uint32_t)(254 - byte) << 23);
+}
+
+// 2^(byte - 127); byte 0 is a subnormal, 255 a NaN.
+__device__ __forceinline__ float scale_value(int byte) {
+  return __uint_as_float(byte == kNanScale ? 0x7fc00000u
+                                           : (byte == 0 ? 0x00400000u : (uint32_t)byte << 23));
+}
+
+// Two values to the format, nearest with ties to even (the second in the upper half).
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 t;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\t"
+      "cvt.u32.u8 %0, t;\n\t}"
+      : "=r"(r)
+      : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Values of one code (the sign, then the magnitude from its exponent and significand).
+__device__ __forceinline__ float from_e4m3(uint32_t c) {
+  const uint32_t mag = c & 0x7fu;
+  // normal: exponent bias 7 -> 127; subnormal: significand * 2^-9
+  const float v = mag >= 8 ? __uint_as_float((mag << 20) + (120u << 23)) : (float)mag * 0.001953125f;
+  return (c & 0x80u) ? -v : v;
+}
+
+__device__ __forceinline__ float from_e2m1(uint32_t c) {
+  const uint32_t mag = c & 7u;
+  const float v = mag >= 2 ? __uint_as_float((mag << 22) + (126u << 23)) : (float)mag * 0.5f;
+  return (c & 8u) ? -v : v;
+}
+
+}  // namespace mx
+}  // namespace spec

@@ -25,6 +25,9 @@ SPEC_SCHEDULE_MAX_CANDIDATES = 16384
  SPEC_KCLASS_PROPOSE) = range(5)
 SPEC_NOALLOC_MAX_ROWS = 65536
 SPEC_ERR_TOO_LARGE = -7
+SPEC_MX_E2M1, SPEC_MX_E4M3 = 0, 1
+SPEC_MX_GROUP = 128
+SPEC_LOGPROBS_MAX_TOP = 32
 
 _lib = None
 
@@ -83,6 +86,18 @@ def lib():
         L.spec_verify_rejection_flat.argtypes = [vp, vp, i, vp, vp, i, i, vp, vp, vp, vp, vp, vp,
                                                  vp, f, vp, vp, i, i, i, vp, vp, vp, vp, vp, sz,
                                                  vp]
+        ll = ctypes.c_longlong
+        L.spec_mx_code_bytes.argtypes = [i, i, i]
+        L.spec_mx_code_bytes.restype = sz
+        L.spec_mx_scale_bytes.argtypes = [i, i]
+        L.spec_mx_scale_bytes.restype = sz
+        L.spec_mx_quantize.argtypes = [vp, i, ll, i, i, i, vp, vp, vp, sz, vp]
+        L.spec_mx_dequantize.argtypes = [vp, vp, i, i, i, vp, i, ll, vp, sz, vp]
+        L.spec_rmsnorm_mx.argtypes = [vp, ll, vp, ll, i, vp, i, f, i, i, vp, ll, i, vp, vp, vp, sz,
+                                      vp]
+        L.spec_mx_logits.argtypes = [vp, vp, i, vp, vp, i, i, i, i, vp, i, ll, vp, sz, vp]
+        L.spec_token_logprobs.argtypes = [vp, i, ll, vp, f, i, i, i, vp, vp, vp, vp, vp, vp, sz,
+                                          vp]
         L.spec_launch_count.restype = ctypes.c_ulonglong
         L.spec_trace_events.argtypes = [i, vp, vp, i]
         L.spec_trace_events.restype = i
@@ -96,7 +111,8 @@ def lib():
                      "spec_markov_propose_target_stats", "spec_mtp_greedy",
                      "spec_flat_layout", "spec_flat_pack", "spec_target_stats_flat",
                      "spec_verify_greedy_flat",
-                     "spec_verify_rejection_flat"):
+                     "spec_verify_rejection_flat", "spec_mx_quantize", "spec_mx_dequantize",
+                     "spec_rmsnorm_mx", "spec_mx_logits", "spec_token_logprobs"):
             getattr(L, name).restype = i
         _lib = L
     return _lib
@@ -563,6 +579,242 @@ def spec_verify_rejection_flat(target, U, W1, W2, anchors, draft_tokens, draft_l
         _stream(stream))
     _check("spec_verify_rejection_flat", rc)
     return accept_len, out_tokens, next_anchor
+
+
+# ----------------------------------------------------------------------------- vocabulary head
+
+class MXTensor:
+    """A block-scaled [rows, K] matrix: `codes` [rows, Kp / 2] (SPEC_MX_E2M1) or [rows, Kp]
+    (SPEC_MX_E4M3) and `scales` [ceil(rows / 128), Kp / 128, 32, 4, 4], both uint8 on the device
+    (Kp = K rounded up to a multiple of 128; the layout is that of include/spec_markov.h)."""
+
+    __slots__ = ("codes", "scales", "fmt", "K")
+
+    def __init__(self, codes, scales, fmt, K):
+        rows, G = codes.shape[0], -(-K // SPEC_MX_GROUP)
+        if fmt not in (SPEC_MX_E2M1, SPEC_MX_E4M3):
+            raise ValueError("fmt must be SPEC_MX_E2M1 or SPEC_MX_E4M3")
+        width = G * (SPEC_MX_GROUP // 2 if fmt == SPEC_MX_E2M1 else SPEC_MX_GROUP)
+        if codes.dtype != torch.uint8 or tuple(codes.shape) != (rows, width):
+            raise ValueError(f"codes must be uint8 [rows, {width}]")
+        if scales.dtype != torch.uint8 or tuple(scales.shape) != (-(-rows // 128), G, 32, 4, 4):
+            raise ValueError(f"scales must be uint8 {(-(-rows // 128), G, 32, 4, 4)}")
+        if scales.device != codes.device:
+            raise ValueError("codes and scales must be on one device")
+        self.codes, self.scales, self.fmt, self.K = codes, scales, fmt, K
+
+    @staticmethod
+    def empty(rows, K, fmt, device):
+        """An uninitialised [rows, K] matrix for a call to write."""
+        G = -(-K // SPEC_MX_GROUP)
+        width = G * (SPEC_MX_GROUP // 2 if fmt == SPEC_MX_E2M1 else SPEC_MX_GROUP)
+        return MXTensor(torch.empty(rows, width, dtype=torch.uint8, device=device),
+                        torch.empty(-(-rows // 128), G, 32, 4, 4, dtype=torch.uint8,
+                                    device=device), fmt, K)
+
+    @property
+    def shape(self):
+        return self.codes.shape[0], self.K
+
+    @property
+    def device(self):
+        return self.codes.device
+
+
+def _rows(t, name):
+    """(pointer, rows, width, row stride) of a matrix whose rows are contiguous: two dimensions
+    with any row stride, or more dimensions that flatten into evenly spaced rows."""
+    if not t.is_cuda:
+        raise ValueError("libspecmarkov takes device tensors")
+    if t.dim() < 1:
+        raise ValueError(f"{name} must have at least one dimension")
+    width = t.shape[-1]
+    if width > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    # leading dimensions of more than one index, innermost last
+    lead = [(n, st) for n, st in zip(t.shape[:-1], t.stride()[:-1]) if n != 1]
+    rows = 1
+    for n, _ in lead:
+        rows *= n
+    if not lead or rows == 0:
+        return ctypes.c_void_p(t.data_ptr()), rows, width, width
+    ld, span = lead[-1][1], lead[-1][1]
+    for n, st in reversed(lead):
+        if st != span:
+            raise ValueError(f"the rows of {name} must be evenly spaced")
+        span = st * n
+    return ctypes.c_void_p(t.data_ptr()), rows, width, ld
+
+
+def _same_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be on {dev}")
+
+
+class _Call:
+    """The device, stream and status workspace of one call: the operands' device is current
+    while it runs, and its current stream is the default."""
+
+    def __init__(self, dev, workspace, stream):
+        if dev.type != "cuda":
+            raise ValueError("libspecmarkov takes device tensors")
+        self.dev, self.guard = dev, None
+        self.ws, self.s = workspace, stream
+
+    def __enter__(self):
+        if torch.cuda.current_device() != self.dev.index:
+            self.guard = torch.cuda.device(self.dev)
+            self.guard.__enter__()
+        ws = self.ws or default_workspace(self.dev)
+        if ws.device != self.dev:
+            self.__exit__(None, None, None)
+            raise ValueError(f"the workspace must be on {self.dev}")
+        ws.reserve(256, self.s)
+        return ws.ptr, ws.nbytes, _stream(self.s)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+            self.guard = None
+
+
+def spec_mx_quantize(x, fmt=SPEC_MX_E2M1, *, out=None, workspace=None, stream=None):
+    """x [rows, K] (or [..., K], evenly spaced rows; bf16 or fp32) as a block-scaled MXTensor of
+    `fmt`: SPEC_MX_E2M1 for a vocabulary matrix, SPEC_MX_E4M3 for hidden rows. `out` is an
+    MXTensor to write into."""
+    ptr, rows, K, ld = _rows(x, "x")
+    if out is None:
+        out = MXTensor.empty(rows, K, fmt, x.device)
+    if out.shape != (rows, K) or out.fmt != fmt:
+        raise ValueError("out must be an MXTensor of x's rows, width and the given format")
+    _same_device(x.device, out=out)
+    with _Call(x.device, workspace, stream) as (wp, wn, st):
+        rc = lib().spec_mx_quantize(ptr, _dt(x), ld, rows, K, fmt, _ptr(out.codes),
+                                    _ptr(out.scales), wp, wn, st)
+    _check("spec_mx_quantize", rc)
+    return out
+
+
+def spec_mx_dequantize(q, *, dtype=torch.bfloat16, out=None, workspace=None, stream=None):
+    """The numbers that the MXTensor q stands for, [rows, K] of `dtype` (bf16 or fp32)."""
+    rows, K = q.shape
+    if out is None:
+        out = torch.empty(rows, K, dtype=dtype, device=q.device)
+    ptr, orows, width, ld = _rows(out, "out")
+    if (orows, width) != (rows, K):
+        raise ValueError("out must have q's rows and width")
+    _same_device(q.device, out=out)
+    with _Call(q.device, workspace, stream) as (wp, wn, st):
+        rc = lib().spec_mx_dequantize(_ptr(q.codes), _ptr(q.scales), q.fmt, rows, K, ptr,
+                                      _dt(out), ld, wp, wn, st)
+    _check("spec_mx_dequantize", rc)
+    return out
+
+
+def spec_rmsnorm_mx(x, weight, eps=1e-6, *, residual=None, residual_out=None, fmt=SPEC_MX_E4M3,
+                    out=None, workspace=None, stream=None):
+    """h = x + residual (x without one), then the RMS norm of h's rows times weight [K], block-
+    scaled in `fmt`. x, residual [rows, K] (or [..., K], evenly spaced rows) of one dtype.
+    Returns (h, MXTensor); h is residual_out (which may be x or residual itself), a new tensor,
+    or x when there is no residual."""
+    ptr, rows, K, ldx = _rows(x, "x")
+    if tuple(weight.shape) != (K,):
+        raise ValueError(f"weight must be [{K}]")
+    rp, ldr, op, ldo, h = None, K, None, K, x
+    if residual is not None:
+        if residual.shape != x.shape or residual.dtype != x.dtype:
+            raise ValueError("residual must have x's shape and dtype")
+        rp, _, _, ldr = _rows(residual, "residual")
+        h = residual_out if residual_out is not None else torch.empty(
+            x.shape, dtype=x.dtype, device=x.device)
+        if h.shape != x.shape or h.dtype != x.dtype:
+            raise ValueError("residual_out must have x's shape and dtype")
+        op, _, _, ldo = _rows(h, "residual_out")
+    elif residual_out is not None:
+        raise ValueError("residual_out is an output of the form with a residual")
+    if out is None:
+        out = MXTensor.empty(rows, K, fmt, x.device)
+    if out.shape != (rows, K) or out.fmt != fmt:
+        raise ValueError("out must be an MXTensor of x's rows, width and the given format")
+    _same_device(x.device, weight=weight, residual=residual, residual_out=h, out=out)
+    with _Call(x.device, workspace, stream) as (wp, wn, st):
+        rc = lib().spec_rmsnorm_mx(ptr, ldx, rp, ldr, _dt(x), _ptr(weight), _dt(weight),
+                                   float(eps), rows, K, op, ldo, fmt, _ptr(out.codes),
+                                   _ptr(out.scales), wp, wn, st)
+    _check("spec_rmsnorm_mx", rc)
+    return h, out
+
+
+def spec_mx_logits(a, w, *, dtype=torch.bfloat16, out=None, workspace=None, stream=None):
+    """Logits [M, V] (bf16 or fp32) of the MXTensor rows a [M, K] against the vocabulary matrix
+    w [V, K]. `out` [M, V] (or [..., V]) may have any even row spacing, for instance one position
+    U[:, k] of U [R, gamma, V]."""
+    (M, K), (V, Kw) = a.shape, w.shape
+    if K != Kw:
+        raise ValueError(f"a has rows of {K} elements, w of {Kw}")
+    if out is None:
+        out = torch.empty(M, V, dtype=dtype, device=a.device)
+    ptr, rows, width, ld = _rows(out, "out")
+    if (rows, width) != (M, V):
+        raise ValueError(f"out must hold {M} rows of {V}")
+    _same_device(a.device, w=w, out=out)
+    with _Call(a.device, workspace, stream) as (wp, wn, st):
+        rc = lib().spec_mx_logits(_ptr(a.codes), _ptr(a.scales), a.fmt, _ptr(w.codes),
+                                  _ptr(w.scales), w.fmt, M, V, K, ptr, _dt(out), ld, wp, wn, st)
+    _check("spec_mx_logits", rc)
+    return out
+
+
+class TokenLogprobs:
+    """Outputs of spec_token_logprobs: logp, rank, entropy [rows], top_ids, top_logp
+    [rows, top]; None where not asked for."""
+
+    __slots__ = ("logp", "rank", "entropy", "top_ids", "top_logp")
+
+    def __init__(self, logp=None, rank=None, entropy=None, top_ids=None, top_logp=None):
+        self.logp, self.rank, self.entropy = logp, rank, entropy
+        self.top_ids, self.top_logp = top_ids, top_logp
+
+
+def spec_token_logprobs(logits, tokens, temperature=1.0, *, top=0, out=None, workspace=None,
+                        stream=None):
+    """Log-probability and rank of tokens[row] (int32, or None), entropy and the `top` most
+    likely tokens under softmax(logits[row] / temperature); logits [rows, V] (or [..., V], evenly
+    spaced rows). Rows whose token is -1 are left as they were. `out` is a TokenLogprobs whose
+    None fields are not computed."""
+    ptr, rows, V, ld = _rows(logits, "logits")
+    dev = logits.device
+    if not 0 <= top <= SPEC_LOGPROBS_MAX_TOP:
+        raise ValueError(f"top must be in [0, {SPEC_LOGPROBS_MAX_TOP}]")
+    if tokens is not None:
+        _i32_on(tokens, dev, "tokens")
+        if tokens.numel() != rows:
+            raise ValueError(f"tokens must hold {rows} ids")
+    if out is None:
+        # one allocation each for the fp32 and the int32 outputs
+        f = torch.empty(rows * (2 + top), dtype=torch.float32, device=dev)
+        i = torch.empty(rows * (1 + top), dtype=torch.int32, device=dev)
+        out = TokenLogprobs(
+            logp=None if tokens is None else f[:rows], rank=None if tokens is None else i[:rows],
+            entropy=f[rows:2 * rows],
+            top_ids=i[rows:].view(rows, top) if top else None,
+            top_logp=f[2 * rows:].view(rows, top) if top else None)
+    for name, dt, n in (("logp", torch.float32, rows), ("entropy", torch.float32, rows),
+                        ("top_logp", torch.float32, rows * top), ("rank", torch.int32, rows),
+                        ("top_ids", torch.int32, rows * top)):
+        t = getattr(out, name)
+        if t is not None and (t.dtype != dt or t.numel() != n or t.device != dev):
+            raise ValueError(f"{name} must hold {n} elements of {dt} on {dev}")
+    if tokens is None and (out.logp is not None or out.rank is not None):
+        raise ValueError("logp and rank need tokens")
+    with _Call(dev, workspace, stream) as (wp, wn, st):
+        rc = lib().spec_token_logprobs(
+            ptr, _dt(logits), ld, _ptr(tokens), float(temperature), rows, V, int(top),
+            _ptr(out.logp), _ptr(out.rank), _ptr(out.entropy), _ptr(out.top_ids),
+            _ptr(out.top_logp), wp, wn, st)
+    _check("spec_token_logprobs", rc)
+    return out
 
 
 def spec_device_status(workspace=None, clear=True, stream=None) -> int:

@@ -418,6 +418,112 @@ int spec_verify_rejection_flat(const void* target, const void* U, int l_dtype, c
                                int32_t* next_anchor, const uint32_t* allowed, void* ws,
                                size_t ws_bytes, void* stream);
 
+/*
+ * The vocabulary head in block-scaled (microscaled) floating point, and token log-probabilities.
+ *
+ * Block-scaled matrices. `rows` rows of K elements, padded with zeros to Kp = K rounded up to a
+ * multiple of SPEC_MX_GROUP. SPEC_MX_BLOCK consecutive elements of a row share one scale 2^e, the
+ * smallest power of two (e >= -127) for which no element of the block passes the format's
+ * largest value, so nothing saturates; an element is x * 2^-e rounded to the nearest value of
+ * the format, ties to the even code. Formats: SPEC_MX_E2M1, 4 bits, +-{0, 0.5, 1, 1.5, 2, 3, 4,
+ * 6}; SPEC_MX_E4M3, 8 bits, up to 448.
+ *   codes   [rows, Kp / 2] bytes (E2M1: element 2i in the lower half of byte i, 2i + 1 in the
+ *           upper half) or [rows, Kp] bytes (E4M3). 32-byte aligned.
+ *   scales  [ceil(rows / 128), Kp / 128, 32, 4, 4] bytes e + 127: the scale of row r, block b of
+ *           128-element group g is at [r / 128][g][r % 32][(r % 128) / 32][b]. A block of zeros
+ *           has e = -127; a block with an infinity or a NaN has the byte 255 and stands for NaN
+ *           in every element (SPEC_DEV_NONFINITE). Rows past `rows` of the last tile are 0.
+ *           16-byte aligned.
+ * The calls below take a workspace for its status word only (256 bytes, initialised by
+ * spec_workspace_init), so they may share it with any other call.
+ */
+#define SPEC_MX_E2M1 0
+#define SPEC_MX_E4M3 1
+#define SPEC_MX_BLOCK 32
+#define SPEC_MX_GROUP 128
+
+/* Bytes of the codes and of the scales of a block-scaled [rows, K] matrix (0 for bad sizes). */
+size_t spec_mx_code_bytes(int fmt, int rows, int K);
+size_t spec_mx_scale_bytes(int rows, int K);
+
+/*
+ * Quantise x [rows, K] (SPEC_F32 or SPEC_BF16, row stride ldx >= K elements) to `fmt`: the draft
+ * head's weights once when they are loaded, activations on their way into spec_mx_logits.
+ * No page defines this entry point; "Module deepseek_v4_mtp", Forward, names the head that the
+ * quantised matrix stands in for.
+ */
+int spec_mx_quantize(const void* x, int x_dtype, long long ldx, int rows, int K, int fmt,
+                     uint8_t* codes, uint8_t* scales, void* ws, size_t ws_bytes, void* stream);
+
+/* The numbers a block-scaled matrix stands for: out [rows, K] (row stride ld_out). Every value
+ * of both formats whose scale a bf16 input can produce is exact in SPEC_BF16 and SPEC_F32,
+ * down to the type's subnormals. */
+int spec_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int fmt, int rows, int K,
+                       void* out, int out_dtype, long long ld_out, void* ws, size_t ws_bytes,
+                       void* stream);
+
+/*
+ * Residual addition, root-mean-square norm and quantisation in one pass.
+ * Defines: "Module deepseek_v4_mtp", Forward (the draft logits are lm_head(rms_norm(h))).
+ *   h = x + residual (rounded to `dtype`, as it is stored), or h = x without a residual;
+ *   y = h * rsqrt(mean(h^2) + eps) * weight, in fp32; codes, scales = quantised y.
+ * Arguments:
+ *   x, residual   [rows, K] of `dtype`, row strides ldx and ldr; residual may be NULL.
+ *   weight        [K] of w_dtype.
+ *   residual_out  [rows, K] of `dtype`, row stride ldo: h (required with a residual, else
+ *                 ignored). May be x or residual itself; must not overlap them otherwise.
+ *   fmt           of codes / scales.
+ * A row with an infinity or a NaN sets SPEC_DEV_NONFINITE and has NaN scales.
+ */
+int spec_rmsnorm_mx(const void* x, long long ldx, const void* residual, long long ldr, int dtype,
+                    const void* weight, int w_dtype, float eps, int rows, int K,
+                    void* residual_out, long long ldo, int fmt, uint8_t* codes, uint8_t* scales,
+                    void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Logits of block-scaled hidden rows against a block-scaled vocabulary matrix.
+ * Defines: "Module deepseek_v4_mtp", Forward (logits = lm_head(.)), for one draft position or a
+ *   whole window: out[m, v] = sum_k a[m, k] w[v, k], products exact, sums in fp32.
+ * Arguments:
+ *   a_codes, a_scales, a_fmt   [M, K] hidden rows (spec_rmsnorm_mx, spec_mx_quantize).
+ *   w_codes, w_scales, w_fmt   [V, K] vocabulary matrix (spec_mx_quantize).
+ *   out           [M, V] of out_dtype, row stride ld_out >= V elements (so that a position of
+ *                 U [R, gamma, V] is written in place). Elements past V of a row are untouched.
+ * A NaN scale makes the logits of its row (or column) NaN. SPEC_DEV_TIMEOUT as elsewhere.
+ */
+int spec_mx_logits(const uint8_t* a_codes, const uint8_t* a_scales, int a_fmt,
+                   const uint8_t* w_codes, const uint8_t* w_scales, int w_fmt, int M, int V,
+                   int K, void* out, int out_dtype, long long ld_out, void* ws, size_t ws_bytes,
+                   void* stream);
+
+/* Largest `top` of spec_token_logprobs. */
+#define SPEC_LOGPROBS_MAX_TOP 32
+
+/*
+ * Log-probabilities of given tokens with rank, entropy and the most likely alternatives, in one
+ * pass over the logits. No page defines this entry point: it reports the distribution that
+ * spec_target_stats normalises ("[DeepSeek-6] DSpark", section 3), per emitted token.
+ *   p = softmax(logits[row, :] / T) (T = 1 if temperature is 0);
+ *   logp = log p(token); rank = 1 + the number of tokens with a larger logit;
+ *   entropy = -sum_v p log p; top_ids / top_logp: the `top` largest logits of the row in
+ *   descending order, ties to the lowest id. Tokens of logit -inf (masked, or truncated) have no
+ *   place among them: missing places get id -1 and log-probability -inf.
+ * Arguments:
+ *   logits   [rows, V], row stride ld >= V elements; dtype SPEC_F32 or SPEC_BF16.
+ *   tokens   [rows] int32, or NULL (no logp, no rank). A row whose token is -1 is neither read
+ *            nor written: the padding of out_tokens of the verify calls. Any other id outside
+ *            [0, V) sets SPEC_DEV_BAD_TOKEN; its logp is NaN and its rank 0.
+ *   top      0 .. SPEC_LOGPROBS_MAX_TOP.
+ *   logp, rank, entropy [rows], top_ids, top_logp [rows, top]: each optional (NULL to skip).
+ * A row whose normaliser is not finite (a NaN or +inf logit, or nothing above -inf) sets
+ * SPEC_DEV_NONFINITE; its log-probabilities and entropy are NaN, its rank still counts larger
+ * logits, and NaN logits have no place in top_ids.
+ */
+int spec_token_logprobs(const void* logits, int dtype, long long ld, const int32_t* tokens,
+                        float temperature, int rows, int V, int top, float* logp, int32_t* rank,
+                        float* entropy, int32_t* top_ids, float* top_logp, void* ws,
+                        size_t ws_bytes, void* stream);
+
 /* Largest R * (gamma + 1) that spec_verify_greedy_noalloc accepts. */
 #define SPEC_NOALLOC_MAX_ROWS 65536
 
