@@ -103,6 +103,10 @@ constexpr int kMaxPropGrid = 256;
 // A 2-D or 3-D bf16 tensor map with a 128-byte swizzle (false if it cannot be encoded).
 bool make_tensor_map_bf16(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
                           const cuuint64_t* strides_bytes, const cuuint32_t* box);
+// A 2-D map of block-scaled codes (rows of Kp elements) in boxes of 128 elements x box_rows, with
+// a 128-byte swizzle; 4-bit codes are spread over 16-byte units on the way.
+bool make_tensor_map_codes(CUtensorMap* m, const void* base, int fmt, int Kp, int rows,
+                           int box_rows);
 // Consume the test request that makes the next tensor-core launch never load its first W2
 // tile (spec_test_stall_next_markov).
 int take_stall_request();

@@ -223,6 +223,57 @@ __device__ __forceinline__ void tmem_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+// ------------------------------------------------------------------------------ block scaling
+
+// Instruction descriptor, kind::mxf8f6f4 with E8M0 scales: element formats af / bf (0 = E4M3,
+// 5 = E2M1), both operands K-major, fp32 accumulate, M x N. block_scale_ids adds which byte of a
+// scale word (which 32-element block of a 128-element group) the instruction uses.
+__host__ __device__ constexpr uint32_t idesc_mx(int M, int N, int af, int bf) {
+  return ((uint32_t)af << 7) | ((uint32_t)bf << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
+         ((uint32_t)(M >> 7) << 27);
+}
+__host__ __device__ constexpr uint32_t block_scale_ids(int b) {
+  return ((uint32_t)b << 29) | ((uint32_t)b << 4);
+}
+
+// D (+)= (A * sA) x (B * sB)^T, 32 elements of K, one scale a row of each operand in tensor
+// memory (lane = row % 32, column = row / 32).
+__device__ __forceinline__ void mma_mx(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                       uint32_t idesc, uint32_t sa_tmem, uint32_t sb_tmem,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X "
+      "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+      : "memory");
+}
+
+// Shared-memory descriptor of a scale tile for tcgen05.cp: 32 rows of 16 bytes, contiguous (no
+// swizzle, 8-row groups 128 B apart).
+__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 16) |
+         ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+}
+
+// 512 bytes of shared memory to four columns of tensor memory: row i to lane i of each of the
+// four lane quarters.
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+               : "memory");
+}
+
+// Untiled bulk copy global -> shared (16-byte aligned addresses and size).
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1], %2, [%3], %4;" ::"r"(smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
 // Packed pair arithmetic (two fp32 lanes per instruction).
 __device__ __forceinline__ unsigned long long pack2(float lo, float hi) {
   unsigned long long r;
