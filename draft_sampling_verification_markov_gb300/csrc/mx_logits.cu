@@ -50,7 +50,7 @@ struct LogitArgs {
   int NT, n_tok;        // hidden rows of a tile, tiles of them
   long long units;
   int stages;
-  uint32_t copied;      // code bytes a stage's copies report (the gaps of 4-bit codes not counted)
+  uint32_t w_bytes, a_bytes;  // code bytes a copy reports (the gaps of 4-bit codes not counted)
   uint32_t idesc;       // without N
   int odt;
   bool pairs;           // two tokens in one store
@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 3);
       mbar_init(&empty[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -109,84 +109,90 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const uint32_t sf_col0 = 2 * p.NT;  // scales after the two accumulators
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 2 || warp == 3) {
     // ------------------------------------------------------------------ copies
-    if (lane == 0) {
-      const uint64_t once = policy_evict_first(), keep = policy_evict_last();
-      int s = 0;
-      uint32_t ph = 0;
-      bool ok = true, first = true;
-      for (long long u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
-        const int vt = (int)(u / p.n_tok), tt = (int)(u - (long long)vt * p.n_tok);
-        const int m0 = tt * p.NT, rows = min(p.NT, p.M - m0);
-        const int st0 = m0 / kTileRows, st1 = (m0 + rows - 1) / kTileRows;
-        const uint32_t bytes = p.copied + kTileBytes * (2 + st1 - st0);
-        const uint8_t* wsp = p.ws + (size_t)vt * p.G * kTileBytes;
-        const uint8_t* asp = p.as + (size_t)st0 * p.G * kTileBytes;
-        for (int g = 0; g < p.G; ++g) {
-          ok = mbar_wait(&empty[s], ph ^ 1, abort, p.status);
-          if (!ok) break;
-          mbar_arrive_expect_tx(&full[s], bytes);
-          if (!(p.stall && first))
-            tma_load_2d(sA + (size_t)s * kWBytes, &map_w, g * kGroup, vt * kTileV, &full[s],
-                        p.n_tok > 1 ? keep : once);
-          first = false;
-          tma_load_2d(sB + (size_t)s * b_bytes, &map_a, g * kGroup, m0, &full[s], keep);
+    // one warp each for the vocabulary codes, the hidden codes and the scales
+    const uint32_t lead = elect_lane();
+    const uint64_t keep = policy_evict_last();
+    const uint64_t w_pol = p.n_tok > 1 ? keep : policy_evict_first();
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true, skip = p.stall;
+    for (long long u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
+      const int vt = (int)(u / p.n_tok), tt = (int)(u - (long long)vt * p.n_tok);
+      const int m0 = tt * p.NT, rows = min(p.NT, p.M - m0);
+      const int st0 = m0 / kTileRows, st1 = (m0 + rows - 1) / kTileRows;
+      const uint8_t* wsp = p.ws + (size_t)vt * p.G * kTileBytes;
+      const uint8_t* asp = p.as + (size_t)st0 * p.G * kTileBytes;
+      for (int g = 0; g < p.G; ++g) {
+        ok = mbar_wait_warp(&empty[s], ph ^ 1, abort, p.status);
+        if (!ok) break;
+        if (warp == 0) {
+          expect_tx_if(lead, &full[s], p.w_bytes);
+          tma_load_2d_if(skip ? 0 : lead, sA + (size_t)s * kWBytes, &map_w, g * kGroup,
+                         vt * kTileV, &full[s], w_pol);
+          skip = false;
+        } else if (warp == 2) {
+          expect_tx_if(lead, &full[s], p.a_bytes);
+          tma_load_2d_if(lead, sB + (size_t)s * b_bytes, &map_a, g * kGroup, m0, &full[s], keep);
+        } else {
           unsigned char* sc = sS + (size_t)s * kScaleBytes;
-          bulk_load(sc, wsp + (size_t)g * kTileBytes, kTileBytes, &full[s],
-                    p.n_tok > 1 ? keep : once);
-          bulk_load(sc + kTileBytes, asp + (size_t)g * kTileBytes, kTileBytes, &full[s], keep);
+          expect_tx_if(lead, &full[s], kTileBytes * (2 + st1 - st0));
+          bulk_load_if(lead, sc, wsp + (size_t)g * kTileBytes, kTileBytes, &full[s], w_pol);
+          bulk_load_if(lead, sc + kTileBytes, asp + (size_t)g * kTileBytes, kTileBytes, &full[s],
+                       keep);
           if (st1 > st0)
-            bulk_load(sc + 2 * kTileBytes, asp + (size_t)(p.G + g) * kTileBytes, kTileBytes,
-                      &full[s], keep);
-          if (++s == S) { s = 0; ph ^= 1; }
+            bulk_load_if(lead, sc + 2 * kTileBytes, asp + (size_t)(p.G + g) * kTileBytes,
+                         kTileBytes, &full[s], keep);
         }
+        if (++s == S) { s = 0; ph ^= 1; }
       }
-      // copies in flight land before the CTA's shared memory goes away
-      for (int i = 0; i < S; ++i) mbar_drain(&full[i], i < s ? ph : (ph ^ 1));
     }
+    // copies in flight land before the CTA's shared memory goes away
+    for (int i = 0; i < S; ++i) mbar_drain(&full[i], i < s ? ph : (ph ^ 1));
+    __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA
-    if (lane == 0) {
-      int s = 0, as = 0;
-      uint32_t ph = 0, aph[2] = {0, 0};
-      bool ok = true;
-      for (long long u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
-        const int tt = (int)(u % p.n_tok), m0 = tt * p.NT, rows = min(p.NT, p.M - m0);
-        const int n = (rows + 15) & ~15;
-        const uint32_t idesc = p.idesc | ((uint32_t)(n >> 3) << 17);
-        const bool two = m0 / kTileRows != (m0 + rows - 1) / kTileRows;
-        ok = mbar_wait(&acc_empty[as], aph[as] ^ 1, abort, p.status);
+    const uint32_t lead = elect_lane();
+    int s = 0, as = 0;
+    uint32_t ph = 0, aph = 0;
+    bool ok = true;
+    for (long long u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
+      const int tt = (int)(u % p.n_tok), m0 = tt * p.NT, rows = min(p.NT, p.M - m0);
+      const int n = (rows + 15) & ~15;
+      const uint32_t idesc = p.idesc | ((uint32_t)(n >> 3) << 17);
+      const bool two = m0 / kTileRows != (m0 + rows - 1) / kTileRows;
+      ok = mbar_wait_warp(&acc_empty[as], aph ^ 1, abort, p.status);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d = tmem + as * p.NT;
+      for (int g = 0; g < p.G; ++g) {
+        ok = mbar_wait_warp(&full[s], ph, abort, p.status);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tmem + as * p.NT;
-        for (int g = 0; g < p.G; ++g) {
-          ok = mbar_wait(&full[s], ph, abort, p.status);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t sc = smem_u32(sS + (size_t)s * kScaleBytes);
-          const uint32_t sa = tmem + sf_col0 + s * kScaleCols, sb = sa + 4;
-          copy_scales(sa, scale_desc(sc));
-          copy_scales(sb, scale_desc(sc + kTileBytes));
-          if (two) copy_scales(sb + 4, scale_desc(sc + 2 * kTileBytes));
-          const uint64_t da = sw128_desc(smem_u32(sA + (size_t)s * kWBytes));
-          const uint64_t db = sw128_desc(smem_u32(sB + (size_t)s * b_bytes));
+        const uint32_t sc = smem_u32(sS + (size_t)s * kScaleBytes);
+        const uint32_t sa = tmem + sf_col0 + s * kScaleCols, sb = sa + 4;
+        copy_scales(lead, sa, scale_desc(sc));
+        copy_scales(lead, sb, scale_desc(sc + kTileBytes));
+        if (two) copy_scales(lead, sb + 4, scale_desc(sc + 2 * kTileBytes));
+        const uint64_t da = sw128_desc(smem_u32(sA + (size_t)s * kWBytes));
+        const uint64_t db = sw128_desc(smem_u32(sB + (size_t)s * b_bytes));
 #pragma unroll
-          for (int b = 0; b < 4; ++b)  // 32 bytes of a row a step
-            mma_mx(d, da + 2 * b, db + 2 * b, idesc | block_scale_ids(b), sa,
-                   sb + (m0 % kTileRows) / 32, (g | b) != 0);
-          mma_commit(&empty[s]);
-          if (++s == S) { s = 0; ph ^= 1; }
-        }
-        if (!ok) break;
-        mma_commit(&acc_full[as]);
-        aph[as] ^= 1;
-        as ^= 1;
+        for (int b = 0; b < 4; ++b)  // 32 bytes of a row a step
+          mma_mx(lead, d, da + 2 * b, db + 2 * b, idesc | block_scale_ids(b), sa,
+                 sb + (m0 % kTileRows) / 32, (g | b) != 0);
+        mma_commit_if(lead, &empty[s]);
+        if (++s == S) { s = 0; ph ^= 1; }
       }
-      // every MMA issued here completes before tensor memory is released
-      mma_commit(done);
-      mbar_drain(done, 0);
+      if (!ok) break;
+      mma_commit_if(lead, &acc_full[as]);
+      as ^= 1;
+      if (as == 0) aph ^= 1;
     }
+    // every MMA issued here completes before tensor memory is released
+    mma_commit_if(lead, done);
+    mbar_drain(done, 0);
+    __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------------------------ epilogue
     const int q = warp & 3;  // the lane quarter this warp may read
@@ -274,7 +280,8 @@ cudaError_t launch_mx_logits(const uint8_t* ac, const uint8_t* as, int af, const
   const int cols = (kTmemCols - 2 * p.NT) / kScaleCols;
   S = S < kMaxStages ? S : kMaxStages;
   p.stages = S < cols ? S : cols;
-  p.copied = (uint32_t)(kTileV * code_row(wf, kGroup) + p.NT * code_row(af, kGroup));
+  p.w_bytes = (uint32_t)(kTileV * code_row(wf, kGroup));
+  p.a_bytes = (uint32_t)(p.NT * code_row(af, kGroup));
   const int e2m1 = 5, e4m3 = 0;  // the instruction's format codes
   p.idesc = tc::idesc_mx(kTileV, 0, wf == SPEC_MX_E2M1 ? e2m1 : e4m3,
                          af == SPEC_MX_E2M1 ? e2m1 : e4m3);
