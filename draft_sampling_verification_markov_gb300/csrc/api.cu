@@ -982,7 +982,8 @@ int spec_token_logprobs(const void* logits, int dtype, long long ld, const int32
                         float temperature, int rows, int V, int top, float* logp, int32_t* rank,
                         float* entropy, int32_t* top_ids, float* top_logp, void* ws,
                         size_t ws_bytes, void* stream) {
-  if (rows < 0 || rows > (1 << 30) || V < 1 || (long long)rows * V > (1LL << 46) || ld < V)
+  if (rows < 0 || rows > (1 << 30) || V < 1 || V > (1 << 30) ||
+      (long long)rows * V > (1LL << 46) || ld < V)
     return SPEC_ERR_INVALID_ARG;
   if (!dtype_ok(dtype)) return SPEC_ERR_UNSUPPORTED_DTYPE;
   if (!(temperature >= 0.0f) || !isfinite(temperature) || top < 0) return SPEC_ERR_INVALID_ARG;

@@ -1,4 +1,24 @@
-// logprobs.cu -- log-probabilities of given tokens with rank, entropy and top alternatives.
+// logprobs.cu -- log-probabilities of given tokens with rank, entropy and top alternatives, in
+// one pass over the logits.
+//
+// With z = x / T, m = max z and e = exp(z - m):  S = sum e,  S1 = sum e (z - m);
+//   log p(t) = z_t - m - log S,   entropy = log S - S1 / S,   rank = 1 + #{x > x_t}.
+// A thread keeps (max, S, S1) of its elements in the base-2 scale t = (x - max) log2(e) / T and
+// rescales S and S1 where its maximum grows (2^d S, 2^d (S1 + d S) for a shift d); the pieces are
+// merged the same way in a fixed order.
+//
+// The largest k <= 32 logits need no second pass. The maxima of 64 groups of the first batch
+// bound the k-th largest logit from below (k groups hold a logit at least as large as the k-th
+// group maximum). After that batch, a 16-byte piece of the row goes on a list when its maximum
+// reaches the bound: a few hundred pieces of a row of 129280 logits. At the end the same argument
+// on the listed maxima gives a bound that few elements reach; those are reloaded and ranked by
+// counting, larger logits first, then lower ids. Rows that defeat the bound (long ascending runs,
+// hundreds of equal logits) overflow a list and take a radix selection over the row instead.
+//
+// Few rows are split over a thread-block cluster of up to 8 CTAs, which merge through distributed
+// shared memory: no workspace, one launch.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -8,70 +28,509 @@
 namespace spec {
 namespace {
 
-constexpr int kThreads = 512;
+namespace cg = cooperative_groups;
 
-// One block a row: a pass for the maximum, one for the sums and the rank, one a place of the
-// alternatives (the largest logit after the place before it).
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBatch = 4;             // 16-byte pieces a thread has in flight, and as many next
+constexpr int kMaxTop = SPEC_LOGPROBS_MAX_TOP;
+constexpr int kPieces = 1024;         // listed pieces at most
+constexpr int kKeys = 512;            // elements ranked at most
+constexpr int kGroups = 64;           // maxima behind a bound; at least 2 * kMaxTop
+constexpr uint32_t kFull = 0xffffffffu;
+
+struct Sums {
+  float m, s, s1;  // maximum logit, S, S1 (t in base 2)
+};
+
+struct Shared {
+  float group[kGroups];
+  float bound;
+  int n_pieces, n_keys;
+  uint32_t piece[kPieces];
+  float piece_max[kPieces];
+  unsigned long long keys[kKeys];
+  unsigned long long top[kMaxTop];    // this CTA's largest, in order; 0 = none
+  Sums sums[kWarps];
+  int count[kWarps];
+  Sums total;
+  int total_count;
+  // radix selection
+  int hist[256];
+  uint32_t prefix;
+  int need, running;
+  int scan[kWarps];
+};
+
+// Ordered bits: larger floats have larger bits, zeros of both signs are equal. 0 stands for
+// "no place" (NaN and -inf).
+__device__ __forceinline__ uint32_t order_bits(float x) {
+  if (!(x > -INFINITY)) return 0;
+  const uint32_t b = __float_as_uint(x + 0.0f);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float order_value(uint32_t u) {
+  return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
+}
+__device__ __forceinline__ unsigned long long make_key(uint32_t bits, int id) {
+  return ((unsigned long long)bits << 32) | (0xffffffffu - (uint32_t)id);
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+__device__ __forceinline__ Sums merge(Sums a, Sums b, float c) {
+  if (b.m > a.m) {
+    const Sums x = a;
+    a = b;
+    b = x;
+  }
+  if (b.m > -INFINITY && !(b.s == 0.0f)) {
+    const float d = (b.m - a.m) * c, f = fast_exp2(fmaxf(d, -256.0f));
+    a.s1 += f * (b.s1 + fmaxf(d, -256.0f) * b.s);
+    a.s += f * b.s;
+  } else {
+    a.s += b.s;  // 0, or the NaN of a part without a maximum
+  }
+  return a;
+}
+
+// ------------------------------------------------------------------------------ a row's pieces
+
+// A row as 16-byte pieces at 16-byte aligned addresses: piece j holds ids j * N - head ...; the
+// first and the last piece may be partly outside the row.
 template <int DT>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobArgs a) {
-  const int row = blockIdx.x;
-  const int t = a.tokens ? a.tokens[row] : -1;
-  if (a.tokens && t == -1) return;
+struct Row {
+  static constexpr int N = DT == SPEC_BF16 ? 8 : 4;
+  const char* base;  // address of piece 0
+  int head, V;
+
+  __device__ Row(const void* x, size_t off, int V_) : V(V_) {
+    const char* p = static_cast<const char*>(x) + off * (16 / N);
+    const int mis = (int)(reinterpret_cast<uintptr_t>(p) & 15);
+    base = p - mis;
+    head = mis / (16 / N);
+  }
+  __device__ int pieces() const { return (head + V + N - 1) / N; }
+
+  // Piece j, with -inf outside the row and past `end`.
+  __device__ __forceinline__ uint4 load(int j, int end) const {
+    const uint32_t none = DT == SPEC_BF16 ? 0xff80ff80u : 0xff800000u;
+    if (j >= end) return make_uint4(none, none, none, none);
+    const int v = j * N - head;
+    if (v >= 0 && v + N <= V) return ld_stream16(base + (size_t)j * 16);
+    uint32_t w[4] = {none, none, none, none};
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (v + i < 0 || v + i >= V) continue;
+      if constexpr (DT == SPEC_BF16) {
+        const uint32_t b =
+            __ldg(reinterpret_cast<const unsigned short*>(base + (size_t)j * 16) + i);
+        w[i / 2] = i & 1 ? (w[i / 2] & 0xffffu) | b << 16 : (w[i / 2] & 0xffff0000u) | b;
+      } else {
+        w[i] = __ldg(reinterpret_cast<const uint32_t*>(base + (size_t)j * 16) + i);
+      }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+template <int DT>
+__device__ __forceinline__ void unpack(const uint4& q, float (&x)[Row<DT>::N]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (DT == SPEC_BF16) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    } else {
+      x[i] = __uint_as_float(w[i]);
+    }
+  }
+}
+
+// Maximum of a piece (NaN ignored, -inf if nothing else).
+template <int DT>
+__device__ __forceinline__ float piece_max(const float (&x)[Row<DT>::N]) {
+  float m = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+  if constexpr (DT == SPEC_BF16) m = fmaxf(m, fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+  return m;
+}
+
+// Elements of a piece larger than the given token's logit.
+template <int DT>
+__device__ __forceinline__ int count_larger(const uint4& q, float xt) {
+  if constexpr (DT == SPEC_BF16) {
+    // two comparisons and two additions an instruction; counts up to 8 are exact in bf16
+    const __nv_bfloat162 t = __float2bfloat162_rn(xt);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    __nv_bfloat162 n = __hgt2(*reinterpret_cast<const __nv_bfloat162*>(&w[0]), t);
+#pragma unroll
+    for (int i = 1; i < 4; ++i)
+      n = __hadd2(n, __hgt2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), t));
+    return (int)(__low2float(n) + __high2float(n));
+  } else {
+    float x[4];
+    unpack<DT>(q, x);
+    return (x[0] > xt) + (x[1] > xt) + (x[2] > xt) + (x[3] > xt);
+  }
+}
+
+// ------------------------------------------------------------------------------ bounds
+
+// The k-th largest of 64 group maxima (a group: four neighbouring threads), a lower bound of the
+// k-th largest of the elements behind `local`. Every thread calls it and gets the bound.
+__device__ __forceinline__ float bound_of(Shared& sh, float local, int k) {
+  const int lane = threadIdx.x & 31;
+  local = fmaxf(local, __shfl_xor_sync(kFull, local, 1));
+  local = fmaxf(local, __shfl_xor_sync(kFull, local, 2));
+  if ((lane & 3) == 0) sh.group[threadIdx.x >> 2] = local;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const float a = sh.group[lane], b = sh.group[lane + 32];
+    int ra = 0, rb = b <= a ? 1 : 0;  // places; equal maxima in order of their index
+    ra = b > a ? 1 : 0;
+#pragma unroll
+    for (int i = 1; i < 32; ++i) {
+      const int o = (lane + i) & 31;
+      const float p = __shfl_sync(kFull, a, o), q = __shfl_sync(kFull, b, o);
+      ra += (p > a || (p == a && o < lane)) + (q > a);
+      rb += (p >= b) + (q > b || (q == b && o < lane));
+    }
+    if (ra == k - 1) sh.bound = a;
+    if (rb == k - 1) sh.bound = b;
+  }
+  __syncthreads();
+  return sh.bound;
+}
+
+// ------------------------------------------------------------------------------ radix selection
+
+// The k largest elements of pieces [j0, j1) into sh.keys (sh.n_keys of them), whatever their order
+// and however many are equal: the k-th largest value by its leading bytes, then every larger
+// element and the first of the equal ones.
+template <int DT>
+__device__ __noinline__ void select_radix(Shared& sh, const Row<DT>& row, int j0, int j1, int k) {
+  constexpr int N = Row<DT>::N;
+  constexpr int kBits = DT == SPEC_BF16 ? 16 : 32;  // a bf16's ordered bits are the upper half
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    sh.prefix = 0;
+    sh.need = k;
+    sh.n_keys = 0;
+    sh.running = 0;
+  }
+  bool all = false;  // fewer than k elements have a place
+  for (int shift = kBits - 8; shift >= 0 && !all; shift -= 8) {
+    sh.hist[tid] = 0;
+    __syncthreads();
+    const uint32_t prefix = sh.prefix;
+    for (int j = j0 + tid; j < j1; j += kThreads) {
+      float x[N];
+      unpack<DT>(row.load(j, j1), x);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const uint32_t u = order_bits(x[i]);
+        const uint32_t b = u >> (32 - kBits);
+        // shift + 8 may be the whole width, where every element matches
+        if (u && (shift + 8 == kBits || (b >> (shift + 8)) == prefix))
+          atomicAdd(&sh.hist[(b >> shift) & 255], 1);
+      }
+    }
+    __syncthreads();
+    if (tid == 0) {
+      int cum = 0, b = 255;
+      for (; b >= 0 && cum + sh.hist[b] < sh.need; --b) cum += sh.hist[b];
+      if (b < 0) {
+        sh.need = -1;
+      } else {
+        sh.prefix = prefix << 8 | (uint32_t)b;
+        sh.need -= cum;
+      }
+    }
+    __syncthreads();
+    all = sh.need < 0;
+    __syncthreads();
+  }
+  const uint32_t cut = all ? 0 : sh.prefix;
+  const int need = all ? 0 : sh.need;
+  for (int j = j0; j < j1; j += kThreads) {  // ascending, a piece a thread
+    float x[N];
+    unpack<DT>(row.load(j + tid, j1), x);
+    uint32_t same = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t u = order_bits(x[i]), b = u >> (32 - kBits);
+      if (u && (all || b > cut)) sh.keys[atomicAdd(&sh.n_keys, 1)] =
+          make_key(u, (j + tid) * N - row.head + i);
+      if (u && !all && b == cut) same |= 1u << i;
+    }
+    if (sh.running >= need) continue;  // uniform: written between the barriers below only
+    // place of this thread's equal elements among all of them
+    int c = __popc(same), at = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kFull, at, o);
+      if (lane >= o) at += y;
+    }
+    if (lane == 31) sh.scan[warp] = at;
+    __syncthreads();
+    int before = sh.running + at - c, sum = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += sh.scan[w];
+      sum += sh.scan[w];
+    }
+    for (uint32_t s = same; s && before < need; s &= s - 1, ++before) {
+      const int i = __ffs(s) - 1;
+      uint32_t u = 0;
+#pragma unroll
+      for (int q = 0; q < N; ++q)
+        if (q == i) u = order_bits(x[q]);
+      sh.keys[atomicAdd(&sh.n_keys, 1)] = make_key(u, (j + tid) * N - row.head + i);
+    }
+    __syncthreads();
+    if (tid == 0) sh.running += sum;
+    __syncthreads();
+  }
+  __syncthreads();
+}
+
+// ------------------------------------------------------------------------------ kernel
+
+template <int DT, bool TOP>
+__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs a, int split) {
+  constexpr int N = Row<DT>::N;
+  __shared__ Shared sh;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int row = blockIdx.x / split, part = blockIdx.x % split;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int t = a.tokens ? a.tokens[row] : 0;
+  if (a.tokens && t == -1) return;  // the whole cluster
   const bool bad = t < 0 || t >= a.V;
-  if (a.tokens && bad && threadIdx.x == 0) atomicOr(a.status, SPEC_DEV_BAD_TOKEN);
   const size_t off = (size_t)row * a.ld;
-  const float xt = bad ? INFINITY : ld_elem<DT>(a.x, off + t);
-  float m = -INFINITY;
-  for (int v = threadIdx.x; v < a.V; v += kThreads) m = fmaxf(m, ld_elem<DT>(a.x, off + v));
-  m = block_merge({m, 0.0f, 0}).m;
-  float s = 0.0f, s1 = 0.0f, rank = 0.0f;
-  for (int v = threadIdx.x; v < a.V; v += kThreads) {
-    const float x = ld_elem<DT>(a.x, off + v);
-    const float z = (x - m) * a.scale, e = expf(z);
-    s += e;
-    if (!(e == 0.0f)) s1 += e * z;
-    rank += x > xt ? 1.0f : 0.0f;
+  const Row<DT> r(a.x, off, a.V);
+  const int np = r.pieces(), per = (np + split - 1) / split;
+  const int j0 = part * per, j1 = min(np, j0 + per);
+  const float c = a.scale * kLog2e;
+
+  uint4 cur[kBatch], nxt[kBatch];
+#pragma unroll
+  for (int b = 0; b < kBatch; ++b) cur[b] = r.load(j0 + tid + b * kThreads, j1);
+  const float xt = bad || !a.tokens ? INFINITY : ld_elem<DT>(a.x, off + t);
+
+  Sums acc = {-INFINITY, 0.0f, 0.0f};
+  int larger = 0;
+  float bound = INFINITY;
+  if (TOP && tid == 0) {
+    sh.n_pieces = 0;
+    sh.n_keys = 0;
   }
-  s = block_sum(s);
-  s1 = block_sum(s1);
-  rank = block_sum(rank);
-  const bool finite = s > 0.0f && s < INFINITY && m > -INFINITY;
-  const float ls = finite ? logf(s) : NAN;
-  if (threadIdx.x == 0) {
-    if (!finite) atomicOr(a.status, SPEC_DEV_NONFINITE);
-    if (a.tokens && a.logp) a.logp[row] = bad ? NAN : (xt - m) * a.scale - ls;
-    if (a.tokens && a.rank) a.rank[row] = bad ? 0 : (int)rank + 1;
-    if (a.entropy) a.entropy[row] = ls - s1 / s;
-  }
-  float px = INFINITY;
-  int pi = -1;
-  for (int j = 0; j < a.top; ++j) {
-    StatsAcc b = stats_empty();
-    for (int v = threadIdx.x; v < a.V; v += kThreads) {
-      const float x = ld_elem<DT>(a.x, off + v);
-      if ((x < px || (x == px && v > pi)) && x > b.m) b = {x, 0.0f, v};
+  if (TOP) {
+    float first = -INFINITY;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      float x[N];
+      unpack<DT>(cur[b], x);
+      first = fmaxf(first, piece_max<DT>(x));
     }
-    b = block_merge(b);
-    px = b.m;
-    pi = b.idx;
-    const bool none = b.m == -INFINITY;
-    if (threadIdx.x == 0) {
-      const size_t o = (size_t)row * a.top + j;
-      if (a.top_ids) a.top_ids[o] = none ? -1 : pi;
-      if (a.top_logp) a.top_logp[o] = none ? -INFINITY : (px - m) * a.scale - ls;
+    bound = bound_of(sh, first, a.top);
+    // nothing of -inf has a place
+    bound = fmaxf(bound, -3.402823466e38f);
+  }
+  for (int jb = j0 + tid; jb - tid < j1; jb += kBatch * kThreads) {
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+      nxt[b] = r.load(jb + (kBatch + b) * kThreads, j1);
+    float pm[kBatch], bm = -INFINITY;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      float x[N];
+      unpack<DT>(cur[b], x);
+      pm[b] = piece_max<DT>(x);
+      bm = fmaxf(bm, pm[b]);
+      if (TOP && pm[b] >= bound) {
+        const int at = atomicAdd(&sh.n_pieces, 1);
+        if (at < kPieces) {
+          sh.piece[at] = jb + b * kThreads;
+          sh.piece_max[at] = pm[b];
+        }
+      }
+    }
+    if (bm > acc.m) {
+      if (acc.m > -INFINITY) {
+        const float d = fmaxf((acc.m - bm) * c, -256.0f), f = fast_exp2(d);
+        acc.s1 = f * (acc.s1 + d * acc.s);
+        acc.s *= f;
+      }
+      acc.m = bm;
+    }
+    // a thread that has seen nothing above -inf measures from 0: its terms are 0, or NaN
+    const float m = acc.m > -INFINITY ? acc.m : 0.0f;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      float x[N];
+      unpack<DT>(cur[b], x);
+      float s = 0.0f, s1 = 0.0f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float z = max_nan((x[i] - m) * c, -256.0f), e = fast_exp2(z);
+        s += e;
+        s1 = fmaf(e, z, s1);
+      }
+      acc.s += s;
+      acc.s1 += s1;
+      larger += count_larger<DT>(cur[b], xt);
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) cur[b] = nxt[b];
+  }
+
+  // this CTA's sums
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    Sums y;
+    y.m = __shfl_down_sync(kFull, acc.m, o);
+    y.s = __shfl_down_sync(kFull, acc.s, o);
+    y.s1 = __shfl_down_sync(kFull, acc.s1, o);
+    acc = merge(acc, y, c);
+    larger += __shfl_down_sync(kFull, larger, o);
+  }
+  if (lane == 0) {
+    sh.sums[warp] = acc;
+    sh.count[warp] = larger;
+  }
+  if (TOP && tid < kMaxTop) sh.top[tid] = 0;
+  __syncthreads();
+  if (tid == 0) {
+    for (int w = 1; w < kWarps; ++w) {
+      acc = merge(acc, sh.sums[w], c);
+      larger += sh.count[w];
+    }
+    sh.total = acc;
+    sh.total_count = larger;
+  }
+  if (TOP) {
+    const int n = sh.n_pieces;
+    bool fits = n <= kPieces;
+    if (fits) {
+      float local = -INFINITY;
+      for (int i = tid; i < n; i += kThreads) local = fmaxf(local, sh.piece_max[i]);
+      // fewer listed pieces than places leave the first bound
+      const float cut = fmaxf(bound_of(sh, local, a.top), bound);
+      for (int i = tid; i < n; i += kThreads) {
+        if (sh.piece_max[i] < cut) continue;
+        const int j = sh.piece[i];
+        float x[N];
+        unpack<DT>(r.load(j, j1), x);
+#pragma unroll
+        for (int q = 0; q < N; ++q)
+          if (x[q] >= cut) {
+            const int at = atomicAdd(&sh.n_keys, 1);
+            if (at < kKeys) sh.keys[at] = make_key(order_bits(x[q]), j * N - r.head + q);
+          }
+      }
+      __syncthreads();
+      fits = sh.n_keys <= kKeys;
+    }
+    __syncthreads();
+    if (!fits) select_radix<DT>(sh, r, j0, j1, a.top);
+    const int nk = sh.n_keys;
+    for (int i = tid; i < nk; i += kThreads) {
+      const unsigned long long key = sh.keys[i];
+      int place = 0;
+      for (int q = 0; q < nk; ++q) place += sh.keys[q] > key;
+      if (place < a.top) sh.top[place] = key;
     }
   }
+
+  // the cluster's parts, merged by its first CTA
+  if (split > 1) cluster.sync(); else __syncthreads();
+  if (part == 0) {
+    Sums sum = sh.total;
+    int count = sh.total_count;
+    if (tid < 32) {  // every lane the same
+      for (int p = 1; p < split; ++p) {
+        const Shared* other = cluster.map_shared_rank(&sh, p);
+        sum = merge(sum, other->total, c);
+        count += other->total_count;
+      }
+      const bool finite = sum.s > 0.0f && sum.s < INFINITY && sum.m > -INFINITY;
+      const float ls = finite ? logf(sum.s) : NAN;
+      if (lane == 0) {
+        if (!finite) atomicOr(a.status, SPEC_DEV_NONFINITE);
+        if (a.tokens && bad) atomicOr(a.status, SPEC_DEV_BAD_TOKEN);
+        if (a.logp) a.logp[row] = bad ? NAN : (xt - sum.m) * a.scale - ls;
+        if (a.rank) a.rank[row] = bad ? 0 : count + 1;
+        if (a.entropy) a.entropy[row] = ls - sum.s1 / sum.s * kLn2;
+        sh.total = {sum.m, ls, 0.0f};  // for the alternatives below
+      }
+    }
+    if (TOP) {
+      __syncthreads();
+      const float m = sh.total.m, ls = sh.total.s;
+      // place of each part's entry among all parts' entries
+      const int p = tid / kMaxTop, e = tid % kMaxTop;
+      static_assert(kThreads / kMaxTop == 8 && kKeys >= kThreads,
+                    "one thread an entry of up to 8 parts");
+      unsigned long long key = 0;
+      int place = kMaxTop;
+      if (p < split && e < a.top)
+        key = split > 1 ? *cluster.map_shared_rank(&sh.top[e], p) : sh.top[e];
+      if (split > 1) {
+        sh.keys[tid] = key;
+        __syncthreads();
+      }
+      if (key) {
+        place = e;
+        for (int o = 0; o < split; ++o) {
+          if (o == p) continue;
+          for (int q = 0; q < a.top; ++q) place += sh.keys[o * kMaxTop + q] > key;
+        }
+      }
+      const size_t at = (size_t)row * a.top;
+      if (place < a.top) {
+        const float x = order_value((uint32_t)(key >> 32));
+        if (a.top_ids) a.top_ids[at + place] = (int)(0xffffffffu - (uint32_t)key);
+        if (a.top_logp) a.top_logp[at + place] = (x - m) * a.scale - ls;
+      }
+      // places that no logit has
+      const int have = __syncthreads_count(key != 0);
+      if (tid < a.top && tid >= have) {
+        if (a.top_ids) a.top_ids[at + tid] = -1;
+        if (a.top_logp) a.top_logp[at + tid] = -INFINITY;
+      }
+    }
+  }
+  if (split > 1) cluster.sync();
 }
 
 }  // namespace
 
 cudaError_t launch_token_logprobs(const LogprobArgs& a, int dt, cudaStream_t s) {
   TraceScope ts(SPEC_KCLASS_OTHER, s);
+  // split rows while that leaves CTAs without work and the parts have a batch or more
+  const int batch = kThreads * kBatch * (dt == SPEC_BF16 ? 8 : 4);
+  int split = 1;
+  while (split < 8 && (long long)a.rows * split < 4 * num_sms() && a.V >= 2 * split * batch)
+    split *= 2;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = split;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.rows * split);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
   if (dt == SPEC_BF16)
-    logprobs_kernel<SPEC_BF16><<<a.rows, kThreads, 0, s>>>(a);
-  else
-    logprobs_kernel<SPEC_F32><<<a.rows, kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+    return a.top ? cudaLaunchKernelEx(&cfg, logprobs_kernel<SPEC_BF16, true>, a, split)
+                 : cudaLaunchKernelEx(&cfg, logprobs_kernel<SPEC_BF16, false>, a, split);
+  return a.top ? cudaLaunchKernelEx(&cfg, logprobs_kernel<SPEC_F32, true>, a, split)
+               : cudaLaunchKernelEx(&cfg, logprobs_kernel<SPEC_F32, false>, a, split);
 }
 
 }  // namespace spec

@@ -295,9 +295,17 @@ cudaError_t launch_mx_logits(const uint8_t* ac, const uint8_t* as, int af, const
     return cudaErrorInvalidValue;
   const size_t smem = kSmemFixed + p.stages * stage;
   static_assert(kSmemFixed - 1024 >= (2 * kMaxStages + 5) * 8 + 8, "room for the barriers");
-  cudaError_t e = cudaFuncSetAttribute(logits_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)kSmemMax);
+  // the opt-in to large shared memory holds for the life of the device's context
+  static bool opted[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev >= 64 || !__atomic_load_n(&opted[dev], __ATOMIC_RELAXED)) {
+    e = cudaFuncSetAttribute(logits_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)kSmemMax);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) __atomic_store_n(&opted[dev], true, __ATOMIC_RELAXED);
+  }
   const int grid = (int)(p.units < num_sms() ? p.units : num_sms());
   logits_kernel<<<grid, kThreads, smem, s>>>(mw, ma, p);
   return cudaGetLastError();

@@ -582,68 +582,104 @@ def spec_verify_rejection_flat(target, U, W1, W2, anchors, draft_tokens, draft_l
 
 
 # ----------------------------------------------------------------------------- vocabulary head
+# These calls are short at small batches, so their binding is written for few host operations:
+# one allocation a matrix, plain integers for pointers, views made only when they are read.
+
+_DTYPES = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
+def _mx_sizes(rows, K, fmt):
+    """Bytes of a row of codes, number of scale tiles, 128-element groups of a row."""
+    if fmt not in (SPEC_MX_E2M1, SPEC_MX_E4M3):
+        raise ValueError("fmt must be SPEC_MX_E2M1 or SPEC_MX_E4M3")
+    if K < 1:
+        raise ValueError("a block-scaled matrix has at least one column")
+    G = -(-K // SPEC_MX_GROUP)
+    return G * (SPEC_MX_GROUP // 2 if fmt == SPEC_MX_E2M1 else SPEC_MX_GROUP), -(-rows // 128), G
+
 
 class MXTensor:
     """A block-scaled [rows, K] matrix: `codes` [rows, Kp / 2] (SPEC_MX_E2M1) or [rows, Kp]
-    (SPEC_MX_E4M3) and `scales` [ceil(rows / 128), Kp / 128, 32, 4, 4], both uint8 on the device
-    (Kp = K rounded up to a multiple of 128; the layout is that of include/spec_markov.h)."""
+    (SPEC_MX_E4M3) and `scales` [ceil(rows / 128), Kp / 128, 32, 4, 4], both contiguous uint8 on
+    the device (Kp = K rounded up to a multiple of 128; the layout is that of
+    include/spec_markov.h)."""
 
-    __slots__ = ("codes", "scales", "fmt", "K")
+    __slots__ = ("rows", "K", "fmt", "device", "_buf", "_codes", "_scales", "_cp", "_sp")
 
     def __init__(self, codes, scales, fmt, K):
-        rows, G = codes.shape[0], -(-K // SPEC_MX_GROUP)
-        if fmt not in (SPEC_MX_E2M1, SPEC_MX_E4M3):
-            raise ValueError("fmt must be SPEC_MX_E2M1 or SPEC_MX_E4M3")
-        width = G * (SPEC_MX_GROUP // 2 if fmt == SPEC_MX_E2M1 else SPEC_MX_GROUP)
-        if codes.dtype != torch.uint8 or tuple(codes.shape) != (rows, width):
-            raise ValueError(f"codes must be uint8 [rows, {width}]")
-        if scales.dtype != torch.uint8 or tuple(scales.shape) != (-(-rows // 128), G, 32, 4, 4):
-            raise ValueError(f"scales must be uint8 {(-(-rows // 128), G, 32, 4, 4)}")
+        rows = codes.shape[0]
+        width, tiles, G = _mx_sizes(rows, K, fmt)
+        if codes.dtype != torch.uint8 or codes.shape != (rows, width) or not codes.is_contiguous():
+            raise ValueError(f"codes must be contiguous uint8 [rows, {width}]")
+        if (scales.dtype != torch.uint8 or scales.shape != (tiles, G, 32, 4, 4)
+                or not scales.is_contiguous()):
+            raise ValueError(f"scales must be contiguous uint8 {(tiles, G, 32, 4, 4)}")
         if scales.device != codes.device:
             raise ValueError("codes and scales must be on one device")
-        self.codes, self.scales, self.fmt, self.K = codes, scales, fmt, K
+        self.rows, self.K, self.fmt, self.device = rows, K, fmt, codes.device
+        self._buf, self._codes, self._scales = None, codes, scales
+        self._cp, self._sp = codes.data_ptr(), scales.data_ptr()
 
-    @staticmethod
-    def empty(rows, K, fmt, device):
+    @classmethod
+    def empty(cls, rows, K, fmt, device):
         """An uninitialised [rows, K] matrix for a call to write."""
-        G = -(-K // SPEC_MX_GROUP)
-        width = G * (SPEC_MX_GROUP // 2 if fmt == SPEC_MX_E2M1 else SPEC_MX_GROUP)
-        return MXTensor(torch.empty(rows, width, dtype=torch.uint8, device=device),
-                        torch.empty(-(-rows // 128), G, 32, 4, 4, dtype=torch.uint8,
-                                    device=device), fmt, K)
+        width, tiles, G = _mx_sizes(rows, K, fmt)
+        q = cls.__new__(cls)
+        q._buf = buf = torch.empty(rows * width + tiles * G * 512, dtype=torch.uint8,
+                                   device=device)
+        q.rows, q.K, q.fmt, q.device = rows, K, fmt, buf.device
+        q._codes = q._scales = None
+        q._cp = buf.data_ptr()
+        q._sp = q._cp + rows * width
+        return q
+
+    @property
+    def codes(self):
+        if self._codes is None:
+            width = _mx_sizes(self.rows, self.K, self.fmt)[0]
+            self._codes = self._buf[:self.rows * width].view(self.rows, width)
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            width, tiles, G = _mx_sizes(self.rows, self.K, self.fmt)
+            self._scales = self._buf[self.rows * width:].view(tiles, G, 32, 4, 4)
+        return self._scales
 
     @property
     def shape(self):
-        return self.codes.shape[0], self.K
-
-    @property
-    def device(self):
-        return self.codes.device
+        return self.rows, self.K
 
 
 def _rows(t, name):
-    """(pointer, rows, width, row stride) of a matrix whose rows are contiguous: two dimensions
+    """(address, rows, width, row stride) of a matrix whose rows are contiguous: two dimensions
     with any row stride, or more dimensions that flatten into evenly spaced rows."""
     if not t.is_cuda:
         raise ValueError("libspecmarkov takes device tensors")
-    if t.dim() < 1:
+    shape, strides = t.shape, t.stride()
+    if not shape:
         raise ValueError(f"{name} must have at least one dimension")
-    width = t.shape[-1]
-    if width > 1 and t.stride(-1) != 1:
+    width = shape[-1]
+    if width > 1 and strides[-1] != 1:
         raise ValueError(f"the rows of {name} must be contiguous")
+    if len(shape) == 2:
+        return t.data_ptr(), shape[0], width, strides[0] if shape[0] > 1 else width
     # leading dimensions of more than one index, innermost last
-    lead = [(n, st) for n, st in zip(t.shape[:-1], t.stride()[:-1]) if n != 1]
+    lead = [(n, st) for n, st in zip(shape[:-1], strides[:-1]) if n != 1]
     rows = 1
     for n, _ in lead:
         rows *= n
     if not lead or rows == 0:
-        return ctypes.c_void_p(t.data_ptr()), rows, width, width
-    ld, span = lead[-1][1], lead[-1][1]
+        return t.data_ptr(), rows, width, width
+    ld = span = lead[-1][1]
     for n, st in reversed(lead):
         if st != span:
             raise ValueError(f"the rows of {name} must be evenly spaced")
         span = st * n
-    return ctypes.c_void_p(t.data_ptr()), rows, width, ld
+    return t.data_ptr(), rows, width, ld
 
 
 def _same_device(dev, **tensors):
@@ -652,31 +688,41 @@ def _same_device(dev, **tensors):
             raise ValueError(f"{name} must be on {dev}")
 
 
-class _Call:
-    """The device, stream and status workspace of one call: the operands' device is current
-    while it runs, and its current stream is the default."""
+def _dtype_code(dtype):
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"logits and weights must be float32 or bfloat16, got {dtype}")
+    return code
 
-    def __init__(self, dev, workspace, stream):
-        if dev.type != "cuda":
-            raise ValueError("libspecmarkov takes device tensors")
-        self.dev, self.guard = dev, None
-        self.ws, self.s = workspace, stream
 
-    def __enter__(self):
-        if torch.cuda.current_device() != self.dev.index:
-            self.guard = torch.cuda.device(self.dev)
-            self.guard.__enter__()
-        ws = self.ws or default_workspace(self.dev)
-        if ws.device != self.dev:
-            self.__exit__(None, None, None)
-            raise ValueError(f"the workspace must be on {self.dev}")
-        ws.reserve(256, self.s)
-        return ws.ptr, ws.nbytes, _stream(self.s)
+def _launch(name, dev, workspace, stream, *args):
+    """Call entry point `name` with args, the status workspace and the stream. The operands'
+    device is current meanwhile and its current stream is the default."""
+    if dev.type != "cuda":
+        raise ValueError("libspecmarkov takes device tensors")
+    i = dev.index
+    ws = workspace or _default_ws.get(i) or default_workspace(dev)
+    if ws.device.index != i:
+        raise ValueError(f"the workspace must be on {dev}")
+    if torch._C._cuda_getDevice() != i:
+        with torch.cuda.device(i):
+            return _launch(name, dev, ws, stream, *args)
+    if ws.buf is None:
+        ws.reserve(256, stream)
+    st = _raw_stream(i) if stream is None else stream.cuda_stream
+    rc = getattr(_lib or lib(), name)(*args, ws.buf.data_ptr() + ws._off, ws.nbytes, st)
+    if rc != SPEC_OK:
+        raise SpecError(name, rc)
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-            self.guard = None
+
+def _mx_out(out, rows, K, fmt, dev):
+    if out is None:
+        return MXTensor.empty(rows, K, fmt, dev)
+    if out.rows != rows or out.K != K or out.fmt != fmt:
+        raise ValueError("out must be an MXTensor of x's rows, width and the given format")
+    if out.device != dev:
+        raise ValueError(f"out must be on {dev}")
+    return out
 
 
 def spec_mx_quantize(x, fmt=SPEC_MX_E2M1, *, out=None, workspace=None, stream=None):
@@ -684,31 +730,25 @@ def spec_mx_quantize(x, fmt=SPEC_MX_E2M1, *, out=None, workspace=None, stream=No
     `fmt`: SPEC_MX_E2M1 for a vocabulary matrix, SPEC_MX_E4M3 for hidden rows. `out` is an
     MXTensor to write into."""
     ptr, rows, K, ld = _rows(x, "x")
-    if out is None:
-        out = MXTensor.empty(rows, K, fmt, x.device)
-    if out.shape != (rows, K) or out.fmt != fmt:
-        raise ValueError("out must be an MXTensor of x's rows, width and the given format")
-    _same_device(x.device, out=out)
-    with _Call(x.device, workspace, stream) as (wp, wn, st):
-        rc = lib().spec_mx_quantize(ptr, _dt(x), ld, rows, K, fmt, _ptr(out.codes),
-                                    _ptr(out.scales), wp, wn, st)
-    _check("spec_mx_quantize", rc)
+    dt, dev = _dtype_code(x.dtype), x.device
+    out = _mx_out(out, rows, K, fmt, dev)
+    _launch("spec_mx_quantize", dev, workspace, stream, ptr, dt, ld, rows, K, fmt, out._cp,
+            out._sp)
     return out
 
 
 def spec_mx_dequantize(q, *, dtype=torch.bfloat16, out=None, workspace=None, stream=None):
     """The numbers that the MXTensor q stands for, [rows, K] of `dtype` (bf16 or fp32)."""
-    rows, K = q.shape
+    rows, K, dev = q.rows, q.K, q.device
     if out is None:
-        out = torch.empty(rows, K, dtype=dtype, device=q.device)
+        out = torch.empty(rows, K, dtype=dtype, device=dev)
     ptr, orows, width, ld = _rows(out, "out")
-    if (orows, width) != (rows, K):
+    if orows != rows or width != K:
         raise ValueError("out must have q's rows and width")
-    _same_device(q.device, out=out)
-    with _Call(q.device, workspace, stream) as (wp, wn, st):
-        rc = lib().spec_mx_dequantize(_ptr(q.codes), _ptr(q.scales), q.fmt, rows, K, ptr,
-                                      _dt(out), ld, wp, wn, st)
-    _check("spec_mx_dequantize", rc)
+    if out.device != dev:
+        raise ValueError(f"out must be on {dev}")
+    _launch("spec_mx_dequantize", dev, workspace, stream, q._cp, q._sp, q.fmt, rows, K, ptr,
+            _dtype_code(out.dtype), ld)
     return out
 
 
@@ -719,30 +759,29 @@ def spec_rmsnorm_mx(x, weight, eps=1e-6, *, residual=None, residual_out=None, fm
     Returns (h, MXTensor); h is residual_out (which may be x or residual itself), a new tensor,
     or x when there is no residual."""
     ptr, rows, K, ldx = _rows(x, "x")
-    if tuple(weight.shape) != (K,):
-        raise ValueError(f"weight must be [{K}]")
-    rp, ldr, op, ldo, h = None, K, None, K, x
+    dt, dev = _dtype_code(x.dtype), x.device
+    if weight.shape != (K,) or not weight.is_contiguous():
+        raise ValueError(f"weight must be contiguous [{K}]")
+    rp = op = None
+    ldr = ldo = K
+    h = x
     if residual is not None:
         if residual.shape != x.shape or residual.dtype != x.dtype:
             raise ValueError("residual must have x's shape and dtype")
         rp, _, _, ldr = _rows(residual, "residual")
-        h = residual_out if residual_out is not None else torch.empty(
-            x.shape, dtype=x.dtype, device=x.device)
-        if h.shape != x.shape or h.dtype != x.dtype:
-            raise ValueError("residual_out must have x's shape and dtype")
+        if residual_out is None:
+            h = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        else:
+            h = residual_out
+            if h.shape != x.shape or h.dtype != x.dtype:
+                raise ValueError("residual_out must have x's shape and dtype")
         op, _, _, ldo = _rows(h, "residual_out")
     elif residual_out is not None:
         raise ValueError("residual_out is an output of the form with a residual")
-    if out is None:
-        out = MXTensor.empty(rows, K, fmt, x.device)
-    if out.shape != (rows, K) or out.fmt != fmt:
-        raise ValueError("out must be an MXTensor of x's rows, width and the given format")
-    _same_device(x.device, weight=weight, residual=residual, residual_out=h, out=out)
-    with _Call(x.device, workspace, stream) as (wp, wn, st):
-        rc = lib().spec_rmsnorm_mx(ptr, ldx, rp, ldr, _dt(x), _ptr(weight), _dt(weight),
-                                   float(eps), rows, K, op, ldo, fmt, _ptr(out.codes),
-                                   _ptr(out.scales), wp, wn, st)
-    _check("spec_rmsnorm_mx", rc)
+    _same_device(dev, weight=weight, residual=residual, residual_out=h)
+    out = _mx_out(out, rows, K, fmt, dev)
+    _launch("spec_rmsnorm_mx", dev, workspace, stream, ptr, ldx, rp, ldr, dt, weight.data_ptr(),
+            _dtype_code(weight.dtype), eps, rows, K, op, ldo, fmt, out._cp, out._sp)
     return h, out
 
 
@@ -750,19 +789,17 @@ def spec_mx_logits(a, w, *, dtype=torch.bfloat16, out=None, workspace=None, stre
     """Logits [M, V] (bf16 or fp32) of the MXTensor rows a [M, K] against the vocabulary matrix
     w [V, K]. `out` [M, V] (or [..., V]) may have any even row spacing, for instance one position
     U[:, k] of U [R, gamma, V]."""
-    (M, K), (V, Kw) = a.shape, w.shape
-    if K != Kw:
-        raise ValueError(f"a has rows of {K} elements, w of {Kw}")
+    M, V, K, dev = a.rows, w.rows, a.K, a.device
+    if K != w.K:
+        raise ValueError(f"a has rows of {K} elements, w of {w.K}")
     if out is None:
-        out = torch.empty(M, V, dtype=dtype, device=a.device)
+        out = torch.empty(M, V, dtype=dtype, device=dev)
     ptr, rows, width, ld = _rows(out, "out")
-    if (rows, width) != (M, V):
+    if rows != M or width != V:
         raise ValueError(f"out must hold {M} rows of {V}")
-    _same_device(a.device, w=w, out=out)
-    with _Call(a.device, workspace, stream) as (wp, wn, st):
-        rc = lib().spec_mx_logits(_ptr(a.codes), _ptr(a.scales), a.fmt, _ptr(w.codes),
-                                  _ptr(w.scales), w.fmt, M, V, K, ptr, _dt(out), ld, wp, wn, st)
-    _check("spec_mx_logits", rc)
+    _same_device(dev, w=w, out=out)
+    _launch("spec_mx_logits", dev, workspace, stream, a._cp, a._sp, a.fmt, w._cp, w._sp, w.fmt, M,
+            V, K, ptr, _dtype_code(out.dtype), ld)
     return out
 
 
@@ -770,11 +807,58 @@ class TokenLogprobs:
     """Outputs of spec_token_logprobs: logp, rank, entropy [rows], top_ids, top_logp
     [rows, top]; None where not asked for."""
 
-    __slots__ = ("logp", "rank", "entropy", "top_ids", "top_logp")
+    __slots__ = ("_f", "_i", "_n", "_top", "_t")
 
     def __init__(self, logp=None, rank=None, entropy=None, top_ids=None, top_logp=None):
-        self.logp, self.rank, self.entropy = logp, rank, entropy
-        self.top_ids, self.top_logp = top_ids, top_logp
+        self._f = self._i = None
+        self._t = {"logp": logp, "rank": rank, "entropy": entropy, "top_ids": top_ids,
+                   "top_logp": top_logp}
+
+    @classmethod
+    def empty(cls, rows, top, tokens, device):
+        """Uninitialised outputs for a call to write: every field, logp and rank only with
+        `tokens`."""
+        r = cls.__new__(cls)
+        r._n, r._top = rows, top
+        r._f = torch.empty(rows * (2 + top), dtype=torch.float32, device=device)
+        r._i = torch.empty(rows * (1 + top), dtype=torch.int32, device=device)
+        r._t = {} if tokens else {"logp": None, "rank": None}
+        if not top:
+            r._t["top_ids"] = r._t["top_logp"] = None
+        return r
+
+    def _get(self, name):
+        if name not in self._t:
+            n, top = self._n, self._top
+            self._t[name] = (
+                self._f[:n] if name == "logp" else self._f[n:2 * n] if name == "entropy" else
+                self._i[:n] if name == "rank" else
+                (self._i[n:] if name == "top_ids" else self._f[2 * n:]).view(n, top))
+        return self._t[name]
+
+    logp = property(lambda self: self._get("logp"))
+    rank = property(lambda self: self._get("rank"))
+    entropy = property(lambda self: self._get("entropy"))
+    top_ids = property(lambda self: self._get("top_ids"))
+    top_logp = property(lambda self: self._get("top_logp"))
+
+    def _addresses(self, rows, top, dev):
+        """Addresses of logp, rank, entropy, top_ids, top_logp (None where not asked for)."""
+        if self._f is not None and (self._n, self._top) == (rows, top) and self._f.device == dev:
+            f, i, t = self._f.data_ptr(), self._i.data_ptr(), self._t
+            none = t.get("logp", t) is None
+            return (None if none else f, None if none else i, f + 4 * rows,
+                    i + 4 * rows if top else None, f + 8 * rows if top else None)
+        out = []
+        for name, dt, n in (("logp", torch.float32, rows), ("rank", torch.int32, rows),
+                            ("entropy", torch.float32, rows), ("top_ids", torch.int32, rows * top),
+                            ("top_logp", torch.float32, rows * top)):
+            t = self._get(name)
+            if t is not None and (t.dtype != dt or t.numel() != n or t.device != dev
+                                  or not t.is_contiguous()):
+                raise ValueError(f"{name} must hold {n} contiguous elements of {dt} on {dev}")
+            out.append(None if t is None else t.data_ptr())
+        return tuple(out)
 
 
 def spec_token_logprobs(logits, tokens, temperature=1.0, *, top=0, out=None, workspace=None,
@@ -784,36 +868,22 @@ def spec_token_logprobs(logits, tokens, temperature=1.0, *, top=0, out=None, wor
     spaced rows). Rows whose token is -1 are left as they were. `out` is a TokenLogprobs whose
     None fields are not computed."""
     ptr, rows, V, ld = _rows(logits, "logits")
-    dev = logits.device
+    dt, dev = _dtype_code(logits.dtype), logits.device
     if not 0 <= top <= SPEC_LOGPROBS_MAX_TOP:
         raise ValueError(f"top must be in [0, {SPEC_LOGPROBS_MAX_TOP}]")
+    tp = None
     if tokens is not None:
         _i32_on(tokens, dev, "tokens")
-        if tokens.numel() != rows:
-            raise ValueError(f"tokens must hold {rows} ids")
+        if tokens.numel() != rows or not tokens.is_contiguous():
+            raise ValueError(f"tokens must hold {rows} contiguous ids")
+        tp = tokens.data_ptr()
     if out is None:
-        # one allocation each for the fp32 and the int32 outputs
-        f = torch.empty(rows * (2 + top), dtype=torch.float32, device=dev)
-        i = torch.empty(rows * (1 + top), dtype=torch.int32, device=dev)
-        out = TokenLogprobs(
-            logp=None if tokens is None else f[:rows], rank=None if tokens is None else i[:rows],
-            entropy=f[rows:2 * rows],
-            top_ids=i[rows:].view(rows, top) if top else None,
-            top_logp=f[2 * rows:].view(rows, top) if top else None)
-    for name, dt, n in (("logp", torch.float32, rows), ("entropy", torch.float32, rows),
-                        ("top_logp", torch.float32, rows * top), ("rank", torch.int32, rows),
-                        ("top_ids", torch.int32, rows * top)):
-        t = getattr(out, name)
-        if t is not None and (t.dtype != dt or t.numel() != n or t.device != dev):
-            raise ValueError(f"{name} must hold {n} elements of {dt} on {dev}")
-    if tokens is None and (out.logp is not None or out.rank is not None):
+        out = TokenLogprobs.empty(rows, top, tokens is not None, dev)
+    lp, rank, ent, ti, tl = out._addresses(rows, top, dev)
+    if tp is None and (lp is not None or rank is not None):
         raise ValueError("logp and rank need tokens")
-    with _Call(dev, workspace, stream) as (wp, wn, st):
-        rc = lib().spec_token_logprobs(
-            ptr, _dt(logits), ld, _ptr(tokens), float(temperature), rows, V, int(top),
-            _ptr(out.logp), _ptr(out.rank), _ptr(out.entropy), _ptr(out.top_ids),
-            _ptr(out.top_logp), wp, wn, st)
-    _check("spec_token_logprobs", rc)
+    _launch("spec_token_logprobs", dev, workspace, stream, ptr, dt, ld, tp, temperature, rows, V,
+            top, lp, rank, ent, ti, tl)
     return out
 
 
