@@ -24,6 +24,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "tc_ptx.cuh"
 
 namespace spec {
 namespace {
@@ -38,6 +39,11 @@ constexpr int kPieces = 1024;         // listed pieces at most
 constexpr int kKeys = 512;            // elements ranked at most
 constexpr int kGroups = 64;           // maxima behind a bound; at least 2 * kMaxTop
 constexpr uint32_t kFull = 0xffffffffu;
+
+constexpr float kLowest2 = -256.0f;   // 2^kLowest2 is 0 in fp32
+// The fast sums need |max| < kFastMax and log2(e) / T < kFastScale: 2^101 * 2^20 is finite, and
+// (-2^100 + 2^99) * c is below -256 for every c > 2^-90.
+constexpr float kFastMax = 0x1p99f, kFastScale = 0x1p20f, kFastLeast = 0x1p-90f;
 
 struct Sums {
   float m, s, s1;  // maximum logit, S, S1 (t in base 2)
@@ -89,8 +95,8 @@ __device__ __forceinline__ Sums merge(Sums a, Sums b, float c) {
     b = x;
   }
   if (b.m > -INFINITY && !(b.s == 0.0f)) {
-    const float d = (b.m - a.m) * c, f = fast_exp2(fmaxf(d, -256.0f));
-    a.s1 += f * (b.s1 + fmaxf(d, -256.0f) * b.s);
+    const float d = (b.m - a.m) * c, f = fast_exp2(fmaxf(d, kLowest2));
+    a.s1 += f * (b.s1 + fmaxf(d, kLowest2) * b.s);
     a.s += f * b.s;
   } else {
     a.s += b.s;  // 0, or the NaN of a part without a maximum
@@ -152,12 +158,47 @@ __device__ __forceinline__ void unpack(const uint4& q, float (&x)[Row<DT>::N]) {
   }
 }
 
-// Maximum of a piece (NaN ignored, -inf if nothing else).
+__device__ __forceinline__ __nv_bfloat162 as_bf2(uint32_t w) {
+  return *reinterpret_cast<const __nv_bfloat162*>(&w);
+}
+__device__ __forceinline__ uint32_t as_word(__nv_bfloat162 v) {
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float max3f(float a, float b, float c) {
+  return fmaxf(a, fmaxf(b, c));
+}
+
+// Maximum of a piece (NaN ignored).
 template <int DT>
-__device__ __forceinline__ float piece_max(const float (&x)[Row<DT>::N]) {
-  float m = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-  if constexpr (DT == SPEC_BF16) m = fmaxf(m, fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-  return m;
+__device__ __forceinline__ float piece_max(const uint4& q) {
+  if constexpr (DT == SPEC_BF16) {
+    const uint32_t w = as_word(__hmax2(__hmax2(as_bf2(q.x), as_bf2(q.y)),
+                                       __hmax2(as_bf2(q.z), as_bf2(q.w))));
+    return fmaxf(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  } else {
+    return fmaxf(fmaxf(__uint_as_float(q.x), __uint_as_float(q.y)),
+                 fmaxf(__uint_as_float(q.z), __uint_as_float(q.w)));
+  }
+}
+
+// The piece with everything below -2^100 (masked logits) raised to it, NaN kept. Against a
+// maximum of less than 2^100 such a logit still has exp = 0, and (x - max) log2(e) / T stays
+// finite, so that its term of S1 is 0 too and needs no comparison of its own.
+template <int DT>
+__device__ __forceinline__ uint4 raised(const uint4& q) {
+  if constexpr (DT == SPEC_BF16) {
+    const __nv_bfloat162 low = as_bf2(0xf180f180u);
+    return make_uint4(as_word(__hmax2_nan(as_bf2(q.x), low)),
+                      as_word(__hmax2_nan(as_bf2(q.y), low)),
+                      as_word(__hmax2_nan(as_bf2(q.z), low)),
+                      as_word(__hmax2_nan(as_bf2(q.w), low)));
+  } else {
+    const float low = -0x1p100f;
+    return make_uint4(__float_as_uint(max_nan(__uint_as_float(q.x), low)),
+                      __float_as_uint(max_nan(__uint_as_float(q.y), low)),
+                      __float_as_uint(max_nan(__uint_as_float(q.z), low)),
+                      __float_as_uint(max_nan(__uint_as_float(q.w), low)));
+  }
 }
 
 // Elements of a piece larger than the given token's logit.
@@ -166,11 +207,8 @@ __device__ __forceinline__ int count_larger(const uint4& q, float xt) {
   if constexpr (DT == SPEC_BF16) {
     // two comparisons and two additions an instruction; counts up to 8 are exact in bf16
     const __nv_bfloat162 t = __float2bfloat162_rn(xt);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-    __nv_bfloat162 n = __hgt2(*reinterpret_cast<const __nv_bfloat162*>(&w[0]), t);
-#pragma unroll
-    for (int i = 1; i < 4; ++i)
-      n = __hadd2(n, __hgt2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), t));
+    const __nv_bfloat162 n = __hadd2(__hadd2(__hgt2(as_bf2(q.x), t), __hgt2(as_bf2(q.y), t)),
+                                     __hadd2(__hgt2(as_bf2(q.z), t), __hgt2(as_bf2(q.w), t)));
     return (int)(__low2float(n) + __high2float(n));
   } else {
     float x[4];
@@ -321,7 +359,11 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
   for (int b = 0; b < kBatch; ++b) cur[b] = r.load(j0 + tid + b * kThreads, j1);
   const float xt = bad || !a.tokens ? INFINITY : ld_elem<DT>(a.x, off + t);
 
-  Sums acc = {-INFINITY, 0.0f, 0.0f};
+#pragma unroll
+  for (int b = 0; b < kBatch; ++b) nxt[b] = r.load(j0 + tid + (kBatch + b) * kThreads, j1);
+
+  float am = -INFINITY;                                 // running maximum
+  unsigned long long as = tc::pack2(0.0f, 0.0f), as1 = as;  // S and S1, two partial sums each
   int larger = 0;
   float bound = INFINITY;
   if (TOP && tid == 0) {
@@ -331,61 +373,88 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
   if (TOP) {
     float first = -INFINITY;
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      float x[N];
-      unpack<DT>(cur[b], x);
-      first = fmaxf(first, piece_max<DT>(x));
-    }
-    bound = bound_of(sh, first, a.top);
-    // nothing of -inf has a place
-    bound = fmaxf(bound, -3.402823466e38f);
-  }
-  for (int jb = j0 + tid; jb - tid < j1; jb += kBatch * kThreads) {
-#pragma unroll
     for (int b = 0; b < kBatch; ++b)
-      nxt[b] = r.load(jb + (kBatch + b) * kThreads, j1);
-    float pm[kBatch], bm = -INFINITY;
+      first = max3f(first, piece_max<DT>(cur[b]), piece_max<DT>(nxt[b]));
+    // nothing of -inf has a place
+    bound = fmaxf(bound_of(sh, first, a.top), -3.402823466e38f);
+  }
+  const unsigned long long c2 = tc::pack2(c, c);
+  const bool small_c = c < kFastScale && c > kFastLeast;
+  for (int jb = j0 + tid; jb - tid < j1; jb += kBatch * kThreads) {
+    float bm = -INFINITY;
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      float x[N];
-      unpack<DT>(cur[b], x);
-      pm[b] = piece_max<DT>(x);
-      bm = fmaxf(bm, pm[b]);
-      if (TOP && pm[b] >= bound) {
+      const float pm = piece_max<DT>(cur[b]);
+      bm = fmaxf(bm, pm);
+      if (TOP && pm >= bound) {
         const int at = atomicAdd(&sh.n_pieces, 1);
         if (at < kPieces) {
           sh.piece[at] = jb + b * kThreads;
-          sh.piece_max[at] = pm[b];
+          sh.piece_max[at] = pm;
         }
       }
     }
-    if (bm > acc.m) {
-      if (acc.m > -INFINITY) {
-        const float d = fmaxf((acc.m - bm) * c, -256.0f), f = fast_exp2(d);
-        acc.s1 = f * (acc.s1 + d * acc.s);
-        acc.s *= f;
+    if (bm > am) {
+      if (am > -INFINITY) {
+        const float d = fmaxf((am - bm) * c, kLowest2), f = fast_exp2(d);
+        const unsigned long long f2 = tc::pack2(f, f);
+        as1 = tc::mul2(f2, tc::fma2(tc::pack2(d, d), as, as1));
+        as = tc::mul2(f2, as);
       }
-      acc.m = bm;
+      am = bm;
     }
-    // a thread that has seen nothing above -inf measures from 0: its terms are 0, or NaN
-    const float m = acc.m > -INFINITY ? acc.m : 0.0f;
+    if (small_c && fabsf(am) < kFastMax) {
+      const unsigned long long m2 = tc::pack2(-am, -am);
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        float x[N];
+        unpack<DT>(raised<DT>(cur[b]), x);
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+          const unsigned long long z = tc::mul2(tc::add2(tc::pack2(x[i], x[i + 1]), m2), c2);
+          float z0, z1;
+          tc::unpack2(z, z0, z1);
+          const unsigned long long e = tc::pack2(fast_exp2(z0), fast_exp2(z1));
+          as = tc::add2(as, e);
+          as1 = tc::fma2(e, z, as1);
+        }
+      }
+    } else {
+      // extreme maxima, extreme temperatures, or nothing above -inf yet (then measured from 0:
+      // the terms are 0, or NaN)
+      const float m = am > -INFINITY ? am : 0.0f;
+#pragma unroll 1
+      for (int b = 0; b < kBatch; ++b) {
+        float x[N];
+        unpack<DT>(b == 0 ? cur[0] : b == 1 ? cur[1] : b == 2 ? cur[2] : cur[3], x);
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+          const float z0 = max_nan((x[i] - m) * c, kLowest2);
+          const float z1 = max_nan((x[i + 1] - m) * c, kLowest2);
+          const unsigned long long e = tc::pack2(fast_exp2(z0), fast_exp2(z1));
+          as = tc::add2(as, e);
+          as1 = tc::fma2(e, tc::pack2(z0, z1), as1);
+        }
+      }
+    }
+    if (bm > xt) {
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) larger += count_larger<DT>(cur[b], xt);
+    }
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      float x[N];
-      unpack<DT>(cur[b], x);
-      float s = 0.0f, s1 = 0.0f;
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float z = max_nan((x[i] - m) * c, -256.0f), e = fast_exp2(z);
-        s += e;
-        s1 = fmaf(e, z, s1);
-      }
-      acc.s += s;
-      acc.s1 += s1;
-      larger += count_larger<DT>(cur[b], xt);
+      cur[b] = nxt[b];
+      nxt[b] = r.load(jb + (2 * kBatch + b) * kThreads, j1);
     }
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) cur[b] = nxt[b];
+  }
+  Sums acc;
+  {
+    float s0, s1;
+    acc.m = am;
+    tc::unpack2(as, s0, s1);
+    acc.s = s0 + s1;
+    tc::unpack2(as1, s0, s1);
+    acc.s1 = s0 + s1;
   }
 
   // this CTA's sums
