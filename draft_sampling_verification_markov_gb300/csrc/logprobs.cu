@@ -3,9 +3,9 @@
 //
 // With z = x / T, m = max z and e = exp(z - m):  S = sum e,  S1 = sum e (z - m);
 //   log p(t) = z_t - m - log S,   entropy = log S - S1 / S,   rank = 1 + #{x > x_t}.
-// A thread keeps (max, S, S1) of its elements in the base-2 scale t = (x - max) log2(e) / T and
-// rescales S and S1 where its maximum grows (2^d S, 2^d (S1 + d S) for a shift d); the pieces are
-// merged the same way in a fixed order.
+// A thread keeps S and S1 of its elements against a reference logit m of its own, in the base-2
+// scale (x - m) log2(e) / T, and moves them to another reference (2^d S, 2^d (S1 + d S) for a
+// shift d) where a logit is far above; the parts are merged the same way in a fixed order.
 //
 // The largest k <= 32 logits need no second pass. The maxima of 64 groups of the first batch
 // bound the k-th largest logit from below (k groups hold a logit at least as large as the k-th
@@ -35,25 +35,27 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBatch = 4;             // 16-byte pieces a thread has in flight, and as many next
 constexpr int kMaxTop = SPEC_LOGPROBS_MAX_TOP;
-constexpr int kPieces = 1024;         // listed pieces at most
+constexpr int kPieces = 512;          // listed pieces at most
 constexpr int kKeys = 512;            // elements ranked at most
 constexpr int kGroups = 64;           // maxima behind a bound; at least 2 * kMaxTop
 constexpr uint32_t kFull = 0xffffffffu;
 
 constexpr float kLowest2 = -256.0f;   // 2^kLowest2 is 0 in fp32
-// The fast sums need |max| < kFastMax and log2(e) / T < kFastScale: 2^101 * 2^20 is finite, and
-// (-2^100 + 2^99) * c is below -256 for every c > 2^-90.
-constexpr float kFastMax = 0x1p99f, kFastScale = 0x1p20f, kFastLeast = 0x1p-90f;
+// The fast sums need log2(e) / T = c in (kFastLeast, kFastScale) and a reference with |m| c below
+// kFastMax. Then fl(m c) is off by less than 2^-14; -2^100 c is finite; and (-2^100 - m) c is far
+// below -256, as |m| < 2^90.
+constexpr float kFastMax = 1024.0f, kFastScale = 0x1p20f, kFastLeast = 0x1p-80f;
 
 struct Sums {
-  float m, s, s1;  // maximum logit, S, S1 (t in base 2)
+  float m, s, s1;  // reference logit, S, S1 (in base 2)
 };
 
 struct Shared {
-  float group[kGroups];
+  alignas(16) float group[kGroups];
   float bound;
   int n_pieces, n_keys;
-  uint32_t piece[kPieces];
+  uint4 piece[kPieces];               // listed pieces: content, index, maximum
+  uint32_t piece_at[kPieces];
   float piece_max[kPieces];
   unsigned long long keys[kKeys];
   unsigned long long top[kMaxTop];    // this CTA's largest, in order; 0 = none
@@ -104,6 +106,27 @@ __device__ __forceinline__ Sums merge(Sums a, Sums b, float c) {
   return a;
 }
 
+// The sums of the first n lanes (a power of two) in every one of them: against their largest
+// reference, then added.
+template <int n>
+__device__ __forceinline__ Sums merge_lanes(Sums a, float c) {
+  float m = a.m;
+#pragma unroll
+  for (int o = n / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+  if (a.m > -INFINITY) {
+    const float d = fmaxf((a.m - m) * c, kLowest2), f = fast_exp2(d);
+    a.s1 = f * (a.s1 + d * a.s);
+    a.s *= f;
+  }  // else 0, or NaN
+  a.m = m;
+#pragma unroll
+  for (int o = n / 2; o > 0; o >>= 1) {
+    a.s += __shfl_xor_sync(kFull, a.s, o);
+    a.s1 += __shfl_xor_sync(kFull, a.s1, o);
+  }
+  return a;
+}
+
 // ------------------------------------------------------------------------------ a row's pieces
 
 // A row as 16-byte pieces at 16-byte aligned addresses: piece j holds ids j * N - head ...; the
@@ -122,8 +145,12 @@ struct Row {
   }
   __device__ int pieces() const { return (head + V + N - 1) / N; }
 
+  // Pieces jb + thread + b * kThreads, b < B.
+  template <int B>
+  __device__ __forceinline__ void load_batch(uint4 (&q)[B], int jb, int end) const;
+
   // Piece j, with -inf outside the row and past `end`.
-  __device__ __forceinline__ uint4 load(int j, int end) const {
+  __device__ __noinline__ uint4 load(int j, int end) const {
     const uint32_t none = DT == SPEC_BF16 ? 0xff80ff80u : 0xff800000u;
     if (j >= end) return make_uint4(none, none, none, none);
     const int v = j * N - head;
@@ -143,6 +170,21 @@ struct Row {
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
 };
+
+template <int DT>
+template <int B>
+__device__ __forceinline__ void Row<DT>::load_batch(uint4 (&q)[B], int jb, int end) const {
+  const int j = jb + threadIdx.x;
+  // whole batches inside the row: one address, no tests of single pieces
+  if (jb * N >= head && jb + B * kThreads <= end && (jb + B * kThreads) * N - head <= V) {
+    const char* p = base + (size_t)j * 16;
+#pragma unroll
+    for (int b = 0; b < B; ++b) q[b] = ld_stream16(p + b * kThreads * 16);
+  } else {
+#pragma unroll
+    for (int b = 0; b < B; ++b) q[b] = load(j + b * kThreads, end);
+  }
+}
 
 template <int DT>
 __device__ __forceinline__ void unpack(const uint4& q, float (&x)[Row<DT>::N]) {
@@ -182,8 +224,8 @@ __device__ __forceinline__ float piece_max(const uint4& q) {
 }
 
 // The piece with everything below -2^100 (masked logits) raised to it, NaN kept. Against a
-// maximum of less than 2^100 such a logit still has exp = 0, and (x - max) log2(e) / T stays
-// finite, so that its term of S1 is 0 too and needs no comparison of its own.
+// reference that the fast sums take such a logit still has exp = 0, and (x - m) c stays finite,
+// so that its term of S1 is 0 too and needs no comparison of its own.
 template <int DT>
 __device__ __forceinline__ uint4 raised(const uint4& q) {
   if constexpr (DT == SPEC_BF16) {
@@ -201,48 +243,176 @@ __device__ __forceinline__ uint4 raised(const uint4& q) {
   }
 }
 
-// Elements of a piece larger than the given token's logit.
+// Elements of a batch larger than the given token's logit.
 template <int DT>
-__device__ __forceinline__ int count_larger(const uint4& q, float xt) {
+__device__ __forceinline__ int count_larger(const uint4 (&q)[kBatch], float xt) {
   if constexpr (DT == SPEC_BF16) {
-    // two comparisons and two additions an instruction; counts up to 8 are exact in bf16
+    // two comparisons and two additions an instruction; counts up to 16 are exact in bf16
     const __nv_bfloat162 t = __float2bfloat162_rn(xt);
-    const __nv_bfloat162 n = __hadd2(__hadd2(__hgt2(as_bf2(q.x), t), __hgt2(as_bf2(q.y), t)),
-                                     __hadd2(__hgt2(as_bf2(q.z), t), __hgt2(as_bf2(q.w), t)));
+    __nv_bfloat162 n = __float2bfloat162_rn(0.0f);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+      n = __hadd2(n, __hadd2(__hadd2(__hgt2(as_bf2(q[b].x), t), __hgt2(as_bf2(q[b].y), t)),
+                             __hadd2(__hgt2(as_bf2(q[b].z), t), __hgt2(as_bf2(q[b].w), t))));
     return (int)(__low2float(n) + __high2float(n));
   } else {
-    float x[4];
-    unpack<DT>(q, x);
-    return (x[0] > xt) + (x[1] > xt) + (x[2] > xt) + (x[3] > xt);
+    int n = 0;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      float x[4];
+      unpack<DT>(q[b], x);
+      n += (x[0] > xt) + (x[1] > xt) + (x[2] > xt) + (x[3] > xt);
+    }
+    return n;
   }
+}
+
+// A thread's sums against a reference `m`, one of its logits and at most 32 octaves of
+// exp((max - m) / T) below its maximum: 2^32 times the number of logits is far from overflow, and
+// the reference changes in few batches. fma(x, c, -fl(m c)) is (x - m) c + delta with delta the
+// exact rounding error of m c, the same for every term: it is taken out of the sums where the
+// reference changes and at the end.
+struct RunningSums {
+  float m, limit;                    // reference, and the logit that calls for another
+  float most;                        // maximum
+  unsigned long long s, s1;          // S and S1, two partial sums each
+
+  __device__ __forceinline__ void start() {
+    m = limit = most = -INFINITY;
+    s = s1 = tc::pack2(0.0f, 0.0f);
+  }
+  __device__ __forceinline__ bool tame(float c) const { return fabsf(m) * c < kFastMax; }
+
+  // Sums that are free of delta, of exp((x - m') c) for another reference m'.
+  __device__ __forceinline__ void rebase(float to, float c, float delta) {
+    const float d = fmaxf((m - to) * c, kLowest2);
+    const float f = fast_exp2(d) * (1.0f - delta * kLn2), g = d - delta;
+    const unsigned long long f2 = tc::pack2(f, f);
+    s1 = tc::mul2(f2, tc::fma2(tc::pack2(g, g), s, s1));
+    s = tc::mul2(f2, s);
+  }
+  __device__ __forceinline__ float delta(float c) const { return fmaf(m, c, -(m * c)); }
+  // Against the maximum, where the log-probabilities of likely tokens cancel least.
+  __device__ __forceinline__ Sums sums(float c, bool tame_c) {
+    Sums o;
+    float a, b;
+    if (m > -INFINITY) rebase(most, c, tame_c && tame(c) ? delta(c) : 0.0f);
+    o.m = most;
+    tc::unpack2(s, a, b);
+    o.s = a + b;
+    tc::unpack2(s1, a, b);
+    o.s1 = a + b;
+    return o;
+  }
+};
+
+// One batch into the lists, the sums and the count; j is this thread's first piece.
+template <int DT, bool TOP>
+__device__ __forceinline__ void take_batch(Shared& sh, const uint4 (&q)[kBatch], int j,
+                                           float bound, float xt, float c, bool tame,
+                                           RunningSums& run, int& larger) {
+  constexpr int N = Row<DT>::N;
+  float pm[kBatch], bm = -INFINITY;
+#pragma unroll
+  for (int b = 0; b < kBatch; ++b) {
+    pm[b] = piece_max<DT>(q[b]);
+    bm = fmaxf(bm, pm[b]);
+  }
+  if (TOP && bm >= bound) {
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      if (pm[b] < bound) continue;
+      const int at = atomicAdd(&sh.n_pieces, 1);
+      if (at < kPieces) {
+        sh.piece[at] = q[b];
+        sh.piece_at[at] = j + b * kThreads;
+        sh.piece_max[at] = pm[b];
+      }
+    }
+  }
+  run.most = fmaxf(run.most, bm);
+  if (bm > run.limit) {
+    if (run.m > -INFINITY) run.rebase(bm, c, tame && run.tame(c) ? run.delta(c) : 0.0f);
+    run.m = bm;
+    run.limit = bm + 32.0f / c;
+  }
+  if (tame && run.tame(c)) {
+    const float off = -(run.m * c);
+    const unsigned long long c2 = tc::pack2(c, c), off2 = tc::pack2(off, off);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      float x[N];
+      unpack<DT>(raised<DT>(q[b]), x);
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        const unsigned long long z = tc::fma2(tc::pack2(x[i], x[i + 1]), c2, off2);
+        float z0, z1;
+        tc::unpack2(z, z0, z1);
+        const unsigned long long e = tc::pack2(fast_exp2(z0), fast_exp2(z1));
+        run.s = tc::add2(run.s, e);
+        run.s1 = tc::fma2(e, z, run.s1);
+      }
+    }
+  } else {
+    // extreme maxima, extreme temperatures, or nothing above -inf yet (then measured from 0: the
+    // terms are 0, or NaN)
+    const float m = run.m > -INFINITY ? run.m : 0.0f;
+#pragma unroll 1
+    for (int b = 0; b < kBatch; ++b) {
+      float x[N];
+      uint4 w = q[0];
+#pragma unroll
+      for (int i = 1; i < kBatch; ++i)
+        if (b == i) w = q[i];
+      unpack<DT>(w, x);
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        const float z0 = max_nan((x[i] - m) * c, kLowest2);
+        const float z1 = max_nan((x[i + 1] - m) * c, kLowest2);
+        const unsigned long long e = tc::pack2(fast_exp2(z0), fast_exp2(z1));
+        run.s = tc::add2(run.s, e);
+        run.s1 = tc::fma2(e, tc::pack2(z0, z1), run.s1);
+      }
+    }
+  }
+  if (bm > xt) larger += count_larger<DT>(q, xt);
 }
 
 // ------------------------------------------------------------------------------ bounds
 
 // The k-th largest of 64 group maxima (a group: four neighbouring threads), a lower bound of the
-// k-th largest of the elements behind `local`. Every thread calls it and gets the bound.
+// k-th largest of the elements behind `local`. Every thread calls it and gets the bound. Four
+// threads rank a maximum, each against sixteen others; equal ones in order of their index.
 __device__ __forceinline__ float bound_of(Shared& sh, float local, int k) {
-  const int lane = threadIdx.x & 31;
+  const int g = threadIdx.x >> 2, part = threadIdx.x & 3;
   local = fmaxf(local, __shfl_xor_sync(kFull, local, 1));
   local = fmaxf(local, __shfl_xor_sync(kFull, local, 2));
-  if ((lane & 3) == 0) sh.group[threadIdx.x >> 2] = local;
+  if (part == 0) sh.group[g] = local;
   __syncthreads();
-  if (threadIdx.x < 32) {
-    const float a = sh.group[lane], b = sh.group[lane + 32];
-    int ra = 0, rb = b <= a ? 1 : 0;  // places; equal maxima in order of their index
-    ra = b > a ? 1 : 0;
+  int place = 0;
 #pragma unroll
-    for (int i = 1; i < 32; ++i) {
-      const int o = (lane + i) & 31;
-      const float p = __shfl_sync(kFull, a, o), q = __shfl_sync(kFull, b, o);
-      ra += (p > a || (p == a && o < lane)) + (q > a);
-      rb += (p >= b) + (q > b || (q == b && o < lane));
-    }
-    if (ra == k - 1) sh.bound = a;
-    if (rb == k - 1) sh.bound = b;
+  for (int i = 0; i < kGroups / 16; ++i) {
+    const float4 o = *reinterpret_cast<const float4*>(&sh.group[16 * part + 4 * i]);
+    const int at = 16 * part + 4 * i;
+    place += (o.x > local || (o.x == local && at < g)) + (o.y > local || (o.y == local && at + 1 < g)) +
+             (o.z > local || (o.z == local && at + 2 < g)) +
+             (o.w > local || (o.w == local && at + 3 < g));
   }
+  place += __shfl_xor_sync(kFull, place, 1);
+  place += __shfl_xor_sync(kFull, place, 2);
+  if (place == k - 1 && part == 0) sh.bound = local;
   __syncthreads();
   return sh.bound;
+}
+
+// The same over the listed pieces; +inf (list nothing more) once they do not fit.
+__device__ __forceinline__ float bound_of_list(Shared& sh, float bound, int k) {
+  __syncthreads();  // every push so far
+  const int n = sh.n_pieces;
+  if (n > kPieces) return INFINITY;
+  float local = -INFINITY;
+  for (int i = threadIdx.x; i < n; i += kThreads) local = fmaxf(local, sh.piece_max[i]);
+  return fmaxf(bound, bound_of(sh, local, k));
 }
 
 // ------------------------------------------------------------------------------ radix selection
@@ -355,16 +525,10 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
   const float c = a.scale * kLog2e;
 
   uint4 cur[kBatch], nxt[kBatch];
-#pragma unroll
-  for (int b = 0; b < kBatch; ++b) cur[b] = r.load(j0 + tid + b * kThreads, j1);
+  r.template load_batch<kBatch>(cur, j0, j1);
+  r.template load_batch<kBatch>(nxt, j0 + kBatch * kThreads, j1);
   const float xt = bad || !a.tokens ? INFINITY : ld_elem<DT>(a.x, off + t);
 
-#pragma unroll
-  for (int b = 0; b < kBatch; ++b) nxt[b] = r.load(j0 + tid + (kBatch + b) * kThreads, j1);
-
-  float am = -INFINITY;                                 // running maximum
-  unsigned long long as = tc::pack2(0.0f, 0.0f), as1 = as;  // S and S1, two partial sums each
-  int larger = 0;
   float bound = INFINITY;
   if (TOP && tid == 0) {
     sh.n_pieces = 0;
@@ -378,108 +542,44 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
     // nothing of -inf has a place
     bound = fmaxf(bound_of(sh, first, a.top), -3.402823466e38f);
   }
-  const unsigned long long c2 = tc::pack2(c, c);
-  const bool small_c = c < kFastScale && c > kFastLeast;
-  for (int jb = j0 + tid; jb - tid < j1; jb += kBatch * kThreads) {
-    float bm = -INFINITY;
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const float pm = piece_max<DT>(cur[b]);
-      bm = fmaxf(bm, pm);
-      if (TOP && pm >= bound) {
-        const int at = atomicAdd(&sh.n_pieces, 1);
-        if (at < kPieces) {
-          sh.piece[at] = jb + b * kThreads;
-          sh.piece_max[at] = pm;
-        }
-      }
-    }
-    if (bm > am) {
-      if (am > -INFINITY) {
-        const float d = fmaxf((am - bm) * c, kLowest2), f = fast_exp2(d);
-        const unsigned long long f2 = tc::pack2(f, f);
-        as1 = tc::mul2(f2, tc::fma2(tc::pack2(d, d), as, as1));
-        as = tc::mul2(f2, as);
-      }
-      am = bm;
-    }
-    if (small_c && fabsf(am) < kFastMax) {
-      const unsigned long long m2 = tc::pack2(-am, -am);
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        float x[N];
-        unpack<DT>(raised<DT>(cur[b]), x);
-#pragma unroll
-        for (int i = 0; i < N; i += 2) {
-          const unsigned long long z = tc::mul2(tc::add2(tc::pack2(x[i], x[i + 1]), m2), c2);
-          float z0, z1;
-          tc::unpack2(z, z0, z1);
-          const unsigned long long e = tc::pack2(fast_exp2(z0), fast_exp2(z1));
-          as = tc::add2(as, e);
-          as1 = tc::fma2(e, z, as1);
-        }
-      }
-    } else {
-      // extreme maxima, extreme temperatures, or nothing above -inf yet (then measured from 0:
-      // the terms are 0, or NaN)
-      const float m = am > -INFINITY ? am : 0.0f;
-#pragma unroll 1
-      for (int b = 0; b < kBatch; ++b) {
-        float x[N];
-        unpack<DT>(b == 0 ? cur[0] : b == 1 ? cur[1] : b == 2 ? cur[2] : cur[3], x);
-#pragma unroll
-        for (int i = 0; i < N; i += 2) {
-          const float z0 = max_nan((x[i] - m) * c, kLowest2);
-          const float z1 = max_nan((x[i + 1] - m) * c, kLowest2);
-          const unsigned long long e = tc::pack2(fast_exp2(z0), fast_exp2(z1));
-          as = tc::add2(as, e);
-          as1 = tc::fma2(e, tc::pack2(z0, z1), as1);
-        }
-      }
-    }
-    if (bm > xt) {
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) larger += count_larger<DT>(cur[b], xt);
-    }
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      cur[b] = nxt[b];
-      nxt[b] = r.load(jb + (2 * kBatch + b) * kThreads, j1);
+  RunningSums run;
+  run.start();
+  int larger = 0;
+  constexpr int kStep = kBatch * kThreads;
+  const bool tame = c < kFastScale && c > kFastLeast;
+  // the bound is renewed from the list whenever the number of batches seen has doubled: a list
+  // then grows by little more than k pieces between two renewals, however long the row
+  int renew = j0 + 4 * kStep;
+  for (int jb = j0; jb < j1; jb += 2 * kStep) {
+    take_batch<DT, TOP>(sh, cur, jb + tid, bound, xt, c, tame, run, larger);
+    r.template load_batch<kBatch>(cur, jb + 2 * kStep, j1);
+    if (jb + kStep >= j1) break;
+    take_batch<DT, TOP>(sh, nxt, jb + kStep + tid, bound, xt, c, tame, run, larger);
+    r.template load_batch<kBatch>(nxt, jb + 3 * kStep, j1);
+    if (TOP && jb + 2 * kStep == renew && renew < j1) {
+      renew += renew - j0;
+      bound = bound_of_list(sh, bound, a.top);
     }
   }
-  Sums acc;
-  {
-    float s0, s1;
-    acc.m = am;
-    tc::unpack2(as, s0, s1);
-    acc.s = s0 + s1;
-    tc::unpack2(as1, s0, s1);
-    acc.s1 = s0 + s1;
-  }
+  Sums acc = run.sums(c, tame);
 
-  // this CTA's sums
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Sums y;
-    y.m = __shfl_down_sync(kFull, acc.m, o);
-    y.s = __shfl_down_sync(kFull, acc.s, o);
-    y.s1 = __shfl_down_sync(kFull, acc.s1, o);
-    acc = merge(acc, y, c);
-    larger += __shfl_down_sync(kFull, larger, o);
-  }
+  // this CTA's sums: lanes against their warp's maximum, then warps against the CTA's
+  acc = merge_lanes<32>(acc, c);
+  larger = __reduce_add_sync(kFull, larger);
   if (lane == 0) {
     sh.sums[warp] = acc;
     sh.count[warp] = larger;
   }
   if (TOP && tid < kMaxTop) sh.top[tid] = 0;
-  __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < kWarps; ++w) {
-      acc = merge(acc, sh.sums[w], c);
-      larger += sh.count[w];
+  __syncthreads();  // every push, too
+  if (warp == kWarps - 1) {
+    const bool has = lane < kWarps;
+    acc = merge_lanes<kWarps>(has ? sh.sums[lane] : Sums{-INFINITY, 0.0f, 0.0f}, c);
+    larger = __reduce_add_sync(kFull, has ? sh.count[lane] : 0);
+    if (lane == 0) {
+      sh.total = acc;
+      sh.total_count = larger;
     }
-    sh.total = acc;
-    sh.total_count = larger;
   }
   if (TOP) {
     const int n = sh.n_pieces;
@@ -487,13 +587,13 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
     if (fits) {
       float local = -INFINITY;
       for (int i = tid; i < n; i += kThreads) local = fmaxf(local, sh.piece_max[i]);
-      // fewer listed pieces than places leave the first bound
+      // fewer listed pieces than places leave the bound they were listed by
       const float cut = fmaxf(bound_of(sh, local, a.top), bound);
       for (int i = tid; i < n; i += kThreads) {
         if (sh.piece_max[i] < cut) continue;
-        const int j = sh.piece[i];
+        const int j = sh.piece_at[i];
         float x[N];
-        unpack<DT>(r.load(j, j1), x);
+        unpack<DT>(sh.piece[i], x);
 #pragma unroll
         for (int q = 0; q < N; ++q)
           if (x[q] >= cut) {
@@ -510,6 +610,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
     for (int i = tid; i < nk; i += kThreads) {
       const unsigned long long key = sh.keys[i];
       int place = 0;
+#pragma unroll 8
       for (int q = 0; q < nk; ++q) place += sh.keys[q] > key;
       if (place < a.top) sh.top[place] = key;
     }
@@ -553,10 +654,17 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
         __syncthreads();
       }
       if (key) {
+        // its place in its own list, plus the larger entries of every other (descending, zeros
+        // at the end)
         place = e;
-        for (int o = 0; o < split; ++o) {
-          if (o == p) continue;
-          for (int q = 0; q < a.top; ++q) place += sh.keys[o * kMaxTop + q] > key;
+#pragma unroll
+        for (int o = 0; o < 8; ++o) {
+          if (o >= split || o == p) continue;
+          const unsigned long long* list = sh.keys + o * kMaxTop;
+          int n = 0;
+#pragma unroll
+          for (int w = kMaxTop / 2; w > 0; w /= 2) n += list[n + w - 1] > key ? w : 0;
+          place += n + (list[n] > key ? 1 : 0);
         }
       }
       const size_t at = (size_t)row * a.top;
