@@ -32,11 +32,13 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256;
+constexpr int kCtas = 4;               // CTAs of an SM
 constexpr int kWarps = kThreads / 32;
 constexpr int kBatch = 4;             // 16-byte pieces a thread has in flight, and as many next
 constexpr int kMaxTop = SPEC_LOGPROBS_MAX_TOP;
 constexpr int kPieces = 512;          // listed pieces at most
 constexpr int kKeys = 512;            // elements ranked at most
+constexpr int kMaxSplit = 8;          // parts of a row at most
 constexpr int kGroups = 64;           // maxima behind a bound; at least 2 * kMaxTop
 constexpr uint32_t kFull = 0xffffffffu;
 
@@ -49,6 +51,8 @@ constexpr float kFastMax = 1024.0f, kFastScale = 0x1p20f, kFastLeast = 0x1p-80f;
 struct Sums {
   float m, s, s1;  // reference logit, S, S1 (in base 2)
 };
+
+static_assert(kKeys >= kMaxSplit * kMaxTop && kMaxTop == 32, "the merged lists");
 
 struct Shared {
   alignas(16) float group[kGroups];
@@ -380,26 +384,29 @@ __device__ __forceinline__ void take_batch(Shared& sh, const uint4 (&q)[kBatch],
 
 // ------------------------------------------------------------------------------ bounds
 
-// The k-th largest of 64 group maxima (a group: four neighbouring threads), a lower bound of the
-// k-th largest of the elements behind `local`. Every thread calls it and gets the bound. Four
-// threads rank a maximum, each against sixteen others; equal ones in order of their index.
+// The k-th largest of 64 group maxima (a group: kPer neighbouring threads), a lower bound of the
+// k-th largest of the elements behind `local`. Every thread calls it and gets the bound. A
+// group's threads rank its maximum, each against its share of the others; equal ones in order of
+// their index.
 __device__ __forceinline__ float bound_of(Shared& sh, float local, int k) {
-  const int g = threadIdx.x >> 2, part = threadIdx.x & 3;
-  local = fmaxf(local, __shfl_xor_sync(kFull, local, 1));
-  local = fmaxf(local, __shfl_xor_sync(kFull, local, 2));
+  constexpr int kPer = kThreads / kGroups, kShare = kGroups / kPer;
+  const int g = threadIdx.x / kPer, part = threadIdx.x % kPer;
+#pragma unroll
+  for (int o = 1; o < kPer; o *= 2) local = fmaxf(local, __shfl_xor_sync(kFull, local, o));
   if (part == 0) sh.group[g] = local;
   __syncthreads();
   int place = 0;
 #pragma unroll
-  for (int i = 0; i < kGroups / 16; ++i) {
-    const float4 o = *reinterpret_cast<const float4*>(&sh.group[16 * part + 4 * i]);
-    const int at = 16 * part + 4 * i;
-    place += (o.x > local || (o.x == local && at < g)) + (o.y > local || (o.y == local && at + 1 < g)) +
+  for (int i = 0; i < kShare; i += 4) {
+    const int at = kShare * part + i;
+    const float4 o = *reinterpret_cast<const float4*>(&sh.group[at]);
+    place += (o.x > local || (o.x == local && at < g)) +
+             (o.y > local || (o.y == local && at + 1 < g)) +
              (o.z > local || (o.z == local && at + 2 < g)) +
              (o.w > local || (o.w == local && at + 3 < g));
   }
-  place += __shfl_xor_sync(kFull, place, 1);
-  place += __shfl_xor_sync(kFull, place, 2);
+#pragma unroll
+  for (int o = 1; o < kPer; o *= 2) place += __shfl_xor_sync(kFull, place, o);
   if (place == k - 1 && part == 0) sh.bound = local;
   __syncthreads();
   return sh.bound;
@@ -433,7 +440,7 @@ __device__ __noinline__ void select_radix(Shared& sh, const Row<DT>& row, int j0
   }
   bool all = false;  // fewer than k elements have a place
   for (int shift = kBits - 8; shift >= 0 && !all; shift -= 8) {
-    sh.hist[tid] = 0;
+    for (int b = tid; b < 256; b += kThreads) sh.hist[b] = 0;
     __syncthreads();
     const uint32_t prefix = sh.prefix;
     for (int j = j0 + tid; j < j1; j += kThreads) {
@@ -509,7 +516,7 @@ __device__ __noinline__ void select_radix(Shared& sh, const Row<DT>& row, int j0
 // ------------------------------------------------------------------------------ kernel
 
 template <int DT, bool TOP>
-__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs a, int split) {
+__global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const LogprobArgs a, int split) {
   constexpr int N = Row<DT>::N;
   __shared__ Shared sh;
   cg::cluster_group cluster = cg::this_cluster();
@@ -641,43 +648,42 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
     if (TOP) {
       __syncthreads();
       const float m = sh.total.m, ls = sh.total.s;
-      // place of each part's entry among all parts' entries
-      const int p = tid / kMaxTop, e = tid % kMaxTop;
-      static_assert(kThreads / kMaxTop == 8 && kKeys >= kThreads,
-                    "one thread an entry of up to 8 parts");
-      unsigned long long key = 0;
-      int place = kMaxTop;
-      if (p < split && e < a.top)
-        key = split > 1 ? *cluster.map_shared_rank(&sh.top[e], p) : sh.top[e];
+      // place of each part's entry: its own place in its part's list, plus the larger entries of
+      // every other (descending, zeros at the end)
       if (split > 1) {
-        sh.keys[tid] = key;
+        for (int i = tid; i < split * kMaxTop; i += kThreads)
+          sh.keys[i] = *cluster.map_shared_rank(&sh.top[i % kMaxTop], i / kMaxTop);
         __syncthreads();
       }
-      if (key) {
-        // its place in its own list, plus the larger entries of every other (descending, zeros
-        // at the end)
-        place = e;
+      const unsigned long long* lists = split > 1 ? sh.keys : sh.top;
+      const size_t at = (size_t)row * a.top;
+      for (int i0 = 0; i0 < split * kMaxTop; i0 += kThreads) {
+        const int i = i0 + tid, p = i / kMaxTop, e = i % kMaxTop;
+        const unsigned long long key = i < split * kMaxTop ? lists[i] : 0;
+        if (!key) continue;
+        int place = e;
 #pragma unroll
-        for (int o = 0; o < 8; ++o) {
+        for (int o = 0; o < kMaxSplit; ++o) {
           if (o >= split || o == p) continue;
-          const unsigned long long* list = sh.keys + o * kMaxTop;
+          const unsigned long long* list = lists + o * kMaxTop;
           int n = 0;
 #pragma unroll
           for (int w = kMaxTop / 2; w > 0; w /= 2) n += list[n + w - 1] > key ? w : 0;
           place += n + (list[n] > key ? 1 : 0);
         }
-      }
-      const size_t at = (size_t)row * a.top;
-      if (place < a.top) {
+        if (place >= a.top) continue;
         const float x = order_value((uint32_t)(key >> 32));
         if (a.top_ids) a.top_ids[at + place] = (int)(0xffffffffu - (uint32_t)key);
         if (a.top_logp) a.top_logp[at + place] = (x - m) * a.scale - ls;
       }
       // places that no logit has
-      const int have = __syncthreads_count(key != 0);
-      if (tid < a.top && tid >= have) {
-        if (a.top_ids) a.top_ids[at + tid] = -1;
-        if (a.top_logp) a.top_logp[at + tid] = -INFINITY;
+      if (warp == 0) {
+        int have = 0;
+        for (int o = 0; o < split; ++o) have += __popc(__ballot_sync(kFull, lists[o * kMaxTop + lane] != 0));
+        if (lane < a.top && lane >= have) {
+          if (a.top_ids) a.top_ids[at + lane] = -1;
+          if (a.top_logp) a.top_logp[at + lane] = -INFINITY;
+        }
       }
     }
   }
@@ -688,10 +694,13 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
 
 cudaError_t launch_token_logprobs(const LogprobArgs& a, int dt, cudaStream_t s) {
   TraceScope ts(SPEC_KCLASS_OTHER, s);
-  // split rows while that leaves CTAs without work and the parts have a batch or more
+  // A CTA has some 6 us of latencies outside its stream of logits, more in a cluster: rows are
+  // split while the parts still find SMs of their own and have a batch or more. 129280 bf16
+  // logits, top 20, us at splits of 1 / 2 / 4 / 8: 1 row 17 / 13 / 11 / 10, 64 rows 21 / 16 / 15 /
+  // 16, 128 rows 22 / 19 / 20 / 30, 256 rows 26 / 27 / 35 / 56.
   const int batch = kThreads * kBatch * (dt == SPEC_BF16 ? 8 : 4);
   int split = 1;
-  while (split < 8 && (long long)a.rows * split < 4 * num_sms() && a.V >= 2 * split * batch)
+  while (split < kMaxSplit && (long long)a.rows * split * 2 <= 2 * num_sms() && a.V >= 2 * split * batch)
     split *= 2;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
