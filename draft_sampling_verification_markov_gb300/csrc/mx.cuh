@@ -71,18 +71,35 @@ __device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi) {
   return r;
 }
 
-// Values of one code (the sign, then the magnitude from its exponent and significand).
-__device__ __forceinline__ float from_e4m3(uint32_t c) {
-  const uint32_t mag = c & 0x7fu;
-  // normal: exponent bias 7 -> 127; subnormal: significand * 2^-9
-  const float v = mag >= 8 ? __uint_as_float((mag << 20) + (120u << 23)) : (float)mag * 0.001953125f;
-  return (c & 0x80u) ? -v : v;
+// Values of two codes (exact in fp16, the instruction's result type); the upper bits of c are
+// ignored.
+__device__ __forceinline__ void half2_to_float(uint32_t h, float& lo, float& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.f32.f16 %0, a;\n\t"
+      "cvt.f32.f16 %1, b;\n\t}"
+      : "=f"(lo), "=f"(hi)
+      : "r"(h));
 }
 
-__device__ __forceinline__ float from_e2m1(uint32_t c) {
-  const uint32_t mag = c & 7u;
-  const float v = mag >= 2 ? __uint_as_float((mag << 22) + (126u << 23)) : (float)mag * 0.5f;
-  return (c & 8u) ? -v : v;
+__device__ __forceinline__ void from_e4m3x2(uint32_t c, float& lo, float& hi) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 a;\n\t"
+      "cvt.u16.u32 a, %1;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t}"
+      : "=r"(h)
+      : "r"(c));
+  half2_to_float(h, lo, hi);
+}
+
+__device__ __forceinline__ void from_e2m1x2(uint32_t c, float& lo, float& hi) {
+  uint32_t h;
+  asm("{\n\t.reg .b8 a;\n\t"
+      "cvt.u8.u32 a, %1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t}"
+      : "=r"(h)
+      : "r"(c));
+  half2_to_float(h, lo, hi);
 }
 
 }  // namespace mx
