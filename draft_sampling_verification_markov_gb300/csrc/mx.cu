@@ -46,30 +46,57 @@ __device__ __forceinline__ float ld1(const void* p, size_t i) {
     return *(reinterpret_cast<const volatile float*>(p) + i);
 }
 
+// Eight consecutive elements as they are stored.
+template <int DT>
+struct Piece {
+  uint4 q[DT == SPEC_BF16 ? 1 : 2];
+};
+
+template <int DT>
+__device__ __forceinline__ void clear(Piece<DT>& p) {
+#pragma unroll
+  for (uint4& q : p.q) q = make_uint4(0, 0, 0, 0);
+}
+
 // Elements v .. v + 7 of a row of K (zero past K); 16-byte loads when `vec`. RO: the memory is
 // not written while the kernel runs (the read-only path may serve it).
 template <int DT, bool RO>
 __device__ __forceinline__ void load8(const void* base, size_t off, int v, int K, bool vec,
-                                      float (&x)[8]) {
+                                      Piece<DT>& p) {
+  constexpr size_t es = DT == SPEC_BF16 ? 2 : 4;
+  const char* at = static_cast<const char*>(base) + (off + v) * es;
   if (vec && v + 8 <= K) {
-    if constexpr (DT == SPEC_BF16) {
-      const uint4 q = ld16<RO>(reinterpret_cast<const uint16_t*>(base) + off + v);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      }
+    for (int i = 0; i < (int)es / 2; ++i) p.q[i] = ld16<RO>(at + 16 * i);
+  } else {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      w[i] = v + i < K ? __float_as_uint(ld1<DT, RO>(base, off + v + i)) : 0u;
+    if constexpr (DT == SPEC_BF16) {  // an element's bits are the upper half of its fp32's
+      p.q[0] = make_uint4(w[0] >> 16 | w[1], w[2] >> 16 | w[3], w[4] >> 16 | w[5],
+                          w[6] >> 16 | w[7]);
     } else {
-      const float* p = reinterpret_cast<const float*>(base) + off + v;
-      const uint4 a = ld16<RO>(p), b = ld16<RO>(p + 4);
-      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      p.q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      p.q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void unpack(const Piece<DT>& p, float (&x)[8]) {
+  if constexpr (DT == SPEC_BF16) {
+    const uint32_t w[4] = {p.q[0].x, p.q[0].y, p.q[0].z, p.q[0].w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   } else {
+    const uint32_t w[8] = {p.q[0].x, p.q[0].y, p.q[0].z, p.q[0].w,
+                           p.q[1].x, p.q[1].y, p.q[1].z, p.q[1].w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = v + i < K ? ld1<DT, RO>(base, off + v + i) : 0.0f;
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
   }
 }
 
@@ -79,43 +106,58 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
+// Eight values as they are stored, rounded to the type.
+template <int DT>
+__device__ __forceinline__ void pack(const float (&x)[8], Piece<DT>& p) {
+  if constexpr (DT == SPEC_BF16) {
+    p.q[0] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                        pack_bf16(x[6], x[7]));
+  } else {
+    p.q[0] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                        __float_as_uint(x[3]));
+    p.q[1] = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]),
+                        __float_as_uint(x[7]));
+  }
+}
+
 template <int DT>
 __device__ __forceinline__ void store8(void* base, size_t off, int v, int K, bool vec,
-                                       const float (&x)[8]) {
+                                       const Piece<DT>& p) {
+  constexpr size_t es = DT == SPEC_BF16 ? 2 : 4;
+  char* at = static_cast<char*>(base) + (off + v) * es;
   if (vec && v + 8 <= K) {
-    if constexpr (DT == SPEC_BF16) {
-      *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(base) + off + v) =
-          make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                     pack_bf16(x[6], x[7]));
-    } else {
-      float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(base) + off + v);
-      p[0] = make_float4(x[0], x[1], x[2], x[3]);
-      p[1] = make_float4(x[4], x[5], x[6], x[7]);
-    }
+#pragma unroll
+    for (int i = 0; i < (int)es / 2; ++i) *reinterpret_cast<uint4*>(at + 16 * i) = p.q[i];
   } else {
+    float x[8];
+    unpack<DT>(p, x);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (v + i >= K) break;
       if constexpr (DT == SPEC_BF16)
-        reinterpret_cast<uint16_t*>(base)[off + v + i] = (uint16_t)pack_bf16(x[i], 0.0f);
+        reinterpret_cast<uint16_t*>(at)[i] = (uint16_t)(__float_as_uint(x[i]) >> 16);
       else
-        reinterpret_cast<float*>(base)[off + v + i] = x[i];
+        reinterpret_cast<float*>(at)[i] = x[i];
     }
   }
 }
 
-// Quantises this lane's eight elements (element 8 * (lane % 16) of group g of row `row`) and
-// stores codes and, from the group's first lane, the scale word. All 32 lanes call it; `live`
-// masks the stores. Returns whether the block was finite.
+__device__ __forceinline__ float max_abs_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return d;
+}
+
+// Quantises this lane's eight elements (element 8 * (lane % 16) of a group): stores its codes at
+// `codes` and, from the group's first lane, the scale word at `scale`. All 32 lanes call it;
+// `live` masks the stores. Returns whether the block was finite.
 template <int FMT>
-__device__ __forceinline__ bool quantize8(const float (&x)[8], int row, int g, int G, bool live,
-                                          uint8_t* codes, uint8_t* scales) {
-  uint32_t amax = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t b = __float_as_uint(x[i]) & 0x7fffffffu;
-    amax = b > amax ? b : amax;
-  }
+__device__ __forceinline__ bool quantize8(const float (&x)[8], bool live, uint8_t* codes,
+                                          uint8_t* scale) {
+  const float m = max_abs_nan(max_abs_nan(max_abs_nan(x[0], x[1]), max_abs_nan(x[2], x[3])),
+                              max_abs_nan(max_abs_nan(x[4], x[5]), max_abs_nan(x[6], x[7])));
+  // as integers NaN is above infinity
+  uint32_t amax = __float_as_uint(m) & 0x7fffffffu;
   amax = max(amax, __shfl_xor_sync(kFull, amax, 1));
   amax = max(amax, __shfl_xor_sync(kFull, amax, 2));
   const int sb = scale_byte<FMT>(amax);
@@ -125,63 +167,77 @@ __device__ __forceinline__ bool quantize8(const float (&x)[8], int row, int g, i
   word |= __shfl_xor_sync(kFull, word, 4);
   word |= __shfl_xor_sync(kFull, word, 8);
   if (!live) return true;
-  const float f = finite ? unscale(sb) : 0.0f;
+  const float f = unscale(finite ? sb : 0);
   float y[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = finite ? x[i] * f : 0.0f;
-  const int l = threadIdx.x & 15;
+  for (int i = 0; i < 8; ++i) y[i] = x[i] * f;
   if constexpr (FMT == SPEC_MX_E2M1) {
-    const uint32_t c = to_e2m1x2(y[0], y[1]) | to_e2m1x2(y[2], y[3]) << 8 |
-                       to_e2m1x2(y[4], y[5]) << 16 | to_e2m1x2(y[6], y[7]) << 24;
-    *reinterpret_cast<uint32_t*>(codes + (size_t)row * G * (kGroup / 2) + g * (kGroup / 2) + 4 * l) = c;
+    const uint32_t c = to_e2m1x8(y);
+    *reinterpret_cast<uint32_t*>(codes) = finite ? c : 0;
   } else {
-    const uint2 c = make_uint2(to_e4m3x2(y[0], y[1]) | to_e4m3x2(y[2], y[3]) << 16,
-                               to_e4m3x2(y[4], y[5]) | to_e4m3x2(y[6], y[7]) << 16);
-    *reinterpret_cast<uint2*>(codes + (size_t)row * G * kGroup + g * kGroup + 8 * l) = c;
+    const uint2 c = to_e4m3x8(y);
+    *reinterpret_cast<uint2*>(codes) = finite ? c : make_uint2(0, 0);
   }
-  if (l == 0) *reinterpret_cast<uint32_t*>(scales + scale_word(row, g, G)) = word;
+  if ((threadIdx.x & 15) == 0) *reinterpret_cast<uint32_t*>(scale) = word;
   return finite;
 }
 
-// Row and group of unit u0 + t (t < 2^16) for a block-uniform u0.
+// Bytes of a group's codes, and of a lane's part of them.
+template <int FMT>
+constexpr int kGroupCode = FMT == SPEC_MX_E2M1 ? kGroup / 2 : kGroup;
+template <int FMT>
+constexpr int kLaneCode = kGroupCode<FMT> / 16;
+
+// Row and group of unit u0 + t, t < 64, for a block-uniform u0 at (row0, g0). A row of 64 groups
+// or more ends at most once within; a shorter one's quotient comes from its reciprocal (both
+// factors are below 128, so ceil(2^32 / G) is exact enough).
 struct Unit {
   int row, g;
-  __device__ __forceinline__ Unit(int row0, int g0, int t, int G) {
-    const uint32_t x = (uint32_t)(g0 + t), q = x / (uint32_t)G;
+  __device__ __forceinline__ Unit(int row0, int g0, int t, int G, uint32_t recip) {
+    const uint32_t x = (uint32_t)(g0 + t);
+    const uint32_t q = G >= 64 ? (x >= (uint32_t)G ? 1u : 0u)
+                               : (G == 1 ? x : __umulhi(x, recip));
     row = row0 + (int)q;
     g = (int)(x - q * (uint32_t)G);
   }
 };
+__device__ __forceinline__ uint32_t reciprocal(int G) { return 0xffffffffu / (uint32_t)G + 1u; }
 
 // ------------------------------------------------------------------------------ quantise
 
 // Groups of all rows, the last tile's missing rows among them (their scales are 0).
 template <int DT, int FMT>
-__global__ void __launch_bounds__(kThreads) quantize_kernel(const void* x, long long ldx, int rows,
+__global__ void __launch_bounds__(kThreads, DT == SPEC_BF16 ? 5 : 4) quantize_kernel(const void* x, long long ldx, int rows,
                                                             int K, bool vec, uint8_t* codes,
                                                             uint8_t* scales, uint32_t* status) {
   const int G = groups(K), l = threadIdx.x & 15;
   const int tiled = (rows + kTileRows - 1) / kTileRows * kTileRows;
   const long long units = (long long)tiled * G;
   const long long step = (long long)gridDim.x * kUnits * kUnroll;
+  const uint32_t recip = reciprocal(G);
   bool finite = true;
   for (long long u0 = (long long)blockIdx.x * kUnits * kUnroll; u0 < units; u0 += step) {
     const int row0 = (int)(u0 / G), g0 = (int)(u0 - (long long)row0 * G);
-    float v[kUnroll][8];
+    Piece<DT> v[kUnroll];
+    int row[kUnroll];
+    uint8_t* scale[kUnroll];
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-      const Unit u(row0, g0, i * kUnits + threadIdx.x / 16, G);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
+      const Unit u(row0, g0, i * kUnits + threadIdx.x / 16, G, recip);
+      row[i] = u.row;
+      scale[i] = scales + scale_word(u.row, u.g, G);
+      clear<DT>(v[i]);
       if (u.row < rows)
         load8<DT, true>(x, (size_t)u.row * ldx, u.g * kGroup + 8 * l, K, vec, v[i]);
     }
+    uint8_t* c = codes + (size_t)(u0 + threadIdx.x / 16) * kGroupCode<FMT> + kLaneCode<FMT> * l;
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-      const Unit u(row0, g0, i * kUnits + threadIdx.x / 16, G);
-      finite &= quantize8<FMT>(v[i], u.row, u.g, G, u.row < rows, codes, scales);
-      if (u.row >= rows && u.row < tiled && l == 0)
-        *reinterpret_cast<uint32_t*>(scales + scale_word(u.row, u.g, G)) = 0;
+      float y[8];
+      unpack<DT>(v[i], y);
+      finite &= quantize8<FMT>(y, row[i] < rows, c + (size_t)i * kUnits * kGroupCode<FMT>,
+                               scale[i]);
+      if (row[i] >= rows && row[i] < tiled && l == 0) *reinterpret_cast<uint32_t*>(scale[i]) = 0;
     }
   }
   if (!finite) atomicOr(status, SPEC_DEV_NONFINITE);
@@ -197,29 +253,32 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint8_t* cod
   const int G = groups(K), l = threadIdx.x & 15;
   const long long units = (long long)rows * G;
   const long long step = (long long)gridDim.x * kUnits * kUnroll;
+  const uint32_t recip = reciprocal(G);
   for (long long u0 = (long long)blockIdx.x * kUnits * kUnroll; u0 < units; u0 += step) {
     const int row0 = (int)(u0 / G), g0 = (int)(u0 - (long long)row0 * G);
     uint2 c[kUnroll];
     uint32_t sb[kUnroll];
+    int row[kUnroll], k[kUnroll];
+    const uint8_t* p = codes + (size_t)(u0 + threadIdx.x / 16) * kGroupCode<FMT> +
+                       kLaneCode<FMT> * l;
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-      const Unit u(row0, g0, i * kUnits + threadIdx.x / 16, G);
+      const Unit u(row0, g0, i * kUnits + threadIdx.x / 16, G, recip);
+      row[i] = u.row;
+      k[i] = u.g * kGroup + 8 * l;
       c[i] = make_uint2(0, 0);
       sb[i] = 0;
       if (u.row >= rows) continue;
+      const uint8_t* at = p + (size_t)i * kUnits * kGroupCode<FMT>;
       if constexpr (FMT == SPEC_MX_E2M1)
-        c[i].x = __ldg(reinterpret_cast<const uint32_t*>(
-            codes + ((size_t)u.row * G + u.g) * (kGroup / 2) + 4 * l));
+        c[i].x = __ldg(reinterpret_cast<const uint32_t*>(at));
       else
-        c[i] = __ldg(reinterpret_cast<const uint2*>(codes + ((size_t)u.row * G + u.g) * kGroup +
-                                                    8 * l));
+        c[i] = __ldg(reinterpret_cast<const uint2*>(at));
       sb[i] = __ldg(scales + scale_word(u.row, u.g, G) + (l >> 2));
     }
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-      const Unit u(row0, g0, i * kUnits + threadIdx.x / 16, G);
-      const int k = u.g * kGroup + 8 * l;
-      if (u.row >= rows || k >= K) continue;
+      if (row[i] >= rows || k[i] >= K) continue;
       const float s = scale_value((int)sb[i]);
       float y[8];
 #pragma unroll
@@ -231,7 +290,9 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint8_t* cod
         y[e] *= s;
         y[e + 1] *= s;
       }
-      store8<DT>(out, (size_t)u.row * ldo, k, K, vec, y);
+      Piece<DT> o;
+      pack<DT>(y, o);
+      store8<DT>(out, (size_t)row[i] * ldo, k[i], K, vec, o);
     }
   }
 }
@@ -244,35 +305,52 @@ struct NormArgs {
   void* res_out;
   const void* weight;
   long long ldx, ldr, ldo;
-  int rows, K, wdt;
-  float eps;
+  int rows, K;
+  float eps, inv_K;
   bool vec, wvec;
   uint8_t* codes;
   uint8_t* scales;
   uint32_t* status;
 };
 
-__device__ __forceinline__ float round_to(float x, int dt) {
-  return dt == SPEC_BF16 ? bf16_to_f32((uint16_t)pack_bf16(x, 0.0f)) : x;
-}
-
-// h of one eight-element piece: x, plus the residual and the rounding of its stored form.
+// A row's piece of x and of the residual, as loaded.
 template <int DT>
-__device__ __forceinline__ void load_h(const NormArgs& a, int row, int k, float (&h)[8]) {
-  load8<DT, false>(a.x, (size_t)row * a.ldx, k, a.K, a.vec, h);
-  if (a.res) {
-    float r[8];
-    load8<DT, false>(a.res, (size_t)row * a.ldr, k, a.K, a.vec, r);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = round_to(h[i] + r[i], DT);
-  }
+struct Pair {
+  Piece<DT> x, r;
+};
+
+template <int DT>
+__device__ __forceinline__ void load_pair(const NormArgs& a, int row, int k, Pair<DT>& p) {
+  load8<DT, false>(a.x, (size_t)row * a.ldx, k, a.K, a.vec, p.x);
+  if (a.res) load8<DT, false>(a.res, (size_t)row * a.ldr, k, a.K, a.vec, p.r);
 }
 
-__device__ __forceinline__ void load_w(const NormArgs& a, int k, float (&w)[8]) {
-  if (a.wdt == SPEC_BF16)
-    load8<SPEC_BF16, true>(a.weight, 0, k, a.K, a.wvec, w);
-  else
-    load8<SPEC_F32, true>(a.weight, 0, k, a.K, a.wvec, w);
+// h of one piece, as it is stored: x, or x + residual rounded to the type (and stored).
+template <int DT>
+__device__ __forceinline__ Piece<DT> add_pair(const NormArgs& a, int row, int k,
+                                              const Pair<DT>& p) {
+  if (!a.res) return p.x;
+  float h[8], r[8];
+  unpack<DT>(p.x, h);
+  unpack<DT>(p.r, r);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h[i] += r[i];
+  Piece<DT> o;
+  pack<DT>(h, o);
+  if (a.res_out) store8<DT>(a.res_out, (size_t)row * a.ldo, k, a.K, a.vec, o);
+  return o;
+}
+
+template <int DT>
+__device__ __forceinline__ float sum_squares(const Piece<DT>& p) {
+  float h[8], s0 = 0.0f, s1 = 0.0f;
+  unpack<DT>(p, h);
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    s0 = fmaf(h[i], h[i], s0);
+    s1 = fmaf(h[i + 1], h[i + 1], s1);
+  }
+  return s0 + s1;
 }
 
 // 1 / sqrt(sum / K + eps) as an unevaluated pair, from a sum known as a pair: the quotient with
@@ -280,10 +358,10 @@ __device__ __forceinline__ void load_w(const NormArgs& a, int k, float (&w)[8]) 
 // whose residual is formed with fused products. Everything in a row is scaled by this one number,
 // so its rounding would move every code of the row the same way. A sum that is not finite gives
 // NaN for the whole row.
-__device__ __forceinline__ DF inverse_rms(DF sum, float K, float eps) {
+__device__ __forceinline__ DF inverse_rms(DF sum, float K, float inv_K, float eps) {
   if (!(sum.hi < INFINITY)) return {NAN, 0.0f};
-  const float q = __fdiv_rn(sum.hi, K);
-  const float ql = (fmaf(-q, K, sum.hi) + sum.lo) / K;
+  const float q = sum.hi * inv_K;
+  const float ql = (fmaf(-q, K, sum.hi) + sum.lo) * inv_K;
   DF v = two_sum(q, eps);
   v = fast_two_sum(v.hi, v.lo + ql);
   const float y = rsqrtf(v.hi);
@@ -292,23 +370,68 @@ __device__ __forceinline__ DF inverse_rms(DF sum, float K, float eps) {
   return fast_two_sum(y, 0.5f * y * r);
 }
 
-// h * rstd * w with one rounding: the product with rstd as a pair, then the weight.
-__device__ __forceinline__ float scaled(float h, DF rstd, float w) {
-  const float q = h * rstd.hi, e = fmaf(h, rstd.hi, -q) + h * rstd.lo;
-  return fmaf(q, w, e * w);
+// Sum of one non-negative number a lane as a pair, exact to 2^-42 of the largest: under the
+// largest one's exponent the numbers are two whole numbers of 24 bits each, which the warp's
+// integer reduction adds (five rounds of pair additions were most of a row's latency).
+__device__ __forceinline__ DF warp_sum_exact(float x) {
+  const int e = (int)(__reduce_max_sync(kFull, __float_as_uint(x)) >> 23);
+  if (e == 255 || e < 24) return {warp_sum(x), 0.0f};  // not finite, or below 2^-103
+  const float f = __uint_as_float((uint32_t)(277 - e) << 23);    // 2^(150 - e): x * f < 2^24
+  const float back = __uint_as_float((uint32_t)(e - 23) << 23);  // 2^(e - 150)
+  const float t = x * f;
+  const uint32_t hi = (uint32_t)t, lo = (uint32_t)((t - (float)hi) * 0x1p24f);
+  const uint32_t sh = __reduce_add_sync(kFull, hi), sl = __reduce_add_sync(kFull, lo);
+  // sums below 2^29: the upper 23 bits convert exactly
+  const DF s = fast_two_sum((float)(sh & ~0x3fu),
+                            (float)(sh & 0x3fu) + (float)sl * 0x1p-24f);
+  return {s.hi * back, s.lo * back};
 }
 
-// Sum over the block of one number a thread, as a pair: fp32 within a warp, exact additions over
-// the warps. blockDim.x is a multiple of 32.
-__device__ __forceinline__ DF block_sum_pair(float x) {
+// The scale of a row: 1 / rms = (hi + lo) * two with `two` a power of two and hi in [1, 2).
+struct RowScale {
+  float hi, lo, two;
+  RowScale() = default;
+  __device__ __forceinline__ explicit RowScale(DF r) {
+    const int e = (int)(__float_as_uint(r.hi) >> 23) - 127;  // a normal number, or NaN
+    two = __uint_as_float((uint32_t)(e + 127) << 23);
+    const float back = __uint_as_float((uint32_t)(127 - e) << 23);
+    hi = r.hi * back;
+    lo = r.lo * back;
+    if (!(r.hi < INFINITY)) hi = NAN, two = 1.0f;
+  }
+};
+
+// h * rstd * w, truncated, with the last bit set for the rest that was cut off (rounding to odd:
+// a product that has no rest is taken to have one, which only moves an exact tie of the format).
+// Rounding that to the format rounds the product itself; rounding to the nearest fp32 in between
+// meets a midpoint of the format about once in 2^20 elements and may then go the wrong way. The
+// power of two comes first: h * two is exact, and of the size of the result. EXACT: the product
+// with the weight has no rounding error (two bf16 numbers).
+template <bool EXACT>
+__device__ __forceinline__ float scaled(float h, const RowScale& r, float w) {
+  const float g = h * r.two, p = g * w;
+  float low = p * r.lo;
+  if (!EXACT) low = fmaf(fmaf(g, w, -p), r.hi, low);
+  return __uint_as_float(__float_as_uint(__fmaf_rz(p, r.hi, low)) | 1u);
+}
+
+// The scale of a row from each thread's sum of squares: fp32 within a warp, exact additions over
+// the warps. One warp does what is the same for all (done by every thread it was most of the
+// kernel's instructions). blockDim.x is a multiple of 32.
+__device__ __forceinline__ RowScale row_scale(float x, const NormArgs& a) {
   __shared__ float part[32];
+  __shared__ RowScale scale;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   x = warp_sum(x);
   if (lane == 0) part[warp] = x;
   __syncthreads();
-  DF s = {part[0], 0.0f};
-  for (int w = 1; w < (int)(blockDim.x >> 5); ++w) s = df_add(s, part[w]);
-  return s;
+  if (warp == 0) {
+    const DF sum = warp_sum_exact(lane < (int)(blockDim.x >> 5) ? part[lane] : 0.0f);
+    const RowScale rs(inverse_rms(sum, (float)a.K, a.inv_K, a.eps));
+    if (lane == 0) scale = rs;
+  }
+  __syncthreads();  // after it a next call may write `part`, but not yet `scale`
+  return scale;
 }
 
 // The last block of a norm's grid clears the scales of the last tile's missing rows.
@@ -318,95 +441,108 @@ __device__ __forceinline__ void clear_missing(const NormArgs& a, int G) {
     *reinterpret_cast<uint32_t*>(a.scales + scale_word(a.rows + u / G, u % G, G)) = 0;
 }
 
-// One block a row, the row in registers: P pieces of eight elements a thread.
-template <int DT, int FMT, int P>
-__global__ void __launch_bounds__(1024 / P) rmsnorm_kernel(NormArgs a) {
-  const int G = groups(a.K), Kp = G * kGroup, row = blockIdx.x;
-  if (row == a.rows) {
+// A block takes rows in turn, each in registers (eight elements a thread), and loads the next one
+// while it works on a row: the block's sum and what follows it would leave the memory idle
+// otherwise. The weight stays in registers. The last block clears the missing rows' scales.
+template <int DT, int WDT, int FMT>
+__global__ void __launch_bounds__(1024) rmsnorm_kernel(NormArgs a) {
+  constexpr bool kExact = DT == SPEC_BF16 && WDT == SPEC_BF16;
+  const int G = groups(a.K), Kp = G * kGroup, blocks = gridDim.x - 1;
+  if ((int)blockIdx.x == blocks) {
     clear_missing(a, G);
     return;
   }
-  float h[P][8], ss = 0.0f;
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    const int k = 8 * (threadIdx.x + p * blockDim.x);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[p][i] = 0.0f;
-    if (k < a.K) load_h<DT>(a, row, k, h[p]);
+  const int k = 8 * threadIdx.x;
+  Pair<DT> next;
+  Piece<WDT> w;
+  clear<DT>(next.x);
+  clear<DT>(next.r);
+  clear<WDT>(w);
+  if (k < a.K) {
+    load_pair<DT>(a, blockIdx.x, k, next);
+    load8<WDT, true>(a.weight, 0, k, a.K, a.wvec, w);
   }
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      s0 = fmaf(h[p][i], h[p][i], s0);
-      s1 = fmaf(h[p][i + 1], h[p][i + 1], s1);
-    }
-    ss += s0 + s1;
-    const int k = 8 * (threadIdx.x + p * blockDim.x);
-    if (a.res && k < a.K) store8<DT>(a.res_out, (size_t)row * a.ldo, k, a.K, a.vec, h[p]);
-  }
-  const DF rstd = inverse_rms(block_sum_pair(ss), (float)a.K, a.eps);
   bool finite = true;
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    const int k = 8 * (threadIdx.x + p * blockDim.x);
-    float w[8];
+  for (int row = blockIdx.x; row < a.rows; row += blocks) {
+    Piece<DT> h;
+    clear<DT>(h);
     if (k < a.K) {
-      load_w(a, k, w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) h[p][i] = scaled(h[p][i], rstd, w[i]);
+      h = add_pair<DT>(a, row, k, next);
+      if (row + blocks < a.rows) load_pair<DT>(a, row + blocks, k, next);
     }
-    if (k - 8 * (threadIdx.x & 31) < Kp)  // uniform in a warp
-      finite &= quantize8<FMT>(h[p], row, k / kGroup, G, k < Kp, a.codes, a.scales);
+    const RowScale rs = row_scale(sum_squares<DT>(h), a);
+    float y[8], v[8];
+    unpack<DT>(h, y);
+    unpack<WDT>(w, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = k + i < a.K ? scaled<kExact>(y[i], rs, v[i]) : 0.0f;
+    finite &= quantize8<FMT>(y, k < Kp,
+                             a.codes + ((size_t)row * G * kGroup + k) / 8 * kLaneCode<FMT>,
+                             a.scales + scale_word(row, k / kGroup, G));
   }
   if (!finite) atomicOr(a.status, SPEC_DEV_NONFINITE);
 }
 
-// Rows too long for registers: read twice (the second time from cache).
-template <int DT, int FMT>
+// Rows too long for registers, one block each: read twice (the second time from cache).
+template <int DT, int WDT, int FMT>
 __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(NormArgs a) {
+  constexpr bool kExact = DT == SPEC_BF16 && WDT == SPEC_BF16;
   const int G = groups(a.K), Kp = G * kGroup, row = blockIdx.x, step = 8 * blockDim.x;
   if (row == a.rows) {
     clear_missing(a, G);
     return;
   }
+  NormArgs sum_only = a;
+  sum_only.res_out = nullptr;
   DF sum = df_zero();  // a chain of K / 8192 pieces: exact additions
   for (int k = 8 * threadIdx.x; k < a.K; k += step) {
-    float h[8], s = 0.0f;
-    load_h<DT>(a, row, k, h);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s = fmaf(h[i], h[i], s);
-    sum = df_add(sum, s);
+    Pair<DT> p;
+    load_pair<DT>(a, row, k, p);
+    sum = df_add(sum, sum_squares<DT>(add_pair<DT>(sum_only, row, k, p)));
   }
-  const DF rstd = inverse_rms(block_sum_pair(df_float(sum)), (float)a.K, a.eps);
+  const RowScale rs = row_scale(df_float(sum), a);
+  uint8_t* codes = a.codes + (size_t)row * G * kGroupCode<FMT>;
   bool finite = true;
   for (int k0 = 0; k0 < Kp; k0 += step) {
     const int k = k0 + 8 * threadIdx.x;
-    float h[8] = {0, 0, 0, 0, 0, 0, 0, 0}, w[8];
+    float h[8] = {0, 0, 0, 0, 0, 0, 0, 0}, v[8];
     if (k < a.K) {
-      load_h<DT>(a, row, k, h);
-      if (a.res) store8<DT>(a.res_out, (size_t)row * a.ldo, k, a.K, a.vec, h);
-      load_w(a, k, w);
+      Pair<DT> p;
+      Piece<WDT> w;
+      load_pair<DT>(a, row, k, p);
+      unpack<DT>(add_pair<DT>(a, row, k, p), h);
+      load8<WDT, true>(a.weight, 0, k, a.K, a.wvec, w);
+      unpack<WDT>(w, v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[i] = scaled(h[i], rstd, w[i]);
+      for (int i = 0; i < 8; ++i) h[i] = k + i < a.K ? scaled<kExact>(h[i], rs, v[i]) : 0.0f;
     }
-    finite &= quantize8<FMT>(h, row, k / kGroup, G, k < Kp, a.codes, a.scales);
+    finite &= quantize8<FMT>(h, k < Kp, codes + k / 8 * kLaneCode<FMT>,
+                             a.scales + scale_word(row, k / kGroup, G));
   }
   if (!finite) atomicOr(a.status, SPEC_DEV_NONFINITE);
 }
 
-template <int DT, int FMT>
+template <int DT, int WDT, int FMT>
 void launch_norm_t(const NormArgs& a, cudaStream_t s) {
-  const int pieces = groups(a.K) * (kGroup / 8), grid = a.rows + 1;
-  // one piece a thread while rows are few and latency counts (1 row of 4096: 512 threads), more
-  // pieces and smaller blocks, of which an SM holds several rows, once they are many
-  const int most = a.rows <= 2 * num_sms() ? 1024 : 256;
-  auto threads = [&](int p) { return (pieces + p * 32 - 1) / (p * 32) * 32; };
-  if (threads(1) <= most) rmsnorm_kernel<DT, FMT, 1><<<grid, threads(1), 0, s>>>(a);
-  else if (threads(2) <= (most < 512 ? most : 512)) rmsnorm_kernel<DT, FMT, 2><<<grid, threads(2), 0, s>>>(a);
-  else if (threads(4) <= 256) rmsnorm_kernel<DT, FMT, 4><<<grid, threads(4), 0, s>>>(a);
-  else rmsnorm_long_kernel<DT, FMT><<<grid, 1024, 0, s>>>(a);
+  const int pieces = groups(a.K) * (kGroup / 8), threads = (pieces + 31) / 32 * 32;
+  if (threads > 1024) {
+    rmsnorm_long_kernel<DT, WDT, FMT><<<a.rows + 1, 1024, 0, s>>>(a);
+    return;
+  }
+  auto k = rmsnorm_kernel<DT, WDT, FMT>;
+  static int per_sm[33] = {};  // resident blocks by warps of a block
+  int& n = per_sm[threads / 32];
+  if (!n && (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, threads, 0) != cudaSuccess ||
+             n < 1))
+    n = 1;
+  const int blocks = a.rows < n * num_sms() ? a.rows : n * num_sms();
+  k<<<blocks + 1, threads, 0, s>>>(a);
+}
+
+template <int DT, int WDT>
+void launch_norm_w(const NormArgs& a, int fmt, cudaStream_t s) {
+  fmt == SPEC_MX_E2M1 ? launch_norm_t<DT, WDT, SPEC_MX_E2M1>(a, s)
+                      : launch_norm_t<DT, WDT, SPEC_MX_E4M3>(a, s);
 }
 
 int grid_for(long long units) {
@@ -458,16 +594,17 @@ void launch_rmsnorm_mx(const void* x, long long ldx, const void* res, long long 
                        cudaStream_t s) {
   using namespace mx;
   TraceScope ts(SPEC_KCLASS_OTHER, s);
-  NormArgs a{x, res, res_out, weight, ldx, ldr, ldo, rows, K, wdt, eps, false, false, codes,
+  NormArgs a{x, res, res_out, weight, ldx, ldr, ldo, rows, K, eps, 1.0f / (float)K, false, false,
+             codes,
              scales, status};
   a.vec = vec_ok(x, ldx, dt) && (!res || (vec_ok(res, ldr, dt) && vec_ok(res_out, ldo, dt)));
   a.wvec = vec_ok(weight, 0, wdt);
   if (dt == SPEC_BF16)
-    fmt == SPEC_MX_E2M1 ? launch_norm_t<SPEC_BF16, SPEC_MX_E2M1>(a, s)
-                        : launch_norm_t<SPEC_BF16, SPEC_MX_E4M3>(a, s);
+    wdt == SPEC_BF16 ? launch_norm_w<SPEC_BF16, SPEC_BF16>(a, fmt, s)
+                     : launch_norm_w<SPEC_BF16, SPEC_F32>(a, fmt, s);
   else
-    fmt == SPEC_MX_E2M1 ? launch_norm_t<SPEC_F32, SPEC_MX_E2M1>(a, s)
-                        : launch_norm_t<SPEC_F32, SPEC_MX_E4M3>(a, s);
+    wdt == SPEC_BF16 ? launch_norm_w<SPEC_F32, SPEC_BF16>(a, fmt, s)
+                     : launch_norm_w<SPEC_F32, SPEC_F32>(a, fmt, s);
 }
 
 }  // namespace spec

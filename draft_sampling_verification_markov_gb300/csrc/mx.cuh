@@ -54,21 +54,35 @@ __device__ __forceinline__ float scale_value(int byte) {
                                            : (byte == 0 ? 0x00400000u : (uint32_t)byte << 23));
 }
 
-// Two values to the format, nearest with ties to even (the second in the upper half).
-__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
+// Eight values to the format, nearest with ties to even; the first in the lowest bits.
+__device__ __forceinline__ uint2 to_e4m3x8(const float (&y)[8]) {
+  uint2 c;
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\t"
+      "mov.b32 %0, {a, b};\n\t}"
+      : "=r"(c.x)
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]));
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\t"
+      "mov.b32 %0, {a, b};\n\t}"
+      : "=r"(c.y)
+      : "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+  return c;
 }
 
-__device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 t;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\t"
-      "cvt.u32.u8 %0, t;\n\t}"
-      : "=r"(r)
-      : "f"(hi), "f"(lo));
-  return r;
+__device__ __forceinline__ uint32_t to_e2m1x8(const float (&y)[8]) {
+  uint32_t c;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(c)
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+  return c;
 }
 
 // Values of two codes (exact in fp16, the instruction's result type); the upper bits of c are
