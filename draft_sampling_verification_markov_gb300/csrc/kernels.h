@@ -107,6 +107,8 @@ bool make_tensor_map_bf16(CUtensorMap* m, const void* base, int rank, const cuui
 // a 128-byte swizzle; 4-bit codes are spread over 16-byte units on the way.
 bool make_tensor_map_codes(CUtensorMap* m, const void* base, int fmt, int Kp, int rows,
                            int box_rows);
+// A 2-D map of 512-byte scale tiles, one a box.
+bool make_tensor_map_scales(CUtensorMap* m, const void* base, long long tiles);
 // Consume the test request that makes the next tensor-core launch never load its first W2
 // tile (spec_test_stall_next_markov).
 int take_stall_request();

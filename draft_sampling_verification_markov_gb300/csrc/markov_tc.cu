@@ -841,6 +841,16 @@ bool make_tensor_map_codes(CUtensorMap* m, const void* base, int fmt, int Kp, in
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_tensor_map_scales(CUtensorMap* m, const void* base, long long tiles) {
+  if (!tc::encode_fn()) return false;
+  const cuuint64_t dims[2] = {128, (cuuint64_t)tiles}, strides[1] = {512};
+  const cuuint32_t box[2] = {128, 1}, estr[2] = {1, 1};
+  return tc::encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims,
+                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t launch_markov_tc(const RowJob& j, float* pm, float* ps, int* pi, bool argmax,
                              cudaStream_t s) {
   using namespace tc;

@@ -244,16 +244,32 @@ __host__ __device__ constexpr uint32_t block_scale_ids(int b) {
   return ((uint32_t)b << 29) | ((uint32_t)b << 4);
 }
 
-// D (+)= (A * sA) x (B * sB)^T, 32 elements of K, one scale a row of each operand in tensor
-// memory (lane = row % 32, column = row / 32).
-__device__ __forceinline__ void mma_mx(uint32_t lead, uint32_t d_tmem, uint64_t a_desc,
-                                       uint64_t b_desc, uint32_t idesc, uint32_t sa_tmem,
-                                       uint32_t sb_tmem, uint32_t accumulate) {
+// 1 in one lane of a converged warp, 0 in the others. A warp whose lanes all run an issue loop,
+// with only the asynchronous instructions predicated on this, keeps their operands in uniform
+// registers.
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r;
+}
+
+// ---- CTA pairs (cta_group::2): the even CTA of a two-CTA cluster issues for both.
+
+// D (+)= (A * sA) x (B * sB)^T, 32 elements of K, M = 256: each CTA holds its 128 rows of A and of
+// D, half the rows of B, and one scale a row of its A and of all of B in tensor memory (lane =
+// row % 32, column = row / 32). `lead`: issue from this lane.
+__device__ __forceinline__ void mma_mx_pair(uint32_t lead, uint32_t d_tmem, uint64_t a_desc,
+                                            uint64_t b_desc, uint32_t idesc, uint32_t sa_tmem,
+                                            uint32_t sb_tmem, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %6, 0;\n\t"
       "setp.ne.b32 q, %7, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X "
+      "@q tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X "
       "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate), "r"(lead)
       : "memory");
@@ -266,42 +282,52 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
          ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
 }
 
-// 512 bytes of shared memory to four columns of tensor memory: row i to lane i of each of the
-// four lane quarters.
-__device__ __forceinline__ void copy_scales(uint32_t lead, uint32_t taddr, uint64_t desc) {
+// 512 bytes of each CTA's shared memory to four columns of its tensor memory: row i to lane i of
+// each of the four lane quarters.
+__device__ __forceinline__ void copy_scales_pair(uint32_t lead, uint32_t taddr, uint64_t desc) {
   asm volatile(
       "{\n\t.reg .pred q;\n\t"
       "setp.ne.b32 q, %2, 0;\n\t"
-      "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+      "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
       "l"(desc), "r"(lead)
       : "memory");
 }
 
-// mma_commit from the lane with `lead` set.
-__device__ __forceinline__ void mma_commit_if(uint32_t lead, uint64_t* bar) {
+// Arrive on the barrier at this offset in the CTAs of `mask` once the MMAs issued so far are done.
+__device__ __forceinline__ void commit_pair(uint32_t lead, uint64_t* bar, uint16_t mask = 3) {
   asm volatile(
       "{\n\t.reg .pred q;\n\t"
       "setp.ne.b32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
-          smem_u32(bar)),
-      "r"(lead)
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
+      ".multicast::cluster.b64 [%0], %2;\n\t}" ::"r"(smem_u32(bar)),
+      "r"(lead), "h"(mask)
       : "memory");
 }
 
-// 1 in one lane of a converged warp, 0 in the others. A warp whose lanes all run an issue loop,
-// with only the tcgen05 instructions predicated on this, keeps their operands in uniform
-// registers.
-__device__ __forceinline__ uint32_t elect_lane() {
+// The cluster address of a local shared-memory object in CTA `rank`.
+__device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t rank) {
   uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r));
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
   return r;
 }
 
-// Forms of the producer's instructions for a converged warp, issued by the lane with `lead` set.
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+               : "memory");
+}
+
+// Tile copy into this CTA that reports to a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t lead, void* dst, const CUtensorMap* map,
+                                                 int c0, int c1, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %6, 0;\n\t"
+      "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".cta_group::2.L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;\n\t}" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar), "l"(policy), "r"(lead)
+      : "memory");
+}
+
 __device__ __forceinline__ void expect_tx_if(uint32_t lead, uint64_t* bar, uint32_t bytes) {
   asm volatile(
       "{\n\t.reg .pred q;\n\t"
@@ -311,28 +337,9 @@ __device__ __forceinline__ void expect_tx_if(uint32_t lead, uint64_t* bar, uint3
       : "memory");
 }
 
-__device__ __forceinline__ void tma_load_2d_if(uint32_t lead, void* dst, const CUtensorMap* map,
-                                               int c0, int c1, uint64_t* bar, uint64_t policy) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.b32 q, %6, 0;\n\t"
-      "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;\n\t}" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar)), "l"(policy),
-      "r"(lead)
-      : "memory");
-}
-
-// Untiled bulk copy global -> shared (16-byte aligned addresses and size).
-__device__ __forceinline__ void bulk_load_if(uint32_t lead, void* dst, const void* src,
-                                             uint32_t bytes, uint64_t* bar, uint64_t policy) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "@q cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
-      "[%0], [%1], %2, [%3], %4;\n\t}" ::"r"(smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy), "r"(lead)
-      : "memory");
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Packed pair arithmetic (two fp32 lanes per instruction).
