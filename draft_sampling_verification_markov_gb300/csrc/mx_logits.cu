@@ -5,7 +5,7 @@
 // out[m, v] = sum over blocks b of 2^(ea[m, b] + ew[v, b]) sum_{k in b} a[m, k] w[v, k].
 //
 // The vocabulary is the M side of the instruction (always full) and the hidden rows its N side (32
-// .. 192 of them), so that one request costs no more tensor-core rows than it must and the
+// .. 256 of them), so that one request costs no more tensor-core rows than it must and the
 // vocabulary matrix, which is the traffic at small batches, is read once for all of them. CTAs work
 // in pairs (cta_group::2) on tiles of 256 tokens x NT rows: each holds 128 tokens' codes and half
 // of the hidden rows' codes. A single CTA on 128 tokens x 192 rows was bound by its shared memory
@@ -18,9 +18,10 @@
 //                  took longer than the copies;
 //   warp 1         of the even CTA copies a stage's scales to tensor memory and issues four MMAs
 //                  of 32 elements for the pair;
-//   warps 4-7      read the finished fp32 tile from tensor memory (two accumulators, so that the
-//                  next tile's MMAs run meanwhile), round and store it: lanes are tokens, so a warp
-//                  stores 32 consecutive tokens of one row at a time.
+//   warps 4-11     read the finished fp32 tile from tensor memory, round and store it: lanes are
+//                  tokens, so a warp stores 32 consecutive tokens of one row at a time. Up to 192
+//                  rows two accumulators alternate; above, tensor memory holds one beside the
+//                  scales.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -35,9 +36,11 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
 constexpr int kTileV = 128;                     // vocabulary rows of a CTA's tile
-constexpr int kMaxNT = 192;                     // hidden rows of a tile at most
+constexpr int kMaxNT = 256;                     // hidden rows of a tile at most
+constexpr int kTwoNT = 192;                     // ... with two accumulators
+constexpr int kChunks = kMaxNT / 32 / 2;        // 32-row chunks of an epilogue warp
 constexpr int kWBytes = kTileV * kGroup;        // a stage's vocabulary codes, spread to bytes
 constexpr int kScaleBytes = 3 * kTileBytes;     // one tile of vocabulary scales, two of hidden
 constexpr int kMaxStages = 10;
@@ -45,7 +48,9 @@ constexpr int kScaleCols = 12;                  // tensor-memory columns of a st
 constexpr int kTmemCols = 512;
 constexpr size_t kSmemMax = 232448;
 constexpr size_t kSmemFixed = 1024 + 512;       // alignment of the ring, barriers
-static_assert(2 * kMaxNT + kMaxStages * kScaleCols <= kTmemCols, "tensor memory");
+static_assert(2 * kTwoNT + kMaxStages * kScaleCols <= kTmemCols &&
+                  kMaxNT + kMaxStages * kScaleCols <= kTmemCols,
+              "tensor memory");
 static_assert((2 * kMaxStages + 5) * 8 + 8 <= 512, "room for the barriers");
 
 struct LogitArgs {
@@ -53,6 +58,7 @@ struct LogitArgs {
   long long ldo;
   int M, V, G;
   int NT, n_tok;        // hidden rows of a tile, tiles of them
+  int n_acc;            // accumulators
   int n_voc;            // 128-row tiles of the vocabulary
   long long units;      // pairs of vocabulary tiles x hidden tiles
   int stages;
@@ -87,6 +93,36 @@ struct Work {
   }
 };
 
+// Rows m .. m + min(32, n) - 1 of token v (this lane's), from their fp32 sums.
+__device__ __forceinline__ void store_chunk(const LogitArgs& p, const uint32_t (&x)[32], int m,
+                                            int n, int v) {
+  const size_t at = (size_t)m * p.ldo + v;
+  const bool live = v < p.V;
+  if (p.odt == SPEC_F32) {
+    uint32_t* o = reinterpret_cast<uint32_t*>(p.out) + at;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j < n && live) o[(size_t)j * p.ldo] = x[j];
+  } else if (p.pairs) {
+    // neighbouring lanes trade halves: the even lane stores both tokens of row j, the odd one
+    // those of row j + 1
+    const bool odd = threadIdx.x & 1;
+    uint16_t* o = reinterpret_cast<uint16_t*>(p.out) + at - odd + (odd ? p.ldo : 0);
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      const uint32_t both = pack_bf16(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, both, 1);
+      const uint32_t b = odd ? __byte_perm(other, both, 0x7632) : __byte_perm(both, other, 0x5410);
+      if (j + odd < n && live) *reinterpret_cast<uint32_t*>(o + (size_t)j * p.ldo) = b;
+    }
+  } else {
+    uint16_t* o = reinterpret_cast<uint16_t*>(p.out) + at;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j < n && live) o[(size_t)j * p.ldo] = (uint16_t)pack_bf16(__uint_as_float(x[j]), 0.0f);
+  }
+}
+
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     logits_kernel(const __grid_constant__ CUtensorMap map_w,
                   const __grid_constant__ CUtensorMap map_a,
@@ -116,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);   // each CTA's own
-      mbar_init(&acc_empty[i], 8);  // the even CTA's: both CTAs' epilogue warps
+      mbar_init(&acc_empty[i], 16);  // the even CTA's: both CTAs' epilogue warps
     }
     mbar_init(done, 1);
     *abort = 0;
@@ -134,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   cluster_sync();  // the pair's barriers are ready
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t sf_col0 = 2 * p.NT;  // scales after the two accumulators
+  const uint32_t sf_col0 = p.n_acc * p.NT;  // scales after the accumulators
 
   if (warp == 0 || warp == 2 || warp == 3) {
     // ------------------------------------------------------------------ copies
@@ -210,8 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       }
       if (!ok) break;
       commit_pair(lead, &acc_full[as]);
-      as ^= 1;
-      if (as == 0) aph ^= 1;
+      if (++as == p.n_acc) { as = 0; aph ^= 1; }
     }
     // every MMA issued here completes before tensor memory is released
     commit_pair(lead, done, 1);
@@ -219,50 +254,36 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------------------------ epilogue
-    const int q = warp & 3;  // the lane quarter this warp may read
+    // Two warps a lane quarter share its 32-row chunks. A warp takes all of its chunks into
+    // registers first, so that a single accumulator is free again after some hundred cycles and
+    // the stores run beside the next tile's MMAs.
+    const int q = warp & 3;            // the lane quarter this warp may read
+    const int half = (warp - 4) >> 2;
     int as = 0;
     uint32_t aph = 0;
     for (long long u = u_first; u < p.units; u += u_step) {
       const Work w(p, u, rank);
-      if (!mbar_wait(&acc_full[as], aph, abort, p.status)) break;
+      if (!mbar_wait_warp(&acc_full[as], aph, abort, p.status)) break;
       tc_fence_after();
-      const int v = w.vt * kTileV + q * 32 + lane;
-      for (int c = 0; c < w.rows; c += 32) {
-        float x[32];
-        tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + as * p.NT + c, x);
-        if (c + 32 >= w.rows) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) arrive_cluster(in_cta(&acc_empty[as], 0));
-        }
-        const int n = w.rows - c;
-        const size_t at = (size_t)(w.m0 + c) * p.ldo + v;
-        if (p.odt == SPEC_F32) {
-          float* o = reinterpret_cast<float*>(p.out) + at;
+      uint32_t x[kChunks][32];
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (j < n && v < p.V) o[(size_t)j * p.ldo] = x[j];
-        } else if (p.pairs) {
-          // neighbouring lanes trade halves: the even lane stores both tokens of row j, the odd
-          // one those of row j + 1
-          const bool odd = lane & 1;
-          uint16_t* o = reinterpret_cast<uint16_t*>(p.out) + at - odd;
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            const float other = __shfl_xor_sync(0xffffffffu, odd ? x[j] : x[j + 1], 1);
-            const uint32_t b = odd ? pack_bf16(other, x[j + 1]) : pack_bf16(x[j], other);
-            if (j + odd < n && v < p.V)
-              *reinterpret_cast<uint32_t*>(o + (size_t)(j + odd) * p.ldo) = b;
-          }
-        } else {
-          uint16_t* o = reinterpret_cast<uint16_t*>(p.out) + at;
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (j < n && v < p.V) o[(size_t)j * p.ldo] = (uint16_t)pack_bf16(x[j], 0.0f);
-        }
+      for (int i = 0; i < kChunks; ++i) {
+        const int c = 32 * (2 * i + half);
+        if (c < w.rows)
+          tmem_ld32_async(tmem + ((uint32_t)(q * 32) << 16) + as * p.NT + c, x[i]);
       }
-      as ^= 1;
-      if (as == 0) aph ^= 1;
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(in_cta(&acc_empty[as], 0));
+      const int v = w.vt * kTileV + q * 32 + lane;
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        const int c = 32 * (2 * i + half);
+        if (c >= w.rows) break;
+        store_chunk(p, x[i], w.m0 + c, w.rows - c, v);
+      }
+      if (++as == p.n_acc) { as = 0; aph ^= 1; }
     }
   }
 
@@ -324,6 +345,7 @@ cudaError_t launch_mx_logits(const uint8_t* ac, const uint8_t* as, int af, const
   p.n_tok = (M + kMaxNT - 1) / kMaxNT;
   p.NT = p.n_tok == 1 ? (M + 31) / 32 * 32 : ((M + p.n_tok - 1) / p.n_tok + 63) / 64 * 64;
   p.n_tok = (M + p.NT - 1) / p.NT;
+  p.n_acc = p.NT <= kTwoNT ? 2 : 1;
   p.n_voc = (V + kTileV - 1) / kTileV;
   p.units = (long long)((p.n_voc + 1) / 2) * p.n_tok;
   const size_t stage = kWBytes + (size_t)p.NT / 2 * kGroup + kScaleBytes;
