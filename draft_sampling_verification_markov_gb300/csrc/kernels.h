@@ -109,6 +109,9 @@ bool make_tensor_map_codes(CUtensorMap* m, const void* base, int fmt, int Kp, in
                            int box_rows);
 // A 2-D map of 512-byte scale tiles, one a box.
 bool make_tensor_map_scales(CUtensorMap* m, const void* base, long long tiles);
+// A 2-D bf16 output map (row stride ld elements, a multiple of 8) without a swizzle.
+bool make_tensor_map_out(CUtensorMap* m, void* base, int cols, int rows, long long ld,
+                         int box_cols, int box_rows);
 // Consume the test request that makes the next tensor-core launch never load its first W2
 // tile (spec_test_stall_next_markov).
 int take_stall_request();

@@ -841,6 +841,18 @@ bool make_tensor_map_codes(CUtensorMap* m, const void* base, int fmt, int Kp, in
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_tensor_map_out(CUtensorMap* m, void* base, int cols, int rows, long long ld,
+                         int box_cols, int box_rows) {
+  if (!tc::encode_fn()) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, estr[2] = {1, 1};
+  return tc::encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                         CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_tensor_map_scales(CUtensorMap* m, const void* base, long long tiles) {
   if (!tc::encode_fn()) return false;
   const cuuint64_t dims[2] = {128, (cuuint64_t)tiles}, strides[1] = {512};

@@ -24,6 +24,7 @@
 //                  scales.
 #include <cuda_runtime.h>
 #include <stdint.h>
+#include <string.h>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -47,7 +48,9 @@ constexpr int kMaxStages = 10;
 constexpr int kScaleCols = 12;                  // tensor-memory columns of a stage's scales
 constexpr int kTmemCols = 512;
 constexpr size_t kSmemMax = 232448;
-constexpr size_t kSmemFixed = 1024 + 512;       // alignment of the ring, barriers
+constexpr int kOutRows = 16;                    // rows of a staged piece of bf16 output
+constexpr int kOutBytes = kOutRows * kTileV * 2;
+constexpr size_t kSmemFixed = 1024 + 512 + 4 * kOutBytes;  // alignment, barriers, staged output
 static_assert(2 * kTwoNT + kMaxStages * kScaleCols <= kTmemCols &&
                   kMaxNT + kMaxStages * kScaleCols <= kTmemCols,
               "tensor memory");
@@ -65,7 +68,8 @@ struct LogitArgs {
   uint32_t w_bytes, a_bytes;  // code bytes a copy reports (the gaps of 4-bit codes not counted)
   uint32_t idesc;       // without N
   int odt;
-  bool pairs;           // two tokens in one store
+  bool staged;          // bf16 output through shared memory and bulk stores
+  bool pairs;           // ... else two tokens in one store
   int stall;            // test request: never load the first tile
   uint32_t* status;
 };
@@ -127,13 +131,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     logits_kernel(const __grid_constant__ CUtensorMap map_w,
                   const __grid_constant__ CUtensorMap map_a,
                   const __grid_constant__ CUtensorMap map_ws,
-                  const __grid_constant__ CUtensorMap map_as, const LogitArgs p) {
+                  const __grid_constant__ CUtensorMap map_as,
+                  const __grid_constant__ CUtensorMap map_out, const LogitArgs p) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const int S = p.stages, b_bytes = p.NT / 2 * kGroup;
   unsigned char* sA = ring;                          // [S][kWBytes]
   unsigned char* sB = sA + (size_t)S * kWBytes;      // [S][b_bytes]
-  unsigned char* sS = sB + (size_t)S * b_bytes;      // [S][kScaleBytes]
+  unsigned char* sO = sB + (size_t)S * b_bytes;      // [2 halves][2][kOutBytes]
+  unsigned char* sS = sO + 4 * kOutBytes;            // [S][kScaleBytes]
   uint64_t* full = reinterpret_cast<uint64_t*>(sS + (size_t)S * kScaleBytes);
   uint64_t* empty = full + kMaxStages;
   uint64_t* acc_full = empty + kMaxStages;
@@ -259,6 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     // the stores run beside the next tile's MMAs.
     const int q = warp & 3;            // the lane quarter this warp may read
     const int half = (warp - 4) >> 2;
+    const int issuer = 128 * (1 + half);  // the half's thread that hands pieces over
     int as = 0;
     uint32_t aph = 0;
     for (long long u = u_first; u < p.units; u += u_step) {
@@ -277,14 +284,47 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       __syncwarp();
       if (lane == 0) arrive_cluster(in_cta(&acc_empty[as], 0));
       const int v = w.vt * kTileV + q * 32 + lane;
+      if (p.staged) {
+        // pieces of 16 rows x 128 tokens, two buffers a half: the half's four warps write their
+        // tokens, one thread hands the piece to the copy engine, which clips it to the output
 #pragma unroll
-      for (int i = 0; i < kChunks; ++i) {
-        const int c = 32 * (2 * i + half);
-        if (c >= w.rows) break;
-        store_chunk(p, x[i], w.m0 + c, w.rows - c, v);
+        for (int i = 0; i < 2 * kChunks; ++i) {
+          const int c = 32 * (i - i % 2 + half) + kOutRows * (i % 2);
+          if (c >= w.rows) break;
+          const uint32_t buf = smem_u32(sO + (2 * half + i % 2) * kOutBytes);
+          if (threadIdx.x == issuer)
+            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
+          const uint32_t at = buf + (q * 32 + lane) * 2;
+#pragma unroll
+          for (int j = 0; j < kOutRows; ++j)
+            asm volatile("st.shared.b16 [%0], %1;" ::"r"(at + j * kTileV * 2),
+                         "h"((uint16_t)pack_bf16(
+                             __uint_as_float(x[i / 2][kOutRows * (i % 2) + j]), 0.0f))
+                         : "memory");
+          fence_async_smem();
+          asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
+          if (threadIdx.x == issuer) {
+            asm volatile(
+                "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                    reinterpret_cast<uint64_t>(&map_out)),
+                "r"(w.vt * kTileV), "r"(w.m0 + c), "r"(buf)
+                : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          const int c = 32 * (2 * i + half);
+          if (c >= w.rows) break;
+          store_chunk(p, x[i], w.m0 + c, w.rows - c, v);
+        }
       }
       if (++as == p.n_acc) { as = 0; aph ^= 1; }
     }
+    // staged pieces are read before shared memory goes away
+    if (threadIdx.x == issuer) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
 
   tc_fence_before();
@@ -357,17 +397,22 @@ cudaError_t launch_mx_logits(const uint8_t* ac, const uint8_t* as, int af, const
   p.idesc = tc::idesc_mx(2 * kTileV, 0, wf == SPEC_MX_E2M1 ? e2m1 : e4m3,
                          af == SPEC_MX_E2M1 ? e2m1 : e4m3);
   p.odt = odt;
+  p.staged = odt == SPEC_BF16 && (ldo * 2) % 16 == 0 &&
+             (reinterpret_cast<uintptr_t>(out) & 15) == 0;
   p.pairs = V % 2 == 0 && ldo % 2 == 0 && (reinterpret_cast<uintptr_t>(out) & 3) == 0;
   p.stall = take_stall_request();
   p.status = status;
-  CUtensorMap mw, ma, mws, mas;
+  CUtensorMap mw, ma, mws, mas, mo;
+  memset(&mo, 0, sizeof mo);
+  if (p.staged && !make_tensor_map_out(&mo, out, V, M, ldo, kTileV, kOutRows))
+    return cudaErrorInvalidValue;
   if (!make_tensor_map_codes(&mw, wc, wf, padded(K), V, kTileV) ||
       !make_tensor_map_codes(&ma, ac, af, padded(K), M, p.NT / 2) ||
       !make_tensor_map_scales(&mws, wsc, (long long)p.n_voc * p.G) ||
       !make_tensor_map_scales(&mas, as, (long long)((M + kTileRows - 1) / kTileRows) * p.G))
     return cudaErrorInvalidValue;
   const int grid = 2 * (int)(p.units < pairs ? p.units : pairs);
-  logits_kernel<<<grid, kThreads, kSmemFixed + p.stages * stage, s>>>(mw, ma, mws, mas, p);
+  logits_kernel<<<grid, kThreads, kSmemFixed + p.stages * stage, s>>>(mw, ma, mws, mas, mo, p);
   return cudaGetLastError();
 }
 
