@@ -7,7 +7,8 @@ scheduler's lengths (section 6), and lossless rejection verification of the sche
 (speculative sampling with the residual / bonus draw). The token each request emits at the end
 of iteration t (its residual or bonus draw) is the anchor x_0 of iteration t + 1; iteration t
 reads slice t of the pre-drawn uniforms. The logit tensors stay fixed across iterations (the
-models that would produce new logits are outside this library).
+models that would produce new logits are outside this library), unless a vocabulary head computes
+the draft's from each iteration's hidden states.
 
 Every step is a call into libspecmarkov (argument marshalling only), and the iterations can be
 captured into one CUDA graph so that no host round trip separates them.
@@ -39,12 +40,32 @@ class SpecLoop:
     are packed into B = sum_r (1 + l_r) consecutive rows with per-request offsets, the target
     normalisers are packed alike, and rejection verification reads the packed rows. The
     packing copy stands in for a target model that writes only the B scheduled rows; the
-    outputs equal the padded loop's bit for bit."""
+    outputs equal the padded loop's bit for bit.
+
+    With `head` (a head.VocabHead) every iteration t first computes the draft's base logits
+    from hidden[t], hidden [iters, R, gamma, K] (plus residual[t], of the same shape, when given):
+    "Module deepseek_v4_mtp", Forward, logits = lm_head(rms_norm(h)). U is then a buffer that
+    each iteration overwrites; it may be None.
+
+    With `logprobs` = k (0 .. 32) every iteration also scores its emitted tokens under the target
+    rows that they answer to, at the loop's temperature: token_logp, token_rank, token_entropy
+    [iters, R, gamma + 1] and the k most likely tokens of each row, top_ids and top_logp
+    [iters, R, gamma + 1, k]. Places past an iteration's emitted tokens keep NaN, 0 and -1."""
 
     def __init__(self, U, target, W1, W2, anchors0, u_draft, u_accept, u_resid, temperature,
                  sps=None, *, iterations=None, schedule=True, allowed=None,
-                 async_schedule=False, flat=False):
+                 async_schedule=False, flat=False, head=None, hidden=None, residual=None,
+                 logprobs=None):
+        if (head is None) != (hidden is None) or (residual is not None and head is None):
+            raise ValueError("head and hidden go together, residual with them")
+        if head is not None and U is None:
+            R, gamma = hidden.shape[1:3]
+            U = torch.empty(R, gamma, head.V, dtype=target.dtype, device=target.device)
         R, gamma, V = U.shape
+        if head is not None and (tuple(hidden.shape[1:]) != (R, gamma, head.K) or head.V != V):
+            raise ValueError("hidden must be [iters, R, gamma, K] of a head over U's vocabulary")
+        if head is not None and residual is not None and residual.shape != hidden.shape:
+            raise ValueError("residual must have hidden's shape")
         self.R, self.gamma, self.V = R, gamma, V
         self.iters = int(iterations if iterations is not None else u_draft.shape[0])
         self.U, self.target, self.W1, self.W2 = U, target, W1, W2
@@ -79,6 +100,21 @@ class SpecLoop:
             self.offsets = torch.empty(R + 1, **i32)
             self.packed_target = torch.empty(R * (gamma + 1), V, dtype=target.dtype, device=dev)
             self.packed_stats = torch.empty(R * (gamma + 1), 2, **f32)
+        self.head, self.hidden, self.residual = head, hidden, residual
+        self.logprobs = None if logprobs is None else int(logprobs)
+        if head is not None and self.iters > hidden.shape[0]:
+            raise ValueError("hidden must have a slice for every iteration")
+        if head is not None:
+            self.draft_hidden = (torch.empty(R, gamma, head.K, dtype=hidden.dtype, device=dev)
+                                 if residual is not None else None)
+        if self.logprobs is not None:
+            k = self.logprobs
+            nan, ninf = float("nan"), -float("inf")
+            self.token_logp = torch.full((n, R, gamma + 1), nan, **f32)
+            self.token_rank = torch.zeros(n, R, gamma + 1, **i32)
+            self.token_entropy = torch.full((n, R, gamma + 1), nan, **f32)
+            self.top_ids = torch.full((n, R, gamma + 1, k), -1, **i32) if k else None
+            self.top_logp = torch.full((n, R, gamma + 1, k), ninf, **f32) if k else None
         # one workspace large enough for every step, reserved before any capture
         self.ws = S.Workspace(device=dev)
         self.ws.reserve(int(S.lib().spec_workspace_bytes(S.SPEC_OP_ALL, R, gamma, V, self.rank)))
@@ -88,6 +124,10 @@ class SpecLoop:
         """Enqueue iteration t on `stream` (the current stream by default)."""
         ws, T = self.ws, self.temperature
         a_t = self.anchors[t]
+        if self.head is not None:
+            self.head.logits(self.hidden[t],
+                             None if self.residual is None else self.residual[t], out=self.U,
+                             residual_out=self.draft_hidden, workspace=ws, stream=stream)
         S.spec_markov_propose(self.U, self.W1, self.W2, a_t, self.u_draft[t], T,
                               draft_tokens=self.draft_tokens[t], draft_logp=self.draft_logp,
                               draft_stats=self.draft_stats, workspace=ws, stream=stream,
@@ -127,6 +167,7 @@ class SpecLoop:
                                          out_tokens=self.out_tokens[t],
                                          next_anchor=self.anchors[t + 1], workspace=ws,
                                          stream=stream, allowed=self.allowed)
+            self._score(t, stream)
             return
         S.spec_verify_rejection(self.target, self.U, self.W1, self.W2, a_t, self.draft_tokens[t],
                                 self.draft_logp, self.draft_stats, self.u_accept[t],
@@ -134,6 +175,18 @@ class SpecLoop:
                                 accept_len=self.accept_len[t], out_tokens=self.out_tokens[t],
                                 next_anchor=self.anchors[t + 1], workspace=ws, stream=stream,
                                 allowed=self.allowed)
+        self._score(t, stream)
+
+    def _score(self, t, stream):
+        """Log-probabilities of iteration t's emitted tokens: out_tokens[r, i] answers to target
+        row (r, i); its -1 padding is skipped."""
+        if self.logprobs is None:
+            return
+        out = S.TokenLogprobs(self.token_logp[t], self.token_rank[t], self.token_entropy[t],
+                              None if self.top_ids is None else self.top_ids[t],
+                              None if self.top_logp is None else self.top_logp[t])
+        S.spec_token_logprobs(self.target, self.out_tokens[t], self.temperature,
+                              top=self.logprobs, out=out, workspace=self.ws, stream=stream)
 
     def run(self, first: int = 0, last: int | None = None, stream=None):
         """Iterations first..last-1, enqueued eagerly. The loop state is anchors[first] and the
