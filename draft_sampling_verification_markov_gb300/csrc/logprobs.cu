@@ -42,6 +42,7 @@ constexpr int kMaxSplit = 8;          // parts of a row at most
 constexpr int kGroups = 64;           // maxima behind a bound; at least 2 * kMaxTop
 constexpr uint32_t kFull = 0xffffffffu;
 
+constexpr float kOctaves = 4.0f;
 constexpr float kLowest2 = -256.0f;   // 2^kLowest2 is 0 in fp32
 // The fast sums need log2(e) / T = c in (kFastLeast, kFastScale) and a reference with |m| c below
 // kFastMax. Then fl(m c) is off by less than 2^-14; -2^100 c is finite; and (-2^100 - m) c is far
@@ -271,9 +272,10 @@ __device__ __forceinline__ int count_larger(const uint4 (&q)[kBatch], float xt) 
   }
 }
 
-// A thread's sums against a reference `m`, one of its logits and at most 32 octaves of
-// exp((max - m) / T) below its maximum: 2^32 times the number of logits is far from overflow, and
-// the reference changes in few batches. fma(x, c, -fl(m c)) is (x - m) c + delta with delta the
+// A thread's sums against a reference `m`, one of its logits and at most kOctaves of
+// exp((max - m) / T) below its maximum, so that the reference changes in few batches. A term of S1
+// is up to kOctaves times one of S, and its roundings count against the entropy: with 32 octaves
+// the entropy of peaked rows was off by up to 2e-5. fma(x, c, -fl(m c)) is (x - m) c + delta with delta the
 // exact rounding error of m c, the same for every term: it is taken out of the sums where the
 // reference changes and at the end.
 struct RunningSums {
@@ -338,7 +340,7 @@ __device__ __forceinline__ void take_batch(Shared& sh, const uint4 (&q)[kBatch],
   if (bm > run.limit) {
     if (run.m > -INFINITY) run.rebase(bm, c, tame && run.tame(c) ? run.delta(c) : 0.0f);
     run.m = bm;
-    run.limit = bm + 32.0f / c;
+    run.limit = bm + kOctaves / c;
   }
   if (tame && run.tame(c)) {
     const float off = -(run.m * c);
