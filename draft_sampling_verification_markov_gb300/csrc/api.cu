@@ -874,10 +874,11 @@ int spec_tv_confidence_masked(const void* U, const void* target, int l_dtype, co
 
 static bool mx_fmt_ok(int fmt) { return fmt == SPEC_MX_E2M1 || fmt == SPEC_MX_E4M3; }
 
-// K small enough for int element indexes, and rows * K for int indexes of 128 x 128 tiles.
+// K small enough for int element indexes, and the padded rows for int indexes of their tiles and
+// of the kernels' blocks.
 static bool mx_sizes_ok(int rows, int K) {
   return rows >= 0 && rows <= (1 << 30) && K >= 1 && K <= (1 << 24) &&
-         (long long)rows * K <= (1LL << 44);
+         (long long)rows * mx::padded(K) <= (1LL << 42);
 }
 
 static bool mx_aligned(const void* codes, const void* scales) {
