@@ -173,6 +173,7 @@ class Workspace:
         self.buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=self.device)
         base = self.buf.data_ptr()
         self._off = (-base) % 256
+        self._addr = base + self._off
         self.nbytes = nbytes
         _check("spec_workspace_init", lib().spec_workspace_init(self.ptr, nbytes, _stream(stream)))
 
@@ -710,7 +711,7 @@ def _launch(name, dev, workspace, stream, *args):
     if ws.buf is None:
         ws.reserve(256, stream)
     st = _raw_stream(i) if stream is None else stream.cuda_stream
-    rc = getattr(_lib or lib(), name)(*args, ws.buf.data_ptr() + ws._off, ws.nbytes, st)
+    rc = getattr(_lib or lib(), name)(*args, ws._addr, ws.nbytes, st)
     if rc != SPEC_OK:
         raise SpecError(name, rc)
 
@@ -807,58 +808,36 @@ class TokenLogprobs:
     """Outputs of spec_token_logprobs: logp, rank, entropy [rows], top_ids, top_logp
     [rows, top]; None where not asked for."""
 
-    __slots__ = ("_f", "_i", "_n", "_top", "_t")
+    __slots__ = ("logp", "rank", "entropy", "top_ids", "top_logp")
 
     def __init__(self, logp=None, rank=None, entropy=None, top_ids=None, top_logp=None):
-        self._f = self._i = None
-        self._t = {"logp": logp, "rank": rank, "entropy": entropy, "top_ids": top_ids,
-                   "top_logp": top_logp}
+        self.logp, self.rank, self.entropy = logp, rank, entropy
+        self.top_ids, self.top_logp = top_ids, top_logp
 
     @classmethod
     def empty(cls, rows, top, tokens, device):
         """Uninitialised outputs for a call to write: every field, logp and rank only with
         `tokens`."""
-        r = cls.__new__(cls)
-        r._n, r._top = rows, top
-        r._f = torch.empty(rows * (2 + top), dtype=torch.float32, device=device)
-        r._i = torch.empty(rows * (1 + top), dtype=torch.int32, device=device)
-        r._t = {} if tokens else {"logp": None, "rank": None}
-        if not top:
-            r._t["top_ids"] = r._t["top_logp"] = None
-        return r
-
-    def _get(self, name):
-        if name not in self._t:
-            n, top = self._n, self._top
-            self._t[name] = (
-                self._f[:n] if name == "logp" else self._f[n:2 * n] if name == "entropy" else
-                self._i[:n] if name == "rank" else
-                (self._i[n:] if name == "top_ids" else self._f[2 * n:]).view(n, top))
-        return self._t[name]
-
-    logp = property(lambda self: self._get("logp"))
-    rank = property(lambda self: self._get("rank"))
-    entropy = property(lambda self: self._get("entropy"))
-    top_ids = property(lambda self: self._get("top_ids"))
-    top_logp = property(lambda self: self._get("top_logp"))
+        # tensors of their own: five small allocations take less than two and five views
+        f, i, new = torch.float32, torch.int32, torch.empty
+        return cls(new(rows, dtype=f, device=device) if tokens else None,
+                   new(rows, dtype=i, device=device) if tokens else None,
+                   new(rows, dtype=f, device=device),
+                   new(rows, top, dtype=i, device=device) if top else None,
+                   new(rows, top, dtype=f, device=device) if top else None)
 
     def _addresses(self, rows, top, dev):
         """Addresses of logp, rank, entropy, top_ids, top_logp (None where not asked for)."""
-        if self._f is not None and (self._n, self._top) == (rows, top) and self._f.device == dev:
-            f, i, t = self._f.data_ptr(), self._i.data_ptr(), self._t
-            none = t.get("logp", t) is None
-            return (None if none else f, None if none else i, f + 4 * rows,
-                    i + 4 * rows if top else None, f + 8 * rows if top else None)
         out = []
         for name, dt, n in (("logp", torch.float32, rows), ("rank", torch.int32, rows),
                             ("entropy", torch.float32, rows), ("top_ids", torch.int32, rows * top),
                             ("top_logp", torch.float32, rows * top)):
-            t = self._get(name)
+            t = getattr(self, name)
             if t is not None and (t.dtype != dt or t.numel() != n or t.device != dev
                                   or not t.is_contiguous()):
                 raise ValueError(f"{name} must hold {n} contiguous elements of {dt} on {dev}")
             out.append(None if t is None else t.data_ptr())
-        return tuple(out)
+        return out
 
 
 def spec_token_logprobs(logits, tokens, temperature=1.0, *, top=0, out=None, workspace=None,
