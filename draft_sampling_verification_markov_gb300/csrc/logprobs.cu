@@ -66,8 +66,9 @@ struct Shared {
   unsigned long long top[kMaxTop];    // this CTA's largest, in order; 0 = none
   Sums sums[kWarps];
   int count[kWarps];
-  Sums total;
+  Sums total;                         // of this part
   int total_count;
+  Sums row;                           // (maximum, log S) of a split row
   // radix selection
   int hist[256];
   uint32_t prefix;
@@ -93,22 +94,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   float d;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
   return d;
-}
-
-__device__ __forceinline__ Sums merge(Sums a, Sums b, float c) {
-  if (b.m > a.m) {
-    const Sums x = a;
-    a = b;
-    b = x;
-  }
-  if (b.m > -INFINITY && !(b.s == 0.0f)) {
-    const float d = (b.m - a.m) * c, f = fast_exp2(fmaxf(d, kLowest2));
-    a.s1 += f * (b.s1 + fmaxf(d, kLowest2) * b.s);
-    a.s += f * b.s;
-  } else {
-    a.s += b.s;  // 0, or the NaN of a part without a maximum
-  }
-  return a;
 }
 
 // The sums of the first n lanes (a power of two) in every one of them: against their largest
@@ -154,13 +139,26 @@ struct Row {
   template <int B>
   __device__ __forceinline__ void load_batch(uint4 (&q)[B], int jb, int end) const;
 
-  // Piece j, with -inf outside the row and past `end`.
-  __device__ __noinline__ uint4 load(int j, int end) const {
-    const uint32_t none = DT == SPEC_BF16 ? 0xff80ff80u : 0xff800000u;
-    if (j >= end) return make_uint4(none, none, none, none);
+  static constexpr uint32_t kNone = DT == SPEC_BF16 ? 0xff80ff80u : 0xff800000u;  // -inf
+
+  // Piece j, with -inf outside the row and past `end`. A row has at most two pieces that are
+  // partly outside; they go through a call of their own, so that the loads of whole ones stay in
+  // flight together.
+  __device__ __forceinline__ uint4 load(int j, int end) const {
+    uint4 q = make_uint4(kNone, kNone, kNone, kNone);
+    if (j < end) {
+      const int v = j * N - head;
+      if (v >= 0 && v + N <= V) q = ld_stream16(base + (size_t)j * 16);
+    }
+    return q;
+  }
+  __device__ __forceinline__ bool partial(int j, int end) const {
     const int v = j * N - head;
-    if (v >= 0 && v + N <= V) return ld_stream16(base + (size_t)j * 16);
-    uint32_t w[4] = {none, none, none, none};
+    return j < end && (v < 0 || v + N > V);
+  }
+  __device__ __noinline__ uint4 load_partial(int j) const {
+    uint32_t w[4] = {kNone, kNone, kNone, kNone};
+    const int v = j * N - head;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       if (v + i < 0 || v + i >= V) continue;
@@ -173,6 +171,10 @@ struct Row {
       }
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  // Either kind.
+  __device__ __forceinline__ uint4 load_any(int j, int end) const {
+    return partial(j, end) ? load_partial(j) : load(j, end);
   }
 };
 
@@ -188,6 +190,9 @@ __device__ __forceinline__ void Row<DT>::load_batch(uint4 (&q)[B], int jb, int e
   } else {
 #pragma unroll
     for (int b = 0; b < B; ++b) q[b] = load(j + b * kThreads, end);
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+      if (partial(j + b * kThreads, end)) q[b] = load_partial(j + b * kThreads);
   }
 }
 
@@ -325,15 +330,19 @@ __device__ __forceinline__ void take_batch(Shared& sh, const uint4 (&q)[kBatch],
     bm = fmaxf(bm, pm[b]);
   }
   if (TOP && bm >= bound) {
+    int hits = 0;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) hits += pm[b] >= bound;
+    int at = atomicAdd(&sh.n_pieces, hits);
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      if (pm[b] < bound) continue;
-      const int at = atomicAdd(&sh.n_pieces, 1);
+      if (!(pm[b] >= bound)) continue;
       if (at < kPieces) {
         sh.piece[at] = q[b];
         sh.piece_at[at] = j + b * kThreads;
         sh.piece_max[at] = pm[b];
       }
+      ++at;
     }
   }
   run.most = fmaxf(run.most, bm);
@@ -447,7 +456,7 @@ __device__ __noinline__ void select_radix(Shared& sh, const Row<DT>& row, int j0
     const uint32_t prefix = sh.prefix;
     for (int j = j0 + tid; j < j1; j += kThreads) {
       float x[N];
-      unpack<DT>(row.load(j, j1), x);
+      unpack<DT>(row.load_any(j, j1), x);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const uint32_t u = order_bits(x[i]);
@@ -476,7 +485,7 @@ __device__ __noinline__ void select_radix(Shared& sh, const Row<DT>& row, int j0
   const int need = all ? 0 : sh.need;
   for (int j = j0; j < j1; j += kThreads) {  // ascending, a piece a thread
     float x[N];
-    unpack<DT>(row.load(j + tid, j1), x);
+    unpack<DT>(row.load_any(j + tid, j1), x);
     uint32_t same = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -516,6 +525,19 @@ __device__ __noinline__ void select_radix(Shared& sh, const Row<DT>& row, int j0
 }
 
 // ------------------------------------------------------------------------------ kernel
+
+// A row's scalar outputs; returns (maximum, log S) for the alternatives.
+__device__ __forceinline__ Sums write_row(const LogprobArgs& a, int row, bool bad, float xt,
+                                          Sums sum, int larger) {
+  const bool finite = sum.s > 0.0f && sum.s < INFINITY && sum.m > -INFINITY;
+  const float ls = finite ? logf(sum.s) : NAN;
+  if (!finite) atomicOr(a.status, SPEC_DEV_NONFINITE);
+  if (a.tokens && bad) atomicOr(a.status, SPEC_DEV_BAD_TOKEN);
+  if (a.logp) a.logp[row] = bad ? NAN : (xt - sum.m) * a.scale - ls;
+  if (a.rank) a.rank[row] = bad ? 0 : larger + 1;
+  if (a.entropy) a.entropy[row] = ls - sum.s1 / sum.s * kLn2;
+  return {sum.m, ls, 0.0f};
+}
 
 template <int DT, bool TOP>
 __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const LogprobArgs a, int split) {
@@ -586,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Logprob
     acc = merge_lanes<kWarps>(has ? sh.sums[lane] : Sums{-INFINITY, 0.0f, 0.0f}, c);
     larger = __reduce_add_sync(kFull, has ? sh.count[lane] : 0);
     if (lane == 0) {
-      sh.total = acc;
+      sh.total = split > 1 ? acc : write_row(a, row, bad, xt, acc, larger);
       sh.total_count = larger;
     }
   }
@@ -603,11 +625,15 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Logprob
         const int j = sh.piece_at[i];
         float x[N];
         unpack<DT>(sh.piece[i], x);
+        int hits = 0;
+#pragma unroll
+        for (int q = 0; q < N; ++q) hits += x[q] >= cut;
+        int at = atomicAdd(&sh.n_keys, hits);
 #pragma unroll
         for (int q = 0; q < N; ++q)
           if (x[q] >= cut) {
-            const int at = atomicAdd(&sh.n_keys, 1);
             if (at < kKeys) sh.keys[at] = make_key(order_bits(x[q]), j * N - r.head + q);
+            ++at;
           }
       }
       __syncthreads();
@@ -628,28 +654,14 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Logprob
   // the cluster's parts, merged by its first CTA
   if (split > 1) cluster.sync(); else __syncthreads();
   if (part == 0) {
-    Sums sum = sh.total;
-    int count = sh.total_count;
-    if (tid < 32) {  // every lane the same
-      for (int p = 1; p < split; ++p) {
-        const Shared* other = cluster.map_shared_rank(&sh, p);
-        sum = merge(sum, other->total, c);
-        count += other->total_count;
-      }
-      const bool finite = sum.s > 0.0f && sum.s < INFINITY && sum.m > -INFINITY;
-      const float ls = finite ? logf(sum.s) : NAN;
-      if (lane == 0) {
-        if (!finite) atomicOr(a.status, SPEC_DEV_NONFINITE);
-        if (a.tokens && bad) atomicOr(a.status, SPEC_DEV_BAD_TOKEN);
-        if (a.logp) a.logp[row] = bad ? NAN : (xt - sum.m) * a.scale - ls;
-        if (a.rank) a.rank[row] = bad ? 0 : count + 1;
-        if (a.entropy) a.entropy[row] = ls - sum.s1 / sum.s * kLn2;
-        sh.total = {sum.m, ls, 0.0f};  // for the alternatives below
-      }
+    if (split > 1 && tid < kMaxTop) {  // lane p: part p
+      const Shared* other = cluster.map_shared_rank(&sh, lane < split ? lane : 0);
+      Sums sum = lane < split ? other->total : Sums{-INFINITY, 0.0f, 0.0f};
+      const int count = __reduce_add_sync(kFull, lane < split ? other->total_count : 0);
+      sum = merge_lanes<kMaxSplit>(sum, c);
+      if (lane == 0) sh.row = write_row(a, row, bad, xt, sum, count);
     }
     if (TOP) {
-      __syncthreads();
-      const float m = sh.total.m, ls = sh.total.s;
       // place of each part's entry: its own place in its part's list, plus the larger entries of
       // every other (descending, zeros at the end)
       if (split > 1) {
@@ -657,6 +669,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Logprob
           sh.keys[i] = *cluster.map_shared_rank(&sh.top[i % kMaxTop], i / kMaxTop);
         __syncthreads();
       }
+      const float m = split > 1 ? sh.row.m : sh.total.m, ls = split > 1 ? sh.row.s : sh.total.s;
       const unsigned long long* lists = split > 1 ? sh.keys : sh.top;
       const size_t at = (size_t)row * a.top;
       for (int i0 = 0; i0 < split * kMaxTop; i0 += kThreads) {
