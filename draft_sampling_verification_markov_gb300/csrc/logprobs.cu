@@ -539,170 +539,232 @@ __device__ __forceinline__ Sums write_row(const LogprobArgs& a, int row, bool ba
   return {sum.m, ls, 0.0f};
 }
 
-template <int DT, bool TOP>
-__global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const LogprobArgs a, int split) {
+// The a.top largest elements of pieces [j0, j1) as keys, unordered, sh.n_keys of them or a few
+// more: those of the listed pieces that reach the list's bound, or by radix selection.
+template <int DT>
+__device__ __forceinline__ void collect_keys(Shared& sh, const Row<DT>& r, int j0, int j1,
+                                             float bound, int k) {
   constexpr int N = Row<DT>::N;
-  __shared__ Shared sh;
-  cg::cluster_group cluster = cg::this_cluster();
-  const int row = blockIdx.x / split, part = blockIdx.x % split;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int t = a.tokens ? a.tokens[row] : 0;
-  if (a.tokens && t == -1) return;  // the whole cluster
-  const bool bad = t < 0 || t >= a.V;
-  const size_t off = (size_t)row * a.ld;
-  const Row<DT> r(a.x, off, a.V);
-  const int np = r.pieces(), per = (np + split - 1) / split;
-  const int j0 = part * per, j1 = min(np, j0 + per);
-  const float c = a.scale * kLog2e;
-
-  uint4 cur[kBatch], nxt[kBatch];
-  r.template load_batch<kBatch>(cur, j0, j1);
-  r.template load_batch<kBatch>(nxt, j0 + kBatch * kThreads, j1);
-  const float xt = bad || !a.tokens ? INFINITY : ld_elem<DT>(a.x, off + t);
-
-  float bound = INFINITY;
-  if (TOP && tid == 0) {
-    sh.n_pieces = 0;
-    sh.n_keys = 0;
-  }
-  if (TOP) {
-    float first = -INFINITY;
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b)
-      first = max3f(first, piece_max<DT>(cur[b]), piece_max<DT>(nxt[b]));
-    // nothing of -inf has a place
-    bound = fmaxf(bound_of(sh, first, a.top), -3.402823466e38f);
-  }
-  RunningSums run;
-  run.start();
-  int larger = 0;
-  constexpr int kStep = kBatch * kThreads;
-  const bool tame = c < kFastScale && c > kFastLeast;
-  // the bound is renewed from the list whenever the number of batches seen has doubled: a list
-  // then grows by little more than k pieces between two renewals, however long the row
-  int renew = j0 + 4 * kStep;
-  for (int jb = j0; jb < j1; jb += 2 * kStep) {
-    take_batch<DT, TOP>(sh, cur, jb + tid, bound, xt, c, tame, run, larger);
-    r.template load_batch<kBatch>(cur, jb + 2 * kStep, j1);
-    if (jb + kStep >= j1) break;
-    take_batch<DT, TOP>(sh, nxt, jb + kStep + tid, bound, xt, c, tame, run, larger);
-    r.template load_batch<kBatch>(nxt, jb + 3 * kStep, j1);
-    if (TOP && jb + 2 * kStep == renew && renew < j1) {
-      renew += renew - j0;
-      bound = bound_of_list(sh, bound, a.top);
-    }
-  }
-  Sums acc = run.sums(c, tame);
-
-  // this CTA's sums: lanes against their warp's maximum, then warps against the CTA's
-  acc = merge_lanes<32>(acc, c);
-  larger = __reduce_add_sync(kFull, larger);
-  if (lane == 0) {
-    sh.sums[warp] = acc;
-    sh.count[warp] = larger;
-  }
-  if (TOP && tid < kMaxTop) sh.top[tid] = 0;
-  __syncthreads();  // every push, too
-  if (warp == kWarps - 1) {
-    const bool has = lane < kWarps;
-    acc = merge_lanes<kWarps>(has ? sh.sums[lane] : Sums{-INFINITY, 0.0f, 0.0f}, c);
-    larger = __reduce_add_sync(kFull, has ? sh.count[lane] : 0);
-    if (lane == 0) {
-      sh.total = split > 1 ? acc : write_row(a, row, bad, xt, acc, larger);
-      sh.total_count = larger;
-    }
-  }
-  if (TOP) {
-    const int n = sh.n_pieces;
-    bool fits = n <= kPieces;
-    if (fits) {
-      float local = -INFINITY;
-      for (int i = tid; i < n; i += kThreads) local = fmaxf(local, sh.piece_max[i]);
-      // fewer listed pieces than places leave the bound they were listed by
-      const float cut = fmaxf(bound_of(sh, local, a.top), bound);
-      for (int i = tid; i < n; i += kThreads) {
-        if (sh.piece_max[i] < cut) continue;
-        const int j = sh.piece_at[i];
-        float x[N];
-        unpack<DT>(sh.piece[i], x);
-        int hits = 0;
-#pragma unroll
-        for (int q = 0; q < N; ++q) hits += x[q] >= cut;
-        int at = atomicAdd(&sh.n_keys, hits);
-#pragma unroll
-        for (int q = 0; q < N; ++q)
-          if (x[q] >= cut) {
-            if (at < kKeys) sh.keys[at] = make_key(order_bits(x[q]), j * N - r.head + q);
-            ++at;
-          }
-      }
-      __syncthreads();
-      fits = sh.n_keys <= kKeys;
+  const int tid = threadIdx.x, n = sh.n_pieces;
+  bool fits = n <= kPieces;
+  if (fits) {
+    float local = -INFINITY;
+    for (int i = tid; i < n; i += kThreads) local = fmaxf(local, sh.piece_max[i]);
+    // fewer listed pieces than places leave the bound they were listed by
+    const float cut = fmaxf(bound_of(sh, local, k), bound);
+    for (int e = tid; e < n * N; e += kThreads) {  // an element a thread
+      const int i = e / N, q = e % N;
+      if (sh.piece_max[i] < cut) continue;
+      float x;
+      if constexpr (DT == SPEC_BF16)
+        x = bf16_to_f32(reinterpret_cast<const uint16_t*>(&sh.piece[i])[q]);
+      else
+        x = reinterpret_cast<const float*>(&sh.piece[i])[q];
+      if (!(x >= cut)) continue;
+      const int at = atomicAdd(&sh.n_keys, 1);
+      if (at < kKeys) sh.keys[at] = make_key(order_bits(x), (int)sh.piece_at[i] * N - r.head + q);
     }
     __syncthreads();
-    if (!fits) select_radix<DT>(sh, r, j0, j1, a.top);
-    const int nk = sh.n_keys;
-    for (int i = tid; i < nk; i += kThreads) {
-      const unsigned long long key = sh.keys[i];
-      int place = 0;
-#pragma unroll 8
-      for (int q = 0; q < nk; ++q) place += sh.keys[q] > key;
-      if (place < a.top) sh.top[place] = key;
-    }
+    fits = sh.n_keys <= kKeys;
   }
+  if (!fits) {
+    __syncthreads();
+    select_radix<DT>(sh, r, j0, j1, k);
+  }
+}
 
-  // the cluster's parts, merged by its first CTA
-  if (split > 1) cluster.sync(); else __syncthreads();
-  if (part == 0) {
-    if (split > 1 && tid < kMaxTop) {  // lane p: part p
-      const Shared* other = cluster.map_shared_rank(&sh, lane < split ? lane : 0);
-      Sums sum = lane < split ? other->total : Sums{-INFINITY, 0.0f, 0.0f};
-      const int count = __reduce_add_sync(kFull, lane < split ? other->total_count : 0);
-      sum = merge_lanes<kMaxSplit>(sum, c);
-      if (lane == 0) sh.row = write_row(a, row, bad, xt, sum, count);
-    }
-    if (TOP) {
-      // place of each part's entry: its own place in its part's list, plus the larger entries of
-      // every other (descending, zeros at the end)
-      if (split > 1) {
-        for (int i = tid; i < split * kMaxTop; i += kThreads)
-          sh.keys[i] = *cluster.map_shared_rank(&sh.top[i % kMaxTop], i / kMaxTop);
-        __syncthreads();
-      }
-      const float m = split > 1 ? sh.row.m : sh.total.m, ls = split > 1 ? sh.row.s : sh.total.s;
-      const unsigned long long* lists = split > 1 ? sh.keys : sh.top;
-      const size_t at = (size_t)row * a.top;
-      for (int i0 = 0; i0 < split * kMaxTop; i0 += kThreads) {
-        const int i = i0 + tid, p = i / kMaxTop, e = i % kMaxTop;
-        const unsigned long long key = i < split * kMaxTop ? lists[i] : 0;
-        if (!key) continue;
-        int place = e;
-#pragma unroll
-        for (int o = 0; o < kMaxSplit; ++o) {
-          if (o >= split || o == p) continue;
-          const unsigned long long* list = lists + o * kMaxTop;
-          int n = 0;
-#pragma unroll
-          for (int w = kMaxTop / 2; w > 0; w /= 2) n += list[n + w - 1] > key ? w : 0;
-          place += n + (list[n] > key ? 1 : 0);
-        }
-        if (place >= a.top) continue;
-        const float x = order_value((uint32_t)(key >> 32));
-        if (a.top_ids) a.top_ids[at + place] = (int)(0xffffffffu - (uint32_t)key);
-        if (a.top_logp) a.top_logp[at + place] = (x - m) * a.scale - ls;
-      }
-      // places that no logit has
-      if (warp == 0) {
-        int have = 0;
-        for (int o = 0; o < split; ++o) have += __popc(__ballot_sync(kFull, lists[o * kMaxTop + lane] != 0));
-        if (lane < a.top && lane >= have) {
-          if (a.top_ids) a.top_ids[at + lane] = -1;
-          if (a.top_logp) a.top_logp[at + lane] = -INFINITY;
-        }
-      }
-    }
+// Place of a key among the n of sh.keys.
+__device__ __forceinline__ int place_of(const Shared& sh, unsigned long long key, int n) {
+  int place = 0;
+#pragma unroll 8
+  for (int q = 0; q < n; ++q) place += sh.keys[q] > key;
+  return place;
+}
+
+__device__ __forceinline__ void write_top(const LogprobArgs& a, int row, int place,
+                                          unsigned long long key, Sums ms) {
+  const size_t at = (size_t)row * a.top + place;
+  const float x = order_value((uint32_t)(key >> 32));
+  if (a.top_ids) a.top_ids[at] = key ? (int)(0xffffffffu - (uint32_t)key) : -1;
+  if (a.top_logp) a.top_logp[at] = key ? (x - ms.m) * a.scale - ms.s : -INFINITY;
+}
+
+// SPLIT: a cluster takes one row, each CTA a part of it. Else a CTA takes rows in turn and has the
+// first batches of the next one on their way before it finishes a row: all CTAs of an SM start
+// together and would leave the memory idle together (10 of 56 thousand cycles a row).
+template <int DT, bool TOP, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const LogprobArgs a,
+                                                                   const int parts) {
+  __shared__ Shared sh;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int split = SPLIT ? parts : 1;
+  const int part = SPLIT ? blockIdx.x % split : 0;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const float c = a.scale * kLog2e;
+  const bool tame = c < kFastScale && c > kFastLeast;
+  constexpr int kStep = kBatch * kThreads;
+
+  int row = SPLIT ? blockIdx.x / split : blockIdx.x;
+  Row<DT> r(a.x, (size_t)row * a.ld, a.V);
+  // the first logits are on their way while the token is read
+  uint4 cur[kBatch], nxt[kBatch];
+  {
+    const int np = r.pieces(), per = (np + split - 1) / split;
+    r.template load_batch<kBatch>(cur, part * per, min(np, part * per + per));
+    r.template load_batch<kBatch>(nxt, part * per + kStep, min(np, part * per + per));
   }
-  if (split > 1) cluster.sync();
+  int t = a.tokens ? a.tokens[row] : 0;
+  while (true) {
+    const int next = SPLIT ? a.rows : row + gridDim.x;
+    const int t_next = next < a.rows && a.tokens ? a.tokens[next] : 0;
+    const bool skip = a.tokens && t == -1;
+    if (SPLIT && skip) return;  // the whole cluster
+    const int np = r.pieces(), per = (np + split - 1) / split;
+    const int j0 = part * per, j1 = min(np, j0 + per);
+    if (!skip) {
+      const bool bad = t < 0 || t >= a.V;
+      const float xt = bad || !a.tokens ? INFINITY : ld_elem<DT>(a.x, (size_t)row * a.ld + t);
+      float bound = INFINITY;
+      if (TOP) {
+        if (tid == 0) {
+          sh.n_pieces = 0;
+          sh.n_keys = 0;
+        }
+        float first = -INFINITY;
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+          first = max3f(first, piece_max<DT>(cur[b]), piece_max<DT>(nxt[b]));
+        // nothing of -inf has a place
+        bound = fmaxf(bound_of(sh, first, a.top), -3.402823466e38f);
+      }
+      RunningSums run;
+      run.start();
+      int larger = 0;
+      // the bound is renewed from the list whenever the number of batches seen has doubled: a
+      // list then grows by little more than k pieces between two renewals, however long the row
+      int renew = j0 + 4 * kStep;
+      for (int jb = j0; jb < j1; jb += 2 * kStep) {
+        take_batch<DT, TOP>(sh, cur, jb + tid, bound, xt, c, tame, run, larger);
+        r.template load_batch<kBatch>(cur, jb + 2 * kStep, j1);
+        if (jb + kStep >= j1) break;
+        take_batch<DT, TOP>(sh, nxt, jb + kStep + tid, bound, xt, c, tame, run, larger);
+        r.template load_batch<kBatch>(nxt, jb + 3 * kStep, j1);
+        if (TOP && jb + 2 * kStep == renew && renew < j1) {
+          renew += renew - j0;
+          bound = bound_of_list(sh, bound, a.top);
+        }
+      }
+      const Row<DT> done = r;
+      if (next < a.rows) {
+        r = Row<DT>(a.x, (size_t)next * a.ld, a.V);
+        r.template load_batch<kBatch>(cur, 0, r.pieces());
+        r.template load_batch<kBatch>(nxt, kStep, r.pieces());
+      }
+
+      // this CTA's sums: lanes against their warp's maximum, then warps against the CTA's
+      Sums acc = merge_lanes<32>(run.sums(c, tame), c);
+      larger = __reduce_add_sync(kFull, larger);
+      if (lane == 0) {
+        sh.sums[warp] = acc;
+        sh.count[warp] = larger;
+      }
+      if (TOP && SPLIT && tid < kMaxTop) sh.top[tid] = 0;
+      __syncthreads();  // every push, too
+      if (warp == kWarps - 1) {
+        const bool has = lane < kWarps;
+        acc = merge_lanes<kWarps>(has ? sh.sums[lane] : Sums{-INFINITY, 0.0f, 0.0f}, c);
+        larger = __reduce_add_sync(kFull, has ? sh.count[lane] : 0);
+        if (lane == 0) {
+          sh.total = SPLIT ? acc : write_row(a, row, bad, xt, acc, larger);
+          sh.total_count = larger;
+        }
+      }
+      if (TOP) {
+        collect_keys<DT>(sh, done, j0, j1, bound, a.top);
+        const int nk = sh.n_keys;
+        for (int i = tid; i < nk; i += kThreads) {
+          const unsigned long long key = sh.keys[i];
+          const int place = place_of(sh, key, nk);
+          if (place >= a.top) continue;
+          if (SPLIT)
+            sh.top[place] = key;
+          else
+            write_top(a, row, place, key, sh.total);
+        }
+        // places that no logit has
+        if (!SPLIT && tid < a.top && tid >= nk) write_top(a, row, tid, 0, sh.total);
+      }
+
+      if (SPLIT) {  // the cluster's parts, merged by its first CTA
+        cluster.sync();
+        if (part == 0) {
+          if (warp == kWarps - 1) {  // lane p: part p
+            const bool has = lane < split;
+            const Shared* other = cluster.map_shared_rank(&sh, has ? lane : 0);
+            Sums sum = has ? other->total : Sums{-INFINITY, 0.0f, 0.0f};
+            const int count = __reduce_add_sync(kFull, has ? other->total_count : 0);
+            sum = merge_lanes<kMaxSplit>(sum, c);
+            if (lane == 0) sh.row = write_row(a, row, bad, xt, sum, count);
+          }
+          if (TOP) {
+            for (int i = tid; i < split * kMaxTop; i += kThreads)
+              sh.keys[i] = *cluster.map_shared_rank(&sh.top[i % kMaxTop], i / kMaxTop);
+            __syncthreads();
+            // place of each part's entry: its own place in its part's list, plus the larger
+            // entries of every other (descending, zeros at the end)
+            for (int i = tid; i < split * kMaxTop; i += kThreads) {
+              const unsigned long long key = sh.keys[i];
+              if (!key) continue;
+              int place = i % kMaxTop;
+#pragma unroll
+              for (int o = 0; o < kMaxSplit; ++o) {
+                if (o >= split || o == i / kMaxTop) continue;
+                const unsigned long long* list = sh.keys + o * kMaxTop;
+                int n = 0;
+#pragma unroll
+                for (int w = kMaxTop / 2; w > 0; w /= 2) n += list[n + w - 1] > key ? w : 0;
+                place += n + (list[n] > key ? 1 : 0);
+              }
+              if (place < a.top) write_top(a, row, place, key, sh.row);
+            }
+            if (warp == 0) {  // places that no logit has
+              int have = 0;
+              for (int o = 0; o < split; ++o)
+                have += __popc(__ballot_sync(kFull, sh.keys[o * kMaxTop + lane] != 0));
+              if (lane < a.top && lane >= have) write_top(a, row, lane, 0, sh.row);
+            }
+          }
+        }
+        cluster.sync();  // no part leaves before it has been read
+        return;
+      }
+      if (next < a.rows) __syncthreads();  // the next row reuses the shared state
+    } else if (next < a.rows) {
+      r = Row<DT>(a.x, (size_t)next * a.ld, a.V);
+      r.template load_batch<kBatch>(cur, 0, r.pieces());
+      r.template load_batch<kBatch>(nxt, kStep, r.pieces());
+    }
+    if (next >= a.rows) return;
+    row = next;
+    t = t_next;
+  }
+}
+
+template <int DT, bool TOP>
+cudaError_t launch_t(const LogprobArgs& a, int split, cudaStream_t s) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = split;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  const int most = kCtas * num_sms();
+  cfg.gridDim = dim3((unsigned)(split > 1 ? a.rows * split : (a.rows < most ? a.rows : most)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = split > 1 ? 1 : 0;
+  return split > 1 ? cudaLaunchKernelEx(&cfg, logprobs_kernel<DT, TOP, true>, a, split)
+                   : cudaLaunchKernelEx(&cfg, logprobs_kernel<DT, TOP, false>, a, split);
 }
 
 }  // namespace
@@ -717,21 +779,9 @@ cudaError_t launch_token_logprobs(const LogprobArgs& a, int dt, cudaStream_t s) 
   int split = 1;
   while (split < kMaxSplit && (long long)a.rows * split * 2 <= 2 * num_sms() && a.V >= 2 * split * batch)
     split *= 2;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = split;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.rows * split);
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
   if (dt == SPEC_BF16)
-    return a.top ? cudaLaunchKernelEx(&cfg, logprobs_kernel<SPEC_BF16, true>, a, split)
-                 : cudaLaunchKernelEx(&cfg, logprobs_kernel<SPEC_BF16, false>, a, split);
-  return a.top ? cudaLaunchKernelEx(&cfg, logprobs_kernel<SPEC_F32, true>, a, split)
-               : cudaLaunchKernelEx(&cfg, logprobs_kernel<SPEC_F32, false>, a, split);
+    return a.top ? launch_t<SPEC_BF16, true>(a, split, s) : launch_t<SPEC_BF16, false>(a, split, s);
+  return a.top ? launch_t<SPEC_F32, true>(a, split, s) : launch_t<SPEC_F32, false>(a, split, s);
 }
 
 }  // namespace spec

@@ -510,8 +510,9 @@ int spec_mx_logits(const uint8_t* a_codes, const uint8_t* a_scales, int a_fmt,
  *   place among them: missing places get id -1 and log-probability -inf.
  * Arguments:
  *   logits   [rows, V], row stride ld >= V elements; dtype SPEC_F32 or SPEC_BF16.
- *   tokens   [rows] int32, or NULL (no logp, no rank). A row whose token is -1 is neither read
- *            nor written: the padding of out_tokens of the verify calls. Any other id outside
+ *   tokens   [rows] int32, or NULL (no logp, no rank). The outputs of a row whose token is -1
+ *            (the padding of out_tokens of the verify calls) stay as they were and its logits do
+ *            not matter. Any other id outside
  *            [0, V) sets SPEC_DEV_BAD_TOKEN; its logp is NaN and its rank 0.
  *   top      0 .. SPEC_LOGPROBS_MAX_TOP.
  *   logp, rank, entropy [rows], top_ids, top_logp [rows, top]: each optional (NULL to skip).
