@@ -889,6 +889,21 @@ static bool elem_aligned(const void* p, int dtype) {
   return (reinterpret_cast<uintptr_t>(p) & (esize(dtype) - 1)) == 0;
 }
 
+// Whether a kernel may write p's rows while it reads q's: the same rows, or rows of one stride
+// that do not meet, or arrays apart.
+static bool rows_apart(const void* p, long long ldp, const void* q, long long ldq, int rows, int K,
+                       int dtype) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  const uintptr_t es = esize(dtype);
+  const uintptr_t na = ((uintptr_t)(rows - 1) * ldp + K) * es;
+  const uintptr_t nb = ((uintptr_t)(rows - 1) * ldq + K) * es;
+  if (a + na <= b || b + nb <= a) return true;
+  if (rows == 1) return a == b;
+  if (ldp != ldq) return false;
+  const uintptr_t d = (a > b ? a - b : b - a) / es % (uintptr_t)ldp;
+  return a == b || (d >= (uintptr_t)K && (uintptr_t)ldp - d >= (uintptr_t)K);
+}
+
 static bool status_ws_ok(void* ws) {
   return ws && (reinterpret_cast<uintptr_t>(ws) % kAlign) == 0;
 }
@@ -949,8 +964,9 @@ int spec_rmsnorm_mx(const void* x, long long ldx, const void* residual, long lon
   if (residual && (!residual_out || !elem_aligned(residual, dtype) ||
                    !elem_aligned(residual_out, dtype)))
     return SPEC_ERR_INVALID_ARG;
-  // written in place only where it has the stride of what it replaces
-  if (residual && ((residual_out == x && ldo != ldx) || (residual_out == residual && ldo != ldr)))
+  // written in place of x or residual, or clear of both
+  if (residual && (!rows_apart(residual_out, ldo, x, ldx, rows, K, dtype) ||
+                   !rows_apart(residual_out, ldo, residual, ldr, rows, K, dtype)))
     return SPEC_ERR_INVALID_ARG;
   launch_rmsnorm_mx(x, ldx, residual, ldr, dtype, weight, w_dtype, eps, rows, K, residual_out, ldo,
                     fmt, codes, scales, static_cast<uint32_t*>(ws),

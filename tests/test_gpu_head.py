@@ -193,6 +193,19 @@ def test_norm_non_finite_row(bad):
     assert status(ws) == S.SPEC_DEV_NONFINITE
 
 
+def test_norm_between_rows_of_one_buffer():
+    """x, residual and the stored sum as column ranges of one wide buffer."""
+    wide = randn(7, 3, 264, seed=12, dtype=torch.bfloat16).to(DEV)
+    x, r, o = wide[:, 0], wide[:, 1], wide[:, 2]
+    w = randn(264, seed=6).to(DEV)
+    h0, q0 = S.spec_rmsnorm_mx(x.clone(), w, residual=r.clone())
+    _, q = S.spec_rmsnorm_mx(x, w, residual=r, residual_out=o)
+    assert torch.equal(o, h0) and torch.equal(q.codes, q0.codes)
+    shifted = wide.as_strided((6, 264), (792, 1), 8)  # eight elements into x's columns
+    with pytest.raises(S.SpecError):
+        S.spec_rmsnorm_mx(x[:6], w, residual=r[:6], residual_out=shifted)
+
+
 def test_norm_zero_row():
     x = torch.zeros(2, 256, device=DEV)
     _, q = S.spec_rmsnorm_mx(x, torch.ones(256, device=DEV), 1e-6)
@@ -297,6 +310,46 @@ def test_logits_refuses_mismatched_operands():
         S.spec_mx_logits(a, w, out=torch.zeros(4, 9, device=DEV))
     with pytest.raises(TypeError):
         S.spec_mx_logits(a, w, dtype=torch.float16)
+
+
+def test_arrays_beyond_two_to_the_31_elements():
+    """Logits of 17000 rows over 129280 tokens, quantised and read back: last rows against the
+    definitions."""
+    M, V, K = 17000, 129280, 128
+    a, a64 = random_mx(M, K, S.SPEC_MX_E4M3, 1)
+    w, w64 = random_mx(V, K, S.SPEC_MX_E2M1, 2)
+    ws = S.Workspace(device=DEV)
+    out = S.spec_mx_logits(a, w, workspace=ws)
+    rows = [0, 8191, M - 130, M - 1]
+    check_logits(out[rows], a64[rows], w64, K, torch.bfloat16)
+    q = S.spec_mx_quantize(out, S.SPEC_MX_E4M3, workspace=ws)
+    del a, w
+    x = f64(out[M - 3:])
+    codes, s = ref.quantize(np.concatenate([np.zeros((M % 128 - 3, V)), x]), S.SPEC_MX_E4M3)
+    np.testing.assert_array_equal(q.codes[M - 3:].cpu().numpy(), codes[-3:])
+    y = S.spec_mx_dequantize(q, workspace=ws)
+    np.testing.assert_array_equal(f64(y[M - 3:]),
+                                  ref.dequantize(codes, s, S.SPEC_MX_E4M3, V)[-3:])
+    tok = torch.full((M,), -1, dtype=torch.int32)
+    tok[[5, M - 1]] = torch.tensor([7, V - 1], dtype=torch.int32)
+    r = S.spec_token_logprobs(out, tok.to(DEV), 1.0, top=3, workspace=ws)
+    for row in (5, M - 1):
+        want = ref.token_logprobs(out[row:row + 1].cpu().double(), tok[row:row + 1], 1.0, 3)
+        assert torch.equal(r.top_ids[row].cpu().long(), want["top_ids"][0])
+        assert r.rank[row].item() == want["rank"].item()
+        z = out[row].float()
+        tol = ref.logp_tol(V, float(z.max() - z.min()))
+        assert abs(r.logp[row].item() - want["logp"].item()) <= tol
+    h, n = S.spec_rmsnorm_mx(out, torch.ones(V, device=DEV), residual=y, workspace=ws)
+    last = h[M - 1:].double().cpu().numpy()
+    want = last / np.sqrt((last ** 2).mean() + 1e-6)
+    tile = n.scales[-1:].cpu()
+    keep = (M - 1) % 128
+    s1 = np.zeros((1,) + tuple(tile.shape[1:]), np.uint8)
+    s1[0, :, 0, 0] = tile[0, :, keep % 32, keep // 32]
+    got = ref.dequantize(n.codes[M - 1:].cpu(), s1, S.SPEC_MX_E4M3, V)
+    ref.check_rounded(got, s1, S.SPEC_MX_E4M3, want, ref.norm_rel(V))
+    assert status(ws) == 0
 
 
 def test_head_chain_on_a_stream_and_in_a_graph():

@@ -72,7 +72,11 @@ NORM = dict(x=OK_PTR, ldx=64, r=OK_PTR, ldr=64, dt=1, w=OK_PTR, wdt=1, eps=1e-6,
     (dict(eps=-1.0), -1), (dict(eps=float("nan")), -1), (dict(eps=float("inf")), -1),
     (dict(x=None), -1), (dict(w=None), -1), (dict(ro=None), -1), (dict(ro=ODD), -1),
     (dict(codes=vp(0x1010)), -1), (dict(wn=0), -3), (dict(ws=None), -1),
-    (dict(ro=OK_PTR, ldo=128), -1), (dict(rows=0, x=None, ro=None), 0)])
+    (dict(ro=OK_PTR, ldo=128), -1), (dict(ro=vp(0x1010)), -1), (dict(ro=vp(0x1000 + 2 * 64)), -1),
+    (dict(ro=vp(0x1000 + 2 * 32), ldx=128, ldr=128, ldo=128), -1),
+    (dict(ro=vp(0x1000 + 2 * 4 * 64 - 2)), -1),
+    (dict(r=vp(0x8000), ro=vp(0x8000 + 2 * 100), ldr=128, ldo=128), -1),
+    (dict(rows=0, x=None, ro=None), 0)])
 def test_norm_refusals(L, at, rc):
     assert L.spec_rmsnorm_mx(*changed(NORM, **at)) == rc
 
