@@ -159,8 +159,9 @@ class Workspace:
     """Caller-owned device workspace (a torch uint8 buffer) for the library's scratch."""
 
     def __init__(self, nbytes: int = 0, device=None):
-        self.device = torch.device(device) if device is not None else torch.device(
-            "cuda", torch.cuda.current_device())
+        self.device = torch.device(device) if device is not None else torch.device("cuda")
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
         self.buf = None
         self.nbytes = 0
         if nbytes:
@@ -617,8 +618,8 @@ class MXTensor:
         if (scales.dtype != torch.uint8 or scales.shape != (tiles, G, 32, 4, 4)
                 or not scales.is_contiguous()):
             raise ValueError(f"scales must be contiguous uint8 {(tiles, G, 32, 4, 4)}")
-        if scales.device != codes.device:
-            raise ValueError("codes and scales must be on one device")
+        if scales.device != codes.device or not codes.is_cuda:
+            raise ValueError("codes and scales must be on one CUDA device")
         self.rows, self.K, self.fmt, self.device = rows, K, fmt, codes.device
         self._buf, self._codes, self._scales = None, codes, scales
         self._cp, self._sp = codes.data_ptr(), scales.data_ptr()
@@ -628,12 +629,14 @@ class MXTensor:
         """An uninitialised [rows, K] matrix for a call to write."""
         width, tiles, G = _mx_sizes(rows, K, fmt)
         q = cls.__new__(cls)
-        q._buf = buf = torch.empty(rows * width + tiles * G * 512, dtype=torch.uint8,
-                                   device=device)
+        n = rows * width
+        q._buf = buf = torch.empty(n + tiles * G * 512, dtype=torch.uint8, device=device)
+        if not buf.is_cuda:
+            raise ValueError("libspecmarkov takes device tensors")
         q.rows, q.K, q.fmt, q.device = rows, K, fmt, buf.device
         q._codes = q._scales = None
-        q._cp = buf.data_ptr()
-        q._sp = q._cp + rows * width
+        q._cp = at = buf.data_ptr()
+        q._sp = at + n
         return q
 
     @property
@@ -683,10 +686,9 @@ def _rows(t, name):
     return t.data_ptr(), rows, width, ld
 
 
-def _same_device(dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be on {dev}")
+def _on(dev, t, name):
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
 
 
 def _dtype_code(dtype):
@@ -696,11 +698,12 @@ def _dtype_code(dtype):
     return code
 
 
+_entry = {}  # entry points by name, looked up once
+
+
 def _launch(name, dev, workspace, stream, *args):
     """Call entry point `name` with args, the status workspace and the stream. The operands'
     device is current meanwhile and its current stream is the default."""
-    if dev.type != "cuda":
-        raise ValueError("libspecmarkov takes device tensors")
     i = dev.index
     ws = workspace or _default_ws.get(i) or default_workspace(dev)
     if ws.device.index != i:
@@ -710,8 +713,10 @@ def _launch(name, dev, workspace, stream, *args):
             return _launch(name, dev, ws, stream, *args)
     if ws.buf is None:
         ws.reserve(256, stream)
-    st = _raw_stream(i) if stream is None else stream.cuda_stream
-    rc = getattr(_lib or lib(), name)(*args, ws._addr, ws.nbytes, st)
+    fn = _entry.get(name)
+    if fn is None:
+        fn = _entry[name] = getattr(lib(), name)
+    rc = fn(*args, ws._addr, ws.nbytes, _raw_stream(i) if stream is None else stream.cuda_stream)
     if rc != SPEC_OK:
         raise SpecError(name, rc)
 
@@ -742,14 +747,17 @@ def spec_mx_dequantize(q, *, dtype=torch.bfloat16, out=None, workspace=None, str
     """The numbers that the MXTensor q stands for, [rows, K] of `dtype` (bf16 or fp32)."""
     rows, K, dev = q.rows, q.K, q.device
     if out is None:
+        dt = _dtype_code(dtype)
         out = torch.empty(rows, K, dtype=dtype, device=dev)
-    ptr, orows, width, ld = _rows(out, "out")
-    if orows != rows or width != K:
-        raise ValueError("out must have q's rows and width")
-    if out.device != dev:
-        raise ValueError(f"out must be on {dev}")
-    _launch("spec_mx_dequantize", dev, workspace, stream, q._cp, q._sp, q.fmt, rows, K, ptr,
-            _dtype_code(out.dtype), ld)
+        ptr, ld = out.data_ptr(), K
+    else:
+        dt = _dtype_code(out.dtype)
+        ptr, orows, width, ld = _rows(out, "out")
+        if orows != rows or width != K:
+            raise ValueError("out must have q's rows and width")
+        _on(dev, out, "out")
+    _launch("spec_mx_dequantize", dev, workspace, stream, q._cp, q._sp, q.fmt, rows, K, ptr, dt,
+            ld)
     return out
 
 
@@ -770,16 +778,19 @@ def spec_rmsnorm_mx(x, weight, eps=1e-6, *, residual=None, residual_out=None, fm
         if residual.shape != x.shape or residual.dtype != x.dtype:
             raise ValueError("residual must have x's shape and dtype")
         rp, _, _, ldr = _rows(residual, "residual")
+        _on(dev, residual, "residual")
         if residual_out is None:
             h = torch.empty(x.shape, dtype=x.dtype, device=dev)
+            op = h.data_ptr()
         else:
             h = residual_out
             if h.shape != x.shape or h.dtype != x.dtype:
                 raise ValueError("residual_out must have x's shape and dtype")
-        op, _, _, ldo = _rows(h, "residual_out")
+            op, _, _, ldo = _rows(h, "residual_out")
+            _on(dev, h, "residual_out")
     elif residual_out is not None:
         raise ValueError("residual_out is an output of the form with a residual")
-    _same_device(dev, weight=weight, residual=residual, residual_out=h)
+    _on(dev, weight, "weight")
     out = _mx_out(out, rows, K, fmt, dev)
     _launch("spec_rmsnorm_mx", dev, workspace, stream, ptr, ldx, rp, ldr, dt, weight.data_ptr(),
             _dtype_code(weight.dtype), eps, rows, K, op, ldo, fmt, out._cp, out._sp)
@@ -793,14 +804,19 @@ def spec_mx_logits(a, w, *, dtype=torch.bfloat16, out=None, workspace=None, stre
     M, V, K, dev = a.rows, w.rows, a.K, a.device
     if K != w.K:
         raise ValueError(f"a has rows of {K} elements, w of {w.K}")
+    _on(dev, w, "w")
     if out is None:
+        dt = _dtype_code(dtype)
         out = torch.empty(M, V, dtype=dtype, device=dev)
-    ptr, rows, width, ld = _rows(out, "out")
-    if rows != M or width != V:
-        raise ValueError(f"out must hold {M} rows of {V}")
-    _same_device(dev, w=w, out=out)
+        ptr, ld = out.data_ptr(), V
+    else:
+        dt = _dtype_code(out.dtype)
+        ptr, rows, width, ld = _rows(out, "out")
+        if rows != M or width != V:
+            raise ValueError(f"out must hold {M} rows of {V}")
+        _on(dev, out, "out")
     _launch("spec_mx_logits", dev, workspace, stream, a._cp, a._sp, a.fmt, w._cp, w._sp, w.fmt, M,
-            V, K, ptr, _dtype_code(out.dtype), ld)
+            V, K, ptr, dt, ld)
     return out
 
 
@@ -858,9 +874,13 @@ def spec_token_logprobs(logits, tokens, temperature=1.0, *, top=0, out=None, wor
         tp = tokens.data_ptr()
     if out is None:
         out = TokenLogprobs.empty(rows, top, tokens is not None, dev)
-    lp, rank, ent, ti, tl = out._addresses(rows, top, dev)
-    if tp is None and (lp is not None or rank is not None):
-        raise ValueError("logp and rank need tokens")
+        lp, rank = (None, None) if tp is None else (out.logp.data_ptr(), out.rank.data_ptr())
+        ent = out.entropy.data_ptr()
+        ti, tl = (out.top_ids.data_ptr(), out.top_logp.data_ptr()) if top else (None, None)
+    else:
+        lp, rank, ent, ti, tl = out._addresses(rows, top, dev)
+        if tp is None and (lp is not None or rank is not None):
+            raise ValueError("logp and rank need tokens")
     _launch("spec_token_logprobs", dev, workspace, stream, ptr, dt, ld, tp, temperature, rows, V,
             top, lp, rank, ent, ti, tl)
     return out

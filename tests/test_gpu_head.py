@@ -128,6 +128,13 @@ def test_quantize_strided_rows_and_leading_dimensions():
         S.spec_mx_quantize(big[:, :4])
 
 
+def test_workspaces_named_without_an_index():
+    x = randn(3, 64, seed=1).to(DEV)
+    want = S.spec_mx_quantize(x)
+    got = S.spec_mx_quantize(x, workspace=S.Workspace(device="cuda"))
+    assert torch.equal(got.codes, want.codes)
+
+
 def test_no_rows():
     q = S.spec_mx_quantize(torch.zeros(0, 64, device=DEV), S.SPEC_MX_E4M3)
     assert q.shape == (0, 64) and S.spec_mx_dequantize(q).shape == (0, 64)

@@ -125,6 +125,13 @@ def test_binding_refuses_host_tensors_and_bad_shapes():
     with pytest.raises(ValueError, match="fmt"):
         spec.MXTensor(torch.zeros(4, 64, dtype=torch.uint8),
                       torch.zeros(1, 1, 32, 4, 4, dtype=torch.uint8), 3, 64)
+    with pytest.raises(ValueError, match="device tensors"):
+        spec.MXTensor.empty(4, 64, 0, "cpu")
+    with pytest.raises(ValueError, match="column"):
+        spec.MXTensor.empty(4, 0, 0, "cpu")
+    with pytest.raises(ValueError, match="CUDA device"):
+        spec.MXTensor(torch.zeros(4, 64, dtype=torch.uint8),
+                      torch.zeros(1, 1, 32, 4, 4, dtype=torch.uint8), 0, 64)
 
 
 # --------------------------------------------------------------------- the 64-bit definitions
