@@ -280,9 +280,9 @@ __device__ __forceinline__ int count_larger(const uint4 (&q)[kBatch], float xt) 
 // A thread's sums against a reference `m`, one of its logits and at most kOctaves of
 // exp((max - m) / T) below its maximum, so that the reference changes in few batches. A term of S1
 // is up to kOctaves times one of S, and its roundings count against the entropy: with 32 octaves
-// the entropy of peaked rows was off by up to 2e-5. fma(x, c, -fl(m c)) is (x - m) c + delta with delta the
-// exact rounding error of m c, the same for every term: it is taken out of the sums where the
-// reference changes and at the end.
+// the entropy of peaked rows was off by up to 2e-5. fma(x, c, -fl(m c)) is (x - m) c + delta with
+// delta the exact rounding error of m c, the same for every term: it is taken out of the sums
+// where the reference changes and at the end.
 struct RunningSums {
   float m, limit;                    // reference, and the logit that calls for another
   float most;                        // maximum
@@ -437,7 +437,8 @@ __device__ __forceinline__ float bound_of_list(Shared& sh, float bound, int k) {
 
 // The k largest elements of pieces [j0, j1) into sh.keys (sh.n_keys of them), whatever their order
 // and however many are equal: the k-th largest value by its leading bytes, then every larger
-// element and the first of the equal ones.
+// element and the first of the equal ones. Two (bf16) or four passes more over the row: 2048 equal
+// or ascending rows of 129280 take 0.93 and 1.0 ms in bf16, 2.3 and 2.4 ms in fp32.
 template <int DT>
 __device__ __noinline__ void select_radix(Shared& sh, const Row<DT>& row, int j0, int j1, int k) {
   constexpr int N = Row<DT>::N;
