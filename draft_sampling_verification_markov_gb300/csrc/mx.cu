@@ -1,10 +1,10 @@
 // mx.cu -- block-scaled matrices: quantisation, reading back, and the residual RMS norm that
 // writes its output block-scaled. Streaming kernels; every element is read and written once.
 //
-// Work split. Sixteen consecutive lanes hold a 128-element group of one row, eight elements each:
-// four lanes are a block, whose largest magnitude is two shuffles away, and the group's four
-// scales are one 32-bit store. A warp's loads and code stores are contiguous. A thread has
-// several such pieces in flight: with one, the kernels waited on memory.
+// Work split. Consecutive lanes hold a 128-element group of one row, eight elements each (sixteen
+// in the quantiser): four (two) lanes are a block, whose largest magnitude is two (one) shuffles
+// away, and the group's four scales are one 32-bit store. A warp's loads and code stores are
+// contiguous. A thread has 64 bytes in flight: with 16 the kernels waited on memory.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -18,11 +18,11 @@ namespace mx {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnits = kThreads / 16;  // groups a block takes at once
-// Pieces in flight: 64 bytes a thread either way (129280 x 4096 bf16 to E2M1: 269 us with four, 335
-// with two; 17408 x 2048 fp32 to E4M3: 31 us with two, 37 with four).
+constexpr int kUnits = kThreads / 16;  // groups a block takes at once, eight elements a thread
+constexpr int kWide = kThreads / 8;    // ... sixteen elements a thread
+// Pieces in flight.
 template <int DT>
-constexpr int kUnroll = DT == SPEC_BF16 ? 4 : 2;
+constexpr int kUnroll = DT == SPEC_BF16 ? 2 : 1;
 constexpr int kUnrollBack = 4;
 constexpr uint32_t kFull = 0xffffffffu;
 
@@ -34,6 +34,14 @@ __device__ __forceinline__ uint4 ld_coherent16(const void* p) {
                : "l"(p)
                : "memory");
   return r;
+}
+
+// Streaming (read-once) 32-byte load.
+__device__ __forceinline__ void ld_stream32(const void* p, uint4& a, uint4& b) {
+  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z),
+                 "=r"(b.w)
+               : "l"(p));
 }
 
 template <bool RO>
@@ -209,37 +217,95 @@ __device__ __forceinline__ uint32_t reciprocal(int G) { return 0xffffffffu / (ui
 
 // ------------------------------------------------------------------------------ quantise
 
-// Groups of all rows, the last tile's missing rows among them (their scales are 0).
+// Sixteen elements from v of a row of K (zero past K): 32-byte loads (vec 2), 16-byte ones (1) or
+// single elements.
+template <int DT>
+__device__ __forceinline__ void load16(const void* base, size_t off, int v, int K, int vec,
+                                       Piece<DT> (&p)[2]) {
+  constexpr size_t es = DT == SPEC_BF16 ? 2 : 4;
+  if (vec == 2 && v + 16 <= K) {
+    const char* at = static_cast<const char*>(base) + (off + v) * es;
+    if constexpr (DT == SPEC_BF16) {
+      ld_stream32(at, p[0].q[0], p[1].q[0]);
+    } else {
+      ld_stream32(at, p[0].q[0], p[0].q[1]);
+      ld_stream32(at + 32, p[1].q[0], p[1].q[1]);
+    }
+  } else {
+    load8<DT, true>(base, off, v, K, vec > 0, p[0]);
+    load8<DT, true>(base, off, v + 8, K, vec > 0, p[1]);
+  }
+}
+
+// As quantize8 with sixteen elements a lane (element 16 * (lane % 8) of a group).
+template <int FMT>
+__device__ __forceinline__ bool quantize16(const float (&x)[2][8], bool live, uint8_t* codes,
+                                           uint8_t* scale) {
+  float m = 0.0f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    m = max_abs_nan(m, max_abs_nan(
+                           max_abs_nan(max_abs_nan(x[h][0], x[h][1]), max_abs_nan(x[h][2], x[h][3])),
+                           max_abs_nan(max_abs_nan(x[h][4], x[h][5]), max_abs_nan(x[h][6], x[h][7]))));
+  uint32_t amax = __float_as_uint(m) & 0x7fffffffu;
+  amax = max(amax, __shfl_xor_sync(kFull, amax, 1));
+  const int sb = scale_byte<FMT>(amax);
+  const bool finite = sb != kNanScale;
+  uint32_t word = (uint32_t)sb << (8 * ((threadIdx.x >> 1) & 3));
+  word |= __shfl_xor_sync(kFull, word, 2);
+  word |= __shfl_xor_sync(kFull, word, 4);
+  if (!live) return true;
+  const float f = unscale(finite ? sb : 0);
+  float y[2][8];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[h][i] = x[h][i] * f;
+  if constexpr (FMT == SPEC_MX_E2M1) {
+    const uint2 c = make_uint2(to_e2m1x8(y[0]), to_e2m1x8(y[1]));
+    *reinterpret_cast<uint2*>(codes) = finite ? c : make_uint2(0, 0);
+  } else {
+    const uint2 c = to_e4m3x8(y[0]), d = to_e4m3x8(y[1]);
+    *reinterpret_cast<uint4*>(codes) =
+        finite ? make_uint4(c.x, c.y, d.x, d.y) : make_uint4(0, 0, 0, 0);
+  }
+  if ((threadIdx.x & 7) == 0) *reinterpret_cast<uint32_t*>(scale) = word;
+  return finite;
+}
+
+// Groups of all rows, the last tile's missing rows among them (their scales are 0). Bound by issue
+// more than by memory: with eight elements a lane it took 272 us for 129280 x 4096 bf16.
 template <int DT, int FMT>
-__global__ void __launch_bounds__(kThreads, DT == SPEC_BF16 ? 5 : 8)
-    quantize_kernel(const void* x, long long ldx, int rows, int K, bool vec, uint8_t* codes,
+__global__ void __launch_bounds__(kThreads)
+    quantize_kernel(const void* x, long long ldx, int rows, int K, int vec, uint8_t* codes,
                     uint8_t* scales, uint32_t* status) {
-  const int G = groups(K), l = threadIdx.x & 15;
+  const int G = groups(K), l = threadIdx.x & 7;
   const int tiled = (rows + kTileRows - 1) / kTileRows * kTileRows;
   const uint32_t recip = reciprocal(G);
   constexpr int U = kUnroll<DT>;
   bool finite = true;
-  const long long u0 = (long long)blockIdx.x * kUnits * U;
+  const long long u0 = (long long)blockIdx.x * kWide * U;
   const int row0 = (int)(u0 / G), g0 = (int)(u0 - (long long)row0 * G);
-  Piece<DT> v[U];
+  Piece<DT> v[U][2];
   int row[U];
   uint8_t* scale[U];
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    const Unit u(row0, g0, i * kUnits + threadIdx.x / 16, G, recip);
+    const Unit u(row0, g0, i * kWide + threadIdx.x / 8, G, recip);
     row[i] = u.row;
     scale[i] = scales + scale_word(u.row, u.g, G);
-    clear<DT>(v[i]);
+    clear<DT>(v[i][0]);
+    clear<DT>(v[i][1]);
     if (u.row < rows)
-      load8<DT, true>(x, (size_t)u.row * ldx, u.g * kGroup + 8 * l, K, vec, v[i]);
+      load16<DT>(x, (size_t)u.row * ldx, u.g * kGroup + 16 * l, K, vec, v[i]);
   }
-  uint8_t* c = codes + (size_t)(u0 + threadIdx.x / 16) * kGroupCode<FMT> + kLaneCode<FMT> * l;
+  uint8_t* c = codes + (size_t)(u0 + threadIdx.x / 8) * kGroupCode<FMT> + 2 * kLaneCode<FMT> * l;
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    float y[8];
-    unpack<DT>(v[i], y);
-    finite &= quantize8<FMT>(y, row[i] < rows, c + (size_t)i * kUnits * kGroupCode<FMT>,
-                             scale[i]);
+    float y[2][8];
+    unpack<DT>(v[i][0], y[0]);
+    unpack<DT>(v[i][1], y[1]);
+    finite &= quantize16<FMT>(y, row[i] < rows, c + (size_t)i * kWide * kGroupCode<FMT>, scale[i]);
     if (row[i] >= rows && row[i] < tiled && l == 0) *reinterpret_cast<uint32_t*>(scale[i]) = 0;
   }
   if (!finite) atomicOr(status, SPEC_DEV_NONFINITE);
@@ -534,15 +600,15 @@ int resident(K k, int threads) {
 // Blocks of a streaming kernel: one for each of its units. Loops over fewer, resident blocks were
 // slower (129280 x 4096: 289 against 269 us to quantise, 237 against 211 us to read back): a new
 // block's loads overlap the end of those beside it.
-int grid_for(long long units, int unroll) {
-  return (int)((units + kUnits * unroll - 1) / (kUnits * unroll));
+int grid_for(long long units, int per_block) {
+  return (int)((units + per_block - 1) / per_block);
 }
 
 template <int DT, int FMT>
-void launch_quantize_t(const void* x, long long ldx, int rows, int K, bool vec, uint8_t* codes,
+void launch_quantize_t(const void* x, long long ldx, int rows, int K, int vec, uint8_t* codes,
                        uint8_t* scales, uint32_t* status, cudaStream_t s) {
   const long long units = (long long)((rows + kTileRows - 1) / kTileRows) * kTileRows * groups(K);
-  quantize_kernel<DT, FMT><<<grid_for(units, kUnroll<DT>), kThreads, 0, s>>>(
+  quantize_kernel<DT, FMT><<<grid_for(units, kWide * kUnroll<DT>), kThreads, 0, s>>>(
       x, ldx, rows, K, vec, codes, scales, status);
 }
 
@@ -550,7 +616,7 @@ template <int DT, int FMT>
 void launch_dequantize_t(const uint8_t* codes, const uint8_t* scales, int rows, int K, bool vec,
                          void* out, long long ldo, cudaStream_t s) {
   dequantize_kernel<DT, FMT>
-      <<<grid_for((long long)rows * groups(K), kUnrollBack), kThreads, 0, s>>>(codes, scales, rows,
+      <<<grid_for((long long)rows * groups(K), kUnits * kUnrollBack), kThreads, 0, s>>>(codes, scales, rows,
                                                                                K, vec, out, ldo);
 }
 
@@ -575,9 +641,10 @@ void launch_norm_w(const NormArgs& a, int fmt, cudaStream_t s) {
                       : launch_norm_t<DT, WDT, SPEC_MX_E4M3>(a, s);
 }
 
-bool vec_ok(const void* p, long long ld, int dt) {
+// Rows at multiples of `bytes`.
+bool vec_ok(const void* p, long long ld, int dt, int bytes = 16) {
   const size_t es = dt == SPEC_BF16 ? 2 : 4;
-  return p == nullptr || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * es) % 16 == 0);
+  return p == nullptr || (reinterpret_cast<uintptr_t>(p) % bytes == 0 && (ld * es) % bytes == 0);
 }
 
 }  // namespace
@@ -588,7 +655,7 @@ void launch_mx_quantize(const void* x, int dt, long long ldx, int rows, int K, i
                         uint8_t* codes, uint8_t* scales, uint32_t* status, cudaStream_t s) {
   using namespace mx;
   TraceScope ts(SPEC_KCLASS_OTHER, s);
-  const bool vec = vec_ok(x, ldx, dt);
+  const int vec = vec_ok(x, ldx, dt, 32) ? 2 : vec_ok(x, ldx, dt) ? 1 : 0;
   auto launch = dt == SPEC_BF16
                     ? (fmt == SPEC_MX_E2M1 ? launch_quantize_t<SPEC_BF16, SPEC_MX_E2M1>
                                            : launch_quantize_t<SPEC_BF16, SPEC_MX_E4M3>)
