@@ -103,15 +103,14 @@ constexpr int kMaxPropGrid = 256;
 // A 2-D or 3-D bf16 tensor map with a 128-byte swizzle (false if it cannot be encoded).
 bool make_tensor_map_bf16(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
                           const cuuint64_t* strides_bytes, const cuuint32_t* box);
-// A 2-D map of block-scaled codes (rows of Kp elements) in boxes of 128 elements x box_rows, with
-// a 128-byte swizzle; 4-bit codes are spread over 16-byte units on the way.
-bool make_tensor_map_codes(CUtensorMap* m, const void* base, int fmt, int Kp, int rows,
-                           int box_rows);
-// A 2-D map of 512-byte scale tiles, one a box.
-bool make_tensor_map_scales(CUtensorMap* m, const void* base, long long tiles);
-// A 2-D bf16 output map (row stride ld elements, a multiple of 8) without a swizzle.
-bool make_tensor_map_out(CUtensorMap* m, void* base, int cols, int rows, long long ld,
-                         int box_cols, int box_rows);
+// The driver's tensor-map encoder (null where there is no driver), defined in markov_tc.cu.
+namespace tc {
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn();
+}  // namespace tc
 // Consume the test request that makes the next tensor-core launch never load its first W2
 // tile (spec_test_stall_next_markov).
 int take_stall_request();

@@ -823,46 +823,6 @@ bool make_tensor_map_bf16(CUtensorMap* m, const void* base, int rank, const cuui
   return tc::make_map(m, base, rank, dims, strides_bytes, box);
 }
 
-bool make_tensor_map_codes(CUtensorMap* m, const void* base, int fmt, int Kp, int rows,
-                           int box_rows) {
-  if (!tc::encode_fn()) return false;
-  // 4-bit codes land in shared memory as one byte each slot of a 16-byte unit: sixteen codes,
-  // then eight bytes of gap
-  const bool e2m1 = fmt == SPEC_MX_E2M1;
-  const cuuint64_t dims[2] = {(cuuint64_t)Kp, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)(e2m1 ? Kp / 2 : Kp)};
-  const cuuint32_t box[2] = {128, (cuuint32_t)box_rows}, estr[2] = {1, 1};
-  return tc::encode_fn()(m,
-                         e2m1 ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B
-                              : CU_TENSOR_MAP_DATA_TYPE_UINT8,
-                         2, const_cast<void*>(base), dims, strides, box, estr,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-bool make_tensor_map_out(CUtensorMap* m, void* base, int cols, int rows, long long ld,
-                         int box_cols, int box_rows) {
-  if (!tc::encode_fn()) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, estr[2] = {1, 1};
-  return tc::encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-                         CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-bool make_tensor_map_scales(CUtensorMap* m, const void* base, long long tiles) {
-  if (!tc::encode_fn()) return false;
-  const cuuint64_t dims[2] = {128, (cuuint64_t)tiles}, strides[1] = {512};
-  const cuuint32_t box[2] = {128, 1}, estr[2] = {1, 1};
-  return tc::encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims,
-                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 cudaError_t launch_markov_tc(const RowJob& j, float* pm, float* ps, int* pi, bool argmax,
                              cudaStream_t s) {
   using namespace tc;

@@ -29,7 +29,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "mx.cuh"
-#include "tc_ptx.cuh"
+#include "tc_pair.cuh"
 
 namespace spec {
 namespace mx {
@@ -338,6 +338,38 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   }
 }
 
+// ------------------------------------------------------------------------------ host side
+
+// A 2-D map of cols x rows elements in boxes of box_cols x box_rows.
+bool make_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, long long cols,
+              long long rows, long long row_bytes, int box_cols, int box_rows,
+              CUtensorMapSwizzle swizzle) {
+  if (!tc::encode_fn()) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, estr[2] = {1, 1};
+  return tc::encode_fn()(m, type, 2, const_cast<void*>(base), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows of codes in boxes of one group. 4-bit codes land in shared memory spread over 16-byte
+// units: sixteen codes, then eight bytes of gap.
+bool map_codes(CUtensorMap* m, const void* codes, int fmt, int Kp, int rows, int box_rows) {
+  return make_map(m,
+                  fmt == SPEC_MX_E2M1 ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B
+                                      : CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                  codes, Kp, rows, (long long)code_row(fmt, Kp), kGroup, box_rows,
+                  CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Scale tiles, one a box.
+bool map_scales(CUtensorMap* m, const void* scales, long long tiles) {
+  return make_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, scales, kTileBytes / 4, tiles, kTileBytes,
+                  kTileBytes / 4, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
 // Pairs of CTAs the device holds at once (of the current device; 0 if it cannot be found out).
 int max_pairs() {
   static int cached[64] = {};
@@ -404,12 +436,13 @@ cudaError_t launch_mx_logits(const uint8_t* ac, const uint8_t* as, int af, const
   p.status = status;
   CUtensorMap mw, ma, mws, mas, mo;
   memset(&mo, 0, sizeof mo);
-  if (p.staged && !make_tensor_map_out(&mo, out, V, M, ldo, kTileV, kOutRows))
+  if (p.staged && !make_map(&mo, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, out, V, M, ldo * 2, kTileV,
+                            kOutRows, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
-  if (!make_tensor_map_codes(&mw, wc, wf, padded(K), V, kTileV) ||
-      !make_tensor_map_codes(&ma, ac, af, padded(K), M, p.NT / 2) ||
-      !make_tensor_map_scales(&mws, wsc, (long long)p.n_voc * p.G) ||
-      !make_tensor_map_scales(&mas, as, (long long)((M + kTileRows - 1) / kTileRows) * p.G))
+  if (!map_codes(&mw, wc, wf, padded(K), V, kTileV) ||
+      !map_codes(&ma, ac, af, padded(K), M, p.NT / 2) ||
+      !map_scales(&mws, wsc, (long long)p.n_voc * p.G) ||
+      !map_scales(&mas, as, (long long)((M + kTileRows - 1) / kTileRows) * p.G))
     return cudaErrorInvalidValue;
   const int grid = 2 * (int)(p.units < pairs ? p.units : pairs);
   logits_kernel<<<grid, kThreads, kSmemFixed + p.stages * stage, s>>>(mw, ma, mws, mas, mo, p);
