@@ -8,6 +8,19 @@
 namespace spec {
 namespace tc {
 
+// Whether the phase of `parity` is complete, without waiting (try_wait may suspend the thread).
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // mbar_wait by a converged warp, with one answer for all its lanes (the votes keep the warp's
 // control flow uniform, which its uniform registers need).
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity,
