@@ -160,16 +160,20 @@ __device__ __forceinline__ float max_abs_nan(float a, float b) {
   return d;
 }
 
+// Largest magnitude, NaN if there is one.
+__device__ __forceinline__ float max_abs8(const float (&x)[8]) {
+  return max_abs_nan(max_abs_nan(max_abs_nan(x[0], x[1]), max_abs_nan(x[2], x[3])),
+                     max_abs_nan(max_abs_nan(x[4], x[5]), max_abs_nan(x[6], x[7])));
+}
+
 // Quantises this lane's eight elements (element 8 * (lane % 16) of a group): stores its codes at
 // `codes` and, from the group's first lane, the scale word at `scale`. All 32 lanes call it;
 // `live` masks the stores. Returns whether the block was finite.
 template <int FMT>
 __device__ __forceinline__ bool quantize8(const float (&x)[8], bool live, uint8_t* codes,
                                           uint8_t* scale) {
-  const float m = max_abs_nan(max_abs_nan(max_abs_nan(x[0], x[1]), max_abs_nan(x[2], x[3])),
-                              max_abs_nan(max_abs_nan(x[4], x[5]), max_abs_nan(x[6], x[7])));
   // as integers NaN is above infinity
-  uint32_t amax = __float_as_uint(m) & 0x7fffffffu;
+  uint32_t amax = __float_as_uint(max_abs8(x)) & 0x7fffffffu;
   amax = max(amax, __shfl_xor_sync(kFull, amax, 1));
   amax = max(amax, __shfl_xor_sync(kFull, amax, 2));
   const int sb = scale_byte<FMT>(amax);
@@ -241,12 +245,7 @@ __device__ __forceinline__ void load16(const void* base, size_t off, int v, int 
 template <int FMT>
 __device__ __forceinline__ bool quantize16(const float (&x)[2][8], bool live, uint8_t* codes,
                                            uint8_t* scale) {
-  float m = 0.0f;
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    m = max_abs_nan(m, max_abs_nan(
-                           max_abs_nan(max_abs_nan(x[h][0], x[h][1]), max_abs_nan(x[h][2], x[h][3])),
-                           max_abs_nan(max_abs_nan(x[h][4], x[h][5]), max_abs_nan(x[h][6], x[h][7]))));
+  const float m = max_abs_nan(max_abs8(x[0]), max_abs8(x[1]));
   uint32_t amax = __float_as_uint(m) & 0x7fffffffu;
   amax = max(amax, __shfl_xor_sync(kFull, amax, 1));
   const int sb = scale_byte<FMT>(amax);
@@ -273,8 +272,9 @@ __device__ __forceinline__ bool quantize16(const float (&x)[2][8], bool live, ui
   return finite;
 }
 
-// Groups of all rows, the last tile's missing rows among them (their scales are 0). Bound by issue
-// more than by memory: with eight elements a lane it took 272 us for 129280 x 4096 bf16.
+// Groups of all rows, the last tile's missing rows among them (their scales are 0). 129280 x 4096
+// bf16 to E2M1: 212 us, 6.3 TB/s of values read and codes written; with eight elements a lane the
+// kernel was bound by issue, at 272 us.
 template <int DT, int FMT>
 __global__ void __launch_bounds__(kThreads)
     quantize_kernel(const void* x, long long ldx, int rows, int K, int vec, uint8_t* codes,
@@ -313,6 +313,7 @@ __global__ void __launch_bounds__(kThreads)
 
 // ------------------------------------------------------------------------------ read back
 
+// 129280 x 4096 E2M1 to bf16: 213 us, 6.3 TB/s of codes read and values written.
 template <int DT, int FMT>
 __global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint8_t* codes,
                                                               const uint8_t* scales, int rows,
@@ -509,7 +510,8 @@ __device__ __forceinline__ void clear_missing(const NormArgs& a, int G) {
 
 // A block takes rows in turn, each in registers (eight elements a thread), and loads the next one
 // while it works on a row: the block's sum and what follows it would leave the memory idle
-// otherwise. The weight stays in registers. The last block clears the missing rows' scales.
+// otherwise. The weight stays in registers. The last block clears the missing rows' scales. With a
+// residual: 17408 x 2048 fp32 77 us (6.0 TB/s), 2048 x 4096 bf16 13.9 us, one row of 4096 3.3 us.
 template <int DT, int WDT, int FMT>
 __global__ void __launch_bounds__(1024) rmsnorm_kernel(NormArgs a) {
   constexpr bool kExact = DT == SPEC_BF16 && WDT == SPEC_BF16;
@@ -598,8 +600,8 @@ int resident(K k, int threads) {
 }
 
 // Blocks of a streaming kernel: one for each of its units. Loops over fewer, resident blocks were
-// slower (129280 x 4096: 289 against 269 us to quantise, 237 against 211 us to read back): a new
-// block's loads overlap the end of those beside it.
+// slower (129280 x 4096: 237 against 211 us to read back): a new block's loads overlap the end of
+// those beside it.
 int grid_for(long long units, int per_block) {
   return (int)((units + per_block - 1) / per_block);
 }
@@ -615,9 +617,8 @@ void launch_quantize_t(const void* x, long long ldx, int rows, int K, int vec, u
 template <int DT, int FMT>
 void launch_dequantize_t(const uint8_t* codes, const uint8_t* scales, int rows, int K, bool vec,
                          void* out, long long ldo, cudaStream_t s) {
-  dequantize_kernel<DT, FMT>
-      <<<grid_for((long long)rows * groups(K), kUnits * kUnrollBack), kThreads, 0, s>>>(codes, scales, rows,
-                                                                               K, vec, out, ldo);
+  const int grid = grid_for((long long)rows * groups(K), kUnits * kUnrollBack);
+  dequantize_kernel<DT, FMT><<<grid, kThreads, 0, s>>>(codes, scales, rows, K, vec, out, ldo);
 }
 
 template <int DT, int WDT, int FMT>

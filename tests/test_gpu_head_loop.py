@@ -73,7 +73,8 @@ def test_head_logits_against_the_definition(built):
     h, out = head.logits(hidden[0], res[0], dtype=torch.float32)
     assert out.shape == (wl.R, wl.gamma, wl.V)
     x = h.double().cpu().reshape(-1, head.K).numpy()
-    y = x / ((x ** 2).mean(1, keepdims=True) + head.eps) ** 0.5 * head.norm_weight.double().cpu().numpy()
+    y = x / ((x ** 2).mean(1, keepdims=True) + head.eps) ** 0.5
+    y = y * head.norm_weight.double().cpu().numpy()
     w = ref.dequantize(head.w.codes.cpu(), head.w.scales.cpu(), head.w.fmt, head.K)
     want = y @ w.T
     _, q = S.spec_rmsnorm_mx(hidden[0], head.norm_weight, head.eps, residual=res[0])
