@@ -48,10 +48,9 @@ constexpr uint32_t kFull = 0xffffffffu;
 
 constexpr float kOctaves = 4.0f;
 constexpr float kLowest2 = -256.0f;   // 2^kLowest2 is 0 in fp32
-// The fast sums need log2(e) / T = c in (kFastLeast, kFastScale) and a reference with |m| c below
-// kFastMax. Then fl(m c) is off by less than 2^-14; -2^100 c is finite; and (-2^100 - m) c is far
-// below -256, as |m| < 2^90.
-constexpr float kFastMax = 1024.0f, kFastScale = 0x1p20f, kFastLeast = 0x1p-80f;
+// The fast sums need log2(e) / T = c in (kFastLeast, kFastScale) and a reference |m| < kFastMax:
+// then 2^101 c is finite, and (-2^100 - m) c is below -256.
+constexpr float kFastMax = 0x1p99f, kFastScale = 0x1p20f, kFastLeast = 0x1p-90f;
 
 struct Sums {
   float m, s, s1;  // reference logit, S, S1 (in base 2)
@@ -284,9 +283,8 @@ __device__ __forceinline__ int count_larger(const uint4 (&q)[kBatch], float xt) 
 // A thread's sums against a reference `m`, one of its logits and at most kOctaves of
 // exp((max - m) / T) below its maximum, so that the reference changes in few batches. A term of S1
 // is up to kOctaves times one of S, and its roundings count against the entropy: with 32 octaves
-// the entropy of peaked rows was off by up to 2e-5. fma(x, c, -fl(m c)) is (x - m) c + delta with
-// delta the exact rounding error of m c, the same for every term: it is taken out of the sums
-// where the reference changes and at the end.
+// the entropy of peaked rows was off by up to 2e-5. z = (x - m) c is a subtraction and a product:
+// the largest logit of a row is exactly 1 in S, so a point mass has log-probability and entropy 0.
 struct RunningSums {
   float m, limit;                    // reference, and the logit that calls for another
   float most;                        // maximum
@@ -296,22 +294,18 @@ struct RunningSums {
     m = limit = most = -INFINITY;
     s = s1 = tc::pack2(0.0f, 0.0f);
   }
-  __device__ __forceinline__ bool tame(float c) const { return fabsf(m) * c < kFastMax; }
-
-  // Sums that are free of delta, of exp((x - m') c) for another reference m'.
-  __device__ __forceinline__ void rebase(float to, float c, float delta) {
-    const float d = fmaxf((m - to) * c, kLowest2);
-    const float f = fast_exp2(d) * (1.0f - delta * kLn2), g = d - delta;
+  // The same sums against another reference.
+  __device__ __forceinline__ void rebase(float to, float c) {
+    const float d = fmaxf((m - to) * c, kLowest2), f = fast_exp2(d);
     const unsigned long long f2 = tc::pack2(f, f);
-    s1 = tc::mul2(f2, tc::fma2(tc::pack2(g, g), s, s1));
+    s1 = tc::mul2(f2, tc::fma2(tc::pack2(d, d), s, s1));
     s = tc::mul2(f2, s);
   }
-  __device__ __forceinline__ float delta(float c) const { return fmaf(m, c, -(m * c)); }
   // Against the maximum, where the log-probabilities of likely tokens cancel least.
-  __device__ __forceinline__ Sums sums(float c, bool tame_c) {
+  __device__ __forceinline__ Sums sums(float c) {
     Sums o;
     float a, b;
-    if (m > -INFINITY) rebase(most, c, tame_c && tame(c) ? delta(c) : 0.0f);
+    if (m > -INFINITY) rebase(most, c);
     o.m = most;
     tc::unpack2(s, a, b);
     o.s = a + b;
@@ -351,20 +345,19 @@ __device__ __forceinline__ void take_batch(Shared& sh, const uint4 (&q)[kBatch],
   }
   run.most = fmaxf(run.most, bm);
   if (bm > run.limit) {
-    if (run.m > -INFINITY) run.rebase(bm, c, tame && run.tame(c) ? run.delta(c) : 0.0f);
+    if (run.m > -INFINITY) run.rebase(bm, c);
     run.m = bm;
     run.limit = bm + kOctaves / c;
   }
-  if (tame && run.tame(c)) {
-    const float off = -(run.m * c);
-    const unsigned long long c2 = tc::pack2(c, c), off2 = tc::pack2(off, off);
+  if (tame && fabsf(run.m) < kFastMax) {
+    const unsigned long long c2 = tc::pack2(c, c), m2 = tc::pack2(-run.m, -run.m);
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
       float x[N];
       unpack<DT>(raised<DT>(q[b]), x);
 #pragma unroll
       for (int i = 0; i < N; i += 2) {
-        const unsigned long long z = tc::fma2(tc::pack2(x[i], x[i + 1]), c2, off2);
+        const unsigned long long z = tc::mul2(tc::add2(tc::pack2(x[i], x[i + 1]), m2), c2);
         float z0, z1;
         tc::unpack2(z, z0, z1);
         const unsigned long long e = tc::pack2(fast_exp2(z0), fast_exp2(z1));
@@ -667,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Logprob
       }
 
       // this CTA's sums: lanes against their warp's maximum, then warps against the CTA's
-      Sums acc = merge_lanes<32>(run.sums(c, tame), c);
+      Sums acc = merge_lanes<32>(run.sums(c), c);
       larger = __reduce_add_sync(kFull, larger);
       if (lane == 0) {
         sh.sums[warp] = acc;

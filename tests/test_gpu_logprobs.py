@@ -217,3 +217,18 @@ def test_agrees_with_the_verify_normalisers():
     at = x.gather(1, tok.long()[:, None])[:, 0].float()
     lp = at / 0.8 - st[:, 0] - st[:, 1]
     assert ((lp - r.logp.cpu()).abs() <= 1e-5 * lp.abs().clamp(min=1)).all()
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("T", [1.0, 0.7, 1.3])
+def test_point_masses_are_exact(dt, T):
+    """One token above -inf, or so far above the rest that they vanish in fp32."""
+    x = torch.full((6, 9000), -INF)
+    x[:, 4321] = torch.tensor([0.0, 3.7, -11.3, 250.0, -1e5, 1e20])
+    x[1, 77], x[3, 5] = -400.0, 0.0
+    tok = torch.full((6,), 4321, dtype=torch.int32)
+    r, st = run(x.to(dt), tok, T, 2)
+    assert st == 0
+    assert (r.logp == 0).all() and (r.entropy == 0).all() and (r.top_logp[:, 0] == 0).all()
+    one, _ = run(torch.full((3, 1), 5.5).to(dt), torch.zeros(3, dtype=torch.int32), T, 1)
+    assert (one.logp == 0).all() and (one.entropy == 0).all()
