@@ -40,7 +40,7 @@ constexpr int kCtas = 4;               // CTAs of an SM
 constexpr int kWarps = kThreads / 32;
 constexpr int kBatch = 4;             // 16-byte pieces a thread has in flight, and as many next
 constexpr int kMaxTop = SPEC_LOGPROBS_MAX_TOP;
-constexpr int kPieces = 512;          // listed pieces at most
+constexpr int kEntries = 512;         // listed batches at most
 constexpr int kKeys = 512;            // elements ranked at most
 constexpr int kMaxSplit = 8;          // parts of a row at most
 constexpr int kGroups = 64;           // maxima behind a bound; at least 2 * kMaxTop
@@ -57,14 +57,15 @@ struct Sums {
 };
 
 static_assert(kKeys >= kMaxSplit * kMaxTop && kMaxTop == 32, "the merged lists");
+static_assert(kBatch * 8 <= 32, "a lane an element of a listed batch");
 
 struct Shared {
   alignas(16) float group[kGroups];
   float bound;
-  int n_pieces, n_keys;
-  uint4 piece[kPieces];               // listed pieces: content, index, maximum
-  uint32_t piece_at[kPieces];
-  float piece_max[kPieces];
+  int n_entries, n_keys;
+  uint4 entry[kEntries][kBatch];      // listed batches: content, first piece, maximum
+  uint32_t entry_at[kEntries];
+  float entry_max[kEntries];
   unsigned long long keys[kKeys];
   unsigned long long top[kMaxTop];    // this CTA's largest, in order; 0 = none
   Sums sums[kWarps];
@@ -223,16 +224,26 @@ __device__ __forceinline__ float max3f(float a, float b, float c) {
   return fmaxf(a, fmaxf(b, c));
 }
 
-// Maximum of a piece (NaN ignored).
+// Maximum of a batch (NaN ignored).
 template <int DT>
-__device__ __forceinline__ float piece_max(const uint4& q) {
+__device__ __forceinline__ float batch_max(const uint4 (&q)[kBatch]) {
   if constexpr (DT == SPEC_BF16) {
-    const uint32_t w = as_word(__hmax2(__hmax2(as_bf2(q.x), as_bf2(q.y)),
-                                       __hmax2(as_bf2(q.z), as_bf2(q.w))));
+    __nv_bfloat162 m[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+      m[b] = __hmax2(__hmax2(as_bf2(q[b].x), as_bf2(q[b].y)),
+                     __hmax2(as_bf2(q[b].z), as_bf2(q[b].w)));
+#pragma unroll
+    for (int b = 1; b < kBatch; ++b) m[0] = __hmax2(m[0], m[b]);
+    const uint32_t w = as_word(m[0]);
     return fmaxf(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   } else {
-    return fmaxf(fmaxf(__uint_as_float(q.x), __uint_as_float(q.y)),
-                 fmaxf(__uint_as_float(q.z), __uint_as_float(q.w)));
+    float m = -INFINITY;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+      m = max3f(max3f(m, __uint_as_float(q[b].x), __uint_as_float(q[b].y)),
+                __uint_as_float(q[b].z), __uint_as_float(q[b].w));
+    return m;
   }
 }
 
@@ -260,14 +271,16 @@ __device__ __forceinline__ uint4 raised(const uint4& q) {
 template <int DT>
 __device__ __forceinline__ int count_larger(const uint4 (&q)[kBatch], float xt) {
   if constexpr (DT == SPEC_BF16) {
-    // two comparisons and two additions an instruction; counts up to 16 are exact in bf16
+    // two comparisons an instruction, each a mask of 16 bits, and integer sums of the masks:
+    // 65535 lo + 65535 * 65536 hi, or -lo modulo 2^16 and then 65536 (lo - hi) modulo 2^32
     const __nv_bfloat162 t = __float2bfloat162_rn(xt);
-    __nv_bfloat162 n = __float2bfloat162_rn(0.0f);
+    uint32_t n = 0;
 #pragma unroll
     for (int b = 0; b < kBatch; ++b)
-      n = __hadd2(n, __hadd2(__hadd2(__hgt2(as_bf2(q[b].x), t), __hgt2(as_bf2(q[b].y), t)),
-                             __hadd2(__hgt2(as_bf2(q[b].z), t), __hgt2(as_bf2(q[b].w), t))));
-    return (int)(__low2float(n) + __high2float(n));
+      n += __hgt2_mask(as_bf2(q[b].x), t) + __hgt2_mask(as_bf2(q[b].y), t) +
+           __hgt2_mask(as_bf2(q[b].z), t) + __hgt2_mask(as_bf2(q[b].w), t);
+    const int lo = -n & 0xffffu;
+    return 2 * lo - ((int)(n + lo) >> 16);
   } else {
     int n = 0;
 #pragma unroll
@@ -321,26 +334,14 @@ __device__ __forceinline__ void take_batch(Shared& sh, const uint4 (&q)[kBatch],
                                            float bound, float xt, float c, bool tame,
                                            RunningSums& run, int& larger) {
   constexpr int N = Row<DT>::N;
-  float pm[kBatch], bm = -INFINITY;
-#pragma unroll
-  for (int b = 0; b < kBatch; ++b) {
-    pm[b] = piece_max<DT>(q[b]);
-    bm = fmaxf(bm, pm[b]);
-  }
+  const float bm = batch_max<DT>(q);
   if (TOP && bm >= bound) {
-    int hits = 0;
+    const int at = atomicAdd(&sh.n_entries, 1);
+    if (at < kEntries) {
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) hits += pm[b] >= bound;
-    int at = atomicAdd(&sh.n_pieces, hits);
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      if (!(pm[b] >= bound)) continue;
-      if (at < kPieces) {
-        sh.piece[at] = q[b];
-        sh.piece_at[at] = j + b * kThreads;
-        sh.piece_max[at] = pm[b];
-      }
-      ++at;
+      for (int b = 0; b < kBatch; ++b) sh.entry[at][b] = q[b];
+      sh.entry_at[at] = j;
+      sh.entry_max[at] = bm;
     }
   }
   run.most = fmaxf(run.most, bm);
@@ -420,13 +421,13 @@ __device__ __forceinline__ float bound_of(Shared& sh, float local, int k) {
   return sh.bound;
 }
 
-// The same over the listed pieces; +inf (list nothing more) once they do not fit.
+// The same over the listed batches; +inf (list nothing more) once they do not fit.
 __device__ __forceinline__ float bound_of_list(Shared& sh, float bound, int k) {
   __syncthreads();  // every push so far
-  const int n = sh.n_pieces;
-  if (n > kPieces) return INFINITY;
+  const int n = sh.n_entries;
+  if (n > kEntries) return INFINITY;
   float local = -INFINITY;
-  for (int i = threadIdx.x; i < n; i += kThreads) local = fmaxf(local, sh.piece_max[i]);
+  for (int i = threadIdx.x; i < n; i += kThreads) local = fmaxf(local, sh.entry_max[i]);
   return fmaxf(bound, bound_of(sh, local, k));
 }
 
@@ -543,24 +544,43 @@ template <int DT>
 __device__ __forceinline__ void collect_keys(Shared& sh, const Row<DT>& r, int j0, int j1,
                                              float bound, int k) {
   constexpr int N = Row<DT>::N;
-  const int tid = threadIdx.x, n = sh.n_pieces;
-  bool fits = n <= kPieces;
+  const int tid = threadIdx.x, lane = tid & 31, n = sh.n_entries;
+  bool fits = n <= kEntries;
   if (fits) {
     float local = -INFINITY;
-    for (int i = tid; i < n; i += kThreads) local = fmaxf(local, sh.piece_max[i]);
-    // fewer listed pieces than places leave the bound they were listed by
+    for (int i = tid; i < n; i += kThreads) local = fmaxf(local, sh.entry_max[i]);
+    // fewer listed batches than places leave the bound they were listed by
     const float cut = fmaxf(bound_of(sh, local, k), bound);
-    for (int e = tid; e < n * N; e += kThreads) {  // an element a thread
-      const int i = e / N, q = e % N;
-      if (sh.piece_max[i] < cut) continue;
-      float x;
-      if constexpr (DT == SPEC_BF16)
-        x = bf16_to_f32(reinterpret_cast<const uint16_t*>(&sh.piece[i])[q]);
-      else
-        x = reinterpret_cast<const float*>(&sh.piece[i])[q];
-      if (!(x >= cut)) continue;
-      const int at = atomicAdd(&sh.n_keys, 1);
-      if (at < kKeys) sh.keys[at] = make_key(order_bits(x), (int)sh.piece_at[i] * N - r.head + q);
+    // a warp takes every kWarps-th batch, its lanes the elements of those that reach the cut
+    for (int base = tid >> 5; base < n; base += kThreads) {
+      const int mine = base + lane * kWarps;
+      uint32_t hit = __ballot_sync(kFull, mine < n && sh.entry_max[mine] >= cut);
+      while (hit) {
+        constexpr int kAtOnce = 2;
+        int i[kAtOnce], n_mine = 0;
+        float x[kAtOnce];
+#pragma unroll
+        for (int q = 0; q < kAtOnce; ++q) {
+          i[q] = base + (hit ? __ffs(hit) - 1 : 0) * kWarps;
+          x[q] = -INFINITY;
+          if (hit && lane < kBatch * N) {
+            if constexpr (DT == SPEC_BF16)
+              x[q] = bf16_to_f32(reinterpret_cast<const uint16_t*>(sh.entry[i[q]])[lane]);
+            else
+              x[q] = reinterpret_cast<const float*>(sh.entry[i[q]])[lane];
+          }
+          n_mine += x[q] >= cut;
+          hit &= hit - 1;
+        }
+        if (!n_mine) continue;
+        int at = atomicAdd(&sh.n_keys, n_mine);
+#pragma unroll
+        for (int q = 0; q < kAtOnce; ++q)
+          if (x[q] >= cut && at < kKeys)
+            sh.keys[at++] =
+                make_key(order_bits(x[q]), ((int)sh.entry_at[i[q]] + lane / N * kThreads) * N -
+                                               r.head + lane % N);
+      }
     }
     __syncthreads();
     fits = sh.n_keys <= kKeys;
@@ -625,22 +645,19 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Logprob
       float bound = INFINITY;
       if (TOP) {
         if (tid == 0) {
-          sh.n_pieces = 0;
+          sh.n_entries = 0;
           sh.n_keys = 0;
         }
-        float first = -INFINITY;
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b)
-          first = max3f(first, piece_max<DT>(cur[b]), piece_max<DT>(nxt[b]));
         // nothing of -inf has a place
-        bound = fmaxf(bound_of(sh, first, a.top), -3.402823466e38f);
+        bound = fmaxf(bound_of(sh, fmaxf(batch_max<DT>(cur), batch_max<DT>(nxt)), a.top),
+                      -3.402823466e38f);
       }
       RunningSums run;
       run.start();
       int larger = 0;
       // the bound is renewed from the list whenever the number of batches seen has doubled: a
       // list then grows by little more than k pieces between two renewals, however long the row
-      int renew = j0 + 4 * kStep;
+      int renew = j0 + (a.top <= 20 ? 16 : 8) * kStep;
       for (int jb = j0; jb < j1; jb += 2 * kStep) {
         take_batch<DT, TOP>(sh, cur, jb + tid, bound, xt, c, tame, run, larger);
         r.template load_batch<kBatch>(cur, jb + 2 * kStep, j1);
