@@ -7,20 +7,22 @@
 // scale (x - m) log2(e) / T, and moves them to another reference (2^d S, 2^d (S1 + d S) for a
 // shift d) where a logit is far above; the parts are merged the same way in a fixed order.
 //
-// The largest k <= 32 logits need no second pass. The maxima of 64 groups of the first batch
+// The largest k <= 32 logits need no second pass. The maxima of 64 groups of the first two batches
 // bound the k-th largest logit from below (k groups hold a logit at least as large as the k-th
-// group maximum). After that batch, a 16-byte piece of the row goes on a list when its maximum
-// reaches the bound: a few hundred pieces of a row of 129280 logits. At the end the same argument
-// on the listed maxima gives a bound that few elements reach; those are reloaded and ranked by
-// counting, larger logits first, then lower ids. Rows that defeat the bound (long ascending runs,
-// hundreds of equal logits) overflow a list and take a radix selection over the row instead.
+// group maximum). A thread's batch of 64 bytes then goes on a list when its maximum reaches the
+// bound: some two hundred batches of a row of 129280 logits. At the end the same argument on the
+// listed maxima gives a bound that few elements reach; those are ranked by counting, larger logits
+// first, then lower ids. Rows that defeat the bound (long ascending runs, hundreds of equal
+// logits) overflow a list and take a radix selection over the row instead.
 //
 // Few rows are split over a thread-block cluster of up to 8 CTAs, which merge through distributed
 // shared memory: no workspace, one launch.
 //
-// Measured (V = 129280): 2048 bf16 rows 87 us without alternatives (6.1 TB/s), 110 us with 20 (4.8
-// TB/s; while a CTA streams an SM reads 52 GB/s, the rest is the ends of rows), 256 rows 24 us, one
-// row 7.3 us; 1024 fp32 rows with 20 95 us (5.6 TB/s).
+// Measured (V = 129280): 2048 bf16 rows 87 us without alternatives (6.1 TB/s), 105 us with 20 (5.0
+// TB/s), 256 rows 23 us, one row 7.3 us; 1024 fp32 rows with 20 95 us (5.6 TB/s). Without
+// alternatives memory bounds it. With them each row takes 41 instead of 33 thousand warp
+// instructions, and an SM issues in 64 % of its cycles; half of the difference is the lists, half
+// the row's end. Prefetching the next row into L2 during that end is slower (107 to 111 us).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -61,7 +63,8 @@ static_assert(kBatch * 8 <= 32, "a lane an element of a listed batch");
 
 struct Shared {
   alignas(16) float group[kGroups];
-  float bound;
+  float bound, room;                  // entries until the next renewal
+  bool full[2];
   int n_entries, n_keys;
   uint4 entry[kEntries][kBatch];      // listed batches: content, first piece, maximum
   uint32_t entry_at[kEntries];
@@ -421,9 +424,17 @@ __device__ __forceinline__ float bound_of(Shared& sh, float local, int k) {
   return sh.bound;
 }
 
-// The same over the listed batches; +inf (list nothing more) once they do not fit.
-__device__ __forceinline__ float bound_of_list(Shared& sh, float bound, int k) {
-  __syncthreads();  // every push so far
+// The bound renewed from the listed batches if there are more than sh.room, which doubles for the
+// next call; +inf (list nothing more) once they do not fit. `turn` alternates between two calls.
+__device__ __forceinline__ float renewed(Shared& sh, float bound, int k, int turn) {
+  if (threadIdx.x == 0) {
+    // one thread's count, however many entries others add meanwhile: all go the same way
+    sh.full[turn] = *(volatile int*)&sh.n_entries > sh.room;
+    sh.room *= 2.0f;
+  }
+  __syncthreads();
+  // a thread may reach the next call, but not the one after it, before another reads this
+  if (!sh.full[turn]) return bound;
   const int n = sh.n_entries;
   if (n > kEntries) return INFINITY;
   float local = -INFINITY;
@@ -612,7 +623,8 @@ __device__ __forceinline__ void write_top(const LogprobArgs& a, int row, int pla
 // together and would leave the memory idle together (10 of 56 thousand cycles a row).
 template <int DT, bool TOP, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const LogprobArgs a,
-                                                                   const int parts) {
+                                                                   const int parts,
+                                                                   const float room) {
   __shared__ Shared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int split = SPLIT ? parts : 1;
@@ -646,6 +658,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Logprob
       if (TOP) {
         if (tid == 0) {
           sh.n_entries = 0;
+          sh.room = room;
           sh.n_keys = 0;
         }
         // nothing of -inf has a place
@@ -655,9 +668,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Logprob
       RunningSums run;
       run.start();
       int larger = 0;
-      // the bound is renewed from the list whenever the number of batches seen has doubled: a
-      // list then grows by little more than k pieces between two renewals, however long the row
-      int renew = j0 + (a.top <= 20 ? 16 : 8) * kStep;
+      // Whenever the number of batches seen has doubled, the bound is renewed from the list if the
+      // list would pass half its room by the row's end at this rate. 2048 bf16 rows of 129280:
+      // always renewed 110 us, never 105; uniform on [0, 1), with hundreds of logits equal to the
+      // k-th, the list overflows without: 166 us against 465. By this rule 106 and 162.
+      int renew = j0 + 4 * kStep;
       for (int jb = j0; jb < j1; jb += 2 * kStep) {
         take_batch<DT, TOP>(sh, cur, jb + tid, bound, xt, c, tame, run, larger);
         r.template load_batch<kBatch>(cur, jb + 2 * kStep, j1);
@@ -666,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Logprob
         r.template load_batch<kBatch>(nxt, jb + 3 * kStep, j1);
         if (TOP && jb + 2 * kStep == renew && renew < j1) {
           renew += renew - j0;
-          bound = bound_of_list(sh, bound, a.top);
+          bound = renewed(sh, bound, a.top, __ffs(renew - j0) & 1);
         }
       }
       const Row<DT> done = r;
@@ -778,8 +793,10 @@ cudaError_t launch_t(const LogprobArgs& a, int split, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = split > 1 ? 1 : 0;
-  return split > 1 ? cudaLaunchKernelEx(&cfg, logprobs_kernel<DT, TOP, true>, a, split)
-                   : cudaLaunchKernelEx(&cfg, logprobs_kernel<DT, TOP, false>, a, split);
+  // entries a part may list in its first four batches if it is to fill half the list by its end
+  const float room = kEntries / 2 * 4.0f * kBatch * kThreads * Row<DT>::N * split / a.V;
+  return split > 1 ? cudaLaunchKernelEx(&cfg, logprobs_kernel<DT, TOP, true>, a, split, room)
+                   : cudaLaunchKernelEx(&cfg, logprobs_kernel<DT, TOP, false>, a, split, room);
 }
 
 }  // namespace

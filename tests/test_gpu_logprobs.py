@@ -232,3 +232,24 @@ def test_point_masses_are_exact(dt, T):
     assert (r.logp == 0).all() and (r.entropy == 0).all() and (r.top_logp[:, 0] == 0).all()
     one, _ = run(torch.full((3, 1), 5.5).to(dt), torch.zeros(3, dtype=torch.int32), T, 1)
     assert (one.logp == 0).all() and (one.entropy == 0).all()
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("top", [1, 20, 32])
+def test_rows_that_renew_their_bound(dt, top):
+    """Long rows that are not split, with a few or hundreds of logits equal to the last one that
+    has a place, and maxima that come late."""
+    V, g = 150001, torch.Generator().manual_seed(top)
+    x = torch.stack([torch.randn(V, generator=g) * 2, torch.rand(V, generator=g),
+                     torch.round(torch.randn(V, generator=g) * 4),
+                     torch.randn(V, generator=g) + torch.linspace(0, 4, V),
+                     torch.randn(V, generator=g) * torch.linspace(3, 0.1, V)]).to(dt)
+    tok = tokens_for(5, V, top)
+    r, st = run(x.repeat(32, 1), tok.repeat(32), 0.9, top)
+    assert st == 0
+    # the copies begin at other addresses, so their sums may add in another order
+    for c in (0, 5, 155):
+        check(x, tok, 0.9, top, S.TokenLogprobs(*(getattr(r, f)[c:c + 5]
+                                                  for f in S.TokenLogprobs.__slots__)))
+    assert torch.equal(r.rank, r.rank[:5].repeat(32))
+    assert torch.equal(r.top_ids, r.top_ids[:5].repeat(32, 1))
