@@ -292,7 +292,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     uint32_t aph = 0;
     for (long long u = u_first; u < p.units; u += u_step) {
       const Work w(p, u, rank);
-      if (!mbar_wait_warp(&acc_full[as], aph, abort, p.status)) break;
+      // the four warps of a half meet at barriers below: they go on together or not at all
+      if (!all_of(1 + half, 128, mbar_wait_warp(&acc_full[as], aph, abort, p.status))) break;
       tc_fence_after();
       uint32_t x[kChunks][32];
 #pragma unroll

@@ -29,6 +29,20 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity,
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
 }
 
+// Named barrier `id` of `threads` threads; whether `ok` holds in all of them.
+__device__ __forceinline__ bool all_of(int id, int threads, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.and.aligned.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"((uint32_t)ok)
+      : "memory");
+  return r != 0;
+}
+
 // ------------------------------------------------------------------------------ block scaling
 
 // Instruction descriptor, kind::mxf8f6f4 with E8M0 scales: element formats af / bf (0 = E4M3,
