@@ -630,8 +630,8 @@ void launch_norm_t(const NormArgs& a, cudaStream_t s) {
   }
   auto k = rmsnorm_kernel<DT, WDT, FMT>;
   static int most[33] = {};  // resident blocks by warps of a block
-  int& n = most[threads / 32];
-  if (!n) n = resident(k, threads);
+  int n = __atomic_load_n(&most[threads / 32], __ATOMIC_RELAXED);
+  if (!n) __atomic_store_n(&most[threads / 32], n = resident(k, threads), __ATOMIC_RELAXED);
   const int blocks = a.rows < n ? a.rows : n;
   k<<<blocks + 1, threads, 0, s>>>(a);
 }

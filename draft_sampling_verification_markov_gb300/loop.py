@@ -50,7 +50,9 @@ class SpecLoop:
     With `logprobs` = k (0 .. 32) every iteration also scores its emitted tokens under the target
     rows that they answer to, at the loop's temperature: token_logp, token_rank, token_entropy
     [iters, R, gamma + 1] and the k most likely tokens of each row, top_ids and top_logp
-    [iters, R, gamma + 1, k]. Places past an iteration's emitted tokens keep NaN, 0 and -1."""
+    [iters, R, gamma + 1, k]. `allowed` does not enter these: they are of the target's own
+    distribution. Places past an iteration's emitted tokens (-1 in out_tokens) are left as they
+    were: NaN, 0 and -1 until a run emits more tokens there."""
 
     def __init__(self, U, target, W1, W2, anchors0, u_draft, u_accept, u_resid, temperature,
                  sps=None, *, iterations=None, schedule=True, allowed=None,
