@@ -40,7 +40,8 @@ class VocabHead:
         """Logits [..., V] of hidden rows [..., K] (plus residual, added first). Returns
         (h, logits) with h = hidden + residual, or hidden itself without a residual."""
         if out is None:
-            out = torch.empty(*hidden.shape[:-1], self.V, dtype=dtype, device=hidden.device)
+            out = S._on_stream(stream, torch.empty, *hidden.shape[:-1], self.V, dtype=dtype,
+                               device=hidden.device)
         h, rows = S.spec_rmsnorm_mx(hidden, self.norm_weight, self.eps, residual=residual,
                                     residual_out=residual_out, workspace=workspace, stream=stream)
         S.spec_mx_logits(rows, self.w, out=out, workspace=workspace, stream=stream)

@@ -721,9 +721,18 @@ def _launch(name, dev, workspace, stream, *args):
         raise SpecError(name, rc)
 
 
-def _mx_out(out, rows, K, fmt, dev):
+def _on_stream(stream, new, *args, **kw):
+    """new(*args), with its memory from the stream that will write it: that of the current one
+    could still be in use there, or be given away there while `stream` uses it."""
+    if stream is None:
+        return new(*args, **kw)
+    with torch.cuda.stream(stream):
+        return new(*args, **kw)
+
+
+def _mx_out(out, rows, K, fmt, dev, stream):
     if out is None:
-        return MXTensor.empty(rows, K, fmt, dev)
+        return _on_stream(stream, MXTensor.empty, rows, K, fmt, dev)
     if out.rows != rows or out.K != K or out.fmt != fmt:
         raise ValueError("out must be an MXTensor of x's rows, width and the given format")
     if out.device != dev:
@@ -737,7 +746,7 @@ def spec_mx_quantize(x, fmt=SPEC_MX_E2M1, *, out=None, workspace=None, stream=No
     MXTensor to write into."""
     ptr, rows, K, ld = _rows(x, "x")
     dt, dev = _dtype_code(x.dtype), x.device
-    out = _mx_out(out, rows, K, fmt, dev)
+    out = _mx_out(out, rows, K, fmt, dev, stream)
     _launch("spec_mx_quantize", dev, workspace, stream, ptr, dt, ld, rows, K, fmt, out._cp,
             out._sp)
     return out
@@ -748,7 +757,7 @@ def spec_mx_dequantize(q, *, dtype=torch.bfloat16, out=None, workspace=None, str
     rows, K, dev = q.rows, q.K, q.device
     if out is None:
         dt = _dtype_code(dtype)
-        out = torch.empty(rows, K, dtype=dtype, device=dev)
+        out = _on_stream(stream, torch.empty, rows, K, dtype=dtype, device=dev)
         ptr, ld = out.data_ptr(), K
     else:
         dt = _dtype_code(out.dtype)
@@ -780,7 +789,7 @@ def spec_rmsnorm_mx(x, weight, eps=1e-6, *, residual=None, residual_out=None, fm
         rp, _, _, ldr = _rows(residual, "residual")
         _on(dev, residual, "residual")
         if residual_out is None:
-            h = torch.empty(x.shape, dtype=x.dtype, device=dev)
+            h = _on_stream(stream, torch.empty, x.shape, dtype=x.dtype, device=dev)
             op = h.data_ptr()
         else:
             h = residual_out
@@ -791,7 +800,7 @@ def spec_rmsnorm_mx(x, weight, eps=1e-6, *, residual=None, residual_out=None, fm
     elif residual_out is not None:
         raise ValueError("residual_out is an output of the form with a residual")
     _on(dev, weight, "weight")
-    out = _mx_out(out, rows, K, fmt, dev)
+    out = _mx_out(out, rows, K, fmt, dev, stream)
     _launch("spec_rmsnorm_mx", dev, workspace, stream, ptr, ldx, rp, ldr, dt, weight.data_ptr(),
             _dtype_code(weight.dtype), eps, rows, K, op, ldo, fmt, out._cp, out._sp)
     return h, out
@@ -807,7 +816,7 @@ def spec_mx_logits(a, w, *, dtype=torch.bfloat16, out=None, workspace=None, stre
     _on(dev, w, "w")
     if out is None:
         dt = _dtype_code(dtype)
-        out = torch.empty(M, V, dtype=dtype, device=dev)
+        out = _on_stream(stream, torch.empty, M, V, dtype=dtype, device=dev)
         ptr, ld = out.data_ptr(), V
     else:
         dt = _dtype_code(out.dtype)
@@ -873,7 +882,7 @@ def spec_token_logprobs(logits, tokens, temperature=1.0, *, top=0, out=None, wor
             raise ValueError(f"tokens must hold {rows} contiguous ids")
         tp = tokens.data_ptr()
     if out is None:
-        out = TokenLogprobs.empty(rows, top, tokens is not None, dev)
+        out = _on_stream(stream, TokenLogprobs.empty, rows, top, tokens is not None, dev)
         lp, rank = (None, None) if tp is None else (out.logp.data_ptr(), out.rank.data_ptr())
         ent = out.entropy.data_ptr()
         ti, tl = (out.top_ids.data_ptr(), out.top_logp.data_ptr()) if top else (None, None)

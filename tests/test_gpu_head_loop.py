@@ -172,3 +172,36 @@ def test_expired_wait_of_the_product_reports_timeout(built):
     again = S.spec_mx_logits(a, w, workspace=ws)
     torch.cuda.synchronize()
     assert ws.status() == 0 and torch.equal(again, want)
+
+
+def test_tensors_of_a_call_belong_to_its_stream(built, monkeypatch):
+    """What a call allocates comes from the stream it was given, not from the current one, where
+    the memory may still be read or be given away again: the intermediate rows of the head too."""
+    from draft_sampling_verification_markov_gb300.head import VocabHead
+    side, seen = torch.cuda.Stream(), []
+    g = torch.Generator().manual_seed(3)
+    w, x = (torch.randn(n, 256, generator=g).to(DEV) for n in (640, 5))
+    head = VocabHead(w, torch.ones(256, device=DEV))
+    tok = torch.zeros(5, dtype=torch.int32, device=DEV)
+
+    def calls(**kw):
+        h, z = head.logits(x, x, dtype=torch.float32, **kw)
+        q = S.spec_mx_quantize(x, **kw)
+        y = S.spec_mx_dequantize(q, dtype=torch.float32, **kw)
+        z2 = S.spec_mx_logits(q, head.w, dtype=torch.float32, **kw)
+        r = S.spec_token_logprobs(z, tok, 1.0, top=3, **kw)
+        return [h, z, y, z2, r.logp, r.rank, r.entropy, r.top_ids, r.top_logp]
+
+    want = calls()
+    torch.cuda.synchronize()
+    empty = torch.empty
+
+    def recorded(*a, **kw):
+        seen.append(torch.cuda.current_stream().cuda_stream)
+        return empty(*a, **kw)
+
+    monkeypatch.setattr(torch, "empty", recorded)
+    got = calls(stream=side)
+    side.synchronize()
+    assert seen and set(seen) == {side.cuda_stream}
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
