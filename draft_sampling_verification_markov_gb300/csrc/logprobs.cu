@@ -7,7 +7,7 @@
 // scale (x - m) log2(e) / T, and moves them to another reference (2^d S, 2^d (S1 + d S) for a
 // shift d) where a logit is far above; the parts are merged the same way in a fixed order.
 //
-// The largest k <= 32 logits need no second pass. The maxima of 64 groups of the first two batches
+// The largest k <= 32 logits need no second pass. The maxima of 64 groups of the first batches
 // bound the k-th largest logit from below (k groups hold a logit at least as large as the k-th
 // group maximum). A thread's batch of 64 bytes then goes on a list when its maximum reaches the
 // bound: some two hundred batches of a row of 129280 logits. At the end the same argument on the
@@ -19,7 +19,7 @@
 // shared memory: no workspace, one launch.
 //
 // Measured (V = 129280): 2048 bf16 rows 87 us without alternatives (6.1 TB/s), 105 us with 20 (5.0
-// TB/s), 256 rows 23 us, one row 7.3 us; 1024 fp32 rows with 20 95 us (5.6 TB/s). Without
+// TB/s), 256 rows 22 us, one row 7.4 us; 1024 fp32 rows with 20 95 us (5.6 TB/s). Without
 // alternatives memory bounds it. With them each row takes 41 instead of 33 thousand warp
 // instructions, and an SM issues in 64 % of its cycles; half of the difference is the lists, half
 // the row's end. Prefetching the next row into L2 during that end is slower (107 to 111 us).
@@ -38,9 +38,8 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256;
-constexpr int kCtas = 4;               // CTAs of an SM
 constexpr int kWarps = kThreads / 32;
-constexpr int kBatch = 4;             // 16-byte pieces a thread has in flight, and as many next
+constexpr int kBatch = 4;             // 16-byte pieces of a thread's batch
 constexpr int kMaxTop = SPEC_LOGPROBS_MAX_TOP;
 constexpr int kEntries = 512;         // listed batches at most
 constexpr int kKeys = 512;            // elements ranked at most
@@ -618,13 +617,18 @@ __device__ __forceinline__ void write_top(const LogprobArgs& a, int row, int pla
   if (a.top_logp) a.top_logp[at] = key ? (x - ms.m) * a.scale - ms.s : -INFINITY;
 }
 
+// D batches of a thread in flight: 2, and four CTAs an SM, or for rows that leave an SM two CTAs 4.
+// 256 rows of 129280 with 2 / 4, us: bf16 22.7 / 21.7, fp32 32.9 / 28.9 (parts of split rows gain
+// nothing). 512 threads a CTA instead: 23.3 and 30.0.
+__host__ __device__ constexpr int ctas(int D) { return 8 / D; }
+
 // SPLIT: a cluster takes one row, each CTA a part of it. Else a CTA takes rows in turn and has the
 // first batches of the next one on their way before it finishes a row: all CTAs of an SM start
 // together and would leave the memory idle together (10 of 56 thousand cycles a row).
-template <int DT, bool TOP, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const LogprobArgs a,
-                                                                   const int parts,
-                                                                   const float room) {
+template <int DT, bool TOP, bool SPLIT, int D>
+__global__ void __launch_bounds__(kThreads, ctas(D)) logprobs_kernel(const LogprobArgs a,
+                                                                     const int parts,
+                                                                     const float room) {
   __shared__ Shared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int split = SPLIT ? parts : 1;
@@ -637,11 +641,12 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Logprob
   int row = SPLIT ? blockIdx.x / split : blockIdx.x;
   Row<DT> r(a.x, (size_t)row * a.ld, a.V);
   // the first logits are on their way while the token is read
-  uint4 cur[kBatch], nxt[kBatch];
+  uint4 q[D][kBatch];
   {
     const int np = r.pieces(), per = (np + split - 1) / split;
-    r.template load_batch<kBatch>(cur, part * per, min(np, part * per + per));
-    r.template load_batch<kBatch>(nxt, part * per + kStep, min(np, part * per + per));
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+      r.template load_batch<kBatch>(q[d], part * per + d * kStep, min(np, part * per + per));
   }
   int t = a.tokens ? a.tokens[row] : 0;
   while (true) {
@@ -661,9 +666,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Logprob
           sh.room = room;
           sh.n_keys = 0;
         }
+        float first = batch_max<DT>(q[0]);
+#pragma unroll
+        for (int d = 1; d < D; ++d) first = fmaxf(first, batch_max<DT>(q[d]));
         // nothing of -inf has a place
-        bound = fmaxf(bound_of(sh, fmaxf(batch_max<DT>(cur), batch_max<DT>(nxt)), a.top),
-                      -3.402823466e38f);
+        bound = fmaxf(bound_of(sh, first, a.top), -3.402823466e38f);
       }
       RunningSums run;
       run.start();
@@ -672,14 +679,16 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Logprob
       // list would pass half its room by the row's end at this rate. 2048 bf16 rows of 129280:
       // always renewed 110 us, never 105; uniform on [0, 1), with hundreds of logits equal to the
       // k-th, the list overflows without: 166 us against 465. By this rule 106 and 162.
-      int renew = j0 + 4 * kStep;
-      for (int jb = j0; jb < j1; jb += 2 * kStep) {
-        take_batch<DT, TOP>(sh, cur, jb + tid, bound, xt, c, tame, run, larger);
-        r.template load_batch<kBatch>(cur, jb + 2 * kStep, j1);
-        if (jb + kStep >= j1) break;
-        take_batch<DT, TOP>(sh, nxt, jb + kStep + tid, bound, xt, c, tame, run, larger);
-        r.template load_batch<kBatch>(nxt, jb + 3 * kStep, j1);
-        if (TOP && jb + 2 * kStep == renew && renew < j1) {
+      int renew = j0 + 2 * D * kStep;
+      for (int jb = j0; jb < j1; jb += D * kStep) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+          const int j = jb + d * kStep;
+          if (d && j >= j1) break;
+          take_batch<DT, TOP>(sh, q[d], j + tid, bound, xt, c, tame, run, larger);
+          r.template load_batch<kBatch>(q[d], j + D * kStep, j1);
+        }
+        if (TOP && jb + D * kStep == renew && renew < j1) {
           renew += renew - j0;
           bound = renewed(sh, bound, a.top, __ffs(renew - j0) & 1);
         }
@@ -687,8 +696,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Logprob
       const Row<DT> done = r;
       if (next < a.rows) {
         r = Row<DT>(a.x, (size_t)next * a.ld, a.V);
-        r.template load_batch<kBatch>(cur, 0, r.pieces());
-        r.template load_batch<kBatch>(nxt, kStep, r.pieces());
+#pragma unroll
+        for (int d = 0; d < D; ++d) r.template load_batch<kBatch>(q[d], d * kStep, r.pieces());
       }
 
       // this CTA's sums: lanes against their warp's maximum, then warps against the CTA's
@@ -771,8 +780,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Logprob
       if (next < a.rows) __syncthreads();  // the next row reuses the shared state
     } else if (next < a.rows) {
       r = Row<DT>(a.x, (size_t)next * a.ld, a.V);
-      r.template load_batch<kBatch>(cur, 0, r.pieces());
-      r.template load_batch<kBatch>(nxt, kStep, r.pieces());
+#pragma unroll
+      for (int d = 0; d < D; ++d) r.template load_batch<kBatch>(q[d], d * kStep, r.pieces());
     }
     if (next >= a.rows) return;
     row = next;
@@ -780,23 +789,29 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Logprob
   }
 }
 
-template <int DT, bool TOP>
+template <int DT, bool TOP, bool SPLIT, int D>
 cudaError_t launch_t(const LogprobArgs& a, int split, cudaStream_t s) {
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = split;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  const int most = kCtas * num_sms();
-  cfg.gridDim = dim3((unsigned)(split > 1 ? a.rows * split : (a.rows < most ? a.rows : most)));
+  const int most = ctas(D) * num_sms();
+  cfg.gridDim = dim3((unsigned)(SPLIT ? a.rows * split : (a.rows < most ? a.rows : most)));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
   cfg.attrs = &attr;
-  cfg.numAttrs = split > 1 ? 1 : 0;
-  // entries a part may list in its first four batches if it is to fill half the list by its end
-  const float room = kEntries / 2 * 4.0f * kBatch * kThreads * Row<DT>::N * split / a.V;
-  return split > 1 ? cudaLaunchKernelEx(&cfg, logprobs_kernel<DT, TOP, true>, a, split, room)
-                   : cudaLaunchKernelEx(&cfg, logprobs_kernel<DT, TOP, false>, a, split, room);
+  cfg.numAttrs = SPLIT ? 1 : 0;
+  // entries a part may list before its first renewal if it is to fill half the list by its end
+  const float room = kEntries / 2 * 2.0f * D * kBatch * kThreads * Row<DT>::N * split / a.V;
+  return cudaLaunchKernelEx(&cfg, logprobs_kernel<DT, TOP, SPLIT, D>, a, split, room);
+}
+
+template <int DT, bool TOP>
+cudaError_t launch_split(const LogprobArgs& a, int split, cudaStream_t s) {
+  if (split > 1) return launch_t<DT, TOP, true, 2>(a, split, s);
+  return a.rows <= ctas(4) * num_sms() ? launch_t<DT, TOP, false, 4>(a, 1, s)
+                                       : launch_t<DT, TOP, false, 2>(a, 1, s);
 }
 
 }  // namespace
@@ -813,8 +828,10 @@ cudaError_t launch_token_logprobs(const LogprobArgs& a, int dt, cudaStream_t s) 
          a.V >= 2 * split * batch)
     split *= 2;
   if (dt == SPEC_BF16)
-    return a.top ? launch_t<SPEC_BF16, true>(a, split, s) : launch_t<SPEC_BF16, false>(a, split, s);
-  return a.top ? launch_t<SPEC_F32, true>(a, split, s) : launch_t<SPEC_F32, false>(a, split, s);
+    return a.top ? launch_split<SPEC_BF16, true>(a, split, s)
+                 : launch_split<SPEC_BF16, false>(a, split, s);
+  return a.top ? launch_split<SPEC_F32, true>(a, split, s)
+               : launch_split<SPEC_F32, false>(a, split, s);
 }
 
 }  // namespace spec
