@@ -638,6 +638,7 @@ __global__ void __launch_bounds__(kThreads, ctas(D)) logprobs_kernel(const Logpr
   const bool tame = c < kFastScale && c > kFastLeast;
   constexpr int kStep = kBatch * kThreads;
 
+  grid_dep_wait();
   int row = SPLIT ? blockIdx.x / split : blockIdx.x;
   Row<DT> r(a.x, (size_t)row * a.ld, a.V);
   // the first logits are on their way while the token is read
@@ -791,17 +792,19 @@ __global__ void __launch_bounds__(kThreads, ctas(D)) logprobs_kernel(const Logpr
 
 template <int DT, bool TOP, bool SPLIT, int D>
 cudaError_t launch_t(const LogprobArgs& a, int split, cudaStream_t s) {
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = split;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = trace_active() ? 0 : 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = split;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   const int most = ctas(D) * num_sms();
   cfg.gridDim = dim3((unsigned)(SPLIT ? a.rows * split : (a.rows < most ? a.rows : most)));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = SPLIT ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = SPLIT ? 2 : 1;
   // entries a part may list before its first renewal if it is to fill half the list by its end
   const float room = kEntries / 2 * 2.0f * D * kBatch * kThreads * Row<DT>::N * split / a.V;
   return cudaLaunchKernelEx(&cfg, logprobs_kernel<DT, TOP, SPLIT, D>, a, split, room);

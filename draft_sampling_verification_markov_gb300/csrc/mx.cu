@@ -284,6 +284,7 @@ __global__ void __launch_bounds__(kThreads)
   const uint32_t recip = reciprocal(G);
   constexpr int U = kUnroll<DT>;
   bool finite = true;
+  grid_dep_wait();
   const long long u0 = (long long)blockIdx.x * kWide * U;
   const int row0 = (int)(u0 / G), g0 = (int)(u0 - (long long)row0 * G);
   Piece<DT> v[U][2];
@@ -322,6 +323,7 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint8_t* cod
   const int G = groups(K), l = threadIdx.x & 15;
   const uint32_t recip = reciprocal(G);
   constexpr int U = kUnrollBack;
+  grid_dep_wait();
   const long long u0 = (long long)blockIdx.x * kUnits * U;
   const int row0 = (int)(u0 / G), g0 = (int)(u0 - (long long)row0 * G);
   uint2 c[U];
@@ -516,6 +518,7 @@ template <int DT, int WDT, int FMT>
 __global__ void __launch_bounds__(1024) rmsnorm_kernel(NormArgs a) {
   constexpr bool kExact = DT == SPEC_BF16 && WDT == SPEC_BF16;
   const int G = groups(a.K), Kp = G * kGroup, blocks = gridDim.x - 1;
+  grid_dep_wait();
   if ((int)blockIdx.x == blocks) {
     clear_missing(a, G);
     return;
@@ -556,6 +559,7 @@ template <int DT, int WDT, int FMT>
 __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(NormArgs a) {
   constexpr bool kExact = DT == SPEC_BF16 && WDT == SPEC_BF16;
   const int G = groups(a.K), Kp = G * kGroup, row = blockIdx.x, step = 8 * blockDim.x;
+  grid_dep_wait();
   if (row == a.rows) {
     clear_missing(a, G);
     return;
@@ -610,22 +614,23 @@ template <int DT, int FMT>
 void launch_quantize_t(const void* x, long long ldx, int rows, int K, int vec, uint8_t* codes,
                        uint8_t* scales, uint32_t* status, cudaStream_t s) {
   const long long units = (long long)((rows + kTileRows - 1) / kTileRows) * kTileRows * groups(K);
-  quantize_kernel<DT, FMT><<<grid_for(units, kWide * kUnroll<DT>), kThreads, 0, s>>>(
-      x, ldx, rows, K, vec, codes, scales, status);
+  launch_kernel(quantize_kernel<DT, FMT>, grid_for(units, kWide * kUnroll<DT>), kThreads, 0, s,
+                true, x, ldx, rows, K, vec, codes, scales, status);
 }
 
 template <int DT, int FMT>
 void launch_dequantize_t(const uint8_t* codes, const uint8_t* scales, int rows, int K, bool vec,
                          void* out, long long ldo, cudaStream_t s) {
   const int grid = grid_for((long long)rows * groups(K), kUnits * kUnrollBack);
-  dequantize_kernel<DT, FMT><<<grid, kThreads, 0, s>>>(codes, scales, rows, K, vec, out, ldo);
+  launch_kernel(dequantize_kernel<DT, FMT>, grid, kThreads, 0, s, true, codes, scales, rows, K, vec,
+                out, ldo);
 }
 
 template <int DT, int WDT, int FMT>
 void launch_norm_t(const NormArgs& a, cudaStream_t s) {
   const int pieces = groups(a.K) * (kGroup / 8), threads = (pieces + 31) / 32 * 32;
   if (threads > 1024) {
-    rmsnorm_long_kernel<DT, WDT, FMT><<<a.rows + 1, 1024, 0, s>>>(a);
+    launch_kernel(rmsnorm_long_kernel<DT, WDT, FMT>, a.rows + 1, 1024, 0, s, true, a);
     return;
   }
   auto k = rmsnorm_kernel<DT, WDT, FMT>;
@@ -633,7 +638,7 @@ void launch_norm_t(const NormArgs& a, cudaStream_t s) {
   int n = __atomic_load_n(&most[threads / 32], __ATOMIC_RELAXED);
   if (!n) __atomic_store_n(&most[threads / 32], n = resident(k, threads), __ATOMIC_RELAXED);
   const int blocks = a.rows < n ? a.rows : n;
-  k<<<blocks + 1, threads, 0, s>>>(a);
+  launch_kernel(k, blocks + 1, threads, 0, s, true, a);
 }
 
 template <int DT, int WDT>

@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   __syncthreads();
   cluster_sync();  // the pair's barriers are ready
   tc_fence_after();
+  grid_dep_wait();
   const uint32_t tmem = *tmem_slot;
   const uint32_t sf_col0 = p.n_acc * p.NT;  // scales after the accumulators
 
@@ -468,8 +469,8 @@ cudaError_t launch_mx_logits(const uint8_t* ac, const uint8_t* as, int af, const
       !map_scales(&mas, as, (long long)((M + kTileRows - 1) / kTileRows) * p.G))
     return cudaErrorInvalidValue;
   const int grid = 2 * (int)(p.units < pairs ? p.units : pairs);
-  logits_kernel<<<grid, kThreads, kSmemFixed + p.stages * stage, s>>>(mw, ma, mws, mas, mo, p);
-  return cudaGetLastError();
+  return launch_kernel(logits_kernel, grid, kThreads, kSmemFixed + p.stages * stage, s, true, mw, ma,
+                       mws, mas, mo, p);
 }
 
 }  // namespace spec

@@ -205,3 +205,75 @@ def test_tensors_of_a_call_belong_to_its_stream(built, monkeypatch):
     side.synchronize()
     assert seen and set(seen) == {side.cuda_stream}
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_calls_in_a_row_wait_for_what_they_read(built):
+    """Each call may be scheduled while the kernel before it ends. Chains that hand buffers over
+    and write them again, over two streams that meet, after copies and fills, eager and replayed
+    from a graph, give what the same calls give one at a time."""
+    from draft_sampling_verification_markov_gb300.head import VocabHead
+    g = torch.Generator().manual_seed(9)
+    K, V, M, n = 512, 5000, 40, 12
+    head = VocabHead(torch.randn(V, K, generator=g).to(DEV) * 0.1, torch.ones(K, device=DEV))
+    xs = torch.randn(n, M, K, generator=g).to(DEV)
+    tok = torch.randint(V, (n, M), generator=g, dtype=torch.int32).to(DEV)
+    side = torch.cuda.Stream()
+    ws, ws2 = S.Workspace(device=DEV), S.Workspace(device=DEV)
+    ws.reserve(256), ws2.reserve(256)
+    x, r, z = torch.empty(M, K, device=DEV), torch.empty(M, K, device=DEV), torch.empty(
+        M, V, device=DEV)
+    q, back = S.MXTensor.empty(M, K, S.SPEC_MX_E4M3, DEV), torch.empty(M, K, device=DEV)
+    out = [S.TokenLogprobs.empty(M, 3, True, torch.device(DEV)) for _ in range(n)]
+    backs = torch.empty(n, M, K, device=DEV)
+
+    def chain(step):
+        main = torch.cuda.current_stream()
+        r.zero_()
+        for i in range(n):
+            x.copy_(xs[i])
+            S.spec_rmsnorm_mx(x, head.norm_weight, residual=r, residual_out=r, out=q,
+                              workspace=ws)
+            step()
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                S.spec_mx_dequantize(q, out=back, workspace=ws2)
+                step()
+                S.spec_mx_quantize(back, S.SPEC_MX_E4M3, out=q2, workspace=ws2)
+                step()
+                S.spec_mx_dequantize(q2, out=backs[i], workspace=ws2)
+                step()
+            S.spec_mx_logits(q, head.w, out=z, workspace=ws)
+            step()
+            S.spec_token_logprobs(z, tok[i], 1.0, top=3, out=out[i], workspace=ws)
+            step()
+            main.wait_stream(side)
+            if i % 3 == 0:  # straight after both streams
+                S.spec_token_logprobs(z, tok[i], 1.0, top=3, out=out[i], workspace=ws)
+                step()
+
+    q2 = S.MXTensor.empty(M, K, S.SPEC_MX_E4M3, DEV)
+
+    def results():
+        torch.cuda.synchronize()
+        assert ws.status() == 0 and ws2.status() == 0
+        return [getattr(o, f).clone() for o in out for f in S.TokenLogprobs.__slots__] + [
+            backs.clone(), r.clone()]
+
+    def spoil():
+        for t in [x, r, z, back, backs] + [getattr(o, f) for o in out
+                                           for f in S.TokenLogprobs.__slots__]:
+            t.fill_(7)
+
+    chain(torch.cuda.synchronize)
+    want = results()
+    for _ in range(20):
+        spoil()
+        chain(lambda: None)
+        assert all(torch.equal(a, b) for a, b in zip(results(), want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain(lambda: None)
+    for _ in range(20):
+        spoil()
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(results(), want))
