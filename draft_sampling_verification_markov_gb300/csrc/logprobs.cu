@@ -226,7 +226,7 @@ __device__ __forceinline__ float max3f(float a, float b, float c) {
   return fmaxf(a, fmaxf(b, c));
 }
 
-// Maximum of a batch (NaN ignored).
+// Maximum of a batch (NaN ignored, unless there is nothing else).
 template <int DT>
 __device__ __forceinline__ float batch_max(const uint4 (&q)[kBatch]) {
   if constexpr (DT == SPEC_BF16) {
@@ -667,9 +667,9 @@ __global__ void __launch_bounds__(kThreads, ctas(D)) logprobs_kernel(const Logpr
           sh.room = room;
           sh.n_keys = 0;
         }
-        float first = batch_max<DT>(q[0]);
+        float first = -INFINITY;  // a batch of NaN has the maximum NaN
 #pragma unroll
-        for (int d = 1; d < D; ++d) first = fmaxf(first, batch_max<DT>(q[d]));
+        for (int d = 0; d < D; ++d) first = fmaxf(first, batch_max<DT>(q[d]));
         // nothing of -inf has a place
         bound = fmaxf(bound_of(sh, first, a.top), -3.402823466e38f);
       }

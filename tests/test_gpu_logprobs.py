@@ -253,3 +253,22 @@ def test_rows_that_renew_their_bound(dt, top):
                                                   for f in S.TokenLogprobs.__slots__)))
     assert torch.equal(r.rank, r.rank[:5].repeat(32))
     assert torch.equal(r.top_ids, r.top_ids[:5].repeat(32, 1))
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("first", [1, 1300])
+def test_alternatives_behind_a_run_of_nans(first, dt):
+    """A row that begins with more NaN logits than the first bound is made from still has its
+    alternatives, whatever rows were before it."""
+    V, n, k = 129280, 17000, 20
+    x = logits(4, V, 5, dt)
+    x[0] += 50
+    x[1:, :n] = float("nan")
+    x[2, :n:700] = x[2, n:n + 25]
+    rows = torch.tensor([0] * first + [1, 2, 3] * 40)
+    r = S.spec_token_logprobs(x.to(DEV)[rows.to(DEV)], None, 1.0, top=k,
+                              workspace=S.Workspace(device=DEV))
+    want = torch.where(x.isnan(), -INF, x.double())
+    order = want.sort(dim=1, descending=True, stable=True).indices[:, :k]
+    assert torch.equal(r.top_ids.cpu().long(), order[rows])
+    assert r.top_logp[first:].isnan().all() and r.top_logp[:first].isfinite().all()
