@@ -103,7 +103,7 @@ constexpr int kMaxPropGrid = 256;
 // A 2-D or 3-D bf16 tensor map with a 128-byte swizzle (false if it cannot be encoded).
 bool make_tensor_map_bf16(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
                           const cuuint64_t* strides_bytes, const cuuint32_t* box);
-// The driver's tensor-map encoder (null where there is no driver), defined in markov_tc.cu.
+// The CUDA driver's tensor-map encoder (null where there is no driver), defined in markov_tc.cu.
 namespace tc {
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,

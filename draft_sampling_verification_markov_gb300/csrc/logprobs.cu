@@ -18,8 +18,8 @@
 // Few rows are split over a thread-block cluster of up to 8 CTAs, which merge through distributed
 // shared memory: no workspace, one launch.
 //
-// Measured (V = 129280): 2048 bf16 rows 87 us without alternatives (6.1 TB/s), 105 us with 20 (5.0
-// TB/s), 256 rows 22 us, one row 7.4 us; 1024 fp32 rows with 20 95 us (5.6 TB/s). Without
+// Measured (V = 129280): 2048 bf16 rows 87 us without alternatives (6.1 TB/s), 105 us with 20 (5.1
+// TB/s), 256 rows 21 us, one row 7.4 us; 1024 fp32 rows with 20 95 us (5.6 TB/s). Without
 // alternatives memory bounds it. With them each row takes 41 instead of 33 thousand warp
 // instructions, and an SM issues in 64 % of its cycles; half of the difference is the lists, half
 // the row's end. Prefetching the next row into L2 during that end is slower (107 to 111 us).
@@ -423,6 +423,17 @@ __device__ __forceinline__ float bound_of(Shared& sh, float local, int k) {
   return sh.bound;
 }
 
+// This thread's share of the n listed maxima. Neighbours in the list go to different groups of
+// bound_of: with consecutive ones in a group, a list of a hundred left most groups empty and the
+// bound low (2048 rows of 32000, top 20: 47.0 -> 43.1 us; 256 of 129280: 21.8 -> 21.2).
+__device__ __forceinline__ float listed_max(const Shared& sh, int n) {
+  constexpr int kPer = kThreads / kGroups;
+  float m = -INFINITY;
+  for (int i = threadIdx.x / kPer + threadIdx.x % kPer * kGroups; i < n; i += kThreads)
+    m = fmaxf(m, sh.entry_max[i]);
+  return m;
+}
+
 // The bound renewed from the listed batches if there are more than sh.room, which doubles for the
 // next call; +inf (list nothing more) once they do not fit. `turn` alternates between two calls.
 __device__ __forceinline__ float renewed(Shared& sh, float bound, int k, int turn) {
@@ -436,9 +447,7 @@ __device__ __forceinline__ float renewed(Shared& sh, float bound, int k, int tur
   if (!sh.full[turn]) return bound;
   const int n = sh.n_entries;
   if (n > kEntries) return INFINITY;
-  float local = -INFINITY;
-  for (int i = threadIdx.x; i < n; i += kThreads) local = fmaxf(local, sh.entry_max[i]);
-  return fmaxf(bound, bound_of(sh, local, k));
+  return fmaxf(bound, bound_of(sh, listed_max(sh, n), k));
 }
 
 // ------------------------------------------------------------------------------ radix selection
@@ -557,10 +566,8 @@ __device__ __forceinline__ void collect_keys(Shared& sh, const Row<DT>& r, int j
   const int tid = threadIdx.x, lane = tid & 31, n = sh.n_entries;
   bool fits = n <= kEntries;
   if (fits) {
-    float local = -INFINITY;
-    for (int i = tid; i < n; i += kThreads) local = fmaxf(local, sh.entry_max[i]);
     // fewer listed batches than places leave the bound they were listed by
-    const float cut = fmaxf(bound_of(sh, local, k), bound);
+    const float cut = fmaxf(bound_of(sh, listed_max(sh, n), k), bound);
     // a warp takes every kWarps-th batch, its lanes the elements of those that reach the cut
     for (int base = tid >> 5; base < n; base += kThreads) {
       const int mine = base + lane * kWarps;
