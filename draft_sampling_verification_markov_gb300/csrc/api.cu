@@ -988,11 +988,11 @@ int spec_mx_logits(const uint8_t* a_codes, const uint8_t* a_scales, int a_fmt,
   if (!a_codes || !a_scales || !w_codes || !w_scales || !out || !mx_aligned(a_codes, a_scales) ||
       !mx_aligned(w_codes, w_scales) || !elem_aligned(out, out_dtype))
     return SPEC_ERR_INVALID_ARG;
-  if (launch_mx_logits(a_codes, a_scales, a_fmt, w_codes, w_scales, w_fmt, M, V, K, out, out_dtype,
-                       ld_out, static_cast<uint32_t*>(ws),
-                       static_cast<cudaStream_t>(stream)) != cudaSuccess)
-    return SPEC_ERR_CUDA;
-  return finish();
+  const cudaError_t e = launch_mx_logits(a_codes, a_scales, a_fmt, w_codes, w_scales, w_fmt, M, V, K,
+                                         out, out_dtype, ld_out, static_cast<uint32_t*>(ws),
+                                         static_cast<cudaStream_t>(stream));
+  const int rc = finish();  // a failed launch is not left for the next call to report
+  return e == cudaSuccess ? rc : SPEC_ERR_CUDA;
 }
 
 int spec_token_logprobs(const void* logits, int dtype, long long ld, const int32_t* tokens,
@@ -1014,9 +1014,9 @@ int spec_token_logprobs(const void* logits, int dtype, long long ld, const int32
   LogprobArgs a{logits, ld, tokens, temperature > 0.0f ? 1.0f / temperature : 1.0f, rows, V,
                 top_ids || top_logp ? top : 0, logp, rank, entropy, top_ids, top_logp,
                 static_cast<uint32_t*>(ws)};
-  if (launch_token_logprobs(a, dtype, static_cast<cudaStream_t>(stream)) != cudaSuccess)
-    return SPEC_ERR_CUDA;
-  return finish();
+  const cudaError_t e = launch_token_logprobs(a, dtype, static_cast<cudaStream_t>(stream));
+  const int rc = finish();
+  return e == cudaSuccess ? rc : SPEC_ERR_CUDA;
 }
 
 }  // extern "C"
