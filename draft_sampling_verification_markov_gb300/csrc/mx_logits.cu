@@ -23,11 +23,13 @@
 //                  rows two accumulators alternate; above, tensor memory holds one beside the
 //                  scales.
 //
-// Measured (V = 129280, K = 4096, 4-bit vocabulary, 8-bit rows, bf16 out, back to back in a
-// graph): 64 rows 47.6 us (6.3 TB/s; the 298 MB alone are 44 us), 128 rows 53.4, 256 rows 87 us
-// (tensor pipe active 79 %), 1792 rows 528 us (3.6 PFLOP/s, tensor pipe active 87 %); in a loop of
-// a second the power limit brings the last to 600 us. At 256 rows the reading of the accumulator
-// between tiles costs some 14 us, the scale copies 5, the stores 10.
+// Measured (V = 129280, K = 4096, 4-bit vocabulary, 8-bit rows, bf16 out, back to back in a graph,
+// two vocabulary matrices in turn so that none of one stays in L2): 64 rows 50.7 us (5.9 TB/s; the
+// 298 MB alone are 44 us), 128 rows 55.7, 256 rows 87 us (tensor pipe active 79 %), 1792 rows 517
+// us (3.7 PFLOP/s, tensor pipe active 87 %); in a loop of a second the power limit brings the last
+// to 600 us. At 256 rows the reading of the accumulator between tiles costs some 14 us, the scale
+// copies 5, the stores 10. Polling the barriers without suspending is 1 to 2 % slower, and so is
+// fetching the tensor maps ahead.
 #include <cuda_runtime.h>
 #include <stdint.h>
 #include <string.h>
@@ -230,8 +232,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     // ------------------------------------------------------------------ MMA
     // At small N this warp's own instructions are part of the bound (one more branch a stage cost
     // 8 % at 64 rows): a stage's descriptors are additions to the last one's, and whether the next
-    // stage is full is asked before this stage's instructions are issued (64 rows: 49.6 -> 47.6
-    // us).
+    // stage is full is asked before this stage's instructions are issued (64 rows of one
+    // matrix: 49.6 -> 47.6 us).
     const uint32_t lead = elect_lane();
     const uint64_t da0 = sw128_desc(smem_u32(sA)), db0 = sw128_desc(smem_u32(sB));
     const uint64_t ds0 = scale_desc(smem_u32(sS));
