@@ -312,14 +312,21 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       const int v = w.vt * kTileV + q * 32 + lane;
       if (p.staged) {
         // pieces of 16 rows x 128 tokens, two buffers a half: the half's four warps write their
-        // tokens, one thread hands the piece to the copy engine, which clips it to the output
+        // tokens, one thread hands the piece to the copy engine, which clips it to the output.
+        // A piece's buffer must have been read by the copy of the piece before the last. A tile
+        // starts with the first buffer whichever the last tile ended with (an odd number of
+        // pieces ends with the first, too), so its first piece waits for every copy before it.
 #pragma unroll
         for (int i = 0; i < 2 * kChunks; ++i) {
           const int c = 32 * (i - i % 2 + half) + kOutRows * (i % 2);
           if (c >= w.rows) break;
           const uint32_t buf = smem_u32(sO + (2 * half + i % 2) * kOutBytes);
-          if (threadIdx.x == issuer)
-            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          if (threadIdx.x == issuer) {
+            if (i == 0)
+              asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            else
+              asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          }
           asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
           const uint32_t at = buf + (q * 32 + lane) * 2;
 #pragma unroll
