@@ -457,6 +457,9 @@ __device__ __forceinline__ DF warp_sum_exact(float x) {
 }
 
 // The scale of a row: 1 / rms = (hi + lo) * two with `two` a power of two and hi in [1, 2).
+// lo is 0 exactly where the root is a fraction with a power of two below: then
+// rms^2 = sum / K + eps = 4^j / m^2 with m odd, so m^2 divides K and m has 12 bits at most; a pair
+// that is such a number up to its own error (2^-45) is taken to be it.
 struct RowScale {
   float hi, lo, two;
   RowScale() = default;
@@ -466,22 +469,39 @@ struct RowScale {
     const float back = __uint_as_float((uint32_t)(127 - e) << 23);
     hi = r.hi * back;
     lo = r.lo * back;
+    if (fabsf(lo) < 0x1p-42f && !(__float_as_uint(hi) & 0xfffu)) lo = 0.0f;
     if (!(r.hi < INFINITY)) hi = NAN, two = 1.0f;
   }
 };
 
-// h * rstd * w, truncated, with the last bit set for the rest that was cut off (rounding to odd:
-// a product that has no rest is taken to have one, which only moves an exact tie of the format).
-// Rounding that to the format rounds the product itself; rounding to the nearest fp32 in between
-// meets a midpoint of the format about once in 2^20 elements and may then go the wrong way. The
-// power of two comes first: h * two is exact, and of the size of the result. EXACT: the product
-// with the weight has no rounding error (two bf16 numbers).
-template <bool EXACT>
+// h * rstd * w, truncated, with the last bit set where something was cut off (rounding to odd).
+// Rounding that to the format rounds the product itself, and a block's scale is the least that fits
+// the product; rounding to the nearest fp32 in between meets a midpoint of the format about once
+// in 2^20 elements and may then go the wrong way. The power of two comes first: h * two is exact,
+// and of the size of the result. EXACT: the product with the weight has no rounding error (two
+// bf16 numbers). REST: the product may have no rest, which takes its own look; otherwise (lo is
+// not 0: the root is no fraction with a power of two below) it always has one.
+template <bool EXACT, bool REST>
 __device__ __forceinline__ float scaled(float h, const RowScale& r, float w) {
   const float g = h * r.two, p = g * w;
   float low = p * r.lo;
   if (!EXACT) low = fmaf(fmaf(g, w, -p), r.hi, low);
-  return __uint_as_float(__float_as_uint(__fmaf_rz(p, r.hi, low)) | 1u);
+  const float y = __fmaf_rz(p, r.hi, low);
+  const bool rest = !REST || fmaf(p, r.hi, -y) + low != 0.0f;
+  return __uint_as_float(__float_as_uint(y) | (rest ? 1u : 0u));
+}
+
+// The products of eight elements from k of a row of K, 0 past K.
+template <bool EXACT>
+__device__ __forceinline__ void scale8(float (&h)[8], const RowScale& r, const float (&w)[8], int k,
+                                       int K) {
+  if (r.lo != 0.0f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = k + i < K ? scaled<EXACT, false>(h[i], r, w[i]) : 0.0f;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = k + i < K ? scaled<EXACT, true>(h[i], r, w[i]) : 0.0f;
+  }
 }
 
 // The scale of a row from each thread's sum of squares: fp32 within a warp, exact additions over
@@ -545,8 +565,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(NormArgs a) {
     float y[8], v[8];
     unpack<DT>(h, y);
     unpack<WDT>(w, v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = k + i < a.K ? scaled<kExact>(y[i], rs, v[i]) : 0.0f;
+    scale8<kExact>(y, rs, v, k, a.K);
     finite &= quantize8<FMT>(y, k < Kp,
                              a.codes + ((size_t)row * G * kGroup + k) / 8 * kLaneCode<FMT>,
                              a.scales + scale_word(row, k / kGroup, G));
@@ -585,8 +604,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(NormArgs a) {
       unpack<DT>(add_pair<DT>(a, row, k, p), h);
       load8<WDT, true>(a.weight, 0, k, a.K, a.wvec, w);
       unpack<WDT>(w, v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) h[i] = k + i < a.K ? scaled<kExact>(h[i], rs, v[i]) : 0.0f;
+      scale8<kExact>(h, rs, v, k, a.K);
     }
     finite &= quantize8<FMT>(h, k < Kp, codes + k / 8 * kLaneCode<FMT>,
                              a.scales + scale_word(row, k / kGroup, G));

@@ -466,7 +466,9 @@ int spec_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int fmt, int
  * Residual addition, root-mean-square norm and quantisation in one pass.
  * Defines: "Module deepseek_v4_mtp", Forward (the draft logits are lm_head(rms_norm(h))).
  *   h = x + residual (rounded to `dtype`, as it is stored), or h = x without a residual;
- *   y = h * rsqrt(mean(h^2) + eps) * weight, in fp32; codes, scales = quantised y.
+ *   y = h * rsqrt(mean(h^2) + eps) * weight; codes, scales = quantised y. The products are not
+ *   rounded before the format: where the root is exact (eps = 0 and a row of one magnitude that is
+ *   a power of two, say) the scale is the least that fits y and ties go to the even code.
  * Arguments:
  *   x, residual   [rows, K] of `dtype`, row strides ldx and ldr; residual may be NULL.
  *   weight        [K] of w_dtype.

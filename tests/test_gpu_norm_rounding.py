@@ -1,0 +1,151 @@
+"""Codes and scales of the residual RMS norm, element by element, against exact arithmetic: products
+that are exact, and products next to the formats' midpoints."""
+from fractions import Fraction
+
+import numpy as np
+import pytest
+import torch
+
+import head_ref as ref
+from draft_sampling_verification_markov_gb300 import spec as S
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+FMTS = [S.SPEC_MX_E2M1, S.SPEC_MX_E4M3]
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def magnitudes(fmt):
+    return ref.code_values(fmt)[:(8 if fmt == ref.E2M1 else 127)]
+
+
+def block_codes(y, fmt):
+    """Scale byte and codes of one block of Fractions: the least scale that fits, each element the
+    nearest value, a tie the even code."""
+    vals = [Fraction(float(v)) for v in magnitudes(fmt)]
+    mids = [(a + b) / 2 for a, b in zip(vals, vals[1:])]
+    amax, e = max(map(abs, y)), -127
+    while amax > vals[-1] * Fraction(2) ** e:
+        e += 1
+    codes = []
+    for v in y:
+        a = abs(v) / Fraction(2) ** e
+        lo, hi = 0, len(mids)       # number of midpoints that a passes
+        while lo < hi:
+            m = (lo + hi) // 2
+            if a > mids[m] or (a == mids[m] and m % 2 == 1):
+                lo = m + 1
+            else:
+                hi = m
+        codes.append(lo + (len(vals) + (fmt == ref.E4M3) if v < 0 else 0))
+    return e + 127, codes
+
+
+def exact(h, w, root, fmt):
+    """Bytes [rows, K / 32] and codes [rows, K] of h * root[row] * w, for K a multiple of 32."""
+    rows, K = h.shape
+    byte, code = np.zeros((rows, K // 32), int), np.zeros((rows, K), int)
+    hw = [[Fraction(float(a)) * Fraction(float(b)) for a, b in zip(r, w)] for r in h]
+    for r in range(rows):
+        for b in range(K // 32):
+            at = slice(32 * b, 32 * b + 32)
+            byte[r, b], code[r, at] = block_codes([v * root[r] for v in hw[r][at]], fmt)
+    return byte, code
+
+
+def stored(q, K):
+    """The same of an MXTensor; codes of zeros without their sign."""
+    c, s = q.codes.cpu().numpy().astype(int), q.scales.cpu().numpy().astype(int)
+    if q.fmt == ref.E2M1:
+        c = np.stack([c & 15, c >> 4], 2).reshape(q.rows, -1)
+    c = np.where(c == (8 if q.fmt == ref.E2M1 else 128), 0, c)[:, :K]
+    r, k = np.arange(q.rows)[:, None], np.arange(K // 32)[None, :]
+    return s[r // 128, k // 4, r % 32, r % 128 // 32, k % 4], c
+
+
+def assert_same(q, byte, code):
+    sign = 8 if q.fmt == ref.E2M1 else 128
+    got_byte, got = stored(q, code.shape[1])
+    np.testing.assert_array_equal(got_byte, byte)
+    np.testing.assert_array_equal(got, np.where(code == sign, 0, code))
+
+
+def border_weights(fmt, K, scale):
+    """Blocks of the format's largest value, its midpoints and its values, times `scale`; a last
+    block whose largest is one step of bf16 above the largest value (so that its scale is twice)."""
+    v = magnitudes(fmt)
+    pts = np.concatenate([(v[1:] + v[:-1]) / 2, v])
+    w = np.zeros((K // 32, 32))
+    at = 0
+    for b in range(K // 32):
+        w[b, 0] = v[-1]
+        for i in range(1, 32):
+            w[b, i] = pts[at % len(pts)] * (1 if at % 3 else -1)
+            at += 1
+    w[-1, 0] = v[-1] + 2.0 ** (np.floor(np.log2(v[-1])) - 7)
+    return w.reshape(-1) * scale
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dt,wdt", [(BF16, BF16), (F32, F32), (BF16, F32)])
+@pytest.mark.parametrize("K", [32, 512, 992, 9216])
+def test_exact_products(K, dt, wdt, fmt):
+    """eps = 0 and rows of one power of two: 1 / rms is one too, and every product is a number of
+    eight bits. Blocks whose largest product is the format's largest value keep the least scale,
+    ties go to the even code."""
+    n = [0, 2, -7, 30, -30]
+    rng = np.random.default_rng(K)
+    sign = rng.choice([-1.0, 1.0], (len(n), K))
+    h = sign * 2.0 ** np.array(n)[:, None]
+    w = border_weights(fmt, K, 2.0 ** -2)
+    x = torch.from_numpy(h).to(dt)
+    half = x / 2                                     # x + residual = h, exactly
+    wt = torch.from_numpy(w).to(wdt)
+    assert (wt.double().numpy() == w).all()
+    byte, code = exact(h, w, [Fraction(2) ** -e for e in n], fmt)
+    for args in (dict(x=x, res=None), dict(x=half, res=half)):
+        res = None if args["res"] is None else args["res"].to(DEV)
+        _, q = S.spec_rmsnorm_mx(args["x"].to(DEV), wt.to(DEV), 0.0, residual=res, fmt=fmt)
+        assert_same(q, byte, code)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dt,wdt", [(BF16, BF16), (F32, F32)])
+@pytest.mark.parametrize("root,K", [(3, 288), (5, 800), (15, 7200), (21, 14112)])
+def test_exact_odd_roots(root, K, dt, wdt, fmt):
+    """K / root^2 ones in a row of zeros: 1 / rms = root, an odd number."""
+    ones = K // root ** 2
+    h = np.zeros((2, K))
+    h[0, :ones] = 1.0
+    h[1, K - ones:] = -4.0
+    v = magnitudes(fmt)
+    pts = np.concatenate([(v[1:] + v[:-1]) / 2, v])
+    pts = pts[(pts / root * 2 ** 9) % 1 == 0]        # w = pts / root has a few bits
+    w = np.resize(pts / root, K)
+    w[::7] = 2.0 * v[1]
+    wt = torch.from_numpy(w).to(wdt)
+    assert (wt.double().numpy() == w).all()
+    byte, code = exact(h, w, [Fraction(root), Fraction(root, 4)], fmt)
+    _, q = S.spec_rmsnorm_mx(torch.from_numpy(h).to(dt).to(DEV), wt.to(DEV), 0.0, fmt=fmt)
+    assert_same(q, byte, code)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_exact_root_of_other_elements(fmt):
+    """Rows with rms 2 whose elements are not powers of two, fp32 weights of 24 bits that bring
+    them to within 2^-24 of a midpoint, or onto it."""
+    h = np.array([5, 5, 2, 2, 1, 1, 1, 1, 1, 1, 0, 0, 0, 0, 0, 0] * 2, float)  # sum of squares 128
+    h = np.tile(h, 8)
+    v = magnitudes(fmt)
+    mid = (v[1:] + v[:-1]) / 2
+    w = np.zeros(h.size)
+    for i in range(h.size):
+        if h[i]:
+            w[i] = np.float32(mid[(7 * i) % len(mid)] * 2 / h[i])
+    w[::32] = np.float32(v[-1] * 2 / 5)
+    root = [Fraction(1, 2)]
+    byte, code = exact(h[None], w, root, fmt)
+    for dt in (F32, BF16):
+        _, q = S.spec_rmsnorm_mx(torch.from_numpy(h[None]).to(dt).to(DEV),
+                                 torch.from_numpy(w).float().to(DEV), 0.0, fmt=fmt)
+        assert_same(q, byte, code)
