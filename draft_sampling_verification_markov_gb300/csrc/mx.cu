@@ -410,10 +410,13 @@ __device__ __forceinline__ Piece<DT> add_pair(const NormArgs& a, int row, int k,
   return o;
 }
 
+// Sum of the squares of one piece times `pre`, a power of two.
 template <int DT>
-__device__ __forceinline__ float sum_squares(const Piece<DT>& p) {
+__device__ __forceinline__ float sum_squares(const Piece<DT>& p, float pre) {
   float h[8], s0 = 0.0f, s1 = 0.0f;
   unpack<DT>(p, h);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h[i] *= pre;
 #pragma unroll
   for (int i = 0; i < 8; i += 2) {
     s0 = fmaf(h[i], h[i], s0);
@@ -422,17 +425,27 @@ __device__ __forceinline__ float sum_squares(const Piece<DT>& p) {
   return s0 + s1;
 }
 
-// 1 / sqrt(sum / K + eps) as an unevaluated pair, from a sum known as a pair: the quotient with
-// its remainder, the exact sum with eps, and one Newton step from the hardware's reciprocal root
-// whose residual is formed with fused products. Everything in a row is scaled by this one number,
-// so its rounding would move every code of the row the same way. A sum that is not finite gives
-// NaN for the whole row.
-__device__ __forceinline__ DF inverse_rms(DF sum, float K, float inv_K, float eps) {
-  if (!(sum.hi < INFINITY)) return {NAN, 0.0f};
+// sum / K + eps as an unevaluated pair, from a sum known as a pair: the quotient with its
+// remainder and the exact sum with eps.
+__device__ __forceinline__ DF mean_square(DF sum, float K, float inv_K, float eps) {
   const float q = sum.hi * inv_K;
   const float ql = (fmaf(-q, K, sum.hi) + sum.lo) * inv_K;
-  DF v = two_sum(q, eps);
-  v = fast_two_sum(v.hi, v.lo + ql);
+  const DF v = two_sum(q, eps);
+  return fast_two_sum(v.hi, v.lo + ql);
+}
+
+// Squares leave fp32's range before their row does. Where v = mean(h^2) + eps overflows, or is so
+// small (below kLeast) that its squares may have lost bits, the sum is taken again over h times a
+// power of two, which then scales eps twice and the row's elements once. Shrunk, 2^24 squares
+// of at most 2^48 are finite, and a v that overflowed is 2^-80 at least. Grown, a v that was below
+// kLeast is below 2^97 and its sum below 2^121; the square of the least subnormal is 2^-102.
+constexpr float kShrink = 0x1p-80f, kGrow = 0x1p98f, kLeast = 0x1p-100f;
+
+// 1 / sqrt(v) as an unevaluated pair: one Newton step from the hardware's reciprocal root whose
+// residual is formed with fused products. Everything in a row is scaled by this one number, so its
+// rounding would move every code of the row the same way. NaN for a v that is not finite.
+__device__ __forceinline__ DF inverse_root(DF v) {
+  if (!(v.hi < INFINITY)) return {NAN, 0.0f};
   const float y = rsqrtf(v.hi);
   const float t = v.hi * y, te = fmaf(v.hi, y, -t);
   const float r = fmaf(-t, y, 1.0f) - (te + v.lo * y) * y;  // 1 - v y^2
@@ -456,12 +469,13 @@ __device__ __forceinline__ DF warp_sum_exact(float x) {
   return {s.hi * back, s.lo * back};
 }
 
-// The scale of a row: 1 / rms = (hi + lo) * two with `two` a power of two and hi in [1, 2).
+// The scale of a row: 1 / rms = (hi + lo) * two with `two` a power of two and hi in [1, 2), or a
+// factor `pre` other than 1 to take the row's squares with instead (lo is 0 then, too).
 // lo is 0 exactly where the root is a fraction with a power of two below: then
 // rms^2 = sum / K + eps = 4^j / m^2 with m odd, so m^2 divides K and m has 12 bits at most; a pair
 // that is such a number up to its own error (2^-45) is taken to be it.
-struct RowScale {
-  float hi, lo, two;
+struct alignas(16) RowScale {
+  float hi, lo, two, pre;
   RowScale() = default;
   __device__ __forceinline__ explicit RowScale(DF r) {
     const int e = (int)(__float_as_uint(r.hi) >> 23) - 127;  // a normal number, or NaN
@@ -471,6 +485,7 @@ struct RowScale {
     lo = r.lo * back;
     if (fabsf(lo) < 0x1p-42f && !(__float_as_uint(hi) & 0xfffu)) lo = 0.0f;
     if (!(r.hi < INFINITY)) hi = NAN, two = 1.0f;
+    pre = 1.0f;
   }
 };
 
@@ -479,35 +494,30 @@ struct RowScale {
 // the product; rounding to the nearest fp32 in between meets a midpoint of the format about once
 // in 2^20 elements and may then go the wrong way. The power of two comes first: h * two is exact,
 // and of the size of the result. EXACT: the product with the weight has no rounding error (two
-// bf16 numbers). REST: the product may have no rest, which takes its own look; otherwise (lo is
-// not 0: the root is no fraction with a power of two below) it always has one.
+// bf16 numbers). REST: the product may have no rest, which takes its own look; where lo is not 0
+// (the root is no fraction with a power of two below) it always has one.
 template <bool EXACT, bool REST>
 __device__ __forceinline__ float scaled(float h, const RowScale& r, float w) {
   const float g = h * r.two, p = g * w;
   float low = p * r.lo;
   if (!EXACT) low = fmaf(fmaf(g, w, -p), r.hi, low);
   const float y = __fmaf_rz(p, r.hi, low);
-  const bool rest = !REST || fmaf(p, r.hi, -y) + low != 0.0f;
+  const bool rest = !REST || r.lo != 0.0f || fmaf(p, r.hi, -y) + low != 0.0f;
   return __uint_as_float(__float_as_uint(y) | (rest ? 1u : 0u));
 }
 
 // The products of eight elements from k of a row of K, 0 past K.
-template <bool EXACT>
+template <bool EXACT, bool REST>
 __device__ __forceinline__ void scale8(float (&h)[8], const RowScale& r, const float (&w)[8], int k,
                                        int K) {
-  if (r.lo != 0.0f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = k + i < K ? scaled<EXACT, false>(h[i], r, w[i]) : 0.0f;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = k + i < K ? scaled<EXACT, true>(h[i], r, w[i]) : 0.0f;
-  }
+  for (int i = 0; i < 8; ++i) h[i] = k + i < K ? scaled<EXACT, REST>(h[i], r, w[i]) : 0.0f;
 }
 
-// The scale of a row from each thread's sum of squares: fp32 within a warp, exact additions over
-// the warps. One warp does what is the same for all (done by every thread it was most of the
-// kernel's instructions). blockDim.x is a multiple of 32.
-__device__ __forceinline__ RowScale row_scale(float x, const NormArgs& a) {
+// The scale of a row from each thread's sum of squares (of elements times `pre`): fp32 within a
+// warp, exact additions over the warps. One warp does what is the same for all (done by every
+// thread it was most of the kernel's instructions). blockDim.x is a multiple of 32.
+__device__ __forceinline__ RowScale row_scale(float x, const NormArgs& a, float pre) {
   __shared__ float part[32];
   __shared__ RowScale scale;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -516,7 +526,12 @@ __device__ __forceinline__ RowScale row_scale(float x, const NormArgs& a) {
   __syncthreads();
   if (warp == 0) {
     const DF sum = warp_sum_exact(lane < (int)(blockDim.x >> 5) ? part[lane] : 0.0f);
-    const RowScale rs(inverse_rms(sum, (float)a.K, a.inv_K, a.eps));
+    const DF v = mean_square(sum, (float)a.K, a.inv_K, a.eps * pre * pre);
+    RowScale rs(inverse_root(v));
+    if (pre == 1.0f && !(v.hi >= kLeast && v.hi < INFINITY)) {
+      rs.pre = v.hi < kLeast ? kGrow : kShrink;
+      rs.lo = 0.0f;
+    }
     if (lane == 0) scale = rs;
   }
   __syncthreads();  // after it a next call may write `part`, but not yet `scale`
@@ -561,11 +576,20 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(NormArgs a) {
       h = add_pair<DT>(a, row, k, next);
       if (row + blocks < a.rows) load_pair<DT>(a, row + blocks, k, next);
     }
-    const RowScale rs = row_scale(sum_squares<DT>(h), a);
+    RowScale rs = row_scale(sum_squares<DT>(h, 1.0f), a, 1.0f);
     float y[8], v[8];
     unpack<DT>(h, y);
     unpack<WDT>(w, v);
-    scale8<kExact>(y, rs, v, k, a.K);
+    if (rs.lo != 0.0f) {  // the same in all threads
+      scale8<kExact, false>(y, rs, v, k, a.K);
+    } else {
+      if (const float pre = rs.pre; pre != 1.0f) {
+        rs = row_scale(sum_squares<DT>(h, pre), a, pre);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] *= pre;
+      }
+      scale8<kExact, true>(y, rs, v, k, a.K);
+    }
     finite &= quantize8<FMT>(y, k < Kp,
                              a.codes + ((size_t)row * G * kGroup + k) / 8 * kLaneCode<FMT>,
                              a.scales + scale_word(row, k / kGroup, G));
@@ -585,13 +609,18 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(NormArgs a) {
   }
   NormArgs sum_only = a;
   sum_only.res_out = nullptr;
-  DF sum = df_zero();  // a chain of K / 8192 pieces: exact additions
-  for (int k = 8 * threadIdx.x; k < a.K; k += step) {
-    Pair<DT> p;
-    load_pair<DT>(a, row, k, p);
-    sum = df_add(sum, sum_squares<DT>(add_pair<DT>(sum_only, row, k, p)));
-  }
-  const RowScale rs = row_scale(df_float(sum), a);
+  auto scale_of = [&](float pre) {
+    DF sum = df_zero();  // a chain of K / 8192 pieces: exact additions
+    for (int k = 8 * threadIdx.x; k < a.K; k += step) {
+      Pair<DT> p;
+      load_pair<DT>(a, row, k, p);
+      sum = df_add(sum, sum_squares<DT>(add_pair<DT>(sum_only, row, k, p), pre));
+    }
+    return row_scale(df_float(sum), a, pre);
+  };
+  RowScale rs = scale_of(1.0f);
+  const float pre = rs.pre;
+  if (pre != 1.0f) rs = scale_of(pre);  // the same in all threads
   uint8_t* codes = a.codes + (size_t)row * G * kGroupCode<FMT>;
   bool finite = true;
   for (int k0 = 0; k0 < Kp; k0 += step) {
@@ -602,9 +631,16 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(NormArgs a) {
       Piece<WDT> w;
       load_pair<DT>(a, row, k, p);
       unpack<DT>(add_pair<DT>(a, row, k, p), h);
+      if (pre != 1.0f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] *= pre;
+      }
       load8<WDT, true>(a.weight, 0, k, a.K, a.wvec, w);
       unpack<WDT>(w, v);
-      scale8<kExact>(h, rs, v, k, a.K);
+      if (rs.lo != 0.0f)
+        scale8<kExact, false>(h, rs, v, k, a.K);
+      else
+        scale8<kExact, true>(h, rs, v, k, a.K);
     }
     finite &= quantize8<FMT>(h, k < Kp, codes + k / 8 * kLaneCode<FMT>,
                              a.scales + scale_word(row, k / kGroup, G));

@@ -149,3 +149,69 @@ def test_exact_root_of_other_elements(fmt):
         _, q = S.spec_rmsnorm_mx(torch.from_numpy(h[None]).to(dt).to(DEV),
                                  torch.from_numpy(w).float().to(DEV), 0.0, fmt=fmt)
         assert_same(q, byte, code)
+
+
+# ------------------------------------------------------------------------------ range of the rows
+
+# 1 / rms from a sum in fp32 within a thread and a warp. A square passes at most 4 roundings in its
+# thread's chain, 1 that joins two chains, 5 in its warp and, in rows above 8192, 1 of the thread's
+# pair; across warps the sum is exact to 2^-42. The root halves the relative error of the sum.
+NORM_REL = (0.5 * 11 + 0.01) * ref.U32
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("K", [40, 1000, 8192, 9000])
+def test_rows_whose_squares_leave_fp32(K, dt, fmt):
+    """Rows of 1e-38 to 1e38, one large element among small ones, and an eps of their size."""
+    g = torch.Generator().manual_seed(K)
+    base = torch.randn(12, K, generator=g)
+    base = base.clamp(-3, 3) + 0.01
+    size = torch.tensor([1e38, 1e30, 3e19, 1.5e19, 1e-12, 1e-16, 1e-20, 1e-25, 1e-30, 1e-36, 1.0,
+                         1e-37])[:, None]
+    x = (base * size).to(dt)
+    x[8, 1:] *= 1e-6                                 # one element of 1e-30, the others far below
+    x[3, K // 2] = 2e38
+    w = (1 + 0.2 * torch.randn(K, generator=g)).to(dt)
+    assert torch.isfinite(x).all()
+    for eps in (0.0, float(np.float32(1e-34)), float(np.float32(1e-6)), 1e30):
+        # further rows would have products below fp32's normal range
+        rows = x if eps == 0 else x[:6] if eps > 1 else x[:8]
+        ws = S.Workspace(256, device=DEV)
+        _, q = S.spec_rmsnorm_mx(rows.to(DEV), w.to(DEV), eps, fmt=fmt, workspace=ws)
+        h = rows.double().numpy()
+        y = h / np.sqrt((h * h).mean(1, keepdims=True) + float(np.float32(eps)))
+        y = y * w.double().numpy()
+        got = ref.dequantize(q.codes.cpu(), q.scales.cpu(), fmt, K)
+        assert np.isfinite(got).all() and ws.status() == 0
+        ref.check_rounded(got, q.scales.cpu(), fmt, y, NORM_REL)
+
+
+@pytest.mark.parametrize("K", [256, 9216])
+def test_exact_products_of_extreme_rows(K):
+    """One power of two a row, subnormals and the largest among them: the codes of its weights."""
+    n = [127, 70, -55, -110, -126, -133, -149]
+    h = 2.0 ** np.array(n, float)[:, None] * np.random.default_rng(1).choice([-1.0, 1.0],
+                                                                             (len(n), K))
+    w = border_weights(ref.E4M3, K, 0.25)
+    byte, code = exact(h, w, [Fraction(2) ** -e for e in n], ref.E4M3)
+    _, q = S.spec_rmsnorm_mx(torch.from_numpy(h).float().to(DEV),
+                             torch.from_numpy(w).float().to(DEV), 0.0)
+    assert_same(q, byte, code)
+
+
+@pytest.mark.parametrize("K", [256, 9216])
+def test_rows_without_a_scale(K):
+    """A row of zeros is 0 with any eps above 0 and NaN without; rows beside it are not touched by
+    its second sum, nor by that of rows with a NaN or an infinity."""
+    x = torch.randn(6, K, generator=torch.Generator().manual_seed(3))
+    x[1] = 0.0
+    x[2, 5], x[3, 7], x[4, 9] = float("nan"), float("inf"), -float("inf")
+    x[5] *= 1e30
+    for eps, zero in ((0.0, False), (1e-45, True), (1e-33, True)):
+        ws = S.Workspace(256, device=DEV)
+        _, q = S.spec_rmsnorm_mx(x.to(DEV), torch.ones(K, device=DEV), eps, workspace=ws)
+        y = S.spec_mx_dequantize(q, dtype=torch.float32, workspace=ws).cpu()
+        assert torch.isnan(y[2:5]).all() and torch.isfinite(y[[0, 5]]).all()
+        assert (y[1] == 0).all() if zero else torch.isnan(y[1]).all()
+        assert ws.status() == S.SPEC_DEV_NONFINITE
