@@ -166,7 +166,7 @@ __device__ __forceinline__ float max_abs8(const float (&x)[8]) {
                      max_abs_nan(max_abs_nan(x[4], x[5]), max_abs_nan(x[6], x[7])));
 }
 
-// Quantises this lane's eight elements (element 8 * (lane % 16) of a group): stores its codes at
+// Quantises this lane's eight products of the norm (element 8 * (lane % 16) of a group): stores its codes at
 // `codes` and, from the group's first lane, the scale word at `scale`. All 32 lanes call it;
 // `live` masks the stores. Returns whether the block was finite.
 template <int FMT>
@@ -176,7 +176,8 @@ __device__ __forceinline__ bool quantize8(const float (&x)[8], bool live, uint8_
   uint32_t amax = __float_as_uint(max_abs8(x)) & 0x7fffffffu;
   amax = max(amax, __shfl_xor_sync(kFull, amax, 1));
   amax = max(amax, __shfl_xor_sync(kFull, amax, 2));
-  const int sb = scale_byte<FMT>(amax);
+  // a product that passes fp32 was truncated to its largest number
+  const int sb = amax == 0x7f7fffffu ? kNanScale : scale_byte<FMT>(amax);
   const bool finite = sb != kNanScale;
   // four block bytes -> one word in the group's first lane
   uint32_t word = (uint32_t)sb << (8 * ((threadIdx.x >> 2) & 3));

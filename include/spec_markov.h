@@ -476,7 +476,8 @@ int spec_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int fmt, int
  *                 ignored). May be x or residual itself; must not overlap them otherwise.
  *   fmt           of codes / scales.
  * A row with an infinity or a NaN sets SPEC_DEV_NONFINITE and has NaN scales, as has a row of zeros
- * with eps = 0. Rows whose squares pass fp32's range are normalised like others.
+ * with eps = 0. So has a block with a y that passes fp32's largest number (to its last bit). Rows
+ * whose squares pass fp32's range are normalised like others.
  */
 int spec_rmsnorm_mx(const void* x, long long ldx, const void* residual, long long ldr, int dtype,
                     const void* weight, int w_dtype, float eps, int rows, int K,

@@ -215,3 +215,25 @@ def test_rows_without_a_scale(K):
         assert torch.isnan(y[2:5]).all() and torch.isfinite(y[[0, 5]]).all()
         assert (y[1] == 0).all() if zero else torch.isnan(y[1]).all()
         assert ws.status() == S.SPEC_DEV_NONFINITE
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("K", [288, 9216])
+@pytest.mark.parametrize("wdt", [F32, BF16])
+def test_products_beyond_fp32(K, wdt, fmt):
+    """Finite rows and weights whose product passes fp32's largest number: that block is NaN, those
+    beside it are not."""
+    x = torch.zeros(2, K)
+    x[0, :32 * (K // 288)] = 1.0                     # 1 / rms = 3
+    x[1] = torch.randn(K, generator=torch.Generator().manual_seed(1)).clamp(-2, 2)
+    x[1, 40] = 2.0
+    w = torch.ones(K)
+    w[[5, 40]] = torch.tensor([1.2e38, 2.5e38])
+    ws = S.Workspace(256, device=DEV)
+    _, q = S.spec_rmsnorm_mx(x.to(DEV), w.to(wdt).to(DEV), 0.0, fmt=fmt, workspace=ws)
+    h, w64 = x.double().numpy(), w.to(wdt).double().numpy()
+    y = h / np.sqrt((h * h).mean(1, keepdims=True)) * w64
+    bad = (np.abs(y) >= 2.0 ** 128).reshape(2, -1, 32).any(2)
+    assert bad[0, 0] and bad[1, 1] and bad.sum() <= 3
+    np.testing.assert_array_equal(stored(q, K)[0] == 255, bad)
+    assert ws.status() == S.SPEC_DEV_NONFINITE
