@@ -649,13 +649,13 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(NormArgs a) {
   if (!finite) atomicOr(a.status, SPEC_DEV_NONFINITE);
 }
 
-// Blocks of a kernel that are resident at once, by its warps a block (they loop over the rest).
+// Blocks of a kernel that an SM holds at once.
 template <typename K>
-int resident(K k, int threads) {
+int blocks_per_sm(K k, int threads) {
   int n = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, threads, 0) != cudaSuccess || n < 1)
     n = 1;
-  return n * num_sms();
+  return n;
 }
 
 // Blocks of a streaming kernel: one for each of its units. Loops over fewer, resident blocks were
@@ -689,9 +689,11 @@ void launch_norm_t(const NormArgs& a, cudaStream_t s) {
     return;
   }
   auto k = rmsnorm_kernel<DT, WDT, FMT>;
-  static int most[33] = {};  // resident blocks by warps of a block
-  int n = __atomic_load_n(&most[threads / 32], __ATOMIC_RELAXED);
-  if (!n) __atomic_store_n(&most[threads / 32], n = resident(k, threads), __ATOMIC_RELAXED);
+  // by warps of a block; devices differ in their number of SMs
+  static int per_sm[33] = {};
+  int n = __atomic_load_n(&per_sm[threads / 32], __ATOMIC_RELAXED);
+  if (!n) __atomic_store_n(&per_sm[threads / 32], n = blocks_per_sm(k, threads), __ATOMIC_RELAXED);
+  n *= num_sms();  // they loop over the rest of the rows
   const int blocks = a.rows < n ? a.rows : n;
   launch_kernel(k, blocks + 1, threads, 0, s, true, a);
 }
