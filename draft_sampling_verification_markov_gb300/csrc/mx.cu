@@ -516,7 +516,8 @@ __device__ __forceinline__ void scale8(float (&h)[8], const RowScale& r, const f
 }
 
 // The scale of a row from each thread's sum of squares (of elements times `pre`): fp32 within a
-// warp, exact additions over the warps. One warp does what is the same for all (done by every
+// warp (10 roundings, which put 1 to 3 of the 35.7 million codes of 17408 x 2048 random elements a
+// step off those of the exact root), exact over the warps. One warp does what is the same for all (done by every
 // thread it was most of the kernel's instructions). blockDim.x is a multiple of 32.
 __device__ __forceinline__ RowScale row_scale(float x, const NormArgs& a, float pre) {
   __shared__ float part[32];

@@ -1,6 +1,7 @@
 """Codes and scales of the residual RMS norm, element by element, against exact arithmetic: products
 that are exact, and products next to the formats' midpoints."""
 from fractions import Fraction
+from math import isqrt
 
 import numpy as np
 import pytest
@@ -151,13 +152,79 @@ def test_exact_root_of_other_elements(fmt):
         assert_same(q, byte, code)
 
 
-# ------------------------------------------------------------------------------ range of the rows
+# ------------------------------------------------------------------------------ rounded once
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("K", [96, 992, 4096, 9216])
+def test_products_next_to_midpoints(K, dt, fmt):
+    """Rows of small whole numbers, whose sum of squares is exact in fp32, with an irrational root:
+    1 / rms is known to 2^-44 (the pair's Newton step and its sums). The weights are the fp32
+    numbers that bring every product to within 2^-24 of a midpoint of the format, where a product
+    rounded to fp32 first lands on the midpoint and the tie may go the wrong way."""
+    rng = np.random.default_rng(K + fmt)
+    h = rng.integers(1, 4, K).astype(float)
+    total = int((h * h).sum())
+    assert total < 2 ** 24 and isqrt(total * K) ** 2 != total * K
+    root = Fraction(isqrt(2 ** 240 * K * total), 2 ** 120 * total)  # sqrt(K / total) to 2^-110
+    v = magnitudes(fmt)
+    mid = (v[1:] + v[:-1]) / 2
+    sign = rng.choice([-1.0, 1.0], K)
+    w = np.zeros(K)
+    for i in range(K):
+        at = v[-1] * 0.97 if i % 32 == 0 else mid[rng.integers(len(mid))] * sign[i]
+        w[i] = np.float32(at / (h[i] * float(root)))
+    byte, code = exact(h[None], w, [root], fmt)
+    # none within the root's error of a midpoint, so every code is decided
+    a = h * np.abs(w) * float(root) / 2.0 ** (np.repeat(byte[0], 32) - 127.0)
+    close = mid[np.abs(a[:, None] / mid - 1).argmin(1)]
+    near = min(abs(Fraction(x) * Fraction(abs(y)) * root / Fraction(2) ** int(e - 127) /
+                   Fraction(m) - 1)
+               for x, y, e, m in zip(h, w, np.repeat(byte[0], 32), close))
+    assert near > Fraction(1, 2 ** 42)
+    _, q = S.spec_rmsnorm_mx(torch.from_numpy(h[None]).to(dt).to(DEV),
+                             torch.from_numpy(w).float().to(DEV), 0.0, fmt=fmt)
+    assert_same(q, byte, code)
+
 
 # 1 / rms from a sum in fp32 within a thread and a warp. A square passes at most 4 roundings in its
 # thread's chain, 1 that joins two chains, 5 in its warp and, in rows above 8192, 1 of the thread's
 # pair; across warps the sum is exact to 2^-42. The root halves the relative error of the sum.
 NORM_REL = (0.5 * 11 + 0.01) * ref.U32
 
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dt,wdt", [(BF16, BF16), (F32, F32), (BF16, F32)])
+@pytest.mark.parametrize("rows,K", [(300, 96), (200, 992), (130, 4096), (64, 8192), (9, 16384)])
+def test_codes_of_random_rows(rows, K, dt, wdt, fmt):
+    """Codes and scales are those of the exact product, but for products that lie within the
+    root's own error of a midpoint or, for the scale, of the format's largest value."""
+    g = torch.Generator().manual_seed(rows + K)
+    x, r = torch.randn(rows, K, generator=g).to(dt), (3 * torch.randn(rows, K, generator=g)).to(dt)
+    w = (1 + 0.2 * torch.randn(K, generator=g)).to(wdt)
+    eps = float(np.float32(1e-5))
+    h, q = S.spec_rmsnorm_mx(x.to(DEV), w.to(DEV), eps, residual=r.to(DEV), fmt=fmt)
+    h = h.cpu().double().numpy()
+    y = h / np.sqrt((h * h).mean(1, keepdims=True) + eps) * w.double().numpy()
+    byte, code = stored(q, K)
+    # scales: the least that fits, at both ends of the error
+    amax = np.abs(y).reshape(rows, -1, 32).max(2) / ref.TOP[fmt]
+    lo = 127 + np.ceil(np.log2(amax * (1 - NORM_REL))).astype(int)
+    hi = 127 + np.ceil(np.log2(amax * (1 + NORM_REL))).astype(int)
+    assert ((lo <= byte) & (byte <= hi)).all() and (lo != hi).sum() <= 2
+    # codes: the number of midpoints below, at both ends of the error
+    v = magnitudes(fmt)
+    mid = (v[1:] + v[:-1]) / 2
+    a = np.abs(y) / 2.0 ** (np.repeat(byte, 32, 1) - 127.0)
+    least, most = (np.searchsorted(mid, a * (1 + s * NORM_REL)) for s in (-1, 1))
+    got = code & (7 if fmt == ref.E2M1 else 127)
+    assert ((least <= got) & (got <= most)).all()
+    assert (least != most).mean() < 1e-4                # and nearly all have no choice
+    sign = code >= (8 if fmt == ref.E2M1 else 128)
+    assert (sign == ((y < 0) & (got > 0))).all()
+
+
+# ------------------------------------------------------------------------------ range of the rows
 
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("dt", [F32, BF16])
