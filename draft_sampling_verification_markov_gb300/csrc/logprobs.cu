@@ -19,7 +19,7 @@
 // shared memory: no workspace, one launch.
 //
 // Measured (V = 129280): 2048 bf16 rows 87 us without alternatives (6.1 TB/s), 105 us with 20 (5.1
-// TB/s), 256 rows 21 us, one row 7.4 us; 1024 fp32 rows with 20 95 us (5.6 TB/s). Without
+// TB/s), 256 rows 21 us, one row 7.7 us; 1024 fp32 rows with 20 95 us (5.6 TB/s). Without
 // alternatives memory bounds it. With them each row takes 41 instead of 33 thousand warp
 // instructions, and an SM issues in 64 % of its cycles; half of the difference is the lists, half
 // the row's end. Prefetching the next row into L2 during that end is slower (107 to 111 us).
@@ -830,8 +830,8 @@ cudaError_t launch_token_logprobs(const LogprobArgs& a, int dt, cudaStream_t s) 
   TraceScope ts(SPEC_KCLASS_OTHER, s);
   // A CTA has some 5 us of latencies outside its stream of logits, more in a cluster: rows are
   // split while the parts still find SMs of their own and have a batch or more. 129280 bf16
-  // logits, top 20, us at splits of 1 / 2 / 4 / 8: 1 row 15 / 11 / 8.6 / 7.8, 64 rows 19 / 14 / 12
-  // / 14, 128 rows 19 / 17 / 18 / 25, 256 rows 24 / 25 / 31 / 44.
+  // logits, top 20, us at splits of 1 / 2 / 4 / 8: 1 row 12.8 / 10.9 / 8.6 / 7.8, 64 rows 15.1 /
+  // 13.3 / 11.9 / 14.0, 128 rows 15.8 / 15.7 / 17.2 / 24.9, 256 rows 21.0 / 23.1 / 28.0 / 42.8.
   const int batch = kThreads * kBatch * (dt == SPEC_BF16 ? 8 : 4);
   int split = 1;
   while (split < kMaxSplit && (long long)a.rows * split <= num_sms() &&
