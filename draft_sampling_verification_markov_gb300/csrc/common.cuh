@@ -55,6 +55,27 @@ __device__ __forceinline__ uint4 ld_stream16(const void* p) {
   return r;
 }
 
+// The same two through the coherent path, for what may have been written since the kernel began: by
+// the kernel itself, or by the kernel before it where that is no kernel of the same call (a chained
+// kernel's blocks start while it still runs; the read-only path asks for memory that nobody writes
+// from then on).
+template <int DT>
+__device__ __forceinline__ float ld_elem_coherent(const void* p, size_t i) {
+  if constexpr (DT == SPEC_BF16) {
+    return bf16_to_f32(reinterpret_cast<const uint16_t*>(p)[i]);
+  } else {
+    return reinterpret_cast<const float*>(p)[i];
+  }
+}
+__device__ __forceinline__ uint4 ld_coherent16(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+
 // exp2 on the MUFU pipe (ex2.approx, flush-to-zero): max relative error ~2^-22.
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;

@@ -177,9 +177,10 @@ bool trace_active();
 // first are chained, so what a chained kernel reads before its wait (inputs of the call that
 // no kernel of the call writes) was finished before the call's first kernel began. The calls of
 // the vocabulary head and the token log-probabilities are one kernel each, chained to whatever
-// is before it on the stream: nothing outside the SM is touched before its wait. One after the
-// other without a graph, a norm of 2048 x 4096 and its read-back take 16.9 instead of 22.5 us,
-// the product of 4 rows with 32000 tokens 10.3 instead of 12.3.
+// is before it on the stream: nothing outside the SM is touched before its wait, and what the
+// kernel before may have written is read through the coherent path. One after the other without a
+// graph, a norm of 2048 x 4096 and its read-back take 16.9 instead of 22.5 us, the product of 4
+// rows with 32000 tokens 10.3 instead of 12.3.
 template <typename... P, typename... A>
 cudaError_t launch_kernel(void (*k)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                           bool chained, A&&... args) {

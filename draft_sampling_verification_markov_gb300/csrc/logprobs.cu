@@ -154,7 +154,7 @@ struct Row {
     uint4 q = make_uint4(kNone, kNone, kNone, kNone);
     if (j < end) {
       const int v = j * N - head;
-      if (v >= 0 && v + N <= V) q = ld_stream16(base + (size_t)j * 16);
+      if (v >= 0 && v + N <= V) q = ld_coherent16(base + (size_t)j * 16);
     }
     return q;
   }
@@ -169,11 +169,10 @@ struct Row {
     for (int i = 0; i < N; ++i) {
       if (v + i < 0 || v + i >= V) continue;
       if constexpr (DT == SPEC_BF16) {
-        const uint32_t b =
-            __ldg(reinterpret_cast<const unsigned short*>(base + (size_t)j * 16) + i);
+        const uint32_t b = reinterpret_cast<const uint16_t*>(base + (size_t)j * 16)[i];
         w[i / 2] = i & 1 ? (w[i / 2] & 0xffffu) | b << 16 : (w[i / 2] & 0xffff0000u) | b;
       } else {
-        w[i] = __ldg(reinterpret_cast<const uint32_t*>(base + (size_t)j * 16) + i);
+        w[i] = reinterpret_cast<const uint32_t*>(base + (size_t)j * 16)[i];
       }
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
@@ -192,7 +191,7 @@ __device__ __forceinline__ void Row<DT>::load_batch(uint4 (&q)[B], int jb, int e
   if (jb * N >= head && jb + B * kThreads <= end && (jb + B * kThreads) * N - head <= V) {
     const char* p = base + (size_t)j * 16;
 #pragma unroll
-    for (int b = 0; b < B; ++b) q[b] = ld_stream16(p + b * kThreads * 16);
+    for (int b = 0; b < B; ++b) q[b] = ld_coherent16(p + b * kThreads * 16);
   } else {
 #pragma unroll
     for (int b = 0; b < B; ++b) q[b] = load(j + b * kThreads, end);
@@ -666,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, ctas(D)) logprobs_kernel(const Logpr
     const int j0 = part * per, j1 = min(np, j0 + per);
     if (!skip) {
       const bool bad = t < 0 || t >= a.V;
-      const float xt = bad || !a.tokens ? INFINITY : ld_elem<DT>(a.x, (size_t)row * a.ld + t);
+      const float xt = bad || !a.tokens ? INFINITY : ld_elem_coherent<DT>(a.x, (size_t)row * a.ld + t);
       float bound = INFINITY;
       if (TOP) {
         if (tid == 0) {

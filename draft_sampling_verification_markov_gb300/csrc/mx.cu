@@ -4,7 +4,8 @@
 // Work split. Consecutive lanes hold a 128-element group of one row, eight elements each (sixteen
 // in the quantiser): four (two) lanes are a block, whose largest magnitude is two (one) shuffles
 // away, and the group's four scales are one 32-bit store. A warp's loads and code stores are
-// contiguous. A thread has 64 bytes in flight: with 16 the kernels waited on memory.
+// contiguous. A thread has 64 bytes in flight: with 16 the kernels waited on memory. Loads go
+// through the coherent path (common.cuh says why).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -26,36 +27,13 @@ constexpr int kUnroll = DT == SPEC_BF16 ? 2 : 1;
 constexpr int kUnrollBack = 4;
 constexpr uint32_t kFull = 0xffffffffu;
 
-// Streaming 16-byte load from memory that the same kernel may also write (the coherent path).
-__device__ __forceinline__ uint4 ld_coherent16(const void* p) {
-  uint4 r;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p)
-               : "memory");
-  return r;
-}
-
-// Streaming (read-once) 32-byte load.
-__device__ __forceinline__ void ld_stream32(const void* p, uint4& a, uint4& b) {
-  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+// ld_coherent16 of 32 bytes.
+__device__ __forceinline__ void ld_coherent32(const void* p, uint4& a, uint4& b) {
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z),
                  "=r"(b.w)
-               : "l"(p));
-}
-
-template <bool RO>
-__device__ __forceinline__ uint4 ld16(const void* p) {
-  return RO ? ld_stream16(p) : ld_coherent16(p);
-}
-
-template <int DT, bool RO>
-__device__ __forceinline__ float ld1(const void* p, size_t i) {
-  if constexpr (RO) return ld_elem<DT>(p, i);
-  if constexpr (DT == SPEC_BF16)
-    return bf16_to_f32(*(reinterpret_cast<const volatile uint16_t*>(p) + i));
-  else
-    return *(reinterpret_cast<const volatile float*>(p) + i);
+               : "l"(p)
+               : "memory");
 }
 
 // Eight consecutive elements as they are stored.
@@ -70,21 +48,26 @@ __device__ __forceinline__ void clear(Piece<DT>& p) {
   for (uint4& q : p.q) q = make_uint4(0, 0, 0, 0);
 }
 
-// Elements v .. v + 7 of a row of K (zero past K); 16-byte loads when `vec`. RO: the memory is
-// not written while the kernel runs (the read-only path may serve it).
-template <int DT, bool RO>
+// Elements v .. v + 7 of a row of K (zero past K); 16-byte loads when `vec`, kept in L1 when SHARED
+// (other blocks of the SM read them too).
+template <int DT, bool SHARED = false>
 __device__ __forceinline__ void load8(const void* base, size_t off, int v, int K, bool vec,
                                       Piece<DT>& p) {
   constexpr size_t es = DT == SPEC_BF16 ? 2 : 4;
   const char* at = static_cast<const char*>(base) + (off + v) * es;
   if (vec && v + 8 <= K) {
 #pragma unroll
-    for (int i = 0; i < (int)es / 2; ++i) p.q[i] = ld16<RO>(at + 16 * i);
+    for (int i = 0; i < (int)es / 2; ++i) {
+      if constexpr (SHARED)
+        p.q[i] = *reinterpret_cast<const uint4*>(at + 16 * i);
+      else
+        p.q[i] = ld_coherent16(at + 16 * i);
+    }
   } else {
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      w[i] = v + i < K ? __float_as_uint(ld1<DT, RO>(base, off + v + i)) : 0u;
+      w[i] = v + i < K ? __float_as_uint(ld_elem_coherent<DT>(base, off + v + i)) : 0u;
     if constexpr (DT == SPEC_BF16) {  // an element's bits are the upper half of its fp32's
       p.q[0] = make_uint4(w[0] >> 16 | w[1], w[2] >> 16 | w[3], w[4] >> 16 | w[5],
                           w[6] >> 16 | w[7]);
@@ -231,14 +214,14 @@ __device__ __forceinline__ void load16(const void* base, size_t off, int v, int 
   if (vec == 2 && v + 16 <= K) {
     const char* at = static_cast<const char*>(base) + (off + v) * es;
     if constexpr (DT == SPEC_BF16) {
-      ld_stream32(at, p[0].q[0], p[1].q[0]);
+      ld_coherent32(at, p[0].q[0], p[1].q[0]);
     } else {
-      ld_stream32(at, p[0].q[0], p[0].q[1]);
-      ld_stream32(at + 32, p[1].q[0], p[1].q[1]);
+      ld_coherent32(at, p[0].q[0], p[0].q[1]);
+      ld_coherent32(at + 32, p[1].q[0], p[1].q[1]);
     }
   } else {
-    load8<DT, true>(base, off, v, K, vec > 0, p[0]);
-    load8<DT, true>(base, off, v + 8, K, vec > 0, p[1]);
+    load8<DT>(base, off, v, K, vec > 0, p[0]);
+    load8<DT>(base, off, v + 8, K, vec > 0, p[1]);
   }
 }
 
@@ -315,7 +298,8 @@ __global__ void __launch_bounds__(kThreads)
 
 // ------------------------------------------------------------------------------ read back
 
-// 129280 x 4096 E2M1 to bf16: 213 us, 6.3 TB/s of codes read and values written.
+// 129280 x 4096 E2M1 to bf16: 202 us, 6.6 TB/s of codes read and values written (213 us with loads
+// through the read-only path).
 template <int DT, int FMT>
 __global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint8_t* codes,
                                                               const uint8_t* scales, int rows,
@@ -342,10 +326,10 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint8_t* cod
     if (u.row >= rows) continue;
     const uint8_t* at = p + (size_t)i * kUnits * kGroupCode<FMT>;
     if constexpr (FMT == SPEC_MX_E2M1)
-      c[i].x = __ldg(reinterpret_cast<const uint32_t*>(at));
+      c[i].x = *reinterpret_cast<const uint32_t*>(at);
     else
-      c[i] = __ldg(reinterpret_cast<const uint2*>(at));
-    sb[i] = __ldg(scales + scale_word(u.row, u.g, G) + (l >> 2));
+      c[i] = *reinterpret_cast<const uint2*>(at);
+    sb[i] = scales[scale_word(u.row, u.g, G) + (l >> 2)];
   }
 #pragma unroll
   for (int i = 0; i < U; ++i) {
@@ -391,8 +375,8 @@ struct Pair {
 
 template <int DT>
 __device__ __forceinline__ void load_pair(const NormArgs& a, int row, int k, Pair<DT>& p) {
-  load8<DT, false>(a.x, (size_t)row * a.ldx, k, a.K, a.vec, p.x);
-  if (a.res) load8<DT, false>(a.res, (size_t)row * a.ldr, k, a.K, a.vec, p.r);
+  load8<DT>(a.x, (size_t)row * a.ldx, k, a.K, a.vec, p.x);
+  if (a.res) load8<DT>(a.res, (size_t)row * a.ldr, k, a.K, a.vec, p.r);
 }
 
 // h of one piece, as it is stored: x, or x + residual rounded to the type (and stored).
@@ -550,7 +534,7 @@ __device__ __forceinline__ void clear_missing(const NormArgs& a, int G) {
 // A block takes rows in turn, each in registers (eight elements a thread), and loads the next one
 // while it works on a row: the block's sum and what follows it would leave the memory idle
 // otherwise. The weight stays in registers. The last block clears the missing rows' scales. With a
-// residual: 17408 x 2048 fp32 75.5 us (6.2 TB/s), 2048 x 4096 bf16 13.4 us (4.4 TB/s: two block
+// residual: 17408 x 2048 fp32 73 us (6.4 TB/s), 2048 x 4096 bf16 13.4 us (4.4 TB/s: two block
 // barriers and a root each row), one row of 4096 3.2 us.
 template <int DT, int WDT, int FMT>
 __global__ void __launch_bounds__(1024) rmsnorm_kernel(NormArgs a) {
@@ -601,9 +585,10 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(NormArgs a) {
 }
 
 // Rows too long for registers, one block each: read twice (the second time from cache), which with
-// one row at a time bounds it: 1024 x 16384 bf16 with a residual 35.8 us (3.3 TB/s), one row 9.4 us.
+// one row at a time bounds it: 1024 x 16384 bf16 with a residual 35.2 us (3.4 TB/s; with one block an
+// SM, above 32 registers a thread, 44), 512 x 16384 fp32 34.0 us, one row 9.4 us.
 template <int DT, int WDT, int FMT>
-__global__ void __launch_bounds__(1024) rmsnorm_long_kernel(NormArgs a) {
+__global__ void __launch_bounds__(1024, 2) rmsnorm_long_kernel(NormArgs a) {
   constexpr bool kExact = DT == SPEC_BF16 && WDT == SPEC_BF16;
   const int G = groups(a.K), Kp = G * kGroup, row = blockIdx.x, step = 8 * blockDim.x;
   grid_dep_wait();
@@ -634,12 +619,12 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(NormArgs a) {
       Pair<DT> p;
       Piece<WDT> w;
       load_pair<DT>(a, row, k, p);
+      load8<WDT, true>(a.weight, 0, k, a.K, a.wvec, w);  // before the sum's store: no wait between
       unpack<DT>(add_pair<DT>(a, row, k, p), h);
       if (pre != 1.0f) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[i] *= pre;
       }
-      load8<WDT, true>(a.weight, 0, k, a.K, a.wvec, w);
       unpack<WDT>(w, v);
       if (rs.lo != 0.0f)
         scale8<kExact, false>(h, rs, v, k, a.K);
@@ -662,7 +647,7 @@ int blocks_per_sm(K k, int threads) {
 }
 
 // Blocks of a streaming kernel: one for each of its units. Loops over fewer, resident blocks were
-// slower (129280 x 4096: 237 against 211 us to read back): a new block's loads overlap the end of
+// slower (129280 x 4096: 237 against 213 us to read back): a new block's loads overlap the end of
 // those beside it.
 int grid_for(long long units, int per_block) {
   return (int)((units + per_block - 1) / per_block);

@@ -185,6 +185,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   cluster_sync();  // the pair's barriers are ready
   tc_fence_after();
   grid_dep_wait();
+  // what the kernel before wrote with plain stores is read by the copy engine
+  asm volatile("fence.proxy.async.global;" ::: "memory");
   const uint32_t tmem = *tmem_slot;
   const uint32_t sf_col0 = p.n_acc * p.NT;  // scales after the accumulators
 
