@@ -1019,4 +1019,78 @@ int spec_token_logprobs(const void* logits, int dtype, long long ld, const int32
   return e == cudaSuccess ? rc : SPEC_ERR_CUDA;
 }
 
+// ------------------------------------------------------------------------------ truncated sampling
+
+static int sample_args(const void* logits, int dtype, long long ld, int rows, int V,
+                       const spec_truncation* rule, const int32_t* row_count, void* ws,
+                       size_t ws_bytes, SampleArgs* a) {
+  if (rows < 0 || rows > (1 << 26) || V < 1 || ld < V || !rule) return SPEC_ERR_INVALID_ARG;
+  if (V > SPEC_SAMPLE_MAX_VOCAB) return SPEC_ERR_TOO_LARGE;
+  if (!dtype_ok(dtype)) return SPEC_ERR_UNSUPPORTED_DTYPE;
+  if (rule->rows_per_param < 1) return SPEC_ERR_INVALID_ARG;
+  const float T = rule->temperature;
+  if (!rule->temperatures && (!(T >= 0.0f) || !isfinite(T) || (T > 0.0f && !isfinite(1.0f / T))))
+    return SPEC_ERR_INVALID_ARG;
+  if (!rule->top_ks && rule->top_k < 0) return SPEC_ERR_INVALID_ARG;
+  if (!rule->top_ps && !(rule->top_p >= 0.0f && rule->top_p <= 1.0f)) return SPEC_ERR_INVALID_ARG;
+  if (!rule->min_ps && !(rule->min_p >= 0.0f && rule->min_p <= 1.0f)) return SPEC_ERR_INVALID_ARG;
+  if (!status_ws_ok(ws)) return SPEC_ERR_INVALID_ARG;
+  if (ws_bytes < kHeader) return SPEC_ERR_WORKSPACE_TOO_SMALL;
+  if (rows && (!logits || !elem_aligned(logits, dtype))) return SPEC_ERR_INVALID_ARG;
+  *a = SampleArgs{};
+  a->x = logits;
+  a->ld = ld;
+  a->rows = rows;
+  a->V = V;
+  a->row_count = row_count;
+  a->temperature = rule->temperatures;
+  a->top_k = rule->top_ks;
+  a->top_p = rule->top_ps;
+  a->min_p = rule->min_ps;
+  a->temperature_all = T;
+  a->top_k_all = rule->top_k;
+  a->top_p_all = rule->top_p;
+  a->min_p_all = rule->min_p;
+  a->rows_per_param = rule->rows_per_param;
+  a->status = static_cast<uint32_t*>(ws);
+  return SPEC_OK;
+}
+
+int spec_sample(const void* logits, int dtype, long long ld, int rows, int V,
+                const spec_truncation* rule, const float* u, const int32_t* row_count,
+                int32_t* tokens, float* logp, int32_t* kept, void* ws, size_t ws_bytes,
+                void* stream) {
+  SampleArgs a;
+  const int bad = sample_args(logits, dtype, ld, rows, V, rule, row_count, ws, ws_bytes, &a);
+  if (bad != SPEC_OK || rows == 0) return bad;
+  if (!u || !tokens) return SPEC_ERR_INVALID_ARG;
+  a.u = u;
+  a.tokens = tokens;
+  a.logp = logp;
+  a.kept = kept;
+  const cudaError_t e = launch_sample(a, dtype, static_cast<cudaStream_t>(stream));
+  const int rc = finish();
+  return e == cudaSuccess ? rc : SPEC_ERR_CUDA;
+}
+
+int spec_truncate(const void* logits, int dtype, long long ld, int rows, int V,
+                  const spec_truncation* rule, const int32_t* row_count, void* out,
+                  long long ld_out, int32_t* kept, float* stats, void* ws, size_t ws_bytes,
+                  void* stream) {
+  SampleArgs a;
+  const int bad = sample_args(logits, dtype, ld, rows, V, rule, row_count, ws, ws_bytes, &a);
+  if (bad != SPEC_OK) return bad;
+  if (ld_out < V) return SPEC_ERR_INVALID_ARG;
+  if (rows == 0) return SPEC_OK;
+  if (!out || !elem_aligned(out, dtype)) return SPEC_ERR_INVALID_ARG;
+  if (!rows_apart(out, ld_out, logits, ld, rows, V, dtype)) return SPEC_ERR_INVALID_ARG;
+  a.out = out;
+  a.ldo = ld_out;
+  a.kept = kept;
+  a.stats = stats;
+  const cudaError_t e = launch_sample(a, dtype, static_cast<cudaStream_t>(stream));
+  const int rc = finish();
+  return e == cudaSuccess ? rc : SPEC_ERR_CUDA;
+}
+
 }  // extern "C"

@@ -159,6 +159,32 @@ struct LogprobArgs {
 };
 cudaError_t launch_token_logprobs(const LogprobArgs& a, int dt, cudaStream_t s);
 
+// Truncated sampling (sample.cu): a draw a row (out null), or the truncated row.
+struct SampleArgs {
+  const void* x;  // [rows, V], row stride ld
+  long long ld;
+  int rows, V;
+  const int32_t* row_count;  // rows of the batch, or null
+  // of every rows_per_param rows, or of all where the array is null
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  float temperature_all;
+  int top_k_all;
+  float top_p_all, min_p_all;
+  int rows_per_param;
+  const float* u;   // [rows], for a draw
+  int32_t* tokens;
+  float* logp;      // may be null, as may kept and stats
+  int32_t* kept;
+  void* out;        // [rows, V], row stride ldo
+  long long ldo;
+  float* stats;     // [rows, 2]
+  uint32_t* status;
+};
+cudaError_t launch_sample(const SampleArgs& a, int dt, cudaStream_t s);
+
 int num_sms();
 
 // Tracing hooks around every launch (api.cu): count the launch and record the attached begin /

@@ -30,6 +30,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "row_pieces.cuh"
 #include "tc_ptx.cuh"
 
 namespace spec {
@@ -82,26 +83,6 @@ struct Shared {
   int scan[kWarps];
 };
 
-// Ordered bits: larger floats have larger bits, zeros of both signs are equal. 0 stands for
-// "no place" (NaN and -inf).
-__device__ __forceinline__ uint32_t order_bits(float x) {
-  if (!(x > -INFINITY)) return 0;
-  const uint32_t b = __float_as_uint(x + 0.0f);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-}
-__device__ __forceinline__ float order_value(uint32_t u) {
-  return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
-}
-__device__ __forceinline__ unsigned long long make_key(uint32_t bits, int id) {
-  return ((unsigned long long)bits << 32) | (0xffffffffu - (uint32_t)id);
-}
-
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
-}
-
 // The sums of the first n lanes (a power of two) in every one of them: against their largest
 // reference, then added.
 template <int n>
@@ -121,108 +102,6 @@ __device__ __forceinline__ Sums merge_lanes(Sums a, float c) {
     a.s1 += __shfl_xor_sync(kFull, a.s1, o);
   }
   return a;
-}
-
-// ------------------------------------------------------------------------------ a row's pieces
-
-// A row as 16-byte pieces at 16-byte aligned addresses: piece j holds ids j * N - head ...; the
-// first and the last piece may be partly outside the row.
-template <int DT>
-struct Row {
-  static constexpr int N = DT == SPEC_BF16 ? 8 : 4;
-  const char* base;  // address of piece 0
-  int head, V;
-
-  __device__ Row(const void* x, size_t off, int V_) : V(V_) {
-    const char* p = static_cast<const char*>(x) + off * (16 / N);
-    const int mis = (int)(reinterpret_cast<uintptr_t>(p) & 15);
-    base = p - mis;
-    head = mis / (16 / N);
-  }
-  __device__ int pieces() const { return (head + V + N - 1) / N; }
-
-  // Pieces jb + thread + b * kThreads, b < B.
-  template <int B>
-  __device__ __forceinline__ void load_batch(uint4 (&q)[B], int jb, int end) const;
-
-  static constexpr uint32_t kNone = DT == SPEC_BF16 ? 0xff80ff80u : 0xff800000u;  // -inf
-
-  // Piece j, with -inf outside the row and past `end`. A row has at most two pieces that are
-  // partly outside; they go through a call of their own, so that the loads of whole ones stay in
-  // flight together.
-  __device__ __forceinline__ uint4 load(int j, int end) const {
-    uint4 q = make_uint4(kNone, kNone, kNone, kNone);
-    if (j < end) {
-      const int v = j * N - head;
-      if (v >= 0 && v + N <= V) q = ld_coherent16(base + (size_t)j * 16);
-    }
-    return q;
-  }
-  __device__ __forceinline__ bool partial(int j, int end) const {
-    const int v = j * N - head;
-    return j < end && (v < 0 || v + N > V);
-  }
-  __device__ __noinline__ uint4 load_partial(int j) const {
-    uint32_t w[4] = {kNone, kNone, kNone, kNone};
-    const int v = j * N - head;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (v + i < 0 || v + i >= V) continue;
-      if constexpr (DT == SPEC_BF16) {
-        const uint32_t b = reinterpret_cast<const uint16_t*>(base + (size_t)j * 16)[i];
-        w[i / 2] = i & 1 ? (w[i / 2] & 0xffffu) | b << 16 : (w[i / 2] & 0xffff0000u) | b;
-      } else {
-        w[i] = reinterpret_cast<const uint32_t*>(base + (size_t)j * 16)[i];
-      }
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
-  // Either kind.
-  __device__ __forceinline__ uint4 load_any(int j, int end) const {
-    return partial(j, end) ? load_partial(j) : load(j, end);
-  }
-};
-
-template <int DT>
-template <int B>
-__device__ __forceinline__ void Row<DT>::load_batch(uint4 (&q)[B], int jb, int end) const {
-  const int j = jb + threadIdx.x;
-  // whole batches inside the row: one address, no tests of single pieces
-  if (jb * N >= head && jb + B * kThreads <= end && (jb + B * kThreads) * N - head <= V) {
-    const char* p = base + (size_t)j * 16;
-#pragma unroll
-    for (int b = 0; b < B; ++b) q[b] = ld_coherent16(p + b * kThreads * 16);
-  } else {
-#pragma unroll
-    for (int b = 0; b < B; ++b) q[b] = load(j + b * kThreads, end);
-#pragma unroll
-    for (int b = 0; b < B; ++b)
-      if (partial(j + b * kThreads, end)) q[b] = load_partial(j + b * kThreads);
-  }
-}
-
-template <int DT>
-__device__ __forceinline__ void unpack(const uint4& q, float (&x)[Row<DT>::N]) {
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (DT == SPEC_BF16) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    } else {
-      x[i] = __uint_as_float(w[i]);
-    }
-  }
-}
-
-__device__ __forceinline__ __nv_bfloat162 as_bf2(uint32_t w) {
-  return *reinterpret_cast<const __nv_bfloat162*>(&w);
-}
-__device__ __forceinline__ uint32_t as_word(__nv_bfloat162 v) {
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-__device__ __forceinline__ float max3f(float a, float b, float c) {
-  return fmaxf(a, fmaxf(b, c));
 }
 
 // Maximum of a batch (NaN ignored, unless there is nothing else).
@@ -653,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, ctas(D)) logprobs_kernel(const Logpr
     const int np = r.pieces(), per = (np + split - 1) / split;
 #pragma unroll
     for (int d = 0; d < D; ++d)
-      r.template load_batch<kBatch>(q[d], part * per + d * kStep, min(np, part * per + per));
+      r.template load_batch<kBatch, kThreads>(q[d], part * per + d * kStep, min(np, part * per + per));
   }
   int t = a.tokens ? a.tokens[row] : 0;
   while (true) {
@@ -693,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, ctas(D)) logprobs_kernel(const Logpr
           const int j = jb + d * kStep;
           if (d && j >= j1) break;
           take_batch<DT, TOP>(sh, q[d], j + tid, bound, xt, c, tame, run, larger);
-          r.template load_batch<kBatch>(q[d], j + D * kStep, j1);
+          r.template load_batch<kBatch, kThreads>(q[d], j + D * kStep, j1);
         }
         if (TOP && jb + D * kStep == renew && renew < j1) {
           renew += renew - j0;
@@ -704,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, ctas(D)) logprobs_kernel(const Logpr
       if (next < a.rows) {
         r = Row<DT>(a.x, (size_t)next * a.ld, a.V);
 #pragma unroll
-        for (int d = 0; d < D; ++d) r.template load_batch<kBatch>(q[d], d * kStep, r.pieces());
+        for (int d = 0; d < D; ++d) r.template load_batch<kBatch, kThreads>(q[d], d * kStep, r.pieces());
       }
 
       // this CTA's sums: lanes against their warp's maximum, then warps against the CTA's
@@ -788,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, ctas(D)) logprobs_kernel(const Logpr
     } else if (next < a.rows) {
       r = Row<DT>(a.x, (size_t)next * a.ld, a.V);
 #pragma unroll
-      for (int d = 0; d < D; ++d) r.template load_batch<kBatch>(q[d], d * kStep, r.pieces());
+      for (int d = 0; d < D; ++d) r.template load_batch<kBatch, kThreads>(q[d], d * kStep, r.pieces());
     }
     if (next >= a.rows) return;
     row = next;

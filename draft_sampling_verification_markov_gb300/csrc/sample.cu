@@ -1,0 +1,1000 @@
+// sample.cu -- truncated sampling: top-k, top-p and min-p over softmax(x / T), one draw a row from a
+// given uniform, or the row itself with -inf outside what is left.
+//
+// Tokens are ordered by key: larger logits first, then lower ids. Each of the three rules leaves a
+// prefix of that order, so a row's truncation is one key: a token stays iff its key is at least it.
+//   top-k   the k-th key;
+//   top-p   the last key before which less than p of the mass (of what top-k left) has been reached;
+//   min-p   the last key of a logit >= max x + T log(min_p).
+// The draw walks what is left in order of the ids: the first token whose cumulative mass passes u.
+//
+// A border between two tokens, in the order or in the draw, is decided by the last bits of a sum
+// over the vocabulary: a fp32 sum, or an approximate exponential, moves the borders of unlikely
+// tokens by more than their own mass. So masses are whole numbers (Weigher): exp((x - max) / T)
+// in units of 2^-(S + 1), to a relative error of about 2^-31, summed without rounding in 64 bits.
+// Sums do not depend on their order, the draw is the same however the row is split, and p and u
+// are compared exactly.
+//
+// The first pass over a row keeps the largest key of every thread's batch (64 bytes; more where a
+// row has more than 4096 batches) in shared memory. The k-th largest of these bounds the k-th
+// largest logit from below, and only the batches that reach the bound are read again, from L2: a
+// few hundred tokens, sorted, on which the three rules and the draw are decided. Rows that defeat
+// this (flat ones under top-p, hundreds of equal logits) are searched for the key by passes over
+// the row; what a temperature alone asks for is one pass of masses.
+//
+// Few rows are split over a cluster of up to 8 CTAs, which merge through distributed shared memory.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "row_pieces.cuh"
+
+namespace spec {
+namespace {
+
+namespace cg = cooperative_groups;
+typedef unsigned long long u64;
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBatch = 4;                       // 16-byte pieces of a thread's batch
+constexpr int kWarpStep = 32 * kBatch;          // consecutive pieces of a warp: a segment
+constexpr int kStep = kThreads * kBatch;        // ... of a CTA
+constexpr int kGroupsMost = 16;                 // index entries of a thread
+constexpr int kEntries = kGroupsMost * kThreads;
+constexpr int kList = 2048;                     // tokens sorted at most
+constexpr int kListTop = 1024;                  // largest k that goes through the list
+constexpr int kTryFirst = 256, kTryNext = 1024; // batches listed for a nucleus
+constexpr int kMaxSplit = 8;
+constexpr int kBuckets = kThreads;
+constexpr uint32_t kFull = 0xffffffffu;
+
+// Segments of the largest row.
+constexpr int kSegs = SPEC_SAMPLE_MAX_VOCAB / 4 / kWarpStep + kWarps;
+
+struct Shared {
+  uint32_t index[kEntries];  // largest order_bits of a thread's batches
+  union {
+    u64 keys[kList];         // listed tokens, sorted
+    u64 seg[kSegs];          // masses of a part's segments
+  };
+  int n_list;                // in the first CTA of a cluster
+  u64 pub[2][2];             // what a CTA shows its cluster
+  u64 red[2][kWarps];
+  // the row's parameters
+  float scale, ch, cl;
+  int k;
+  float p;
+  uint32_t tm;               // order_bits of the least logit that min-p leaves
+  // decided by one thread or CTA for the others
+  u64 limit, total, at, rest;
+  int kept, done, hit;
+};
+
+// ------------------------------------------------------------------------------ whole-number masses
+
+// 2^(30 + j / 32), rounded.
+__constant__ uint32_t kPowers[32] = {
+    0x40000000u, 0x4166c34cu, 0x42d561b4u, 0x444c0740u, 0x45cae0f2u, 0x47521cc6u, 0x48e1e9bau, 0x4a7a77d4u,
+    0x4c1bf829u, 0x4dc69cddu, 0x4f7a9930u, 0x51382182u, 0x52ff6b55u, 0x54d0ad5au, 0x56ac1f75u, 0x5891fac1u,
+    0x5a82799au, 0x5c7dd7a4u, 0x5e8451d0u, 0x60962665u, 0x62b39509u, 0x64dcdec3u, 0x6712460bu, 0x69540ec9u,
+    0x6ba27e65u, 0x6dfddbccu, 0x70666f76u, 0x72dc8374u, 0x75606374u, 0x77f25cceu, 0x7a92be8bu, 0x7d41d96eu,
+};
+
+// exp((x - m) / T) in units of 2^-(S + 1). With c = log2(e) / T as a pair of fp32 numbers,
+// y = (x - m) c as a pair, 32 y = i + 32 r with a whole i and |r| <= 1/64:
+//   2^y = 2^(i >> 5) 2^((i & 31) / 32) (1 + (2^r - 1)).
+// Lane j of a warp holds 2^(j / 32) in 31 bits, 2^r - 1 is its Taylor polynomial of degree 4 (the
+// next term is 2^-39), one 64-bit product-sum joins them. The last bit is set instead of rounded:
+// the error is between -1 and 1 units with mean 0, so that a hundred thousand small masses are not
+// all rounded the same way. Every lane of the warp has to call it.
+struct Weigher {
+  float m, ch, cl, least;  // least: y below it has no mass
+  uint32_t table;          // kPowers[lane]
+  int shift;               // 61 - S
+
+  template <int DT>
+  __device__ __forceinline__ u64 operator()(float x) const {
+    const float dh = __fsub_rn(x, m);
+    const float yh = __fmul_rn(dh, ch);
+    float yl = fmaf(dh, cl, fmaf(dh, ch, -yh));
+    if constexpr (DT == SPEC_F32) {  // a difference of bf16 numbers that matters is exact
+      yl = fmaf(two_sum(x, -m).lo, ch, yl);
+    }
+    constexpr float kMagic = 393216.0f;  // 1.5 * 2^18: ulp 1/32
+    const float t = __fadd_rn(yh, kMagic);
+    const int i = __float_as_int(t) - __float_as_int(kMagic);
+    const float r = __fadd_rn(__fsub_rn(yh, __fsub_rn(t, kMagic)), yl);
+    // ln2^j / j!
+    float q = fmaf(r, 9.618129107e-3f, 5.550410867e-2f);
+    q = fmaf(r, q, 2.402265070e-1f);
+    q = fmaf(r, q, -1.904654e-9f);  // what the last one's fp32 form leaves
+    q = fmaf(r, 6.931471825e-1f, r * q);
+    const int frac = __float2int_rn(q * 4294967296.0f);
+    const int tab = (int)__shfl_sync(kFull, table, i & 31);
+    const long long w = ((long long)tab << 32) + (long long)tab * frac;
+    const int by = shift - (i >> 5);
+    const u64 v = ((u64)w >> (by & 63)) | 1u;
+    return yh >= least ? v : 0;  // also for NaN
+  }
+};
+
+// u * z for a u in [0, 1) of whole z: the product exactly, rounded down (or up).
+__device__ __forceinline__ u64 exact_share(float u, u64 z, bool up) {
+  const uint32_t b = __float_as_uint(u);
+  const int e = (int)(b >> 23);                          // u >= 0
+  const u64 man = e ? (b & 0x7fffffu) | 0x800000u : b & 0x7fffffu;
+  const int sh = 150 - (e ? e : 1);                      // u = man * 2^-sh, sh >= 24
+  const u64 hi = __umul64hi(man, z), lo = man * z;       // below 2^88
+  u64 v, rest;
+  if (sh >= 128) {
+    v = 0;
+    rest = hi | lo;
+  } else if (sh >= 64) {
+    v = sh == 64 ? hi : hi >> (sh - 64);
+    rest = lo | (sh == 64 ? 0 : hi & ((1ull << (sh - 64)) - 1));
+  } else {
+    v = lo >> sh | hi << (64 - sh);
+    rest = lo & ((1ull << sh) - 1);
+  }
+  return v + (up && rest ? 1 : 0);
+}
+
+// What a key asks for: x > cut, or x == cut with an id up to last.
+struct Cut {
+  float x;
+  uint32_t id;
+  __device__ __forceinline__ explicit Cut(u64 key)
+      : x(key >> 32 ? order_value((uint32_t)(key >> 32)) : -INFINITY),
+        id(key >> 32 ? 0xffffffffu - (uint32_t)key : 0u) {}
+  __device__ __forceinline__ bool leaves(float v, int at) const {
+    // key 0 leaves everything above -inf
+    return v > x || (v == x && (uint32_t)at <= id && v > -INFINITY);
+  }
+};
+
+// ------------------------------------------------------------------------------ a CTA or cluster
+
+template <bool SPLIT>
+struct Team {
+  Shared& sh;
+  cg::cluster_group cluster;
+  int parts, part, turn;
+
+  __device__ Team(Shared& s, int n)
+      : sh(s), cluster(cg::this_cluster()), parts(SPLIT ? n : 1),
+        part(SPLIT ? (int)(blockIdx.x % n) : 0), turn(0) {}
+  __device__ __forceinline__ void sync() {
+    if constexpr (SPLIT)
+      cluster.sync();
+    else
+      __syncthreads();
+  }
+  __device__ __forceinline__ Shared* leader() {
+    if constexpr (SPLIT) return cluster.map_shared_rank(&sh, 0);
+    return &sh;
+  }
+
+  // Sums of two numbers over the team's threads, and the first one's over the parts before. The
+  // slots alternate, so a part may be a call ahead of one that still reads.
+  struct Sum {
+    u64 a, b, before, own;
+  };
+  __device__ __noinline__ Sum sum(u64 a, u64 b) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      a += __shfl_xor_sync(kFull, a, o);
+      b += __shfl_xor_sync(kFull, b, o);
+    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (lane == 0) {
+      sh.red[0][warp] = a;
+      sh.red[1][warp] = b;
+    }
+    __syncthreads();
+    Sum s{0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      s.a += sh.red[0][w];
+      s.b += sh.red[1][w];
+    }
+    s.own = s.a;
+    if constexpr (SPLIT) {
+      if (threadIdx.x == 0) {
+        sh.pub[turn][0] = s.a;
+        sh.pub[turn][1] = s.b;
+      }
+      cluster.sync();
+      s.a = s.b = 0;
+      for (int q = 0; q < parts; ++q) {
+        const Shared* o = cluster.map_shared_rank(&sh, q);
+        if (q == part) s.before = s.a;
+        s.a += o->pub[turn][0];
+        s.b += o->pub[turn][1];
+      }
+      turn ^= 1;
+    } else {
+      __syncthreads();
+    }
+    return s;
+  }
+  __device__ __noinline__ u64 max(u64 a) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const u64 y = __shfl_xor_sync(kFull, a, o);
+      a = a > y ? a : y;
+    }
+    if ((threadIdx.x & 31) == 0) sh.red[0][threadIdx.x >> 5] = a;
+    __syncthreads();
+    a = sh.red[0][0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) a = sh.red[0][w] > a ? sh.red[0][w] : a;
+    if constexpr (SPLIT) {
+      if (threadIdx.x == 0) sh.pub[turn][0] = a;
+      cluster.sync();
+      for (int q = 0; q < parts; ++q) {
+        const u64 y = cluster.map_shared_rank(&sh, q)->pub[turn][0];
+        a = a > y ? a : y;
+      }
+      turn ^= 1;
+    } else {
+      __syncthreads();
+    }
+    return a;
+  }
+};
+
+// A part of a row.
+template <int DT>
+struct Part {
+  Row<DT> row;
+  int j0, j1;  // its pieces
+  __device__ __forceinline__ int steps() const { return (j1 - j0 + kStep - 1) / kStep; }
+  // First piece of this thread's batch in step `it`; its pieces are 32 apart.
+  __device__ __forceinline__ int first(int it) const {
+    return j0 + it * kStep + (int)(threadIdx.x >> 5) * kWarpStep + (int)(threadIdx.x & 31);
+  }
+  __device__ __forceinline__ void load(uint4 (&q)[kBatch], int it) const {
+    const int jw = j0 + it * kStep + (int)(threadIdx.x >> 5) * kWarpStep;
+    const int j = jw + (int)(threadIdx.x & 31);
+    if (jw * Row<DT>::N >= row.head && jw + kWarpStep <= j1 &&
+        (jw + kWarpStep) * Row<DT>::N - row.head <= row.V) {
+      const char* p = row.base + (size_t)j * 16;
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) q[b] = ld_coherent16(p + b * 512);
+    } else {
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) q[b] = row.load(j + b * 32, j1);
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+        if (row.partial(j + b * 32, j1)) q[b] = row.load_partial(j + b * 32);
+    }
+  }
+};
+
+// Largest logit of a batch, NaN if there is one.
+template <int DT>
+__device__ __forceinline__ float batch_max_nan(const uint4 (&q)[kBatch]) {
+  if constexpr (DT == SPEC_BF16) {
+    __nv_bfloat162 m[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+      m[b] = __hmax2_nan(__hmax2_nan(as_bf2(q[b].x), as_bf2(q[b].y)),
+                         __hmax2_nan(as_bf2(q[b].z), as_bf2(q[b].w)));
+#pragma unroll
+    for (int b = 1; b < kBatch; ++b) m[0] = __hmax2_nan(m[0], m[b]);
+    const uint32_t w = as_word(m[0]);
+    return max_nan(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  } else {
+    float m = -INFINITY;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      m = max_nan(m, max_nan(__uint_as_float(q[b].x), __uint_as_float(q[b].y)));
+      m = max_nan(m, max_nan(__uint_as_float(q[b].z), __uint_as_float(q[b].w)));
+    }
+    return m;
+  }
+}
+
+// ------------------------------------------------------------------------------ passes over a row
+
+// Mass (MASS) and number of the part's tokens that a cut leaves; with SEG the masses of its
+// segments, too.
+template <int DT, bool MASS, bool SEG>
+__device__ __noinline__ void pass(Shared& sh, const Part<DT> part, const Weigher wt, u64 key,
+                                  u64& mass, u64& count) {
+  constexpr int N = Row<DT>::N;
+  const Cut cut(key);
+  // nothing below has a mass or stays
+  const int n = part.steps(), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  mass = 0;
+  uint32_t c = 0;
+  uint4 q[kBatch];
+  part.load(q, 0);
+  for (int it = 0; it < n; ++it) {
+    const int j = part.first(it);
+    uint4 now[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) now[b] = q[b];
+    if (it + 1 < n) part.load(q, it + 1);
+    u64 s = 0;
+    if (__any_sync(kFull, batch_max_nan<DT>(now) >= cut.x)) {
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        float x[N];
+        unpack<DT>(now[b], x);
+        const int v = (j + b * 32) * N - part.row.head;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const bool in = cut.leaves(x[i], v + i);
+          c += in;
+          if constexpr (MASS) s += wt.template operator()<DT>(in ? x[i] : -INFINITY);
+        }
+      }
+    }
+    if constexpr (SEG) {
+      u64 t = s;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(kFull, t, o);
+      if (lane == 0) sh.seg[it * kWarps + warp] = t;
+    }
+    mass += s;
+  }
+  count = c;
+}
+
+// The largest key that leaves a mass (MASS) or number of at least `least` among what `limit`
+// leaves: by halving over the logits, then over the ids of the equal ones. A pass over the row a
+// step, 16 or 32 for the logit and up to 20 for the id.
+template <int DT, bool SPLIT, bool MASS>
+__device__ __noinline__ u64 search(Team<SPLIT>& team, const Part<DT>& part, const Weigher& wt,
+                                   u64 limit, u64 least, u64 top_key) {
+  auto enough = [&](u64 key) {
+    u64 m, c;
+    pass<DT, MASS, false>(team.sh, part, wt, key > limit ? key : limit, m, c);
+    const auto s = team.sum(m, c);
+    return (MASS ? s.a : s.b) >= least;
+  };
+  constexpr int kLow = DT == SPEC_BF16 ? 16 : 0;  // order_bits of a bf16 end in 16 zeros or ones
+  constexpr uint32_t kLeast = 0x00800000u >> kLow;  // of the lowest finite number
+  uint32_t lo = (uint32_t)(limit >> 32) >> kLow, hi = ((uint32_t)(top_key >> 32) >> kLow) + 1;
+  lo = lo > kLeast ? lo : kLeast;
+  while (hi - lo > 1) {
+    const uint32_t mid = lo + (hi - lo) / 2;
+    if (enough((u64)(mid << kLow) << 32))
+      lo = mid;
+    else
+      hi = mid;
+  }
+  uint32_t bits = lo << kLow;
+  if (DT == SPEC_BF16 && !(bits & 0x80000000u)) bits |= 0xffffu;
+  uint32_t a = 0, b = (uint32_t)part.row.V;  // ids up to b - 1 are enough, up to a - 1 are not
+  while (b - a > 1) {
+    const uint32_t mid = a + (b - a) / 2;
+    if (enough((u64)bits << 32 | (0xffffffffu - (mid - 1))))
+      b = mid;
+    else
+      a = mid;
+  }
+  const u64 key = (u64)bits << 32 | (0xffffffffu - (b - 1));
+  return key > limit ? key : limit;
+}
+
+// ------------------------------------------------------------------------------ the list
+
+// A bound that at least k of this CTA's index entries reach, and not many more where it can be
+// had: halving over the entries.
+__device__ __noinline__ uint32_t index_bound(Shared& sh, int groups, int k, uint32_t top) {
+  const int tid = threadIdx.x;
+  auto count = [&](uint32_t v) {
+    int n = 0;
+    for (int g = 0; g < groups; ++g) n += sh.index[g * kThreads + tid] >= v;
+    n = __reduce_add_sync(kFull, n);
+    if ((tid & 31) == 0) sh.red[0][tid >> 5] = (u64)n;
+    __syncthreads();
+    n = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) n += (int)sh.red[0][w];
+    __syncthreads();
+    return n;
+  };
+  uint32_t lo = 1, hi = top + 1;  // top >= every entry
+  if (count(1) < k) return 1;
+  while (hi - lo > 1) {
+    const uint32_t mid = lo + (hi - lo) / 2;
+    const int n = count(mid);
+    if (n < k) {
+      hi = mid;
+    } else {
+      lo = mid;
+      if (n <= k + k / 8) break;
+    }
+  }
+  return lo;
+}
+
+// Tokens of bits >= bound of the whole row in the leader's list. Returns how many there are; more
+// than kList means that they are not all there.
+template <int DT, bool SPLIT>
+__device__ __noinline__ int collect(Team<SPLIT>& team, const Part<DT>& part, int per_group,
+                                    uint32_t bound) {
+  constexpr int N = Row<DT>::N;
+  Shared& sh = team.sh;
+  Shared* lead = team.leader();
+  if (team.part == 0 && threadIdx.x == 0) sh.n_list = 0;
+  team.sync();
+  const int n = part.steps(), groups = (n + per_group - 1) / per_group;
+  for (int g = 0; g < groups; ++g) {
+    if (sh.index[g * kThreads + threadIdx.x] < bound) continue;
+    const int end = min(n, (g + 1) * per_group);
+    for (int it = g * per_group; it < end; ++it) {
+      const int j = part.first(it);
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        float x[N];
+        unpack<DT>(part.row.load_any(j + b * 32, part.j1), x);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const uint32_t bits = order_bits(x[i]);
+          if (bits >= bound) {
+            const int at = atomicAdd(&lead->n_list, 1);
+            if (at < kList)
+              lead->keys[at] = make_key(bits, (j + b * 32) * N - part.row.head + i);
+          }
+        }
+      }
+    }
+  }
+  team.sync();
+  return lead->n_list;
+}
+
+// Descending order of sh.keys[0 .. n).
+__device__ __noinline__ void sort_keys(Shared& sh, int n) {
+  int P = 32;
+  while (P < n) P *= 2;
+  for (int i = n + threadIdx.x; i < P; i += kThreads) sh.keys[i] = 0;
+  __syncthreads();
+  for (int size = 2; size <= P; size *= 2) {
+    for (int o = size / 2; o > 0; o /= 2) {
+      for (int i = threadIdx.x; i < P / 2; i += kThreads) {
+        const int a = 2 * i - (i & (o - 1)), b = a + o;
+        const u64 x = sh.keys[a], y = sh.keys[b];
+        if ((x < y) == ((a & size) == 0)) {
+          sh.keys[a] = y;
+          sh.keys[b] = x;
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// Exclusive prefix over the CTA's threads, and the sum.
+__device__ __noinline__ u64 scan(Shared& sh, u64 v, u64& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  u64 x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 y = __shfl_up_sync(kFull, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sh.red[0][warp] = x;
+  __syncthreads();
+  u64 before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += sh.red[0][w];
+    total += sh.red[0][w];
+  }
+  __syncthreads();
+  return before + x - v;
+}
+
+__device__ __forceinline__ float key_value(u64 key) { return order_value((uint32_t)(key >> 32)); }
+__device__ __forceinline__ int key_id(u64 key) { return (int)(0xffffffffu - (uint32_t)key); }
+
+// The three rules on the n sorted keys of the list, in one CTA: sh.kept tokens of sh.total mass
+// stay, sh.limit is the last one's key. `all` is the mass that p refers to where the list is only
+// the row's beginning (0: the list's first sh.k). False if the nucleus ends behind the list, which
+// holds every token of bits >= bound.
+template <int DT>
+__device__ __noinline__ bool rules(Shared& sh, const Weigher& wt, int n, u64 all, uint32_t bound) {
+  const int per = (n + kThreads - 1) / kThreads, first = threadIdx.x * per;
+  const int nk = sh.k > 0 && sh.k < n ? sh.k : n;
+  u64 mine = 0, w[kList / kThreads];
+#pragma unroll
+  for (int i = 0; i < kList / kThreads; ++i) {
+    w[i] = 0;
+    if (i >= per) continue;
+    w[i] = wt.template operator()<DT>(first + i < nk ? key_value(sh.keys[first + i]) : -INFINITY);
+    mine += w[i];
+  }
+  u64 mass;
+  const u64 at = scan(sh, mine, mass);
+  const bool by_p = sh.p < 1.0f;
+  const u64 need = by_p ? exact_share(sh.p, all ? all : mass, true) : ~0ull;
+  if (by_p && all && mass < need && sh.tm < bound) return false;
+  u64 before = at;
+  int np = 0, nm = 0;
+#pragma unroll
+  for (int i = 0; i < kList / kThreads; ++i) {
+    if (i < per && first + i < nk) {
+      np += before < need;
+      nm += (uint32_t)(sh.keys[first + i] >> 32) >= sh.tm;
+    }
+    before += w[i];
+  }
+  u64 t, counts = (u64)np << 32 | (u64)nm;
+  scan(sh, counts, t);
+  int kept = min((int)(t >> 32), (int)(uint32_t)t);
+  kept = kept > 1 ? kept : 1;
+  mine = 0;
+#pragma unroll
+  for (int i = 0; i < kList / kThreads; ++i)
+    if (i < per && first + i < kept) mine += w[i];
+  scan(sh, mine, t);
+  if (threadIdx.x == 0) {
+    sh.kept = kept;
+    sh.total = t;
+    sh.limit = sh.keys[kept - 1];
+  }
+  __syncthreads();
+  return true;
+}
+
+// ------------------------------------------------------------------------------ outputs
+
+__device__ __forceinline__ float log_mass(u64 mass, const Weigher& wt) {
+  // mass / 2^(S + 1) as a pair
+  const float hi = __ull2float_rn(mass);
+  const long long rest = (long long)(mass - __float2ull_rz(hi));
+  const float unit = ldexpf(1.0f, wt.shift - 62);
+  return df_log(DF{hi * unit, __ll2float_rn(rest) * unit});
+}
+
+__device__ __forceinline__ void write_draw(const SampleArgs& a, int row, int id, float x,
+                                           const Weigher& wt, float scale, u64 total, int kept) {
+  a.tokens[row] = id;
+  if (a.logp) a.logp[row] = (x - wt.m) * scale - log_mass(total, wt);
+  if (a.kept) a.kept[row] = kept;
+}
+
+__device__ __forceinline__ u64 draw_at(const SampleArgs& a, int row, u64 total) {
+  float u = a.u[row];
+  if (!(u >= 0.0f && u < 1.0f)) {
+    atomicOr(a.status, SPEC_DEV_BAD_PARAM);
+    if (u >= 1.0f) return total - 1;
+    u = 0.0f;
+  }
+  return exact_share(u, total, false);
+}
+
+// The draw among the list's first sh.kept keys: by 256 ranges of ids, then within one.
+template <int DT>
+__device__ __noinline__ void draw_list(Shared& sh, const SampleArgs& a, int row, const Weigher& wt,
+                                       float scale) {
+  u64* bucket = reinterpret_cast<u64*>(sh.index);
+  const int tid = threadIdx.x, n = sh.kept;
+  int by = 0;
+  while ((a.V - 1) >> by >= kBuckets) ++by;
+  bucket[tid] = 0;
+  __syncthreads();
+  for (int base = 0; base < n; base += kThreads) {
+    const int i = base + tid;
+    const u64 key = i < n ? sh.keys[i] : 0;
+    const u64 w = wt.template operator()<DT>(i < n ? key_value(key) : -INFINITY);
+    if (w) atomicAdd(&bucket[key_id(key) >> by], w);
+  }
+  __syncthreads();
+  const u64 at = draw_at(a, row, sh.total), mine = bucket[tid];
+  u64 t;
+  const u64 before = scan(sh, mine, t);
+  if (before <= at && at < before + mine) {
+    sh.hit = tid;
+    sh.rest = at - before;
+  }
+  __syncthreads();
+  const int hit = sh.hit;
+  const u64 rest = sh.rest;
+  // this bucket's tokens, few of them, behind one another in place of the buckets
+  u64* some = bucket;
+  if (tid == 0) sh.done = 0;
+  __syncthreads();
+  for (int i = tid; i < n; i += kThreads)
+    if (key_id(sh.keys[i]) >> by == hit) some[atomicAdd(&sh.done, 1)] = sh.keys[i];
+  __syncthreads();
+  const int m = sh.done;
+  for (int base = 0; base < m; base += kThreads) {
+    const bool in = base + tid < m;
+    const u64 key = in ? some[base + tid] : 0;
+    u64 below = 0;
+    for (int q = 0; q < m; ++q) {
+      const u64 w = wt.template operator()<DT>(key_value(some[q]));
+      if (in && key_id(some[q]) < key_id(key)) below += w;
+    }
+    const u64 w = wt.template operator()<DT>(in ? key_value(key) : -INFINITY);
+    if (in && below <= rest && rest < below + w)
+      write_draw(a, row, key_id(key), key_value(key), wt, scale, sh.total, n);
+  }
+}
+
+// The draw among all tokens that the cut leaves, from the segments' masses; in the CTA whose part
+// holds it.
+template <int DT>
+__device__ __noinline__ void draw_segment(Shared& sh, const SampleArgs& a, int row,
+                                          const Part<DT>& part, const Weigher& wt, float scale,
+                                          u64 key, u64 at, u64 total, int kept) {
+  constexpr int N = Row<DT>::N;
+  const int n = part.steps() * kWarps, per = (n + kThreads - 1) / kThreads;
+  const int first = threadIdx.x * per, lane = threadIdx.x & 31;
+  u64 mine = 0, t;
+  for (int i = first; i < min(n, first + per); ++i) mine += sh.seg[i];
+  u64 before = scan(sh, mine, t);
+  if (before <= at && at < before + mine) {
+    int i = first;
+    for (; before + sh.seg[i] <= at; ++i) before += sh.seg[i];
+    sh.hit = i;
+    sh.rest = at - before;
+  }
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  const int base = part.j0 + sh.hit * kWarpStep;
+  u64 rest = sh.rest;
+  const Cut cut(key);
+  for (int b = 0; b < kBatch; ++b) {
+    const int j = base + b * 32 + lane;
+    float x[N];
+    unpack<DT>(part.row.load_any(j, part.j1), x);
+    const int v = j * N - part.row.head;
+    u64 w[N], s = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      w[i] = wt.template operator()<DT>(cut.leaves(x[i], v + i) ? x[i] : -INFINITY);
+      s += w[i];
+    }
+    u64 up = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64 y = __shfl_up_sync(kFull, up, o);
+      if (lane >= o) up += y;
+    }
+    u64 c = up - s;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (c <= rest && rest < c + w[i])
+        write_draw(a, row, v + i, x[i], wt, scale, total, kept);
+      c += w[i];
+    }
+    const u64 all = __shfl_sync(kFull, up, 31);
+    if (rest < all) break;  // uniform
+    rest -= all;
+  }
+}
+
+// The part with -inf where the cut does not leave a token (everything, where `copy`).
+template <int DT>
+__device__ __noinline__ void write_part(const SampleArgs& a, int row, const Part<DT>& part, u64 key,
+                                        bool copy) {
+  constexpr int N = Row<DT>::N;
+  const Cut cut(key);
+  const Row<DT> to(a.out, (size_t)row * a.ldo, a.V);
+  char* base = const_cast<char*>(to.base);
+  const bool same = to.head == part.row.head;
+  const int n = part.steps();
+  for (int it = 0; it < n; ++it) {
+    uint4 q[kBatch];
+    part.load(q, it);
+    const int j = part.first(it);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int v = (j + b * 32) * N - part.row.head;
+      float x[N];
+      unpack<DT>(q[b], x);
+      uint32_t w[4] = {q[b].x, q[b].y, q[b].z, q[b].w};
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const bool in = copy || cut.leaves(x[i], v + i);
+        if constexpr (DT == SPEC_BF16) {
+          if (!in) w[i / 2] = i & 1 ? (w[i / 2] & 0xffffu) | 0xff800000u
+                                    : (w[i / 2] & 0xffff0000u) | 0xff80u;
+        } else {
+          if (!in) w[i] = 0xff800000u;
+        }
+      }
+      if (j + b * 32 >= part.j1) continue;
+      if (same && v >= 0 && v + N <= a.V) {
+        *reinterpret_cast<uint4*>(base + (size_t)(j + b * 32) * 16) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          if (v + i < 0 || v + i >= a.V) continue;
+          const size_t at = (size_t)(to.head + v + i);
+          if constexpr (DT == SPEC_BF16)
+            reinterpret_cast<uint16_t*>(base)[at] = (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
+          else
+            reinterpret_cast<uint32_t*>(base)[at] = w[i];
+        }
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------ kernel
+
+// The row's parameters, out of range ones replaced and flagged; by one thread.
+__device__ __noinline__ void read_params(Shared& sh, const SampleArgs& a, int row) {
+  const int at = row / a.rows_per_param;
+  float T = a.temperature ? a.temperature[at] : a.temperature_all;
+  int k = a.top_k ? a.top_k[at] : a.top_k_all;
+  float p = a.top_p ? a.top_p[at] : a.top_p_all;
+  float mp = a.min_p ? a.min_p[at] : a.min_p_all;
+  bool bad = false;
+  if (!(T >= 0.0f) || T == INFINITY) {
+    T = 1.0f;
+    bad = true;
+  }
+  if (p != p) {
+    p = 1.0f;
+    bad = true;
+  }
+  if (mp != mp) {
+    mp = 0.0f;
+    bad = true;
+  }
+  if (bad) atomicOr(a.status, SPEC_DEV_BAD_PARAM);
+  const float inv = T > 0.0f ? 1.0f / T : INFINITY;
+  const bool greedy = inv == INFINITY || p <= 0.0f || k == 1;
+  sh.scale = inv == INFINITY ? 1.0f : inv;
+  const double c = fmin((double)sh.scale * 1.4426950408889634074, 3e38);
+  sh.ch = (float)c;
+  sh.cl = (float)(c - (double)sh.ch);
+  sh.k = greedy ? 1 : (k <= 0 || k >= a.V ? 0 : k);
+  sh.p = p < 0.0f ? 0.0f : p;
+  sh.tm = 1;                       // min_p itself, until the row's maximum is known
+  sh.rest = mp > 0.0f ? __float_as_uint(mp < 1.0f ? mp : 1.0f) : 0;
+}
+
+template <int DT, bool SPLIT, bool WRITE>
+__global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a, const int parts) {
+  __shared__ Shared sh;
+  Team<SPLIT> team(sh, parts);
+  const int tid = threadIdx.x, lane = tid & 31;
+  grid_dep_wait();
+  int rows = a.rows;
+  if (a.row_count) rows = min(rows, max(0, *a.row_count));
+  Weigher wt;
+  wt.table = kPowers[lane];
+  int bits = 0;
+  while ((1 << bits) < a.V) ++bits;
+  const int S = min(46, 62 - bits);
+  wt.shift = 61 - S;
+  wt.least = -(float)(S + 1);
+
+  for (int row = SPLIT ? blockIdx.x / parts : blockIdx.x; row < rows; row += gridDim.x) {
+    Part<DT> part{Row<DT>(a.x, (size_t)row * a.ld, a.V), 0, 0};
+    {
+      const int np = part.row.pieces(), per = (np + team.parts - 1) / team.parts;
+      part.j0 = min(np, team.part * per);
+      part.j1 = min(np, part.j0 + per);
+    }
+    if (tid == 0) read_params(sh, a, row);
+    const int steps = part.steps(), per_group = max(1, (steps + kGroupsMost - 1) / kGroupsMost);
+    const int groups = (steps + per_group - 1) / per_group;
+
+    // the largest logit, and those of the batches
+    float m = -INFINITY;
+    {
+      uint4 q[2][kBatch];
+      part.load(q[0], 0);
+      part.load(q[1], 1);
+      float e = -INFINITY;
+      int in = 0, g = 0;
+      auto take = [&](const uint4 (&w)[kBatch]) {
+        e = max_nan(e, batch_max_nan<DT>(w));
+        if (++in == per_group) {
+          sh.index[g++ * kThreads + tid] = order_bits(e);
+          m = max_nan(m, e);
+          e = -INFINITY;
+          in = 0;
+        }
+      };
+      for (int it = 0; it < steps; it += 2) {
+        take(q[0]);
+        part.load(q[0], it + 2);
+        if (it + 1 < steps) take(q[1]);
+        part.load(q[1], it + 3);
+      }
+      if (in) {
+        sh.index[g * kThreads + tid] = order_bits(e);
+        m = max_nan(m, e);
+      }
+    }
+    // NaN comes out as the largest
+    const u64 most = team.max(m != m ? ~0ull : (u64)order_bits(m));
+    if (most == ~0ull || most == 0 || order_value((uint32_t)most) == INFINITY) {
+      // no distribution: the largest logit's id, or 0
+      u64 best = 0;
+      for (int it = 0; it < steps; ++it)
+        for (int b = 0; b < kBatch; ++b) {
+          const int j = part.first(it) + b * 32;
+          float x[Row<DT>::N];
+          unpack<DT>(part.row.load_any(j, part.j1), x);
+          for (int i = 0; i < Row<DT>::N; ++i) {
+            const uint32_t o = order_bits(x[i]);
+            const u64 key = o ? make_key(o, j * Row<DT>::N - part.row.head + i) : 0;
+            best = key > best ? key : best;
+          }
+        }
+      best = team.max(best);
+      if (team.part == 0 && tid == 0) {
+        atomicOr(a.status, SPEC_DEV_NONFINITE);
+        if (a.tokens) a.tokens[row] = best ? key_id(best) : 0;
+        if (a.logp) a.logp[row] = NAN;
+        if (a.kept) a.kept[row] = 0;
+        if (a.stats) a.stats[2 * (size_t)row] = a.stats[2 * (size_t)row + 1] = NAN;
+      }
+      if (WRITE) write_part<DT>(a, row, part, 0, true);
+      team.sync();
+      continue;
+    }
+    const uint32_t top = (uint32_t)most;
+    const u64 top_key = (u64)top << 32 | 0xffffffffu;
+    wt.m = order_value(top);
+    wt.ch = sh.ch;
+    wt.cl = sh.cl;
+    const float scale = sh.scale;
+    if (tid == 0 && sh.rest) {
+      // the least fp32 number x with (x - m) / T >= log(min_p)
+      const double t = (double)wt.m + log((double)__uint_as_float((uint32_t)sh.rest)) / (double)scale;
+      float f = __double2float_ru(t);
+      f = f < wt.m ? f : wt.m;
+      sh.tm = f > -INFINITY ? order_bits(f) : 1;
+    }
+    __syncthreads();
+    const int k = sh.k;
+    const bool by_p = sh.p < 1.0f, by_m = sh.tm > 1;
+    const uint32_t tm = sh.tm;
+
+    bool listed = false;
+    u64 limit = 0, total = 0;
+    int kept = 0;
+    if (k == 1) {
+      u64 best = 0;
+      for (int g = 0; g < groups; ++g) {
+        if (sh.index[g * kThreads + tid] != top) continue;
+        for (int it = g * per_group; it < min(steps, (g + 1) * per_group); ++it)
+          for (int b = 0; b < kBatch; ++b) {
+            const int j = part.first(it) + b * 32;
+            float x[Row<DT>::N];
+            unpack<DT>(part.row.load_any(j, part.j1), x);
+            for (int i = 0; i < Row<DT>::N; ++i)
+              if (x[i] == wt.m) {
+                const u64 key = make_key(top, j * Row<DT>::N - part.row.head + i);
+                best = key > best ? key : best;
+              }
+          }
+      }
+      limit = team.max(best);
+      kept = 1;
+      total = 1ull << (S + 1);
+      if (!WRITE && team.part == 0 && tid == 0)
+        write_draw(a, row, key_id(limit), wt.m, wt, scale, total, 1);
+    } else if (k || by_p || by_m) {
+      // the mass that p refers to
+      u64 all = 0;
+      if (!k && by_p) {
+        u64 mm, cc;
+        pass<DT, true, false>(sh, part, wt, 0, mm, cc);
+        all = team.sum(mm, cc).a;
+      }
+      for (int want = k ? k : kTryFirst; !listed && want <= kListTop;
+           want = !k && by_p && want < kTryNext ? kTryNext : kListTop + 1) {
+        uint32_t bound = tm;
+        if (k || by_p) {
+          bound = index_bound(sh, groups, want, top);
+          if (SPLIT) bound = (uint32_t)team.max(bound);
+        }
+        const int n = collect<DT, SPLIT>(team, part, per_group, bound);
+        if (n > kList) break;
+        if (team.part == 0) {
+          sort_keys(sh, n);
+          const bool ok = rules<DT>(sh, wt, n, all, bound);
+          if (tid == 0) sh.done = ok;
+        }
+        team.sync();
+        listed = team.leader()->done;
+        team.sync();
+      }
+      if (listed) {
+        limit = team.leader()->limit;
+        total = team.leader()->total;
+        kept = team.leader()->kept;
+        if (SPLIT) team.sync();
+        if (!WRITE && team.part == 0) draw_list<DT>(sh, a, row, wt, scale);
+      } else {
+        if (k) limit = search<DT, SPLIT, false>(team, part, wt, 0, (u64)k, top_key);
+        if (by_p) {
+          if (k) {
+            u64 mm, cc;
+            pass<DT, true, false>(sh, part, wt, limit, mm, cc);
+            all = team.sum(mm, cc).a;
+          }
+          const u64 need = exact_share(sh.p, all, true);
+          limit = search<DT, SPLIT, true>(team, part, wt, limit, need ? need : 1, top_key);
+        }
+        const u64 key_m = (u64)tm << 32;
+        limit = by_m && key_m > limit ? key_m : limit;
+      }
+    }
+    if (!kept) {
+      u64 mm, cc;
+      __syncthreads();
+      pass<DT, true, true>(sh, part, wt, limit, mm, cc);
+      const auto s = team.sum(mm, cc);
+      total = s.a;
+      kept = (int)s.b;
+      if (!WRITE) {
+        const u64 at = draw_at(a, row, total);
+        if (s.before <= at && at < s.before + s.own)
+          draw_segment<DT>(sh, a, row, part, wt, scale, limit, at - s.before, total, kept);
+      }
+    }
+    if (WRITE) {
+      write_part<DT>(a, row, part, limit, false);
+      if (team.part == 0 && tid == 0) {
+        if (a.kept) a.kept[row] = kept;
+        if (a.stats) {
+          a.stats[2 * (size_t)row] = wt.m * scale;
+          a.stats[2 * (size_t)row + 1] = log_mass(total, wt);
+        }
+      }
+    }
+    team.sync();  // the next row, or this CTA's end
+  }
+}
+
+template <int DT, bool SPLIT, bool WRITE>
+cudaError_t launch_t(const SampleArgs& a, int split, cudaStream_t s) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = trace_active() ? 0 : 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = split;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  const int most = 3 * num_sms();
+  cfg.gridDim = dim3((unsigned)(SPLIT ? a.rows * split : (a.rows < most ? a.rows : most)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = SPLIT ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, sample_kernel<DT, SPLIT, WRITE>, a, split);
+}
+
+template <int DT, bool WRITE>
+cudaError_t launch_split(const SampleArgs& a, int split, cudaStream_t s) {
+  return split > 1 ? launch_t<DT, true, WRITE>(a, split, s) : launch_t<DT, false, WRITE>(a, 1, s);
+}
+
+}  // namespace
+
+cudaError_t launch_sample(const SampleArgs& a, int dt, cudaStream_t s) {
+  TraceScope ts(SPEC_KCLASS_SELECT, s);
+  const int batch = kStep * (dt == SPEC_BF16 ? 8 : 4);
+  int split = 1;
+  while (split < kMaxSplit && (long long)a.rows * split <= num_sms() && a.V >= 2 * split * batch)
+    split *= 2;
+  if (dt == SPEC_BF16)
+    return a.out ? launch_split<SPEC_BF16, true>(a, split, s)
+                 : launch_split<SPEC_BF16, false>(a, split, s);
+  return a.out ? launch_split<SPEC_F32, true>(a, split, s)
+               : launch_split<SPEC_F32, false>(a, split, s);
+}
+
+}  // namespace spec

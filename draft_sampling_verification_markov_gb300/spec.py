@@ -19,7 +19,7 @@ SPEC_F32, SPEC_BF16 = 0, 1
 (SPEC_OP_PROPOSE, SPEC_OP_VERIFY_GREEDY, SPEC_OP_VERIFY_REJECTION, SPEC_OP_TV_CONFIDENCE,
  SPEC_OP_SCHEDULE, SPEC_OP_TARGET_STATS, SPEC_OP_MTP_GREEDY, SPEC_OP_ALL) = range(8)
 (SPEC_DEV_BAD_TOKEN, SPEC_DEV_NONFINITE, SPEC_DEV_EMPTY_RESIDUAL, SPEC_DEV_BAD_LENGTH,
- SPEC_DEV_TIMEOUT) = 1, 2, 4, 8, 16
+ SPEC_DEV_TIMEOUT, SPEC_DEV_BAD_PARAM) = 1, 2, 4, 8, 16, 32
 SPEC_SCHEDULE_MAX_CANDIDATES = 16384
 (SPEC_KCLASS_MARKOV, SPEC_KCLASS_STREAM, SPEC_KCLASS_SELECT, SPEC_KCLASS_OTHER,
  SPEC_KCLASS_PROPOSE) = range(5)
@@ -28,6 +28,7 @@ SPEC_ERR_TOO_LARGE = -7
 SPEC_MX_E2M1, SPEC_MX_E4M3 = 0, 1
 SPEC_MX_GROUP = 128
 SPEC_LOGPROBS_MAX_TOP = 32
+SPEC_SAMPLE_MAX_VOCAB = 1 << 20
 
 _lib = None
 
@@ -98,6 +99,8 @@ def lib():
         L.spec_mx_logits.argtypes = [vp, vp, i, vp, vp, i, i, i, i, vp, i, ll, vp, sz, vp]
         L.spec_token_logprobs.argtypes = [vp, i, ll, vp, f, i, i, i, vp, vp, vp, vp, vp, vp, sz,
                                           vp]
+        L.spec_sample.argtypes = [vp, i, ll, i, i, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.spec_truncate.argtypes = [vp, i, ll, i, i, vp, vp, vp, ll, vp, vp, vp, sz, vp]
         L.spec_launch_count.restype = ctypes.c_ulonglong
         L.spec_trace_events.argtypes = [i, vp, vp, i]
         L.spec_trace_events.restype = i
@@ -112,7 +115,8 @@ def lib():
                      "spec_flat_layout", "spec_flat_pack", "spec_target_stats_flat",
                      "spec_verify_greedy_flat",
                      "spec_verify_rejection_flat", "spec_mx_quantize", "spec_mx_dequantize",
-                     "spec_rmsnorm_mx", "spec_mx_logits", "spec_token_logprobs"):
+                     "spec_rmsnorm_mx", "spec_mx_logits", "spec_token_logprobs",
+                     "spec_sample", "spec_truncate"):
             getattr(L, name).restype = i
         _lib = L
     return _lib
@@ -892,6 +896,139 @@ def spec_token_logprobs(logits, tokens, temperature=1.0, *, top=0, out=None, wor
             raise ValueError("logp and rank need tokens")
     _launch("spec_token_logprobs", dev, workspace, stream, ptr, dt, ld, tp, temperature, rows, V,
             top, lp, rank, ent, ti, tl)
+    return out
+
+
+# ----------------------------------------------------------------------------- truncated sampling
+
+class _Truncation(ctypes.Structure):
+    """struct spec_truncation."""
+    _fields_ = [("temperature", ctypes.c_float), ("top_k", ctypes.c_int32),
+                ("top_p", ctypes.c_float), ("min_p", ctypes.c_float),
+                ("temperatures", ctypes.c_void_p), ("top_ks", ctypes.c_void_p),
+                ("top_ps", ctypes.c_void_p), ("min_ps", ctypes.c_void_p),
+                ("rows_per_param", ctypes.c_int32)]
+
+
+def _truncation(temperature, top_k, top_p, min_p, rows, dev):
+    """A _Truncation of numbers and of device tensors with one value for each of the rows, or for
+    every so many consecutive ones."""
+    r = _Truncation(1.0, 0, 1.0, 0.0, None, None, None, None, 1)
+    n = None
+    for value, one, many, dt in ((temperature, "temperature", "temperatures", torch.float32),
+                                 (top_k, "top_k", "top_ks", torch.int32),
+                                 (top_p, "top_p", "top_ps", torch.float32),
+                                 (min_p, "min_p", "min_ps", torch.float32)):
+        if not isinstance(value, torch.Tensor):
+            setattr(r, one, value)
+            continue
+        if value.dtype != dt or not value.is_contiguous():
+            raise ValueError(f"{one} must be a number or a contiguous tensor of {dt}")
+        _on(dev, value, one)
+        if n is not None and value.numel() != n:
+            raise ValueError("parameter tensors must have one length")
+        n = value.numel()
+        setattr(r, many, value.data_ptr())
+    if n is not None and rows:
+        if n == 0 or rows % n:
+            raise ValueError(f"parameter tensors must divide the {rows} rows evenly")
+        r.rows_per_param = rows // n
+    return r
+
+
+def _row_count(t, dev):
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.numel() != 1:
+        raise ValueError("row_count must be one int32")
+    _on(dev, t, "row_count")
+    return t.data_ptr()
+
+
+def _rows_out(t, name, dtype, n, dev):
+    """Address of an optional output of n elements."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() != n or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must hold {n} contiguous elements of {dtype} on {dev}")
+    return t.data_ptr()
+
+
+class SampledTokens:
+    """Outputs of spec_sample: tokens [rows] int32, logp [rows] fp32, kept [rows] int32; None where
+    not asked for (tokens are always)."""
+
+    __slots__ = ("tokens", "logp", "kept")
+
+    def __init__(self, tokens, logp=None, kept=None):
+        self.tokens, self.logp, self.kept = tokens, logp, kept
+
+    @classmethod
+    def empty(cls, rows, device):
+        i, new = torch.int32, torch.empty
+        return cls(new(rows, dtype=i, device=device),
+                   new(rows, dtype=torch.float32, device=device),
+                   new(rows, dtype=i, device=device))
+
+
+def spec_sample(logits, u, temperature=1.0, *, top_k=0, top_p=1.0, min_p=0.0, row_count=None,
+                out=None, workspace=None, stream=None):
+    """A token a row of logits [rows, V] (or [..., V], evenly spaced rows) from softmax(logits /
+    temperature) restricted by top_k, top_p and min_p, at the uniforms u [rows]. Each parameter is a
+    number or a device tensor (fp32; top_k int32) with one value for every so many consecutive
+    rows. Rows from row_count (one int32 on the device) on are skipped. `out` is a SampledTokens
+    whose None fields are not written."""
+    ptr, rows, V, ld = _rows(logits, "logits")
+    dt, dev = _dtype_code(logits.dtype), logits.device
+    rule = _truncation(temperature, top_k, top_p, min_p, rows, dev)
+    up = _rows_out(u, "u", torch.float32, rows, dev)
+    if up is None:
+        raise ValueError("a draw needs uniforms")
+    if out is None:
+        out = _on_stream(stream, SampledTokens.empty, rows, dev)
+    tp = _rows_out(out.tokens, "tokens", torch.int32, rows, dev)
+    _launch("spec_sample", dev, workspace, stream, ptr, dt, ld, rows, V, ctypes.addressof(rule), up,
+            _row_count(row_count, dev), tp, _rows_out(out.logp, "logp", torch.float32, rows, dev),
+            _rows_out(out.kept, "kept", torch.int32, rows, dev))
+    return out
+
+
+class TruncatedRows:
+    """Outputs of spec_truncate: logits (of the input's shape), kept [rows] int32, stats [rows, 2]
+    fp32 (m, log Z); kept and stats None where not asked for."""
+
+    __slots__ = ("logits", "kept", "stats")
+
+    def __init__(self, logits, kept=None, stats=None):
+        self.logits, self.kept, self.stats = logits, kept, stats
+
+    @classmethod
+    def empty(cls, like, rows):
+        dev = like.device
+        return cls(torch.empty(like.shape, dtype=like.dtype, device=dev),
+                   torch.empty(rows, dtype=torch.int32, device=dev),
+                   torch.empty(rows, 2, dtype=torch.float32, device=dev))
+
+
+def spec_truncate(logits, temperature=1.0, *, top_k=0, top_p=1.0, min_p=0.0, row_count=None,
+                  out=None, workspace=None, stream=None):
+    """logits [rows, V] (or [..., V], evenly spaced rows) with -inf where softmax(logits /
+    temperature) is cut off by top_k, top_p and min_p (parameters and row_count as in spec_sample),
+    how many tokens are left, and the normalisers that spec_verify_rejection takes as
+    target_stats. `out` is a TruncatedRows, whose logits may be the input."""
+    ptr, rows, V, ld = _rows(logits, "logits")
+    dt, dev = _dtype_code(logits.dtype), logits.device
+    rule = _truncation(temperature, top_k, top_p, min_p, rows, dev)
+    if out is None:
+        out = _on_stream(stream, TruncatedRows.empty, logits, rows)
+    if out.logits.shape != logits.shape or out.logits.dtype != logits.dtype:
+        raise ValueError("out.logits must have the logits' shape and dtype")
+    _on(dev, out.logits, "out.logits")
+    op, _, _, ldo = _rows(out.logits, "out.logits")
+    _launch("spec_truncate", dev, workspace, stream, ptr, dt, ld, rows, V, ctypes.addressof(rule),
+            _row_count(row_count, dev), op, ldo,
+            _rows_out(out.kept, "kept", torch.int32, rows, dev),
+            _rows_out(out.stats, "stats", torch.float32, 2 * rows, dev))
     return out
 
 

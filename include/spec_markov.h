@@ -75,6 +75,7 @@ extern "C" {
 #define SPEC_DEV_EMPTY_RESIDUAL 0x4u /* a rejection met zero residual mass (p_t == p_d) */
 #define SPEC_DEV_BAD_LENGTH 0x8u     /* a per-request length outside [0, gamma] */
 #define SPEC_DEV_TIMEOUT 0x10u       /* a kernel's bounded wait expired; its outputs are invalid */
+#define SPEC_DEV_BAD_PARAM 0x20u     /* a row's sampling parameter or uniform had no meaning */
 
 /* Largest R * gamma the prefix scheduler accepts (its sort runs in one CTA's shared memory). */
 #define SPEC_SCHEDULE_MAX_CANDIDATES 16384
@@ -528,6 +529,70 @@ int spec_token_logprobs(const void* logits, int dtype, long long ld, const int32
                         float temperature, int rows, int V, int top, float* logp, int32_t* rank,
                         float* entropy, int32_t* top_ids, float* top_logp, void* ws,
                         size_t ws_bytes, void* stream);
+
+/*
+ * Truncated sampling: softmax(x / T) restricted by top-k, top-p and min-p, as a draw a row or as
+ * the row itself with -inf outside what is left. No page defines these entry points: they make the
+ * distributions that "[DeepSeek-6] DSpark", section 3, verifies and drafts against where a request
+ * asks for truncated sampling (verification reproduces the target's distribution, whatever it is).
+ *   z = x * fl32(1/T), w = exp(z - max z). Tokens in descending order of x, ties to the lower id:
+ *   top_k   the first top_k stay (0, or V and more: all);
+ *   top_p   of these, those before which less than top_p of their summed w has been reached (1: all);
+ *   min_p   of these, those of w >= min_p (0: all).
+ * The first token always stays; T = 0 leaves it alone (greedy), as does top_p = 0. Tokens of logit
+ * -inf never stay. Sums and borders are exact to about 2^-31 of each w, in whole numbers, so the
+ * results do not depend on how a row is split over the GPU.
+ * A row with a NaN or +inf logit, or with nothing above -inf, sets SPEC_DEV_NONFINITE: its token is
+ * the largest logit's (0 where there is none), its logp and stats are NaN, its kept 0, and
+ * spec_truncate copies it.
+ *
+ * The parameters: one of each for all rows, or device arrays with one for every rows_per_param
+ * consecutive rows (a request's window). Values of an array that have no meaning (a NaN, a negative
+ * or infinite temperature) set SPEC_DEV_BAD_PARAM and count as T = 1, top_p = 1, min_p = 0; others
+ * are clamped to their range, and a temperature whose reciprocal is not finite counts as 0.
+ */
+typedef struct spec_truncation {
+  float temperature;           /* >= 0; each for all rows, where its array below is NULL */
+  int32_t top_k;               /* >= 0 */
+  float top_p, min_p;          /* in [0, 1] */
+  const float* temperatures;   /* device arrays [ceil(rows / rows_per_param)], each optional */
+  const int32_t* top_ks;
+  const float* top_ps;
+  const float* min_ps;
+  int32_t rows_per_param;      /* >= 1 */
+} spec_truncation;
+
+/* Largest V of the two calls. */
+#define SPEC_SAMPLE_MAX_VOCAB (1 << 20)
+
+/*
+ * One token a row. The draw is the first id at which the cumulative w of what is left, in ascending
+ * order of the ids, passes u times their sum.
+ * Arguments:
+ *   logits     [rows, V] of `dtype`, row stride ld >= V elements.
+ *   rule       read on the host during the call.
+ *   u          [rows] fp32 in [0, 1) (others set SPEC_DEV_BAD_PARAM and count as 0, or just below
+ *              1); not read where one token is left by T = 0, top_k = 1 or top_p = 0.
+ *   row_count  device int32, or NULL: rows from *row_count on are not read and their outputs stay
+ *              as they were (offsets + R of spec_flat_layout for a flattened batch).
+ *   tokens     [rows] int32; logp [rows] (optional), log-probability of the token among what is left;
+ *              kept [rows] int32 (optional), the number of tokens left.
+ */
+int spec_sample(const void* logits, int dtype, long long ld, int rows, int V,
+                const spec_truncation* rule, const float* u, const int32_t* row_count,
+                int32_t* tokens, float* logp, int32_t* kept, void* ws, size_t ws_bytes,
+                void* stream);
+
+/*
+ * The rows themselves: out [rows, V] of `dtype` (row stride ld_out) holds the logits that are left
+ * and -inf elsewhere; it may be `logits` itself, else must not overlap it. kept [rows] and stats
+ * [rows, 2] are optional; stats are the (m, log Z) of spec_target_stats for the truncated row, so
+ * verification needs no other pass over it.
+ */
+int spec_truncate(const void* logits, int dtype, long long ld, int rows, int V,
+                  const spec_truncation* rule, const int32_t* row_count, void* out,
+                  long long ld_out, int32_t* kept, float* stats, void* ws, size_t ws_bytes,
+                  void* stream);
 
 /* Largest R * (gamma + 1) that spec_verify_greedy_noalloc accepts. */
 #define SPEC_NOALLOC_MAX_ROWS 65536
