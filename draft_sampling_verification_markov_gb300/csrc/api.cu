@@ -1093,4 +1093,98 @@ int spec_truncate(const void* logits, int dtype, long long ld, int rows, int V,
   return e == cudaSuccess ? rc : SPEC_ERR_CUDA;
 }
 
+// ------------------------------------------------------------------------------ grouped 4-bit weights
+
+static bool w4_ok(int rows, int K, int group) {
+  return mx_sizes_ok(rows, K) && (group == 32 || group == 64 || group == 128);
+}
+
+// Whether two arrays of rows with strides share no byte range.
+static bool ranges_apart(const void* p, long long ldp, int dp, const void* q, long long ldq, int dq,
+                         int rows, int wp, int wq) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  const uintptr_t na = ((uintptr_t)(rows - 1) * ldp + wp) * esize(dp);
+  const uintptr_t nb = ((uintptr_t)(rows - 1) * ldq + wq) * esize(dq);
+  return a + na <= b || b + nb <= a;
+}
+
+size_t spec_w4_code_bytes(int rows, int K) {
+  return mx_sizes_ok(rows, K) ? (size_t)rows * (mx::padded(K) / 2) : 0;
+}
+
+int spec_w4_quantize(const void* x, int x_dtype, long long ldx, int rows, int K, int group,
+                     uint8_t* codes, void* scales, int scale_dtype, void* ws, size_t ws_bytes,
+                     void* stream) {
+  if (!w4_ok(rows, K, group) || ldx < K) return SPEC_ERR_INVALID_ARG;
+  if (!dtype_ok(x_dtype) || !dtype_ok(scale_dtype)) return SPEC_ERR_UNSUPPORTED_DTYPE;
+  if (!status_ws_ok(ws)) return SPEC_ERR_INVALID_ARG;
+  if (ws_bytes < kHeader) return SPEC_ERR_WORKSPACE_TOO_SMALL;
+  if (rows == 0) return SPEC_OK;
+  if (!x || !codes || !scales || !aligned16(codes) || !aligned16(scales) ||
+      !elem_aligned(x, x_dtype))
+    return SPEC_ERR_INVALID_ARG;
+  launch_w4_quantize(x, x_dtype, ldx, rows, K, group, codes, scales, scale_dtype,
+                     static_cast<uint32_t*>(ws), static_cast<cudaStream_t>(stream));
+  return finish();
+}
+
+int spec_w4_dequantize(const uint8_t* codes, const void* scales, int scale_dtype,
+                       const uint8_t* zeros, int rows, int K, int group, void* out, int out_dtype,
+                       long long ld_out, void* ws, size_t ws_bytes, void* stream) {
+  if (!w4_ok(rows, K, group) || ld_out < K) return SPEC_ERR_INVALID_ARG;
+  if (!dtype_ok(out_dtype) || !dtype_ok(scale_dtype)) return SPEC_ERR_UNSUPPORTED_DTYPE;
+  if (!status_ws_ok(ws)) return SPEC_ERR_INVALID_ARG;
+  if (ws_bytes < kHeader) return SPEC_ERR_WORKSPACE_TOO_SMALL;
+  if (rows == 0) return SPEC_OK;
+  if (!codes || !scales || !out || !aligned16(codes) || !aligned16(scales) ||
+      !elem_aligned(out, out_dtype))
+    return SPEC_ERR_INVALID_ARG;
+  launch_w4_dequantize(codes, scales, scale_dtype, zeros, rows, K, group, out, out_dtype, ld_out,
+                       static_cast<cudaStream_t>(stream));
+  return finish();
+}
+
+int spec_w4_logits(const void* x, long long ldx, const void* residual, long long ldr, int dtype,
+                   const void* norm_weight, int nw_dtype, float eps, int M, int K,
+                   const uint8_t* codes, const void* scales, int scale_dtype, const uint8_t* zeros,
+                   int group, int N, void* residual_out, long long ldh, void* out, int out_dtype,
+                   long long ld_out, void* ws, size_t ws_bytes, void* stream) {
+  if (!w4_ok(M, K, group) || !w4_ok(N, K, group) || N < 1 || M > (1 << 20) || ldx < K ||
+      ld_out < N || (long long)M * N > (1LL << 46))
+    return SPEC_ERR_INVALID_ARG;
+  if (residual && (ldr < K || ldh < K)) return SPEC_ERR_INVALID_ARG;
+  if (!dtype_ok(dtype) || !dtype_ok(scale_dtype) || !dtype_ok(out_dtype) ||
+      (norm_weight && !dtype_ok(nw_dtype)))
+    return SPEC_ERR_UNSUPPORTED_DTYPE;
+  if (norm_weight && (!(eps >= 0.0f) || !isfinite(eps))) return SPEC_ERR_INVALID_ARG;
+  if (!status_ws_ok(ws)) return SPEC_ERR_INVALID_ARG;
+  if (ws_bytes < kHeader) return SPEC_ERR_WORKSPACE_TOO_SMALL;
+  const int parts = dtype == SPEC_F32 || (norm_weight && nw_dtype == SPEC_F32) ? 3
+                    : norm_weight                                              ? 2
+                                                                               : 1;
+  if (!w4_fits(parts, K)) return SPEC_ERR_TOO_LARGE;
+  if (M == 0) return SPEC_OK;
+  if (!x || !codes || !scales || !out || !aligned16(codes) || !aligned16(scales) ||
+      !elem_aligned(x, dtype) || !elem_aligned(out, out_dtype) ||
+      (norm_weight && !elem_aligned(norm_weight, nw_dtype)))
+    return SPEC_ERR_INVALID_ARG;
+  if (residual && (!residual_out || !elem_aligned(residual, dtype) ||
+                   !elem_aligned(residual_out, dtype)))
+    return SPEC_ERR_INVALID_ARG;
+  if (residual && (!ranges_apart(residual_out, ldh, dtype, x, ldx, dtype, M, K, K) ||
+                   !ranges_apart(residual_out, ldh, dtype, residual, ldr, dtype, M, K, K)))
+    return SPEC_ERR_INVALID_ARG;
+  if (!ranges_apart(out, ld_out, out_dtype, x, ldx, dtype, M, N, K) ||
+      (residual && (!ranges_apart(out, ld_out, out_dtype, residual, ldr, dtype, M, N, K) ||
+                    !ranges_apart(out, ld_out, out_dtype, residual_out, ldh, dtype, M, N, K))))
+    return SPEC_ERR_INVALID_ARG;
+  const W4Args a{x,     ldx,         residual, ldr,   dtype, norm_weight,  nw_dtype,
+                 eps,   M,           N,        K,     codes, scales,       scale_dtype,
+                 zeros, group,       residual_out, ldh, out, out_dtype,    ld_out,
+                 static_cast<uint32_t*>(ws), parts, 0, 0, 0};
+  const cudaError_t e = launch_w4_logits(a, static_cast<cudaStream_t>(stream));
+  const int rc = finish();
+  return e == cudaSuccess ? rc : SPEC_ERR_CUDA;
+}
+
 }  // extern "C"

@@ -185,6 +185,41 @@ struct SampleArgs {
 };
 cudaError_t launch_sample(const SampleArgs& a, int dt, cudaStream_t s);
 
+// Grouped 4-bit weights (w4.cu); strides in elements.
+struct W4Args {
+  const void* x;  // [M, K], row stride ldx
+  long long ldx;
+  const void* residual;  // [M, K], row stride ldr, or null
+  long long ldr;
+  int dtype;
+  const void* weight;  // [K] of w_dtype, or null: no norm
+  int w_dtype;
+  float eps;
+  int M, N, K;
+  const uint8_t* codes;  // [N, Kp / 2]
+  const void* scales;    // [N, Kp / group]
+  int scale_dtype;
+  const uint8_t* zeros;  // [N, Kp / group] or null
+  int group;
+  void* h;  // [M, K], row stride ldh: x + residual
+  long long ldh;
+  void* out;  // [M, N], row stride ldo
+  int out_dtype;
+  long long ldo;
+  uint32_t* status;
+  int parts;  // columns of a row
+  // set by the launcher: rows of a chunk, chunks, warps that share a matrix row
+  int chunk_rows, chunks, k_warps;
+};
+// Whether a row of K in `parts` columns fits the kernel's shared memory.
+bool w4_fits(int parts, int K);
+cudaError_t launch_w4_logits(W4Args a, cudaStream_t s);
+void launch_w4_quantize(const void* x, int dt, long long ldx, int rows, int K, int group,
+                        uint8_t* codes, void* scales, int sdt, uint32_t* status, cudaStream_t s);
+void launch_w4_dequantize(const uint8_t* codes, const void* scales, int sdt, const uint8_t* zeros,
+                          int rows, int K, int group, void* out, int odt, long long ldo,
+                          cudaStream_t s);
+
 int num_sms();
 
 // Tracing hooks around every launch (api.cu): count the launch and record the attached begin /

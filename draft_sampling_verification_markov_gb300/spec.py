@@ -101,6 +101,12 @@ def lib():
                                           vp]
         L.spec_sample.argtypes = [vp, i, ll, i, i, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.spec_truncate.argtypes = [vp, i, ll, i, i, vp, vp, vp, ll, vp, vp, vp, sz, vp]
+        L.spec_w4_code_bytes.argtypes = [i, i]
+        L.spec_w4_code_bytes.restype = sz
+        L.spec_w4_quantize.argtypes = [vp, i, ll, i, i, i, vp, vp, i, vp, sz, vp]
+        L.spec_w4_dequantize.argtypes = [vp, vp, i, vp, i, i, i, vp, i, ll, vp, sz, vp]
+        L.spec_w4_logits.argtypes = [vp, ll, vp, ll, i, vp, i, f, i, i, vp, vp, i, vp, i, i, vp, ll,
+                                     vp, i, ll, vp, sz, vp]
         L.spec_launch_count.restype = ctypes.c_ulonglong
         L.spec_trace_events.argtypes = [i, vp, vp, i]
         L.spec_trace_events.restype = i
@@ -116,7 +122,8 @@ def lib():
                      "spec_verify_greedy_flat",
                      "spec_verify_rejection_flat", "spec_mx_quantize", "spec_mx_dequantize",
                      "spec_rmsnorm_mx", "spec_mx_logits", "spec_token_logprobs",
-                     "spec_sample", "spec_truncate"):
+                     "spec_sample", "spec_truncate",
+                     "spec_w4_quantize", "spec_w4_dequantize", "spec_w4_logits"):
             getattr(L, name).restype = i
         _lib = L
     return _lib
@@ -1030,6 +1037,138 @@ def spec_truncate(logits, temperature=1.0, *, top_k=0, top_p=1.0, min_p=0.0, row
             _rows_out(out.kept, "kept", torch.int32, rows, dev),
             _rows_out(out.stats, "stats", torch.float32, 2 * rows, dev))
     return out
+
+
+# ----------------------------------------------------------------------------- grouped 4-bit weights
+
+class W4Tensor:
+    """A [rows, K] matrix of grouped 4-bit weights: `codes` [rows, Kp / 2] uint8, `scales` [rows, Kp /
+    group] (bf16 or fp32) and optionally `zeros` [rows, Kp / group] uint8, contiguous on one device
+    (Kp = K rounded up to a multiple of 128; group 32, 64 or 128; the layout is that of
+    include/spec_markov.h)."""
+
+    __slots__ = ("codes", "scales", "zeros", "group", "K", "_at")
+
+    def __init__(self, codes, scales, group, K, *, zeros=None):
+        rows, Kp = codes.shape[0], -(-K // SPEC_MX_GROUP) * SPEC_MX_GROUP
+        if group not in (32, 64, 128):
+            raise ValueError("group must be 32, 64 or 128")
+        if K < 1:
+            raise ValueError("a matrix has at least one column")
+        if codes.dtype != torch.uint8 or codes.shape != (rows, Kp // 2) or not codes.is_contiguous():
+            raise ValueError(f"codes must be contiguous uint8 [rows, {Kp // 2}]")
+        shape = (rows, Kp // group)
+        dt = _dtype_code(scales.dtype)
+        if scales.shape != shape or not scales.is_contiguous():
+            raise ValueError(f"scales must be contiguous {shape}")
+        if not codes.is_cuda or scales.device != codes.device:
+            raise ValueError("codes and scales must be on one CUDA device")
+        if zeros is not None and (zeros.dtype != torch.uint8 or zeros.shape != shape
+                                  or not zeros.is_contiguous() or zeros.device != codes.device):
+            raise ValueError(f"zeros must be contiguous uint8 {shape} on {codes.device}")
+        self.codes, self.scales, self.zeros, self.group, self.K = codes, scales, zeros, group, K
+        self._at = (codes.data_ptr(), scales.data_ptr(), dt,
+                    None if zeros is None else zeros.data_ptr())
+
+    @classmethod
+    def empty(cls, rows, K, group, scale_dtype, device):
+        """An uninitialised [rows, K] matrix for a call to write."""
+        if group not in (32, 64, 128):
+            raise ValueError("group must be 32, 64 or 128")
+        Kp = -(-K // SPEC_MX_GROUP) * SPEC_MX_GROUP
+        return cls(torch.empty(rows, Kp // 2, dtype=torch.uint8, device=device),
+                   torch.empty(rows, Kp // group, dtype=scale_dtype, device=device), group, K)
+
+    @property
+    def rows(self):
+        return self.codes.shape[0]
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    @property
+    def shape(self):
+        return self.codes.shape[0], self.K
+
+
+def spec_w4_quantize(x, group=128, *, scale_dtype=torch.bfloat16, out=None, workspace=None,
+                     stream=None):
+    """x [rows, K] (or [..., K], evenly spaced rows; bf16 or fp32) as a W4Tensor without zero
+    points. `out` is a W4Tensor to write into."""
+    ptr, rows, K, ld = _rows(x, "x")
+    dt, dev = _dtype_code(x.dtype), x.device
+    if out is None:
+        out = _on_stream(stream, W4Tensor.empty, rows, K, group, scale_dtype, dev)
+    elif out.rows != rows or out.K != K or out.group != group or out.zeros is not None:
+        raise ValueError("out must be a W4Tensor of x's rows and width, the given group, no zeros")
+    _on(dev, out, "out")
+    cp, sp, sdt, _ = out._at
+    _launch("spec_w4_quantize", dev, workspace, stream, ptr, dt, ld, rows, K, group, cp, sp, sdt)
+    return out
+
+
+def spec_w4_dequantize(q, *, dtype=torch.bfloat16, out=None, workspace=None, stream=None):
+    """The numbers that the W4Tensor q stands for, [rows, K] of `dtype` (bf16 or fp32)."""
+    rows, K, dev = q.rows, q.K, q.device
+    if out is None:
+        _dtype_code(dtype)
+        out = _on_stream(stream, torch.empty, rows, K, dtype=dtype, device=dev)
+    dt = _dtype_code(out.dtype)
+    ptr, orows, width, ld = _rows(out, "out")
+    if orows != rows or width != K:
+        raise ValueError("out must have q's rows and width")
+    _on(dev, out, "out")
+    cp, sp, sdt, zp = q._at
+    _launch("spec_w4_dequantize", dev, workspace, stream, cp, sp, sdt, zp, rows, K, q.group, ptr, dt,
+            ld)
+    return out
+
+
+def spec_w4_logits(x, w, *, norm_weight=None, eps=1e-6, residual=None, residual_out=None, dtype=None,
+                   out=None, workspace=None, stream=None):
+    """Rows x [M, K] (or [..., K], evenly spaced rows) times the W4Tensor w [N, K]: [..., N] of
+    `dtype` (x's by default). With `residual` it is added first, with `norm_weight` [K] the sum's
+    rows are RMS-normalised. Returns the product, or (h, product) with h = x + residual where there
+    is a residual; h is residual_out or a new tensor."""
+    ptr, M, K, ldx = _rows(x, "x")
+    dt, dev = _dtype_code(x.dtype), x.device
+    if K != w.K:
+        raise ValueError(f"x has rows of {K} elements, w of {w.K}")
+    _on(dev, w, "w")
+    N = w.rows
+    np_, ndt = None, SPEC_BF16
+    if norm_weight is not None:
+        if norm_weight.shape != (K,) or not norm_weight.is_contiguous():
+            raise ValueError(f"norm_weight must be contiguous [{K}]")
+        _on(dev, norm_weight, "norm_weight")
+        np_, ndt = norm_weight.data_ptr(), _dtype_code(norm_weight.dtype)
+    rp = hp = None
+    ldr = ldh = K
+    if residual is not None:
+        if residual.shape != x.shape or residual.dtype != x.dtype:
+            raise ValueError("residual must have x's shape and dtype")
+        rp, _, _, ldr = _rows(residual, "residual")
+        _on(dev, residual, "residual")
+        if residual_out is None:
+            residual_out = _on_stream(stream, torch.empty, x.shape, dtype=x.dtype, device=dev)
+        elif residual_out.shape != x.shape or residual_out.dtype != x.dtype:
+            raise ValueError("residual_out must have x's shape and dtype")
+        hp, _, _, ldh = _rows(residual_out, "residual_out")
+        _on(dev, residual_out, "residual_out")
+    elif residual_out is not None:
+        raise ValueError("residual_out is an output of the form with a residual")
+    if out is None:
+        out = _on_stream(stream, torch.empty, *x.shape[:-1], N, dtype=dtype or x.dtype, device=dev)
+    odt = _dtype_code(out.dtype)
+    op, rows, width, ldo = _rows(out, "out")
+    if rows != M or width != N:
+        raise ValueError(f"out must hold {M} rows of {N}")
+    _on(dev, out, "out")
+    cp, sp, sdt, zp = w._at
+    _launch("spec_w4_logits", dev, workspace, stream, ptr, ldx, rp, ldr, dt, np_, ndt, eps, M, K, cp,
+            sp, sdt, zp, w.group, N, hp, ldh, op, odt, ldo)
+    return out if residual is None else (residual_out, out)
 
 
 def spec_device_status(workspace=None, clear=True, stream=None) -> int:

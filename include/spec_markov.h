@@ -562,7 +562,7 @@ typedef struct spec_truncation {
   int32_t rows_per_param;      /* >= 1 */
 } spec_truncation;
 
-/* Largest V of the two calls. */
+/* Largest V of the two calls below. */
 #define SPEC_SAMPLE_MAX_VOCAB (1 << 20)
 
 /*
@@ -593,6 +593,63 @@ int spec_truncate(const void* logits, int dtype, long long ld, int rows, int V,
                   const spec_truncation* rule, const int32_t* row_count, void* out,
                   long long ld_out, int32_t* kept, float* stats, void* ws, size_t ws_bytes,
                   void* stream);
+
+/*
+ * Grouped 4-bit weights: the form of weight-only checkpoints, for products with few rows.
+ * `rows` rows of K elements, padded to Kp = K rounded up to a multiple of SPEC_MX_GROUP; `group`
+ * (32, 64 or 128) consecutive elements of a row share a scale and, optionally, a zero point:
+ *   w = (code - zero) * scale, zero = 8 where there are none.
+ *   codes   [rows, Kp / 2] bytes, element 2i in the lower half of byte i. 16-byte aligned. Codes of
+ *           the padding do not matter.
+ *   scales  [rows, Kp / group], SPEC_F32 or SPEC_BF16, 16-byte aligned. Scales of groups that lie in
+ *           the padding do not matter.
+ *   zeros   [rows, Kp / group] bytes 0 .. 127 (the upper bit is ignored), or NULL.
+ * The calls take a workspace for its status word only. No page defines them: "Module
+ * deepseek_v4_mtp", Forward, and "spec_mtp" name the head and the projections that they compute.
+ */
+size_t spec_w4_code_bytes(int rows, int K);
+
+/*
+ * x [rows, K] (row stride ldx) as grouped 4-bit weights without zero points: the scale is the least
+ * number of its type with 7 scale >= the group's largest magnitude, a code 8 + x / scale rounded to
+ * the nearest, ties to even (1 .. 15; 8 in a group of zeros, whose scale is 0, and in the padding).
+ * A group with an infinity or a NaN has the scale NaN (SPEC_DEV_NONFINITE).
+ */
+int spec_w4_quantize(const void* x, int x_dtype, long long ldx, int rows, int K, int group,
+                     uint8_t* codes, void* scales, int scale_dtype, void* ws, size_t ws_bytes,
+                     void* stream);
+
+/* The numbers that grouped 4-bit weights stand for, rounded once to out_dtype: out [rows, K] (row
+ * stride ld_out). */
+int spec_w4_dequantize(const uint8_t* codes, const void* scales, int scale_dtype,
+                       const uint8_t* zeros, int rows, int K, int group, void* out, int out_dtype,
+                       long long ld_out, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The product of a few rows with a matrix of grouped 4-bit weights, and what stands before it in a
+ * draft's head: the residual addition and the RMS norm, in one launch.
+ * Defines: "Module deepseek_v4_mtp", Forward (the draft logits are lm_head(rms_norm(h))), and its
+ *   projections, which have neither.
+ *   h = x + residual, rounded to `dtype` (x without a residual);
+ *   a = h * rsqrt(mean(h^2) + eps) * norm_weight (h without a norm_weight);
+ *   out[m, n] = sum_k a[m, k] w[n, k]; a is not rounded below 24 bits, products are exact, sums fp32.
+ * Arguments:
+ *   x, residual   [M, K] of `dtype`, row strides ldx and ldr; residual may be NULL.
+ *   norm_weight   [K] of nw_dtype, or NULL (no norm; eps is ignored).
+ *   residual_out  [M, K] of `dtype`, row stride ldh: h (required with a residual, else ignored). Must
+ *                 not overlap x or residual.
+ *   codes, scales, zeros, group, N   the matrix, [N, K].
+ *   out           [M, N] of out_dtype, row stride ld_out >= N elements; must not overlap an operand.
+ * The matrix is read once for every 32 (bf16 rows without a norm), 16 (bf16 with a bf16 norm) or 10
+ * rows, fewer where K is large; SPEC_ERR_TOO_LARGE where one row does not fit (K above 27264 with
+ * 32-bit numbers, 40960 with a bf16 norm, 81920 else). A row with an infinity or a NaN sets
+ * SPEC_DEV_NONFINITE; its outputs are NaN (or infinities, without a norm).
+ */
+int spec_w4_logits(const void* x, long long ldx, const void* residual, long long ldr, int dtype,
+                   const void* norm_weight, int nw_dtype, float eps, int M, int K,
+                   const uint8_t* codes, const void* scales, int scale_dtype, const uint8_t* zeros,
+                   int group, int N, void* residual_out, long long ldh, void* out, int out_dtype,
+                   long long ld_out, void* ws, size_t ws_bytes, void* stream);
 
 /* Largest R * (gamma + 1) that spec_verify_greedy_noalloc accepts. */
 #define SPEC_NOALLOC_MAX_ROWS 65536
