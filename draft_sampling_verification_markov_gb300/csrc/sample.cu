@@ -31,6 +31,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "row_pieces.cuh"
+#include "tc_ptx.cuh"
 
 namespace spec {
 namespace {
@@ -46,8 +47,12 @@ constexpr int kStep = kThreads * kBatch;        // ... of a CTA
 constexpr int kGroupsMost = 16;                 // index entries of a thread
 constexpr int kEntries = kGroupsMost * kThreads;
 constexpr int kList = 2048;                     // tokens sorted at most
+constexpr int kHits = kList;                    // index entries listed at most
+constexpr int kTopsMost = 64;                   // largest k bounded by the threads' largest logits
 constexpr int kListTop = 1024;                  // largest k that goes through the list
-constexpr int kTryFirst = 256, kTryNext = 1024; // batches listed for a nucleus
+constexpr int kListMost = kList - 256;          // tokens that a guess may put there
+constexpr int kBins = 1536;                     // 1/32 octave each
+constexpr int kBinsThread = kBins / kThreads;
 constexpr int kMaxSplit = 8;
 constexpr int kBuckets = kThreads;
 constexpr uint32_t kFull = 0xffffffffu;
@@ -56,22 +61,33 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kSegs = SPEC_SAMPLE_MAX_VOCAB / 4 / kWarpStep + kWarps;
 
 struct Shared {
-  uint32_t index[kEntries];  // largest order_bits of a thread's batches
   union {
-    u64 keys[kList];         // listed tokens, sorted
-    u64 seg[kSegs];          // masses of a part's segments
+    uint32_t index[kEntries];  // largest order_bits of a thread's batches
+    u64 seg[kSegs];            // masses of a part's segments, once the index is not needed
+    u64 bucket[kBuckets];
   };
-  int n_list;                // in the first CTA of a cluster
+  u64 keys[kList];           // listed tokens, sorted
+  uint32_t bins[kBins];      // tokens by their mass
+  alignas(16) uint32_t tops[kThreads];  // largest order_bits of a thread's share
+  uint16_t hits[kHits];      // index entries that reach a bound
+  int n_list, n_hits;
+  uint32_t bound;
   u64 pub[2][2];             // what a CTA shows its cluster
-  u64 red[2][kWarps];
+  u64 red[3][kWarps];
+  float fred[kWarps];
   // the row's parameters
   float scale, ch, cl;
   int k;
   float p;
+  uint32_t mp;               // bits of min_p
   uint32_t tm;               // order_bits of the least logit that min-p leaves
   // decided by one thread or CTA for the others
-  u64 limit, total, at, rest;
+  u64 limit, total, rest;
   int kept, done, hit;
+  int edge[3], before[3], in;
+  float cum[2];
+  float guess;               // the share of the mass before bin_lo, as the bins have it
+  int bin_lo, bin_hi, n_above, n_window;
 };
 
 // ------------------------------------------------------------------------------ whole-number masses
@@ -90,35 +106,77 @@ __constant__ uint32_t kPowers[32] = {
 // Lane j of a warp holds 2^(j / 32) in 31 bits, 2^r - 1 is its Taylor polynomial of degree 4 (the
 // next term is 2^-39), one 64-bit product-sum joins them. The last bit is set instead of rounded:
 // the error is between -1 and 1 units with mean 0, so that a hundred thousand small masses are not
-// all rounded the same way. Every lane of the warp has to call it.
+// all rounded the same way. Every lane of the warp has to call it. Two at a time share the packed
+// fp32 instructions; one alone goes through the same operations.
+constexpr float kMagic = 393216.0f;  // 1.5 * 2^18: ulp 1/32
+constexpr int kMagicBits = 0x48c00000;
+// ln2^j / j! in units of 2^-32; the first with what its fp32 form leaves
+constexpr float kUnit = 4294967296.0f;
+constexpr float kC4 = 9.618129107e-3f * kUnit, kC3 = 5.550410867e-2f * kUnit,
+                kC2 = 2.402265070e-1f * kUnit, kC1 = 6.931471825e-1f * kUnit,
+                kC1Rest = -1.904654e-9f * kUnit;
+
 struct Weigher {
-  float m, ch, cl, least;  // least: y below it has no mass
+  float m, ch, cl, most;   // most: -y above it has no mass
   uint32_t table;          // kPowers[lane]
   int shift;               // 61 - S
 
+  __device__ __forceinline__ u64 join(float y, float t, float q) const {  // y: -(x - m) c
+    const int bits = __float_as_int(t);
+    const int tab = (int)__shfl_sync(kFull, table, bits);
+    const long long w = ((long long)tab << 32) + (long long)tab * __float2int_rn(q);
+    const int by = shift + (kMagicBits >> 5) - (bits >> 5);
+    const u64 v = ((u64)w >> (by & 63)) | 1u;
+    return y <= most ? v : 0;  // also for NaN
+  }
+
   template <int DT>
   __device__ __forceinline__ u64 operator()(float x) const {
-    const float dh = __fsub_rn(x, m);
-    const float yh = __fmul_rn(dh, ch);
-    float yl = fmaf(dh, cl, fmaf(dh, ch, -yh));
-    if constexpr (DT == SPEC_F32) {  // a difference of bf16 numbers that matters is exact
-      yl = fmaf(two_sum(x, -m).lo, ch, yl);
+    const float d = __fsub_rn(m, x);
+    const float y = __fmul_rn(d, ch);
+    float b = fmaf(d, -cl, fmaf(d, -ch, y));
+    // a difference of bf16 numbers that matters is exact
+    if constexpr (DT == SPEC_F32) b = fmaf(two_sum(m, -x).lo, -ch, b);
+    const float t = __fsub_rn(kMagic, y);
+    const float r = __fsub_rn(b, __fadd_rn(__fsub_rn(t, kMagic), y));
+    float q = fmaf(r, kC4, kC3);
+    q = fmaf(r, q, kC2);
+    q = fmaf(r, q, kC1Rest);
+    q = fmaf(r, kC1, __fmul_rn(r, q));
+    return join(y, t, q);
+  }
+
+  // t0, t1 (optional use): what bin() takes.
+  template <int DT>
+  __device__ __forceinline__ void pair(float x0, float x1, u64& v0, u64& v1, float& t0,
+                                       float& t1) const {
+    using namespace tc;
+    const u64 x = pack2(x0, x1), m2 = pack2(m, m), n1 = pack2(-1.0f, -1.0f);
+    const u64 ch2 = pack2(ch, ch), nch2 = pack2(-ch, -ch), ncl2 = pack2(-cl, -cl);
+    const u64 d = fma2(x, n1, m2);
+    const u64 y = mul2(d, ch2);
+    u64 b = fma2(d, ncl2, fma2(d, nch2, y));
+    if constexpr (DT == SPEC_F32) {
+      const u64 bb = add2(d, pack2(-m, -m));
+      const u64 e = fma2(add2(x, bb), n1, fma2(fma2(bb, n1, d), n1, m2));
+      b = fma2(e, nch2, b);
     }
-    constexpr float kMagic = 393216.0f;  // 1.5 * 2^18: ulp 1/32
-    const float t = __fadd_rn(yh, kMagic);
-    const int i = __float_as_int(t) - __float_as_int(kMagic);
-    const float r = __fadd_rn(__fsub_rn(yh, __fsub_rn(t, kMagic)), yl);
-    // ln2^j / j!
-    float q = fmaf(r, 9.618129107e-3f, 5.550410867e-2f);
-    q = fmaf(r, q, 2.402265070e-1f);
-    q = fmaf(r, q, -1.904654e-9f);  // what the last one's fp32 form leaves
-    q = fmaf(r, 6.931471825e-1f, r * q);
-    const int frac = __float2int_rn(q * 4294967296.0f);
-    const int tab = (int)__shfl_sync(kFull, table, i & 31);
-    const long long w = ((long long)tab << 32) + (long long)tab * frac;
-    const int by = shift - (i >> 5);
-    const u64 v = ((u64)w >> (by & 63)) | 1u;
-    return yh >= least ? v : 0;  // also for NaN
+    const u64 t = fma2(y, n1, pack2(kMagic, kMagic));
+    const u64 r = fma2(add2(add2(t, pack2(-kMagic, -kMagic)), y), n1, b);
+    u64 q = fma2(r, pack2(kC4, kC4), pack2(kC3, kC3));
+    q = fma2(r, q, pack2(kC2, kC2));
+    q = fma2(r, q, pack2(kC1Rest, kC1Rest));
+    q = fma2(r, pack2(kC1, kC1), mul2(r, q));
+    float y0, y1, q0, q1;
+    unpack2(y, y0, y1);
+    unpack2(t, t0, t1);
+    unpack2(q, q0, q1);
+    v0 = join(y0, t0, q0);
+    v1 = join(y1, t1, q1);
+  }
+  // Bin of a mass: -32 y rounded; the last one, and what has none, share a bin.
+  __device__ __forceinline__ static uint32_t bin(float t) {
+    return min((uint32_t)(kMagicBits - __float_as_int(t)), (uint32_t)kBins - 1);
   }
 };
 
@@ -299,7 +357,86 @@ __device__ __forceinline__ float batch_max_nan(const uint4 (&q)[kBatch]) {
   }
 }
 
+// Tokens of a batch above -inf.
+template <int DT>
+__device__ __forceinline__ uint32_t count_finite(const uint4 (&q)[kBatch]) {
+  constexpr int N = Row<DT>::N;
+  float low;
+  if constexpr (DT == SPEC_BF16) {
+    __nv_bfloat162 m = as_bf2(q[0].x);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+      m = __hmin2(__hmin2(__hmin2(m, as_bf2(q[b].x)), __hmin2(as_bf2(q[b].y), as_bf2(q[b].z))),
+                  as_bf2(q[b].w));
+    const uint32_t w = as_word(m);
+    low = fminf(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  } else {
+    low = INFINITY;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+      low = fminf(fminf(low, fminf(__uint_as_float(q[b].x), __uint_as_float(q[b].y))),
+                  fminf(__uint_as_float(q[b].z), __uint_as_float(q[b].w)));
+  }
+  if (low > -INFINITY) return kBatch * N;
+  uint32_t n = 0;
+#pragma unroll
+  for (int b = 0; b < kBatch; ++b) {
+    float x[N];
+    unpack<DT>(q[b], x);
+#pragma unroll
+    for (int i = 0; i < N; ++i) n += x[i] > -INFINITY;
+  }
+  return n;
+}
+
 // ------------------------------------------------------------------------------ passes over a row
+
+// Mass of a warp's step into its segment, if SEG.
+template <bool SEG>
+__device__ __forceinline__ void add_segment(Shared& sh, int it, u64 s) {
+  if constexpr (SEG) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+    if ((threadIdx.x & 31) == 0) sh.seg[it * kWarps + (threadIdx.x >> 5)] = s;
+  }
+}
+
+// Mass of the whole part; with SEG those of its segments, with BINS its tokens by their mass.
+template <int DT, bool SEG, bool BINS>
+__device__ __noinline__ u64 pass_all(Shared& sh, const Part<DT> part, const Weigher wt) {
+  constexpr int N = Row<DT>::N;
+  const int n = part.steps();
+  u64 mass = 0;
+  uint4 q[kBatch];
+  part.load(q, 0);
+  for (int it = 0; it < n; ++it) {
+    uint4 now[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) now[b] = q[b];
+    if (it + 1 < n) part.load(q, it + 1);
+    u64 s = 0;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      float x[N];
+      unpack<DT>(now[b], x);
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        u64 v0, v1;
+        float t0, t1;
+        wt.template pair<DT>(x[i], x[i + 1], v0, v1, t0, t1);
+        if constexpr (BINS) {
+          atomicAdd(&sh.bins[Weigher::bin(t0)], 1u);
+          atomicAdd(&sh.bins[Weigher::bin(t1)], 1u);
+        }
+        s += v0;
+        s += v1;
+      }
+    }
+    add_segment<SEG>(sh, it, s);
+    mass += s;
+  }
+  return mass;
+}
 
 // Mass (MASS) and number of the part's tokens that a cut leaves; with SEG the masses of its
 // segments, too.
@@ -308,8 +445,7 @@ __device__ __noinline__ void pass(Shared& sh, const Part<DT> part, const Weigher
                                   u64& mass, u64& count) {
   constexpr int N = Row<DT>::N;
   const Cut cut(key);
-  // nothing below has a mass or stays
-  const int n = part.steps(), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n = part.steps();
   mass = 0;
   uint32_t c = 0;
   uint4 q[kBatch];
@@ -328,19 +464,76 @@ __device__ __noinline__ void pass(Shared& sh, const Part<DT> part, const Weigher
         unpack<DT>(now[b], x);
         const int v = (j + b * 32) * N - part.row.head;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const bool in = cut.leaves(x[i], v + i);
-          c += in;
-          if constexpr (MASS) s += wt.template operator()<DT>(in ? x[i] : -INFINITY);
+        for (int i = 0; i < N; i += 2) {
+          const bool in0 = cut.leaves(x[i], v + i), in1 = cut.leaves(x[i + 1], v + i + 1);
+          c += in0 + in1;
+          if constexpr (MASS) {
+            u64 v0, v1;
+            float t0, t1;
+            wt.template pair<DT>(in0 ? x[i] : -INFINITY, in1 ? x[i + 1] : -INFINITY, v0, v1, t0,
+                                 t1);
+            s += v0;
+            s += v1;
+          }
         }
       }
     }
-    if constexpr (SEG) {
-      u64 t = s;
+    add_segment<SEG>(sh, it, s);
+    mass += s;
+  }
+  count = c;
+}
+
+// Mass and number of the part's tokens of logits >= hi, and the masses of its segments; those from
+// lo to hi go on the list.
+template <int DT>
+__device__ __noinline__ void pass_window(Shared& sh, const Part<DT> part,
+                                         const Weigher wt, float lo, float hi, u64& mass,
+                                         u64& count) {
+  constexpr int N = Row<DT>::N;
+  const int n = part.steps();
+  mass = 0;
+  uint32_t c = 0;
+  uint4 q[kBatch];
+  part.load(q, 0);
+  for (int it = 0; it < n; ++it) {
+    const int j = part.first(it);
+    uint4 now[kBatch];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(kFull, t, o);
-      if (lane == 0) sh.seg[it * kWarps + warp] = t;
+    for (int b = 0; b < kBatch; ++b) now[b] = q[b];
+    if (it + 1 < n) part.load(q, it + 1);
+    u64 s = 0;
+    if (__any_sync(kFull, batch_max_nan<DT>(now) >= lo)) {
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        float x[N];
+        unpack<DT>(now[b], x);
+        uint32_t win = 0;
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+          const bool in0 = x[i] >= hi, in1 = x[i + 1] >= hi;
+          c += in0 + in1;
+          u64 v0, v1;
+          float t0, t1;
+          wt.template pair<DT>(in0 ? x[i] : -INFINITY, in1 ? x[i + 1] : -INFINITY, v0, v1, t0, t1);
+          s += v0;
+          s += v1;
+          win |= (uint32_t)(!in0 && x[i] >= lo) << i | (uint32_t)(!in1 && x[i + 1] >= lo) << (i + 1);
+        }
+        if (win) {
+          int at = atomicAdd(&sh.n_list, __popc(win));
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (win >> i & 1) {
+              if (at < kList)
+                sh.keys[at] =
+                    make_key(order_bits(x[i]), (j + b * 32) * N - part.row.head + i);
+              ++at;
+            }
+        }
+      }
     }
+    add_segment<true>(sh, it, s);
     mass += s;
   }
   count = c;
@@ -385,82 +578,197 @@ __device__ __noinline__ u64 search(Team<SPLIT>& team, const Part<DT>& part, cons
 
 // ------------------------------------------------------------------------------ the list
 
-// A bound that at least k of this CTA's index entries reach, and not many more where it can be
-// had: halving over the entries.
+// A bound that at least k of this CTA's tokens reach, and not many more where it can be had: the k-th
+// largest of its threads' largest logits, or, for a larger k, about that of the index entries.
 __device__ __noinline__ uint32_t index_bound(Shared& sh, int groups, int k, uint32_t top) {
   const int tid = threadIdx.x;
-  auto count = [&](uint32_t v) {
-    int n = 0;
-    for (int g = 0; g < groups; ++g) n += sh.index[g * kThreads + tid] >= v;
-    n = __reduce_add_sync(kFull, n);
-    if ((tid & 31) == 0) sh.red[0][tid >> 5] = (u64)n;
-    __syncthreads();
-    n = 0;
+  uint32_t e[kGroupsMost], mine = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) n += (int)sh.red[0][w];
-    __syncthreads();
-    return n;
-  };
-  uint32_t lo = 1, hi = top + 1;  // top >= every entry
-  if (count(1) < k) return 1;
-  while (hi - lo > 1) {
-    const uint32_t mid = lo + (hi - lo) / 2;
-    const int n = count(mid);
-    if (n < k) {
-      hi = mid;
-    } else {
-      lo = mid;
-      if (n <= k + k / 8) break;
-    }
+  for (int g = 0; g < kGroupsMost; ++g) {
+    e[g] = g < groups ? sh.index[g * kThreads + tid] : 0;
+    mine = e[g] > mine ? e[g] : mine;
   }
+  if (k <= kTopsMost) {
+    sh.tops[tid] = mine;
+    __syncthreads();
+    int place = 0;
+#pragma unroll 8
+    for (int i = 0; i < kThreads; i += 4) {
+      const uint4 o = *reinterpret_cast<const uint4*>(&sh.tops[i]);
+      place += (o.x > mine || (o.x == mine && i < tid)) +
+               (o.y > mine || (o.y == mine && i + 1 < tid)) +
+               (o.z > mine || (o.z == mine && i + 2 < tid)) +
+               (o.w > mine || (o.w == mine && i + 3 < tid));
+    }
+    if (place == k - 1) sh.bound = mine ? mine : 1;
+    __syncthreads();
+    return sh.bound;
+  }
+  // three pivots a step
+  uint32_t lo = 1, hi = top;  // hi + 1 is more than every entry; lo is enough, or all there are
+  uint32_t* part = reinterpret_cast<uint32_t*>(sh.red);
+  for (int turn = 0; lo < hi; turn ^= 1) {
+    const uint32_t q = (hi - lo) / 4 + 1;
+    const uint32_t p1 = lo + q, p2 = p1 + q < hi ? p1 + q : hi, p3 = p2 + q < hi ? p2 + q : hi;
+    uint32_t n = 0;
+#pragma unroll
+    for (int g = 0; g < kGroupsMost; ++g)
+      n += (uint32_t)(e[g] >= p1) + ((uint32_t)(e[g] >= p2) << 10) +
+           ((uint32_t)(e[g] >= p3) << 20);
+    const uint32_t n1 = __reduce_add_sync(kFull, n & 1023u),
+                   n2 = __reduce_add_sync(kFull, n >> 10 & 1023u),
+                   n3 = __reduce_add_sync(kFull, n >> 20);
+    if ((tid & 31) < 3)
+      part[(turn * 3 + (tid & 31)) * kWarps + (tid >> 5)] =
+          (tid & 31) == 0 ? n1 : (tid & 31) == 1 ? n2 : n3;
+    __syncthreads();
+    int c1 = 0, c2 = 0, c3 = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      c1 += (int)part[(turn * 3 + 0) * kWarps + w];
+      c2 += (int)part[(turn * 3 + 1) * kWarps + w];
+      c3 += (int)part[(turn * 3 + 2) * kWarps + w];
+    }
+    int got;
+    if (c3 >= k) {
+      lo = p3;
+      got = c3;
+    } else if (c2 >= k) {
+      lo = p2;
+      hi = p3 - 1;
+      got = c2;
+    } else if (c1 >= k) {
+      lo = p1;
+      hi = p2 - 1;
+      got = c1;
+    } else {
+      hi = p1 - 1;
+      continue;
+    }
+    if (got <= k + k / 8) break;
+  }
+  __syncthreads();
   return lo;
 }
 
+template <bool SPLIT>
+__device__ __noinline__ int gather(Team<SPLIT>& team);
+
 // Tokens of bits >= bound of the whole row in the leader's list. Returns how many there are; more
-// than kList means that they are not all there.
+// than kList means that they are not all there. The batches that reach the bound are listed, then
+// their pieces dealt to the lanes.
 template <int DT, bool SPLIT>
 __device__ __noinline__ int collect(Team<SPLIT>& team, const Part<DT>& part, int per_group,
                                     uint32_t bound) {
   constexpr int N = Row<DT>::N;
+  constexpr int kAtOnce = 4;  // pieces in flight
   Shared& sh = team.sh;
-  Shared* lead = team.leader();
-  if (team.part == 0 && threadIdx.x == 0) sh.n_list = 0;
-  team.sync();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) sh.n_list = sh.n_hits = 0;
+  __syncthreads();
   const int n = part.steps(), groups = (n + per_group - 1) / per_group;
   for (int g = 0; g < groups; ++g) {
-    if (sh.index[g * kThreads + threadIdx.x] < bound) continue;
-    const int end = min(n, (g + 1) * per_group);
-    for (int it = g * per_group; it < end; ++it) {
-      const int j = part.first(it);
+    const bool hit = sh.index[g * kThreads + tid] >= bound;
+    const uint32_t all = __ballot_sync(kFull, hit);
+    if (!all) continue;
+    int at = 0;
+    if (lane == 0) at = atomicAdd(&sh.n_hits, __popc(all));
+    at = __shfl_sync(kFull, at, 0) + __popc(all & ((1u << lane) - 1));
+    if (hit && at < kHits) sh.hits[at] = (uint16_t)(g * kThreads + tid);
+  }
+  __syncthreads();
+  const int hits = sh.n_hits;
+  if (hits <= kHits) {
+    const float least = order_value(bound > 0x00800000u ? bound : 0x00800000u);
+    const int pieces = hits * per_group * kBatch;
+    for (int base = warp * 32; base < pieces; base += kThreads * kAtOnce) {
+      uint4 q[kAtOnce];
+      int j[kAtOnce];
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        float x[N];
-        unpack<DT>(part.row.load_any(j + b * 32, part.j1), x);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const uint32_t bits = order_bits(x[i]);
-          if (bits >= bound) {
-            const int at = atomicAdd(&lead->n_list, 1);
-            if (at < kList)
-              lead->keys[at] = make_key(bits, (j + b * 32) * N - part.row.head + i);
-          }
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int at = base + i * kThreads + lane, batch = at / kBatch;
+        j[i] = part.j1;
+        if (at < pieces) {
+          const int entry = sh.hits[batch / per_group], t = entry % kThreads;
+          const int it = entry / kThreads * per_group + batch % per_group;
+          j[i] = part.j0 + it * kStep + (t >> 5) * kWarpStep + (t & 31) + at % kBatch * 32;
         }
+        q[i] = part.row.load(j[i], part.j1);
+      }
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        if (part.row.partial(j[i], part.j1)) q[i] = part.row.load_partial(j[i]);
+        float x[N];
+        unpack<DT>(q[i], x);
+        uint32_t in = 0;
+#pragma unroll
+        for (int e = 0; e < N; ++e) in |= (uint32_t)(x[e] >= least) << e;
+        int up = __popc(in);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(kFull, up, o);
+          if (lane >= o) up += y;
+        }
+        int at = 0;
+        if (lane == 31 && up) at = atomicAdd(&sh.n_list, up);
+        at = __shfl_sync(kFull, at, 31) + up - __popc(in);
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (in >> e & 1) {
+            if (at < kList) sh.keys[at] = make_key(order_bits(x[e]), j[i] * N - part.row.head + e);
+            ++at;
+          }
       }
     }
+  } else if (tid == 0) {
+    sh.n_list = kList + 1;
   }
-  team.sync();
-  return lead->n_list;
+  __syncthreads();
+  return gather<SPLIT>(team);
 }
 
-// Descending order of sh.keys[0 .. n).
+// The parts' lists behind one another in the leader's. Returns the number of keys, as collect does.
+template <bool SPLIT>
+__device__ int gather(Team<SPLIT>& team) {
+  Shared& sh = team.sh;
+  if constexpr (SPLIT) {
+    team.cluster.sync();
+    int before = 0, total = 0;
+    for (int q = 0; q < team.parts; ++q) {
+      if (q == team.part) before = total;
+      total += team.cluster.map_shared_rank(&sh, q)->n_list;
+    }
+    if (total <= kList && team.part) {
+      u64* to = team.leader()->keys + before;
+      for (int i = threadIdx.x; i < sh.n_list; i += kThreads) to[i] = sh.keys[i];
+    }
+    team.cluster.sync();
+    return total;
+  }
+  return sh.n_list;
+}
+
+// Descending order of sh.keys[0 .. n): by counting the larger ones, or a bitonic network, whose
+// steps over 32 keys or fewer stay within a warp's 64.
 __device__ __noinline__ void sort_keys(Shared& sh, int n) {
-  int P = 32;
+  const int tid = threadIdx.x;
+  if (n <= kThreads) {
+    const u64 key = tid < n ? sh.keys[tid] : 0;
+    int place = 0;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) place += sh.keys[i] > key;
+    __syncthreads();
+    if (tid < n) sh.keys[place] = key;
+    __syncthreads();
+    return;
+  }
+  int P = 2 * kThreads;
   while (P < n) P *= 2;
-  for (int i = n + threadIdx.x; i < P; i += kThreads) sh.keys[i] = 0;
+  for (int i = n + tid; i < P; i += kThreads) sh.keys[i] = 0;
   __syncthreads();
   for (int size = 2; size <= P; size *= 2) {
     for (int o = size / 2; o > 0; o /= 2) {
-      for (int i = threadIdx.x; i < P / 2; i += kThreads) {
+      for (int i = tid; i < P / 2; i += kThreads) {
         const int a = 2 * i - (i & (o - 1)), b = a + o;
         const u64 x = sh.keys[a], y = sh.keys[b];
         if ((x < y) == ((a & size) == 0)) {
@@ -468,7 +776,10 @@ __device__ __noinline__ void sort_keys(Shared& sh, int n) {
           sh.keys[b] = x;
         }
       }
-      __syncthreads();
+      if (o > 32 || (o == 1 && size >= 64))
+        __syncthreads();
+      else
+        __syncwarp();
     }
   }
 }
@@ -498,14 +809,22 @@ __device__ __noinline__ u64 scan(Shared& sh, u64 v, u64& total) {
 __device__ __forceinline__ float key_value(u64 key) { return order_value((uint32_t)(key >> 32)); }
 __device__ __forceinline__ int key_id(u64 key) { return (int)(0xffffffffu - (uint32_t)key); }
 
-// The three rules on the n sorted keys of the list, in one CTA: sh.kept tokens of sh.total mass
-// stay, sh.limit is the last one's key. `all` is the mass that p refers to where the list is only
-// the row's beginning (0: the list's first sh.k). False if the nucleus ends behind the list, which
-// holds every token of bits >= bound.
+// order_bits of about the least logit of bin b.
+__device__ __forceinline__ uint32_t edge_bits(const Weigher& wt, int b) {
+  const float x = wt.m - ((float)b + 0.5f) / 32.0f / wt.ch;
+  const uint32_t bits = x > -INFINITY ? order_bits(x) : 1;
+  return bits > 0x00800000u ? bits : 0x00800000u;  // of the lowest finite number
+}
+
+// The three rules on the n sorted keys of the list, of which top-k leaves nk, in one CTA: sh.kept of
+// them, of sh.total mass, stay, sh.limit is the last one's key. `all` is the mass that p refers to
+// where that is not the nk tokens' own (0); the list may begin behind a mass of `above`. False
+// if the nucleus ends before or behind the list, which holds every token of bits >= bound (and
+// before that, unless `above`).
 template <int DT>
-__device__ __noinline__ bool rules(Shared& sh, const Weigher& wt, int n, u64 all, uint32_t bound) {
+__device__ __noinline__ bool rules(Shared& sh, const Weigher& wt, int n, int nk, u64 all,
+                                   u64 above, uint32_t bound) {
   const int per = (n + kThreads - 1) / kThreads, first = threadIdx.x * per;
-  const int nk = sh.k > 0 && sh.k < n ? sh.k : n;
   u64 mine = 0, w[kList / kThreads];
 #pragma unroll
   for (int i = 0; i < kList / kThreads; ++i) {
@@ -517,7 +836,9 @@ __device__ __noinline__ bool rules(Shared& sh, const Weigher& wt, int n, u64 all
   u64 mass;
   const u64 at = scan(sh, mine, mass);
   const bool by_p = sh.p < 1.0f;
-  const u64 need = by_p ? exact_share(sh.p, all ? all : mass, true) : ~0ull;
+  u64 need = by_p ? exact_share(sh.p, all ? all : mass, true) : ~0ull;
+  if (above && need <= above) return false;
+  need -= above;
   if (by_p && all && mass < need && sh.tm < bound) return false;
   u64 before = at;
   int np = 0, nm = 0;
@@ -529,22 +850,121 @@ __device__ __noinline__ bool rules(Shared& sh, const Weigher& wt, int n, u64 all
     }
     before += w[i];
   }
-  u64 t, counts = (u64)np << 32 | (u64)nm;
-  scan(sh, counts, t);
+  np = __reduce_add_sync(kFull, np);
+  nm = __reduce_add_sync(kFull, nm);
+  if ((threadIdx.x & 31) == 0) sh.red[1][threadIdx.x >> 5] = (u64)np << 32 | (u64)nm;
+  __syncthreads();
+  u64 t = 0;
+#pragma unroll
+  for (int q = 0; q < kWarps; ++q) t += sh.red[1][q];
   int kept = min((int)(t >> 32), (int)(uint32_t)t);
   kept = kept > 1 ? kept : 1;
-  mine = 0;
+  if (first < kept && kept <= first + per) {
+    u64 sum = at;
 #pragma unroll
-  for (int i = 0; i < kList / kThreads; ++i)
-    if (i < per && first + i < kept) mine += w[i];
-  scan(sh, mine, t);
-  if (threadIdx.x == 0) {
+    for (int i = 0; i < kList / kThreads; ++i)
+      if (first + i < kept) sum += w[i];
     sh.kept = kept;
-    sh.total = t;
+    sh.total = sum;
     sh.limit = sh.keys[kept - 1];
   }
   __syncthreads();
   return true;
+}
+
+// Where a share p of the mass of sh.bins (of every part) ends: bins sh.bin_lo .. sh.bin_hi, with
+// the number of tokens before and in them. The bins' masses are their tokens' number times the
+// middle one's, so the place is a guess, to be checked: the bins in which a share of p (1 -+ kSure)
+// ends, or p alone where those do not fit the list. With k it is the bin of the k-th token.
+constexpr float kSure = 0.0005f;
+template <bool SPLIT>
+__device__ __noinline__ void find_window(Team<SPLIT>& team, float p, int k) {
+  Shared& sh = team.sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  team.sync();
+  uint32_t n[kBinsThread], count = 0;
+  float e[kBinsThread], mine = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kBinsThread; ++i) {
+    const int at = tid * kBinsThread + i;
+    n[i] = 0;
+    for (int q = 0; q < team.parts; ++q) {
+      if constexpr (SPLIT)
+        n[i] += team.cluster.map_shared_rank(&sh, q)->bins[at];
+      else
+        n[i] += sh.bins[at];
+    }
+    if (at == kBins - 1) n[i] = 0;  // no mass
+    e[i] = (float)n[i] * (k ? 1.0f : fast_exp2(at * -0.03125f));
+    mine += e[i];
+    count += n[i];
+  }
+  float up = mine;
+  uint32_t cup = count;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float y = __shfl_up_sync(kFull, up, o);
+    const uint32_t z = __shfl_up_sync(kFull, cup, o);
+    if (lane >= o) {
+      up += y;
+      cup += z;
+    }
+  }
+  if (lane == 31) {
+    sh.fred[warp] = up;
+    sh.red[0][warp] = cup;
+  }
+  if (tid < 3) {
+    sh.edge[tid] = kBins - 1;
+    sh.before[tid] = 0;
+  }
+  __syncthreads();
+  float c = up - mine, total = 0.0f;
+  uint32_t before = cup - count;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) {
+      c += sh.fred[w];
+      before += (uint32_t)sh.red[0][w];
+    }
+    total += sh.fred[w];
+  }
+  // thread ranges follow one another, so the three places are each in one thread's
+  float share[3] = {total * p * (1.0f - kSure), total * p, total * p * (1.0f + kSure)};
+  if (k) share[0] = share[1] = share[2] = (float)k;  // whole numbers below 2^24
+#pragma unroll
+  for (int i = 0; i < kBinsThread; ++i) {
+    const float next = c + e[i];
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+      if (n[i] && c < share[q] && next >= share[q]) {
+        sh.edge[q] = tid * kBinsThread + i;
+        sh.before[q] = (int)(q == 2 ? before + n[i] : before);  // up to the bin, or with it
+        if (q < 2) sh.cum[q] = c / total;
+        if (q == 1) sh.in = (int)n[i];
+      }
+    c = next;
+    before += n[i];
+  }
+  __syncthreads();
+  if (tid == 0) {
+    uint32_t all = 0;
+    for (int w = 0; w < kWarps; ++w) all += (uint32_t)sh.red[0][w];
+    if (sh.edge[2] == kBins - 1) sh.before[2] = (int)all;
+    int lo = sh.edge[0], hi = sh.edge[2];
+    sh.guess = sh.cum[0];
+    sh.n_above = sh.before[0];
+    sh.n_window = sh.before[2] - sh.before[0];
+    if (sh.n_window > kListMost && sh.edge[1] < kBins - 1) {
+      lo = hi = sh.edge[1];
+      sh.guess = sh.cum[1];
+      sh.n_above = sh.before[1];
+      sh.n_window = sh.in;
+    }
+    sh.bin_lo = lo;
+    sh.bin_hi = hi;
+  }
+  team.sync();
 }
 
 // ------------------------------------------------------------------------------ outputs
@@ -578,8 +998,22 @@ __device__ __forceinline__ u64 draw_at(const SampleArgs& a, int row, u64 total) 
 template <int DT>
 __device__ __noinline__ void draw_list(Shared& sh, const SampleArgs& a, int row, const Weigher& wt,
                                        float scale) {
-  u64* bucket = reinterpret_cast<u64*>(sh.index);
+  u64* bucket = sh.bucket;
   const int tid = threadIdx.x, n = sh.kept;
+  if (n <= kThreads) {  // every token against every other
+    const u64 key = tid < n ? sh.keys[tid] : 0;
+    const u64 w = wt.template operator()<DT>(tid < n ? key_value(key) : -INFINITY);
+    bucket[tid] = w;
+    __syncthreads();
+    u64 below = 0;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i)
+      if ((uint32_t)sh.keys[i] > (uint32_t)key) below += bucket[i];  // lower ids
+    const u64 at = draw_at(a, row, sh.total);
+    if (tid < n && below <= at && at < below + w)
+      write_draw(a, row, key_id(key), key_value(key), wt, scale, sh.total, n);
+    return;
+  }
   int by = 0;
   while ((a.V - 1) >> by >= kBuckets) ++by;
   bucket[tid] = 0;
@@ -601,8 +1035,8 @@ __device__ __noinline__ void draw_list(Shared& sh, const SampleArgs& a, int row,
   __syncthreads();
   const int hit = sh.hit;
   const u64 rest = sh.rest;
-  // this bucket's tokens, few of them, behind one another in place of the buckets
-  u64* some = bucket;
+  // this bucket's tokens, few of them, behind one another in place of the index
+  u64* some = sh.seg;
   if (tid == 0) sh.done = 0;
   __syncthreads();
   for (int i = tid; i < n; i += kThreads)
@@ -756,8 +1190,8 @@ __device__ __noinline__ void read_params(Shared& sh, const SampleArgs& a, int ro
   sh.cl = (float)(c - (double)sh.ch);
   sh.k = greedy ? 1 : (k <= 0 || k >= a.V ? 0 : k);
   sh.p = p < 0.0f ? 0.0f : p;
-  sh.tm = 1;                       // min_p itself, until the row's maximum is known
-  sh.rest = mp > 0.0f ? __float_as_uint(mp < 1.0f ? mp : 1.0f) : 0;
+  sh.tm = 1;                       // until the row's maximum is known
+  sh.mp = mp > 0.0f ? __float_as_uint(mp < 1.0f ? mp : 1.0f) : 0;
 }
 
 template <int DT, bool SPLIT, bool WRITE>
@@ -774,7 +1208,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
   while ((1 << bits) < a.V) ++bits;
   const int S = min(46, 62 - bits);
   wt.shift = 61 - S;
-  wt.least = -(float)(S + 1);
+  wt.most = (float)(S + 1);
 
   for (int row = SPLIT ? blockIdx.x / parts : blockIdx.x; row < rows; row += gridDim.x) {
     Part<DT> part{Row<DT>(a.x, (size_t)row * a.ld, a.V), 0, 0};
@@ -789,6 +1223,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
 
     // the largest logit, and those of the batches
     float m = -INFINITY;
+    uint32_t finite = 0;  // tokens above -inf
     {
       uint4 q[2][kBatch];
       part.load(q[0], 0);
@@ -797,6 +1232,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
       int in = 0, g = 0;
       auto take = [&](const uint4 (&w)[kBatch]) {
         e = max_nan(e, batch_max_nan<DT>(w));
+        finite += count_finite<DT>(w);
         if (++in == per_group) {
           sh.index[g++ * kThreads + tid] = order_bits(e);
           m = max_nan(m, e);
@@ -849,9 +1285,9 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
     wt.ch = sh.ch;
     wt.cl = sh.cl;
     const float scale = sh.scale;
-    if (tid == 0 && sh.rest) {
+    if (tid == 0 && sh.mp) {
       // the least fp32 number x with (x - m) / T >= log(min_p)
-      const double t = (double)wt.m + log((double)__uint_as_float((uint32_t)sh.rest)) / (double)scale;
+      const double t = (double)wt.m + log((double)__uint_as_float(sh.mp)) / (double)scale;
       float f = __double2float_ru(t);
       f = f < wt.m ? f : wt.m;
       sh.tm = f > -INFINITY ? order_bits(f) : 1;
@@ -861,7 +1297,6 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
     const bool by_p = sh.p < 1.0f, by_m = sh.tm > 1;
     const uint32_t tm = sh.tm;
 
-    bool listed = false;
     u64 limit = 0, total = 0;
     int kept = 0;
     if (k == 1) {
@@ -886,39 +1321,125 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
       if (!WRITE && team.part == 0 && tid == 0)
         write_draw(a, row, key_id(limit), wt.m, wt, scale, total, 1);
     } else if (k || by_p || by_m) {
-      // the mass that p refers to
-      u64 all = 0;
-      if (!k && by_p) {
+      u64 all = 0;  // the mass that p refers to, where that is not the list's
+      uint32_t bound = tm;
+      bool list = true, window = false, binned = k ? k > kListTop : by_p;
+      if (k && !binned) {
+        if constexpr (SPLIT) {
+          // as many tokens in every part as make k together, or k in one
+          bound = ~(uint32_t)team.max(~index_bound(sh, groups, (k + team.parts - 1) / team.parts, top));
+          if (bound == 1) bound = (uint32_t)team.max(index_bound(sh, groups, k, top));
+        } else {
+          bound = index_bound(sh, groups, k, top);
+        }
+      }
+      while (true) {
+        if (binned) {
+          for (int i = tid; i < kBins; i += kThreads) sh.bins[i] = 0;
+          __syncthreads();
+          const u64 mass = team.sum(pass_all<DT, false, true>(sh, part, wt), 0).a;
+          find_window<SPLIT>(team, sh.p, k);
+          list = sh.n_above + sh.n_window <= kListMost;
+          window = sh.bin_lo > 0 && sh.n_window <= kListMost;
+          bound = edge_bits(wt, sh.bin_hi);
+          if (!k) {
+            all = mass;
+            // min-p's last token is enough, and may be before where the nucleus seems to end
+            if (tm > bound || !list) bound = tm;
+            if (!list) list = by_m && (sh.bin_lo == 0 || tm > edge_bits(wt, sh.bin_lo - 1));
+          }
+        }
+        if (list) {
+          const int n = collect<DT, SPLIT>(team, part, per_group, bound);
+          if (n <= kList) {
+            if (team.part == 0) {
+              sort_keys(sh, n);
+              const bool ok = (k == 0 || k <= n || bound <= 0x00800000u) &&
+                              rules<DT>(sh, wt, n, k && k < n ? k : n, all, 0, bound);
+              if (tid == 0) sh.done = ok;
+            }
+            team.sync();
+            const Shared* lead = team.leader();
+            if (lead->done) {
+              limit = lead->limit;
+              total = lead->total;
+              kept = lead->kept;
+              if (SPLIT) team.sync();
+              if (!WRITE && team.part == 0) draw_list<DT>(sh, a, row, wt, scale);
+            }
+          }
+        }
+        if (kept || !k || binned) break;
+        binned = true;  // too many tokens of the k-th logit, or near it
+      }
+      for (int turn = 0; !kept && window && turn < 3; ++turn) {
+        // too many for the list: its piece around the border, the mass before it
+        if (tid == 0) sh.n_list = 0;
+        const uint32_t lo_bits = edge_bits(wt, sh.bin_hi), hi_bits = edge_bits(wt, sh.bin_lo - 1);
+        __syncthreads();
         u64 mm, cc;
-        pass<DT, true, false>(sh, part, wt, 0, mm, cc);
-        all = team.sum(mm, cc).a;
-      }
-      for (int want = k ? k : kTryFirst; !listed && want <= kListTop;
-           want = !k && by_p && want < kTryNext ? kTryNext : kListTop + 1) {
-        uint32_t bound = tm;
-        if (k || by_p) {
-          bound = index_bound(sh, groups, want, top);
-          if (SPLIT) bound = (uint32_t)team.max(bound);
+        pass_window<DT>(sh, part, wt, order_value(lo_bits), order_value(hi_bits), mm, cc);
+        const auto s = team.sum(mm, cc);
+        const int n = gather<SPLIT>(team), nk = k ? k - (int)s.b : n;
+        window = n <= kList && nk > 0 && nk <= n;
+        if (window) {
+          if (team.part == 0) {
+            sort_keys(sh, n);
+            // a truncation that min-p cuts shorter is not decided here, nor top-p of this top-k
+            bool ok = false;
+            if (k && by_p) {
+              if (tid == 0) sh.limit = sh.keys[nk - 1];
+            } else {
+              ok = rules<DT>(sh, wt, n, nk, all, s.a, ~0u) && (uint32_t)(sh.limit >> 32) >= tm;
+            }
+            if (tid == 0) sh.done = ok;
+            // what stays of the list, into the segments
+            if (ok && !WRITE)
+              for (int base = 0; base < sh.kept; base += kThreads) {
+                const bool in = base + tid < sh.kept;
+                const u64 key = in ? sh.keys[base + tid] : 0;
+                const u64 w = wt.template operator()<DT>(in ? key_value(key) : -INFINITY);
+                if (!in) continue;
+                const int j = (key_id(key) + part.row.head) / Row<DT>::N;
+                const int per = part.j1 - part.j0, q = SPLIT ? j / per : 0;
+                Shared* to = &sh;
+                if constexpr (SPLIT) to = team.cluster.map_shared_rank(&sh, q);
+                atomicAdd(&to->seg[(j - q * per) / kWarpStep], w);
+              }
+          }
+          team.sync();
+          const Shared* lead = team.leader();
+          if (lead->done) {
+            limit = lead->limit;
+            total = s.a + lead->total;
+            kept = (int)s.b + lead->kept;
+            u64 own = 0;
+            if (!WRITE)
+              for (int i = tid; i < steps * kWarps; i += kThreads) own += sh.seg[i];
+            const auto d = team.sum(own, 0);
+            if (!WRITE) {
+              const u64 at = draw_at(a, row, total);
+              if (d.before <= at && at < d.before + d.own)
+                draw_segment<DT>(sh, a, row, part, wt, scale, limit, at - d.before, total, kept);
+            }
+          } else {
+            if (k && by_p) limit = lead->limit;
+            // once more by the mass that there is before the window
+            window = !k;
+            if (window) {
+              const float off = (float)((double)s.a / (double)all) - sh.guess;
+              __syncthreads();
+              find_window<SPLIT>(team, sh.p - off, 0);
+              window = sh.bin_lo > 0 && sh.n_window <= kListMost;
+            } else {
+              team.sync();
+            }
+          }
         }
-        const int n = collect<DT, SPLIT>(team, part, per_group, bound);
-        if (n > kList) break;
-        if (team.part == 0) {
-          sort_keys(sh, n);
-          const bool ok = rules<DT>(sh, wt, n, all, bound);
-          if (tid == 0) sh.done = ok;
-        }
-        team.sync();
-        listed = team.leader()->done;
-        team.sync();
       }
-      if (listed) {
-        limit = team.leader()->limit;
-        total = team.leader()->total;
-        kept = team.leader()->kept;
-        if (SPLIT) team.sync();
-        if (!WRITE && team.part == 0) draw_list<DT>(sh, a, row, wt, scale);
-      } else {
-        if (k) limit = search<DT, SPLIT, false>(team, part, wt, 0, (u64)k, top_key);
+      if (!kept) {
+        const u64 key_m = (u64)tm << 32;
+        if (k && !limit) limit = search<DT, SPLIT, false>(team, part, wt, 0, (u64)k, top_key);
         if (by_p) {
           if (k) {
             u64 mm, cc;
@@ -926,16 +1447,26 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
             all = team.sum(mm, cc).a;
           }
           const u64 need = exact_share(sh.p, all, true);
-          limit = search<DT, SPLIT, true>(team, part, wt, limit, need ? need : 1, top_key);
+          bool more = true;  // whether the nucleus may end before min-p's last token
+          if (by_m) {
+            u64 mm, cc;
+            pass<DT, true, false>(sh, part, wt, key_m > limit ? key_m : limit, mm, cc);
+            more = team.sum(mm, cc).a > need;
+          }
+          if (more) limit = search<DT, SPLIT, true>(team, part, wt, limit, need ? need : 1, top_key);
         }
-        const u64 key_m = (u64)tm << 32;
         limit = by_m && key_m > limit ? key_m : limit;
       }
     }
     if (!kept) {
       u64 mm, cc;
       __syncthreads();
-      pass<DT, true, true>(sh, part, wt, limit, mm, cc);
+      if (limit) {
+        pass<DT, true, true>(sh, part, wt, limit, mm, cc);
+      } else {
+        mm = pass_all<DT, !WRITE, false>(sh, part, wt);
+        cc = finite;
+      }
       const auto s = team.sum(mm, cc);
       total = s.a;
       kept = (int)s.b;
