@@ -40,6 +40,7 @@ namespace cg = cooperative_groups;
 typedef unsigned long long u64;
 
 constexpr int kThreads = 256;
+constexpr int kCtas = 3;                        // of an SM
 constexpr int kWarps = kThreads / 32;
 constexpr int kBatch = 4;                       // 16-byte pieces of a thread's batch
 constexpr int kWarpStep = 32 * kBatch;          // consecutive pieces of a warp: a segment
@@ -68,18 +69,22 @@ struct Shared {
   };
   u64 keys[kList];           // listed tokens, sorted
   uint32_t bins[kBins];      // tokens by their mass
-  alignas(16) uint32_t tops[kThreads];  // largest order_bits of a thread's share
-  uint16_t hits[kHits];      // index entries that reach a bound
+  uint32_t slice[kBins / 2]; // of the cluster's, this part's share
+  union {
+    uint16_t hits[kHits];      // index entries that reach a bound
+    u64 picked[2][kBuckets];   // masses of ranges, keys of one
+  };
   int n_list, n_hits;
-  uint32_t bound;
   u64 pub[2][2];             // what a CTA shows its cluster
   u64 red[3][kWarps];
+  uint32_t best[kWarps];
   float fred[kWarps];
   // the row's parameters
   float scale, ch, cl;
   int k;
   float p;
-  uint32_t mp;               // bits of min_p
+  bool by_m;
+  double below;              // log(min_p) T
   uint32_t tm;               // order_bits of the least logit that min-p leaves
   // decided by one thread or CTA for the others
   u64 limit, total, rest;
@@ -266,37 +271,35 @@ struct Team {
         sh.pub[turn][1] = s.b;
       }
       cluster.sync();
-      s.a = s.b = 0;
-      for (int q = 0; q < parts; ++q) {
-        const Shared* o = cluster.map_shared_rank(&sh, q);
-        if (q == part) s.before = s.a;
-        s.a += o->pub[turn][0];
-        s.b += o->pub[turn][1];
+      // lane q: part q
+      const Shared* o = cluster.map_shared_rank(&sh, lane < parts ? lane : 0);
+      u64 x = lane < parts ? o->pub[turn][0] : 0, y = lane < parts ? o->pub[turn][1] : 0;
+#pragma unroll
+      for (int d = 1; d < kMaxSplit; d <<= 1) {
+        const u64 z = __shfl_up_sync(kFull, x, d);
+        if (lane >= d) x += z;
+        y += __shfl_xor_sync(kFull, y, d);
       }
+      s.a = __shfl_sync(kFull, x, kMaxSplit - 1);
+      s.b = __shfl_sync(kFull, y, 0);
+      s.before = __shfl_sync(kFull, x, part) - s.own;
       turn ^= 1;
     } else {
       __syncthreads();
     }
     return s;
   }
-  __device__ __noinline__ u64 max(u64 a) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const u64 y = __shfl_xor_sync(kFull, a, o);
-      a = a > y ? a : y;
-    }
-    if ((threadIdx.x & 31) == 0) sh.red[0][threadIdx.x >> 5] = a;
+  __device__ __noinline__ uint32_t max(uint32_t a) {
+    const int lane = threadIdx.x & 31;
+    a = __reduce_max_sync(kFull, a);
+    if (lane == 0) sh.best[threadIdx.x >> 5] = a;
     __syncthreads();
-    a = sh.red[0][0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) a = sh.red[0][w] > a ? sh.red[0][w] : a;
+    a = __reduce_max_sync(kFull, sh.best[lane & (kWarps - 1)]);
     if constexpr (SPLIT) {
       if (threadIdx.x == 0) sh.pub[turn][0] = a;
       cluster.sync();
-      for (int q = 0; q < parts; ++q) {
-        const u64 y = cluster.map_shared_rank(&sh, q)->pub[turn][0];
-        a = a > y ? a : y;
-      }
+      a = __reduce_max_sync(
+          kFull, (uint32_t)cluster.map_shared_rank(&sh, lane < parts ? lane : 0)->pub[turn][0]);
       turn ^= 1;
     } else {
       __syncthreads();
@@ -589,20 +592,18 @@ __device__ __noinline__ uint32_t index_bound(Shared& sh, int groups, int k, uint
     mine = e[g] > mine ? e[g] : mine;
   }
   if (k <= kTopsMost) {
-    sh.tops[tid] = mine;
-    __syncthreads();
-    int place = 0;
-#pragma unroll 8
-    for (int i = 0; i < kThreads; i += 4) {
-      const uint4 o = *reinterpret_cast<const uint4*>(&sh.tops[i]);
-      place += (o.x > mine || (o.x == mine && i < tid)) +
-               (o.y > mine || (o.y == mine && i + 1 < tid)) +
-               (o.z > mine || (o.z == mine && i + 2 < tid)) +
-               (o.w > mine || (o.w == mine && i + 3 < tid));
+    uint32_t lo = 1, hi = top;  // lo is enough, or all there are
+    while (lo < hi) {
+      const uint32_t mid = lo + (hi - lo) / 2 + 1;
+      const int n = __syncthreads_count(mine >= mid);
+      if (n < k) {
+        hi = mid - 1;
+      } else {
+        lo = mid;
+        if (n <= k + k / 8) break;
+      }
     }
-    if (place == k - 1) sh.bound = mine ? mine : 1;
-    __syncthreads();
-    return sh.bound;
+    return lo;
   }
   // three pivots a step
   uint32_t lo = 1, hi = top;  // hi + 1 is more than every entry; lo is enough, or all there are
@@ -733,11 +734,10 @@ __device__ int gather(Team<SPLIT>& team) {
   Shared& sh = team.sh;
   if constexpr (SPLIT) {
     team.cluster.sync();
-    int before = 0, total = 0;
-    for (int q = 0; q < team.parts; ++q) {
-      if (q == team.part) before = total;
-      total += team.cluster.map_shared_rank(&sh, q)->n_list;
-    }
+    const int lane = threadIdx.x & 31;
+    int before = team.cluster.map_shared_rank(&sh, lane < team.parts ? lane : 0)->n_list;
+    const int total = __reduce_add_sync(kFull, lane < team.parts ? before : 0);
+    before = __reduce_add_sync(kFull, lane < team.part ? before : 0);
     if (total <= kList && team.part) {
       u64* to = team.leader()->keys + before;
       for (int i = threadIdx.x; i < sh.n_list; i += kThreads) to[i] = sh.keys[i];
@@ -748,40 +748,16 @@ __device__ int gather(Team<SPLIT>& team) {
   return sh.n_list;
 }
 
-// Descending order of sh.keys[0 .. n): by counting the larger ones, or a bitonic network, whose
-// steps over 32 keys or fewer stay within a warp's 64.
+// Descending order of sh.keys[0 .. n), n <= kThreads, by counting the larger ones.
 __device__ __noinline__ void sort_keys(Shared& sh, int n) {
   const int tid = threadIdx.x;
-  if (n <= kThreads) {
-    const u64 key = tid < n ? sh.keys[tid] : 0;
-    int place = 0;
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) place += sh.keys[i] > key;
-    __syncthreads();
-    if (tid < n) sh.keys[place] = key;
-    __syncthreads();
-    return;
-  }
-  int P = 2 * kThreads;
-  while (P < n) P *= 2;
-  for (int i = n + tid; i < P; i += kThreads) sh.keys[i] = 0;
+  const u64 key = tid < n ? sh.keys[tid] : 0;
+  int place = 0;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) place += sh.keys[i] > key;
   __syncthreads();
-  for (int size = 2; size <= P; size *= 2) {
-    for (int o = size / 2; o > 0; o /= 2) {
-      for (int i = tid; i < P / 2; i += kThreads) {
-        const int a = 2 * i - (i & (o - 1)), b = a + o;
-        const u64 x = sh.keys[a], y = sh.keys[b];
-        if ((x < y) == ((a & size) == 0)) {
-          sh.keys[a] = y;
-          sh.keys[b] = x;
-        }
-      }
-      if (o > 32 || (o == 1 && size >= 64))
-        __syncthreads();
-      else
-        __syncwarp();
-    }
-  }
+  if (tid < n) sh.keys[place] = key;
+  __syncthreads();
 }
 
 // Exclusive prefix over the CTA's threads, and the sum.
@@ -816,57 +792,140 @@ __device__ __forceinline__ uint32_t edge_bits(const Weigher& wt, int b) {
   return bits > 0x00800000u ? bits : 0x00800000u;  // of the lowest finite number
 }
 
-// The three rules on the n sorted keys of the list, of which top-k leaves nk, in one CTA: sh.kept of
-// them, of sh.total mass, stay, sh.limit is the last one's key. `all` is the mass that p refers to
-// where that is not the nk tokens' own (0); the list may begin behind a mass of `above`. False
-// if the nucleus ends before or behind the list, which holds every token of bits >= bound (and
-// before that, unless `above`).
+// The largest key of the list's n that leaves, with the larger ones, a mass (or number) of at least
+// `need` among those from `limit` on: by 256 ranges of the keys, then within one.
 template <int DT>
-__device__ __noinline__ bool rules(Shared& sh, const Weigher& wt, int n, int nk, u64 all,
-                                   u64 above, uint32_t bound) {
-  const int per = (n + kThreads - 1) / kThreads, first = threadIdx.x * per;
-  u64 mine = 0, w[kList / kThreads];
-#pragma unroll
-  for (int i = 0; i < kList / kThreads; ++i) {
-    w[i] = 0;
-    if (i >= per) continue;
-    w[i] = wt.template operator()<DT>(first + i < nk ? key_value(sh.keys[first + i]) : -INFINITY);
-    mine += w[i];
+__device__ __noinline__ u64 pick(Shared& sh, const Weigher& wt, int n, u64 limit, u64 need,
+                                 bool by_mass, u64 lo, u64 hi) {
+  const int tid = threadIdx.x;
+  u64 *bucket = sh.picked[0], *some = sh.picked[1];
+  while (true) {
+    const int bits = 64 - __clzll((long long)(hi - lo)), shift = bits > 8 ? bits - 8 : 0;
+    const u64 from = lo > limit ? lo : limit;
+    bucket[tid] = 0;
+    __syncthreads();
+    for (int base = 0; base < n; base += kThreads) {
+      const u64 key = base + tid < n ? sh.keys[base + tid] : 0;
+      const bool in = key >= from && key <= hi && key;
+      const u64 w = by_mass ? wt.template operator()<DT>(in ? key_value(key) : -INFINITY) : 1;
+      if (in && w) atomicAdd(&bucket[(key - lo) >> shift], w);
+    }
+    __syncthreads();
+    const u64 v = bucket[tid];
+    u64 total;
+    const u64 before = scan(sh, v, total), above = total - before - v;
+    if (above < need && need <= above + v) {
+      sh.hit = tid;
+      sh.rest = need - above;
+      sh.done = 0;
+    }
+    __syncthreads();
+    need = sh.rest;
+    lo += (u64)sh.hit << shift;
+    const u64 end = lo + ((1ull << shift) - 1);
+    hi = end < hi ? end : hi;
+    if (shift == 0) return lo;
+    const u64 first = lo > limit ? lo : limit;
+    for (int i = tid; i < n; i += kThreads) {
+      const u64 key = sh.keys[i];
+      if (key < first || key > hi) continue;
+      const int at = atomicAdd(&sh.done, 1);
+      if (at < kThreads) some[at] = key;
+    }
+    __syncthreads();
+    const int m = sh.done;
+    if (m <= kThreads) {
+      const u64 key = tid < m ? some[tid] : 0;
+      const u64 w = by_mass ? wt.template operator()<DT>(tid < m ? key_value(key) : -INFINITY) : 1;
+      bucket[tid] = w;
+      __syncthreads();
+      u64 larger = 0;
+      for (int i = 0; i < m; ++i)
+        if (some[i] > key) larger += bucket[i];
+      if (tid < m && larger < need && need <= larger + w) sh.limit = key;
+      __syncthreads();
+      return sh.limit;
+    }
+    __syncthreads();
   }
-  u64 mass;
-  const u64 at = scan(sh, mine, mass);
+}
+
+// Mass and number of the list's keys from `limit` on.
+template <int DT>
+__device__ __noinline__ u64 list_mass(Shared& sh, const Weigher& wt, int n, u64 limit, int& count) {
+  u64 mine = 0, total;
+  int c = 0;
+  for (int base = 0; base < n; base += kThreads) {
+    const int i = base + threadIdx.x;
+    const u64 key = i < n ? sh.keys[i] : 0;
+    const bool in = key && key >= limit;
+    c += in;
+    mine += wt.template operator()<DT>(in ? key_value(key) : -INFINITY);
+  }
+  scan(sh, mine, total);
+  c = __reduce_add_sync(kFull, c);
+  if ((threadIdx.x & 31) == 0) sh.red[1][threadIdx.x >> 5] = (u64)c;
+  __syncthreads();
+  count = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) count += (int)sh.red[1][w];
+  __syncthreads();
+  return total;
+}
+
+// The three rules on the n keys of the list, of which top-k leaves nk, in one CTA: sh.kept of them,
+// of sh.total mass, stay, those from sh.limit on. `all` is the mass that p refers to where that is
+// not the nk tokens' own (0); the list may begin behind a mass of `above`. False if the nucleus ends
+// before or behind the list, which holds every token of bits >= bound (and before that, unless
+// `above`). Up to kThreads keys are left in descending order.
+template <int DT>
+__device__ __noinline__ bool rules(Shared& sh, const Weigher& wt, int n, int nk, u64 all, u64 above,
+                                   uint32_t bound, u64 top_key) {
   const bool by_p = sh.p < 1.0f;
+  const int tid = threadIdx.x;
+  if (n > kThreads) {
+    const u64 lo = (u64)bound << 32;
+    u64 limit = nk < n ? pick<DT>(sh, wt, n, 0, (u64)nk, false, lo, top_key) : 0;
+    int kept;
+    u64 mass = list_mass<DT>(sh, wt, n, limit, kept);
+    bool cut = sh.tm > 1;
+    if (by_p) {
+      u64 need = exact_share(sh.p, all ? all : mass, true);
+      if (above && need <= above) return false;
+      need -= above;
+      if (mass < need && all && sh.tm < bound) return false;
+      if (need && need <= mass) {
+        limit = pick<DT>(sh, wt, n, limit, need, true, lo, top_key);
+        cut = true;
+      }
+    }
+    const u64 key_m = sh.tm > 1 ? (u64)sh.tm << 32 : 0;
+    limit = limit > key_m ? limit : key_m;
+    if (cut) mass = list_mass<DT>(sh, wt, n, limit, kept);
+    if (tid == 0) {
+      sh.kept = kept;
+      sh.total = mass;
+      sh.limit = limit;
+    }
+    __syncthreads();
+    return kept > 0;
+  }
+  sort_keys(sh, n);
+  const u64 key = tid < n ? sh.keys[tid] : 0;
+  const u64 w = wt.template operator()<DT>(tid < nk ? key_value(key) : -INFINITY);
+  u64 mass;
+  const u64 before = scan(sh, w, mass);
   u64 need = by_p ? exact_share(sh.p, all ? all : mass, true) : ~0ull;
   if (above && need <= above) return false;
   need -= above;
   if (by_p && all && mass < need && sh.tm < bound) return false;
-  u64 before = at;
-  int np = 0, nm = 0;
-#pragma unroll
-  for (int i = 0; i < kList / kThreads; ++i) {
-    if (i < per && first + i < nk) {
-      np += before < need;
-      nm += (uint32_t)(sh.keys[first + i] >> 32) >= sh.tm;
-    }
-    before += w[i];
-  }
-  np = __reduce_add_sync(kFull, np);
-  nm = __reduce_add_sync(kFull, nm);
-  if ((threadIdx.x & 31) == 0) sh.red[1][threadIdx.x >> 5] = (u64)np << 32 | (u64)nm;
-  __syncthreads();
-  u64 t = 0;
-#pragma unroll
-  for (int q = 0; q < kWarps; ++q) t += sh.red[1][q];
-  int kept = min((int)(t >> 32), (int)(uint32_t)t);
-  kept = kept > 1 ? kept : 1;
-  if (first < kept && kept <= first + per) {
-    u64 sum = at;
-#pragma unroll
-    for (int i = 0; i < kList / kThreads; ++i)
-      if (first + i < kept) sum += w[i];
+  // each rule leaves a prefix; the first token always stays
+  const int kept = __syncthreads_count(tid == 0 || (tid < nk && before < need &&
+                                                    (uint32_t)(key >> 32) >= sh.tm));
+  if (tid == kept - 1) {
     sh.kept = kept;
-    sh.total = sum;
-    sh.limit = sh.keys[kept - 1];
+    sh.total = before + w;
+    sh.limit = key;
   }
   __syncthreads();
   return true;
@@ -881,19 +940,29 @@ template <bool SPLIT>
 __device__ __noinline__ void find_window(Team<SPLIT>& team, float p, int k) {
   Shared& sh = team.sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // the cluster's bins: each part sums a share of them, then every part reads all shares
+  const int share_bins = kBins / team.parts;
+  if constexpr (SPLIT) {
+    team.sync();
+    for (int i = tid; i < share_bins; i += kThreads) {
+      uint32_t sum = 0;
+#pragma unroll
+      for (int q = 0; q < kMaxSplit; ++q)
+        if (q < team.parts)
+          sum += team.cluster.map_shared_rank(&sh, q)->bins[team.part * share_bins + i];
+      sh.slice[i] = sum;
+    }
+  }
   team.sync();
   uint32_t n[kBinsThread], count = 0;
   float e[kBinsThread], mine = 0.0f;
 #pragma unroll
   for (int i = 0; i < kBinsThread; ++i) {
     const int at = tid * kBinsThread + i;
-    n[i] = 0;
-    for (int q = 0; q < team.parts; ++q) {
-      if constexpr (SPLIT)
-        n[i] += team.cluster.map_shared_rank(&sh, q)->bins[at];
-      else
-        n[i] += sh.bins[at];
-    }
+    if constexpr (SPLIT)
+      n[i] = team.cluster.map_shared_rank(&sh, at / share_bins)->slice[at % share_bins];
+    else
+      n[i] = sh.bins[at];
     if (at == kBins - 1) n[i] = 0;  // no mass
     e[i] = (float)n[i] * (k ? 1.0f : fast_exp2(at * -0.03125f));
     mine += e[i];
@@ -994,13 +1063,14 @@ __device__ __forceinline__ u64 draw_at(const SampleArgs& a, int row, u64 total) 
   return exact_share(u, total, false);
 }
 
-// The draw among the list's first sh.kept keys: by 256 ranges of ids, then within one.
+// The draw among the listed keys from sh.limit on: by 256 ranges of ids, then within one.
 template <int DT>
 __device__ __noinline__ void draw_list(Shared& sh, const SampleArgs& a, int row, const Weigher& wt,
-                                       float scale) {
+                                       float scale, int listed) {
   u64* bucket = sh.bucket;
-  const int tid = threadIdx.x, n = sh.kept;
-  if (n <= kThreads) {  // every token against every other
+  const int tid = threadIdx.x;
+  if (listed <= kThreads) {  // every token that stays against every other
+    const int n = sh.kept;
     const u64 key = tid < n ? sh.keys[tid] : 0;
     const u64 w = wt.template operator()<DT>(tid < n ? key_value(key) : -INFINITY);
     bucket[tid] = w;
@@ -1018,10 +1088,11 @@ __device__ __noinline__ void draw_list(Shared& sh, const SampleArgs& a, int row,
   while ((a.V - 1) >> by >= kBuckets) ++by;
   bucket[tid] = 0;
   __syncthreads();
-  for (int base = 0; base < n; base += kThreads) {
+  const u64 limit = sh.limit;
+  for (int base = 0; base < listed; base += kThreads) {
     const int i = base + tid;
-    const u64 key = i < n ? sh.keys[i] : 0;
-    const u64 w = wt.template operator()<DT>(i < n ? key_value(key) : -INFINITY);
+    const u64 key = i < listed ? sh.keys[i] : 0;
+    const u64 w = wt.template operator()<DT>(key && key >= limit ? key_value(key) : -INFINITY);
     if (w) atomicAdd(&bucket[key_id(key) >> by], w);
   }
   __syncthreads();
@@ -1039,8 +1110,9 @@ __device__ __noinline__ void draw_list(Shared& sh, const SampleArgs& a, int row,
   u64* some = sh.seg;
   if (tid == 0) sh.done = 0;
   __syncthreads();
-  for (int i = tid; i < n; i += kThreads)
-    if (key_id(sh.keys[i]) >> by == hit) some[atomicAdd(&sh.done, 1)] = sh.keys[i];
+  for (int i = tid; i < listed; i += kThreads)
+    if (sh.keys[i] >= limit && key_id(sh.keys[i]) >> by == hit)
+      some[atomicAdd(&sh.done, 1)] = sh.keys[i];
   __syncthreads();
   const int m = sh.done;
   for (int base = 0; base < m; base += kThreads) {
@@ -1053,7 +1125,7 @@ __device__ __noinline__ void draw_list(Shared& sh, const SampleArgs& a, int row,
     }
     const u64 w = wt.template operator()<DT>(in ? key_value(key) : -INFINITY);
     if (in && below <= rest && rest < below + w)
-      write_draw(a, row, key_id(key), key_value(key), wt, scale, sh.total, n);
+      write_draw(a, row, key_id(key), key_value(key), wt, scale, sh.total, sh.kept);
   }
 }
 
@@ -1184,18 +1256,21 @@ __device__ __noinline__ void read_params(Shared& sh, const SampleArgs& a, int ro
   if (bad) atomicOr(a.status, SPEC_DEV_BAD_PARAM);
   const float inv = T > 0.0f ? 1.0f / T : INFINITY;
   const bool greedy = inv == INFINITY || p <= 0.0f || k == 1;
-  sh.scale = inv == INFINITY ? 1.0f : inv;
-  const double c = fmin((double)sh.scale * 1.4426950408889634074, 3e38);
-  sh.ch = (float)c;
-  sh.cl = (float)(c - (double)sh.ch);
+  const float scale = inv == INFINITY ? 1.0f : inv;
+  // log2(e) / T in a pair; 1 / T near the largest number is cut so that the product is finite
+  constexpr float kHi = 1.44269502162933349609f, kLo = 1.92596303350e-8f;
+  const float sc = fminf(scale, 1.5e38f);
+  sh.scale = scale;
+  sh.ch = sc * kHi;
+  sh.cl = fmaf(sc, kLo, fmaf(sc, kHi, -sh.ch));
   sh.k = greedy ? 1 : (k <= 0 || k >= a.V ? 0 : k);
   sh.p = p < 0.0f ? 0.0f : p;
-  sh.tm = 1;                       // until the row's maximum is known
-  sh.mp = mp > 0.0f ? __float_as_uint(mp < 1.0f ? mp : 1.0f) : 0;
+  sh.by_m = mp > 0.0f;
+  if (sh.by_m) sh.below = log((double)fminf(mp, 1.0f)) / (double)scale;
 }
 
 template <int DT, bool SPLIT, bool WRITE>
-__global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a, const int parts) {
+__global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArgs a, const int parts) {
   __shared__ Shared sh;
   Team<SPLIT> team(sh, parts);
   const int tid = threadIdx.x, lane = tid & 31;
@@ -1217,7 +1292,6 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
       part.j0 = min(np, team.part * per);
       part.j1 = min(np, part.j0 + per);
     }
-    if (tid == 0) read_params(sh, a, row);
     const int steps = part.steps(), per_group = max(1, (steps + kGroupsMost - 1) / kGroupsMost);
     const int groups = (steps + per_group - 1) / per_group;
 
@@ -1228,6 +1302,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
       uint4 q[2][kBatch];
       part.load(q[0], 0);
       part.load(q[1], 1);
+      if (tid == 0) read_params(sh, a, row);
       float e = -INFINITY;
       int in = 0, g = 0;
       auto take = [&](const uint4 (&w)[kBatch]) {
@@ -1252,8 +1327,8 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
       }
     }
     // NaN comes out as the largest
-    const u64 most = team.max(m != m ? ~0ull : (u64)order_bits(m));
-    if (most == ~0ull || most == 0 || order_value((uint32_t)most) == INFINITY) {
+    const uint32_t top = team.max(m != m ? ~0u : order_bits(m));
+    if (top == ~0u || top == 0 || order_value(top) == INFINITY) {
       // no distribution: the largest logit's id, or 0
       u64 best = 0;
       for (int it = 0; it < steps; ++it)
@@ -1267,10 +1342,11 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
             best = key > best ? key : best;
           }
         }
-      best = team.max(best);
+      const uint32_t most = team.max((uint32_t)(best >> 32));
+      const uint32_t low = team.max((uint32_t)(best >> 32) == most ? (uint32_t)best : 0);
       if (team.part == 0 && tid == 0) {
         atomicOr(a.status, SPEC_DEV_NONFINITE);
-        if (a.tokens) a.tokens[row] = best ? key_id(best) : 0;
+        if (a.tokens) a.tokens[row] = most ? (int)(0xffffffffu - low) : 0;
         if (a.logp) a.logp[row] = NAN;
         if (a.kept) a.kept[row] = 0;
         if (a.stats) a.stats[2 * (size_t)row] = a.stats[2 * (size_t)row + 1] = NAN;
@@ -1279,28 +1355,28 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
       team.sync();
       continue;
     }
-    const uint32_t top = (uint32_t)most;
     const u64 top_key = (u64)top << 32 | 0xffffffffu;
     wt.m = order_value(top);
     wt.ch = sh.ch;
     wt.cl = sh.cl;
     const float scale = sh.scale;
-    if (tid == 0 && sh.mp) {
-      // the least fp32 number x with (x - m) / T >= log(min_p)
-      const double t = (double)wt.m + log((double)__uint_as_float(sh.mp)) / (double)scale;
-      float f = __double2float_ru(t);
-      f = f < wt.m ? f : wt.m;
-      sh.tm = f > -INFINITY ? order_bits(f) : 1;
-    }
-    __syncthreads();
     const int k = sh.k;
-    const bool by_p = sh.p < 1.0f, by_m = sh.tm > 1;
-    const uint32_t tm = sh.tm;
+    const bool by_p = sh.p < 1.0f;
+    uint32_t tm = 1;
+    if (sh.by_m) {  // the least fp32 number x with (x - m) / T >= log(min_p)
+      float f = __double2float_ru((double)wt.m + sh.below);
+      f = f < wt.m ? f : wt.m;
+      if (f > -INFINITY) tm = order_bits(f);
+      if (tid == 0) sh.tm = tm;
+    } else if (tid == 0) {
+      sh.tm = 1;
+    }
+    const bool by_m = tm > 1;
 
     u64 limit = 0, total = 0;
     int kept = 0;
     if (k == 1) {
-      u64 best = 0;
+      uint32_t best = 0;
       for (int g = 0; g < groups; ++g) {
         if (sh.index[g * kThreads + tid] != top) continue;
         for (int it = g * per_group; it < min(steps, (g + 1) * per_group); ++it)
@@ -1309,13 +1385,11 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
             float x[Row<DT>::N];
             unpack<DT>(part.row.load_any(j, part.j1), x);
             for (int i = 0; i < Row<DT>::N; ++i)
-              if (x[i] == wt.m) {
-                const u64 key = make_key(top, j * Row<DT>::N - part.row.head + i);
-                best = key > best ? key : best;
-              }
+              if (x[i] == wt.m)
+                best = max(best, 0xffffffffu - (uint32_t)(j * Row<DT>::N - part.row.head + i));
           }
       }
-      limit = team.max(best);
+      limit = (u64)top << 32 | team.max(best);
       kept = 1;
       total = 1ull << (S + 1);
       if (!WRITE && team.part == 0 && tid == 0)
@@ -1327,8 +1401,8 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
       if (k && !binned) {
         if constexpr (SPLIT) {
           // as many tokens in every part as make k together, or k in one
-          bound = ~(uint32_t)team.max(~index_bound(sh, groups, (k + team.parts - 1) / team.parts, top));
-          if (bound == 1) bound = (uint32_t)team.max(index_bound(sh, groups, k, top));
+          bound = ~team.max(~index_bound(sh, groups, (k + team.parts - 1) / team.parts, top));
+          if (bound == 1) bound = team.max(index_bound(sh, groups, k, top));
         } else {
           bound = index_bound(sh, groups, k, top);
         }
@@ -1353,9 +1427,8 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
           const int n = collect<DT, SPLIT>(team, part, per_group, bound);
           if (n <= kList) {
             if (team.part == 0) {
-              sort_keys(sh, n);
               const bool ok = (k == 0 || k <= n || bound <= 0x00800000u) &&
-                              rules<DT>(sh, wt, n, k && k < n ? k : n, all, 0, bound);
+                              rules<DT>(sh, wt, n, k && k < n ? k : n, all, 0, bound, top_key);
               if (tid == 0) sh.done = ok;
             }
             team.sync();
@@ -1365,7 +1438,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
               total = lead->total;
               kept = lead->kept;
               if (SPLIT) team.sync();
-              if (!WRITE && team.part == 0) draw_list<DT>(sh, a, row, wt, scale);
+              if (!WRITE && team.part == 0) draw_list<DT>(sh, a, row, wt, scale, n);
             }
           }
         }
@@ -1384,20 +1457,21 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a,
         window = n <= kList && nk > 0 && nk <= n;
         if (window) {
           if (team.part == 0) {
-            sort_keys(sh, n);
             // a truncation that min-p cuts shorter is not decided here, nor top-p of this top-k
             bool ok = false;
             if (k && by_p) {
-              if (tid == 0) sh.limit = sh.keys[nk - 1];
+              const u64 key = pick<DT>(sh, wt, n, 0, (u64)nk, false, (u64)lo_bits << 32, top_key);
+              if (tid == 0) sh.limit = key;
             } else {
-              ok = rules<DT>(sh, wt, n, nk, all, s.a, ~0u) && (uint32_t)(sh.limit >> 32) >= tm;
+              ok = rules<DT>(sh, wt, n, nk, all, s.a, lo_bits, top_key) &&
+                   (uint32_t)(sh.limit >> 32) >= tm;
             }
             if (tid == 0) sh.done = ok;
             // what stays of the list, into the segments
             if (ok && !WRITE)
-              for (int base = 0; base < sh.kept; base += kThreads) {
-                const bool in = base + tid < sh.kept;
-                const u64 key = in ? sh.keys[base + tid] : 0;
+              for (int base = 0; base < n; base += kThreads) {
+                const u64 key = base + tid < n ? sh.keys[base + tid] : 0;
+                const bool in = key && key >= sh.limit;
                 const u64 w = wt.template operator()<DT>(in ? key_value(key) : -INFINITY);
                 if (!in) continue;
                 const int j = (key_id(key) + part.row.head) / Row<DT>::N;
@@ -1499,7 +1573,7 @@ cudaError_t launch_t(const SampleArgs& a, int split, cudaStream_t s) {
   attr[1].val.clusterDim.x = split;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  const int most = 3 * num_sms();
+  const int most = kCtas * num_sms();
   cfg.gridDim = dim3((unsigned)(SPLIT ? a.rows * split : (a.rows < most ? a.rows : most)));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
