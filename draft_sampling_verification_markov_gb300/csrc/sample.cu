@@ -151,10 +151,8 @@ struct Weigher {
     return join(y, t, q);
   }
 
-  // t0, t1 (optional use): what bin() takes.
   template <int DT>
-  __device__ __forceinline__ void pair(float x0, float x1, u64& v0, u64& v1, float& t0,
-                                       float& t1) const {
+  __device__ __forceinline__ void pair(float x0, float x1, u64& v0, u64& v1) const {
     using namespace tc;
     const u64 x = pack2(x0, x1), m2 = pack2(m, m), n1 = pack2(-1.0f, -1.0f);
     const u64 ch2 = pack2(ch, ch), nch2 = pack2(-ch, -ch), ncl2 = pack2(-cl, -cl);
@@ -172,14 +170,14 @@ struct Weigher {
     q = fma2(r, q, pack2(kC2, kC2));
     q = fma2(r, q, pack2(kC1Rest, kC1Rest));
     q = fma2(r, pack2(kC1, kC1), mul2(r, q));
-    float y0, y1, q0, q1;
+    float y0, y1, t0, t1, q0, q1;
     unpack2(y, y0, y1);
     unpack2(t, t0, t1);
     unpack2(q, q0, q1);
     v0 = join(y0, t0, q0);
     v1 = join(y1, t1, q1);
   }
-  // Bin of a mass: -32 y rounded; the last one, and what has none, share a bin.
+  // Bin of a mass, of t = kMagic + y: -32 y rounded; the last one, and what has none, share a bin.
   __device__ __forceinline__ static uint32_t bin(float t) {
     return min((uint32_t)(kMagicBits - __float_as_int(t)), (uint32_t)kBins - 1);
   }
@@ -404,8 +402,8 @@ __device__ __forceinline__ void add_segment(Shared& sh, int it, u64 s) {
   }
 }
 
-// Mass of the whole part; with SEG those of its segments, with BINS its tokens by their mass.
-template <int DT, bool SEG, bool BINS>
+// Mass of the whole part; with SEG those of its segments.
+template <int DT, bool SEG>
 __device__ __noinline__ u64 pass_all(Shared& sh, const Part<DT> part, const Weigher wt) {
   constexpr int N = Row<DT>::N;
   const int n = part.steps();
@@ -425,18 +423,54 @@ __device__ __noinline__ u64 pass_all(Shared& sh, const Part<DT> part, const Weig
 #pragma unroll
       for (int i = 0; i < N; i += 2) {
         u64 v0, v1;
-        float t0, t1;
-        wt.template pair<DT>(x[i], x[i + 1], v0, v1, t0, t1);
-        if constexpr (BINS) {
-          atomicAdd(&sh.bins[Weigher::bin(t0)], 1u);
-          atomicAdd(&sh.bins[Weigher::bin(t1)], 1u);
-        }
+        wt.template pair<DT>(x[i], x[i + 1], v0, v1);
         s += v0;
         s += v1;
       }
     }
     add_segment<SEG>(sh, it, s);
     mass += s;
+  }
+  return mass;
+}
+
+// About the mass of the whole part, in units of 2^-40, and its tokens by their mass. fp32 sums of 16
+// approximate exponentials: off by at most kSlack, of which (x - m) c in one product is 2^-18 (its
+// error is 3 * 2^-24 ln2 of y, whose mean over the mass is at most log2 V).
+constexpr float kSlack = 0x1p-17f;
+template <int DT>
+__device__ __noinline__ u64 pass_guess(Shared& sh, const Part<DT> part, const Weigher wt) {
+  using namespace tc;
+  constexpr int N = Row<DT>::N;
+  const u64 m2 = pack2(wt.m, wt.m), n1 = pack2(-1.0f, -1.0f), ch2 = pack2(wt.ch, wt.ch);
+  const int n = part.steps();
+  u64 mass = 0;
+  uint4 q[kBatch];
+  part.load(q, 0);
+  for (int it = 0; it < n; ++it) {
+    uint4 now[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) now[b] = q[b];
+    if (it + 1 < n) part.load(q, it + 1);
+    u64 s = pack2(0.0f, 0.0f);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      float x[N];
+      unpack<DT>(now[b], x);
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        const u64 y = mul2(fma2(pack2(x[i], x[i + 1]), n1, m2), ch2);
+        float y0, y1, t0, t1;
+        unpack2(y, y0, y1);
+        unpack2(fma2(y, n1, pack2(kMagic, kMagic)), t0, t1);
+        s = add2(s, pack2(fast_exp2(-y0), fast_exp2(-y1)));
+        atomicAdd(&sh.bins[Weigher::bin(t0)], 1u);
+        atomicAdd(&sh.bins[Weigher::bin(t1)], 1u);
+      }
+    }
+    float s0, s1;
+    unpack2(s, s0, s1);
+    mass += __float2ull_rn((s0 + s1) * 0x1p40f);
   }
   return mass;
 }
@@ -472,9 +506,7 @@ __device__ __noinline__ void pass(Shared& sh, const Part<DT> part, const Weigher
           c += in0 + in1;
           if constexpr (MASS) {
             u64 v0, v1;
-            float t0, t1;
-            wt.template pair<DT>(in0 ? x[i] : -INFINITY, in1 ? x[i + 1] : -INFINITY, v0, v1, t0,
-                                 t1);
+            wt.template pair<DT>(in0 ? x[i] : -INFINITY, in1 ? x[i + 1] : -INFINITY, v0, v1);
             s += v0;
             s += v1;
           }
@@ -487,15 +519,14 @@ __device__ __noinline__ void pass(Shared& sh, const Part<DT> part, const Weigher
   count = c;
 }
 
-// Mass and number of the part's tokens of logits >= hi, and the masses of its segments; those from
-// lo to hi go on the list.
+// Mass and number of the part's tokens of logits >= hi, the masses of its segments of these, and the
+// part's whole mass; tokens from lo to hi go on the list.
 template <int DT>
-__device__ __noinline__ void pass_window(Shared& sh, const Part<DT> part,
-                                         const Weigher wt, float lo, float hi, u64& mass,
-                                         u64& count) {
+__device__ __noinline__ void pass_window(Shared& sh, const Part<DT> part, const Weigher wt, float lo,
+                                         float hi, u64& mass, u64& count, u64& all) {
   constexpr int N = Row<DT>::N;
   const int n = part.steps();
-  mass = 0;
+  mass = all = 0;
   uint32_t c = 0;
   uint4 q[kBatch];
   part.load(q, 0);
@@ -506,34 +537,37 @@ __device__ __noinline__ void pass_window(Shared& sh, const Part<DT> part,
     for (int b = 0; b < kBatch; ++b) now[b] = q[b];
     if (it + 1 < n) part.load(q, it + 1);
     u64 s = 0;
-    if (__any_sync(kFull, batch_max_nan<DT>(now) >= lo)) {
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        float x[N];
-        unpack<DT>(now[b], x);
-        uint32_t win = 0;
+    for (int b = 0; b < kBatch; ++b) {
+      float x[N];
+      unpack<DT>(now[b], x);
+      uint32_t win = 0;
 #pragma unroll
-        for (int i = 0; i < N; i += 2) {
-          const bool in0 = x[i] >= hi, in1 = x[i + 1] >= hi;
-          c += in0 + in1;
-          u64 v0, v1;
-          float t0, t1;
-          wt.template pair<DT>(in0 ? x[i] : -INFINITY, in1 ? x[i + 1] : -INFINITY, v0, v1, t0, t1);
+      for (int i = 0; i < N; i += 2) {
+        u64 v0, v1;
+        wt.template pair<DT>(x[i], x[i + 1], v0, v1);
+        all += v0;
+        all += v1;
+        if (x[i] >= hi) {
           s += v0;
+          ++c;
+        }
+        if (x[i + 1] >= hi) {
           s += v1;
-          win |= (uint32_t)(!in0 && x[i] >= lo) << i | (uint32_t)(!in1 && x[i + 1] >= lo) << (i + 1);
+          ++c;
         }
-        if (win) {
-          int at = atomicAdd(&sh.n_list, __popc(win));
+        win |= (uint32_t)(x[i] < hi && x[i] >= lo) << i |
+               (uint32_t)(x[i + 1] < hi && x[i + 1] >= lo) << (i + 1);
+      }
+      if (win) {
+        int at = atomicAdd(&sh.n_list, __popc(win));
 #pragma unroll
-          for (int i = 0; i < N; ++i)
-            if (win >> i & 1) {
-              if (at < kList)
-                sh.keys[at] =
-                    make_key(order_bits(x[i]), (j + b * 32) * N - part.row.head + i);
-              ++at;
-            }
-        }
+        for (int i = 0; i < N; ++i)
+          if (win >> i & 1) {
+            if (at < kList)
+              sh.keys[at] = make_key(order_bits(x[i]), (j + b * 32) * N - part.row.head + i);
+            ++at;
+          }
       }
     }
     add_segment<true>(sh, it, s);
@@ -875,12 +909,14 @@ __device__ __noinline__ u64 list_mass(Shared& sh, const Weigher& wt, int n, u64 
 
 // The three rules on the n keys of the list, of which top-k leaves nk, in one CTA: sh.kept of them,
 // of sh.total mass, stay, those from sh.limit on. `all` is the mass that p refers to where that is
-// not the nk tokens' own (0); the list may begin behind a mass of `above`. False if the nucleus ends
-// before or behind the list, which holds every token of bits >= bound (and before that, unless
-// `above`). Up to kThreads keys are left in descending order.
+// not the nk tokens' own (0), to within `slack`; the list may begin behind a mass of `above`. kNo if
+// the nucleus ends before or behind the list, which holds every token of bits >= bound (and before
+// that, unless `above`), kUnsure if the slack decides where. Up to kThreads keys are left in
+// descending order.
+enum : int { kNo = 0, kYes = 1, kUnsure = 2 };
 template <int DT>
-__device__ __noinline__ bool rules(Shared& sh, const Weigher& wt, int n, int nk, u64 all, u64 above,
-                                   uint32_t bound, u64 top_key) {
+__device__ __noinline__ int rules(Shared& sh, const Weigher& wt, int n, int nk, u64 all, u64 slack,
+                                  u64 above, uint32_t bound, u64 top_key) {
   const bool by_p = sh.p < 1.0f;
   const int tid = threadIdx.x;
   if (n > kThreads) {
@@ -888,47 +924,60 @@ __device__ __noinline__ bool rules(Shared& sh, const Weigher& wt, int n, int nk,
     u64 limit = nk < n ? pick<DT>(sh, wt, n, 0, (u64)nk, false, lo, top_key) : 0;
     int kept;
     u64 mass = list_mass<DT>(sh, wt, n, limit, kept);
-    bool cut = sh.tm > 1;
+    const u64 key_m = sh.tm > 1 ? (u64)sh.tm << 32 : 0;
     if (by_p) {
-      u64 need = exact_share(sh.p, all ? all : mass, true);
-      if (above && need <= above) return false;
+      const u64 base = all ? all : mass;
+      u64 need = exact_share(sh.p, base - slack, true), most = exact_share(sh.p, base + slack, true);
+      if (above && need <= above) return kNo;
       need -= above;
-      if (mass < need && all && sh.tm < bound) return false;
+      most -= above;
+      if (mass < most && all && sh.tm < bound) return kNo;
       if (need && need <= mass) {
-        limit = pick<DT>(sh, wt, n, limit, need, true, lo, top_key);
-        cut = true;
+        const u64 key = pick<DT>(sh, wt, n, limit, need, true, lo, top_key);
+        limit = key;
+        mass = list_mass<DT>(sh, wt, n, limit, kept);
+        // this token also ends the nucleus of a larger need
+        if (mass < most && key_m <= key) return kUnsure;
       }
     }
-    const u64 key_m = sh.tm > 1 ? (u64)sh.tm << 32 : 0;
-    limit = limit > key_m ? limit : key_m;
-    if (cut) mass = list_mass<DT>(sh, wt, n, limit, kept);
+    if (key_m > limit) {
+      limit = key_m;
+      mass = list_mass<DT>(sh, wt, n, limit, kept);
+    }
     if (tid == 0) {
       sh.kept = kept;
       sh.total = mass;
       sh.limit = limit;
     }
     __syncthreads();
-    return kept > 0;
+    return kept > 0 ? kYes : kNo;
   }
   sort_keys(sh, n);
   const u64 key = tid < n ? sh.keys[tid] : 0;
   const u64 w = wt.template operator()<DT>(tid < nk ? key_value(key) : -INFINITY);
   u64 mass;
   const u64 before = scan(sh, w, mass);
-  u64 need = by_p ? exact_share(sh.p, all ? all : mass, true) : ~0ull;
-  if (above && need <= above) return false;
-  need -= above;
-  if (by_p && all && mass < need && sh.tm < bound) return false;
+  u64 need = ~0ull, most = ~0ull;
+  if (by_p) {
+    const u64 base = all ? all : mass;
+    need = exact_share(sh.p, base - slack, true);
+    most = exact_share(sh.p, base + slack, true);
+    if (above && need <= above) return kNo;
+    need -= above;
+    most -= above;
+    if (all && mass < most && sh.tm < bound) return kNo;
+  }
   // each rule leaves a prefix; the first token always stays
-  const int kept = __syncthreads_count(tid == 0 || (tid < nk && before < need &&
-                                                    (uint32_t)(key >> 32) >= sh.tm));
+  const bool other = tid < nk && (uint32_t)(key >> 32) >= sh.tm;
+  const int kept = __syncthreads_count(tid == 0 || (other && before < need));
+  if (slack && __syncthreads_count(tid == 0 || (other && before < most)) != kept) return kUnsure;
   if (tid == kept - 1) {
     sh.kept = kept;
     sh.total = before + w;
     sh.limit = key;
   }
   __syncthreads();
-  return true;
+  return kYes;
 }
 
 // Where a share p of the mass of sh.bins (of every part) ends: bins sh.bin_lo .. sh.bin_hi, with
@@ -1395,7 +1444,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
       if (!WRITE && team.part == 0 && tid == 0)
         write_draw(a, row, key_id(limit), wt.m, wt, scale, total, 1);
     } else if (k || by_p || by_m) {
-      u64 all = 0;  // the mass that p refers to, where that is not the list's
+      u64 all = 0, slack = 0;  // the mass that p refers to, where that is not the list's
       uint32_t bound = tm;
       bool list = true, window = false, binned = k ? k > kListTop : by_p;
       if (k && !binned) {
@@ -1411,13 +1460,14 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
         if (binned) {
           for (int i = tid; i < kBins; i += kThreads) sh.bins[i] = 0;
           __syncthreads();
-          const u64 mass = team.sum(pass_all<DT, false, true>(sh, part, wt), 0).a;
+          const u64 mass = team.sum(pass_guess<DT>(sh, part, wt), 0).a;
           find_window<SPLIT>(team, sh.p, k);
           list = sh.n_above + sh.n_window <= kListMost;
           window = sh.bin_lo > 0 && sh.n_window <= kListMost;
           bound = edge_bits(wt, sh.bin_hi);
           if (!k) {
-            all = mass;
+            all = mass << (S + 1 - 40);
+            slack = (u64)((float)all * kSlack);
             // min-p's last token is enough, and may be before where the nucleus seems to end
             if (tm > bound || !list) bound = tm;
             if (!list) list = by_m && (sh.bin_lo == 0 || tm > edge_bits(wt, sh.bin_lo - 1));
@@ -1426,14 +1476,23 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
         if (list) {
           const int n = collect<DT, SPLIT>(team, part, per_group, bound);
           if (n <= kList) {
-            if (team.part == 0) {
-              const bool ok = (k == 0 || k <= n || bound <= 0x00800000u) &&
-                              rules<DT>(sh, wt, n, k && k < n ? k : n, all, 0, bound, top_key);
-              if (tid == 0) sh.done = ok;
+            int done = kNo;
+            while (true) {
+              if (team.part == 0) {
+                const int is = k == 0 || k <= n || bound <= 0x00800000u
+                                   ? rules<DT>(sh, wt, n, k && k < n ? k : n, all, slack, 0, bound,
+                                               top_key)
+                                   : kNo;
+                if (tid == 0) sh.done = is;
+              }
+              team.sync();
+              done = team.leader()->done;
+              if (done != kUnsure) break;
+              all = team.sum(pass_all<DT, false>(sh, part, wt), 0).a;
+              slack = 0;
             }
-            team.sync();
             const Shared* lead = team.leader();
-            if (lead->done) {
+            if (done) {
               limit = lead->limit;
               total = lead->total;
               kept = lead->kept;
@@ -1450,9 +1509,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
         if (tid == 0) sh.n_list = 0;
         const uint32_t lo_bits = edge_bits(wt, sh.bin_hi), hi_bits = edge_bits(wt, sh.bin_lo - 1);
         __syncthreads();
-        u64 mm, cc;
-        pass_window<DT>(sh, part, wt, order_value(lo_bits), order_value(hi_bits), mm, cc);
+        u64 mm, cc, zz;
+        pass_window<DT>(sh, part, wt, order_value(lo_bits), order_value(hi_bits), mm, cc, zz);
         const auto s = team.sum(mm, cc);
+        if (!k && (slack || turn == 0)) all = team.sum(zz, 0).a;
+        slack = 0;
         const int n = gather<SPLIT>(team), nk = k ? k - (int)s.b : n;
         window = n <= kList && nk > 0 && nk <= n;
         if (window) {
@@ -1463,7 +1524,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
               const u64 key = pick<DT>(sh, wt, n, 0, (u64)nk, false, (u64)lo_bits << 32, top_key);
               if (tid == 0) sh.limit = key;
             } else {
-              ok = rules<DT>(sh, wt, n, nk, all, s.a, lo_bits, top_key) &&
+              ok = rules<DT>(sh, wt, n, nk, all, 0, s.a, lo_bits, top_key) &&
                    (uint32_t)(sh.limit >> 32) >= tm;
             }
             if (tid == 0) sh.done = ok;
@@ -1515,6 +1576,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
         const u64 key_m = (u64)tm << 32;
         if (k && !limit) limit = search<DT, SPLIT, false>(team, part, wt, 0, (u64)k, top_key);
         if (by_p) {
+          if (!k && slack) all = team.sum(pass_all<DT, false>(sh, part, wt), 0).a;
           if (k) {
             u64 mm, cc;
             pass<DT, true, false>(sh, part, wt, limit, mm, cc);
@@ -1538,7 +1600,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
       if (limit) {
         pass<DT, true, true>(sh, part, wt, limit, mm, cc);
       } else {
-        mm = pass_all<DT, !WRITE, false>(sh, part, wt);
+        mm = pass_all<DT, !WRITE>(sh, part, wt);
         cc = finite;
       }
       const auto s = team.sum(mm, cc);
