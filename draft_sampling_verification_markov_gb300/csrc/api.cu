@@ -1159,9 +1159,7 @@ int spec_w4_logits(const void* x, long long ldx, const void* residual, long long
   if (norm_weight && (!(eps >= 0.0f) || !isfinite(eps))) return SPEC_ERR_INVALID_ARG;
   if (!status_ws_ok(ws)) return SPEC_ERR_INVALID_ARG;
   if (ws_bytes < kHeader) return SPEC_ERR_WORKSPACE_TOO_SMALL;
-  const int parts = dtype == SPEC_F32 || (norm_weight && nw_dtype == SPEC_F32) ? 3
-                    : norm_weight                                              ? 2
-                                                                               : 1;
+  const int parts = dtype == SPEC_F32 || norm_weight ? 2 : 1;
   if (!w4_fits(parts, K)) return SPEC_ERR_TOO_LARGE;
   if (M == 0) return SPEC_OK;
   if (!x || !codes || !scales || !out || !aligned16(codes) || !aligned16(scales) ||
@@ -1181,7 +1179,7 @@ int spec_w4_logits(const void* x, long long ldx, const void* residual, long long
   const W4Args a{x,     ldx,         residual, ldr,   dtype, norm_weight,  nw_dtype,
                  eps,   M,           N,        K,     codes, scales,       scale_dtype,
                  zeros, group,       residual_out, ldh, out, out_dtype,    ld_out,
-                 static_cast<uint32_t*>(ws), parts, 0, 0, 0};
+                 static_cast<uint32_t*>(ws), parts, 0, 0, 0, 0};
   const cudaError_t e = launch_w4_logits(a, static_cast<cudaStream_t>(stream));
   const int rc = finish();
   return e == cudaSuccess ? rc : SPEC_ERR_CUDA;

@@ -1,0 +1,12 @@
+// w4_g64.cu -- the product's kernels for groups of 64.
+#include "w4_product.cuh"
+
+namespace spec {
+namespace w4 {
+
+cudaError_t launch_g64(const W4Args& a, const CUtensorMap& codes, int R, int T, cudaStream_t s) {
+  return launch_group<64>(a, codes, R, T, s);
+}
+
+}  // namespace w4
+}  // namespace spec

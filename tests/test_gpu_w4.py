@@ -143,13 +143,13 @@ def test_rows(M, form):
     check(x, w, v, norm=None if form == "plain" else (1 + randn((512,), 5, F32, 0.1)).to(x.dtype))
 
 
-@pytest.mark.parametrize("K,dt", [(8192, F32), (16384, BF), (27264, F32)])
+@pytest.mark.parametrize("K,dt", [(8192, F32), (16384, BF), (36864, F32)])
 def test_wide_rows(K, dt):
     w, v = packed(48, K, 64, F32, K, zeros=True)
     check(randn((7, K), 6, dt), w, v, norm=randn((K,), 7, F32), dtype=F32)
     with pytest.raises(S.SpecError) as e:
-        big = S.W4Tensor.empty(4, 27265, 64, F32, DEV)
-        S.spec_w4_logits(torch.zeros(1, 27265, device=DEV), big)
+        big = S.W4Tensor.empty(4, 36865, 64, F32, DEV)
+        S.spec_w4_logits(torch.zeros(1, 36865, device=DEV), big)
     assert e.value.status == S.SPEC_ERR_TOO_LARGE
 
 
