@@ -116,36 +116,40 @@ cudaError_t launch_w4_logits(W4Args a, cudaStream_t s) {
   a.chunks = (a.M + a.chunk_rows - 1) / a.chunk_rows;
   a.chunk_rows = (a.M + a.chunks - 1) / a.chunks;
   const int cols = a.chunk_rows * a.parts, T = cols <= 8 ? 1 : cols <= 16 ? 2 : cols <= 24 ? 3 : 5;
-  // Two 16-row tiles a warp halve what it reads of the rows; more warps on a tile leave more tiles
+  // Tiles of 32 rows halve what a warp reads of the columns, more warps on a tile leave more tiles
   // for everyone. The one with the fewest blocks behind one another, each new unit counted as one
-  // more for its sums.
+  // more for its sums. Two blocks a tile, where both fit three times, halve the rest of its cost.
+  auto fits = [&](int r, int w, int stages) {
+    return rest_bytes(a.K, a.chunk_rows, a.parts, T) + stages * stage_bytes(r, w) <= kSmemMost;
+  };
   const int sms = num_sms() / a.chunks > 0 ? num_sms() / a.chunks : 1;
   long long best = 1LL << 60;
-  int R = 1;
-  const bool two = T <= 2 && rest_bytes(a.K, a.chunk_rows, a.parts, 2, T) + 2 * stage_bytes(2) <=
-                               kSmemMost;
-  for (int r = two ? 2 : 1; r >= 1; --r)
+  Form form{1, T, 1};
+  for (int r = T <= 2 && fits(2, 1, 2) ? 2 : 1; r >= 1; --r) {
+    const int wide = r == 2 && T == 1 && KB > 1 && fits(r, 2, 3) ? 2 : 1;
+    const int tiles = (KB + wide - 1) / wide;
     for (int kw = 2; kw <= kWarps; kw *= 2) {
       const long long units = (a.N + 16 * r - 1) / (16 * r), teams = (long long)sms * (kWarps / kw);
-      const long long cost = ((units + teams - 1) / teams) * ((KB + kw - 1) / kw * r + 1);
+      const long long cost = ((units + teams - 1) / teams) * ((tiles + kw - 1) / kw * r * wide + 1);
       if (cost < best) {
         best = cost;
         a.k_warps = kw;
-        R = r;
+        form = Form{r, T, wide};
       }
     }
+  }
   CUtensorMap codes;
   if (!tc::encode_fn()) return cudaErrorNotSupported;
   const cuuint64_t dims[2] = {(cuuint64_t)padded(a.K) / 2, (cuuint64_t)a.N}, stride = dims[0];
-  const cuuint32_t box[2] = {64, (cuuint32_t)(16 * R)}, one[2] = {1, 1};
+  const cuuint32_t box[2] = {64u * form.W, 16u * form.R}, one[2] = {1, 1};
   if (tc::encode_fn()(&codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(a.codes), dims,
-                      &stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                      &stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, form.W == 1 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                       CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  return a.group == 128  ? launch_g128(a, codes, R, T, s)
-         : a.group == 64 ? launch_g64(a, codes, R, T, s)
-                         : launch_g32(a, codes, R, T, s);
+  return a.group == 128  ? launch_g128(a, codes, form, s)
+         : a.group == 64 ? launch_g64(a, codes, form, s)
+                         : launch_g32(a, codes, form, s);
 }
 
 void launch_w4_quantize(const void* x, int dt, long long ldx, int rows, int K, int group,

@@ -98,20 +98,23 @@ constexpr size_t kSmemMost = 226 * 1024;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 // Shared memory of a CTA beside its rings, and of one tile of every ring with its barrier.
-inline size_t rest_bytes(int K, int rows, int parts, int R, int T) {
-  return (size_t)padded(K) * 2 * rows * parts + 1024 +
-         sizeof(float) * ((size_t)kWarps * 16 * R * (8 * T + 1) + rows * (1 + 3 * kWarps));
+__host__ __device__ constexpr int red_floats(int T) {
+  return kWarps * (8 * T + 1) * (T == 1 ? 64 : 16);
 }
-inline size_t stage_bytes(int R) { return (size_t)kWarps * (16 * R * 64 + 8); }
-static_assert(kRowsMost + 1024 + 4 * (kWarps * 16 * (kColumns + 1) + kColumns * (1 + 3 * kWarps)) +
-                      2 * kWarps * (16 * 64 + 8) <=
-                  kSmemMost,
-              "two tiles of 16 rows a ring");
-// The product for one group size (w4_g32.cu, w4_g64.cu, w4_g128.cu): R tiles of 16 matrix rows a
-// warp, T tiles of 8 columns.
-cudaError_t launch_g32(const W4Args& a, const CUtensorMap& codes, int R, int T, cudaStream_t s);
-cudaError_t launch_g64(const W4Args& a, const CUtensorMap& codes, int R, int T, cudaStream_t s);
-cudaError_t launch_g128(const W4Args& a, const CUtensorMap& codes, int R, int T, cudaStream_t s);
+__host__ __device__ constexpr int pieces_of(int K) { return (padded(K) / 8 + 31) / 32; }
+inline size_t rest_bytes(int K, int rows, int parts, int T) {
+  return (size_t)padded(K) * 2 * rows * parts + 1024 +
+         sizeof(float) * ((size_t)red_floats(T) + rows * (2 + 2 * pieces_of(K)));
+}
+inline size_t stage_bytes(int R, int W) { return (size_t)kWarps * (16 * R * 64 * W + 8); }
+// A form of the product: tiles of 16 R matrix rows and W blocks, 8 T columns.
+struct Form {
+  int R, T, W;
+};
+// The product for one group size (w4_g32.cu, w4_g64.cu, w4_g128.cu).
+cudaError_t launch_g32(const W4Args& a, const CUtensorMap& codes, Form form, cudaStream_t s);
+cudaError_t launch_g64(const W4Args& a, const CUtensorMap& codes, Form form, cudaStream_t s);
+cudaError_t launch_g128(const W4Args& a, const CUtensorMap& codes, Form form, cudaStream_t s);
 
 }  // namespace w4
 }  // namespace spec

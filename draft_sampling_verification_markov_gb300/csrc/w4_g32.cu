@@ -4,8 +4,8 @@
 namespace spec {
 namespace w4 {
 
-cudaError_t launch_g32(const W4Args& a, const CUtensorMap& codes, int R, int T, cudaStream_t s) {
-  return launch_group<32>(a, codes, R, T, s);
+cudaError_t launch_g32(const W4Args& a, const CUtensorMap& codes, Form form, cudaStream_t s) {
+  return launch_group<32>(a, codes, form, s);
 }
 
 }  // namespace w4

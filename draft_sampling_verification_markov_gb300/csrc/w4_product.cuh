@@ -42,6 +42,19 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// c = a b (ZERO), or c += a b.
+template <bool ZERO>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (ZERO)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+  else
+    mma(c, a, b0, b1);
+}
+
 __device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -79,11 +92,12 @@ __device__ __forceinline__ uint32_t codes_odd(uint32_t w, const Zero& z) {
 }
 
 struct Frame {
-  uint8_t* ring;  // [warp][stage][16 R rows][64 bytes], 64-byte swizzled
+  uint8_t* ring;  // [warp][stage][16 R rows][64 W bytes], swizzled over that width
   uint4* x;       // the rows' columns: [block][word][column][lane % 4]
-  float* red;     // [warp][16 R][stride]
+  float* red;     // sums: [2][warp][32][stride] for T = 1, else [warp][16][stride]
   float* factor;  // [rows]
-  float* stat;    // [3][rows][kWarps]
+  float* scale;   // [rows]
+  float* stat;    // [2][rows][pieces]
   uint64_t* full; // [warp][stage]
 };
 
@@ -111,118 +125,168 @@ __device__ __forceinline__ float power(int e) {  // 2^e, cut to the normal numbe
   return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
+// 32 pieces (of eight elements) of row m as fp16 columns, the numbers times `scale`; their largest
+// |h| |weight| and the sum of (h hs)^2.
+__device__ __forceinline__ void stage_pieces(const W4Args& a, const Frame& f, int m0, int m, int p,
+                                             int cols, float hs, float scale, bool write,
+                                             float& most, float& sum) {
+  most = sum = 0.0f;
+  if (p >= padded(a.K) / 8) return;
+  float v[8];
+  load_h(a, m0 + m, p * 8, write, v);
+  if (a.weight) {
+    float g[8];
+    load8(a.weight, a.w_dtype, 0, p * 8, a.K, g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] *= hs;
+      sum = fmaf(v[i], v[i], sum);
+      v[i] *= g[i];
+      most = max_nan(most, fabsf(v[i]));
+      v[i] *= scale;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] *= hs;
+      most = max_nan(most, fabsf(v[i]));
+      v[i] *= scale;
+    }
+  }
+  // piece of the block -> (word, lane of the quad)
+  const int pi = p & 15;
+  int w, t;
+  if (a.group == 128) {
+    t = pi >> 2;
+    w = pi & 3;
+  } else if (a.group == 64) {
+    t = (pi & 7) >> 1;
+    w = (pi >> 3) * 2 + (pi & 1);
+  } else {
+    t = pi & 3;
+    w = pi >> 2;
+  }
+  uint4* to = f.x + (size_t)((p >> 4) * 4 + w) * cols * 4 + t;
+  for (int c = 0; c < a.parts; ++c) {
+    __half2 pair[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      pair[i] = __floats2half2_rn(v[i], v[i + 4]);
+      const float2 back = __half22float2(pair[i]);
+      v[i] = __fsub_rn(v[i], back.x);
+      v[i + 4] = __fsub_rn(v[i + 4], back.y);
+    }
+    to[(m * a.parts + c) * 4] = *reinterpret_cast<const uint4*>(pair);
+  }
+}
+
 // The chunk's rows into shared memory as fp16 columns, with the factors that their sums take; h goes
-// out, a share from each CTA of the chunk. A row is scaled by powers of two so that the bound max |h|
-// max |weight| of its numbers is between 2^13 and 2^15: fp16 goes down to 2^-24, 2^-37 of that.
+// out, a share from each CTA of the chunk. fp16 ends at 2^16 and its numbers are 2^-24 apart at the
+// least: rows are multiplied by 2^4, which serves if the largest number, |h| |weight|, is between
+// 2^-3 and 2^11; others are staged once more, by the power of two that brings theirs to 2^12 ..
+// 2^14. The pieces are dealt to the warps by 32, whatever row they are of.
+constexpr float kScale = 16.0f, kScaleLeast = 0x1p-3f, kScaleMost = 0x1p11f;
+template <typename F>
 __device__ __forceinline__ void stage_rows(const W4Args& a, const Frame& f, int m0, int rows,
-                                           int cols, int share, int shares) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int pieces = padded(a.K) / 8;
+                                           int cols, int share, int shares, F&& loaded) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per_row = pieces_of(a.K), all = rows * per_row;
   const bool norm = a.weight != nullptr;
-  for (int m = 0; m < rows; ++m) {
-    float most = 0.0f, sum = 0.0f, gain = norm ? 0.0f : 1.0f;
-    for (int p = tid; p < pieces; p += kThreads) {
-      float v[8];
-      load_h(a, m0 + m, p * 8, p % shares == share, v);
+  auto pass = [&](int c, float hs, float scale, bool write) {
+    const int m = c / per_row, at = c % per_row;
+    float most, sum;
+    stage_pieces(a, f, m0, m, at * 32 + lane, cols, hs, scale, write, most, sum);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        most = max_nan(most, fabsf(v[i]));
-        sum = fmaf(v[i], v[i], sum);
-      }
-      if (norm) {
-        load8(a.weight, a.w_dtype, 0, p * 8, a.K, v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) gain = max_nan(gain, fabsf(v[i]));
-      }
+    for (int o = 16; o > 0; o >>= 1) {
+      most = max_nan(most, __shfl_xor_sync(kFull, most, o));
+      sum += __shfl_xor_sync(kFull, sum, o);
+    }
+    if (lane == 0) {
+      f.stat[c] = most;
+      f.stat[all + c] = sum;
+    }
+  };
+#pragma unroll 2
+  for (int c = warp; c < all; c += kWarps) pass(c, 1.0f, kScale, c % shares == share);
+  loaded();
+  __syncthreads();
+  // the largest number and the sum of a row, in one warp
+  auto row = [&](int m, float& most, float& sum) {
+    most = sum = 0.0f;
+    for (int i = lane; i < per_row; i += 32) {
+      most = max_nan(most, f.stat[m * per_row + i]);
+      sum += f.stat[all + m * per_row + i];
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       most = max_nan(most, __shfl_xor_sync(kFull, most, o));
-      gain = max_nan(gain, __shfl_xor_sync(kFull, gain, o));
       sum += __shfl_xor_sync(kFull, sum, o);
     }
+  };
+  bool again = false;
+  for (int m = warp; m < rows; m += kWarps) {
+    float most, sum;
+    row(m, most, sum);
+    const float factor = norm ? 1.0f / sqrtf(sum / (float)a.K + a.eps) : 1.0f;
+    const bool serves = most >= kScaleLeast && most < kScaleMost &&
+                        (!norm || (sum > 0x1p-60f && sum < INFINITY));
+    float to = 0.0f;
+    if (!serves && (norm || most != 0.0f)) {  // a row of zeros needs no scale without a norm
+      again = true;
+      to = 1.0f;
+    }
     if (lane == 0) {
-      f.stat[m * kWarps + warp] = most;
-      f.stat[(rows + m) * kWarps + warp] = sum;
-      f.stat[(2 * rows + m) * kWarps + warp] = gain;
+      f.factor[m] = factor * (1.0f / kScale);
+      f.scale[m] = to;
     }
   }
-  __syncthreads();
+  if (!__syncthreads_or(again)) return;
+  // Rows again whose numbers, or their squares, leave the range: h 2^-eh is below 2, times the
+  // weight it is scaled by its own largest. Every warp finds both powers for itself.
   for (int m = 0; m < rows; ++m) {
-    float most = 0.0f, sum = 0.0f, gain = 0.0f;
-    for (int w = 0; w < kWarps; ++w) {
-      most = max_nan(most, f.stat[m * kWarps + w]);
-      sum += f.stat[(rows + m) * kWarps + w];
-      gain = max_nan(gain, f.stat[(2 * rows + m) * kWarps + w]);
-    }
-    if (!(most < INFINITY) && share == 0 && tid == 0) atomicOr(a.status, SPEC_DEV_NONFINITE);
-    // h 2^-eh is below 2, times the weight 2^-eg below 4
-    const int eh = most > 0.0f && most < INFINITY ? exponent(most) : 0;
-    const int eg = gain > 0.0f && gain < INFINITY ? exponent(gain) : 0;
-    if (norm && most > 0.0f && most < INFINITY && (most > 0x1p50f || most < 0x1p-40f)) {
-      // squares that leave fp32's range: those of h 2^-eh
-      __syncthreads();
-      sum = 0.0f;
-      for (int p = tid; p < pieces; p += kThreads) {
-        float v[8];
-        load_h(a, m0 + m, p * 8, false, v);
+    if (f.scale[m] == 0.0f) continue;
+    float most_h = 0.0f, most = 0.0f;
+    for (int p = lane; p < per_row * 32; p += 32) {
+      if (p * 8 >= a.K) break;
+      float v[8];
+      load_h(a, m0 + m, p * 8, false, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          v[i] *= power(-eh);
-          sum = fmaf(v[i], v[i], sum);
-        }
+      for (int i = 0; i < 8; ++i) most_h = max_nan(most_h, fabsf(v[i]));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      most_h = max_nan(most_h, __shfl_xor_sync(kFull, most_h, o));
+    if (!(most_h < INFINITY) && share == 0 && threadIdx.x == 0)
+      atomicOr(a.status, SPEC_DEV_NONFINITE);
+    const int eh = most_h > 0.0f && most_h < INFINITY ? exponent(most_h) : 0;
+    if (norm) {
+      for (int p = lane; p < per_row * 32; p += 32) {
+        if (p * 8 >= a.K) break;
+        float v[8], g[8];
+        load_h(a, m0 + m, p * 8, false, v);
+        load8(a.weight, a.w_dtype, 0, p * 8, a.K, g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) most = max_nan(most, fabsf(v[i] * power(-eh) * g[i]));
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-      if (lane == 0) f.stat[(rows + m) * kWarps + warp] = sum;
-      __syncthreads();
-      sum = 0.0f;
-      for (int w = 0; w < kWarps; ++w) sum += f.stat[(rows + m) * kWarps + w];
+      for (int o = 16; o > 0; o >>= 1) most = max_nan(most, __shfl_xor_sync(kFull, most, o));
+    } else {
+      most = most_h * power(-eh);
+    }
+    const int e = most > 0.0f && most < INFINITY ? exponent(most) : 0;
+    __syncthreads();  // the factors and the columns of before have been read
+    for (int c = m * per_row + warp; c < (m + 1) * per_row; c += kWarps)
+      pass(c, power(-eh), power(13 - e), false);
+    __syncthreads();
+    if (warp == 0) {
+      float sum;
+      row(m, most, sum);
       sum /= (float)a.K;
       // beside eps in the scale in which neither passes fp32's range
-      const float q = eh < 0 && a.eps > 0.0f
-                          ? power(eh) / sqrtf(a.eps + sum * power(eh) * power(eh))
-                          : 1.0f / sqrtf(sum + a.eps * power(-eh) * power(-eh));
-      if (tid == 0) f.factor[m] = q * power(eg) * 0x1p-13f;
-    } else if (tid == 0) {
-      f.factor[m] = norm ? power(eh) / sqrtf(sum / (float)a.K + a.eps) * power(eg) * 0x1p-13f
-                         : power(eh) * 0x1p-13f;
-    }
-    for (int p = tid; p < pieces; p += kThreads) {
-      float v[8], g[8];
-      load_h(a, m0 + m, p * 8, false, v);
-      if (norm) load8(a.weight, a.w_dtype, 0, p * 8, a.K, g);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[i] *= power(-eh);
-        if (norm) v[i] *= g[i] * power(-eg);
-        v[i] *= 0x1p13f;
-      }
-      // piece of the block -> (word, lane of the quad)
-      const int pi = p & 15;
-      int w, t;
-      if (a.group == 128) {
-        t = pi >> 2;
-        w = pi & 3;
-      } else if (a.group == 64) {
-        t = (pi & 7) >> 1;
-        w = (pi >> 3) * 2 + (pi & 1);
-      } else {
-        t = pi & 3;
-        w = pi >> 2;
-      }
-      uint4* to = f.x + (size_t)((p >> 4) * 4 + w) * cols * 4 + t;
-      for (int q = 0; q < a.parts; ++q) {
-        __half2 c[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          c[i] = __floats2half2_rn(v[i], v[i + 4]);
-          const float2 back = __half22float2(c[i]);
-          v[i] = __fsub_rn(v[i], back.x);
-          v[i + 4] = __fsub_rn(v[i + 4], back.y);
-        }
-        to[(m * a.parts + q) * 4] = *reinterpret_cast<const uint4*>(c);
-      }
+      const float q = !norm                      ? power(eh)
+                      : eh < 0 && a.eps > 0.0f ? power(eh) / sqrtf(a.eps + sum * power(eh) * power(eh))
+                                               : 1.0f / sqrtf(sum + a.eps * power(-eh) * power(-eh));
+      if (lane == 0) f.factor[m] = q * power(e) * 0x1p-13f;
     }
   }
   __syncthreads();
@@ -268,18 +332,19 @@ struct Side {
   uint32_t z[ZEROS ? R : 1][2];  // a byte a group
 };
 
-// kw warps (a.k_warps) share 16 R matrix rows, each takes a range of the blocks; kWarps / kw such
-// teams a CTA go through the matrix by themselves.
-template <int G, int R, int T, bool ZEROS, bool NARROW>
+// A tile is 16 R matrix rows of W blocks. kw warps (a.k_warps) share its rows, each takes a range of
+// the tiles along K; kWarps / kw such teams a CTA go through the matrix by themselves.
+template <int G, int R, int T, int W, bool ZEROS, bool NARROW>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const W4Args a, const __grid_constant__ CUtensorMap codes) {
   extern __shared__ __align__(1024) uint8_t smem[];
   constexpr int kGroups = kBlock / G;
   constexpr int kStride = 8 * T + 1;
-  constexpr int kTile = 16 * R * 64;  // bytes
+  constexpr int kRow = 64 * W;        // bytes of a tile's row
+  constexpr int kTile = 16 * R * kRow;
   constexpr int kSize = NARROW ? 2 : 4;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int Kp = padded(a.K), KB = Kp / kBlock;
+  const int Kp = padded(a.K), KB = Kp / kBlock, KT = (KB + W - 1) / W;
   const int real_groups = (a.K + G - 1) / G;
   const int chunk = blockIdx.x % a.chunks, share = blockIdx.x / a.chunks;
   const int shares = gridDim.x / a.chunks;
@@ -289,16 +354,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   f.ring = smem + (1024 - (tc::smem_u32(smem) & 1023)) % 1024;
   f.x = reinterpret_cast<uint4*>(f.ring + (size_t)kWarps * stages * kTile);
   f.red = reinterpret_cast<float*>(f.x + (size_t)KB * 16 * a.chunk_rows * a.parts);
-  f.full = reinterpret_cast<uint64_t*>(f.red + kWarps * 16 * R * kStride);
+  f.full = reinterpret_cast<uint64_t*>(f.red + red_floats(T));
   f.factor = reinterpret_cast<float*>(f.full + kWarps * stages);
-  f.stat = f.factor + a.chunk_rows;
+  f.scale = f.factor + a.chunk_rows;
+  f.stat = f.scale + a.chunk_rows;
   __shared__ int abort;
 
   const int kw = a.k_warps, wk = warp & (kw - 1), team = warp / kw;
   const int teams = shares * (kWarps / kw), first = share * (kWarps / kw) + team;
-  const int units = (a.N + 16 * R - 1) / (16 * R), nk = (KB + kw - 1) / kw;
+  const int units = (a.N + 16 * R - 1) / (16 * R), nk = (KT + kw - 1) / kw;
   const int mine = first < units ? (units - first - 1) / teams + 1 : 0;
-  const int my_nk = max(0, min(nk, KB - wk * nk));  // the last warps may have fewer blocks, or none
+  const int my_nk = max(0, min(nk, KT - wk * nk));  // the last warps may have fewer tiles, or none
   const size_t row_groups = Kp / G;
   uint8_t* ring = f.ring + (size_t)warp * stages * kTile;
   uint64_t* full = f.full + warp * stages;
@@ -310,65 +376,76 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   grid_dep_wait();
 
-  // tiles, by the first lane: unit and block of the next one
+  // tiles, by the first lane: coordinates of the next one
   const uint64_t policy = tc::policy_evict_first();
-  const int tiles = mine * my_nk;
-  int pu = first, pk = 0, issued = 0;
+  const int tiles = mine * my_nk, x_end = (wk * nk + my_nk) * kRow;
+  int px = wk * nk * kRow, py = first * 16 * R, issued = 0;
   auto issue = [&](int stage) {
     if (issued < tiles && lane == 0) {
       tc::mbar_arrive_expect_tx(&full[stage], kTile);
-      tc::tma_load_2d(ring + stage * kTile, &codes, (wk * nk + pk) * 64, pu * 16 * R, &full[stage],
-                      policy);
+      tc::tma_load_2d(ring + stage * kTile, &codes, px, py, &full[stage], policy);
     }
     ++issued;
-    if (++pk == my_nk) {
-      pk = 0;
-      pu += teams;
+    px += kRow;
+    if (px == x_end) {
+      px = wk * nk * kRow;
+      py += teams * 16 * R;
     }
   };
-  if (my_nk)
-    for (int i = 0; i < stages; ++i) issue(i);
 
-  // scales and zero points, two blocks ahead
-  Side<G, R, ZEROS, NARROW> side[2];
+  // scales and zero points, a tile ahead
+  Side<G, R, ZEROS, NARROW> side[W];
   int su = first, sk = 0;
   const uint8_t *ps = nullptr, *pz = nullptr;
-  int srow = 0;
-  auto load_side = [&](Side<G, R, ZEROS, NARROW>& to) {
-    if (su >= units) return;
-    if (sk == 0) {
-      srow = su * 16 * R + g;
-      const size_t at = (size_t)srow * row_groups + (size_t)wk * nk * kGroups;
-      ps = static_cast<const uint8_t*>(a.scales) + at * kSize;
-      if (ZEROS) pz = a.zeros + at;
-    }
+  const size_t below = row_groups * kSize * 8;  // eight rows on
+  auto load_side = [&](Side<G, R, ZEROS, NARROW>& to, int kb) {
+    if (su >= units || kb >= KB) return;
+    const uint8_t* p = ps;
+    const uint8_t* zp = pz;
+    const bool whole = (su + 1) * 16 * R <= a.N;
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int below = r * 16 + h * 8;
-        if (srow + below >= a.N) continue;
-        to.s[r][h].load(ps + below * (row_groups * kSize));
+    for (int i = 0; i < 2 * R; ++i) {
+      if (whole || su * 16 * R + i * 8 + g < a.N) {
+        to.s[i / 2][i % 2].load(p);
         if constexpr (ZEROS) {
-          const uint8_t* zp = pz + below * row_groups;
           uint32_t z = zp[0];
 #pragma unroll
-          for (int i = 1; i < kGroups; ++i) z |= (uint32_t)zp[i] << (8 * i);
-          to.z[r][h] = z;
+          for (int q = 1; q < kGroups; ++q) z |= (uint32_t)zp[q] << (8 * q);
+          to.z[i / 2][i % 2] = z;
         }
       }
+      p += below;
+      if (ZEROS) zp += row_groups * 8;
+    }
+  };
+  auto start_unit = [&]() {
+    const size_t at = (size_t)(su * 16 * R + g) * row_groups + (size_t)wk * nk * W * kGroups;
+    ps = static_cast<const uint8_t*>(a.scales) + at * kSize;
+    if (ZEROS) pz = a.zeros + at;
+  };
+  auto next_block = [&]() {
     ps += kGroups * kSize;
     if (ZEROS) pz += kGroups;
+  };
+  auto next_tile = [&]() {
     if (++sk == my_nk) {
       sk = 0;
       su += teams;
+      start_unit();
     }
   };
-  if (my_nk) {
-    load_side(side[0]);
-    load_side(side[1]);
-  }
-  stage_rows(a, f, m0, rows, cols, share, shares);
+  // the rows first: behind the rings' 60 to 190 KB an SM their loads would wait
+  stage_rows(a, f, m0, rows, cols, share, shares, [&]() {
+    if (my_nk == 0) return;
+    for (int i = 0; i < stages; ++i) issue(i);
+    start_unit();
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      load_side(side[i], wk * nk * W + i);
+      next_block();
+    }
+    next_tile();
+  });
 
   float acc[R][T][4];
 #pragma unroll
@@ -378,63 +455,44 @@ __global__ void __launch_bounds__(kThreads, 1)
   int col[T];  // columns past the last one repeat it and are not used
 #pragma unroll
   for (int j = 0; j < T; ++j) col[j] = min(cols - 1, j * 8 + g) * 4 + t;
-  // the lane's 16-byte chunks of matrix rows g and g + 8 (mod 16): chunk ^ (row / 2 % 4)
-  const int turn = (g >> 1) & 3;
+  // 16-byte chunks of a tile's row are stored at chunk ^ (row / 2 % 4), or ^ (row % 8)
+  const int turn = W == 1 ? (g >> 1) & 3 : g & 7;
   int stage = 0, parity = 0, unit = first, ik = 0, done = 0;
   bool ok = true;
 
-  auto block = [&](const Side<G, R, ZEROS, NARROW>& sd) {
-    if (ok && !tc::mbar_wait(&full[stage], parity, &abort, a.status)) {
-      // copies in flight land before the CTA's memory is another's; from here on the warp goes on
-      // without waiting or copying, so that its team's barriers are met
-      ok = false;
-      const int in_flight = min(issued, tiles) - done;
-      for (int i = 0; i < in_flight; ++i) {
-        const int at = stage + i < stages ? stage + i : stage + i - stages;
-        tc::mbar_drain(&full[at], stage + i < stages ? parity : parity ^ 1);
-      }
-    }
-    ++done;
-    const uint8_t* tile = ring + stage * kTile + g * 64;
+  auto block = [&](const uint8_t* tile, int kb, int i, const Side<G, R, ZEROS, NARROW>& sd) {
     uint32_t c[R][2][4];
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint8_t* p = tile + (r * 16 + h * 8) * 64;
+        const uint8_t* p = tile + (r * 16 + h * 8) * kRow;
         if constexpr (G == 128) {
-          const uint4 q = *reinterpret_cast<const uint4*>(p + (t ^ turn) * 16);
+          const uint4 q = *reinterpret_cast<const uint4*>(p + ((4 * i + t) ^ turn) * 16);
           c[r][h][0] = q.x;
           c[r][h][1] = q.y;
           c[r][h][2] = q.z;
           c[r][h][3] = q.w;
         } else if constexpr (G == 64) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint2 q = *reinterpret_cast<const uint2*>(p + ((2 * i + (t >> 1)) ^ turn) * 16 +
-                                                            (t & 1) * 8);
-            c[r][h][2 * i] = q.x;
-            c[r][h][2 * i + 1] = q.y;
+          for (int w = 0; w < 2; ++w) {
+            const uint2 q = *reinterpret_cast<const uint2*>(
+                p + ((4 * i + 2 * w + (t >> 1)) ^ turn) * 16 + (t & 1) * 8);
+            c[r][h][2 * w] = q.x;
+            c[r][h][2 * w + 1] = q.y;
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            c[r][h][i] = *reinterpret_cast<const uint32_t*>(p + (i ^ turn) * 16 + t * 4);
+          for (int w = 0; w < 4; ++w)
+            c[r][h][w] =
+                *reinterpret_cast<const uint32_t*>(p + ((4 * i + w) ^ turn) * 16 + t * 4);
         }
       }
-    const int kb = wk * nk + ik;
     const uint4* xb = f.x + (size_t)kb * 16 * cols;
     float part[R][T][4];
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       constexpr int kPer = 4 / kGroups;  // words of a group
-      if (w % kPer == 0) {
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int j = 0; j < T; ++j)
-            part[r][j][0] = part[r][j][1] = part[r][j][2] = part[r][j][3] = 0.0f;
-      }
       uint4 b[T];
 #pragma unroll
       for (int j = 0; j < T; ++j) b[j] = xb[w * cols * 4 + col[j]];
@@ -452,12 +510,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t q[4] = {codes_even(w0, z0), codes_even(w1, z1), codes_odd(w0, z0),
                                  codes_odd(w1, z1)};
 #pragma unroll
-          for (int j = 0; j < T; ++j) mma(part[r][j], q, s ? b[j].z : b[j].x, s ? b[j].w : b[j].y);
+          for (int j = 0; j < T; ++j) {
+            if (s == 0 && w % kPer == 0)
+              mma<true>(part[r][j], q, b[j].x, b[j].y);
+            else
+              mma<false>(part[r][j], q, s ? b[j].z : b[j].x, s ? b[j].w : b[j].y);
+          }
         }
         if (w % kPer == kPer - 1) {
-          const int i = w / kPer;
-          float s0 = sd.s[r][0][i], s1 = sd.s[r][1][i];
-          if (kb * kGroups + i >= real_groups) s0 = s1 = 0.0f;  // of the padding
+          const int n = w / kPer;
+          float s0 = sd.s[r][0][n], s1 = sd.s[r][1][n];
+          if (kGroups > 1 && kb * kGroups + n >= real_groups) s0 = s1 = 0.0f;  // of the padding
 #pragma unroll
           for (int j = 0; j < T; ++j) {
             acc[r][j][0] = fmaf(s0, part[r][j][0], acc[r][j][0]);
@@ -468,70 +531,95 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+  };
+  // The unit's sums, over the warps that share its rows; with one tile of columns all rows at once,
+  // in one of two buffers, so that one barrier is enough, else 16 rows at a time.
+  int buffer = 0;
+  auto finish = [&]() {
+    constexpr int kRows = T == 1 ? 16 * R : 16;
+#pragma unroll
+    for (int r0 = 0; r0 < R; r0 += kRows / 16) {
+      float* red = f.red + (buffer * kWarps + warp) * kRows * kStride;
+#pragma unroll
+      for (int r = 0; r < kRows / 16; ++r)
+#pragma unroll
+        for (int j = 0; j < T; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            red[(r * 16 + (i >> 1) * 8 + g) * kStride + j * 8 + t * 2 + (i & 1)] =
+                acc[r0 + r][j][i];
+            acc[r0 + r][j][i] = 0.0f;
+          }
+      bar_sync(1 + team, 32 * kw);
+      for (int e = wk * 32 + lane; e < rows * kRows; e += 32 * kw) {
+        const int m = e / kRows, n = (unit * R + r0) * 16 + e % kRows;
+        if (n >= a.N) continue;
+        const float* at = f.red + (buffer * kWarps + team * kw) * kRows * kStride +
+                          (e % kRows) * kStride + m * a.parts;
+        float y = 0.0f;
+        for (int w = 0; w < kw; ++w)
+          for (int q = 0; q < a.parts; ++q) y += at[w * kRows * kStride + q];
+        y *= f.factor[m];
+        const size_t to = (size_t)(m0 + m) * a.ldo + n;
+        if (a.out_dtype == SPEC_BF16)
+          static_cast<__nv_bfloat16*>(a.out)[to] = __float2bfloat16_rn(y);
+        else
+          static_cast<float*>(a.out)[to] = y;
+      }
+      if constexpr (T == 1)
+        buffer ^= 1;
+      else
+        bar_sync(1 + team, 32 * kw);
+    }
+    unit += teams;
+  };
+
+  if (my_nk == 0) {
+    for (int i = 0; i < mine; ++i) finish();
+    return;
+  }
+  for (int it = 0; it < tiles; ++it) {
+    if (ok && !tc::mbar_wait(&full[stage], parity, &abort, a.status)) {
+      // copies in flight land before the CTA's memory is another's; from here on the warp goes on
+      // without waiting or copying, so that its team's barriers are met
+      ok = false;
+      const int in_flight = min(issued, tiles) - done;
+      for (int i = 0; i < in_flight; ++i) {
+        const int at = stage + i < stages ? stage + i : stage + i - stages;
+        tc::mbar_drain(&full[at], stage + i < stages ? parity : parity ^ 1);
+      }
+    }
+    ++done;
+    const uint8_t* tile = ring + stage * kTile + g * kRow;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const int kb = (wk * nk + ik) * W + i;
+      if (i == 0 || kb < KB) block(tile, kb, i, side[i]);
+      load_side(side[i], (wk * nk + sk) * W + i);
+      next_block();
+    }
+    next_tile();
     __syncwarp();  // every lane has read the tile
     if (ok) issue(stage);
     if (++stage == stages) {
       stage = 0;
       parity ^= 1;
     }
-  };
-  // the unit's sums, over the warps that share its rows
-  auto finish = [&]() {
-    float* red = f.red + warp * 16 * R * kStride;
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int j = 0; j < T; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          red[(r * 16 + (i >> 1) * 8 + g) * kStride + j * 8 + t * 2 + (i & 1)] = acc[r][j][i];
-          acc[r][j][i] = 0.0f;
-        }
-    bar_sync(1 + team, 32 * kw);
-    for (int e = wk * 32 + lane; e < rows * 16 * R; e += 32 * kw) {
-      const int m = e / (16 * R), r = e % (16 * R), n = unit * 16 * R + r;
-      if (n >= a.N) continue;
-      const float* at = f.red + (size_t)team * kw * 16 * R * kStride + r * kStride + m * a.parts;
-      float y = 0.0f;
-      for (int w = 0; w < kw; ++w)
-        for (int q = 0; q < a.parts; ++q) y += at[w * 16 * R * kStride + q];
-      y *= f.factor[m];
-      const size_t to = (size_t)(m0 + m) * a.ldo + n;
-      if (a.out_dtype == SPEC_BF16)
-        static_cast<__nv_bfloat16*>(a.out)[to] = __float2bfloat16_rn(y);
-      else
-        static_cast<float*>(a.out)[to] = y;
-    }
-    bar_sync(1 + team, 32 * kw);
-    unit += teams;
-  };
-
-  if (my_nk == 0) {
-    for (int i = 0; i < mine; ++i) finish();
-  } else {
-    for (int it = 0; it < tiles; it += 2) {
-#pragma unroll
-      for (int d = 0; d < 2; ++d) {
-        if (it + d >= tiles) break;
-        block(side[d]);
-        load_side(side[d]);
-        if (++ik == my_nk) {
-          ik = 0;
-          finish();
-        }
-      }
+    if (++ik == my_nk) {
+      ik = 0;
+      finish();
     }
   }
 }
 
-template <int G, int R, int T, bool ZEROS, bool NARROW>
+template <int G, int R, int T, int W, bool ZEROS, bool NARROW>
 cudaError_t launch_t(W4Args a, const CUtensorMap& codes, cudaStream_t s) {
   const int units = (a.N + 16 * R - 1) / (16 * R), teams = kWarps / a.k_warps;
-  const size_t rest = rest_bytes(a.K, a.chunk_rows, a.parts, R, T), kStage = stage_bytes(R);
+  const size_t rest = rest_bytes(a.K, a.chunk_rows, a.parts, T), kStage = stage_bytes(R, W);
   a.stages = 4;
   while (a.stages > 2 && rest + a.stages * kStage > kSmemMost) --a.stages;
   const size_t smem = rest + a.stages * kStage;
-  auto k = product_kernel<G, R, T, ZEROS, NARROW>;
+  auto k = product_kernel<G, R, T, W, ZEROS, NARROW>;
   const cudaError_t e =
       cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
@@ -542,24 +630,26 @@ cudaError_t launch_t(W4Args a, const CUtensorMap& codes, cudaStream_t s) {
                        codes);
 }
 
-template <int G, int R, int T>
+template <int G, int R, int T, int W>
 cudaError_t launch_form(const W4Args& a, const CUtensorMap& codes, cudaStream_t s) {
   const bool narrow = a.scale_dtype == SPEC_BF16;
   if (a.zeros)
-    return narrow ? launch_t<G, R, T, true, true>(a, codes, s)
-                  : launch_t<G, R, T, true, false>(a, codes, s);
-  return narrow ? launch_t<G, R, T, false, true>(a, codes, s)
-                : launch_t<G, R, T, false, false>(a, codes, s);
+    return narrow ? launch_t<G, R, T, W, true, true>(a, codes, s)
+                  : launch_t<G, R, T, W, true, false>(a, codes, s);
+  return narrow ? launch_t<G, R, T, W, false, true>(a, codes, s)
+                : launch_t<G, R, T, W, false, false>(a, codes, s);
 }
 
 template <int G>
-cudaError_t launch_group(const W4Args& a, const CUtensorMap& codes, int R, int T, cudaStream_t s) {
-  if (R == 2)
-    return T == 1 ? launch_form<G, 2, 1>(a, codes, s) : launch_form<G, 2, 2>(a, codes, s);
-  return T == 1   ? launch_form<G, 1, 1>(a, codes, s)
-         : T == 2 ? launch_form<G, 1, 2>(a, codes, s)
-         : T == 3 ? launch_form<G, 1, 3>(a, codes, s)
-                  : launch_form<G, 1, 5>(a, codes, s);
+cudaError_t launch_group(const W4Args& a, const CUtensorMap& codes, Form form, cudaStream_t s) {
+  if (form.R == 2)
+    return form.T == 1 ? form.W == 2 ? launch_form<G, 2, 1, 2>(a, codes, s)
+                                     : launch_form<G, 2, 1, 1>(a, codes, s)
+                       : launch_form<G, 2, 2, 1>(a, codes, s);
+  return form.T == 1   ? launch_form<G, 1, 1, 1>(a, codes, s)
+         : form.T == 2 ? launch_form<G, 1, 2, 1>(a, codes, s)
+         : form.T == 3 ? launch_form<G, 1, 3, 1>(a, codes, s)
+                       : launch_form<G, 1, 5, 1>(a, codes, s);
 }
 
 }  // namespace
