@@ -94,17 +94,20 @@ __device__ __forceinline__ float load_scale(const void* p, int dt, size_t at) {
 // Largest number of columns of a chunk, shared memory of its rows, threads of the product's CTAs.
 constexpr int kColumns = 40;
 constexpr size_t kRowsMost = 144 * 1024;
-constexpr size_t kSmemMost = 226 * 1024;
+constexpr size_t kSmemMost = 225 * 1024;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 // Shared memory of a CTA beside its rings, and of one tile of every ring with its barrier.
-__host__ __device__ constexpr int red_floats(int T) {
-  return kWarps * (8 * T + 1) * (T == 1 ? 64 : 16);
-}
+__host__ __device__ constexpr int red_stride(int rows) { return rows | 1; }
 __host__ __device__ constexpr int pieces_of(int K) { return (padded(K) / 8 + 31) / 32; }
-inline size_t rest_bytes(int K, int rows, int parts, int T) {
+inline size_t rest_bytes(int K, int rows, int parts, int R) {
   return (size_t)padded(K) * 2 * rows * parts + 1024 +
-         sizeof(float) * ((size_t)red_floats(T) + rows * (2 + 2 * pieces_of(K)));
+         sizeof(float) * ((size_t)kWarps * 16 * R * red_stride(rows) + rows * (2 + 2 * pieces_of(K)));
+}
+// Tiles of a warp, of KT that kw warps share: whole multiples of `whole`.
+__host__ __device__ constexpr int tiles_of(int KT, int kw, int whole) {
+  const int n = (KT + kw - 1) / kw, q = whole > 1 ? whole : 1;
+  return (n + q - 1) / q * q;
 }
 inline size_t stage_bytes(int R, int W) { return (size_t)kWarps * (16 * R * 64 * W + 8); }
 // A form of the product: tiles of 16 R matrix rows and W blocks, 8 T columns.

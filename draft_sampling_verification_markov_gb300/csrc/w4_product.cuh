@@ -11,14 +11,15 @@
 // took 104 us.) A warp's mma.sync m16n8k16 takes 16 matrix rows against 8 columns: the codes
 // become fp16 numbers 1024 + code, or 1024 + 16 code, with one logical operation a pair (and a shift
 // for every second one), code - zero with one more, all exact; the scale is applied to a group's fp32
-// sum. Four warps that share a tile's rows, each a quarter of K, add their sums through shared
-// memory; such teams go through the matrix by themselves. tcgen05 would want the unpacked matrix in shared memory, four times the bytes, for a
+// sum. Two to sixteen warps that share a tile's rows, each a range of K, add their sums through
+// shared memory; such teams go through the matrix by themselves. tcgen05 would want the unpacked matrix in shared memory, four times the bytes, for a
 // multiplication that is not the bound.
 //
-// Columns. A number of the rows is one or two fp16 numbers, each a column of its own: one for bf16
-// rows as they are (exact), two where a bf16 norm weight is multiplied in (16 bits, exact) or for
-// 32-bit numbers (off by 2^-24, as the rounding of fp32 is). Rows are scaled by powers of two into
-// fp16's range; that and the norm's 1 / rms are applied to the sums.
+// Columns. A number of the rows is one or two fp16 numbers, each a column of its own. One is exact for
+// bf16 rows as they are, and serves wherever the product is rounded to bf16: 11 bits of a number that
+// is customarily rounded to bf16's 8 before such a product. For fp32 products of 32-bit rows, or with
+// a norm weight multiplied in, two: off by 2^-24, as the rounding of fp32 is. Rows are scaled by
+// powers of two into fp16's range; that and the norm's 1 / rms are applied to the sums.
 //
 // Order. A code's position in k is free as long as the rows' columns are permuted alike. A lane holds
 // words of eight codes; pair s of a word is (code s, code s + 4). With groups of 128 a lane's four
@@ -35,7 +36,7 @@ namespace {
 
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                     uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -46,7 +47,7 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
 template <bool ZERO>
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if constexpr (ZERO)
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%10,%10,%10,%10};"
         : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
@@ -70,10 +71,6 @@ __device__ __forceinline__ uint32_t masked(uint32_t w, uint32_t mask) {  // (w &
   asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(w), "r"(mask), "r"(0x64006400u));
   return d;
 }
-__device__ __forceinline__ void bar_sync(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
 // Zero points of a group as fp16 pairs: 1024 + zero, and -(64 + zero).
 struct Zero {
   uint32_t a = 0x64086408u, b = 0xd480d480u;  // of 8
@@ -94,7 +91,7 @@ __device__ __forceinline__ uint32_t codes_odd(uint32_t w, const Zero& z) {
 struct Frame {
   uint8_t* ring;  // [warp][stage][16 R rows][64 W bytes], swizzled over that width
   uint4* x;       // the rows' columns: [block][word][column][lane % 4]
-  float* red;     // sums: [2][warp][32][stride] for T = 1, else [warp][16][stride]
+  float* red;     // sums: [warp][16 R][stride]
   float* factor;  // [rows]
   float* scale;   // [rows]
   float* stat;    // [2][rows][pieces]
@@ -206,8 +203,13 @@ __device__ __forceinline__ void stage_rows(const W4Args& a, const Frame& f, int 
       f.stat[all + c] = sum;
     }
   };
-#pragma unroll 2
-  for (int c = warp; c < all; c += kWarps) pass(c, 1.0f, kScale, c % shares == share);
+  // every CTA begins elsewhere, or all would ask for the same lines at once
+  const int turn = (int)((long long)all * share / shares);
+#pragma unroll 4
+  for (int i = warp; i < all; i += kWarps) {
+    const int c = i + turn < all ? i + turn : i + turn - all;
+    pass(c, 1.0f, kScale, c % shares == share);
+  }
   loaded();
   __syncthreads();
   // the largest number and the sum of a row, in one warp
@@ -292,44 +294,45 @@ __device__ __forceinline__ void stage_rows(const W4Args& a, const Frame& f, int 
   __syncthreads();
 }
 
-// Scales of the block's groups for one matrix row, as they are stored.
-template <int G, bool NARROW>
-struct Scales {
-  static constexpr int kGroups = kBlock / G;
-  static constexpr int kWords = NARROW ? (kGroups + 1) / 2 : kGroups;
-  uint32_t w[kWords];
-
-  __device__ __forceinline__ void load(const uint8_t* p) {
-    if constexpr (NARROW && kGroups == 1) {
-      w[0] = *reinterpret_cast<const uint16_t*>(p);
-    } else if constexpr (kWords == 1) {
-      w[0] = *reinterpret_cast<const uint32_t*>(p);
-    } else if constexpr (kWords == 2) {
-      const uint2 q = *reinterpret_cast<const uint2*>(p);
-      w[0] = q.x;
-      w[1] = q.y;
-    } else {
-      const uint4 q = *reinterpret_cast<const uint4*>(p);
-      w[0] = q.x;
-      w[1] = q.y;
-      w[2] = q.z;
-      w[3] = q.w;
-    }
-  }
-  __device__ __forceinline__ float operator[](int i) const {
-    if constexpr (NARROW)
-      return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
-    else
-      return __uint_as_float(w[i]);
-  }
-};
-
-// What a lane needs of a block beside the codes: scales and zero points of its matrix rows (16 r +
-// lane / 4, and 8 below).
+// What a lane needs of four groups beside the codes: scales (as they are stored) and zero points of
+// its matrix rows (16 r + lane / 4, and 8 below). The next block's groups come first.
 template <int G, int R, bool ZEROS, bool NARROW>
 struct Side {
-  Scales<G, NARROW> s[R][2];
+  static constexpr int kWords = NARROW ? 2 : 4;
+  uint32_t s[R][2][kWords];
   uint32_t z[ZEROS ? R : 1][2];  // a byte a group
+
+  // Scale n of the next block, n < 128 / G.
+  __device__ __forceinline__ float scale(int r, int h, int n) const {
+    if constexpr (NARROW) {
+      const uint32_t w = s[r][h][n / 2];
+      return __uint_as_float(n & 1 ? w & 0xffff0000u : w << 16);
+    } else {
+      return __uint_as_float(s[r][h][n]);
+    }
+  }
+  __device__ __forceinline__ void next_block() {
+    constexpr int kGroups = kBlock / G;
+    if constexpr (kGroups == 4) return;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t(&w)[kWords] = s[r][h];
+        if constexpr (NARROW) {
+          w[0] = kGroups == 2 ? w[1] : __funnelshift_r(w[0], w[1], 16);
+          w[1] >>= 16;
+        } else if constexpr (kGroups == 2) {
+          w[0] = w[2];
+          w[1] = w[3];
+        } else {
+          w[0] = w[1];
+          w[1] = w[2];
+          w[2] = w[3];
+        }
+        if constexpr (ZEROS) z[r][h] >>= 8 * kGroups;
+      }
+  }
 };
 
 // A tile is 16 R matrix rows of W blocks. kw warps (a.k_warps) share its rows, each takes a range of
@@ -338,9 +341,9 @@ template <int G, int R, int T, int W, bool ZEROS, bool NARROW>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const W4Args a, const __grid_constant__ CUtensorMap codes) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  constexpr int kGroups = kBlock / G;
-  constexpr int kStride = 8 * T + 1;
-  constexpr int kRow = 64 * W;        // bytes of a tile's row
+  typedef Side<G, R, ZEROS, NARROW> SideT;
+  constexpr int kGroups = kBlock / G, kChunk = 4 / kGroups;  // blocks of a Side
+  constexpr int kRow = 64 * W;                               // bytes of a tile's row
   constexpr int kTile = 16 * R * kRow;
   constexpr int kSize = NARROW ? 2 : 4;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -349,20 +352,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int chunk = blockIdx.x % a.chunks, share = blockIdx.x / a.chunks;
   const int shares = gridDim.x / a.chunks;
   const int m0 = chunk * a.chunk_rows, rows = min(a.chunk_rows, a.M - m0);
-  const int cols = rows * a.parts, stages = a.stages;
+  const int cols = rows * a.parts, stages = a.stages, stride = red_stride(a.chunk_rows);
   Frame f;
   f.ring = smem + (1024 - (tc::smem_u32(smem) & 1023)) % 1024;
   f.x = reinterpret_cast<uint4*>(f.ring + (size_t)kWarps * stages * kTile);
   f.red = reinterpret_cast<float*>(f.x + (size_t)KB * 16 * a.chunk_rows * a.parts);
-  f.full = reinterpret_cast<uint64_t*>(f.red + red_floats(T));
+  f.full = reinterpret_cast<uint64_t*>(f.red + kWarps * 16 * R * stride);
   f.factor = reinterpret_cast<float*>(f.full + kWarps * stages);
   f.scale = f.factor + a.chunk_rows;
   f.stat = f.scale + a.chunk_rows;
   __shared__ int abort;
+  __shared__ uint64_t sums_there[kWarps / 2], sums_read[kWarps / 2];  // of a team
 
   const int kw = a.k_warps, wk = warp & (kw - 1), team = warp / kw;
   const int teams = shares * (kWarps / kw), first = share * (kWarps / kw) + team;
-  const int units = (a.N + 16 * R - 1) / (16 * R), nk = (KT + kw - 1) / kw;
+  const int units = (a.N + 16 * R - 1) / (16 * R);
+  const int nk = tiles_of(KT, kw, kChunk / W);
   const int mine = first < units ? (units - first - 1) / teams + 1 : 0;
   const int my_nk = max(0, min(nk, KT - wk * nk));  // the last warps may have fewer tiles, or none
   const size_t row_groups = Kp / G;
@@ -371,6 +376,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (lane == 0)
     for (int i = 0; i < stages; ++i) tc::mbar_init(&full[i], 1);
+  if (threadIdx.x < kWarps / kw) {
+    tc::mbar_init(&sums_there[threadIdx.x], kw);
+    tc::mbar_init(&sums_read[threadIdx.x], kw);
+  }
   if (threadIdx.x == 0) abort = 0;
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   __syncthreads();
@@ -393,58 +402,76 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   };
 
-  // scales and zero points, a tile ahead
-  Side<G, R, ZEROS, NARROW> side[W];
-  int su = first, sk = 0;
+  // scales and zero points, four groups at a time (with the next four loaded ahead the kernels ran out
+  // of registers: a row of 129280 x 4096 54 -> 57 us)
+  const bool aligned = row_groups % 4 == 0 && (reinterpret_cast<uintptr_t>(a.zeros) & 3) == 0;
+  const int first_group = wk * nk * W * kGroups;
+  const int end_group = min((int)row_groups, first_group + my_nk * W * kGroups);
+  int su = first, sg = first_group;  // of the next load
   const uint8_t *ps = nullptr, *pz = nullptr;
-  const size_t below = row_groups * kSize * 8;  // eight rows on
-  auto load_side = [&](Side<G, R, ZEROS, NARROW>& to, int kb) {
-    if (su >= units || kb >= KB) return;
+  auto start_unit = [&]() {
+    const size_t at = (size_t)(su * 16 * R + g) * row_groups + first_group;
+    ps = static_cast<const uint8_t*>(a.scales) + at * kSize;
+    if (ZEROS) pz = a.zeros + at;
+  };
+  auto load_side = [&](SideT& to) {
+    if (su >= units) return;
     const uint8_t* p = ps;
     const uint8_t* zp = pz;
     const bool whole = (su + 1) * 16 * R <= a.N;
 #pragma unroll
     for (int i = 0; i < 2 * R; ++i) {
+      uint32_t(&w)[SideT::kWords] = to.s[i / 2][i % 2];
       if (whole || su * 16 * R + i * 8 + g < a.N) {
-        to.s[i / 2][i % 2].load(p);
-        if constexpr (ZEROS) {
-          uint32_t z = zp[0];
+        if (aligned) {
+          if constexpr (NARROW) {
+            const uint2 q = *reinterpret_cast<const uint2*>(p);
+            w[0] = q.x;
+            w[1] = q.y;
+          } else {
+            const uint4 q = *reinterpret_cast<const uint4*>(p);
+            w[0] = q.x;
+            w[1] = q.y;
+            w[2] = q.z;
+            w[3] = q.w;
+          }
+          if constexpr (ZEROS) to.z[i / 2][i % 2] = *reinterpret_cast<const uint32_t*>(zp);
+        } else {
+          uint32_t z = 0;
 #pragma unroll
-          for (int q = 1; q < kGroups; ++q) z |= (uint32_t)zp[q] << (8 * q);
-          to.z[i / 2][i % 2] = z;
+          for (int q = 0; q < SideT::kWords; ++q) w[q] = 0;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if (sg + q >= (int)row_groups) continue;
+            if constexpr (NARROW)
+              w[q / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[q] << (q & 1 ? 16 : 0);
+            else
+              w[q] = reinterpret_cast<const uint32_t*>(p)[q];
+            if (ZEROS) z |= (uint32_t)zp[q] << (8 * q);
+          }
+          if constexpr (ZEROS) to.z[i / 2][i % 2] = z;
         }
       }
-      p += below;
+      p += row_groups * (8 * kSize);  // eight rows on
       if (ZEROS) zp += row_groups * 8;
     }
-  };
-  auto start_unit = [&]() {
-    const size_t at = (size_t)(su * 16 * R + g) * row_groups + (size_t)wk * nk * W * kGroups;
-    ps = static_cast<const uint8_t*>(a.scales) + at * kSize;
-    if (ZEROS) pz = a.zeros + at;
-  };
-  auto next_block = [&]() {
-    ps += kGroups * kSize;
-    if (ZEROS) pz += kGroups;
-  };
-  auto next_tile = [&]() {
-    if (++sk == my_nk) {
-      sk = 0;
+    sg += 4;
+    ps += 4 * kSize;
+    if (ZEROS) pz += 4;
+    if (sg >= end_group) {
+      sg = first_group;
       su += teams;
       start_unit();
     }
   };
+  SideT side;
+
   // the rows first: behind the rings' 60 to 190 KB an SM their loads would wait
   stage_rows(a, f, m0, rows, cols, share, shares, [&]() {
     if (my_nk == 0) return;
     for (int i = 0; i < stages; ++i) issue(i);
     start_unit();
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      load_side(side[i], wk * nk * W + i);
-      next_block();
-    }
-    next_tile();
+    load_side(side);
   });
 
   float acc[R][T][4];
@@ -457,10 +484,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int j = 0; j < T; ++j) col[j] = min(cols - 1, j * 8 + g) * 4 + t;
   // 16-byte chunks of a tile's row are stored at chunk ^ (row / 2 % 4), or ^ (row % 8)
   const int turn = W == 1 ? (g >> 1) & 3 : g & 7;
-  int stage = 0, parity = 0, unit = first, ik = 0, done = 0;
+  int stage = 0, parity = 0, ik = 0, done = 0, in_chunk = 0;
   bool ok = true;
 
-  auto block = [&](const uint8_t* tile, int kb, int i, const Side<G, R, ZEROS, NARROW>& sd) {
+  auto block = [&](const uint8_t* tile, int kb, int i) {
     uint32_t c[R][2][4];
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -500,8 +527,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int r = 0; r < R; ++r) {
         Zero z0, z1;
         if constexpr (ZEROS) {
-          z0 = Zero(sd.z[r][0] >> (8 * (w / kPer)) & 127u);
-          z1 = Zero(sd.z[r][1] >> (8 * (w / kPer)) & 127u);
+          z0 = Zero(side.z[r][0] >> (8 * (w / kPer)) & 127u);
+          z1 = Zero(side.z[r][1] >> (8 * (w / kPer)) & 127u);
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
@@ -519,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (w % kPer == kPer - 1) {
           const int n = w / kPer;
-          float s0 = sd.s[r][0][n], s1 = sd.s[r][1][n];
+          float s0 = side.scale(r, 0, n), s1 = side.scale(r, 1, n);
           if (kGroups > 1 && kb * kGroups + n >= real_groups) s0 = s1 = 0.0f;  // of the padding
 #pragma unroll
           for (int j = 0; j < T; ++j) {
@@ -531,57 +558,70 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  };
-  // The unit's sums, over the warps that share its rows; with one tile of columns all rows at once,
-  // in one of two buffers, so that one barrier is enough, else 16 rows at a time.
-  int buffer = 0;
-  auto finish = [&]() {
-    constexpr int kRows = T == 1 ? 16 * R : 16;
-#pragma unroll
-    for (int r0 = 0; r0 < R; r0 += kRows / 16) {
-      float* red = f.red + (buffer * kWarps + warp) * kRows * kStride;
-#pragma unroll
-      for (int r = 0; r < kRows / 16; ++r)
-#pragma unroll
-        for (int j = 0; j < T; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            red[(r * 16 + (i >> 1) * 8 + g) * kStride + j * 8 + t * 2 + (i & 1)] =
-                acc[r0 + r][j][i];
-            acc[r0 + r][j][i] = 0.0f;
-          }
-      bar_sync(1 + team, 32 * kw);
-      for (int e = wk * 32 + lane; e < rows * kRows; e += 32 * kw) {
-        const int m = e / kRows, n = (unit * R + r0) * 16 + e % kRows;
-        if (n >= a.N) continue;
-        const float* at = f.red + (buffer * kWarps + team * kw) * kRows * kStride +
-                          (e % kRows) * kStride + m * a.parts;
-        float y = 0.0f;
-        for (int w = 0; w < kw; ++w)
-          for (int q = 0; q < a.parts; ++q) y += at[w * kRows * kStride + q];
-        y *= f.factor[m];
-        const size_t to = (size_t)(m0 + m) * a.ldo + n;
-        if (a.out_dtype == SPEC_BF16)
-          static_cast<__nv_bfloat16*>(a.out)[to] = __float2bfloat16_rn(y);
-        else
-          static_cast<float*>(a.out)[to] = y;
-      }
-      if constexpr (T == 1)
-        buffer ^= 1;
-      else
-        bar_sync(1 + team, 32 * kw);
+    side.next_block();
+    if (++in_chunk == kChunk) {
+      in_chunk = 0;
+      load_side(side);
     }
+  };
+  // A unit's sums go to the other warps that share its rows (a row's columns added first) when they
+  // are done, and are added up a tile later: no warp waits for its team in between.
+  int unit = first, given = 0, taken = 0;
+  float* red = f.red + warp * 16 * R * stride;
+  auto give = [&]() {
+    if (given) tc::mbar_wait(&sums_read[team], (given - 1) & 1, &abort, a.status);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int j = 0; j < T; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float* to = red + (r * 16 + h * 8 + g) * stride;
+          const float y0 = acc[r][j][2 * h], y1 = acc[r][j][2 * h + 1];
+          acc[r][j][2 * h] = acc[r][j][2 * h + 1] = 0.0f;
+          if (a.parts == 2) {
+            if (j * 4 + t < rows) to[j * 4 + t] = y0 + y1;
+          } else {
+            if (j * 8 + t * 2 < rows) to[j * 8 + t * 2] = y0;
+            if (j * 8 + t * 2 + 1 < rows) to[j * 8 + t * 2 + 1] = y1;
+          }
+        }
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&sums_there[team]);
+    ++given;
+  };
+  auto take = [&]() {
+    tc::mbar_wait(&sums_there[team], taken & 1, &abort, a.status);
+    const float* from = f.red + team * kw * 16 * R * stride;
+    for (int e = wk * 32 + lane; e < rows * 16 * R; e += 32 * kw) {
+      const int m = e / (16 * R), r = e % (16 * R), n = unit * 16 * R + r;
+      if (n >= a.N) continue;
+      float y = 0.0f;
+      for (int w = 0; w < kw; ++w) y += from[(w * 16 * R + r) * stride + m];
+      y *= f.factor[m];
+      const size_t to = (size_t)(m0 + m) * a.ldo + n;
+      if (a.out_dtype == SPEC_BF16)
+        static_cast<__nv_bfloat16*>(a.out)[to] = __float2bfloat16_rn(y);
+      else
+        static_cast<float*>(a.out)[to] = y;
+    }
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&sums_read[team]);
+    ++taken;
     unit += teams;
   };
 
   if (my_nk == 0) {
-    for (int i = 0; i < mine; ++i) finish();
+    for (int i = 0; i < mine; ++i) {
+      give();
+      take();
+    }
     return;
   }
   for (int it = 0; it < tiles; ++it) {
     if (ok && !tc::mbar_wait(&full[stage], parity, &abort, a.status)) {
       // copies in flight land before the CTA's memory is another's; from here on the warp goes on
-      // without waiting or copying, so that its team's barriers are met
+      // without waiting or copying
       ok = false;
       const int in_flight = min(issued, tiles) - done;
       for (int i = 0; i < in_flight; ++i) {
@@ -594,28 +634,31 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int i = 0; i < W; ++i) {
       const int kb = (wk * nk + ik) * W + i;
-      if (i == 0 || kb < KB) block(tile, kb, i, side[i]);
-      load_side(side[i], (wk * nk + sk) * W + i);
-      next_block();
+      if (i == 0 || kb < KB) block(tile, kb, i);
     }
-    next_tile();
     __syncwarp();  // every lane has read the tile
     if (ok) issue(stage);
     if (++stage == stages) {
       stage = 0;
       parity ^= 1;
     }
+    if (taken < given) take();
     if (++ik == my_nk) {
       ik = 0;
-      finish();
+      if (in_chunk) {  // the unit ends within four groups
+        in_chunk = 0;
+        load_side(side);
+      }
+      give();
     }
   }
+  if (taken < given) take();
 }
 
 template <int G, int R, int T, int W, bool ZEROS, bool NARROW>
 cudaError_t launch_t(W4Args a, const CUtensorMap& codes, cudaStream_t s) {
   const int units = (a.N + 16 * R - 1) / (16 * R), teams = kWarps / a.k_warps;
-  const size_t rest = rest_bytes(a.K, a.chunk_rows, a.parts, T), kStage = stage_bytes(R, W);
+  const size_t rest = rest_bytes(a.K, a.chunk_rows, a.parts, R), kStage = stage_bytes(R, W);
   a.stages = 4;
   while (a.stages > 2 && rest + a.stages * kStage > kSmemMost) --a.stages;
   const size_t smem = rest + a.stages * kStage;

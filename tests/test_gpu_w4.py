@@ -39,7 +39,7 @@ def check(x, w, values, dtype=None, norm=None, eps=1e-6, residual=None):
         r = r[1]
     assert r.dtype == (dtype or x.dtype)
     off = (r.cpu().double() - y).abs()
-    tol = ref.tolerance(w.K, w.group, mag, y, r.dtype)
+    tol = ref.tolerance(w.K, w.group, mag, y, r.dtype, x.dtype == BF and norm is None)
     assert (off <= tol).all(), float((off / tol).max())
 
 
@@ -149,7 +149,7 @@ def test_wide_rows(K, dt):
     check(randn((7, K), 6, dt), w, v, norm=randn((K,), 7, F32), dtype=F32)
     with pytest.raises(S.SpecError) as e:
         big = S.W4Tensor.empty(4, 36865, 64, F32, DEV)
-        S.spec_w4_logits(torch.zeros(1, 36865, device=DEV), big)
+        S.spec_w4_logits(torch.zeros(1, 36865, device=DEV), big)  # a fp32 product
     assert e.value.status == S.SPEC_ERR_TOO_LARGE
 
 

@@ -60,7 +60,7 @@ def test_dequantize_refusals(S, at, rc):
     (dict(group=256), -1), (dict(res=vp(0x40000), ldr=63), -1), (dict(res=vp(0x40000), ldh=63), -1),
     (dict(dt=2), -2), (dict(sdt=2), -2), (dict(odt=2), -2), (dict(nw=P, nwdt=2), -2),
     (dict(nw=P, eps=-1.0), -1), (dict(nw=P, eps=float("nan")), -1), (dict(ws=None), -1),
-    (dict(wn=8), -3), (dict(dt=0, K=36865, ldx=36865), -7), (dict(K=73729, ldx=73729), -7),
+    (dict(wn=8), -3), (dict(dt=0, odt=0, K=36865, ldx=36865), -7), (dict(K=73729, ldx=73729), -7),
     (dict(x=None), -1), (dict(x=ODD), -1), (dict(out=None), -1), (dict(out=ODD), -1),
     (dict(codes=MIS), -1), (dict(scales=None), -1), (dict(nw=ODD), -1),
     (dict(res=vp(0x40000), ro=None), -1), (dict(res=ODD), -1),

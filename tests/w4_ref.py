@@ -5,7 +5,10 @@ scales of at most 24), except that a 32-bit row times its norm weight is rounded
 are fp32 sums: a group's on the tensor cores (G / 16 steps of 16 products a column, each step off by
 at most two units of 2^-23 of the running magnitude), one addition a group, up to 8 warps of up to 3
 columns joined, and the norm's factor: a sum of squares (2^-20 at most for 2^15 elements added in 512
-threads and a tree), a root and a division. All of it relative to sum |a w|."""
+threads and a tree), a root and a division. All of it relative to sum |a w|.
+
+For a bf16 product the numbers themselves are held in 11 bits, unless they are bf16 already: half a
+step, 2^-12 of each, and so of sum |a w|."""
 import torch
 
 
@@ -53,7 +56,9 @@ def product(x, w, K, norm=None, eps=0.0, residual=None):
     return h, a @ w.t(), a.abs() @ w.abs().t()
 
 
-def tolerance(K, group, magnitude, y, dtype):
+def tolerance(K, group, magnitude, y, dtype, exact=False):
+    """`exact`: rows of bf16 without a norm."""
     steps = 2 * (group / 16) + padded(K) / group + 24
     half = torch.finfo(dtype).eps / 2
-    return (steps * 2.0 ** -23 + 2.0 ** -20) * magnitude + half * y.abs() + 1e-37
+    held = 0.0 if exact or dtype == torch.float32 else 2.0 ** -12
+    return (held + steps * 2.0 ** -23 + 2.0 ** -20) * magnitude + half * y.abs() + 1e-37
