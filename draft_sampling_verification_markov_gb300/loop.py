@@ -47,17 +47,22 @@ class SpecLoop:
     "Module deepseek_v4_mtp", Forward, logits = lm_head(rms_norm(h)). U is then a buffer that
     each iteration overwrites; it may be None.
 
+    With top_k, top_p or min_p (numbers, or device tensors [R] with one for each request; see
+    spec.spec_truncate) the target is truncated at the loop's temperature: every iteration writes the
+    target rows with -inf outside into truncated_target, with their normalisers, and confidence,
+    scheduling and verification go by these, so the emitted tokens follow the truncated target. kept [R, gamma + 1] counts the tokens left in each row.
+
     With `logprobs` = k (0 .. 32) every iteration also scores its emitted tokens under the target
     rows that they answer to, at the loop's temperature: token_logp, token_rank, token_entropy
     [iters, R, gamma + 1] and the k most likely tokens of each row, top_ids and top_logp
-    [iters, R, gamma + 1, k]. `allowed` does not enter these: they are of the target's own
-    distribution. Places past an iteration's emitted tokens (-1 in out_tokens) are left as they
-    were: NaN, 0 and -1 until a run emits more tokens there."""
+    [iters, R, gamma + 1, k]. Neither `allowed` nor a truncation enters these: they are of the
+    target's own distribution. Places past an iteration's emitted tokens (-1 in out_tokens) are
+    left as they were: NaN, 0 and -1 until a run emits more tokens there."""
 
     def __init__(self, U, target, W1, W2, anchors0, u_draft, u_accept, u_resid, temperature,
                  sps=None, *, iterations=None, schedule=True, allowed=None,
                  async_schedule=False, flat=False, head=None, hidden=None, residual=None,
-                 logprobs=None):
+                 logprobs=None, top_k=0, top_p=1.0, min_p=0.0):
         if (head is None) != (hidden is None) or (residual is not None and head is None):
             raise ValueError("head and hidden go together, residual with them")
         if head is not None and U is None:
@@ -102,6 +107,12 @@ class SpecLoop:
             self.offsets = torch.empty(R + 1, **i32)
             self.packed_target = torch.empty(R * (gamma + 1), V, dtype=target.dtype, device=dev)
             self.packed_stats = torch.empty(R * (gamma + 1), 2, **f32)
+        plain = (("top_k", top_k, 0), ("top_p", top_p, 1.0), ("min_p", min_p, 0.0))
+        self.truncation = None
+        if any(isinstance(v, torch.Tensor) or v != none for _, v, none in plain):
+            self.truncation = {name: v for name, v, _ in plain}
+            self.truncated_target = torch.empty(R, gamma + 1, V, dtype=target.dtype, device=dev)
+            self.kept = torch.empty(R, gamma + 1, **i32)
         self.head, self.hidden, self.residual = head, hidden, residual
         self.logprobs = None if logprobs is None else int(logprobs)
         if head is not None and self.iters > hidden.shape[0]:
@@ -134,10 +145,17 @@ class SpecLoop:
                               draft_tokens=self.draft_tokens[t], draft_logp=self.draft_logp,
                               draft_stats=self.draft_stats, workspace=ws, stream=stream,
                               allowed=self.allowed)
-        S.spec_target_stats(self.target, T, stats=self.target_stats, workspace=ws, stream=stream)
+        target = self.target
+        if self.truncation is None:
+            S.spec_target_stats(target, T, stats=self.target_stats, workspace=ws, stream=stream)
+        else:
+            target = self.truncated_target
+            S.spec_truncate(self.target.view_as(target), T, **self.truncation, workspace=ws,
+                            out=S.TruncatedRows(target, self.kept, self.target_stats),
+                            stream=stream)
         lengths = None
         if self.schedule:
-            S.spec_tv_confidence(self.U, self.target, self.W1, self.W2, a_t,
+            S.spec_tv_confidence(self.U, target, self.W1, self.W2, a_t,
                                  self.draft_tokens[t], T, draft_stats=self.draft_stats,
                                  target_stats=self.target_stats, conf=self.conf[t],
                                  survival=self.survival[t], workspace=ws, stream=stream,
@@ -156,7 +174,7 @@ class SpecLoop:
             # the flattened verify batch: B packed target rows and their normalisers
             S.spec_flat_layout(lengths, self.gamma, offsets=self.offsets, markers=False,
                                workspace=ws, stream=stream)
-            tv = self.target.view(self.R, self.gamma + 1, self.V)
+            tv = target.view(self.R, self.gamma + 1, self.V)
             S.spec_flat_pack(tv, lengths, self.offsets, out=self.packed_target, workspace=ws,
                              stream=stream)
             S.spec_flat_pack(self.target_stats.view(self.R, self.gamma + 1, 2), lengths,
@@ -171,7 +189,7 @@ class SpecLoop:
                                          stream=stream, allowed=self.allowed)
             self._score(t, stream)
             return
-        S.spec_verify_rejection(self.target, self.U, self.W1, self.W2, a_t, self.draft_tokens[t],
+        S.spec_verify_rejection(target, self.U, self.W1, self.W2, a_t, self.draft_tokens[t],
                                 self.draft_logp, self.draft_stats, self.u_accept[t],
                                 self.u_resid[t], T, lengths, target_stats=self.target_stats,
                                 accept_len=self.accept_len[t], out_tokens=self.out_tokens[t],
