@@ -42,6 +42,7 @@ typedef unsigned long long u64;
 constexpr int kThreads = 256;
 constexpr int kCtas = 3;                        // of an SM
 constexpr int kWarps = kThreads / 32;
+static_assert((kWarps & (kWarps - 1)) == 0, "lanes wrap around the warps");
 constexpr int kBatch = 4;                       // 16-byte pieces of a thread's batch
 constexpr int kWarpStep = 32 * kBatch;          // consecutive pieces of a warp: a segment
 constexpr int kStep = kThreads * kBatch;        // ... of a CTA
@@ -69,10 +70,10 @@ struct Shared {
   };
   u64 keys[kList];           // listed tokens, sorted
   uint32_t bins[kBins];      // tokens by their mass
-  uint32_t slice[kBins / 2]; // of the cluster's, this part's share
   union {
     uint16_t hits[kHits];      // index entries that reach a bound
     u64 picked[2][kBuckets];   // masses of ranges, keys of one
+    uint32_t slice[kBins / 2]; // of the cluster's bins, this part's share
   };
   int n_list, n_hits;
   u64 pub[2][2];             // what a CTA shows its cluster
@@ -1334,7 +1335,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
   wt.shift = 61 - S;
   wt.most = (float)(S + 1);
 
-  for (int row = SPLIT ? blockIdx.x / parts : blockIdx.x; row < rows; row += gridDim.x) {
+  const int row = SPLIT ? blockIdx.x / parts : blockIdx.x;
+  if (row >= rows) return;
+  {
     Part<DT> part{Row<DT>(a.x, (size_t)row * a.ld, a.V), 0, 0};
     {
       const int np = part.row.pieces(), per = (np + team.parts - 1) / team.parts;
@@ -1402,7 +1405,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
       }
       if (WRITE) write_part<DT>(a, row, part, 0, true);
       team.sync();
-      continue;
+      return;
     }
     const u64 top_key = (u64)top << 32 | 0xffffffffu;
     wt.m = order_value(top);
@@ -1622,7 +1625,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
         }
       }
     }
-    team.sync();  // the next row, or this CTA's end
+    team.sync();  // no part leaves before it has been read
   }
 }
 
@@ -1635,8 +1638,7 @@ cudaError_t launch_t(const SampleArgs& a, int split, cudaStream_t s) {
   attr[1].val.clusterDim.x = split;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  const int most = kCtas * num_sms();
-  cfg.gridDim = dim3((unsigned)(SPLIT ? a.rows * split : (a.rows < most ? a.rows : most)));
+  cfg.gridDim = dim3((unsigned)a.rows * split);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
   cfg.attrs = attr;
