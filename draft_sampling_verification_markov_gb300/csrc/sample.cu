@@ -68,7 +68,15 @@ struct Shared {
     u64 seg[kSegs];            // masses of a part's segments, once the index is not needed
     u64 bucket[kBuckets];
   };
-  u64 keys[kList];           // listed tokens, sorted
+  union {
+    u64 keys[kList];           // listed tokens, sorted
+    struct {                   // while the bins are filled: where in its bin a token lies, of some
+      uint32_t off[kBins], offs[kBins];
+    };
+    struct {                   // then: masses of the bins, and of a share of the cluster's
+      float weight[kBins], shares[kBins / 2];
+    };
+  };
   uint32_t bins[kBins];      // tokens by their mass
   union {
     uint16_t hits[kHits];      // index entries that reach a bound
@@ -93,7 +101,8 @@ struct Shared {
   int edge[3], before[3], in;
   float cum[2];
   float guess;               // the share of the mass before bin_lo, as the bins have it
-  int bin_lo, bin_hi, n_above, n_window;
+  uint32_t lo_bits, hi_bits;
+  int n_above, n_window;
 };
 
 // ------------------------------------------------------------------------------ whole-number masses
@@ -127,12 +136,16 @@ struct Weigher {
   uint32_t table;          // kPowers[lane]
   int shift;               // 61 - S
 
-  __device__ __forceinline__ u64 join(float y, float t, float q) const {  // y: -(x - m) c
+  // The mass is 2 half() + 1 where there is one.
+  __device__ __forceinline__ u64 half(float t, float q) const {
     const int bits = __float_as_int(t);
     const int tab = (int)__shfl_sync(kFull, table, bits);
     const long long w = ((long long)tab << 32) + (long long)tab * __float2int_rn(q);
-    const int by = shift + (kMagicBits >> 5) - (bits >> 5);
-    const u64 v = ((u64)w >> (by & 63)) | 1u;
+    const int by = shift + 1 + (kMagicBits >> 5) - (bits >> 5);
+    return (u64)w >> (by & 63);
+  }
+  __device__ __forceinline__ u64 join(float y, float t, float q) const {  // y: -(x - m) c
+    const u64 v = 2 * half(t, q) + 1;
     return y <= most ? v : 0;  // also for NaN
   }
 
@@ -153,30 +166,50 @@ struct Weigher {
   }
 
   template <int DT>
-  __device__ __forceinline__ void pair(float x0, float x1, u64& v0, u64& v1) const {
+  __device__ __forceinline__ void terms(float x0, float x1, u64& y, u64& t, u64& q) const {
     using namespace tc;
     const u64 x = pack2(x0, x1), m2 = pack2(m, m), n1 = pack2(-1.0f, -1.0f);
     const u64 ch2 = pack2(ch, ch), nch2 = pack2(-ch, -ch), ncl2 = pack2(-cl, -cl);
     const u64 d = fma2(x, n1, m2);
-    const u64 y = mul2(d, ch2);
+    y = mul2(d, ch2);
     u64 b = fma2(d, ncl2, fma2(d, nch2, y));
     if constexpr (DT == SPEC_F32) {
       const u64 bb = add2(d, pack2(-m, -m));
       const u64 e = fma2(add2(x, bb), n1, fma2(fma2(bb, n1, d), n1, m2));
       b = fma2(e, nch2, b);
     }
-    const u64 t = fma2(y, n1, pack2(kMagic, kMagic));
+    t = fma2(y, n1, pack2(kMagic, kMagic));
     const u64 r = fma2(add2(add2(t, pack2(-kMagic, -kMagic)), y), n1, b);
-    u64 q = fma2(r, pack2(kC4, kC4), pack2(kC3, kC3));
+    q = fma2(r, pack2(kC4, kC4), pack2(kC3, kC3));
     q = fma2(r, q, pack2(kC2, kC2));
     q = fma2(r, q, pack2(kC1Rest, kC1Rest));
     q = fma2(r, pack2(kC1, kC1), mul2(r, q));
+  }
+  template <int DT>
+  __device__ __forceinline__ void pair(float x0, float x1, u64& v0, u64& v1) const {
+    u64 y, t, q;
+    terms<DT>(x0, x1, y, t, q);
     float y0, y1, t0, t1, q0, q1;
-    unpack2(y, y0, y1);
-    unpack2(t, t0, t1);
-    unpack2(q, q0, q1);
+    tc::unpack2(y, y0, y1);
+    tc::unpack2(t, t0, t1);
+    tc::unpack2(q, q0, q1);
     v0 = join(y0, t0, q0);
     v1 = join(y1, t1, q1);
+  }
+  // half() of two logits that both have a mass.
+  template <int DT>
+  __device__ __forceinline__ void halves(float x0, float x1, u64& h0, u64& h1) const {
+    u64 y, t, q;
+    terms<DT>(x0, x1, y, t, q);
+    float t0, t1, q0, q1;
+    tc::unpack2(t, t0, t1);
+    tc::unpack2(q, q0, q1);
+    h0 = half(t0, q0);
+    h1 = half(t1, q1);
+  }
+  // A finite logit from which on every one has a mass.
+  __device__ __forceinline__ float surely() const {
+    return fmaxf(m - (most - 0.125f) / ch, -3.402823466e38f);
   }
   // Bin of a mass, of t = kMagic + y: -32 y rounded; the last one, and what has none, share a bin.
   __device__ __forceinline__ static uint32_t bin(float t) {
@@ -359,10 +392,9 @@ __device__ __forceinline__ float batch_max_nan(const uint4 (&q)[kBatch]) {
   }
 }
 
-// Tokens of a batch above -inf.
+// Smallest logit of a batch (NaN ignored).
 template <int DT>
-__device__ __forceinline__ uint32_t count_finite(const uint4 (&q)[kBatch]) {
-  constexpr int N = Row<DT>::N;
+__device__ __forceinline__ float batch_min(const uint4 (&q)[kBatch]) {
   float low;
   if constexpr (DT == SPEC_BF16) {
     __nv_bfloat162 m = as_bf2(q[0].x);
@@ -379,7 +411,14 @@ __device__ __forceinline__ uint32_t count_finite(const uint4 (&q)[kBatch]) {
       low = fminf(fminf(low, fminf(__uint_as_float(q[b].x), __uint_as_float(q[b].y))),
                   fminf(__uint_as_float(q[b].z), __uint_as_float(q[b].w)));
   }
-  if (low > -INFINITY) return kBatch * N;
+  return low;
+}
+
+// Tokens of a batch above -inf.
+template <int DT>
+__device__ __forceinline__ uint32_t count_finite(const uint4 (&q)[kBatch]) {
+  constexpr int N = Row<DT>::N;
+  if (batch_min<DT>(q) > -INFINITY) return kBatch * N;
   uint32_t n = 0;
 #pragma unroll
   for (int b = 0; b < kBatch; ++b) {
@@ -408,6 +447,7 @@ template <int DT, bool SEG>
 __device__ __noinline__ u64 pass_all(Shared& sh, const Part<DT> part, const Weigher wt) {
   constexpr int N = Row<DT>::N;
   const int n = part.steps();
+  const float least = wt.surely();
   u64 mass = 0;
   uint4 q[kBatch];
   part.load(q, 0);
@@ -417,16 +457,36 @@ __device__ __noinline__ u64 pass_all(Shared& sh, const Part<DT> part, const Weig
     for (int b = 0; b < kBatch; ++b) now[b] = q[b];
     if (it + 1 < n) part.load(q, it + 1);
     u64 s = 0;
+    if (__all_sync(kFull, batch_min<DT>(now) >= least)) {
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      float x[N];
-      unpack<DT>(now[b], x);
+      for (int b = 0; b < kBatch; ++b) {
+        float x[N];
+        unpack<DT>(now[b], x);
 #pragma unroll
-      for (int i = 0; i < N; i += 2) {
-        u64 v0, v1;
-        wt.template pair<DT>(x[i], x[i + 1], v0, v1);
-        s += v0;
-        s += v1;
+        for (int i = 0; i < N; i += 2) {
+          u64 h0, h1;
+          wt.template halves<DT>(x[i], x[i + 1], h0, h1);
+          s += h0;
+          s += h1;
+        }
+      }
+      s = 2 * s + kBatch * N;
+    } else {
+#pragma unroll 1
+      for (int b = 0; b < kBatch; ++b) {
+        float x[N];
+        uint4 w = now[0];
+#pragma unroll
+        for (int i = 1; i < kBatch; ++i)
+          if (b == i) w = now[i];
+        unpack<DT>(w, x);
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+          u64 v0, v1;
+          wt.template pair<DT>(x[i], x[i + 1], v0, v1);
+          s += v0;
+          s += v1;
+        }
       }
     }
     add_segment<SEG>(sh, it, s);
@@ -465,8 +525,15 @@ __device__ __noinline__ u64 pass_guess(Shared& sh, const Part<DT> part, const We
         unpack2(y, y0, y1);
         unpack2(fma2(y, n1, pack2(kMagic, kMagic)), t0, t1);
         s = add2(s, pack2(fast_exp2(-y0), fast_exp2(-y1)));
-        atomicAdd(&sh.bins[Weigher::bin(t0)], 1u);
-        atomicAdd(&sh.bins[Weigher::bin(t1)], 1u);
+        const uint32_t b0 = Weigher::bin(t0), b1 = Weigher::bin(t1);
+        atomicAdd(&sh.bins[b0], 1u);
+        atomicAdd(&sh.bins[b1], 1u);
+        if (b == 0 && i == 0) {
+          // 32 y less the bin, in 1/128, from 0 on: a logit in eight tells where a bin's tokens lie
+          const float r = __fadd_rn(__fsub_rn(t0, kMagic), y0);
+          atomicAdd(&sh.off[b0], (uint32_t)(__float2int_rn(r * 4096.0f) + 64));
+          atomicAdd(&sh.offs[b0], 1u);
+        }
       }
     }
     float s0, s1;
@@ -527,6 +594,7 @@ __device__ __noinline__ void pass_window(Shared& sh, const Part<DT> part, const 
                                          float hi, u64& mass, u64& count, u64& all) {
   constexpr int N = Row<DT>::N;
   const int n = part.steps();
+  const float least = wt.surely();
   mass = all = 0;
   uint32_t c = 0;
   uint4 q[kBatch];
@@ -537,28 +605,40 @@ __device__ __noinline__ void pass_window(Shared& sh, const Part<DT> part, const 
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) now[b] = q[b];
     if (it + 1 < n) part.load(q, it + 1);
-    u64 s = 0;
+    u64 s = 0, z = 0;
+    const bool fast = __all_sync(kFull, batch_min<DT>(now) >= least);
+    uint32_t in = 0;  // of this batch
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
       float x[N];
       unpack<DT>(now[b], x);
       uint32_t win = 0;
 #pragma unroll
-      for (int i = 0; i < N; i += 2) {
-        u64 v0, v1;
-        wt.template pair<DT>(x[i], x[i + 1], v0, v1);
-        all += v0;
-        all += v1;
-        if (x[i] >= hi) {
-          s += v0;
-          ++c;
+      for (int i = 0; i < N; ++i) {
+        in += x[i] >= hi;
+        win |= (uint32_t)(x[i] < hi && x[i] >= lo) << i;
+      }
+      if (fast) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+          u64 h0, h1;
+          wt.template halves<DT>(x[i], x[i + 1], h0, h1);
+          z += h0;
+          z += h1;
+          if (x[i] >= hi) s += h0;
+          if (x[i + 1] >= hi) s += h1;
         }
-        if (x[i + 1] >= hi) {
-          s += v1;
-          ++c;
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < N; ++i) {
+          float one = x[0];
+#pragma unroll
+          for (int q = 1; q < N; ++q)
+            if (q == i) one = x[q];
+          const u64 v = wt.template operator()<DT>(one);
+          z += v;
+          if (one >= hi) s += v;
         }
-        win |= (uint32_t)(x[i] < hi && x[i] >= lo) << i |
-               (uint32_t)(x[i + 1] < hi && x[i + 1] >= lo) << (i + 1);
       }
       if (win) {
         int at = atomicAdd(&sh.n_list, __popc(win));
@@ -571,6 +651,12 @@ __device__ __noinline__ void pass_window(Shared& sh, const Part<DT> part, const 
           }
       }
     }
+    c += in;
+    if (fast) {
+      s = 2 * s + in;
+      z = 2 * z + kBatch * N;
+    }
+    all += z;
     add_segment<true>(sh, it, s);
     mass += s;
   }
@@ -820,6 +906,85 @@ __device__ __noinline__ u64 scan(Shared& sh, u64 v, u64& total) {
 __device__ __forceinline__ float key_value(u64 key) { return order_value((uint32_t)(key >> 32)); }
 __device__ __forceinline__ int key_id(u64 key) { return (int)(0xffffffffu - (uint32_t)key); }
 
+// The k-th token by ten leading bits of order_bits at a time: sh.lo_bits .. sh.hi_bits - 1, of which
+// there are sh.n_window, hold it, behind sh.n_above of larger ones. It ends as soon as they fit the
+// list; equal logits that do not are left. False if fewer than k tokens have a place.
+template <int DT, bool SPLIT>
+__device__ __noinline__ bool find_kth(Team<SPLIT>& team, const Part<DT>& part, uint32_t k) {
+  constexpr int N = Row<DT>::N, kDigit = 1024;
+  static_assert(kDigit <= kBins && kDigit % kThreads == 0, "a digit's bins");
+  Shared& sh = team.sh;
+  const int tid = threadIdx.x, n = part.steps();
+  uint32_t prefix = 0, above = 0;
+  // digits of 10, 10, 10 and 2 bits
+  for (int shift = 22, bits = 10;;) {
+    for (int i = tid; i < kDigit; i += kThreads) sh.bins[i] = 0;
+    __syncthreads();
+    for (int it = 0; it < n; ++it) {
+      uint4 q[kBatch];
+      part.load(q, it);
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        float x[N];
+        unpack<DT>(q[b], x);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const uint32_t u = order_bits(x[i]);
+          if (u && (shift == 22 || u >> (shift + bits) == prefix))
+            atomicAdd(&sh.bins[(u >> shift) & ((1u << bits) - 1)], 1u);
+        }
+      }
+    }
+    team.sync();
+    // thread t has the values kPer t .. kPer t + kPer - 1
+    constexpr int kPer = kDigit / kThreads;
+    uint32_t c[kPer], mine = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      c[i] = 0;
+      if constexpr (SPLIT) {
+        for (int q = 0; q < team.parts; ++q)
+          c[i] += team.cluster.map_shared_rank(&sh, q)->bins[tid * kPer + i];
+      } else {
+        c[i] = sh.bins[tid * kPer + i];
+      }
+      mine += c[i];
+    }
+    u64 total;
+    const u64 before = scan(sh, mine, total);
+    uint32_t larger = above + (uint32_t)(total - before) - mine;  // behind this thread's values
+    if (tid == 0) sh.in = -1;
+    __syncthreads();
+#pragma unroll
+    for (int i = kPer - 1; i >= 0; --i) {
+      if (larger < k && k <= larger + c[i]) {
+        sh.in = (int)c[i];
+        sh.hit = tid * kPer + i;
+        sh.n_above = (int)larger;
+      }
+      larger += c[i];
+    }
+    team.sync();  // every part has been read
+    const int in = sh.in;
+    if (in < 0) return false;
+    above = (uint32_t)sh.n_above;
+    prefix = prefix << bits | (uint32_t)sh.hit;
+    __syncthreads();
+    if (in <= kListMost || shift == 0) {
+      if (tid == 0) {
+        const uint32_t lo = prefix << shift;
+        sh.lo_bits = lo > 0x00800000u ? lo : 0x00800000u;
+        sh.hi_bits = (prefix + 1) << shift;
+        sh.n_window = in;
+      }
+      __syncthreads();
+      return true;
+    }
+    bits = shift < 10 ? shift : 10;
+    shift -= bits;
+  }
+}
+
 // order_bits of about the least logit of bin b.
 __device__ __forceinline__ uint32_t edge_bits(const Weigher& wt, int b) {
   const float x = wt.m - ((float)b + 0.5f) / 32.0f / wt.ch;
@@ -982,25 +1147,39 @@ __device__ __noinline__ int rules(Shared& sh, const Weigher& wt, int n, int nk, 
 }
 
 // Where a share p of the mass of sh.bins (of every part) ends: bins sh.bin_lo .. sh.bin_hi, with
-// the number of tokens before and in them. The bins' masses are their tokens' number times the
-// middle one's, so the place is a guess, to be checked: the bins in which a share of p (1 -+ kSure)
-// ends, or p alone where those do not fit the list. With k it is the bin of the k-th token.
+// the number of tokens before and in them. A bin's mass is its tokens' number times that of their mean
+// (of those that were looked at; `again`: of the bin's middle), so the place is a guess, to be
+// checked: the bins in which a share of p (1 -+ kSure) ends, or p alone where those do not fit the
+// list.
 constexpr float kSure = 0.0005f;
 template <bool SPLIT>
-__device__ __noinline__ void find_window(Team<SPLIT>& team, float p, int k) {
+__device__ __noinline__ void find_window(Team<SPLIT>& team, const Weigher& wt, float p, bool again) {
   Shared& sh = team.sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __syncthreads();
+  for (int at = tid; at < kBins; at += kThreads) {
+    const uint32_t q = again ? 0 : sh.offs[at];
+    const float off = q ? (float)sh.off[at] / (float)q * (1.0f / 128.0f) - 0.5f : 0.0f;
+    sh.weight[at] = at == kBins - 1 ? 0.0f : (float)sh.bins[at] * fast_exp2((at + off) * -0.03125f);
+  }
   // the cluster's bins: each part sums a share of them, then every part reads all shares
   const int share_bins = kBins / team.parts;
   if constexpr (SPLIT) {
     team.sync();
-    for (int i = tid; i < share_bins; i += kThreads) {
-      uint32_t sum = 0;
+    float w[kBins / 2 / kThreads];
 #pragma unroll
-      for (int q = 0; q < kMaxSplit; ++q)
-        if (q < team.parts)
-          sum += team.cluster.map_shared_rank(&sh, q)->bins[team.part * share_bins + i];
-      sh.slice[i] = sum;
+    for (int i = 0; i < kBins / 2 / kThreads; ++i) {
+      const int at = tid + i * kThreads;
+      uint32_t sum = 0;
+      w[i] = 0.0f;
+      if (at >= share_bins) continue;
+      for (int q = 0; q < team.parts; ++q) {
+        const Shared* o = team.cluster.map_shared_rank(&sh, q);
+        sum += o->bins[team.part * share_bins + at];
+        w[i] += o->weight[team.part * share_bins + at];
+      }
+      sh.slice[at] = sum;
+      sh.shares[at] = w[i];
     }
   }
   team.sync();
@@ -1009,12 +1188,15 @@ __device__ __noinline__ void find_window(Team<SPLIT>& team, float p, int k) {
 #pragma unroll
   for (int i = 0; i < kBinsThread; ++i) {
     const int at = tid * kBinsThread + i;
-    if constexpr (SPLIT)
-      n[i] = team.cluster.map_shared_rank(&sh, at / share_bins)->slice[at % share_bins];
-    else
+    if constexpr (SPLIT) {
+      const Shared* o = team.cluster.map_shared_rank(&sh, at / share_bins);
+      n[i] = o->slice[at % share_bins];
+      e[i] = o->shares[at % share_bins];
+    } else {
       n[i] = sh.bins[at];
+      e[i] = sh.weight[at];
+    }
     if (at == kBins - 1) n[i] = 0;  // no mass
-    e[i] = (float)n[i] * (k ? 1.0f : fast_exp2(at * -0.03125f));
     mine += e[i];
     count += n[i];
   }
@@ -1049,8 +1231,7 @@ __device__ __noinline__ void find_window(Team<SPLIT>& team, float p, int k) {
     total += sh.fred[w];
   }
   // thread ranges follow one another, so the three places are each in one thread's
-  float share[3] = {total * p * (1.0f - kSure), total * p, total * p * (1.0f + kSure)};
-  if (k) share[0] = share[1] = share[2] = (float)k;  // whole numbers below 2^24
+  const float share[3] = {total * p * (1.0f - kSure), total * p, total * p * (1.0f + kSure)};
 #pragma unroll
   for (int i = 0; i < kBinsThread; ++i) {
     const float next = c + e[i];
@@ -1080,8 +1261,8 @@ __device__ __noinline__ void find_window(Team<SPLIT>& team, float p, int k) {
       sh.n_above = sh.before[1];
       sh.n_window = sh.in;
     }
-    sh.bin_lo = lo;
-    sh.bin_hi = hi;
+    sh.lo_bits = edge_bits(wt, hi);
+    sh.hi_bits = lo ? edge_bits(wt, lo - 1) : 0xff800000u;  // infinity: nothing is above
   }
   team.sync();
 }
@@ -1412,7 +1593,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
     wt.ch = sh.ch;
     wt.cl = sh.cl;
     const float scale = sh.scale;
-    const int k = sh.k;
+    int k = sh.k;
     const bool by_p = sh.p < 1.0f;
     uint32_t tm = 1;
     if (sh.by_m) {  // the least fp32 number x with (x - m) / T >= log(min_p)
@@ -1460,21 +1641,30 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
         }
       }
       while (true) {
-        if (binned) {
-          for (int i = tid; i < kBins; i += kThreads) sh.bins[i] = 0;
+        if (k && binned && !find_kth<DT, SPLIT>(team, part, (uint32_t)k)) {
+          k = 0;  // every token of the row
+          binned = by_p;
+          list = by_m;
+          bound = tm;
+          if (!by_p && !by_m) break;
+        }
+        if (k && binned) {
+          list = sh.n_above + sh.n_window <= kListMost;
+          window = !list && sh.n_window <= kListMost;
+          bound = sh.lo_bits;
+        } else if (binned) {
+          for (int i = tid; i < kBins; i += kThreads) sh.bins[i] = sh.off[i] = sh.offs[i] = 0;
           __syncthreads();
           const u64 mass = team.sum(pass_guess<DT>(sh, part, wt), 0).a;
-          find_window<SPLIT>(team, sh.p, k);
+          find_window<SPLIT>(team, wt, sh.p, false);
+          all = mass << (S + 1 - 40);
+          slack = (u64)((float)all * kSlack);
           list = sh.n_above + sh.n_window <= kListMost;
-          window = sh.bin_lo > 0 && sh.n_window <= kListMost;
-          bound = edge_bits(wt, sh.bin_hi);
-          if (!k) {
-            all = mass << (S + 1 - 40);
-            slack = (u64)((float)all * kSlack);
-            // min-p's last token is enough, and may be before where the nucleus seems to end
-            if (tm > bound || !list) bound = tm;
-            if (!list) list = by_m && (sh.bin_lo == 0 || tm > edge_bits(wt, sh.bin_lo - 1));
-          }
+          window = !list && sh.n_window <= kListMost;
+          bound = sh.lo_bits;
+          // min-p's last token is enough, and may be before where the nucleus seems to end
+          if (tm > bound || !list) bound = tm;
+          if (!list) list = by_m && tm >= sh.hi_bits;
         }
         if (list) {
           const int n = collect<DT, SPLIT>(team, part, per_group, bound);
@@ -1510,7 +1700,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
       for (int turn = 0; !kept && window && turn < 3; ++turn) {
         // too many for the list: its piece around the border, the mass before it
         if (tid == 0) sh.n_list = 0;
-        const uint32_t lo_bits = edge_bits(wt, sh.bin_hi), hi_bits = edge_bits(wt, sh.bin_lo - 1);
+        const uint32_t lo_bits = sh.lo_bits, hi_bits = sh.hi_bits;
         __syncthreads();
         u64 mm, cc, zz;
         pass_window<DT>(sh, part, wt, order_value(lo_bits), order_value(hi_bits), mm, cc, zz);
@@ -1567,8 +1757,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
             if (window) {
               const float off = (float)((double)s.a / (double)all) - sh.guess;
               __syncthreads();
-              find_window<SPLIT>(team, sh.p - off, 0);
-              window = sh.bin_lo > 0 && sh.n_window <= kListMost;
+              find_window<SPLIT>(team, wt, sh.p - off, true);
+              window = sh.n_window <= kListMost;
             } else {
               team.sync();
             }
