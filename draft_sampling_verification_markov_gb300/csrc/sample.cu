@@ -610,14 +610,8 @@ __device__ __noinline__ void pass_window(Shared& sh, const Part<DT> part, const 
     uint32_t in = 0;  // of this batch
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      float x[N];
+      float x[N], below = -INFINITY;  // the largest logit below hi
       unpack<DT>(now[b], x);
-      uint32_t win = 0;
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        in += x[i] >= hi;
-        win |= (uint32_t)(x[i] < hi && x[i] >= lo) << i;
-      }
       if (fast) {
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
@@ -625,8 +619,16 @@ __device__ __noinline__ void pass_window(Shared& sh, const Part<DT> part, const 
           wt.template halves<DT>(x[i], x[i + 1], h0, h1);
           z += h0;
           z += h1;
-          if (x[i] >= hi) s += h0;
-          if (x[i + 1] >= hi) s += h1;
+          const bool in0 = x[i] >= hi, in1 = x[i + 1] >= hi;
+          if (in0) {
+            s += h0;
+            ++in;
+          }
+          if (in1) {
+            s += h1;
+            ++in;
+          }
+          below = max3f(below, in0 ? -INFINITY : x[i], in1 ? -INFINITY : x[i + 1]);
         }
       } else {
 #pragma unroll 1
@@ -637,10 +639,18 @@ __device__ __noinline__ void pass_window(Shared& sh, const Part<DT> part, const 
             if (q == i) one = x[q];
           const u64 v = wt.template operator()<DT>(one);
           z += v;
-          if (one >= hi) s += v;
+          if (one >= hi) {
+            s += v;
+            ++in;
+          } else {
+            below = fmaxf(below, one);
+          }
         }
       }
-      if (win) {
+      if (below >= lo) {
+        uint32_t win = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) win |= (uint32_t)(x[i] < hi && x[i] >= lo) << i;
         int at = atomicAdd(&sh.n_list, __popc(win));
 #pragma unroll
         for (int i = 0; i < N; ++i)
@@ -785,55 +795,47 @@ __device__ __noinline__ int collect(Team<SPLIT>& team, const Part<DT>& part, int
   constexpr int N = Row<DT>::N;
   constexpr int kAtOnce = 4;  // pieces in flight
   Shared& sh = team.sh;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x;
   if (tid == 0) sh.n_list = sh.n_hits = 0;
   __syncthreads();
   const int n = part.steps(), groups = (n + per_group - 1) / per_group;
-  for (int g = 0; g < groups; ++g) {
-    const bool hit = sh.index[g * kThreads + tid] >= bound;
-    const uint32_t all = __ballot_sync(kFull, hit);
-    if (!all) continue;
-    int at = 0;
-    if (lane == 0) at = atomicAdd(&sh.n_hits, __popc(all));
-    at = __shfl_sync(kFull, at, 0) + __popc(all & ((1u << lane) - 1));
-    if (hit && at < kHits) sh.hits[at] = (uint16_t)(g * kThreads + tid);
-  }
+  // few reach it: a counter update each
+#pragma unroll 4
+  for (int g = 0; g < groups; ++g)
+    if (sh.index[g * kThreads + tid] >= bound) {
+      const int at = atomicAdd(&sh.n_hits, 1);
+      if (at < kHits) sh.hits[at] = (uint16_t)(g * kThreads + tid);
+    }
   __syncthreads();
   const int hits = sh.n_hits;
   if (hits <= kHits) {
     const float least = order_value(bound > 0x00800000u ? bound : 0x00800000u);
     const int pieces = hits * per_group * kBatch;
-    for (int base = warp * 32; base < pieces; base += kThreads * kAtOnce) {
+    for (int base = tid; base < pieces; base += kThreads * kAtOnce) {
       uint4 q[kAtOnce];
       int j[kAtOnce];
 #pragma unroll
       for (int i = 0; i < kAtOnce; ++i) {
-        const int at = base + i * kThreads + lane, batch = at / kBatch;
-        j[i] = part.j1;
-        if (at < pieces) {
-          const int entry = sh.hits[batch / per_group], t = entry % kThreads;
-          const int it = entry / kThreads * per_group + batch % per_group;
-          j[i] = part.j0 + it * kStep + (t >> 5) * kWarpStep + (t & 31) + at % kBatch * 32;
-        }
+        const int at = base + i * kThreads;
+        if (i && at >= pieces) break;
+        const int batch = at / kBatch, entry = sh.hits[per_group == 1 ? batch : batch / per_group];
+        const int t = entry % kThreads;
+        const int it = per_group == 1 ? entry / kThreads
+                                      : entry / kThreads * per_group + batch % per_group;
+        j[i] = part.j0 + it * kStep + (t >> 5) * kWarpStep + (t & 31) + at % kBatch * 32;
         q[i] = part.row.load(j[i], part.j1);
       }
 #pragma unroll
       for (int i = 0; i < kAtOnce; ++i) {
+        if (i && base + i * kThreads >= pieces) break;
         if (part.row.partial(j[i], part.j1)) q[i] = part.row.load_partial(j[i]);
         float x[N];
         unpack<DT>(q[i], x);
         uint32_t in = 0;
 #pragma unroll
         for (int e = 0; e < N; ++e) in |= (uint32_t)(x[e] >= least) << e;
-        int up = __popc(in);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(kFull, up, o);
-          if (lane >= o) up += y;
-        }
-        int at = 0;
-        if (lane == 31 && up) at = atomicAdd(&sh.n_list, up);
-        at = __shfl_sync(kFull, at, 31) + up - __popc(in);
+        if (!in) continue;
+        int at = atomicAdd(&sh.n_list, __popc(in));
 #pragma unroll
         for (int e = 0; e < N; ++e)
           if (in >> e & 1) {
@@ -1077,17 +1079,17 @@ __device__ __noinline__ u64 list_mass(Shared& sh, const Weigher& wt, int n, u64 
 // of sh.total mass, stay, those from sh.limit on. `all` is the mass that p refers to where that is
 // not the nk tokens' own (0), to within `slack`; the list may begin behind a mass of `above`. kNo if
 // the nucleus ends before or behind the list, which holds every token of bits >= bound (and before
-// that, unless `above`), kUnsure if the slack decides where. Up to kThreads keys are left in
-// descending order.
+// that, unless `above`), kUnsure if the slack decides where. No key is above last_key. Up to kThreads keys
+// are left in descending order.
 enum : int { kNo = 0, kYes = 1, kUnsure = 2 };
 template <int DT>
 __device__ __noinline__ int rules(Shared& sh, const Weigher& wt, int n, int nk, u64 all, u64 slack,
-                                  u64 above, uint32_t bound, u64 top_key) {
+                                  u64 above, uint32_t bound, u64 last_key) {
   const bool by_p = sh.p < 1.0f;
   const int tid = threadIdx.x;
   if (n > kThreads) {
     const u64 lo = (u64)bound << 32;
-    u64 limit = nk < n ? pick<DT>(sh, wt, n, 0, (u64)nk, false, lo, top_key) : 0;
+    u64 limit = nk < n ? pick<DT>(sh, wt, n, 0, (u64)nk, false, lo, last_key) : 0;
     int kept;
     u64 mass = list_mass<DT>(sh, wt, n, limit, kept);
     const u64 key_m = sh.tm > 1 ? (u64)sh.tm << 32 : 0;
@@ -1099,7 +1101,7 @@ __device__ __noinline__ int rules(Shared& sh, const Weigher& wt, int n, int nk, 
       most -= above;
       if (mass < most && all && sh.tm < bound) return kNo;
       if (need && need <= mass) {
-        const u64 key = pick<DT>(sh, wt, n, limit, need, true, lo, top_key);
+        const u64 key = pick<DT>(sh, wt, n, limit, need, true, lo, last_key);
         limit = key;
         mass = list_mass<DT>(sh, wt, n, limit, kept);
         // this token also ends the nucleus of a larger need
@@ -1284,8 +1286,7 @@ __device__ __forceinline__ void write_draw(const SampleArgs& a, int row, int id,
   if (a.kept) a.kept[row] = kept;
 }
 
-__device__ __forceinline__ u64 draw_at(const SampleArgs& a, int row, u64 total) {
-  float u = a.u[row];
+__device__ __forceinline__ u64 draw_at(const SampleArgs& a, float u, u64 total) {
   if (!(u >= 0.0f && u < 1.0f)) {
     atomicOr(a.status, SPEC_DEV_BAD_PARAM);
     if (u >= 1.0f) return total - 1;
@@ -1296,8 +1297,8 @@ __device__ __forceinline__ u64 draw_at(const SampleArgs& a, int row, u64 total) 
 
 // The draw among the listed keys from sh.limit on: by 256 ranges of ids, then within one.
 template <int DT>
-__device__ __noinline__ void draw_list(Shared& sh, const SampleArgs& a, int row, const Weigher& wt,
-                                       float scale, int listed) {
+__device__ __noinline__ void draw_list(Shared& sh, const SampleArgs& a, int row, float u,
+                                       const Weigher& wt, float scale, int listed) {
   u64* bucket = sh.bucket;
   const int tid = threadIdx.x;
   if (listed <= kThreads) {  // every token that stays against every other
@@ -1310,7 +1311,7 @@ __device__ __noinline__ void draw_list(Shared& sh, const SampleArgs& a, int row,
 #pragma unroll 4
     for (int i = 0; i < n; ++i)
       if ((uint32_t)sh.keys[i] > (uint32_t)key) below += bucket[i];  // lower ids
-    const u64 at = draw_at(a, row, sh.total);
+    const u64 at = draw_at(a, u, sh.total);
     if (tid < n && below <= at && at < below + w)
       write_draw(a, row, key_id(key), key_value(key), wt, scale, sh.total, n);
     return;
@@ -1327,7 +1328,7 @@ __device__ __noinline__ void draw_list(Shared& sh, const SampleArgs& a, int row,
     if (w) atomicAdd(&bucket[key_id(key) >> by], w);
   }
   __syncthreads();
-  const u64 at = draw_at(a, row, sh.total), mine = bucket[tid];
+  const u64 at = draw_at(a, u, sh.total), mine = bucket[tid];
   u64 t;
   const u64 before = scan(sh, mine, t);
   if (before <= at && at < before + mine) {
@@ -1383,10 +1384,22 @@ __device__ __noinline__ void draw_segment(Shared& sh, const SampleArgs& a, int r
   const int base = part.j0 + sh.hit * kWarpStep;
   u64 rest = sh.rest;
   const Cut cut(key);
+  uint4 q[kBatch];
+#pragma unroll
+  for (int b = 0; b < kBatch; ++b) q[b] = part.row.load(base + b * 32 + lane, part.j1);
+#pragma unroll
+  for (int b = 0; b < kBatch; ++b)
+    if (part.row.partial(base + b * 32 + lane, part.j1))
+      q[b] = part.row.load_partial(base + b * 32 + lane);
+#pragma unroll 1
   for (int b = 0; b < kBatch; ++b) {
     const int j = base + b * 32 + lane;
     float x[N];
-    unpack<DT>(part.row.load_any(j, part.j1), x);
+    uint4 now = q[0];
+#pragma unroll
+    for (int i = 1; i < kBatch; ++i)
+      if (i == b) now = q[i];
+    unpack<DT>(now, x);
     const int v = j * N - part.row.head;
     u64 w[N], s = 0;
 #pragma unroll
@@ -1518,6 +1531,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
 
   const int row = SPLIT ? blockIdx.x / parts : blockIdx.x;
   if (row >= rows) return;
+  const float u = WRITE ? 0.0f : a.u[row];  // on its way while the logits are read
   {
     Part<DT> part{Row<DT>(a.x, (size_t)row * a.ld, a.V), 0, 0};
     {
@@ -1690,7 +1704,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
               total = lead->total;
               kept = lead->kept;
               if (SPLIT) team.sync();
-              if (!WRITE && team.part == 0) draw_list<DT>(sh, a, row, wt, scale, n);
+              if (!WRITE && team.part == 0) draw_list<DT>(sh, a, row, u, wt, scale, n);
             }
           }
         }
@@ -1701,6 +1715,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
         // too many for the list: its piece around the border, the mass before it
         if (tid == 0) sh.n_list = 0;
         const uint32_t lo_bits = sh.lo_bits, hi_bits = sh.hi_bits;
+        const u64 last_key = ((u64)hi_bits << 32) - 1;
         __syncthreads();
         u64 mm, cc, zz;
         pass_window<DT>(sh, part, wt, order_value(lo_bits), order_value(hi_bits), mm, cc, zz);
@@ -1714,10 +1729,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
             // a truncation that min-p cuts shorter is not decided here, nor top-p of this top-k
             bool ok = false;
             if (k && by_p) {
-              const u64 key = pick<DT>(sh, wt, n, 0, (u64)nk, false, (u64)lo_bits << 32, top_key);
+              const u64 key = pick<DT>(sh, wt, n, 0, (u64)nk, false, (u64)lo_bits << 32, last_key);
               if (tid == 0) sh.limit = key;
             } else {
-              ok = rules<DT>(sh, wt, n, nk, all, 0, s.a, lo_bits, top_key) &&
+              ok = rules<DT>(sh, wt, n, nk, all, 0, s.a, lo_bits, last_key) &&
                    (uint32_t)(sh.limit >> 32) >= tm;
             }
             if (tid == 0) sh.done = ok;
@@ -1746,7 +1761,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
               for (int i = tid; i < steps * kWarps; i += kThreads) own += sh.seg[i];
             const auto d = team.sum(own, 0);
             if (!WRITE) {
-              const u64 at = draw_at(a, row, total);
+              const u64 at = draw_at(a, u, total);
               if (d.before <= at && at < d.before + d.own)
                 draw_segment<DT>(sh, a, row, part, wt, scale, limit, at - d.before, total, kept);
             }
@@ -1800,7 +1815,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
       total = s.a;
       kept = (int)s.b;
       if (!WRITE) {
-        const u64 at = draw_at(a, row, total);
+        const u64 at = draw_at(a, u, total);
         if (s.before <= at && at < s.before + s.own)
           draw_segment<DT>(sh, a, row, part, wt, scale, limit, at - s.before, total, kept);
       }
