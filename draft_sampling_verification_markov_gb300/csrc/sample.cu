@@ -1010,7 +1010,14 @@ __device__ __noinline__ u64 pick(Shared& sh, const Weigher& wt, int n, u64 limit
       const u64 key = base + tid < n ? sh.keys[base + tid] : 0;
       const bool in = key >= from && key <= hi && key;
       const u64 w = by_mass ? wt.template operator()<DT>(in ? key_value(key) : -INFINITY) : 1;
-      if (in && w) atomicAdd(&bucket[(key - lo) >> shift], w);
+      if (in && w) {
+        // equal logits have equal masses and one range, until the ids are told apart: one addition
+        // for all of a warp's (the few hundred tokens of a bf16 logit met on one counter otherwise)
+        const uint32_t same = shift >= 32 ? __match_any_sync(__activemask(), (uint32_t)(key >> 32))
+                                          : 1u << (tid & 31);
+        if ((tid & 31) == __ffs(same) - 1)
+          atomicAdd(&bucket[(key - lo) >> shift], w * (u64)__popc(same));
+      }
     }
     __syncthreads();
     const u64 v = bucket[tid];
