@@ -1179,7 +1179,7 @@ int spec_w4_logits(const void* x, long long ldx, const void* residual, long long
   const W4Args a{x,     ldx,         residual, ldr,   dtype, norm_weight,  nw_dtype,
                  eps,   M,           N,        K,     codes, scales,       scale_dtype,
                  zeros, group,       residual_out, ldh, out, out_dtype,    ld_out,
-                 static_cast<uint32_t*>(ws), parts, 0, 0, 0, 0};
+                 static_cast<uint32_t*>(ws), parts, 0, 0, 0, 0, 0};
   const cudaError_t e = launch_w4_logits(a, static_cast<cudaStream_t>(stream));
   const int rc = finish();
   return e == cudaSuccess ? rc : SPEC_ERR_CUDA;

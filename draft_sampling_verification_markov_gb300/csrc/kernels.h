@@ -208,8 +208,9 @@ struct W4Args {
   long long ldo;
   uint32_t* status;
   int parts;  // columns of a row
-  // set by the launcher: rows of a chunk, chunks, warps that share a matrix row, tiles of a ring
-  int chunk_rows, chunks, k_warps, stages;
+  // set by the launcher: rows of a chunk, chunks, warps that share a matrix row, tiles of a ring;
+  // whether the first warp's first tile is never asked for (a test of the bounded waits)
+  int chunk_rows, chunks, k_warps, stages, stall;
 };
 // Whether a row of K in `parts` columns fits the kernel's shared memory.
 bool w4_fits(int parts, int K);

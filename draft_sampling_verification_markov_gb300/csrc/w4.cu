@@ -186,6 +186,7 @@ cudaError_t launch_w4_logits(W4Args a, cudaStream_t s) {
       }
     }
   }
+  a.stall = take_stall_request();
   CUtensorMap codes;
   if (!tc::encode_fn()) return cudaErrorNotSupported;
   const cuuint64_t dims[2] = {(cuuint64_t)padded(a.K) / 2, (cuuint64_t)a.N}, stride = dims[0];

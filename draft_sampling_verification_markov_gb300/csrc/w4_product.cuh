@@ -390,7 +390,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tiles = mine * my_nk, x_end = (wk * nk + my_nk) * kRow;
   int px = wk * nk * kRow, py = first * 16 * R, issued = 0;
   auto issue = [&](int stage) {
-    if (issued < tiles && lane == 0) {
+    const bool skip = a.stall && blockIdx.x == 0 && warp == 0 && issued == 0;
+    if (issued < tiles && lane == 0 && !skip) {
       tc::mbar_arrive_expect_tx(&full[stage], kTile);
       tc::tma_load_2d(ring + stage * kTile, &codes, px, py, &full[stage], policy);
     }

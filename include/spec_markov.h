@@ -686,9 +686,9 @@ int spec_verify_greedy_noalloc(const void* target, int t_dtype, const int32_t* d
  * TEST-ONLY: never call this outside a test of the timeout path; the next tensor-core pass it
  * stalls produces no result.
  * Test support for the bounded waits (no counterpart on the pages). The next tensor-core
- * Markov pass or spec_mx_logits product launched by this process never receives its first W2 (or
- * vocabulary) tile, so its MMA thread's wait expires (after about 2 s of SM clock; the product's
- * drain of its copies takes as long again): the kernel sets SPEC_DEV_TIMEOUT in the device
+ * Markov pass, spec_mx_logits or spec_w4_logits product launched by this process never receives its
+ * first W2 (or vocabulary) tile, so the wait for it expires (after about 2 s of SM clock; a
+ * product's drain of its copies takes as long again): the kernel sets SPEC_DEV_TIMEOUT in the device
  * status word, abandons its work (its partials, and the outputs built from them, are
  * invalid), drains its copies, frees its tensor memory and returns; the CUDA context stays
  * usable. Nothing faults or hangs.

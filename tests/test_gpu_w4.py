@@ -1,4 +1,6 @@
 """Grouped 4-bit weights on the GPU against 64 bits: packing, reading back, products."""
+import time
+
 import pytest
 import torch
 
@@ -241,6 +243,24 @@ def test_graph_and_streams():
         static.copy_(randn((4, 512), seed, BF))
         g.replay()
         assert torch.equal(out, S.spec_w4_logits(static, w))
+
+
+def test_expired_wait_reports_timeout():
+    w, _ = packed(3000, 1024, 128, BF, 31)
+    x = randn((3, 1024), 32, BF).to(DEV)
+    ws = S.Workspace(256, device=DEV)
+    want = S.spec_w4_logits(x, w, workspace=ws).clone()
+    torch.cuda.synchronize()
+    assert ws.status() == 0
+    assert S.lib().spec_test_stall_next_markov() == 0
+    t0 = time.time()
+    S.spec_w4_logits(x, w, workspace=ws)
+    torch.cuda.synchronize()
+    assert ws.status() & S.SPEC_DEV_TIMEOUT
+    assert 0.5 < time.time() - t0 < 30.0
+    assert torch.equal(S.spec_w4_logits(x, w, workspace=ws), want)
+    torch.cuda.synchronize()
+    assert ws.status() == 0
 
 
 def test_matrix_beyond_2_31_elements():
