@@ -98,7 +98,7 @@ struct Shared {
   // decided by one thread or CTA for the others
   u64 limit, total, rest;
   int kept, done, hit;
-  int edge[3], before[3], in;
+  int edge[4], before[4], in;
   float cum[2];
   float guess;               // the share of the mass before bin_lo, as the bins have it
   uint32_t lo_bits, hi_bits;
@@ -1086,8 +1086,8 @@ __device__ __noinline__ u64 list_mass(Shared& sh, const Weigher& wt, int n, u64 
 // of sh.total mass, stay, those from sh.limit on. `all` is the mass that p refers to where that is
 // not the nk tokens' own (0), to within `slack`; the list may begin behind a mass of `above`. kNo if
 // the nucleus ends before or behind the list, which holds every token of bits >= bound (and before
-// that, unless `above`), kUnsure if the slack decides where. No key is above last_key. Up to kThreads keys
-// are left in descending order.
+// that, unless `above`), kUnsure if the slack decides where, or if min-p leaves none of the list. No
+// key is above last_key. Up to kThreads keys are left in descending order.
 enum : int { kNo = 0, kYes = 1, kUnsure = 2 };
 template <int DT>
 __device__ __noinline__ int rules(Shared& sh, const Weigher& wt, int n, int nk, u64 all, u64 slack,
@@ -1125,7 +1125,7 @@ __device__ __noinline__ int rules(Shared& sh, const Weigher& wt, int n, int nk, 
       sh.limit = limit;
     }
     __syncthreads();
-    return kept > 0 ? kYes : kNo;
+    return kept > 0 ? kYes : above ? kUnsure : kNo;
   }
   sort_keys(sh, n);
   const u64 key = tid < n ? sh.keys[tid] : 0;
@@ -1159,8 +1159,10 @@ __device__ __noinline__ int rules(Shared& sh, const Weigher& wt, int n, int nk, 
 // the number of tokens before and in them. A bin's mass is its tokens' number times that of their mean
 // (of those that were looked at; `again`: of the bin's middle), so the place is a guess, to be
 // checked: the bins in which a share of p (1 -+ kSure) ends, or p alone where those do not fit the
-// list.
+// list. A token alone in its bin, which was not looked at, is off by up to 2^(1/64), so that a peaked
+// row's place may be a token further: the window has at least kAtLeast tokens, larger ones included.
 constexpr float kSure = 0.0005f;
+constexpr uint32_t kAtLeast = 64;
 template <bool SPLIT>
 __device__ __noinline__ void find_window(Team<SPLIT>& team, const Weigher& wt, float p, bool again) {
   Shared& sh = team.sh;
@@ -1224,7 +1226,7 @@ __device__ __noinline__ void find_window(Team<SPLIT>& team, const Weigher& wt, f
     sh.fred[warp] = up;
     sh.red[0][warp] = cup;
   }
-  if (tid < 3) {
+  if (tid < 4) {
     sh.edge[tid] = kBins - 1;
     sh.before[tid] = 0;
   }
@@ -1252,6 +1254,10 @@ __device__ __noinline__ void find_window(Team<SPLIT>& team, const Weigher& wt, f
         if (q < 2) sh.cum[q] = c / total;
         if (q == 1) sh.in = (int)n[i];
       }
+    if (before < kAtLeast && before + n[i] >= kAtLeast) {
+      sh.edge[3] = tid * kBinsThread + i;
+      sh.before[3] = (int)(before + n[i]);
+    }
     c = next;
     before += n[i];
   }
@@ -1264,6 +1270,10 @@ __device__ __noinline__ void find_window(Team<SPLIT>& team, const Weigher& wt, f
     sh.guess = sh.cum[0];
     sh.n_above = sh.before[0];
     sh.n_window = sh.before[2] - sh.before[0];
+    if (hi < sh.edge[3] && sh.edge[3] < kBins - 1 && sh.before[3] <= kThreads) {
+      hi = sh.edge[3];
+      sh.n_window = sh.before[3] - sh.before[0];
+    }
     if (sh.n_window > kListMost && sh.edge[1] < kBins - 1) {
       lo = hi = sh.edge[1];
       sh.guess = sh.cum[1];
@@ -1714,10 +1724,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
               if (!WRITE && team.part == 0) draw_list<DT>(sh, a, row, u, wt, scale, n);
             }
           }
+          // the guess was wrong: again with the mass that there is
+          window = !kept && !k && binned && by_p && n <= kList && sh.n_window <= kListMost;
         }
         if (kept || !k || binned) break;
         binned = true;  // too many tokens of the k-th logit, or near it
       }
+      bool of_k = false;  // whether `all` is the mass of top-k's tokens, those from `limit` on
       for (int turn = 0; !kept && window && turn < 3; ++turn) {
         // too many for the list: its piece around the border, the mass before it
         if (tid == 0) sh.n_list = 0;
@@ -1727,72 +1740,87 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
         u64 mm, cc, zz;
         pass_window<DT>(sh, part, wt, order_value(lo_bits), order_value(hi_bits), mm, cc, zz);
         const auto s = team.sum(mm, cc);
-        if (!k && (slack || turn == 0)) all = team.sum(zz, 0).a;
+        const u64 whole = team.sum(zz, 0).a;
+        if (!k && !of_k) all = whole;
         slack = 0;
         const int n = gather<SPLIT>(team), nk = k ? k - (int)s.b : n;
         window = n <= kList && nk > 0 && nk <= n;
-        if (window) {
-          if (team.part == 0) {
-            // a truncation that min-p cuts shorter is not decided here, nor top-p of this top-k
-            bool ok = false;
-            if (k && by_p) {
-              const u64 key = pick<DT>(sh, wt, n, 0, (u64)nk, false, (u64)lo_bits << 32, last_key);
-              if (tid == 0) sh.limit = key;
-            } else {
-              ok = rules<DT>(sh, wt, n, nk, all, 0, s.a, lo_bits, last_key) &&
-                   (uint32_t)(sh.limit >> 32) >= tm;
-            }
-            if (tid == 0) sh.done = ok;
-            // what stays of the list, into the segments
-            if (ok && !WRITE)
-              for (int base = 0; base < n; base += kThreads) {
-                const u64 key = base + tid < n ? sh.keys[base + tid] : 0;
-                const bool in = key && key >= sh.limit;
-                const u64 w = wt.template operator()<DT>(in ? key_value(key) : -INFINITY);
-                if (!in) continue;
-                const int j = (key_id(key) + part.row.head) / Row<DT>::N;
-                const int per = part.j1 - part.j0, q = SPLIT ? j / per : 0;
-                Shared* to = &sh;
-                if constexpr (SPLIT) to = team.cluster.map_shared_rank(&sh, q);
-                atomicAdd(&to->seg[(j - q * per) / kWarpStep], w);
-              }
-          }
-          team.sync();
-          const Shared* lead = team.leader();
-          if (lead->done) {
-            limit = lead->limit;
-            total = s.a + lead->total;
-            kept = (int)s.b + lead->kept;
-            u64 own = 0;
-            if (!WRITE)
-              for (int i = tid; i < steps * kWarps; i += kThreads) own += sh.seg[i];
-            const auto d = team.sum(own, 0);
-            if (!WRITE) {
-              const u64 at = draw_at(a, u, total);
-              if (d.before <= at && at < d.before + d.own)
-                draw_segment<DT>(sh, a, row, part, wt, scale, limit, at - d.before, total, kept);
-            }
+        if (!window) break;
+        if (team.part == 0) {
+          int is = kNo;
+          if (k && by_p) {  // the mass that p refers to comes first
+            const u64 key = pick<DT>(sh, wt, n, 0, (u64)nk, false, (u64)lo_bits << 32, last_key);
+            if (tid == 0) sh.limit = key;
           } else {
-            if (k && by_p) limit = lead->limit;
-            // once more by the mass that there is before the window
-            window = !k;
-            if (window) {
-              const float off = (float)((double)s.a / (double)all) - sh.guess;
-              __syncthreads();
-              find_window<SPLIT>(team, wt, sh.p - off, true);
-              window = sh.n_window <= kListMost;
-            } else {
-              team.sync();
-            }
+            is = rules<DT>(sh, wt, n, nk, all, 0, s.a, lo_bits, last_key);
+            // min-p ends before the window, the other two do not
+            if (is == kYes && (uint32_t)(sh.limit >> 32) < tm) is = kUnsure;
           }
+          if (tid == 0) sh.done = is;
+          // what stays of the list, into the segments
+          if (is == kYes && !WRITE)
+            for (int base = 0; base < n; base += kThreads) {
+              const u64 key = base + tid < n ? sh.keys[base + tid] : 0;
+              const bool in = key && key >= sh.limit;
+              const u64 w = wt.template operator()<DT>(in ? key_value(key) : -INFINITY);
+              if (!in) continue;
+              const int j = (key_id(key) + part.row.head) / Row<DT>::N;
+              const int per = part.j1 - part.j0, q = SPLIT ? j / per : 0;
+              Shared* to = &sh;
+              if constexpr (SPLIT) to = team.cluster.map_shared_rank(&sh, q);
+              atomicAdd(&to->seg[(j - q * per) / kWarpStep], w);
+            }
+        }
+        team.sync();
+        const Shared* lead = team.leader();
+        const int done = lead->done;
+        if (done == kYes) {
+          limit = lead->limit;
+          total = s.a + lead->total;
+          kept = (int)s.b + lead->kept;
+          u64 own = 0;
+          if (!WRITE)
+            for (int i = tid; i < steps * kWarps; i += kThreads) own += sh.seg[i];
+          const auto d = team.sum(own, 0);
+          if (!WRITE) {
+            const u64 at = draw_at(a, u, total);
+            if (d.before <= at && at < d.before + d.own)
+              draw_segment<DT>(sh, a, row, part, wt, scale, limit, at - d.before, total, kept);
+          }
+        } else if (done == kUnsure) {
+          limit = (u64)tm << 32;
+          break;
+        } else if (k && by_p) {
+          // the mass of top-k's tokens; its share ends where one of the row's mass does
+          limit = lead->limit;
+          pass<DT, true, false>(sh, part, wt, limit, mm, cc);
+          all = team.sum(mm, cc).a;
+          for (int i = tid; i < kBins; i += kThreads) sh.bins[i] = sh.off[i] = sh.offs[i] = 0;
+          __syncthreads();
+          pass_guess<DT>(sh, part, wt);
+          find_window<SPLIT>(team, wt, sh.p * (float)((double)all / (double)whole), false);
+          window = sh.n_window <= kListMost;
+          of_k = true;
+          turn = -1;
+          k = 0;
+        } else if (k) {
+          window = false;
+          team.sync();
+        } else {
+          // once more by the mass that there is before the window
+          const float off = (float)((double)s.a / (double)whole) - sh.guess;
+          const float share = of_k ? sh.p * (float)((double)all / (double)whole) : sh.p;
+          __syncthreads();
+          find_window<SPLIT>(team, wt, share - off, true);
+          window = sh.n_window <= kListMost;
         }
       }
-      if (!kept) {
-        const u64 key_m = (u64)tm << 32;
+      const u64 key_m = (u64)tm << 32;
+      if (!kept && !(by_m && limit == key_m)) {
         if (k && !limit) limit = search<DT, SPLIT, false>(team, part, wt, 0, (u64)k, top_key);
         if (by_p) {
           if (!k && slack) all = team.sum(pass_all<DT, false>(sh, part, wt), 0).a;
-          if (k) {
+          if (limit && !of_k) {
             u64 mm, cc;
             pass<DT, true, false>(sh, part, wt, limit, mm, cc);
             all = team.sum(mm, cc).a;
