@@ -12,40 +12,64 @@ constexpr int kPackThreads = 256;
 constexpr int kPackWarps = kPackThreads / 32;
 
 // A warp takes 1024 consecutive elements of a row at a time, a lane eight of each 256, so that four
-// loads are in flight and a row's address is found once for 32 elements of a lane.
+// loads are in flight and a row's address is found once for 32 elements of a lane. Groups are powers
+// of two: their numbers are shifts (`by`), and the walk over rows and spans has no division.
 constexpr int kPieces = 4;
+struct Span {
+  int row, at, per_row, rows, row_step, at_step;
+  __device__ __forceinline__ Span(int rows_, int K) : rows(rows_) {
+    per_row = (padded(K) + 1023) / 1024;
+    const int first = (int)blockIdx.x * kPackWarps + (int)(threadIdx.x >> 5);
+    const int step = (int)gridDim.x * kPackWarps;
+    row = first / per_row;
+    at = first - row * per_row;
+    row_step = step / per_row;
+    at_step = step - row_step * per_row;
+  }
+  __device__ __forceinline__ bool more() const { return row < rows; }
+  __device__ __forceinline__ int k0() const { return at * 1024 + (int)(threadIdx.x & 31) * 8; }
+  __device__ __forceinline__ void next() {
+    at += at_step;
+    row += row_step;
+    if (at >= per_row) {
+      at -= per_row;
+      ++row;
+    }
+  }
+};
 
-// Eight elements as they are loaded, G / 8 lanes a group. The scale is the least s of its type with
-// 7 s >= the group's largest magnitude: a seventh of that, cut, is within a step of it, and 7 s
-// against the magnitude is exact in one fused operation. A code is w / s rounded to the
-// nearest, ties to even. w (1 / s) + 1.5 * 2^23 + 8, rounded once, has it in its last bits unless w / s
-// is within 2^-19 of the middle between two codes (1 / s is off by 2^-23); then w - code * s, which is
-// exact, decides.
-__device__ __forceinline__ uint32_t pack8(const float (&v)[8], int G, int sdt, float& s, bool& bad) {
-  float a = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) a = max_nan(a, fabsf(v[i]));
-  for (int o = 1; o < G / 8; o *= 2) a = max_nan(a, __shfl_xor_sync(kFull, a, o));
-  bad = !(a < INFINITY);
-  const uint32_t step = sdt == SPEC_BF16 ? 0x10000u : 1u;
+// The least s of the scales' type with 7 s >= a: a seventh of a, cut, is within a step of it, and 7 s
+// against a is exact in one fused operation.
+template <int SDT>
+__device__ __forceinline__ float least_scale(float a) {
+  constexpr uint32_t step = SDT == SPEC_BF16 ? 0x10000u : 1u;
   uint32_t b = __float_as_uint(a * (1.0f / 7.0f)) & ~(step - 1u);
   if (b && fmaf(7.0f, __uint_as_float(b - step), -a) >= 0.0f) b -= step;
   if (fmaf(7.0f, __uint_as_float(b), -a) < 0.0f) b += step;
   if (fmaf(7.0f, __uint_as_float(b), -a) < 0.0f) b += step;  // a subnormal quotient
-  s = bad ? NAN : __uint_as_float(b);
+  return __uint_as_float(b);
+}
+
+// 1 / s to 2^-23, for s above 2^-100 only.
+__device__ __forceinline__ float about_inverse(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return r;
+}
+
+// Eight elements' codes: w / s rounded to the nearest, ties to even, plus 8. w (1 / s) + 1.5 * 2^23 + 8,
+// rounded once, has it in its last bits unless w / s is within 2^-19 of the middle between two codes
+// (1 / s is off by 2^-23); then w - code * s, which is exact, decides.
+__device__ __forceinline__ uint32_t codes8(const float (&v)[8], float s) {
   if (!(s > 0.0f)) return 0x88888888u;  // zeros, and what has no scale
   uint32_t w = 0;
-  if (s > 0x1p-100f) {  // 1 / s is finite and normal
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
-    const float half = 0.5f * s, near = 0.499997f * s;
+  if (s > 0x1p-100f) {
+    const float r = about_inverse(s), half = 0.5f * s, near = 0.499997f * s;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float t = fmaf(v[i], r, 12582920.0f), c = t - 12582920.0f;
       const float e = fmaf(-c, s, v[i]);
       uint32_t q = __float_as_uint(t) & 15u;
-      // one element in a hundred of bf16 matrices: a branch for each took 656 us for 129280 x 4096,
-      // one for a lane's eight 1039, none 717
       if (fabsf(e) > near && (fabsf(e) > half || (fabsf(e) == half && (q & 1u))))
         q += e > 0.0f ? 1u : ~0u;
       w |= q << (4 * i);
@@ -53,38 +77,113 @@ __device__ __forceinline__ uint32_t pack8(const float (&v)[8], int G, int sdt, f
     return w;
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    w |= (uint32_t)(((int)rintf(__fdiv_rn(v[i], s)) + 8) & 15) << (4 * i);
+  for (int i = 0; i < 8; ++i) {
+    // a quotient may be rounded to the middle: here, too, the remainder decides
+    const float c = rintf(__fdiv_rn(v[i], s)), e = 2.0f * fmaf(-c, s, v[i]);
+    int q = (int)c + 8;
+    if (fabsf(e) > s || (fabsf(e) == s && (q & 1))) q += e > 0.0f ? 1 : -1;
+    w |= (uint32_t)(q & 15) << (4 * i);
+  }
   return w;
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kPackThreads)
-    pack_kernel(const void* x, long long ldx, int rows, int K, int G, uint8_t* codes, void* scales,
-                int sdt, uint32_t* status) {
-  grid_dep_wait();
-  const int Kp = padded(K), per_row = (Kp + 1023) / 1024, lane = threadIdx.x & 31;
-  const long long all = (long long)rows * per_row, step = (long long)gridDim.x * kPackWarps;
-  for (long long at = (long long)blockIdx.x * kPackWarps + (threadIdx.x >> 5); at < all; at += step) {
-    const int row = (int)(at / per_row), k0 = (int)(at - (long long)row * per_row) * 1024 + lane * 8;
-    float v[kPieces][8];
+// The same where elements and scales are bf16, s > 2^-100. With w = W 2^b and s = S 2^a, 128 <= S, W <
+// 256, w / s is the middle between two codes or at least 2^-9 from it: |2 w - (2 c + 1) s| is a
+// multiple of 2^a where w >= 128 * 2^(a - 1), and below that w is at most 255 * 2^(a - 2), which is
+// s / 2 less s / 512 or more. So w (1 / s) to the nearest multiple of 2^-10 (ulp of 1.5 * 2^13) is on
+// the right side, a middle among them exactly, and one more addition rounds it to even: three
+// instructions an element, 1.5 * 2^23 + 8 + c times 16^i summed into the word. (With the remainder as
+// above, one element in a hundred had to branch: 129280 x 4096 took 656 us, 1039 with a branch for
+// eight, 717 without one.)
+__device__ __forceinline__ uint32_t codes8_bf16(const uint32_t (&v)[4], float s) {
+  const float r = about_inverse(s);
+  uint32_t w = 0, m = 1;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i)
-      load8(x, DT, (size_t)row * ldx, k0 + i * 256, K, v[i]);
+  for (int i = 0; i < 8; ++i) {
+    const float x = __uint_as_float(i & 1 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16);
+    const float t = __fadd_rn(fmaf(x, r, 12288.0f), 12582920.0f - 12288.0f);
+    w += __float_as_uint(t) * m;
+    m *= 16;
+  }
+  return w - 0x4b400000u * 0x11111111u;
+}
+
+template <int DT, int SDT>
+__global__ void __launch_bounds__(kPackThreads)
+    pack_kernel(const void* x, long long ldx, int rows, int K, int by, uint8_t* codes, void* scales,
+                uint32_t* status) {
+  grid_dep_wait();
+  const int Kp = padded(K), G = 1 << by, lane = threadIdx.x & 31;
+  for (Span at(rows, K); at.more(); at.next()) {
+    const int row = at.row, k0 = at.k0();
+    const size_t xr = (size_t)row * ldx;
+    float v[DT == SPEC_BF16 ? 1 : kPieces][8], a[kPieces];
+    uint32_t u[DT == SPEC_BF16 ? kPieces : 1][4];
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      if constexpr (DT == SPEC_BF16) {
+        const uint4 q = load8_bf16(x, xr, k0 + i * 256, K);
+        u[i][0] = q.x;
+        u[i][1] = q.y;
+        u[i][2] = q.z;
+        u[i][3] = q.w;
+      } else {
+        load8(x, DT, xr, k0 + i * 256, K, v[i]);
+      }
+    }
+    // the groups' largest magnitudes, NaN if there is one
+    if constexpr (DT == SPEC_BF16) {
+#pragma unroll
+      for (int i = 0; i < kPieces; i += 2) {
+        __nv_bfloat162 m[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          m[q] = __hmax2_nan(
+              __hmax2_nan(__habs2(as_bf2(u[i + q][0])), __habs2(as_bf2(u[i + q][1]))),
+              __hmax2_nan(__habs2(as_bf2(u[i + q][2])), __habs2(as_bf2(u[i + q][3]))));
+        // two groups' in one word
+        __nv_bfloat162 both = __hmax2_nan(as_bf2(__byte_perm(as_word(m[0]), as_word(m[1]), 0x5410)),
+                                          as_bf2(__byte_perm(as_word(m[0]), as_word(m[1]), 0x7632)));
+        for (int o = 1; o < G / 8; o *= 2)
+          both = __hmax2_nan(both, as_bf2(__shfl_xor_sync(kFull, as_word(both), o)));
+        a[i] = __uint_as_float(as_word(both) << 16);
+        a[i + 1] = __uint_as_float(as_word(both) & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        a[i] = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) a[i] = max_nan(a[i], fabsf(v[i][q]));
+        for (int o = 1; o < G / 8; o *= 2) a[i] = max_nan(a[i], __shfl_xor_sync(kFull, a[i], o));
+      }
+    }
+    const size_t words = ((size_t)row * Kp + k0) / 8, groups = (size_t)row * (Kp >> by);
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const int k = k0 + i * 256;
-      if (k - lane * 8 >= Kp) break;  // the warp's last pieces are behind the row
-      float s;
-      bool bad;
-      const uint32_t w = pack8(v[i], G, sdt, s, bad);
-      if (k >= Kp) continue;  // shuffles stay within groups, which end with the row
-      *reinterpret_cast<uint32_t*>(codes + ((size_t)row * Kp + k) / 2) = w;
+      if (k >= Kp) break;
+      const bool bad = !(a[i] < INFINITY);
+      const float s = bad ? NAN : least_scale<SDT>(a[i]);
+      uint32_t w;
+      if constexpr (DT == SPEC_BF16) {
+        if (SDT == SPEC_BF16 && s > 0x1p-100f) {
+          w = codes8_bf16(u[i], s);
+        } else {
+          float f[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            f[q] = __uint_as_float(q & 1 ? u[i][q / 2] & 0xffff0000u : u[i][q / 2] << 16);
+          w = codes8(f, s);
+        }
+      } else {
+        w = codes8(v[i], s);
+      }
+      reinterpret_cast<uint32_t*>(codes)[words + i * 32] = w;
       if ((k & (G - 1)) == 0) {
-        const size_t g = (size_t)row * (Kp / G) + k / G;
-        if (sdt == SPEC_BF16)
-          static_cast<uint16_t*>(scales)[g] =
-              bad ? 0x7fffu : (uint16_t)(__float_as_uint(s) >> 16);
+        const size_t g = groups + (k >> by);
+        if constexpr (SDT == SPEC_BF16)
+          static_cast<uint16_t*>(scales)[g] = bad ? 0x7fffu : (uint16_t)(__float_as_uint(s) >> 16);
         else
           static_cast<float*>(scales)[g] = s;
         if (bad) atomicOr(status, SPEC_DEV_NONFINITE);
@@ -93,53 +192,74 @@ __global__ void __launch_bounds__(kPackThreads)
   }
 }
 
-// The codes of a word as numbers, less the zero point.
-template <int DT>
+// The codes of a word as numbers, less the zero point, times the scale. A lane writes 16 bytes at a
+// time, eight bf16 or four fp32 elements. With bf16 on both sides two at a time: 128 + code and 128 +
+// zero point are bf16, so is their difference, and its product with the scale is rounded once.
+template <int DT, int SDT>
 __global__ void __launch_bounds__(kPackThreads)
-    unpack_kernel(const uint8_t* codes, const void* scales, int sdt, const uint8_t* zeros, int rows,
-                  int K, int G, void* out, long long ldo) {
+    unpack_kernel(const uint8_t* codes, const void* scales, const uint8_t* zeros, int rows, int K,
+                  int by, void* out, long long ldo) {
   grid_dep_wait();
-  const int Kp = padded(K), per_row = (Kp + 1023) / 1024, lane = threadIdx.x & 31;
-  const long long all = (long long)rows * per_row, step = (long long)gridDim.x * kPackWarps;
-  for (long long at = (long long)blockIdx.x * kPackWarps + (threadIdx.x >> 5); at < all; at += step) {
-    const int row = (int)(at / per_row), k0 = (int)(at - (long long)row * per_row) * 1024 + lane * 8;
-    uint32_t w[kPieces];
-    float s[kPieces];
-    int z[kPieces];
+  constexpr int N = DT == SPEC_BF16 ? 8 : 4, kTakes = 32 / N;
+  const int Kp = padded(K), lane = threadIdx.x & 31;
+  for (Span at(rows, K); at.more(); at.next()) {
+    const int row = at.row, k0 = at.at * 1024 + lane * N;
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(codes) + (size_t)row * Kp / 8;
+    const size_t groups = (size_t)row * (Kp >> by);
+    uint32_t w[kTakes];
+    float s[kTakes];
+    int z[kTakes];
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int k = k0 + i * 256;
+    for (int i = 0; i < kTakes; ++i) {
+      const int k = k0 + i * 32 * N;
       w[i] = 0;
       s[i] = 0.0f;
       z[i] = 8;
       if (k >= K) continue;
-      const size_t g = (size_t)row * (Kp / G) + k / G;
-      w[i] = *reinterpret_cast<const uint32_t*>(codes + ((size_t)row * Kp + k) / 2);
-      s[i] = load_scale(scales, sdt, g);
+      const size_t g = groups + (k >> by);
+      w[i] = words[k / 8];
+      s[i] = load_scale(scales, SDT, g);
       if (zeros) z[i] = zeros[g] & 127;
     }
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int k = k0 + i * 256;
+    for (int i = 0; i < kTakes; ++i) {
+      const int k = k0 + i * 32 * N;
       if (k >= K) break;
-      const float base = 8388608.0f + (float)z[i];
-      float v[8];
+      if constexpr (DT == SPEC_BF16 && SDT == SPEC_BF16) {
+        const __nv_bfloat162 base = as_bf2((0x4300u | z[i]) * 0x10001u),
+                             scale = as_bf2((__float_as_uint(s[i]) >> 16) * 0x10001u);
+        uint32_t p[4];  // elements q and q + 4
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const float c = __uint_as_float(0x4b000000u | (w[i] >> (4 * q) & 15u)) - base;
-        v[q] = __fmul_rn(c, s[i]);
-        if (DT == SPEC_BF16 && sdt == SPEC_F32) {
-          // towards the odd neighbour where fp32 does not hold the product, so that bf16 rounds it
-          // once
-          const float rest = fmaf(c, s[i], -v[q]);
-          uint32_t b = __float_as_uint(v[q]);
-          if (rest != 0.0f) {
-            if ((rest < 0.0f) != (v[q] < 0.0f)) --b;
-            v[q] = __uint_as_float(b | 1u);
+        for (int q = 0; q < 4; ++q)
+          p[q] = as_word(__hmul2_rn(
+              __hsub2_rn(as_bf2((w[i] >> (4 * q) & 0x000f000fu) | 0x43004300u), base), scale));
+        const uint32_t o[4] = {__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410),
+                               __byte_perm(p[0], p[1], 0x7632), __byte_perm(p[2], p[3], 0x7632)};
+        store8_bf16(out, (size_t)row * ldo, k, K, o);
+      } else {
+        const float base = 8388608.0f + (float)z[i];
+        const uint32_t own = N == 4 ? w[i] >> (lane & 1) * 16 : w[i];
+        float v[N];
+#pragma unroll
+        for (int q = 0; q < N; ++q) {
+          const float c = __uint_as_float(0x4b000000u | (own >> (4 * q) & 15u)) - base;
+          v[q] = __fmul_rn(c, s[i]);
+          if constexpr (DT == SPEC_BF16) {
+            // towards the odd neighbour where fp32 does not hold the product, so that bf16 rounds it
+            // once
+            const float rest = fmaf(c, s[i], -v[q]);
+            uint32_t b = __float_as_uint(v[q]);
+            if (rest != 0.0f) {
+              if ((rest < 0.0f) != (v[q] < 0.0f)) --b;
+              v[q] = __uint_as_float(b | 1u);
+            }
           }
         }
+        if constexpr (DT == SPEC_BF16)
+          store8(out, DT, (size_t)row * ldo, k, K, v);
+        else
+          store4(static_cast<float*>(out) + (size_t)row * ldo + k, K - k, v);
       }
-      store8(out, DT, (size_t)row * ldo, k, K, v);
     }
   }
 }
@@ -201,28 +321,54 @@ cudaError_t launch_w4_logits(W4Args a, cudaStream_t s) {
                          : launch_g32(a, codes, form, s);
 }
 
-// CTAs for `rows` rows of K.
+// CTAs for `rows` rows of K: four times what is resident, so that they drift apart between reading and
+// writing (129280 x 4096 bf16 packed in 249 us and read back in 202; with one time 267 and 243, with
+// one span a warp 273 and 208).
 static dim3 pack_grid(int rows, int K) {
   const long long warps = (long long)rows * ((w4::padded(K) + 1023) / 1024);
-  const long long n = (warps + w4::kPackWarps - 1) / w4::kPackWarps, most = num_sms() * 8;
+  const long long n = (warps + w4::kPackWarps - 1) / w4::kPackWarps, most = num_sms() * 32;
   return dim3((unsigned)(n < most ? n : most));
+}
+
+static int log2_of(int group) { return group == 32 ? 5 : group == 64 ? 6 : 7; }
+
+template <int DT, int SDT>
+static void launch_pack(const void* x, long long ldx, int rows, int K, int group, uint8_t* codes,
+                        void* scales, uint32_t* status, cudaStream_t s) {
+  launch_kernel(w4::pack_kernel<DT, SDT>, pack_grid(rows, K), dim3(w4::kPackThreads), 0, s, true, x,
+                ldx, rows, K, log2_of(group), codes, scales, status);
 }
 
 void launch_w4_quantize(const void* x, int dt, long long ldx, int rows, int K, int group,
                         uint8_t* codes, void* scales, int sdt, uint32_t* status, cudaStream_t s) {
   TraceScope ts(SPEC_KCLASS_OTHER, s);
-  launch_kernel(dt == SPEC_BF16 ? w4::pack_kernel<SPEC_BF16> : w4::pack_kernel<SPEC_F32>,
-                pack_grid(rows, K), dim3(w4::kPackThreads), 0, s, true, x, ldx, rows, K, group, codes,
-                scales, sdt, status);
+  const bool sb = sdt == SPEC_BF16;
+  if (dt == SPEC_BF16)
+    (sb ? launch_pack<SPEC_BF16, SPEC_BF16> : launch_pack<SPEC_BF16, SPEC_F32>)(
+        x, ldx, rows, K, group, codes, scales, status, s);
+  else
+    (sb ? launch_pack<SPEC_F32, SPEC_BF16> : launch_pack<SPEC_F32, SPEC_F32>)(
+        x, ldx, rows, K, group, codes, scales, status, s);
+}
+
+template <int DT, int SDT>
+static void launch_unpack(const uint8_t* codes, const void* scales, const uint8_t* zeros, int rows,
+                          int K, int group, void* out, long long ldo, cudaStream_t s) {
+  launch_kernel(w4::unpack_kernel<DT, SDT>, pack_grid(rows, K), dim3(w4::kPackThreads), 0, s, true,
+                codes, scales, zeros, rows, K, log2_of(group), out, ldo);
 }
 
 void launch_w4_dequantize(const uint8_t* codes, const void* scales, int sdt, const uint8_t* zeros,
                           int rows, int K, int group, void* out, int odt, long long ldo,
                           cudaStream_t s) {
   TraceScope ts(SPEC_KCLASS_OTHER, s);
-  launch_kernel(odt == SPEC_BF16 ? w4::unpack_kernel<SPEC_BF16> : w4::unpack_kernel<SPEC_F32>,
-                pack_grid(rows, K), dim3(w4::kPackThreads), 0, s, true, codes, scales, sdt, zeros,
-                rows, K, group, out, ldo);
+  const bool sb = sdt == SPEC_BF16;
+  if (odt == SPEC_BF16)
+    (sb ? launch_unpack<SPEC_BF16, SPEC_BF16> : launch_unpack<SPEC_BF16, SPEC_F32>)(
+        codes, scales, zeros, rows, K, group, out, ldo, s);
+  else
+    (sb ? launch_unpack<SPEC_F32, SPEC_BF16> : launch_unpack<SPEC_F32, SPEC_F32>)(
+        codes, scales, zeros, rows, K, group, out, ldo, s);
 }
 
 }  // namespace spec

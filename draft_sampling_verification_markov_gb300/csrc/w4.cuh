@@ -8,6 +8,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "row_pieces.cuh"
 
 namespace spec {
 namespace w4 {
@@ -17,22 +18,27 @@ constexpr int kBlock = 128;     // codes of a row that a warp takes at once
 
 __host__ __device__ constexpr int padded(int K) { return (K + kBlock - 1) / kBlock * kBlock; }
 
+// Eight consecutive bf16 elements of a row, zeros past K.
+__device__ __forceinline__ uint4 load8_bf16(const void* p, size_t row, int k, int K) {
+  const uint16_t* at = static_cast<const uint16_t*>(p) + row + k;
+  if (k + 8 <= K && (reinterpret_cast<uintptr_t>(at) & 15) == 0) return ld_coherent16(at);
+  uint32_t w[4] = {};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (k + i < K) w[i / 2] |= (uint32_t)at[i] << (i & 1 ? 16 : 0);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // Eight consecutive elements of a row as fp32, zeros past K.
 __device__ __forceinline__ void load8(const void* p, int dt, size_t row, int k, int K,
                                       float (&v)[8]) {
   if (dt == SPEC_BF16) {
-    const uint16_t* at = static_cast<const uint16_t*>(p) + row + k;
-    if (k + 8 <= K && (reinterpret_cast<uintptr_t>(at) & 15) == 0) {
-      const uint4 q = ld_coherent16(at);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    const uint4 q = load8_bf16(p, row, k, K);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = k + i < K ? bf16_to_f32(at[i]) : 0.0f;
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   } else {
     const float* at = static_cast<const float*>(p) + row + k;
@@ -54,19 +60,24 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   return d;
 }
 
+__device__ __forceinline__ void store8_bf16(void* p, size_t row, int k, int K,
+                                            const uint32_t (&w)[4]) {
+  uint16_t* at = static_cast<uint16_t*>(p) + row + k;
+  if (k + 8 <= K && (reinterpret_cast<uintptr_t>(at) & 15) == 0) {
+    *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (k + i < K) at[i] = (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
+  }
+}
+
 __device__ __forceinline__ void store8(void* p, int dt, size_t row, int k, int K,
                                        const float (&v)[8]) {
   if (dt == SPEC_BF16) {
-    uint16_t* at = static_cast<uint16_t*>(p) + row + k;
     const uint32_t w[4] = {bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]),
                            bf16_pair(v[6], v[7])};
-    if (k + 8 <= K && (reinterpret_cast<uintptr_t>(at) & 15) == 0) {
-      *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (k + i < K) at[i] = (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
-    }
+    store8_bf16(p, row, k, K, w);
   } else {
     float* at = static_cast<float*>(p) + row + k;
     if (k + 8 <= K && (reinterpret_cast<uintptr_t>(at) & 15) == 0) {
@@ -80,10 +91,15 @@ __device__ __forceinline__ void store8(void* p, int dt, size_t row, int k, int K
   }
 }
 
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
+// Four consecutive elements of a row, of which `left` have a place.
+__device__ __forceinline__ void store4(float* at, int left, const float (&v)[4]) {
+  if (left >= 4 && (reinterpret_cast<uintptr_t>(at) & 15) == 0) {
+    *reinterpret_cast<float4*>(at) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < left) at[i] = v[i];
+  }
 }
 
 __device__ __forceinline__ float load_scale(const void* p, int dt, size_t at) {

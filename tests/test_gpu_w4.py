@@ -82,6 +82,26 @@ def test_pack_ties_and_extremes():
         assert torch.equal(q.scales.cpu(), scales) and torch.equal(q.codes.cpu(), codes)
 
 
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("power", [-130, -100, -99, 0, 60, 124])
+def test_pack_quotients_in_the_middle(power, dt):
+    """Multiples of a quarter or a 32nd: many quotients are halves, at sizes where the reciprocal is
+    taken, where it is not, and at the largest."""
+    g = torch.Generator().manual_seed(power + 200)
+    x = torch.cat([torch.randint(-28, 29, (64, 512), generator=g) / 4.0,
+                   torch.randint(-112, 113, (64, 512), generator=g) / 32.0,
+                   torch.randn(64, 512, generator=g)]).clamp_(-7, 7)
+    x = torch.ldexp(x.double(), torch.tensor(power)).to(dt)
+    for sdt in (BF, F32):
+        codes, scales = ref.pack(x, 32, sdt)
+        q = S.spec_w4_quantize(x.to(DEV), 32, scale_dtype=sdt)
+        assert torch.equal(q.scales.cpu(), scales)
+        assert torch.equal(q.codes.cpu(), codes)
+        for odt in (BF, F32):
+            y = S.spec_w4_dequantize(q, dtype=odt)
+            assert torch.equal(y.cpu(), ref.values(codes, scales, 32, 512).to(odt))
+
+
 def test_read_back_rounds_once():
     """fp32 scales: a bf16 value is the product's own rounding, not that of its fp32 form."""
     g = torch.Generator().manual_seed(4)
