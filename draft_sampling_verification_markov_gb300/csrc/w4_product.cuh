@@ -560,7 +560,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     side.next_block();
-    if (++in_chunk == kChunk) {
+    // a unit may end within four groups
+    if (++in_chunk == kChunk || (ik + 1 == my_nk && (i == W - 1 || kb + 1 == KB))) {
       in_chunk = 0;
       load_side(side);
     }
@@ -646,10 +647,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (taken < given) take();
     if (++ik == my_nk) {
       ik = 0;
-      if (in_chunk) {  // the unit ends within four groups
-        in_chunk = 0;
-        load_side(side);
-      }
       give();
     }
   }
