@@ -1459,6 +1459,8 @@ __device__ __noinline__ void write_part(const SampleArgs& a, int row, const Part
   char* base = const_cast<char*>(to.base);
   const bool same = to.head == part.row.head;
   const int n = part.steps();
+  // what a bf16 above cut.x is above; one that equals it may be cut.x or not
+  const __nv_bfloat162 at = __float2bfloat162_rn(__bfloat162float(__float2bfloat16_rd(cut.x)));
   for (int it = 0; it < n; ++it) {
     uint4 q[kBatch];
     part.load(q, it);
@@ -1466,23 +1468,41 @@ __device__ __noinline__ void write_part(const SampleArgs& a, int row, const Part
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
       const int v = (j + b * 32) * N - part.row.head;
-      float x[N];
-      unpack<DT>(q[b], x);
       uint32_t w[4] = {q[b].x, q[b].y, q[b].z, q[b].w};
+      bool even = !copy;  // whether the logits decide, without the ids
+      if constexpr (DT == SPEC_BF16) {
+        uint32_t equal = 0, o[4];
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const bool in = copy || cut.leaves(x[i], v + i);
-        if constexpr (DT == SPEC_BF16) {
-          if (!in) w[i / 2] = i & 1 ? (w[i / 2] & 0xffffu) | 0xff800000u
-                                    : (w[i / 2] & 0xffff0000u) | 0xff80u;
-        } else {
-          if (!in) w[i] = 0xff800000u;
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t m = __hgt2_mask(as_bf2(w[i]), at);
+          equal |= __heq2_mask(as_bf2(w[i]), at);
+          o[i] = (w[i] & m) | (0xff80ff80u & ~m);
+        }
+        even = even && !equal;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (even) w[i] = o[i];
+      } else {
+        even = false;
+      }
+      if (!copy && !even) {
+        float x[N];
+        unpack<DT>(q[b], x);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const bool in = cut.leaves(x[i], v + i);
+          if constexpr (DT == SPEC_BF16) {
+            if (!in) w[i / 2] = i & 1 ? (w[i / 2] & 0xffffu) | 0xff800000u
+                                      : (w[i / 2] & 0xffff0000u) | 0xff80u;
+          } else {
+            if (!in) w[i] = 0xff800000u;
+          }
         }
       }
       if (j + b * 32 >= part.j1) continue;
       if (same && v >= 0 && v + N <= a.V) {
-        *reinterpret_cast<uint4*>(base + (size_t)(j + b * 32) * 16) =
-            make_uint4(w[0], w[1], w[2], w[3]);
+        __stcs(reinterpret_cast<uint4*>(base + (size_t)(j + b * 32) * 16),
+               make_uint4(w[0], w[1], w[2], w[3]));
       } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
