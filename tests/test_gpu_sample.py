@@ -131,6 +131,50 @@ def test_temperatures(T, dt):
 
 
 @pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("heads", [2, 5, 40, 400])
+def test_nuclei_that_end_next_to_a_heavy_token(heads, dt):
+    """A few tokens hold most of the mass, alone in their places; p is a hundredth or less of the mass
+    away from where one of them ends, so that a border guessed from counts is often a token off."""
+    V, rows = 40000, 180
+    g = torch.Generator().manual_seed(heads)
+    x = torch.randn(rows, V, generator=g) * 2
+    at = torch.stack([torch.randperm(V, generator=g)[:heads] for _ in range(rows)])
+    x = x.scatter(1, at, 12 + 6 * torch.rand(rows, heads, generator=g)).to(dt)
+    w = torch.softmax(x.double(), 1).sort(1, descending=True).values.cumsum(1)
+    j = torch.randint(0, heads, (rows,), generator=g)
+    off = (torch.rand(rows, generator=g).double() - 0.5) * 0.02
+    p = (w.gather(1, j[:, None])[:, 0] * (1 + off)).clamp(0.01, 0.9999).float()
+    u = uniforms(rows, heads)
+    for n in (rows, 9):
+        d, c, st = both(x[:n], u[:n], 1.0, 0, p[:n].contiguous().to(DEV), 0.0)
+        assert st == 0
+        check(x[:n], u[:n], [(1.0, 0, float(p[r]), 0.0) for r in range(n)], d, c,
+              range(0, n, 1 if n < 20 else 6))
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("rows", [6, 170])
+@pytest.mark.parametrize("flat", [False, True])
+def test_large_top_k_with_the_other_rules(flat, rows, dt):
+    """More tokens than a list holds, by each rule and by two or three of them, ending before and
+    behind one another."""
+    V = 40000
+    x = ref.logits(rows, V, 21, dt) if not flat else \
+        (torch.randn(rows, V, generator=torch.Generator().manual_seed(22)) * 0.3).to(dt)
+    u = uniforms(rows, 23)
+    for k in (2000, 9000, 39999):
+        for p in (0.3, 0.9, 0.999, 1.0):
+            for mp in (0.0, 1e-4, 0.02, 0.3):
+                d, c, st = both(x, u, 1.1, k, p, mp)
+                assert st == 0
+                check(x, u, (1.1, k, p, mp), d, c, (0, rows - 1))
+    for p, mp in ((0.3, 1e-4), (0.9, 0.02), (0.99, 0.3), (1.0, 0.05)):
+        d, c, st = both(x, u, 1.1, 0, p, mp)
+        assert st == 0
+        check(x, u, (1.1, 0, p, mp), d, c, (0, 1, rows - 1))
+
+
+@pytest.mark.parametrize("dt", DTS)
 @pytest.mark.parametrize("rows", [24, 600])
 def test_parameters_per_request(rows, dt):
     V, per = 3001, 3
