@@ -389,6 +389,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   __syncthreads();
   grid_dep_wait();
+  // the copies are of another proxy than the stores of whoever packed the matrix just now
+  asm volatile("fence.proxy.async.global;" ::: "memory");
 
   // tiles, by the first lane: coordinates of the next one
   const uint64_t policy = tc::policy_evict_first();
@@ -666,8 +668,9 @@ cudaError_t launch_t(W4Args a, const CUtensorMap& codes, cudaStream_t s) {
   while (a.stages > 2 && rest + a.stages * kStage > kSmemMost) --a.stages;
   const size_t smem = rest + a.stages * kStage;
   auto k = product_kernel<G, R, T, W, ZEROS, NARROW>;
+  // the same for every call: another thread's may come between this and the launch
   const cudaError_t e =
-      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMost);
   if (e != cudaSuccess) return e;
   int shares = num_sms() / a.chunks;
   const int most = (units + teams - 1) / teams;

@@ -1,4 +1,5 @@
 """Grouped 4-bit weights on the GPU against 64 bits: packing, reading back, products."""
+import threading
 import time
 
 import pytest
@@ -263,6 +264,46 @@ def test_graph_and_streams():
         static.copy_(randn((4, 512), seed, BF))
         g.replay()
         assert torch.equal(out, S.spec_w4_logits(static, w))
+
+
+def test_product_right_after_packing():
+    """The copies see what the kernel before them wrote, call after call into the same matrix."""
+    x = randn((2, 256), 41, BF).to(DEV)
+    ms = [randn((3000, 256), 42 + i, BF, 0.1).to(DEV) for i in range(6)]
+    want = [S.spec_w4_logits(x, S.spec_w4_quantize(m, 64)) for m in ms]
+    w = S.spec_w4_quantize(ms[0], 64)
+    got = []
+    for m in ms * 3:
+        S.spec_w4_quantize(m, 64, out=w)
+        got.append(S.spec_w4_logits(x, w))
+    for i, y in enumerate(got):
+        assert torch.equal(y, want[i % 6]), i
+
+
+def test_calls_of_several_threads():
+    """Forms with different shared memory, at once from several host threads on streams of their own."""
+    sizes = [(1, 256), (5, 2048), (17, 4096), (40, 1024)]
+    w = [packed(600, K, 128, BF, K)[0] for _, K in sizes]
+    x = [randn((M, K), M, BF).to(DEV) for M, K in sizes]
+    want = [S.spec_w4_logits(a, b) for a, b in zip(x, w)]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def run(i):
+        side, ws = torch.cuda.Stream(device=DEV), S.Workspace(256, device=DEV)
+        out = torch.empty_like(want[i])
+        side.wait_stream(torch.cuda.default_stream(torch.device(DEV)))
+        for _ in range(100):
+            S.spec_w4_logits(x[i], w[i], out=out, workspace=ws, stream=side)
+        side.synchronize()
+        if ws.status() or not torch.equal(out, want[i]):
+            wrong.append(i)
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(sizes))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert wrong == []
 
 
 def test_expired_wait_reports_timeout():
