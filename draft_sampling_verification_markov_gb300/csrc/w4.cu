@@ -38,12 +38,19 @@ struct Span {
   }
 };
 
-// The least s of the scales' type with 7 s >= a: a seventh of a, cut, is within a step of it, and 7 s
-// against a is exact in one fused operation.
+// The least s of the scales' type with 7 s >= a; 7 s against a is exact in one fused operation. For
+// bf16 a seventh of a, rounded up twice, is at most 2^-22 too large, which moves it past one number at
+// most; for fp32 a seventh, rounded, is within a step.
 template <int SDT>
 __device__ __forceinline__ float least_scale(float a) {
   constexpr uint32_t step = SDT == SPEC_BF16 ? 0x10000u : 1u;
-  uint32_t b = __float_as_uint(a * (1.0f / 7.0f)) & ~(step - 1u);
+  if constexpr (SDT == SPEC_BF16) {
+    constexpr float kSeventh = 0x1.24924ap-3f;  // above 1 / 7
+    const uint32_t b = (__float_as_uint(__fmul_ru(a, kSeventh)) + 0xffffu) & 0xffff0000u;
+    const float less = __uint_as_float(b - step);  // NaN if b is 0
+    return fmaf(7.0f, less, -a) >= 0.0f ? less : __uint_as_float(b);
+  }
+  uint32_t b = __float_as_uint(a * (1.0f / 7.0f));
   if (b && fmaf(7.0f, __uint_as_float(b - step), -a) >= 0.0f) b -= step;
   if (fmaf(7.0f, __uint_as_float(b), -a) < 0.0f) b += step;
   if (fmaf(7.0f, __uint_as_float(b), -a) < 0.0f) b += step;  // a subnormal quotient
@@ -119,17 +126,26 @@ __global__ void __launch_bounds__(kPackThreads)
     const size_t xr = (size_t)row * ldx;
     float v[DT == SPEC_BF16 ? 1 : kPieces][8], a[kPieces];
     uint32_t u[DT == SPEC_BF16 ? kPieces : 1][4];
+    if constexpr (DT == SPEC_BF16) {
+      const uint16_t* px = static_cast<const uint16_t*>(x) + xr + k0;
+      uint4 q[kPieces];
+      if (k0 + (kPieces - 1) * 256 + 8 <= K && (reinterpret_cast<uintptr_t>(px) & 15) == 0) {
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      if constexpr (DT == SPEC_BF16) {
-        const uint4 q = load8_bf16(x, xr, k0 + i * 256, K);
-        u[i][0] = q.x;
-        u[i][1] = q.y;
-        u[i][2] = q.z;
-        u[i][3] = q.w;
+        for (int i = 0; i < kPieces; ++i) q[i] = ld_coherent16(px + i * 256);
       } else {
-        load8(x, DT, xr, k0 + i * 256, K, v[i]);
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) q[i] = load8_bf16(x, xr, k0 + i * 256, K);
       }
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        u[i][0] = q[i].x;
+        u[i][1] = q[i].y;
+        u[i][2] = q[i].z;
+        u[i][3] = q[i].w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) load8(x, DT, xr, k0 + i * 256, K, v[i]);
     }
     // the groups' largest magnitudes, NaN if there is one
     if constexpr (DT == SPEC_BF16) {
@@ -158,11 +174,12 @@ __global__ void __launch_bounds__(kPackThreads)
         for (int o = 1; o < G / 8; o *= 2) a[i] = max_nan(a[i], __shfl_xor_sync(kFull, a[i], o));
       }
     }
-    const size_t words = ((size_t)row * Kp + k0) / 8, groups = (size_t)row * (Kp >> by);
+    uint32_t* words = reinterpret_cast<uint32_t*>(codes) + ((size_t)row * Kp + k0) / 8;
+    const size_t first = (size_t)row * (Kp >> by) + (k0 >> by);
+    const bool leads = (k0 & (G - 1)) == 0;  // its group, in every piece
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int k = k0 + i * 256;
-      if (k >= Kp) break;
+      if (k0 + i * 256 >= Kp) break;
       const bool bad = !(a[i] < INFINITY);
       const float s = bad ? NAN : least_scale<SDT>(a[i]);
       uint32_t w;
@@ -179,9 +196,9 @@ __global__ void __launch_bounds__(kPackThreads)
       } else {
         w = codes8(v[i], s);
       }
-      reinterpret_cast<uint32_t*>(codes)[words + i * 32] = w;
-      if ((k & (G - 1)) == 0) {
-        const size_t g = groups + (k >> by);
+      words[i * 32] = w;
+      if (leads) {
+        const size_t g = first + (i * 256 >> by);
         if constexpr (SDT == SPEC_BF16)
           static_cast<uint16_t*>(scales)[g] = bad ? 0x7fffu : (uint16_t)(__float_as_uint(s) >> 16);
         else
@@ -322,8 +339,8 @@ cudaError_t launch_w4_logits(W4Args a, cudaStream_t s) {
 }
 
 // CTAs for `rows` rows of K: four times what is resident, so that they drift apart between reading and
-// writing (129280 x 4096 bf16 packed in 249 us and read back in 202; with one time 267 and 243, with
-// one span a warp 273 and 208).
+// writing (129280 x 4096 bf16 packed in 249 us, by now 244, and read back in 202; with once 267 and
+// 243, with one span a warp 273 and 208).
 static dim3 pack_grid(int rows, int K) {
   const long long warps = (long long)rows * ((w4::padded(K) + 1023) / 1024);
   const long long n = (warps + w4::kPackWarps - 1) / w4::kPackWarps, most = num_sms() * 32;
