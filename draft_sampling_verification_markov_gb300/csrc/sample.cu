@@ -24,8 +24,9 @@
 //     tokens where the nucleus ends. A list of all before that decides it, or, where they are more, an
 //     exact pass that sums what is above the window and lists the window;
 //   - a larger top-k: the k-th logit by its leading bits, 10 at a time, then as before;
-//   - what defeats all of this (thousands of equal logits at the border): the key by halving, a pass a
-//     step;
+//   - thousands of equal logits at the border, as bf16 has them far from zero: the logit by halving,
+//     beginning at the window, a pass a step, then the token by counting the equal ones (logits of mean
+//     40: 2048 rows at p 0.95 2.6 ms, 14.4 with ids halved too and no window);
 //   - a temperature alone: one exact pass.
 // An exact pass is bound by its instructions, 23 a token; the others by memory and by the latency of
 // a row's steps. 2048 rows of 129280 bf16 logits (529 MB, 78 us at the copy bandwidth): first token 102
@@ -693,43 +694,6 @@ __device__ __noinline__ void pass_window(Shared& sh, const Part<DT> part, const 
   count = c;
 }
 
-// The largest key that leaves a mass (MASS) or number of at least `least` among what `limit`
-// leaves: by halving over the logits, then over the ids of the equal ones. A pass over the row a
-// step, 16 or 32 for the logit and up to 20 for the id.
-template <int DT, bool SPLIT, bool MASS>
-__device__ __noinline__ u64 search(Team<SPLIT>& team, const Part<DT>& part, const Weigher& wt,
-                                   u64 limit, u64 least, u64 top_key) {
-  auto enough = [&](u64 key) {
-    u64 m, c;
-    pass<DT, MASS, false>(team.sh, part, wt, key > limit ? key : limit, m, c);
-    const auto s = team.sum(m, c);
-    return (MASS ? s.a : s.b) >= least;
-  };
-  constexpr int kLow = DT == SPEC_BF16 ? 16 : 0;  // order_bits of a bf16 end in 16 zeros or ones
-  constexpr uint32_t kLeast = 0x00800000u >> kLow;  // of the lowest finite number
-  uint32_t lo = (uint32_t)(limit >> 32) >> kLow, hi = ((uint32_t)(top_key >> 32) >> kLow) + 1;
-  lo = lo > kLeast ? lo : kLeast;
-  while (hi - lo > 1) {
-    const uint32_t mid = lo + (hi - lo) / 2;
-    if (enough((u64)(mid << kLow) << 32))
-      lo = mid;
-    else
-      hi = mid;
-  }
-  uint32_t bits = lo << kLow;
-  if (DT == SPEC_BF16 && !(bits & 0x80000000u)) bits |= 0xffffu;
-  uint32_t a = 0, b = (uint32_t)part.row.V;  // ids up to b - 1 are enough, up to a - 1 are not
-  while (b - a > 1) {
-    const uint32_t mid = a + (b - a) / 2;
-    if (enough((u64)bits << 32 | (0xffffffffu - (mid - 1))))
-      b = mid;
-    else
-      a = mid;
-  }
-  const u64 key = (u64)bits << 32 | (0xffffffffu - (b - 1));
-  return key > limit ? key : limit;
-}
-
 // ------------------------------------------------------------------------------ the list
 
 // A bound that at least k of this CTA's tokens reach, and not many more where it can be had: the k-th
@@ -923,6 +887,108 @@ __device__ __noinline__ u64 scan(Shared& sh, u64 v, u64& total) {
   }
   __syncthreads();
   return before + x - v;
+}
+
+// The key of the c-th token, in order of the ids, whose order_bits are `bits`: its segment by a pass
+// that counts, then its place in there. There are at least c.
+template <int DT, bool SPLIT>
+__device__ __noinline__ u64 nth_equal(Team<SPLIT>& team, const Part<DT>& part, uint32_t bits, u64 c) {
+  constexpr int N = Row<DT>::N;
+  Shared& sh = team.sh;
+  const int tid = threadIdx.x, lane = tid & 31, n = part.steps();
+  const float value = order_value(bits);
+  u64 own = 0;
+  __syncthreads();  // the index may have been read until now
+  for (int it = 0; it < n; ++it) {
+    uint4 q[kBatch];
+    part.load(q, it);
+    uint32_t in = 0;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      float x[N];
+      unpack<DT>(q[b], x);
+#pragma unroll
+      for (int i = 0; i < N; ++i) in += x[i] == value;
+    }
+    own += in;
+    in = __reduce_add_sync(kFull, in);
+    if (lane == 0) sh.seg[it * kWarps + (tid >> 5)] = in;
+  }
+  const auto all = team.sum(own, 0);
+  uint32_t found = 0;
+  if (all.before < c && c <= all.before + all.own) {
+    const int segs = n * kWarps, per = (segs + kThreads - 1) / kThreads, first = tid * per;
+    const u64 at = c - 1 - all.before;
+    u64 mine = 0, t;
+    for (int i = first; i < min(segs, first + per); ++i) mine += sh.seg[i];
+    u64 before = scan(sh, mine, t);
+    if (before <= at && at < before + mine) {
+      int i = first;
+      for (; before + sh.seg[i] <= at; ++i) before += sh.seg[i];
+      sh.hit = i;
+      sh.rest = at - before;
+    }
+    __syncthreads();
+    if (tid < 32) {
+      int rest = (int)sh.rest;
+      const int base = part.j0 + sh.hit * kWarpStep;
+      for (int b = 0; b < kBatch; ++b) {
+        const int j = base + b * 32 + lane;
+        float x[N];
+        unpack<DT>(part.row.load_any(j, part.j1), x);
+        uint32_t in = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) in |= (uint32_t)(x[i] == value) << i;
+        const int here = __popc(in);
+        int up = here;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(kFull, up, o);
+          if (lane >= o) up += y;
+        }
+        int skip = rest - (up - here);  // of this lane's
+        if (skip >= 0 && skip < here) {
+          for (; skip; --skip) in &= in - 1;
+          found = 0xffffffffu - (uint32_t)(j * N - part.row.head + __ffs(in) - 1);
+        }
+        rest -= __shfl_sync(kFull, up, 31);
+        if (rest < 0) break;  // uniform
+      }
+    }
+  }
+  return (u64)bits << 32 | team.max(found);
+}
+
+// The largest key that leaves a mass of at least `least` among what `limit` leaves: by halving over the
+// logits, a pass a step, from a guess (sh.lo_bits .. sh.hi_bits, which may be wrong) where it holds;
+// then by counting the equal ones.
+template <int DT, bool SPLIT>
+__device__ __noinline__ u64 search(Team<SPLIT>& team, const Part<DT>& part, const Weigher& wt,
+                                   u64 limit, u64 least, u64 top_key) {
+  auto mass = [&](u64 key) {
+    u64 m, c;
+    pass<DT, true, false>(team.sh, part, wt, key > limit ? key : limit, m, c);
+    return team.sum(m, c).a;
+  };
+  constexpr int kLow = DT == SPEC_BF16 ? 16 : 0;  // order_bits of a bf16 end in 16 zeros or ones
+  constexpr uint32_t kLeast = 0x00800000u >> kLow;  // of the lowest finite number
+  uint32_t lo = (uint32_t)(limit >> 32) >> kLow, hi = ((uint32_t)(top_key >> 32) >> kLow) + 1;
+  lo = lo > kLeast ? lo : kLeast;
+  uint32_t guess[2] = {(team.sh.hi_bits >> kLow) + (kLow ? 1u : 0u), team.sh.lo_bits >> kLow};
+  for (int i = 0; hi - lo > 1; ++i) {
+    uint32_t mid = i < 2 ? guess[i] : lo + (hi - lo) / 2;
+    if (i < 2 && !(lo < mid && mid < hi)) continue;
+    if (mass((u64)(mid << kLow) << 32) >= least)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  uint32_t bits = lo << kLow;
+  if (DT == SPEC_BF16 && !(bits & 0x80000000u)) bits |= 0xffffu;
+  const u64 larger = mass((u64)(bits + 1) << 32);
+  const u64 each = wt.template operator()<DT>(order_value(bits));
+  const u64 key = nth_equal<DT, SPLIT>(team, part, bits, (least - larger + each - 1) / each);
+  return key > limit ? key : limit;
 }
 
 __device__ __forceinline__ float key_value(u64 key) { return order_value((uint32_t)(key >> 32)); }
@@ -1857,7 +1923,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
       }
       const u64 key_m = (u64)tm << 32;
       if (!kept && !(by_m && limit == key_m)) {
-        if (k && !limit) limit = search<DT, SPLIT, false>(team, part, wt, 0, (u64)k, top_key);
+        // the k-th token is one of many equal ones
+        if (k && !limit)
+          limit = nth_equal<DT, SPLIT>(team, part, sh.lo_bits, (u64)(k - sh.n_above));
         if (by_p) {
           if (!k && slack) all = team.sum(pass_all<DT, false>(sh, part, wt), 0).a;
           if (limit && !of_k) {
@@ -1872,7 +1940,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) sample_kernel(const SampleArg
             pass<DT, true, false>(sh, part, wt, key_m > limit ? key_m : limit, mm, cc);
             more = team.sum(mm, cc).a > need;
           }
-          if (more) limit = search<DT, SPLIT, true>(team, part, wt, limit, need ? need : 1, top_key);
+          if (more) limit = search<DT, SPLIT>(team, part, wt, limit, need ? need : 1, top_key);
         }
         limit = by_m && key_m > limit ? key_m : limit;
       }

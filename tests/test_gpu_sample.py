@@ -174,6 +174,23 @@ def test_large_top_k_with_the_other_rules(flat, rows, dt):
         check(x, u, (1.1, 0, p, mp), d, c, (0, 1, rows - 1))
 
 
+@pytest.mark.parametrize("rows", [1, 5, 170])
+def test_thousands_of_equal_logits(rows):
+    """bf16 logits far from zero lie on a coarse grid: a border is within thousands of equal ones, and
+    ids decide."""
+    V = 60000
+    g = torch.Generator().manual_seed(31)
+    x = torch.randn(rows, V, generator=g)
+    x = torch.cat([x[:1] + 70, x[1:2] - 70, x[2:3] * 0.01 - 3, x[3:] * 2 + 40]).to(torch.bfloat16)
+    x[:, ::7] = -INF
+    u = uniforms(rows, 32)
+    for k, p, mp in ((0, 0.3, 0.0), (0, 0.95, 0.0), (0, 0.9999, 0.0), (7000, 1.0, 0.0),
+                     (30001, 1.0, 0.0), (30001, 0.77, 0.0), (20000, 0.9, 0.1), (0, 0.8, 0.2)):
+        d, c, st = both(x, u, 1.0, k, p, mp)
+        assert st == 0
+        check(x, u, (1.0, k, p, mp), d, c, sorted({0, 1 % rows, 2 % rows, 3 % rows, rows - 1}))
+
+
 @pytest.mark.parametrize("dt", DTS)
 @pytest.mark.parametrize("rows", [24, 600])
 def test_parameters_per_request(rows, dt):
