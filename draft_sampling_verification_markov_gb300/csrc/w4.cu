@@ -328,8 +328,10 @@ cudaError_t launch_w4_logits(W4Args a, cudaStream_t s) {
   if (!tc::encode_fn()) return cudaErrorNotSupported;
   const cuuint64_t dims[2] = {(cuuint64_t)padded(a.K) / 2, (cuuint64_t)a.N}, stride = dims[0];
   const cuuint32_t box[2] = {64u * form.W, 16u * form.R}, one[2] = {1, 1};
+  const CUtensorMapSwizzle swizzle =
+      form.W == 1 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
   if (tc::encode_fn()(&codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(a.codes), dims,
-                      &stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, form.W == 1 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                      &stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                       CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;

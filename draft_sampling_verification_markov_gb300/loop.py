@@ -50,7 +50,8 @@ class SpecLoop:
     With top_k, top_p or min_p (numbers, or device tensors [R] with one for each request; see
     spec.spec_truncate) the target is truncated at the loop's temperature: every iteration writes the
     target rows with -inf outside into truncated_target, with their normalisers, and confidence,
-    scheduling and verification go by these, so the emitted tokens follow the truncated target. kept [R, gamma + 1] counts the tokens left in each row.
+    scheduling and verification go by these, so the emitted tokens follow the truncated target.
+    kept [R, gamma + 1] counts the tokens left in each row.
 
     With `logprobs` = k (0 .. 32) every iteration also scores its emitted tokens under the target
     rows that they answer to, at the loop's temperature: token_logp, token_rank, token_entropy

@@ -644,8 +644,9 @@ int spec_w4_dequantize(const uint8_t* codes, const void* scales, int scale_dtype
  *   codes, scales, zeros, group, N   the matrix, [N, K].
  *   out           [M, N] of out_dtype, row stride ld_out >= N elements; must not overlap an operand.
  * The matrix is read once for every 40 rows (a bf16 out, or bf16 rows without a norm) or 20, fewer
- * where K is large; SPEC_ERR_TOO_LARGE where one row does not fit (K above 73728, or 36864). A row with an infinity or a NaN sets
- * SPEC_DEV_NONFINITE; its outputs are NaN (or infinities, without a norm).
+ * where K is large; SPEC_ERR_TOO_LARGE where one row does not fit (K above 73728, or 36864). A row
+ * with an infinity or a NaN sets SPEC_DEV_NONFINITE; its outputs are NaN (or infinities, without a
+ * norm).
  */
 int spec_w4_logits(const void* x, long long ldx, const void* residual, long long ldr, int dtype,
                    const void* norm_weight, int nw_dtype, float eps, int M, int K,
