@@ -1159,7 +1159,7 @@ int spec_w4_logits(const void* x, long long ldx, const void* residual, long long
   if (norm_weight && (!(eps >= 0.0f) || !isfinite(eps))) return SPEC_ERR_INVALID_ARG;
   if (!status_ws_ok(ws)) return SPEC_ERR_INVALID_ARG;
   if (ws_bytes < kHeader) return SPEC_ERR_WORKSPACE_TOO_SMALL;
-  const int parts = out_dtype == SPEC_F32 && (dtype == SPEC_F32 || norm_weight) ? 2 : 1;
+  const int parts = dtype == SPEC_F32 || norm_weight ? 2 : 1;
   if (!w4_fits(parts, K)) return SPEC_ERR_TOO_LARGE;
   if (M == 0) return SPEC_OK;
   if (!x || !codes || !scales || !out || !aligned16(codes) || !aligned16(scales) ||

@@ -17,14 +17,15 @@
 // the tensor pipe's cycles): what is, is the instructions between memory and the multiplication.
 //
 // Measured, 129280 x 4096: one row at groups of 128 53 us with its norm (75 % of the copy bandwidth),
-// eight rows 65, 60 without the norm; one row at groups of 32 67; 16 rows at groups of 64 113. 4 x 4096
+// eight rows 87, 60 without the norm; one row at groups of 32 67; 16 rows at groups of 64 113. 4 x 4096
 // x 8192 with zero points 16 us; 17 rows fp32 of 32000 x 2048, 40 columns, 48.
 //
 // Columns. A number of the rows is one or two fp16 numbers, each a column of its own. One is exact for
-// bf16 rows as they are, and serves wherever the product is rounded to bf16: 11 bits of a number that
-// is customarily rounded to bf16's 8 before such a product. For fp32 products of 32-bit rows, or with
-// a norm weight multiplied in, two: off by 2^-24, as the rounding of fp32 is. Rows are scaled by
-// powers of two into fp16's range; that and the norm's 1 / rms are applied to the sums.
+// bf16 rows as they are. 32-bit rows, and those with a norm weight multiplied in, take two, off by
+// 2^-24, as the rounding of fp32 is; whatever the product is rounded to: with one, of 11 bits, one
+// bf16 output in ten was a step from the 64-bit product's rounding, and eight rows of 129280 x 4096
+// took 65 us with their norm where they take 87 (one row 53 in both). Rows are scaled by powers of two
+// into fp16's range; that and the norm's 1 / rms are applied to the sums.
 //
 // Order. A code's position in k is free as long as the rows' columns are permuted alike. A lane holds
 // words of eight codes; pair s of a word is (code s, code s + 4). With groups of 128 a lane's four

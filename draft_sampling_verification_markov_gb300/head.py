@@ -51,7 +51,7 @@ class VocabHead:
 class GroupedHead:
     """The same head with weights of 4 bits in groups and rows that are not quantised: residual
     addition, norm and product in one launch, for the few rows of a decoding step. The matrix is read
-    anew for every 40 rows of a bf16 product (20 of a fp32 one), so VocabHead suits wide batches.
+    anew for every 20 rows (for every 9 where K is 4096), so VocabHead suits wide batches.
 
     weight [V, K] (bf16 or fp32) is packed and not kept; a spec.W4Tensor is used as it is, zero points
     and all. norm_weight [K]; `group` is 32, 64 or 128."""

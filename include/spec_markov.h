@@ -632,10 +632,9 @@ int spec_w4_dequantize(const uint8_t* codes, const void* scales, int scale_dtype
  *   projections, which have neither.
  *   h = x + residual, rounded to `dtype` (x without a residual);
  *   a = h * rsqrt(mean(h^2) + eps) * norm_weight (h without a norm_weight);
- *   out[m, n] = sum_k a[m, k] w[n, k]; products are exact, sums fp32. For a fp32 out a is held in 24
- *   bits where it is above 2^-14 of the largest |h| |norm_weight| of its row, and is off by at most
- *   2^-38 of that elsewhere. For a bf16 out it is held in 11 bits (rows of bf16 without a norm stay
- *   exact), off by at most 2^-27 of the largest below 2^-16 of it.
+ *   out[m, n] = sum_k a[m, k] w[n, k]; products are exact, sums fp32, and only a bf16 out rounds
+ *   them. a is held in 24 bits where it is above 2^-14 of the largest |h| |norm_weight| of its row,
+ *   and is off by at most 2^-38 of that elsewhere; rows of bf16 without a norm stay exact.
  * Arguments:
  *   x, residual   [M, K] of `dtype`, row strides ldx and ldr; residual may be NULL.
  *   norm_weight   [K] of nw_dtype, or NULL (no norm; eps is ignored).
@@ -643,8 +642,8 @@ int spec_w4_dequantize(const uint8_t* codes, const void* scales, int scale_dtype
  *                 not overlap x or residual.
  *   codes, scales, zeros, group, N   the matrix, [N, K].
  *   out           [M, N] of out_dtype, row stride ld_out >= N elements; must not overlap an operand.
- * The matrix is read once for every 40 rows (a bf16 out, or bf16 rows without a norm) or 20, fewer
- * where K is large; SPEC_ERR_TOO_LARGE where one row does not fit (K above 73728, or 36864). A row
+ * The matrix is read once for every 40 rows (bf16 rows without a norm) or 20, fewer where K is
+ * large; SPEC_ERR_TOO_LARGE where one row does not fit (K above 73728, or 36864). A row
  * with an infinity or a NaN sets SPEC_DEV_NONFINITE; its outputs are NaN (or infinities, without a
  * norm).
  */
