@@ -21,11 +21,13 @@
 // x 8192 with zero points 16 us; 17 rows fp32 of 32000 x 2048, 40 columns, 48.
 //
 // Columns. A number of the rows is one or two fp16 numbers, each a column of its own. One is exact for
-// bf16 rows as they are. 32-bit rows, and those with a norm weight multiplied in, take two, off by
-// 2^-24, as the rounding of fp32 is; whatever the product is rounded to: with one, of 11 bits, one
-// bf16 output in ten was a step from the 64-bit product's rounding, and eight rows of 129280 x 4096
-// took 65 us with their norm where they take 87 (one row 53 in both). Rows are scaled by powers of two
-// into fp16's range; that and the norm's 1 / rms are applied to the sums.
+// bf16 rows as they are (from 2^-18 of the largest on: fp16's numbers end at 2^-24). 32-bit rows, and
+// those with a norm weight multiplied in, take two, the second 2^12 times what the first leaves, so
+// that it ends at 2^-36: together off by 2^-23, or by 2^-38 of the largest. That goes for bf16
+// products too: with one, of 11 bits, one bf16 output in ten was a step from the 64-bit product's
+// rounding, and eight rows of 129280 x 4096 took 65 us with their norm where they take 87 (one row 53
+// in both). Rows are scaled by powers of two into fp16's range; that and the norm's 1 / rms are
+// applied to the sums.
 //
 // Order. A code's position in k is free as long as the rows' columns are permuted alike. A lane holds
 // words of eight codes; pair s of a word is (code s, code s + 4). With groups of 128 a lane's four
@@ -128,6 +130,9 @@ __device__ __forceinline__ float power(int e) {  // 2^e, cut to the normal numbe
   return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
+// A second column is kRest times what the first leaves: at most 2^15, as the numbers are.
+constexpr float kRest = 0x1p12f;
+
 // 32 pieces (of eight elements) of row m as fp16 columns, the numbers times `scale`; their largest
 // |h| |weight| and the sum of (h hs)^2.
 __device__ __forceinline__ void stage_pieces(const W4Args& a, const Frame& f, int m0, int m, int p,
@@ -176,8 +181,8 @@ __device__ __forceinline__ void stage_pieces(const W4Args& a, const Frame& f, in
     for (int i = 0; i < 4; ++i) {
       pair[i] = __floats2half2_rn(v[i], v[i + 4]);
       const float2 back = __half22float2(pair[i]);
-      v[i] = __fsub_rn(v[i], back.x);
-      v[i + 4] = __fsub_rn(v[i + 4], back.y);
+      v[i] = __fsub_rn(v[i], back.x) * kRest;
+      v[i + 4] = __fsub_rn(v[i + 4], back.y) * kRest;
     }
     to[(m * a.parts + c) * 4] = *reinterpret_cast<const uint4*>(pair);
   }
@@ -590,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float y0 = acc[r][j][2 * h], y1 = acc[r][j][2 * h + 1];
           acc[r][j][2 * h] = acc[r][j][2 * h + 1] = 0.0f;
           if (a.parts == 2) {
-            if (j * 4 + t < rows) to[j * 4 + t] = y0 + y1;
+            if (j * 4 + t < rows) to[j * 4 + t] = fmaf(y1, 1.0f / kRest, y0);
           } else {
             if (j * 8 + t * 2 < rows) to[j * 8 + t * 2] = y0;
             if (j * 8 + t * 2 + 1 < rows) to[j * 8 + t * 2 + 1] = y1;

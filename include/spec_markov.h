@@ -633,8 +633,9 @@ int spec_w4_dequantize(const uint8_t* codes, const void* scales, int scale_dtype
  *   h = x + residual, rounded to `dtype` (x without a residual);
  *   a = h * rsqrt(mean(h^2) + eps) * norm_weight (h without a norm_weight);
  *   out[m, n] = sum_k a[m, k] w[n, k]; products are exact, sums fp32, and only a bf16 out rounds
- *   them. a is held in 24 bits where it is above 2^-14 of the largest |h| |norm_weight| of its row,
- *   and is off by at most 2^-38 of that elsewhere; rows of bf16 without a norm stay exact.
+ *   them. a is off by at most 2^-23 of itself, or by 2^-38 of the largest |h| |norm_weight| of its
+ *   row (times rsqrt(...)) where that is more. Rows of bf16 without a norm are exact but for numbers
+ *   below 2^-18 of the largest, which are off by at most 2^-26 of it.
  * Arguments:
  *   x, residual   [M, K] of `dtype`, row strides ldx and ldr; residual may be NULL.
  *   norm_weight   [K] of nw_dtype, or NULL (no norm; eps is ignored).

@@ -24,3 +24,52 @@ def test_bf16_products_are_rounded_once(M, N, K, group, form):
     tol = ref.tolerance(K, group, mag, y, F32)
     lo, hi = ((y + s * tol).float().to(BF) for s in (-1, 1))
     assert ((got >= lo) & (got <= hi)).all(), int(((got < lo) | (got > hi)).sum())
+
+
+def one_by_one(K):
+    """A matrix whose row n is element n of the product's rows: code 9 there, 8 elsewhere, scale 1."""
+    codes = torch.full((K, ref.padded(K)), 8, dtype=torch.uint8)
+    codes[torch.arange(K), torch.arange(K)] = 9
+    codes = (codes[:, 0::2] | codes[:, 1::2] << 4).contiguous()
+    return S.W4Tensor(codes.to(DEV), torch.ones(K, ref.padded(K) // 128, device=DEV), 128, K)
+
+
+# of a row: what is served at once, its ends, and what is scaled by its own power
+LARGEST = [0.125, 0.13, 1.0, 100.0, 2047.0, 0.11, 3000.0, 1e20, 1e-30]
+
+
+@pytest.mark.parametrize("K", [128, 600])
+def test_small_elements_beside_a_large_one(K):
+    """Each element of a 32-bit row by itself, from the largest to 2^-40 of it: two fp16 numbers, the
+    second of what the first leaves times 2^12, hold it to 2^-23 of itself or 2^-38 of the largest."""
+    x = 1 + torch.rand(len(LARGEST), K, generator=torch.Generator().manual_seed(K), dtype=torch.float64)
+    x *= torch.exp2(-1 - 39.0 * torch.arange(K) / K)
+    x[:, 0] = 1.0
+    x = (x * torch.tensor(LARGEST, dtype=torch.float64)[:, None]).float()
+    y = S.spec_w4_logits(x.to(DEV), one_by_one(K)).cpu().double()
+    off, most = (y - x.double()).abs(), x.double()[:, :1]
+    assert (off <= torch.maximum(2.0 ** -23 * x.double(), 2.0 ** -38 * most)).all()
+    # normalised: a square root, a division and a product with the weight, each off by a rounding or two
+    norm = torch.exp2(torch.randint(-2, 3, (K,), generator=torch.Generator().manual_seed(1)).float())
+    norm[0] = 4.0
+    y = S.spec_w4_logits(x.to(DEV), one_by_one(K), norm_weight=norm.to(DEV), eps=0.0).cpu().double()
+    a = x.double() * norm.double()
+    a /= x.double().square().mean(1, keepdim=True).sqrt()
+    assert ((y - a).abs() <= torch.maximum(2.0 ** -23 * a, 2.0 ** -38 * a[:, :1])
+            + 8 * 2.0 ** -24 * a).all()
+
+
+def test_small_elements_of_bf16_rows():
+    """One fp16 number each: exact from 2^-18 of the largest on, within 2^-26 of it below."""
+    K = 384
+    x = 1 + torch.rand(len(LARGEST), K, generator=torch.Generator().manual_seed(5), dtype=torch.float64)
+    x *= torch.exp2(-1 - 29.0 * torch.arange(K) / K)
+    x[:, 0] = 1.0
+    x = (x * torch.tensor(LARGEST, dtype=torch.float64)[:, None]).to(BF)
+    for dt in (F32, BF):
+        y = S.spec_w4_logits(x.to(DEV), one_by_one(K), dtype=dt).cpu().double()
+        off, most = (y - x.double()).abs(), x.double()[:, :1]
+        exact = x.double() >= 2.0 ** -18 * most
+        assert (off[exact] == 0).all()
+        rounded = 2.0 ** -8 * y if dt == BF else 0.0
+        assert (off <= 2.0 ** -26 * most + rounded).all()
