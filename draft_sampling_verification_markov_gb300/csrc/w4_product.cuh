@@ -100,8 +100,8 @@ struct Frame {
   uint8_t* ring;  // [warp][stage][16 R rows][64 W bytes], swizzled over that width
   uint4* x;       // the rows' columns: [block][word][column][lane % 4]
   float* red;     // sums: [warp][16 R][stride]
-  float* factor;  // [rows]
-  float* scale;   // [rows]
+  float* factor;  // [rows]: what a row's sums are multiplied with,
+  float* power;   // [rows]: and then with this
   float* stat;    // [2][rows][pieces]
   uint64_t* full; // [warp][stage]
 };
@@ -133,8 +133,8 @@ __device__ __forceinline__ float power(int e) {  // 2^e, cut to the normal numbe
 // A second column is kRest times what the first leaves: at most 2^15, as the numbers are.
 constexpr float kRest = 0x1p12f;
 
-// 32 pieces (of eight elements) of row m as fp16 columns, the numbers times `scale`; their largest
-// |h| |weight| and the sum of (h hs)^2.
+// 32 pieces (of eight elements) of row m as fp16 columns, the numbers times hs and `scale`; the largest
+// of these and the sum of (h hs)^2.
 __device__ __forceinline__ void stage_pieces(const W4Args& a, const Frame& f, int m0, int m, int p,
                                              int cols, float hs, float scale, bool write,
                                              float& most, float& sum) {
@@ -149,16 +149,14 @@ __device__ __forceinline__ void stage_pieces(const W4Args& a, const Frame& f, in
     for (int i = 0; i < 8; ++i) {
       v[i] *= hs;
       sum = fmaf(v[i], v[i], sum);
-      v[i] *= g[i];
+      v[i] = v[i] * scale * g[i];  // in this order: the weights may be small
       most = max_nan(most, fabsf(v[i]));
-      v[i] *= scale;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      v[i] *= hs;
+      v[i] = v[i] * hs * scale;
       most = max_nan(most, fabsf(v[i]));
-      v[i] *= scale;
     }
   }
   // piece of the block -> (word, lane of the quad)
@@ -190,10 +188,10 @@ __device__ __forceinline__ void stage_pieces(const W4Args& a, const Frame& f, in
 
 // The chunk's rows into shared memory as fp16 columns, with the factors that their sums take; h goes
 // out, a share from each CTA of the chunk. fp16 ends at 2^16 and its numbers are 2^-24 apart at the
-// least: rows are multiplied by 2^4, which serves if the largest number, |h| |weight|, is between
-// 2^-3 and 2^11; others are staged once more, by the power of two that brings theirs to 2^12 ..
-// 2^14. The pieces are dealt to the warps by 32, whatever row they are of.
-constexpr float kScale = 16.0f, kScaleLeast = 0x1p-3f, kScaleMost = 0x1p11f;
+// least: rows are multiplied by 2^4, which serves if the largest number, |h| |weight|, is then between
+// 2 and 2^15; others are staged once more, by the power of two that brings theirs to 2^13 .. 2^14. The
+// pieces are dealt to the warps by 32, whatever row they are of.
+constexpr float kScale = 16.0f, kScaledLeast = 2.0f, kScaledMost = 0x1p15f;
 template <typename F>
 __device__ __forceinline__ void stage_rows(const W4Args& a, const Frame& f, int m0, int rows,
                                            int cols, int share, int shares, F&& loaded) {
@@ -241,23 +239,21 @@ __device__ __forceinline__ void stage_rows(const W4Args& a, const Frame& f, int 
     float most, sum;
     row(m, most, sum);
     const float factor = norm ? 1.0f / sqrtf(sum / (float)a.K + a.eps) : 1.0f;
-    const bool serves = most >= kScaleLeast && most < kScaleMost &&
+    const bool serves = most >= kScaledLeast && most < kScaledMost &&
                         (!norm || (sum > 0x1p-60f && sum < INFINITY));
-    float to = 0.0f;
-    if (!serves && (norm || most != 0.0f)) {  // a row of zeros needs no scale without a norm
-      again = true;
-      to = 1.0f;
-    }
+    const bool once = serves || (!norm && most == 0.0f);  // without a norm zeros need no scale
+    again |= !once;
     if (lane == 0) {
       f.factor[m] = factor * (1.0f / kScale);
-      f.scale[m] = to;
+      f.power[m] = once ? 1.0f : 0.0f;
     }
   }
   if (!__syncthreads_or(again)) return;
-  // Rows again whose numbers, or their squares, leave the range: h 2^-eh is below 2, times the
-  // weight it is scaled by its own largest. Every warp finds both powers for itself.
+  // Rows again whose numbers, or their squares, leave the range: h 2^-eh is below 4 (2, but for the
+  // largest numbers: 2^-eh has to be one, too), times the weight it is scaled by its own largest.
+  // Every warp finds both powers for itself.
   for (int m = 0; m < rows; ++m) {
-    if (f.scale[m] == 0.0f) continue;
+    if (f.power[m] != 0.0f) continue;
     float most_h = 0.0f, most = 0.0f;
     for (int p = lane; p < per_row * 32; p += 32) {
       if (p * 8 >= a.K) break;
@@ -271,7 +267,7 @@ __device__ __forceinline__ void stage_rows(const W4Args& a, const Frame& f, int 
       most_h = max_nan(most_h, __shfl_xor_sync(kFull, most_h, o));
     if (!(most_h < INFINITY) && share == 0 && threadIdx.x == 0)
       atomicOr(a.status, SPEC_DEV_NONFINITE);
-    const int eh = most_h > 0.0f && most_h < INFINITY ? exponent(most_h) : 0;
+    const int eh = most_h > 0.0f && most_h < INFINITY ? min(exponent(most_h), 126) : 0;
     if (norm) {
       for (int p = lane; p < per_row * 32; p += 32) {
         if (p * 8 >= a.K) break;
@@ -286,7 +282,7 @@ __device__ __forceinline__ void stage_rows(const W4Args& a, const Frame& f, int 
     } else {
       most = most_h * power(-eh);
     }
-    const int e = most > 0.0f && most < INFINITY ? exponent(most) : 0;
+    const int e = most > 0.0f && most < INFINITY ? max(exponent(most), -113) : 0;
     __syncthreads();  // the factors and the columns of before have been read
     for (int c = m * per_row + warp; c < (m + 1) * per_row; c += kWarps)
       pass(c, power(-eh), power(13 - e), false);
@@ -296,10 +292,16 @@ __device__ __forceinline__ void stage_rows(const W4Args& a, const Frame& f, int 
       row(m, most, sum);
       sum /= (float)a.K;
       // beside eps in the scale in which neither passes fp32's range
-      const float q = !norm                      ? power(eh)
-                      : eh < 0 && a.eps > 0.0f ? power(eh) / sqrtf(a.eps + sum * power(eh) * power(eh))
-                                               : 1.0f / sqrtf(sum + a.eps * power(-eh) * power(-eh));
-      if (lane == 0) f.factor[m] = q * power(e) * 0x1p-13f;
+      const bool small = eh < 0 && a.eps > 0.0f;
+      const float q = !norm   ? 1.0f
+                      : small ? 1.0f / sqrtf(a.eps + sum * power(eh) * power(eh))
+                              : 1.0f / sqrtf(sum + a.eps * power(-eh) * power(-eh));
+      // times 2^by, in halves: one number may not hold it
+      const int by = (!norm || small ? eh : 0) + e - 13;
+      if (lane == 0) {
+        f.factor[m] = q * power(by / 2);
+        f.power[m] = power(by - by / 2);
+      }
     }
   }
   __syncthreads();
@@ -370,8 +372,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   f.red = reinterpret_cast<float*>(f.x + (size_t)KB * 16 * a.chunk_rows * a.parts);
   f.full = reinterpret_cast<uint64_t*>(f.red + kWarps * 16 * R * stride);
   f.factor = reinterpret_cast<float*>(f.full + kWarps * stages);
-  f.scale = f.factor + a.chunk_rows;
-  f.stat = f.scale + a.chunk_rows;
+  f.power = f.factor + a.chunk_rows;
+  f.stat = f.power + a.chunk_rows;
   __shared__ int abort;
   __shared__ uint64_t sums_there[kWarps / 2], sums_read[kWarps / 2];  // of a team
 
@@ -613,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (n >= a.N) continue;
       float y = 0.0f;
       for (int w = 0; w < kw; ++w) y += from[(w * 16 * R + r) * stride + m];
-      y *= f.factor[m];
+      y = y * f.factor[m] * f.power[m];
       const size_t to = (size_t)(m0 + m) * a.ldo + n;
       if (a.out_dtype == SPEC_BF16)
         static_cast<__nv_bfloat16*>(a.out)[to] = __float2bfloat16_rn(y);

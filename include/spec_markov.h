@@ -635,7 +635,9 @@ int spec_w4_dequantize(const uint8_t* codes, const void* scales, int scale_dtype
  *   out[m, n] = sum_k a[m, k] w[n, k]; products are exact, sums fp32, and only a bf16 out rounds
  *   them. a is off by at most 2^-23 of itself, or by 2^-38 of the largest |h| |norm_weight| of its
  *   row (times rsqrt(...)) where that is more. Rows of bf16 without a norm are exact but for numbers
- *   below 2^-18 of the largest, which are off by at most 2^-26 of it.
+ *   below 2^-18 of the largest, which are off by at most 2^-26 of it. That holds for finite rows of
+ *   any size, for scales from 2^-126 to 2^89 (a row's numbers are scaled to 2^15 before they are
+ *   summed) and, where there is one, a norm_weight whose largest is from 2^-100 to 2^100.
  * Arguments:
  *   x, residual   [M, K] of `dtype`, row strides ldx and ldr; residual may be NULL.
  *   norm_weight   [K] of nw_dtype, or NULL (no norm; eps is ignored).

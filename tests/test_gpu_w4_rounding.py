@@ -73,3 +73,56 @@ def test_small_elements_of_bf16_rows():
         assert (off[exact] == 0).all()
         rounded = 2.0 ** -8 * y if dt == BF else 0.0
         assert (off <= 2.0 ** -26 * most + rounded).all()
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("size", [3.3e38, 2e38, 1.7e38, 8e37, 1e-36, 1e-38, 1e-40, 9.2e-41])
+def test_rows_of_any_size_without_a_norm(size, dt):
+    """Finite rows up to the largest number and down to subnormals, against scales that bring the
+    product back, with a row of the matrix whose product is 0."""
+    K, group = 256, 128
+    x = torch.rand(3, K, generator=torch.Generator().manual_seed(1)) * 2 - 1
+    x[:, 0] = 1.0
+    x[1] = 0.0
+    x[2, 200] = -1.0
+    x = (x.double() * size).to(dt)
+    codes, scales = ref.pack(randn((40, K), 2, F32), group, F32)
+    codes[7], scales = 0x88, scales * (2.0 ** -100 if size > 1 else 2.0 ** 80)
+    w = S.W4Tensor(codes.to(DEV), scales.to(DEV), group, K)
+    v = ref.values(codes, scales, group, K)
+    ws = S.Workspace(device=DEV)
+    for out in (F32, BF):
+        y = S.spec_w4_logits(x.to(DEV), w, dtype=out, workspace=ws).cpu().double()
+        _, want, mag = ref.product(x, v, K)
+        assert ws.status() == 0 and (y[:, 7] == 0).all() and (y[1] == 0).all()
+        # without the floor of 1e-37 that ref.tolerance adds: it is far above some of these
+        tol = ref.tolerance(K, group, mag, want, out, dt == BF) - 1e-37
+        assert ((y - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+def test_normalised_rows_of_any_size_and_weights(eps, dt):
+    """Rows to both ends of their type, weights whose products with them are small or large."""
+    K, group = 256, 64
+    x = torch.rand(6, K, generator=torch.Generator().manual_seed(3)) * 2 - 1
+    x[:, 5] = 1.0
+    sizes = torch.tensor([3.3e38, 1.7e38, 1.0, 1e-30, 1e-38, 1e-40], dtype=torch.float64)
+    x = (x.double() * sizes[:, None]).to(dt)
+    codes, scales = ref.pack(randn((40, K), 4, F32), group, F32)
+    for wp in (-99, -60, 0, 60, 99):
+        norm = ((1 + randn((K,), 5, F32, 0.1)) * 2.0 ** wp).to(dt)
+        a = x.double().square().mean(1, keepdim=True)
+        a = x.double() / (a + eps).sqrt() * norm.double()
+        # products of about 1, or as near as 2^80 brings them
+        s = (scales.double() * 2.0 ** min(80, -wp)).float()
+        w = S.W4Tensor(codes.to(DEV), s.to(DEV), group, K)
+        v = ref.values(codes, s, group, K)
+        ws = S.Workspace(device=DEV)
+        y = S.spec_w4_logits(x.to(DEV), w, norm_weight=norm.to(DEV), eps=eps, dtype=F32,
+                             workspace=ws).cpu().double()
+        want, mag = a @ v.t(), a.abs() @ v.abs().t()
+        # without the floor, but for a rounding or two of subnormal numbers
+        tol = ref.tolerance(K, group, mag, want, F32) - 1e-37 + 2.0 ** -148
+        assert ws.status() == 0
+        assert ((y - want).abs() <= tol).all(), wp
