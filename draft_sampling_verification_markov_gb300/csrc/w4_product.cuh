@@ -173,17 +173,18 @@ __device__ __forceinline__ void stage_pieces(const W4Args& a, const Frame& f, in
     w = pi >> 2;
   }
   uint4* to = f.x + (size_t)((p >> 4) * 4 + w) * cols * 4 + t;
-  for (int c = 0; c < a.parts; ++c) {
-    __half2 pair[4];
+  to += (size_t)m * a.parts * 4;
+  __half2 pair[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      pair[i] = __floats2half2_rn(v[i], v[i + 4]);
-      const float2 back = __half22float2(pair[i]);
-      v[i] = __fsub_rn(v[i], back.x) * kRest;
-      v[i + 4] = __fsub_rn(v[i + 4], back.y) * kRest;
-    }
-    to[(m * a.parts + c) * 4] = *reinterpret_cast<const uint4*>(pair);
+  for (int i = 0; i < 4; ++i) pair[i] = __floats2half2_rn(v[i], v[i + 4]);
+  *to = *reinterpret_cast<const uint4*>(pair);
+  if (a.parts == 1) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 back = __half22float2(pair[i]);
+    pair[i] = __floats2half2_rn(__fsub_rn(v[i], back.x) * kRest, __fsub_rn(v[i + 4], back.y) * kRest);
   }
+  to[4] = *reinterpret_cast<const uint4*>(pair);
 }
 
 // The chunk's rows into shared memory as fp16 columns, with the factors that their sums take; h goes
