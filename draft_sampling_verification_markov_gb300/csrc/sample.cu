@@ -222,9 +222,12 @@ struct Weigher {
     h0 = half(t0, q0);
     h1 = half(t1, q1);
   }
-  // A finite logit from which on every one has a mass.
+  // A finite logit from which on every one has a mass: rounded up, for where logits are far apart
+  // beside T (100 and its neighbours at T = 1e-5), and no farther below m than fp32's largest number,
+  // or m - x would be infinite.
   __device__ __forceinline__ float surely() const {
-    return fmaxf(m - (most - 0.125f) / ch, -3.402823466e38f);
+    constexpr float kMost = 3.402823466e38f;
+    return fmaxf(__fsub_ru(m, (most - 0.125f) / ch), __fsub_ru(m, kMost));
   }
   // Bin of a mass, of t = kMagic + y: -32 y rounded; the last one, and what has none, share a bin.
   __device__ __forceinline__ static uint32_t bin(float t) {

@@ -540,7 +540,8 @@ int spec_token_logprobs(const void* logits, int dtype, long long ld, const int32
  *   top_p   of these, those before which less than top_p of their summed w has been reached (1: all);
  *   min_p   of these, those of w >= min_p (0: all).
  * The first token always stays; T = 0 leaves it alone (greedy), as does top_p = 0. Tokens of logit
- * -inf never stay. Sums and borders are exact to about 2^-31 of each w, in whole numbers, so the
+ * -inf never stay; those of logits more than 3.4e38 (fp32's largest number) below the largest may stay,
+ * but weigh nothing. Sums and borders are exact to about 2^-31 of each w, in whole numbers, so the
  * results do not depend on how a row is split over the GPU.
  * A row with a NaN or +inf logit, or with nothing above -inf, sets SPEC_DEV_NONFINITE: its token is
  * the largest logit's (0 where there is none), its logp and stats are NaN, its kept 0, and
