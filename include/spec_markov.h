@@ -541,8 +541,11 @@ int spec_token_logprobs(const void* logits, int dtype, long long ld, const int32
  *   min_p   of these, those of w >= min_p (0: all).
  * The first token always stays; T = 0 leaves it alone (greedy), as does top_p = 0. Tokens of logit
  * -inf never stay; those of logits more than 3.4e38 (fp32's largest number) below the largest may stay,
- * but weigh nothing. Sums and borders are exact to about 2^-31 of each w, in whole numbers, so the
- * results do not depend on how a row is split over the GPU.
+ * but weigh nothing. Each w is a whole number of units of 2^-47 (V up to 65,536; 2^-46 up to twice as
+ * many, and so on to 2^-43), off by about 2^-31 of itself and by one unit; sums and borders of these are
+ * exact, so the results do not depend on how a row is split over the GPU. Where the difference of
+ * a bf16 logit and the largest does not fit 24 bits (one is below 2^-16 of the other) its w is off by up to
+ * 2^-24 (max z - z) of itself.
  * A row with a NaN or +inf logit, or with nothing above -inf, sets SPEC_DEV_NONFINITE: its token is
  * the largest logit's (0 where there is none), its logp and stats are NaN, its kept 0, and
  * spec_truncate copies it.

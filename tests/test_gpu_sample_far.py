@@ -4,6 +4,7 @@ import math
 import pytest
 import torch
 
+import sample_ref as ref
 from draft_sampling_verification_markov_gb300 import spec as S
 from test_gpu_sample import DEV, both, check, uniforms
 
@@ -53,3 +54,27 @@ def test_logits_farther_apart_than_the_largest_number(dt, T):
             lp = z.gather(1, d.tokens.long()[:, None])[:, 0] - lz
             assert torch.allclose(d.logp.double(), lp, rtol=1e-5, atol=1e-6)
         assert near.gather(1, d.tokens.long()[:, None]).all()
+
+
+@pytest.mark.parametrize("rows", [2, 170])
+def test_bf16_logits_far_below_the_largest_in_magnitude(rows):
+    """Tails of logits near zero beside a largest of 4 to 5: their differences from it take more than 24
+    bits, so that a mass may be off by 2^-24 (max - x) / T, 2^-21 here. Borders farther off than that
+    are where 64 bits have them."""
+    V = 30000
+    g = torch.Generator().manual_seed(11)
+    x = 1e-5 + 3e-5 * torch.rand(rows, V, generator=g)
+    x[:, 77] = 4 + torch.rand(rows, generator=g)
+    x = x.to(torch.bfloat16)
+    u = uniforms(rows, 12)
+    for p in (0.3, 0.9):
+        d, c, st = both(x, u, 1.0, 0, p, 0.0)
+        assert st == 0
+        for r in (0, 1, rows - 1):
+            tok, logp, kept, _, (m, lz), near, near_u = ref.row_draw(
+                x[r].double().numpy(), 1.0, 0, float(torch.tensor(p)), 0.0, float(u[r]))
+            if near >= 2.0 ** -21:
+                assert int(d.kept[r]) == kept == int(c.kept[r])
+                if near_u >= 2.0 ** -21:
+                    assert int(d.tokens[r]) == tok
+            assert ref.log_close(float(c.stats[r, 1]), lz) or int(d.kept[r]) != kept
