@@ -1099,13 +1099,17 @@ static bool w4_ok(int rows, int K, int group) {
   return mx_sizes_ok(rows, K) && (group == 32 || group == 64 || group == 128);
 }
 
-// Whether two arrays of rows with strides share no byte range.
-static bool ranges_apart(const void* p, long long ldp, int dp, const void* q, long long ldq, int dq,
-                         int rows, int wp, int wq) {
+// Whether a kernel may write p's rows while it reads q's, of another width or type: arrays apart, or
+// rows of one stride that do not meet.
+static bool columns_apart(const void* p, long long ldp, int dp, const void* q, long long ldq, int dq,
+                          int rows, int wp, int wq) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  const uintptr_t na = ((uintptr_t)(rows - 1) * ldp + wp) * esize(dp);
-  const uintptr_t nb = ((uintptr_t)(rows - 1) * ldq + wq) * esize(dq);
-  return a + na <= b || b + nb <= a;
+  const uintptr_t sp = (uintptr_t)ldp * esize(dp), sq = (uintptr_t)ldq * esize(dq);
+  const uintptr_t rp = (uintptr_t)wp * esize(dp), rq = (uintptr_t)wq * esize(dq);
+  if (a + (rows - 1) * sp + rp <= b || b + (rows - 1) * sq + rq <= a) return true;
+  if (rows == 1 || sp != sq) return false;
+  const uintptr_t d = a >= b ? (a - b) % sp : (sp - (b - a) % sp) % sp;  // p's place in q's rows
+  return d >= rq && d + rp <= sp;
 }
 
 size_t spec_w4_code_bytes(int rows, int K) {
@@ -1169,12 +1173,12 @@ int spec_w4_logits(const void* x, long long ldx, const void* residual, long long
   if (residual && (!residual_out || !elem_aligned(residual, dtype) ||
                    !elem_aligned(residual_out, dtype)))
     return SPEC_ERR_INVALID_ARG;
-  if (residual && (!ranges_apart(residual_out, ldh, dtype, x, ldx, dtype, M, K, K) ||
-                   !ranges_apart(residual_out, ldh, dtype, residual, ldr, dtype, M, K, K)))
+  if (residual && (!columns_apart(residual_out, ldh, dtype, x, ldx, dtype, M, K, K) ||
+                   !columns_apart(residual_out, ldh, dtype, residual, ldr, dtype, M, K, K)))
     return SPEC_ERR_INVALID_ARG;
-  if (!ranges_apart(out, ld_out, out_dtype, x, ldx, dtype, M, N, K) ||
-      (residual && (!ranges_apart(out, ld_out, out_dtype, residual, ldr, dtype, M, N, K) ||
-                    !ranges_apart(out, ld_out, out_dtype, residual_out, ldh, dtype, M, N, K))))
+  if (!columns_apart(out, ld_out, out_dtype, x, ldx, dtype, M, N, K) ||
+      (residual && (!columns_apart(out, ld_out, out_dtype, residual, ldr, dtype, M, N, K) ||
+                    !columns_apart(out, ld_out, out_dtype, residual_out, ldh, dtype, M, N, K))))
     return SPEC_ERR_INVALID_ARG;
   const W4Args a{x,     ldx,         residual, ldr,   dtype, norm_weight,  nw_dtype,
                  eps,   M,           N,        K,     codes, scales,       scale_dtype,

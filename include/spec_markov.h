@@ -646,7 +646,7 @@ int spec_w4_dequantize(const uint8_t* codes, const void* scales, int scale_dtype
  *   x, residual   [M, K] of `dtype`, row strides ldx and ldr; residual may be NULL.
  *   norm_weight   [K] of nw_dtype, or NULL (no norm; eps is ignored).
  *   residual_out  [M, K] of `dtype`, row stride ldh: h (required with a residual, else ignored). Must
- *                 not overlap x or residual.
+ *                 not overlap x or residual (other columns of one wide buffer do not).
  *   codes, scales, zeros, group, N   the matrix, [N, K].
  *   out           [M, N] of out_dtype, row stride ld_out >= N elements; must not overlap an operand.
  * The matrix is read once for every 40 rows (bf16 rows without a norm) or 20, fewer where K is
