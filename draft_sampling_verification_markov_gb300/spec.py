@@ -1047,7 +1047,7 @@ class W4Tensor:
     (Kp = K rounded up to a multiple of 128; group 32, 64 or 128; the layout is that of
     include/spec_markov.h)."""
 
-    __slots__ = ("codes", "scales", "zeros", "group", "K", "_at")
+    __slots__ = ("_codes", "_scales", "_zeros", "_group", "_K")
 
     def __init__(self, codes, scales, group, K, *, zeros=None):
         rows, Kp = codes.shape[0], -(-K // SPEC_MX_GROUP) * SPEC_MX_GROUP
@@ -1058,7 +1058,7 @@ class W4Tensor:
         if codes.dtype != torch.uint8 or codes.shape != (rows, Kp // 2) or not codes.is_contiguous():
             raise ValueError(f"codes must be contiguous uint8 [rows, {Kp // 2}]")
         shape = (rows, Kp // group)
-        dt = _dtype_code(scales.dtype)
+        _dtype_code(scales.dtype)
         if scales.shape != shape or not scales.is_contiguous():
             raise ValueError(f"scales must be contiguous {shape}")
         if not codes.is_cuda or scales.device != codes.device:
@@ -1066,9 +1066,7 @@ class W4Tensor:
         if zeros is not None and (zeros.dtype != torch.uint8 or zeros.shape != shape
                                   or not zeros.is_contiguous() or zeros.device != codes.device):
             raise ValueError(f"zeros must be contiguous uint8 {shape} on {codes.device}")
-        self.codes, self.scales, self.zeros, self.group, self.K = codes, scales, zeros, group, K
-        self._at = (codes.data_ptr(), scales.data_ptr(), dt,
-                    None if zeros is None else zeros.data_ptr())
+        self._codes, self._scales, self._zeros, self._group, self._K = codes, scales, zeros, group, K
 
     @classmethod
     def empty(cls, rows, K, group, scale_dtype, device):
@@ -1079,17 +1077,30 @@ class W4Tensor:
         return cls(torch.empty(rows, Kp // 2, dtype=torch.uint8, device=device),
                    torch.empty(rows, Kp // group, dtype=scale_dtype, device=device), group, K)
 
+    # what was checked together stays together: another matrix is another W4Tensor
+    codes = property(lambda self: self._codes)
+    scales = property(lambda self: self._scales)
+    zeros = property(lambda self: self._zeros)
+    group = property(lambda self: self._group)
+    K = property(lambda self: self._K)
+
+    def _at(self):
+        """Addresses of codes and scales, the scales' type, address of the zero points."""
+        z = self._zeros
+        return (self._codes.data_ptr(), self._scales.data_ptr(), _dtype_code(self._scales.dtype),
+                None if z is None else z.data_ptr())
+
     @property
     def rows(self):
-        return self.codes.shape[0]
+        return self._codes.shape[0]
 
     @property
     def device(self):
-        return self.codes.device
+        return self._codes.device
 
     @property
     def shape(self):
-        return self.codes.shape[0], self.K
+        return self._codes.shape[0], self._K
 
 
 def spec_w4_quantize(x, group=128, *, scale_dtype=torch.bfloat16, out=None, workspace=None,
@@ -1103,7 +1114,7 @@ def spec_w4_quantize(x, group=128, *, scale_dtype=torch.bfloat16, out=None, work
     elif out.rows != rows or out.K != K or out.group != group or out.zeros is not None:
         raise ValueError("out must be a W4Tensor of x's rows and width, the given group, no zeros")
     _on(dev, out, "out")
-    cp, sp, sdt, _ = out._at
+    cp, sp, sdt, _ = out._at()
     _launch("spec_w4_quantize", dev, workspace, stream, ptr, dt, ld, rows, K, group, cp, sp, sdt)
     return out
 
@@ -1119,7 +1130,7 @@ def spec_w4_dequantize(q, *, dtype=torch.bfloat16, out=None, workspace=None, str
     if orows != rows or width != K:
         raise ValueError("out must have q's rows and width")
     _on(dev, out, "out")
-    cp, sp, sdt, zp = q._at
+    cp, sp, sdt, zp = q._at()
     _launch("spec_w4_dequantize", dev, workspace, stream, cp, sp, sdt, zp, rows, K, q.group, ptr, dt,
             ld)
     return out
@@ -1165,7 +1176,7 @@ def spec_w4_logits(x, w, *, norm_weight=None, eps=1e-6, residual=None, residual_
     if rows != M or width != N:
         raise ValueError(f"out must hold {M} rows of {N}")
     _on(dev, out, "out")
-    cp, sp, sdt, zp = w._at
+    cp, sp, sdt, zp = w._at()
     _launch("spec_w4_logits", dev, workspace, stream, ptr, ldx, rp, ldr, dt, np_, ndt, eps, M, K, cp,
             sp, sdt, zp, w.group, N, hp, ldh, op, odt, ldo)
     return out if residual is None else (residual_out, out)
