@@ -927,7 +927,8 @@ def _truncation(temperature, top_k, top_p, min_p, rows, dev):
                                  (top_p, "top_p", "top_ps", torch.float32),
                                  (min_p, "min_p", "min_ps", torch.float32)):
         if not isinstance(value, torch.Tensor):
-            setattr(r, one, value)
+            # a top_k past 32 bits is one past the vocabulary: it would be cut to its last 32 bits
+            setattr(r, one, value if one != "top_k" else max(-1, min(value, 0x7fffffff)))
             continue
         if value.dtype != dt or not value.is_contiguous():
             raise ValueError(f"{one} must be a number or a contiguous tensor of {dt}")
