@@ -36,9 +36,12 @@
 // written out instead of drawn from 398 to 447.
 //
 // Three CTAs of 256 threads an SM, a CTA a row. Few rows are split over a cluster of up to 8 CTAs,
-// which merge through distributed shared memory: twice as many as long as there are no more than SMs.
-// A row's steps do not get shorter with its part (64 rows on 512 CTAs instead of 256: top-k 50 25 ->
-// 44 us; 2048 rows on two CTAs each 150 -> 285).
+// which merge through distributed shared memory: twice as many as long as there are no more than SMs,
+// whatever the rules. Measured beside that: 64 rows on 512 CTAs, more than have a place, instead of 256
+// (top-k 50 25 -> 44 us); up to three CTAs for two SMs (180 rows: a temperature alone 56 -> 49, top-k
+// 21 -> 28; 64 rows of the former 29 -> 39); 2048 rows on two CTAs each (top-k 50 150 -> 285). A list's
+// steps do not get shorter with a row's part; a pass over the whole row may, and the best division
+// goes by the rule, which this one does not.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -13,19 +13,21 @@
 // for every second one), code - zero with one more, all exact; the scale is applied to a group's fp32
 // sum. Two to sixteen warps that share a tile's rows, each a range of K, add their sums through
 // shared memory; such teams go through the matrix by themselves. tcgen05 would want the unpacked
-// matrix in shared memory, four times the bytes, for a multiplication that is not the bound (22 % of
-// the tensor pipe's cycles): what is, is the instructions between memory and the multiplication.
+// matrix in shared memory, four times the bytes, for a multiplication that is not the bound (20 to 32 %
+// of the tensor pipe's cycles). No unit is full: half the issue slots are used, and memory for one row
+// to three quarters; what a warp waits for is the chain from its tile to its sums.
 //
 // Measured, 129280 x 4096: one row at groups of 128 53 us with its norm (75 % of the copy bandwidth),
-// eight rows 87, 60 without the norm; one row at groups of 32 67; 16 rows at groups of 64 113. 4 x 4096
-// x 8192 with zero points 16 us; 17 rows fp32 of 32000 x 2048, 40 columns, 48.
+// eight rows 88, 59 without the norm; one row at groups of 32 69; 16 rows at groups of 64 171, 111
+// without the norm. 4 x 4096 x 8192 with zero points 14 us; 17 rows fp32 of 32000 x 2048, 40 columns,
+// 47.
 //
 // Columns. A number of the rows is one or two fp16 numbers, each a column of its own. One is exact for
 // bf16 rows as they are (from 2^-18 of the largest on: fp16's numbers end at 2^-24). 32-bit rows, and
 // those with a norm weight multiplied in, take two, the second 2^12 times what the first leaves, so
 // that it ends at 2^-36: together off by 2^-23, or by 2^-38 of the largest. That goes for bf16
 // products too: with one, of 11 bits, one bf16 output in ten was a step from the 64-bit product's
-// rounding, and eight rows of 129280 x 4096 took 65 us with their norm where they take 87 (one row 53
+// rounding, and eight rows of 129280 x 4096 took 65 us with their norm where they take 88 (one row 53
 // in both). Rows are scaled by powers of two into fp16's range; that and the norm's 1 / rms are
 // applied to the sums.
 //
@@ -88,7 +90,9 @@ struct Zero {
 };
 
 // Codes s and s + 4 of a word less the zero point, for s = 0 and 1 (of the word's upper bytes: 2 and
-// 3). An fp16 number from 1024 to 2047 holds a code in its last bits, or 16 times one four bits up.
+// 3). An fp16 number from 1024 to 2047 holds a code in its last bits, or 16 times one four bits up: the
+// conversion of unsigned codes that Kim, Henry, Fahim and Awadalla published ("Who Says Elephants
+// Can't Run", 2022), from whose arithmetic the constants follow; zero points are subtracted with it.
 __device__ __forceinline__ uint32_t codes_even(uint32_t w, const Zero& z) {
   return sub2(masked(w, 0x000f000fu), z.a);
 }

@@ -599,7 +599,8 @@ int spec_truncate(const void* logits, int dtype, long long ld, int rows, int V,
                   void* stream);
 
 /*
- * Grouped 4-bit weights: the form of weight-only checkpoints, for products with few rows.
+ * Grouped 4-bit weights: what weight-only checkpoints hold (codes, scales and zero points of groups),
+ * in a layout of its own, for products with few rows.
  * `rows` rows of K elements, padded to Kp = K rounded up to a multiple of SPEC_MX_GROUP; `group`
  * (32, 64 or 128) consecutive elements of a row share a scale and, optionally, a zero point:
  *   w = (code - zero) * scale, zero = 8 where there are none.
