@@ -1191,7 +1191,9 @@ __device__ __noinline__ int rules(Shared& sh, const Weigher& wt, int n, int nk, 
   const int tid = threadIdx.x;
   if (n > kThreads) {
     const u64 lo = (u64)bound << 32;
-    u64 limit = nk < n ? pick<DT>(sh, wt, n, 0, (u64)nk, false, lo, last_key) : 0;
+    // all of the list: not all of the row, which is what 0 leaves
+    u64 limit = nk < n ? pick<DT>(sh, wt, n, 0, (u64)nk, false, lo, last_key)
+                       : (u64)(bound > 0x00800000u ? bound : 0x00800000u) << 32;
     int kept;
     u64 mass = list_mass<DT>(sh, wt, n, limit, kept);
     const u64 key_m = sh.tm > 1 ? (u64)sh.tm << 32 : 0;
